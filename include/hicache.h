@@ -616,6 +616,144 @@ int hicache_layer_checksum(const hicache_device_kv *kv, const hicache_pool_desc 
                            const int64_t *device_pages, int64_t n, int32_t layer_id,
                            int32_t reps, uint64_t *out_sum_dev, void *stream);
 
+/* ---- operators on the device pages: append, decode attention, eviction ---------
+ * What a serving step runs on the L1 pages between the moves above: new keys
+ * and values are stored into their slots, the new token attends to the cached
+ * ones, and pages that received little attention leave L1 (their page numbers
+ * go to hicache_backup).  The shape of the device pages comes from the same
+ * hicache_pool_desc as a transfer's (its host_num_pages and layout are not
+ * used), the buffers from the same hicache_device_kv:
+ *   - num_buffers 2: K and V rows of kv_heads * head_dim elements;
+ *   - num_buffers 1: one latent row per token, kv_heads 1, head_dim ==
+ *     row_elems; the value of a token is the first v_dim elements of its row;
+ *   - elem_bytes 2: elements of `dtype`; elem_bytes 1: e4m3 (1 sign, 4
+ *     exponent, 3 mantissa bits, no infinities), element times k_scale (or
+ *     v_scale) being the value.
+ * Conventions, besides those above:
+ *   - Page tables, lengths, slots, positions, weights and budgets are DEVICE
+ *     memory, read by the kernels: the calls never wait for the GPU, can be
+ *     captured into a CUDA graph, and the values may change between replays.
+ *     All pointers belong to the current device.
+ *   - What the host cannot check is bounded by the kernels: a page outside
+ *     [0, device_num_pages) counts as absent, a slot outside the buffers or a
+ *     position outside the table stores nothing, a length counts as clamped
+ *     to [0, max_pages * page_size].
+ *   - Strides are in elements; the innermost dimension is contiguous.
+ *   - Everything is computed in 32 bits and rounded once to the output's type,
+ *     except as noted.  The same call on the same data gives the same bits.
+ *   - A call that returns an error has enqueued nothing. */
+typedef enum { HICACHE_BF16 = 0, HICACHE_FP16 = 1 } hicache_dtype;
+
+/* Norms of the query and key heads, the position rotation and the store of K
+ * and V into the cache, in one pass.  For token n and head h, with x the head's
+ * head_dim elements:
+ *   norm      x_i <- x_i * rsqrt(mean(x_0..x_{m-1} squared) + eps) * weight_i
+ *             for i < m = q_norm_dim (k_norm_dim for keys); m == 0: no norm;
+ *   rotation  of the rot_dim elements from rot_offset on, in pairs (a, b) =
+ *             elements (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved:
+ *             a <- a cos - b sin, b <- b cos + a sin, with cos_j and sin_j the
+ *             elements j and rot_dim/2 + j of row positions[n] of cos_sin;
+ *             rot_dim == 0: no rotation;
+ *   store     q -> q_out[n, h]; k and v (as it came) -> row slots[n] of the
+ *             layer's buffers (slot = page * page_size + offset); an e4m3
+ *             cache takes x / scale, saturated to +-448.
+ * A token whose position lies outside [0, cos_sin_rows) is skipped (rot_dim >
+ * 0); one whose slot lies outside the buffers stores no K and V: rows that only
+ * fill up a batch carry slot -1.  Two tokens of one call with the same slot
+ * leave the row undefined.  q_out may be q itself (same strides), else it must
+ * not overlap an input.  q may be NULL (q_heads 0), or k and v (kv_heads 0,
+ * slots NULL).  Pointers and strides must be multiples of 16 bytes (ALIGNMENT);
+ * head_dim a multiple of 8 (of 16 into an e4m3 cache), at most 768. */
+typedef struct {
+  const void *q;            /* [num_tokens, q_heads, head_dim] of dtype */
+  void *q_out;
+  const void *k;            /* [num_tokens, kv_heads, head_dim] of dtype */
+  const void *v;            /* as k; NULL for a latent cache */
+  const void *q_weight;     /* [q_norm_dim] of dtype */
+  const void *k_weight;     /* [k_norm_dim] of dtype */
+  const int64_t *slots;     /* [num_tokens] */
+  const int64_t *positions; /* [num_tokens]; NULL if rot_dim == 0 */
+  const float *cos_sin;     /* [cos_sin_rows, rot_dim]; NULL if rot_dim == 0 */
+  int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  int64_t num_tokens, cos_sin_rows;
+  int32_t dtype, q_heads, kv_heads, head_dim;
+  int32_t q_norm_dim, k_norm_dim, rot_dim, rot_offset;
+  int32_t interleaved;
+  float eps, k_scale, v_scale;
+} hicache_append_desc;
+int hicache_append_kv(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                      const hicache_append_desc *a, void *stream);
+
+/* Attention of one new token per sequence over its pages.  For sequence b and
+ * query head h, over the tokens t < seq_lens[b] whose page page_table[b,
+ * t / page_size] is present (and, with window > 0, only the last `window`
+ * tokens before seq_lens[b]), with K and V of kv head h / (q_heads / kv_heads):
+ *   s_t = scale * k_scale * (q . k_t),   lse = log(sum exp s_t),
+ *   out = v_scale * sum exp(s_t - lse) v_t.
+ * A sequence without any such token gives out = 0 and lse = -infinity.
+ * weights (optional): for each page p < ceil(seq_lens[b] / page_size),
+ *   weights[b, p] <- decay * weights[b, p] + sum over heads and the page's
+ *   tokens of exp(s_t - lse); what lies behind those pages is left as it was.
+ * The products run on the tensor cores with 32-bit sums; the exponentials are
+ * rounded to the cache's type (fp16 for e4m3) for the product with V alone.
+ * workspace: hicache_decode_workspace bytes of device memory, 256-byte aligned,
+ * zero-filled before its first use; every call leaves it ready for the next
+ * call of any shape it is large enough for.  Calls that may run at the same
+ * time (other streams, graphs replayed together) need one each.
+ * head_dim: a multiple of 8 (of 16 for e4m3) up to 256; a latent cache has 576,
+ * v_dim 512 and elem_bytes 2.  max_pages * page_size < 2^31. */
+typedef struct {
+  const void *q;              /* [batch, q_heads, head_dim] of dtype */
+  void *out;                  /* [batch, q_heads, v_dim] of dtype */
+  const int32_t *page_table;  /* [batch, max_pages] */
+  const int32_t *seq_lens;    /* [batch] */
+  float *lse;                 /* [batch, q_heads], or NULL */
+  float *weights;             /* [batch, max_pages], or NULL */
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t q_batch_stride, q_head_stride, out_batch_stride, out_head_stride;
+  int64_t table_stride, lse_stride, weights_stride;
+  int32_t dtype, batch, q_heads, head_dim, v_dim, max_pages, window, reserved;
+  float scale, k_scale, v_scale, decay;
+} hicache_decode_desc;
+int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                             const hicache_decode_desc *a, void *stream);
+/* The workspace bytes of a call with these sizes (with_weights: whether it
+ * passes weights), on the current device. */
+int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32_t q_heads, int32_t head_dim,
+                             int32_t v_dim, int32_t max_pages, int32_t with_weights, int64_t *bytes);
+
+/* Which pages of each sequence leave L1: those that received the least
+ * attention.  With n = ceil(seq_lens[b] / page_size) pages, the pages in [sink,
+ * n - recent) may go, and count = min(max(0, n - keep[b]), their number,
+ * max_victims) of them do: those with the lowest weights[b, p], the lowest p
+ * first among equals (-0 equals 0; NaN ranks above infinity).
+ *   victims[b, 0..count)        their page_table entries, in the order of p
+ *   num_victims[b]              count
+ *   out_table[b, 0..n-count)    the other entries, in order; [n-count, n) -> -1
+ *   out_weights[b, 0..n-count)  their weights, in order; [n-count, n) -> 0
+ *   out_lens[b]                 seq_lens[b] - count * page_size
+ * and everything else in those arrays is left as it was.  recent >= 1 keeps the
+ * last page, which may not be full.  out_table, out_weights and out_lens may be
+ * page_table, weights and seq_lens themselves (same strides), else nothing may
+ * overlap.  The positions of the tokens that stay do not change: a caller that
+ * evicts keeps its position counter apart from the length. */
+typedef struct {
+  const int32_t *page_table;  /* [batch, max_pages] */
+  const float *weights;       /* [batch, max_pages] */
+  const int32_t *seq_lens;    /* [batch] */
+  const int32_t *keep;        /* [batch]: pages to keep */
+  int32_t *victims;           /* [batch, max_victims] */
+  int32_t *num_victims;       /* [batch] */
+  int32_t *out_table;         /* [batch, max_pages] */
+  float *out_weights;         /* [batch, max_pages] */
+  int32_t *out_lens;          /* [batch] */
+  int64_t table_stride, weights_stride, victims_stride, out_table_stride, out_weights_stride;
+  int32_t page_size, batch, max_pages, max_victims, sink, recent;
+} hicache_evict_desc;
+int hicache_evict_pages(const hicache_evict_desc *a, void *stream);
+
 /* ---- tensor-parallel load of a replicated latent ---------------------------------
  * "Baidu's KVCache Overhaul", section "MLA-class cache optimization": with MLA
  * latents (and the CSA/HCA caches named there) every rank of a tensor-parallel

@@ -1,0 +1,619 @@
+"""The operators on the device pages (append, decode attention, eviction) against
+plain 64-bit forms, at the sizes and masks where they can go wrong."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import serving_reference as ref
+import tiered_kv_cache_gb300 as hc
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+E4 = torch.float8_e4m3fn
+
+
+def desc(P, row, es, buffers=2, layers=1):
+    return hc.PoolDesc(layers, buffers, P, es, row, 1, hc.LAYER_FIRST, 0, 0, 0)
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def raw(t):
+    """Bits, for comparisons in which NaN equals itself."""
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()])
+
+
+# ---- append ---------------------------------------------------------------------
+
+APPEND = [
+    # n, hq, hk, d, P, dtype, e4m3, norm_q, norm_k, rot, off, interleaved, latent
+    (1, 32, 8, 128, 64, "bf16", False, 128, 128, 128, 0, False, False),
+    (1, 1, 1, 8, 1, "fp16", False, 8, 0, 0, 0, False, False),
+    (7, 4, 2, 64, 16, "bf16", False, 0, 0, 64, 0, False, False),
+    (33, 6, 3, 80, 5, "fp16", False, 80, 80, 40, 0, False, False),
+    (50, 5, 1, 80, 16, "bf16", True, 80, 80, 40, 4, False, False),
+    (129, 8, 8, 96, 16, "bf16", True, 96, 96, 48, 10, True, False),
+    (64, 3, 1, 256, 64, "fp16", True, 256, 256, 256, 0, False, False),
+    (19, 2, 2, 192, 7, "bf16", False, 64, 128, 100, 30, True, False),
+    (40, 16, 1, 576, 64, "bf16", False, 0, 512, 64, 512, False, True),
+    (3, 128, 1, 576, 64, "fp16", False, 576, 512, 64, 512, True, True),
+    (11, 2, 1, 768, 4, "bf16", False, 768, 768, 768, 0, False, True),
+    (1000, 14, 2, 128, 16, "fp16", False, 128, 128, 64, 64, False, False),
+]
+
+
+def append_inputs(c, seed):
+    n, hq, hk, d, P, dt, e4, nq, nk, rot, off, il, latent = c
+    dt, g = DT[dt], gen(seed)
+    per = hq + hk * (1 if latent else 2)
+    fused = (2 * torch.randn((n, per, d), generator=g, device="cuda")).to(dt)
+    q, k = fused[:, :hq], fused[:, hq:hq + hk]
+    v = None if latent else fused[:, hq + hk:]
+    pages = -(-n // P) + 2
+    slots = torch.randperm(pages * P, generator=g, device="cuda")[:n]
+    pos = torch.randint(0, 5000, (n,), generator=g, device="cuda")
+    cs = None
+    if rot:
+        ang = torch.arange(5000, device="cuda", dtype=torch.float64)[:, None] * \
+            10000.0 ** (-torch.arange(0, rot, 2, device="cuda", dtype=torch.float64) / rot)
+        cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    w = lambda m: (1 + 0.3 * torch.randn(m, generator=g, device="cuda")).to(dt) if m else None  # noqa: E731
+    cache = E4 if e4 else dt
+    bufs = [torch.full((pages * P, hk * d), 0x5A, dtype=torch.uint8, device="cuda").repeat(1, 1 if e4 else 2)
+            .view(cache) for _ in range(1 if latent else 2)]
+    return q, k, v, slots, pos, cs, w(nq), w(nk), bufs, pages
+
+
+def check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, ks, vs, skip=None):
+    n, hq, hk, d, P, dt, e4, nq, nk, rot, off, il, latent = c
+    dt = DT[dt]
+    skip = torch.zeros(n, dtype=torch.bool, device="cuda") if skip is None else skip
+    rows = cs[pos.clamp(0, 4999)] if cs is not None else None
+    y, err = ref.norm_rotate(q.double(), qw, rows, off, il, 1e-6)
+    ok = (q_out.double() - y).abs() <= err + (y.abs() + err) * ref.UNIT[dt] + ref.TINY[dt]
+    assert ok[~skip].all(), "q_out"
+    live = (slots >= 0) & (slots < old[0].shape[0]) & ~skip
+    at = slots[live]
+    cache = bufs[0].dtype
+    rest = torch.ones(old[0].shape[0], dtype=torch.bool, device="cuda")
+    rest[at] = False
+    stored = [ref.norm_rotate(k.double(), kw, rows, off, il, 1e-6) + (ks,)]
+    if v is not None:
+        stored.append((v.double(), torch.zeros_like(v, dtype=torch.float64), vs))
+    for buf, before, (y, err, sc) in zip(bufs, old, stored):
+        y, err = y[live].reshape(-1, hk * d) / sc, err[live].reshape(-1, hk * d) / sc
+        if cache == E4:
+            err = err + y.abs() * ref.U32
+            y = y.clamp(-448, 448)
+        got = raw(buf)[at].view(cache).double()
+        assert ((got - y).abs() <= err + (y.abs() + err) * ref.UNIT[cache] + ref.TINY[cache]).all(), "cache"
+        assert torch.equal(raw(buf)[rest], raw(before)[rest]), "rows that no token has were written"
+
+
+@pytest.mark.parametrize("c", APPEND, ids=[f"{i}" for i in range(len(APPEND))])
+def test_append(c):
+    q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, 3)
+    old = [b.clone() for b in bufs]
+    ks, vs = (0.03, 0.05) if c[6] else (1.0, 1.0)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    kv = hc.DeviceKV(bufs, pages)
+    dd = desc(c[4], c[2] * c[3], bufs[0].element_size(), len(bufs))
+    before = hc.launch_count()
+    hc.append_kv(kv, dd, 0, q, k, v, slots, q_out=q_out, positions=pos if cs is not None else None, cos_sin=cs,
+                 rot_offset=c[10], interleaved=c[11], q_weight=qw, k_weight=kw, k_scale=ks, v_scale=vs)
+    assert hc.launch_count() == before + 1
+    check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, ks, vs)
+    # in place (q is a view of the fused tensor): the same bits
+    keep = q_out.clone()
+    hc.append_kv(kv, dd, 0, q, None, None, None, positions=pos if cs is not None else None, cos_sin=cs,
+                 rot_offset=c[10], interleaved=c[11], q_weight=qw)
+    assert torch.equal(raw(q), raw(keep))
+
+
+def test_append_skips_rows():
+    """Slots and positions outside their ranges: nothing is stored there, and
+    rows whose position is outside are left as they were."""
+    c = (24, 4, 2, 64, 8, "bf16", False, 64, 64, 64, 0, False, False)
+    q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, 5)
+    slots[2], slots[3], slots[4], slots[5] = -1, pages * 8, 2 ** 62, -2 ** 63
+    pos[7], pos[8], pos[9] = -1, 5000, 2 ** 61
+    old = [b.clone() for b in bufs]
+    q_out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    hc.append_kv(hc.DeviceKV(bufs, pages), desc(8, 128, 2), 0, q, k, v, slots, q_out=q_out, positions=pos, cos_sin=cs,
+                 q_weight=qw, k_weight=kw)
+    skip = (pos < 0) | (pos >= 5000)
+    check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, 1.0, 1.0, skip)
+    assert (q_out[skip] == 7.0).all()
+
+
+def test_append_heads_outer_and_extremes():
+    """Heads outside tokens, e4m3 saturation, infinities and NaN."""
+    g = gen(9)
+    k = torch.randn((2, 5, 64), generator=g, device="cuda").to(torch.float16).transpose(0, 1)
+    k = k.clone(memory_format=torch.preserve_format)
+    v = torch.full((5, 2, 64), 60000.0, dtype=torch.float16, device="cuda")
+    v[1], v[2, 0], v[3, 1] = -60000.0, float("inf"), float("nan")
+    bufs = [torch.zeros((16, 128), dtype=torch.uint8, device="cuda").view(E4) for _ in range(2)]
+    slots = torch.arange(5, device="cuda") * 3
+    hc.append_kv(hc.DeviceKV(bufs, 4), desc(4, 128, 1), 0, None, k, v, slots, k_scale=0.5, v_scale=2.0)
+    got = bufs[1].float().view(16, 2, 64)[slots]
+    assert (got[0] == 448).all() and (got[1] == -448).all() and (got[2, 0] == 448).all()
+    assert got[3, 1].isnan().all() and (got[3, 0] == 448).all()
+    want = (k.float() / 0.5).to(E4).float().reshape(5, 128)
+    assert torch.equal(bufs[0].float()[slots], want)
+
+
+# ---- decode ---------------------------------------------------------------------
+
+def decode_inputs(lens, hq, hk, d, P, dtype="bf16", e4=False, latent=False, seed=1, holes=False, sharp=2.0, width=0,
+                  spare=3):
+    """Caches filled with NaN, in which only the tokens of the sequences are
+    written, and page tables whose other entries are out of range."""
+    g, dt = gen(seed), DT[dtype]
+    rnd = random.Random(seed)
+    counts = [-(-n // P) for n in lens]
+    width = max(width, max(counts), 1)
+    Dp = sum(counts) + spare
+    order = list(range(Dp))
+    rnd.shuffle(order)
+    bad = [-1, Dp, 2 ** 31 - 1, -2 ** 31, Dp + 17]
+    table, at = [], 0
+    for c in counts:
+        row = order[at:at + c]
+        at += c
+        if holes:
+            row = [p if rnd.random() < 0.7 else rnd.choice(bad) for p in row]
+        table.append(row + [rnd.choice(bad) for _ in range(width - c)])
+    row_e = d if latent else hk * d
+    es = 1 if e4 else 2
+    bufs = []
+    for _ in range(1 if latent else 2):
+        b = torch.full((Dp * P, row_e * es), 0x7F if e4 else 0xFF, dtype=torch.uint8, device="cuda")
+        b = b.view(E4 if e4 else dt)
+        for i, n in enumerate(lens):
+            for j, p in enumerate(table[i][:counts[i]]):
+                m = min(P, n - j * P)
+                if 0 <= p < Dp:
+                    x = torch.randn((m, row_e), generator=g, device="cuda")
+                    if e4:
+                        b.view(torch.uint8)[p * P:p * P + m] = (8 * x).to(E4).view(torch.uint8)
+                    else:
+                        b[p * P:p * P + m] = x.to(dt)
+        bufs.append(b)
+    q = (sharp * torch.randn((len(lens), hq, d), generator=g, device="cuda")).to(dt)
+    clean = [[p if 0 <= p < Dp else -1 for p in r] for r in table]
+    return {"q": q, "bufs": bufs, "table": torch.tensor(table, dtype=torch.int32, device="cuda"), "clean": clean,
+            "lens": torch.tensor(lens, dtype=torch.int32, device="cuda"), "Dp": Dp, "width": width, "dt": dt,
+            "ks": 0.125 if e4 else 1.0, "vs": 0.25 if e4 else 1.0, "desc": desc(P, row_e, es, len(bufs)),
+            "kv": hc.DeviceKV(bufs, Dp)}
+
+
+def workspace(s, hq, d, dv, weights):
+    n = hc.decode_workspace(s["desc"], s["q"].shape[0], hq, d, dv, s["width"], weights)
+    return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+def run_decode(lens, hq, hk, d, P, dtype="bf16", e4=False, latent=False, window=0, weights=True, holes=False,
+               sharp=2.0, seed=1, scale=None, width=0):
+    s = decode_inputs(lens, hq, hk, d, P, dtype, e4, latent, seed, holes, sharp, width)
+    dv = 512 if latent else d
+    scale = d ** -0.5 if scale is None else scale
+    out = torch.full((len(lens), hq, dv), 3.0, dtype=s["dt"], device="cuda")
+    lse = torch.full((len(lens), hq), 3.0, device="cuda")
+    w = torch.rand((len(lens), s["width"]), generator=gen(8), device="cuda") if weights else None
+    before = w.clone() if weights else None
+    ws = workspace(s, hq, d, dv, weights)
+    hc.decode_attention(s["kv"], s["desc"], 0, s["q"], s["table"], s["lens"], out, ws, scale=scale, window=window,
+                        weights=w, decay=0.5, lse=lse, k_scale=s["ks"], v_scale=s["vs"])
+    k = s["bufs"][0].view(s["Dp"] * P, -1, d)
+    v = k[..., :512] if latent else s["bufs"][1].view(s["Dp"] * P, -1, d)
+    want = ref.decode(s["q"], k, v, s["clean"], [max(0, n) for n in lens], P, scale, window, s["ks"], s["vs"])
+    ref.check_decode(out, want, s["dt"], torch.float16 if e4 else s["dt"], lse, w, before, 0.5)
+    return s, out
+
+
+DECODE = [
+    # lens, hq, hk, d, P, dtype, e4m3
+    ([1], 1, 1, 64, 1, "bf16", False),
+    ([1, 0, 2], 4, 2, 64, 16, "fp16", False),
+    ([15, 16, 17, 31, 32, 33], 8, 2, 64, 16, "bf16", False),
+    ([4097], 32, 8, 128, 64, "bf16", False),
+    ([63, 64, 65, 129, 1000, 0, 5], 32, 8, 128, 64, "fp16", False),
+    ([300, 7, 2500], 6, 2, 96, 5, "bf16", False),
+    ([700, 13], 5, 1, 80, 16, "fp16", False),
+    ([257, 1024], 3, 3, 72, 1, "bf16", False),
+    ([900, 30], 16, 1, 256, 128, "bf16", False),
+    ([513, 100], 24, 1, 192, 300, "fp16", False),
+    ([513, 100], 40, 2, 128, 16, "bf16", False),
+    ([1, 0, 1500, 31], 8, 2, 128, 16, "fp16", True),
+    ([4097, 255], 32, 8, 128, 64, "bf16", True),
+    ([300, 7, 1100], 12, 2, 96, 5, "bf16", True),
+    ([900, 30], 16, 1, 256, 1, "fp16", True),
+    ([513, 100], 20, 1, 192, 300, "bf16", True),
+    ([77, 2000], 7, 1, 16, 16, "bf16", True),
+    ([77, 2000], 7, 7, 8, 16, "bf16", False),
+    ([33000, 5, 9000], 8, 2, 128, 16, "bf16", False),
+    ([3 + 37 * i % 400 for i in range(70)], 8, 2, 64, 16, "fp16", False),
+]
+
+
+@pytest.mark.parametrize("c", DECODE, ids=[f"{i}" for i in range(len(DECODE))])
+def test_decode(c):
+    run_decode(*c)
+
+
+@pytest.mark.parametrize("c", [
+    ([1], 16, 64), ([0, 1, 63, 64, 65], 16, 64), ([129, 4000, 127, 0, 128], 128, 64), ([1000, 17], 20, 5),
+    ([300, 9], 64, 1), ([513, 2049], 8, 300), ([20000], 33, 16), ([400 + 3 * i for i in range(40)], 16, 16),
+], ids=[f"{i}" for i in range(8)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_decode_latent(c, dtype):
+    run_decode(c[0], c[1], 1, 576, c[2], dtype, latent=True, scale=192 ** -0.5)
+
+
+@pytest.mark.parametrize("latent,e4", [(False, False), (False, True), (True, False)])
+@pytest.mark.parametrize("window", [1, 16, 100, 1023])
+def test_decode_window_and_absent_pages(latent, e4, window):
+    """A window and absent pages, among them sequences of which nothing is left."""
+    run_decode([1, 100, 1000, 0, 2040, 17], 8, 2, 576 if latent else 64, 16, "bf16", e4, latent, window=window,
+               holes=True, seed=window)
+
+
+@pytest.mark.parametrize("latent,e4", [(False, False), (False, True), (True, False)])
+def test_decode_sharp_scores_and_negative_scale(latent, e4):
+    d = 576 if latent else 128
+    run_decode([700, 64, 2], 8, 2, d, 16, "fp16", e4, latent, sharp=40.0)
+    run_decode([700, 64, 2], 8, 2, d, 16, "bf16", e4, latent, scale=-0.1)
+
+
+def plain_call(s, out, ws, **kw):
+    hc.decode_attention(s["kv"], s["desc"], 0, s["q"], s["table"], s["lens"], out, ws, k_scale=s["ks"],
+                        v_scale=s["vs"], **kw)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_lengths_outside_the_table(latent):
+    """Negative lengths count as 0, lengths behind the table as its end."""
+    s = decode_inputs([320, 320, 100], 4, 2, 576 if latent else 64, 16, latent=latent)
+    dv = 512 if latent else 64
+    ws = workspace(s, 4, s["q"].shape[2], dv, False)
+    a, b = (torch.empty((3, 4, dv), dtype=s["dt"], device="cuda") for _ in range(2))
+    s["lens"][0], s["lens"][1] = -5, 320
+    plain_call(s, a, ws)
+    s["lens"][0], s["lens"][1] = -2 ** 31, 2 ** 31 - 1
+    plain_call(s, b, ws)
+    assert torch.equal(a, b) and (a[0] == 0).all() and (a[1] != 0).any()
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_strides(latent):
+    """q and out as views of wider tensors, tables, lse and weights with longer
+    rows, one layer of several: the same bits as contiguous arguments, and
+    nothing else written."""
+    d, hq, P = (576, 6, 16) if latent else (64, 6, 16)
+    dv = 512 if latent else d
+    s = decode_inputs([100, 33, 650], hq, 2, d, P, latent=latent)
+    ws = workspace(s, hq, d, dv, True)
+    out = torch.empty((3, hq, dv), dtype=s["dt"], device="cuda")
+    lse = torch.empty((3, hq), device="cuda")
+    w = torch.zeros((3, s["width"]), device="cuda")
+    plain_call(s, out, ws, weights=w, lse=lse)
+    wide_q = torch.full((3, hq + 4, d + 16), float("nan"), dtype=s["dt"], device="cuda")
+    wide_q[:, 2:2 + hq, 8:8 + d] = s["q"]
+    wide_o = torch.full((hq, 3, dv + 24), 5.0, dtype=s["dt"], device="cuda")
+    wide_t = torch.full((3, s["width"] + 7), -9, dtype=torch.int32, device="cuda")
+    wide_t[:, 3:3 + s["width"]] = s["table"]
+    wide_l = torch.full((3, hq + 3), 5.0, device="cuda")
+    wide_w = torch.full((3, s["width"] + 5), 5.0, device="cuda")
+    wide_w[:, 1:1 + s["width"]] = 0
+    layers = 3
+    bufs = []
+    for b in s["bufs"]:
+        bufs += [torch.full_like(b, float("nan")), b, torch.full_like(b, float("nan"))]
+    dd = hc.PoolDesc(layers, len(s["bufs"]), P, 2, s["desc"].row_elems, 1, hc.PAGE_FIRST, 0, 0, 0)
+    hc.decode_attention(hc.DeviceKV(bufs, s["Dp"]), dd, 1, wide_q[:, 2:2 + hq, 8:8 + d], wide_t[:, 3:3 + s["width"]],
+                        s["lens"], wide_o.transpose(0, 1)[:, :, 16:16 + dv], ws, weights=wide_w[:, 1:1 + s["width"]],
+                        lse=wide_l[:, 2:2 + hq])
+    assert torch.equal(wide_o.transpose(0, 1)[:, :, 16:16 + dv], out)
+    assert (wide_o[..., :16] == 5).all() and (wide_o[..., 16 + dv:] == 5).all()
+    assert torch.equal(wide_l[:, 2:2 + hq], lse) and (wide_l[:, :2] == 5).all() and (wide_l[:, 2 + hq:] == 5).all()
+    assert torch.equal(wide_w[:, 1:1 + s["width"]], w) and (wide_w[:, 0] == 5).all()
+    # a broadcast query
+    one = s["q"][:1, :1].expand(3, hq, d)
+    a, b = torch.empty_like(out), torch.empty_like(out)
+    s["q"] = one
+    plain_call(s, a, ws)
+    s["q"] = one.contiguous()
+    plain_call(s, b, ws)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_far_pages(latent):
+    """Pages whose byte and element offsets pass 32 bits."""
+    d = 576 if latent else 128
+    row, P, hk = (576, 64, 1) if latent else (1024, 64, 8)
+    dp = (5 << 30) // row // P
+    buf = torch.empty((dp * P, row), dtype=torch.bfloat16, device="cuda")
+    pages = [dp - 1, 0, dp - 2, dp // 2, dp - 3]
+    rows = torch.cat([torch.arange(p * P, (p + 1) * P, device="cuda") for p in pages])
+    vals = torch.randn((rows.numel(), row), generator=gen(4), device="cuda").to(torch.bfloat16)
+    buf[rows] = vals
+    small = torch.cat([vals])
+    q = torch.randn((1, 8, d), generator=gen(5), device="cuda").to(torch.bfloat16)
+    dv = 512 if latent else d
+    outs = []
+    for b, n, t in ((buf, dp, pages), (small, len(pages), list(range(len(pages))))):
+        bufs = [b] if latent else [b, b]
+        dd = desc(P, row, 2, len(bufs))
+        out = torch.empty((1, 8, dv), dtype=torch.bfloat16, device="cuda")
+        ws = torch.zeros(hc.decode_workspace(dd, 1, 8, d, dv, len(pages)), dtype=torch.uint8, device="cuda")
+        hc.decode_attention(hc.DeviceKV(bufs, n), dd, 0, q, torch.tensor([t], dtype=torch.int32, device="cuda"),
+                            torch.tensor([P * 5 - 3], dtype=torch.int32, device="cuda"), out, ws)
+        outs.append(out)
+    assert torch.equal(*outs)
+    if not latent:        # the append finds the same rows
+        slots = rows[torch.randperm(rows.numel(), generator=gen(6), device="cuda")[:50]]
+        k = torch.randn((50, 8, 128), generator=gen(7), device="cuda").to(torch.bfloat16)
+        hc.append_kv(hc.DeviceKV([buf, buf], dp), desc(P, row, 2), 0, None, k, k, slots)
+        assert torch.equal(buf[slots], k.reshape(50, row))
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_repeats_streams_and_one_workspace(latent):
+    """The same bits each time, on any stream, with a workspace that calls of
+    other shapes used in between."""
+    d, dv = (576, 512) if latent else (128, 128)
+    big = decode_inputs([5000, 70, 0, 3000], 16, 4, d, 16, latent=latent, seed=2)
+    small = decode_inputs([90, 4] * 9, 16, 4, d, 16, latent=latent, seed=3, width=400)
+    n = max(workspace(x, 16, d, dv, True).numel() for x in (big, small))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    first = {}
+    streams = [None, torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(6):
+        stream = streams[turn % 3]
+        for name, x in (("big", big), ("small", small)):
+            out = torch.empty((x["q"].shape[0], 16, dv), dtype=x["dt"], device="cuda")
+            w = torch.zeros((x["q"].shape[0], x["width"]), device="cuda")
+            torch.cuda.synchronize()
+            plain_call(x, out, ws, weights=w, stream=stream)
+            torch.cuda.synchronize()
+            if name in first:
+                assert torch.equal(first[name][0], out) and torch.equal(first[name][1], w)
+            first[name] = (out, w)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_graphs(latent):
+    """Captured once, replayed with other lengths and pages; two graphs with a
+    workspace each replayed together."""
+    d, dv = (576, 512) if latent else (128, 128)
+    lens = [2000, 64, 900]
+    sets = [decode_inputs(lens, 8, 2, d, 16, latent=latent, seed=i) for i in (11, 12)]
+    graphs, outs, ws, wts = [], [], [], []
+    for s in sets:
+        o = torch.empty((3, 8, dv), dtype=s["dt"], device="cuda")
+        k = workspace(s, 8, d, dv, True)
+        w = torch.zeros((3, s["width"]), device="cuda")
+        plain_call(s, o, k, weights=w)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plain_call(s, o, k, weights=w, stream=torch.cuda.current_stream())
+        graphs.append(g)
+        outs.append(o)
+        ws.append(k)
+        wts.append(w)
+    streams = [torch.cuda.Stream() for _ in sets]
+    for shorter in (0, 3, 61):
+        want = []
+        for s, w in zip(sets, wts):
+            s["lens"].copy_(torch.tensor([n - shorter for n in lens], dtype=torch.int32))
+            w.zero_()
+            o, w2 = torch.empty((3, 8, dv), dtype=s["dt"], device="cuda"), torch.zeros_like(w)
+            plain_call(s, o, workspace(s, 8, d, dv, True), weights=w2)
+            want.append((o, w2))
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for w in wts:
+                w.zero_()
+            torch.cuda.synchronize()
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+            torch.cuda.synchronize()
+            for o, w, (a, b) in zip(outs, wts, want):
+                assert torch.equal(o, a) and torch.equal(w, b)
+
+
+def test_decode_random_corpus():
+    """Random shapes over the documented ranges."""
+    rnd = random.Random(20)
+    for i in range(60):
+        latent = rnd.random() < 0.25
+        e4 = not latent and rnd.random() < 0.4
+        unit = 16 if e4 else 8
+        d = 576 if latent else unit * rnd.randint(1, 256 // unit)
+        hk = 1 if latent else rnd.randint(1, 4)
+        group = rnd.choice((1, 2, 3, 4, 7, 8, 9, 16, 17, 33))
+        P = rnd.choice((1, 2, 3, 16, 37, 64, 128))
+        lens = [int(2 ** rnd.uniform(0, 11)) - 1 for _ in range(rnd.randint(1, 12))]
+        run_decode(lens, hk * group, hk, d, P, rnd.choice(("bf16", "fp16")), e4, latent,
+                   window=rnd.choice((0, 0, rnd.randint(1, 2000))), weights=rnd.random() < 0.5,
+                   holes=rnd.random() < 0.3, seed=i, scale=192 ** -0.5 if latent else None)
+
+
+# ---- eviction -------------------------------------------------------------------
+
+def run_evict(table, w, lens, keep, P, sink, recent, cap, in_place, pad=0):
+    t = torch.tensor(table, dtype=torch.int32, device="cuda")
+    wt = torch.tensor(w, dtype=torch.float32, device="cuda")
+    b, width = t.shape
+    if pad:
+        t = torch.cat([t, torch.full((b, pad), 77, dtype=torch.int32, device="cuda")], 1)[:, :width]
+        wt = torch.cat([wt, torch.full((b, pad), 77.0, device="cuda")], 1)[:, :width]
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kp = torch.tensor(keep, dtype=torch.int32, device="cuda")
+    vic = torch.full((b, max(1, cap)), -7, dtype=torch.int32, device="cuda")[:, :cap]
+    cnt = torch.full((b,), -7, dtype=torch.int32, device="cuda")
+    if in_place:
+        before = t.clone(), wt.clone()
+        ot, ow, ol = t, wt, ln
+        hc.evict_pages(P, t, ln, wt, kp, vic, cnt, sink=sink, recent=recent)
+    else:
+        ot, ow, ol = torch.full_like(t, 55), torch.full_like(wt, 55.0), torch.full_like(ln, 55)
+        before = ot.clone(), ow.clone()
+        hc.evict_pages(P, t, ln, wt, kp, vic, cnt, sink=sink, recent=recent, out_table=ot, out_weights=ow, out_lens=ol)
+    exact = [[float(np.float32(x)) for x in r] for r in w]
+    for i, (v, tt, ww, n) in enumerate(ref.evict(table, exact, lens, keep, P, sink, recent, cap)):
+        assert cnt[i].item() == len(v) and ol[i].item() == n
+        assert vic[i, :len(v)].tolist() == v and (vic[i, len(v):] == -7).all()
+        m = len(tt)
+        assert ot[i, :m].tolist() == tt and torch.equal(ot[i, m:], before[0][i, m:])
+        assert torch.equal(raw(ow)[i, :m], raw(torch.tensor(ww, dtype=torch.float32, device="cuda")))
+        assert torch.equal(raw(ow)[i, m:], raw(before[1])[i, m:])
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_small_and_special(in_place):
+    w = [[3.0, 1.0, 2.0, 1.0, 0.0, -0.0, 0.0, 5.0],
+         [NAN, INF, -INF, -1.0, 1e-45, -1e-45, 0.0, NAN],
+         [1.0] * 8, [0.0] * 8, [NAN] * 8, [2.0] * 8, [2.0] * 8, [1.0, 2.0] * 4]
+    table = [[10 * i + j for j in range(8)] for i in range(8)]
+    table[5][3] = -1
+    lens = [32, 30, 29, 0, 31, -4, 1, 1 << 30]
+    for keep in ([4] * 8, [0] * 8, [-3] * 8, [100] * 8, [1, 2, 3, 4, 5, 6, 7, 7]):
+        for sink, recent, cap in ((0, 1, 8), (2, 1, 8), (0, 3, 8), (0, 1, 2), (0, 1, 0), (7, 1, 8), (0, 100, 8), (50, 1, 8)):
+            run_evict(table, w, lens, keep, 4, sink, recent, cap, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,b,kinds", [(1, 3, 2), (31, 2, 3), (1023, 2, 5), (1024, 2, 0), (1025, 3, 0), (2049, 300, 4),
+                                       (5000, 2, 0), (40000, 2, 9), (131072, 3, 0), (300001, 1, 3)])
+def test_evict_sizes(n, b, kinds, in_place):
+    """kinds > 0: that many different weights only, so that most are equal."""
+    rng = np.random.default_rng(n + b)
+    w = rng.integers(0, kinds, (b, n)).astype(np.float32) if kinds else rng.standard_normal((b, n)).astype(np.float32)
+    lens = [int(x) for x in rng.integers(0, 3 * n + 1, b)]
+    lens[0] = 3 * n - 1
+    keep = [int(x) for x in rng.integers(0, n + 1, b)]
+    run_evict(rng.integers(-1, 10 ** 6, (b, n)).tolist(), w.tolist(), lens, keep, 3, int(rng.integers(0, 5)),
+              int(rng.integers(1, 5)), n if b < 3 else max(1, n // 3), in_place, pad=5)
+
+
+# ---- together --------------------------------------------------------------------
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_serving_step_through_both_tiers(latent):
+    """Prefill and decode steps through append and attention, pages evicted by
+    their weight and backed up to the host, loaded back into other pages behind
+    a per-layer wait, and attended to again: each against the plain forms."""
+    L, P, B, steps = 2, 8, 3, 5
+    hq, hk, d = (8, 1, 576) if latent else (8, 2, 64)
+    dv, row = (512, 576) if latent else (64, 128)
+    nb = 1 if latent else 2
+    dp, width = 80, 24
+    g = gen(21)
+    bf = torch.bfloat16
+    bufs = [torch.full((dp * P, row), float("nan"), dtype=bf, device="cuda") for _ in range(nb * L)]
+    kv = hc.DeviceKV(bufs, dp)
+    free = list(range(dp))
+    random.Random(3).shuffle(free)
+    lens = [100, 37, 9]
+    table = [[-1] * width for _ in range(B)]
+    cs = torch.randn((400, 64), generator=g, device="cuda")
+    kw = (1 + 0.1 * torch.randn(512 if latent else d, generator=g, device="cuda")).to(bf)
+    off = 512 if latent else 0
+    comp, xfer = torch.cuda.Stream(), torch.cuda.Stream()
+    with hc.Pool(L, nb, P, row, 64, "page_first") as pool:
+        ws = torch.zeros(hc.decode_workspace(pool, B, hq, d, dv, width, True), dtype=torch.uint8, device="cuda")
+
+        def slot(i, t):
+            if table[i][t // P] < 0:
+                table[i][t // P] = free.pop()
+            return table[i][t // P] * P + t % P
+
+        def append(layer, slots, positions):
+            n = len(slots)
+            k = torch.randn((n, hk, d), generator=g, device="cuda").to(bf)
+            v = None if latent else torch.randn((n, hk, d), generator=g, device="cuda").to(bf)
+            q = torch.randn((n, hq, d), generator=g, device="cuda").to(bf)
+            raw_q = q.clone()
+            sl, po = (torch.tensor(x, device="cuda") for x in (slots, positions))
+            hc.append_kv(kv, pool, layer, q, k, v, sl, positions=po, cos_sin=cs, rot_offset=off, k_weight=kw,
+                         stream=torch.cuda.current_stream())
+            y, err = ref.norm_rotate(k.double(), kw, cs[po], off, False, 1e-6)
+            got = bufs[layer][sl].double().view(n, hk, d)
+            assert ((got - y).abs() <= err + (y.abs() + err) * 2.0 ** -8).all()
+            y, err = ref.norm_rotate(raw_q.double(), None, cs[po], off, False, 1e-6)
+            assert ((q.double() - y).abs() <= err + (y.abs() + err) * 2.0 ** -8).all()
+            return q
+
+        def attend(layer, q, weights):
+            t = torch.tensor(table, dtype=torch.int32, device="cuda")
+            n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+            out = torch.empty((B, hq, dv), dtype=bf, device="cuda")
+            before = weights.clone()
+            hc.decode_attention(kv, pool, layer, q, t, n, out, ws, weights=weights, decay=0.75,
+                                stream=torch.cuda.current_stream())
+            k = bufs[layer].view(dp * P, hk, d)
+            v = k[..., :512] if latent else bufs[L + layer].view(dp * P, hk, d)
+            want = ref.decode(q, k, v, table, lens, P, d ** -0.5)
+            ref.check_decode(out, want, bf, bf, None, weights, before, 0.75)
+            return out
+
+        with torch.cuda.stream(comp):
+            weights = torch.zeros((B, width), device="cuda")
+            for layer in range(L):
+                append(layer, [slot(i, t) for i in range(B) for t in range(lens[i])],
+                       [t for i in range(B) for t in range(lens[i])])
+            for _ in range(steps):
+                at = [slot(i, lens[i]) for i in range(B)]
+                pos = list(lens)
+                lens = [n + 1 for n in lens]
+                for layer in range(L):
+                    attend(layer, append(layer, at, pos), weights)
+            # the least attended pages of each sequence leave for the host
+            t = torch.tensor(table, dtype=torch.int32, device="cuda")
+            n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+            keep = torch.tensor([5, 3, 10], dtype=torch.int32, device="cuda")
+            vic = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+            cnt = torch.empty(B, dtype=torch.int32, device="cuda")
+            exp = ref.evict(table, weights.tolist(), lens, [5, 3, 10], P, 1, 1, width)
+            hc.evict_pages(P, t, n, weights, keep, vic, cnt, sink=1, recent=1, stream=comp)
+            comp.synchronize()
+            victims = [vic[i, :c].tolist() for i, c in enumerate(cnt.tolist())]
+            assert victims == [e[0] for e in exp] and cnt.tolist()[0] > 0 and cnt.tolist()[2] == 0
+            old_table, old_lens = [list(r) for r in table], list(lens)
+            gone = [p for r in victims for p in r]
+            pool.backup(kv, gone, list(range(len(gone))), stream=comp)
+            q = torch.randn((B, hq, d), generator=g, device="cuda").to(bf)
+            whole = attend(1, q, torch.zeros((B, width), device="cuda"))
+            table = [r[1] + [-1] * (width - len(r[1])) for r in exp]
+            assert t.tolist() == table and n.tolist() == [e[3] for e in exp]
+            lens = [e[3] for e in exp]
+            attend(0, q, weights)                       # what stays
+        comp.synchronize()
+        # back into other pages, attention behind the layer's wait
+        new = [free.pop() for _ in gone]
+        for b in bufs:
+            b.view(dp, P, row)[gone] = float("nan")
+        torch.cuda.synchronize()
+        pool.load_pipelined(kv, new, list(range(len(gone))), stream=xfer)
+        pool.wait_layer(1, comp)
+        moved = dict(zip(gone, new))
+        table = [[moved.get(p, p) for p in r] for r in old_table]
+        lens = old_lens
+        with torch.cuda.stream(comp):
+            again = attend(1, q, torch.zeros((B, width), device="cuda"))
+        torch.cuda.synchronize()
+        assert torch.equal(whole, again)

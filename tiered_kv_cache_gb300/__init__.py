@@ -13,6 +13,7 @@ Names follow the C ABI in ``include/hicache.h``:
     Engine (submission engine), PageAllocator (host pages)
     host_alloc / host_free, wait, prepass, segment_count, page_span, layer_checksum
     tp_share / tp_load_pipelined / Pool.layer_counters (tensor-parallel load of a replicated latent)
+    append_kv / decode_attention / decode_workspace / evict_pages (operators on the device pages)
     stream_copy (roofline probe: plain zero-copy streaming copy)
     checked_build / check_status (the bounds-checked build, HICACHE_CHECKED=1)
 """
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -31,7 +33,7 @@ __all__ = [
     "MAX_GROUP", "PAGE_FIRST_DIRECT_KV",
     "host_alloc", "host_free", "wait", "prepass", "segment_count", "layer_checksum", "page_span",
     "launch_count", "version", "stream_copy", "tp_share", "tp_load_pipelined", "checked_build",
-    "check_status",
+    "check_status", "append_kv", "decode_attention", "decode_workspace", "evict_pages",
 ]
 
 LAYOUT_POOL = -1
@@ -143,6 +145,10 @@ def _bind(lib):
         "hicache_allocator_alloc": (ctypes.c_int, [_vp, _i64, _vp]),
         "hicache_allocator_free": (ctypes.c_int, [_vp, _vp, _i64]),
         "hicache_allocator_available": (_i64, [_vp]),
+        "hicache_append_kv": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
+        "hicache_decode_attention": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
+        "hicache_decode_workspace": (ctypes.c_int, [_P(PoolDesc), _i32, _i32, _i32, _i32, _i32, _i32, _P(_i64)]),
+        "hicache_evict_pages": (ctypes.c_int, [ctypes.c_char_p, _vp]),
         "hicache_layer_checksum": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _vp, _i64, _i32,
                                                   _i32, _vp, _vp]),
     }
@@ -729,3 +735,227 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+# ---- operators on the device pages ------------------------------------------------
+# The descriptors of include/hicache.h, field by field in their order there.
+_APPEND_DESC = struct.Struct("9P10q9i3f")
+_DECODE_DESC = struct.Struct("7P8q8i4f")
+_EVICT_DESC = struct.Struct("9P5q6i")
+BF16 = 0
+FP16 = 1
+
+
+def _tensor(name, t, dtype, ndim, device):
+    """Checks a torch tensor argument: type, dimensions, a contiguous innermost
+    dimension, and the device the call runs on."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected {ndim}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.stride(-1) != 1 and t.size(-1) > 1:
+        raise ValueError(f"{name}: the innermost dimension must be contiguous")
+    return t
+
+
+def _shape(name, t, shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
+def _activations(name, t):
+    """(dtype code, device) of the tensor that decides both for a call: a
+    [n, heads, dim] tensor on the current CUDA device."""
+    import torch
+    code = BF16 if t.dtype == torch.bfloat16 else FP16 if t.dtype == torch.float16 else -1
+    if code < 0:
+        raise ValueError(f"{name}: {t.dtype}, expected bfloat16 or float16")
+    _current(name, t)
+    return code, t.device
+
+
+def _current(name, t):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, expected the current CUDA device")
+
+
+def _pool_desc(pool_or_desc) -> PoolDesc:
+    return pool_or_desc.desc if isinstance(pool_or_desc, Pool) else pool_or_desc
+
+
+def _check_cache(kv, desc, layer, device):
+    """The cache must hold desc's buffers; its torch tensors must be on the
+    call's device and hold the pages they are said to (raw addresses cannot be
+    checked)."""
+    if kv.num_buffers_total != desc.num_buffers * desc.num_layers:
+        raise ValueError(f"DeviceKV has {kv.num_buffers_total} buffers, the pool "
+                         f"{desc.num_buffers} x {desc.num_layers}")
+    if not 0 <= layer < desc.num_layers:
+        return                       # the library's own error
+    need = kv.device_num_pages * desc.page_size * desc.row_elems * desc.elem_bytes
+    for b in range(desc.num_buffers):
+        t = kv._tensors[b * desc.num_layers + layer]
+        if isinstance(t, int):
+            continue
+        if t.device != device:
+            raise ValueError(f"the cache is on {t.device}, expected {device}")
+        if t.numel() * t.element_size() < need:
+            raise ValueError(f"a cache buffer has {t.numel() * t.element_size()} bytes, its pages need {need}")
+
+
+def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=None, positions=None, cos_sin=None,
+              rot_offset: int = 0, interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6,
+              k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+    """Norms of the query and key heads (over the first len(weight) elements;
+    none without a weight), the rotation of cos_sin.shape[1] elements from
+    rot_offset on by row positions[n] of cos_sin (cosines, then sines), and the
+    store of k and v into rows slots[n] of the layer's buffers.
+
+    q [n, q_heads, dim] -> q_out (None: in place); k, v [n, kv_heads, dim] (v is
+    None for a latent cache).  q, or k and v and slots, may be None."""
+    import torch
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are both None")
+    code, dev = _activations("q" if q is not None else "k", first)
+    dt = first.dtype
+    desc = _pool_desc(pool_or_desc)
+    _check_cache(kv, desc, layer, dev)
+    n, dim = first.shape[0], first.shape[-1]
+    qp = op = kp = vp = qst = qsh = ost = osh = kst = ksh = vst = vsh = hq = hk = 0
+    if q is not None:
+        _tensor("q", q, dt, 3, dev)
+        o = q if q_out is None else _tensor("q_out", q_out, dt, 3, dev)
+        hq = q.shape[1]
+        _shape("q_out", o, (n, hq, dim))
+        qp, op = q.data_ptr(), o.data_ptr()
+        qst, qsh, _ = q.stride()
+        ost, osh, _ = o.stride()
+    sp = 0
+    if k is not None:
+        hk = k.shape[1]
+        _tensor("k", k, dt, 3, dev)
+        _shape("k", k, (n, hk, dim))
+        kp = k.data_ptr()
+        kst, ksh, _ = k.stride()
+        if (v is None) != (desc.num_buffers == 1):
+            raise ValueError("a K, V cache takes v, a latent cache none")
+        if v is not None:
+            _tensor("v", v, dt, 3, dev)
+            _shape("v", v, (n, hk, dim))
+            vp = v.data_ptr()
+            vst, vsh, _ = v.stride()
+        _shape("slots", _tensor("slots", slots, torch.int64, 1, dev), (n,))
+        sp = slots.data_ptr()
+    elif v is not None:
+        raise ValueError("v without k")
+    qw = kw = qn = kn = 0
+    if q_weight is not None:
+        qw, qn = _tensor("q_weight", q_weight, dt, 1, dev).data_ptr(), q_weight.shape[0]
+    if k_weight is not None:
+        kw, kn = _tensor("k_weight", k_weight, dt, 1, dev).data_ptr(), k_weight.shape[0]
+    pp = cp = rows = rot = 0
+    if cos_sin is not None:
+        _tensor("cos_sin", cos_sin, torch.float32, 2, dev)
+        rows, rot = cos_sin.shape
+        if rows > 1 and cos_sin.stride(0) != rot:
+            raise ValueError("cos_sin must be contiguous")
+        if positions is None:
+            raise ValueError("cos_sin without positions")
+        _shape("positions", _tensor("positions", positions, torch.int64, 1, dev), (n,))
+        pp, cp = positions.data_ptr(), cos_sin.data_ptr()
+    a = _APPEND_DESC.pack(qp, op, kp, vp, qw, kw, sp, pp, cp, qst, qsh, ost, osh, kst, ksh, vst, vsh, n, rows,
+                          code, hq, hk, dim, qn, kn, rot, rot_offset, bool(interleaved), eps, k_scale, v_scale)
+    _check(library().hicache_append_kv(kv.ref, ctypes.byref(desc), layer, a, _stream(stream)))
+
+
+def decode_workspace(pool_or_desc, batch: int, q_heads: int, head_dim: int, v_dim: int, max_pages: int,
+                     weights: bool = False) -> int:
+    """Bytes of workspace a decode_attention of these sizes needs.  Zero-fill
+    it once; calls that may run at the same time need one each."""
+    out = ctypes.c_int64()
+    _check(library().hicache_decode_workspace(ctypes.byref(_pool_desc(pool_or_desc)), batch, q_heads, head_dim, v_dim,
+                                              max_pages, int(weights), ctypes.byref(out)))
+    return out.value
+
+
+def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_lens, out, workspace, *, scale=None,
+                     window: int = 0, weights=None, decay: float = 1.0, lse=None, k_scale: float = 1.0,
+                     v_scale: float = 1.0, stream=None):
+    """Attention of one new token per sequence: q [batch, q_heads, head_dim]
+    over the first seq_lens[b] tokens of the pages page_table[b] (int32; the last
+    `window` of them if window > 0) into out [batch, q_heads, v_dim]; lse
+    (optional) [batch, q_heads] the log of the softmax sums; weights (optional)
+    [batch, max_pages] <- decay * weights + the attention each page received.
+    scale: head_dim ** -0.5 unless given."""
+    import torch
+    code, dev = _activations("q", q)
+    dt = q.dtype
+    desc = _pool_desc(pool_or_desc)
+    _check_cache(kv, desc, layer, dev)
+    _tensor("q", q, dt, 3, dev)
+    b, hq, d = q.shape
+    _tensor("out", out, dt, 3, dev)
+    dv = out.shape[-1]
+    _shape("out", out, (b, hq, dv))
+    _tensor("page_table", page_table, torch.int32, 2, dev)
+    width = page_table.shape[1]
+    _shape("page_table", page_table, (b, width))
+    _shape("seq_lens", _tensor("seq_lens", seq_lens, torch.int32, 1, dev), (b,))
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on {dev}")
+    lp = wp = lst = wst = 0
+    if lse is not None:
+        _shape("lse", _tensor("lse", lse, torch.float32, 2, dev), (b, hq))
+        lp, lst = lse.data_ptr(), lse.stride(0)
+    if weights is not None:
+        _shape("weights", _tensor("weights", weights, torch.float32, 2, dev), (b, width))
+        wp, wst = weights.data_ptr(), weights.stride(0)
+    qb, qh, _ = q.stride()
+    ob, oh, _ = out.stride()
+    a = _DECODE_DESC.pack(q.data_ptr(), out.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), lp, wp,
+                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), qb, qh, ob, oh,
+                          page_table.stride(0), lst, wst, code, b, hq, d, dv, width, window, 0,
+                          d ** -0.5 if scale is None else scale, k_scale, v_scale, decay)
+    _check(library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _stream(stream)))
+
+
+def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, num_victims, *, sink: int = 0,
+                recent: int = 1, out_table=None, out_lens=None, out_weights=None, stream=None):
+    """Of each sequence's pages in [sink, n - recent), the ones with the lowest
+    weights leave until keep[b] are left (or none may go, or victims is full):
+    victims [batch, max_victims] receives their pages, num_victims their number,
+    and out_table, out_lens, out_weights (None: in place) what stays."""
+    import torch
+    _current("page_table", page_table)
+    dev = page_table.device
+    i32 = torch.int32
+    _tensor("page_table", page_table, i32, 2, dev)
+    b, width = page_table.shape
+    _shape("weights", _tensor("weights", weights, torch.float32, 2, dev), (b, width))
+    _shape("seq_lens", _tensor("seq_lens", seq_lens, i32, 1, dev), (b,))
+    _shape("keep", _tensor("keep", keep, i32, 1, dev), (b,))
+    _shape("num_victims", _tensor("num_victims", num_victims, i32, 1, dev), (b,))
+    _tensor("victims", victims, i32, 2, dev)
+    _shape("victims", victims, (b, victims.shape[1]))
+    if out_table is None:
+        out_table = page_table
+    else:
+        _shape("out_table", _tensor("out_table", out_table, i32, 2, dev), (b, width))
+    if out_weights is None:
+        out_weights = weights
+    else:
+        _shape("out_weights", _tensor("out_weights", out_weights, torch.float32, 2, dev), (b, width))
+    if out_lens is None:
+        out_lens = seq_lens
+    else:
+        _shape("out_lens", _tensor("out_lens", out_lens, i32, 1, dev), (b,))
+    a = _EVICT_DESC.pack(page_table.data_ptr(), weights.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(),
+                         victims.data_ptr(), num_victims.data_ptr(), out_table.data_ptr(), out_weights.data_ptr(),
+                         out_lens.data_ptr(), page_table.stride(0), weights.stride(0), victims.stride(0),
+                         out_table.stride(0), out_weights.stride(0), page_size, b, width, victims.shape[1], sink,
+                         recent)
+    _check(library().hicache_evict_pages(a, _stream(stream)))

@@ -1,6 +1,6 @@
 """Build libhicache.so in-tree with nvcc for sm_103a (GB300).
 
-Nine translation units, compiled in parallel, linked with the static CUDA
+Thirteen translation units, compiled in parallel, linked with the static CUDA
 runtime so the library loads on a machine without a GPU driver (and the
 kernel file a second time with HICACHE_CHECKED=1 for libhicache_checked.so,
 the bounds-checked build):
@@ -13,6 +13,10 @@ the bounds-checked build):
   csrc/hicache_alloc.cpp     LIFO host-page allocator
   csrc/hicache_engine.cpp    submission engine (queue + worker thread)
   csrc/hicache_tp.cpp        tensor-parallel load of a replicated latent
+  csrc/hicache_serving.cpp   checks of the operators on the device pages
+  csrc/hicache_append.cu     head norms, rotation and the store into the cache
+  csrc/hicache_decode.cu     attention of one new token over a paged cache
+  csrc/hicache_evict.cu      eviction of pages by accumulated attention weight
 """
 from __future__ import annotations
 
@@ -34,7 +38,8 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
           f"-I{INCLUDE}", f"-I{CSRC}"]
 SOURCES = ["hicache_kernels.cu", "hicache_api.cpp", "hicache_index.cpp", "hicache_pipeline.cpp",
            "hicache_plan.cpp", "hicache_group.cpp", "hicache_alloc.cpp", "hicache_engine.cpp",
-           "hicache_tp.cpp"]
+           "hicache_tp.cpp", "hicache_serving.cpp", "hicache_append.cu", "hicache_decode.cu",
+           "hicache_evict.cu"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,69 @@
+// hicache_serving.h -- kernel parameters shared by the operators on the device
+// pages (hicache_append.cu, hicache_decode.cu, hicache_evict.cu) and their
+// argument checks (hicache_serving.cpp).  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "hicache_internal.h"
+
+namespace hicache {
+
+struct AppendParams {
+  const void *q, *k, *v;
+  void *q_out;
+  const void *q_weight, *k_weight;
+  const int64_t *slots, *positions;
+  const float *cos_sin;
+  void *k_cache, *v_cache;    // the layer's buffers
+  int64_t q_st, q_sh, o_st, o_sh, k_st, k_sh, v_st, v_sh;   // token and head strides
+  int64_t num_tokens, cos_sin_rows, num_slots;
+  int64_t row;                // elements of a cache row
+  int32_t q_heads, kv_heads, D;
+  int32_t q_norm, k_norm, rot, rot_off;
+  int32_t interleaved, has_v;
+  int32_t bf16, e4m3;
+  float eps, k_scale, v_scale;
+};
+int launch_append(const AppendParams &p, void *stream);
+
+struct DecodeParams {
+  const void *q, *k, *v;      // k, v: the layer's buffers (v == k for a latent)
+  void *out;
+  const int32_t *table, *lens;
+  float *lse;                 // natural logarithm, or null
+  float *weights;             // or null
+  int64_t q_sb, q_sh, o_sb, o_sh, t_sb, lse_sb, w_sb;
+  int64_t row;                // elements of a cache row
+  int64_t num_pages;          // device pages
+  // workspace
+  float *scores;              // [batch, q_heads, score_row] in units of log2, if weights
+  float *lse2;                // [batch, q_heads] base-2 logarithm, if weights
+  int64_t score_row;
+  int32_t B, Hq, Hkv, G, D, Dv, P, max_pages, window;
+  int32_t bf16, e4m3, latent;
+  FastDiv fd_page;            // tokens per page
+  float scale2;               // scale * k_scale * log2(e)
+  float v_scale, decay;
+};
+// The workspace of a call: byte offsets of its parts.
+struct DecodeSpace {
+  int64_t lse2, scores, bytes;
+  int64_t score_row;
+};
+DecodeSpace decode_space(int64_t batch, int64_t q_heads, int64_t max_pages, int64_t page, bool weights);
+int launch_decode(const DecodeParams &p, void *stream, int *launches);
+
+struct EvictParams {
+  const int32_t *table;
+  const float *weights;
+  const int32_t *lens, *keep;
+  int32_t *victims, *num_victims, *out_table, *out_lens;
+  float *out_weights;
+  int64_t t_sb, w_sb, v_sb, ot_sb, ow_sb;
+  int32_t P, B, max_pages, max_victims, sink, recent;
+};
+int launch_evict(const EvictParams &p, void *stream);
+
+}  // namespace hicache
