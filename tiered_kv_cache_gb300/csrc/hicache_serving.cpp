@@ -92,8 +92,9 @@ int launched(int e, int n, const char *what) {
   return e ? cuda_error(cudaError_t(e), what) : HICACHE_OK;
 }
 
-int check_decode_sizes(const Shape &s, int64_t batch, int64_t q_heads, int64_t head_dim, int64_t v_dim,
-                       int64_t max_pages) {
+// Checks a call's sizes and fills them in.
+int decode_sizes(const Shape &s, int64_t batch, int64_t q_heads, int64_t head_dim, int64_t v_dim, int64_t max_pages,
+                 hicache::DecodeParams *p) {
   int rc = check_grid("batch", batch, 65535);
   if (rc) return rc;
   if (q_heads < 1 || q_heads > 4096 || head_dim < 1 || v_dim < 1 || max_pages < 1)
@@ -109,16 +110,29 @@ int check_decode_sizes(const Shape &s, int64_t batch, int64_t q_heads, int64_t h
                        "a latent cache has rows of 576 elements of 2 bytes, head_dim 576 and v_dim 512 "
                        "(row_elems %lld, elem_bytes %lld, head_dim %lld, v_dim %lld)",
                        (long long)s.R, (long long)s.es, (long long)head_dim, (long long)v_dim);
-    return HICACHE_OK;
-  }
-  const int64_t unit = 16 / s.es;
-  if (head_dim > 256 || head_dim % unit || v_dim != head_dim)
+  } else if (const int64_t unit = 16 / s.es; head_dim > 256 || head_dim % unit || v_dim != head_dim) {
     return set_error(HICACHE_ERR_INVALID_ARG, "head_dim %lld must be a multiple of %lld up to 256, v_dim %lld the same",
                      (long long)head_dim, (long long)unit, (long long)v_dim);
-  if (s.R % head_dim || q_heads % (s.R / head_dim))
+  } else if (s.R % head_dim || q_heads % (s.R / head_dim)) {
     return set_error(HICACHE_ERR_INVALID_ARG,
                      "rows of %lld elements must hold whole heads of %lld, and q_heads %lld be a multiple of their number",
                      (long long)s.R, (long long)head_dim, (long long)q_heads);
+  }
+  // tiles of 16 tokens per head, counted in 64 bits with room for the number of warps
+  if ((max_pages * s.P / 16 + 1) * batch > (int64_t(1) << 48) / q_heads)
+    return set_error(HICACHE_ERR_INVALID_ARG, "batch * max_pages * page_size * q_heads must be < 2^52");
+  p->B = int32_t(batch);
+  p->Hq = int32_t(q_heads);
+  p->D = int32_t(head_dim);
+  p->Dv = int32_t(v_dim);
+  p->row = s.R;
+  p->Hkv = int32_t(s.R / head_dim);
+  p->G = p->Hq / p->Hkv;
+  p->QB = (p->G + hicache::decode_rows(p->G) - 1) / hicache::decode_rows(p->G);
+  p->P = int32_t(s.P);
+  p->max_pages = int32_t(max_pages);
+  p->e4m3 = s.es == 1;
+  p->latent = s.B == 1;
   return HICACHE_OK;
 }
 
@@ -237,8 +251,9 @@ int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32
   int rc = check_desc(desc, &s, true);
   if (rc) return rc;
   if (!bytes) return set_error(HICACHE_ERR_INVALID_ARG, "bytes is NULL");
-  if ((rc = check_decode_sizes(s, batch, q_heads, head_dim, v_dim, max_pages))) return rc;
-  *bytes = hicache::decode_space(batch, q_heads, max_pages, s.P, with_weights != 0).bytes;
+  hicache::DecodeParams p{};
+  if ((rc = decode_sizes(s, batch, q_heads, head_dim, v_dim, max_pages, &p))) return rc;
+  *bytes = hicache::decode_space(p, with_weights != 0).bytes;
   return HICACHE_OK;
 }
 
@@ -254,7 +269,8 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
     return set_error(HICACHE_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
   if (a->reserved != 0) return set_error(HICACHE_ERR_INVALID_ARG, "reserved must be 0");
   if ((rc = check_scales(s, a->k_scale, a->v_scale))) return rc;
-  if ((rc = check_decode_sizes(s, a->batch, a->q_heads, a->head_dim, a->v_dim, a->max_pages))) return rc;
+  hicache::DecodeParams p{};
+  if ((rc = decode_sizes(s, a->batch, a->q_heads, a->head_dim, a->v_dim, a->max_pages, &p))) return rc;
   if (!std::isfinite(a->scale) || !std::isfinite(a->decay))
     return set_error(HICACHE_ERR_INVALID_ARG, "scale and decay must be finite");
   if (a->window < 0) return set_error(HICACHE_ERR_INVALID_ARG, "window must be >= 0");
@@ -273,11 +289,10 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   if (!aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->lse, 4) || !aligned(a->weights, 4))
     return set_error(HICACHE_ERR_ALIGNMENT, "page_table, seq_lens, lse or weights is not aligned to its elements");
   if (!aligned(a->workspace, 256)) return set_error(HICACHE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-  const hicache::DecodeSpace sp = hicache::decode_space(a->batch, a->q_heads, a->max_pages, s.P, a->weights != nullptr);
+  const hicache::DecodeSpace sp = hicache::decode_space(p, a->weights != nullptr);
   if (a->workspace_bytes < sp.bytes)
     return set_error(HICACHE_ERR_INVALID_ARG, "workspace of %lld bytes is below the %lld needed",
                      (long long)a->workspace_bytes, (long long)sp.bytes);
-  hicache::DecodeParams p{};
   char *ws = static_cast<char *>(a->workspace);
   p.q = a->q;
   p.k = k;
@@ -294,29 +309,23 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.t_sb = a->table_stride;
   p.lse_sb = a->lse_stride;
   p.w_sb = a->weights_stride;
-  p.row = s.R;
   p.num_pages = kv->device_num_pages;
+  p.counters = reinterpret_cast<unsigned int *>(ws);
+  p.cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
+  p.warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
   p.lse2 = reinterpret_cast<float *>(ws + sp.lse2);
   p.scores = reinterpret_cast<float *>(ws + sp.scores);
   p.score_row = sp.score_row;
-  p.B = a->batch;
-  p.Hq = a->q_heads;
-  p.D = a->head_dim;
-  p.Dv = a->v_dim;
-  p.Hkv = int32_t(s.R / a->head_dim);
-  p.G = p.Hq / p.Hkv;
-  p.P = int32_t(s.P);
-  p.max_pages = a->max_pages;
   p.window = a->window;
   p.bf16 = a->dtype == HICACHE_BF16;
-  p.e4m3 = s.es == 1;
-  p.latent = s.B == 1;
   p.fd_page = hicache::make_fastdiv(uint32_t(s.P));
   p.scale2 = float(double(a->scale) * double(a->k_scale) * 1.4426950408889634);
   p.v_scale = a->v_scale;
   p.decay = a->decay;
-  int n = 0;
-  const int e = hicache::launch_decode(p, stream, &n);
+  int n = 0, device = 0;
+  const cudaError_t de = cudaGetDevice(&device);
+  if (de != cudaSuccess) return cuda_error(de, "cudaGetDevice");
+  const int e = hicache::launch_decode(p, device, stream, &n);
   return launched(e, n, "decode kernel launch");
 }
 

@@ -37,7 +37,10 @@ struct DecodeParams {
   int64_t q_sb, q_sh, o_sb, o_sh, t_sb, lse_sb, w_sb;
   int64_t row;                // elements of a cache row
   int64_t num_pages;          // device pages
+  int32_t QB;                 // units of a kv head: its G query heads by decode_rows(G)
   // workspace
+  unsigned int *counters;     // kDecodeCtas, zero between calls
+  float *cta_parts, *warp_parts;
   float *scores;              // [batch, q_heads, score_row] in units of log2, if weights
   float *lse2;                // [batch, q_heads] base-2 logarithm, if weights
   int64_t score_row;
@@ -47,13 +50,20 @@ struct DecodeParams {
   float scale2;               // scale * k_scale * log2(e)
   float v_scale, decay;
 };
-// The workspace of a call: byte offsets of its parts.
+// Query heads of a unit of work (the rows of a product), and the CTAs of a
+// launch: one on each of a GB300's 152 SMs.
+HC_HD int decode_rows(int group) { return group <= 8 ? 8 : 16; }
+constexpr int kDecodeCtas = 152;
+// The workspace of a call: byte offsets of its parts (from the sizes in p).
 struct DecodeSpace {
-  int64_t lse2, scores, bytes;
+  int64_t cta_parts, warp_parts, lse2, scores, bytes;
   int64_t score_row;
 };
-DecodeSpace decode_space(int64_t batch, int64_t q_heads, int64_t max_pages, int64_t page, bool weights);
-int launch_decode(const DecodeParams &p, void *stream, int *launches);
+DecodeSpace decode_space(const DecodeParams &p, bool weights);
+int launch_decode(const DecodeParams &p, int device, void *stream, int *launches);
+
+// Whether a page table's entry is a page of the cache (else it counts as absent).
+HC_HD bool page_present(int32_t page, int64_t num_pages) { return page >= 0 && page < num_pages; }
 
 struct EvictParams {
   const int32_t *table;
