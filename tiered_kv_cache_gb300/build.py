@@ -1,6 +1,6 @@
 """Build libhicache.so in-tree with nvcc for sm_103a (GB300).
 
-Thirteen translation units, compiled in parallel, linked with the static CUDA
+Fourteen translation units, compiled in parallel, linked with the static CUDA
 runtime so the library loads on a machine without a GPU driver (and the
 kernel file a second time with HICACHE_CHECKED=1 for libhicache_checked.so,
 the bounds-checked build):
@@ -16,6 +16,7 @@ the bounds-checked build):
   csrc/hicache_serving.cpp   checks of the operators on the device pages
   csrc/hicache_append.cu     head norms, rotation and the store into the cache
   csrc/hicache_decode.cu     attention of one new token over a paged cache
+  csrc/hicache_decode_latent.cu  the same over a latent cache
   csrc/hicache_evict.cu      eviction of pages by accumulated attention weight
 """
 from __future__ import annotations
@@ -39,7 +40,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 SOURCES = ["hicache_kernels.cu", "hicache_api.cpp", "hicache_index.cpp", "hicache_pipeline.cpp",
            "hicache_plan.cpp", "hicache_group.cpp", "hicache_alloc.cpp", "hicache_engine.cpp",
            "hicache_tp.cpp", "hicache_serving.cpp", "hicache_append.cu", "hicache_decode.cu",
-           "hicache_evict.cu"]
+           "hicache_decode_latent.cu", "hicache_evict.cu"]
 
 
 def _nvcc() -> str:
@@ -69,7 +70,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     same parallel batch."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")]
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     headers.append(os.path.join(INCLUDE, "hicache.h"))
     flags = COMMON + (extra_flags or [])
     objs, procs = [], []

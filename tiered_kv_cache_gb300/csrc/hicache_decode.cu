@@ -20,31 +20,16 @@
 // pieces exist depends on the lengths alone and they are added in order, so
 // timing cannot change the result.
 //
-// Latent caches: one CTA per sequence and query head; its warps take the tokens
-// in turn, each with a running maximum and sum of its own, and are joined in
-// shared memory.
+// Latent caches: hicache_decode_latent.cu.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
-#include <cuda_runtime.h>
 
 #include <atomic>
 
-#include "hicache_serving.h"
+#include "hicache_decode.cuh"
 
 namespace hicache {
 namespace {
-
-constexpr float kLn2 = 0.693147180559945309f;
-
-// The tokens [start, len) that sequence b attends to.
-__device__ __forceinline__ void seq_range(const DecodeParams &p, int b, int *start, int *len) {
-  const int64_t cap = int64_t(p.max_pages) * p.P;
-  const int n = max(0, __ldg(p.lens + b));
-  *len = int(min(int64_t(n), cap));
-  *start = p.window > 0 ? max(0, *len - p.window) : 0;
-}
 
 // ---- K, V caches -----------------------------------------------------------------
 
@@ -73,18 +58,6 @@ struct KvConfig {
   static constexpr int SMEM = WARPS * RING_B;
   static_assert(STAGES >= 2 && RING_B >= ROWS_ * DP_ * 4, "ring");
 };
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
-
-// 16 bytes, of which the first `bytes` (0 or 16) are read and the rest is zero
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t *r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -115,16 +88,6 @@ __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, ui
         : "r"(a[0]), "r"(a1), "r"(a[2]), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-}
 __device__ __forceinline__ float2 unpack2(uint32_t u, bool bf16) {
   return bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u))
               : __half22float2(*reinterpret_cast<const __half2 *>(&u));
@@ -140,12 +103,6 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
   asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi;}" : "=r"(r) : "r"(w));
   return r;
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // Where chunk c of row r lies in its row of shared memory.  2-byte types: eight
 // rows at one chunk (ldmatrix) fall on eight different 16-byte bank groups.
 // e4m3 K: 16-byte loads of four chunks of two rows; e4m3 V: 4-byte loads of
@@ -172,21 +129,6 @@ struct TileMeta {
   uint32_t flags;
   int32_t b, u, t0;   // sequence, unit within it, first token
 };
-
-__device__ __forceinline__ void store_out(const DecodeParams &p, int b, int h, int col, float v) {
-  if (col >= p.D) return;
-  const int64_t at = int64_t(b) * p.o_sb + int64_t(h) * p.o_sh + col;
-  if (p.bf16)
-    static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half *>(p.out)[at] = __float2half_rn(v);
-}
-// l == 0: nothing attended to
-__device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int h, float m, float l) {
-  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-  if (p.lse) p.lse[int64_t(b) * p.lse_sb + h] = lse2 * kLn2;
-  if (p.weights) p.lse2[int64_t(b) * p.Hq + h] = lse2;
-}
 
 __device__ __forceinline__ int tiles_of(int start, int len) {
   return len > start ? (len + kTok - 1) / kTok - start / kTok : 0;
@@ -219,21 +161,11 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     seq_range(p, b, &start, &len);
     mine += tiles_of(start, len);
   }
-  long long inc = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) warp_tot[warp] = inc;
   if (lane < 2) piece_state[warp][lane] = 0;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < C::WARPS; ++w) {
-    if (w < warp) before += warp_tot[w];
-    total += warp_tot[w];
-  }
+  long long total = 0;
+  const long long before = block_prefix<C::WARPS>(mine, warp_tot, &total);
   total *= units;
-  prefix[tid] = (before + inc - mine) * units;
+  prefix[tid] = before * units;
   if (tid == 0) prefix[THREADS] = total;
   __syncthreads();
 
@@ -245,6 +177,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     for (int i = tid; i < p.Hq * DP; i += THREADS) store_out(p, b, i / DP, i % DP, 0.f);
     for (int h = tid; h < p.Hq; h += THREADS) store_lse(p, b, h, 0.f, 0.f);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // with fewer tiles than CTAs, only as many CTAs take part: each has a tile then
   const long long n_cta = min((long long)gridDim.x, total);
   if (blockIdx.x >= n_cta) return;
@@ -673,94 +607,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   }
 }
 
-// ---- latent caches ---------------------------------------------------------------
-
-constexpr int kSimpleWarps = 8;
-constexpr int kSimpleElems = 18;   // elements of a row per lane: rows of up to 576
-
-__device__ __forceinline__ float load_elem(const void *base, int64_t i, bool bf16, bool e4m3) {
-  if (e4m3) {
-    __nv_fp8_e4m3 x;
-    x.__x = static_cast<const uint8_t *>(base)[i];
-    return float(x);
-  }
-  if (bf16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[i]);
-  return __half2float(static_cast<const __half *>(base)[i]);
-}
-
-__global__ void __launch_bounds__(kSimpleWarps * 32) decode_simple_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ float sm_m[kSimpleWarps], sm_l[kSimpleWarps];
-  __shared__ float sm_o[kSimpleWarps][kSimpleElems * 32];
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  const int kvh = h / p.G;
-  const int64_t cap = int64_t(p.max_pages) * p.P;
-  const int len = int(min(int64_t(max(0, p.lens[b])), cap));
-  const int start = p.window > 0 ? max(0, len - p.window) : 0;
-  float q[kSimpleElems], o[kSimpleElems];
-#pragma unroll
-  for (int j = 0; j < kSimpleElems; ++j) {
-    const int i = lane + 32 * j;
-    q[j] = i < p.D ? load_elem(p.q, b * p.q_sb + h * p.q_sh + i, p.bf16, false) : 0.f;
-    o[j] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int t = start + warp; t < len; t += kSimpleWarps) {
-    const int pg = int(fast_div(uint32_t(t), p.fd_page));
-    const int page = p.table[b * p.t_sb + pg];
-    float s = -INFINITY;
-    if (page_present(page, p.num_pages)) {
-      const int64_t row = (int64_t(page) * p.P + (t - pg * p.P)) * p.row + int64_t(kvh) * p.D;
-      float a = 0.f;
-#pragma unroll
-      for (int j = 0; j < kSimpleElems; ++j) {
-        const int i = lane + 32 * j;
-        if (i < p.D) a = fmaf(q[j], load_elem(p.k, row + i, p.bf16, p.e4m3), a);
-      }
-      for (int x = 16; x > 0; x >>= 1) a += __shfl_xor_sync(0xffffffffu, a, x);
-      s = a * p.scale2;
-      const float m2 = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - m2), e = exp2f(s - m2);
-      m = m2;
-      l = l * f + e;
-#pragma unroll
-      for (int j = 0; j < kSimpleElems; ++j) {
-        const int i = lane + 32 * j;
-        if (i < p.Dv) o[j] = o[j] * f + e * load_elem(p.v, row + i, p.bf16, p.e4m3);
-      }
-    }
-    if (p.weights && lane == 0) p.scores[(int64_t(b) * p.Hq + h) * p.score_row + t] = s;
-  }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int j = 0; j < kSimpleElems; ++j) sm_o[warp][lane + 32 * j] = o[j];
-  __syncthreads();
-  float top = -INFINITY, sum = 0.f;
-  for (int w = 0; w < kSimpleWarps; ++w) top = fmaxf(top, sm_m[w]);
-  float f[kSimpleWarps];
-  for (int w = 0; w < kSimpleWarps; ++w) {
-    f[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - top);
-    sum += f[w] * sm_l[w];
-  }
-  const float inv = sum > 0.f ? p.v_scale / sum : 0.f;
-  for (int i = int(threadIdx.x); i < p.Dv; i += kSimpleWarps * 32) {
-    float a = 0.f;
-    for (int w = 0; w < kSimpleWarps; ++w) a += f[w] * sm_o[w][i];
-    a *= inv;
-    const int64_t at = b * p.o_sb + h * p.o_sh + i;
-    if (p.bf16)
-      static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(a);
-    else
-      static_cast<__half *>(p.out)[at] = __float2half_rn(a);
-  }
-  if (threadIdx.x == 0) {
-    const float lse2 = top + log2f(sum);
-    if (p.lse) p.lse[b * p.lse_sb + h] = lse2 * kLn2;
-    if (p.weights) p.lse2[int64_t(b) * p.Hq + h] = lse2;
-  }
-}
+// ---- page weights ----------------------------------------------------------------
 
 // weights[b, p] <- decay * weights[b, p] + sum over heads and tokens of
 // 2^(score - lse2).  A block takes as many whole pages as 256 tokens hold (one
@@ -769,6 +616,7 @@ __global__ void __launch_bounds__(kSimpleWarps * 32) decode_simple_kernel(const 
 constexpr int kWeightThreads = 256;
 
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ DecodeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores and lse of the kernel before
   __shared__ float val[kWeightThreads];
   const int b = blockIdx.y, tid = int(threadIdx.x);
   const int64_t cap = int64_t(p.max_pages) * p.P;
@@ -844,10 +692,15 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 DecodeSpace decode_space(const DecodeParams &p, bool weights) {
   DecodeSpace s{};
   const int64_t grid = kDecodeCtas;
-  int64_t at = round_up(grid * 4, 256);
-  if (!p.latent) {
+  int64_t at = round_up((grid + 1) * 4, 256);
+  s.cta_parts = at;
+  if (p.latent) {
+    const int64_t rows = latent_rows(p.Hq);
+    at = round_up(at + grid * 2 * (rows * 512 + 2 * rows) * 4, 256);
+    s.seq_pieces = at;
+    at = round_up(at + int64_t(p.B) * 8, 256);
+  } else {
     const int64_t rows = decode_rows(p.G), dp = p.D <= 64 ? 64 : p.D <= 128 ? 128 : 256;
-    s.cta_parts = at;
     at = round_up(at + grid * 2 * (rows * dp + 2 * rows) * 4, 256);
     s.warp_parts = at;
     at = round_up(at + grid * 8 * rows * dp * 4, 256);
@@ -865,24 +718,20 @@ DecodeSpace decode_space(const DecodeParams &p, bool weights) {
 
 int launch_decode(const DecodeParams &p, int device, void *stream, int *launches) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = kDecodeCtas;
   int e = 0;
   if (p.latent) {
-    decode_simple_kernel<<<dim3(unsigned(p.Hq), unsigned(p.B)), kSimpleWarps * 32, 0, st>>>(p);
-    e = int(cudaGetLastError());
+    e = launch_decode_latent(p, device, stream, launches);
   } else {
-    e = decode_rows(p.G) == 8 ? launch_kv_type<8>(p, grid, device, st) : launch_kv_type<16>(p, grid, device, st);
+    e = decode_rows(p.G) == 8 ? launch_kv_type<8>(p, kDecodeCtas, device, st)
+                              : launch_kv_type<16>(p, kDecodeCtas, device, st);
+    *launches += e == 0;
   }
-  if (e) return e;
-  ++*launches;
-  if (p.weights) {
-    const int per = p.P < kWeightThreads ? kWeightThreads / p.P : 1;
-    weights_kernel<<<dim3(unsigned((p.max_pages + per - 1) / per), unsigned(p.B)), kWeightThreads, 0, st>>>(p);
-    e = int(cudaGetLastError());
-    if (e) return e;
-    ++*launches;
-  }
-  return 0;
+  if (e || !p.weights) return e;
+  const int per = p.P < kWeightThreads ? kWeightThreads / p.P : 1;
+  e = launch_dependent(weights_kernel, dim3(unsigned((p.max_pages + per - 1) / per), unsigned(p.B)), kWeightThreads, st,
+                       p);
+  *launches += e == 0;
+  return e;
 }
 
 }  // namespace hicache

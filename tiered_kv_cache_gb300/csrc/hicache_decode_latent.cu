@@ -1,0 +1,650 @@
+// hicache_decode_latent.cu -- attention of one new token per sequence over a
+// latent cache: rows of 576 elements, all of them the key, the first 512 the
+// value, one row for every query head.
+//
+// A cached byte serves all heads, so with many heads this is a pair of matrix
+// products: 16 heads do 30 multiply-adds per byte read, 128 heads 242.  The
+// tensor cores (tcgen05) take them with the TOKENS as the 128 rows and the
+// heads as the columns:
+//   S^T [128 tokens, heads] = K q^T       36 steps of 16 over the 576 elements
+//   O^T [512, heads]      += V^T P^T      4 blocks of 128 rows, 8 steps of 16 tokens
+// so that few heads cost few columns, and the cache tile, as it lies in shared
+// memory (rows of 128 bytes, 128-byte swizzle), is the first operand of both:
+// K-major for S, M-major for O.  Accumulators live in tensor memory (4 + 1
+// blocks of `heads` columns).  A thread of the softmax owns a token; the
+// running maximum of each head is raised only when some score passes it by 8 in
+// log2, so that the usual tile needs one barrier and no reduction, and row sums
+// stay per thread until the piece ends.
+//
+// The work is cut into strips of 32 tokens; the strips of all sequences, in
+// order, are dealt in equal contiguous ranges to the CTAs (one per SM; with more
+// than 64 heads, CTAs in groups that walk the same range with 64 heads each, so
+// that the cache is read from HBM once and from L2 after that).  A CTA's part of
+// a sequence is a piece; whole sequences are written out directly, the other
+// pieces go to the workspace and latent_join_kernel adds them in order.
+//
+// Warps: 0-3 softmax and epilogue (token = thread), 4 issues the products,
+// 5-8 copy the cache and q into shared memory (cp.async, 16 bytes per lane, so
+// any page size, absent pages as zeros), signalling by mbarrier.  The tile's
+// rope block (elements 512..575) is free once S is there and then holds P.
+//
+// Every wait has a limit of about two seconds, after which the CTA gives up,
+// sets the workspace's error word and returns.
+
+#include <atomic>
+
+#include "hicache_decode.cuh"
+
+namespace hicache {
+namespace {
+
+constexpr int kLatD = 576, kLatDv = 512;
+constexpr int kTileTok = 128, kStrip = 32;
+constexpr int kPairB = 2 * kTileTok * 128;        // two 64-element column blocks
+constexpr int kRopeB = kTileTok * 128;
+constexpr int kLatWarps = 9, kLatThreads = kLatWarps * 32;
+constexpr int kJoinThreads = 128;
+
+template <int NH_, bool BF16_>
+struct LatConfig {
+  static constexpr int NH = NH_;                  // heads (columns)
+  static constexpr bool BF16 = BF16_;
+  static constexpr int PAIRS = NH_ == 64 ? 4 : 5; // a tile needs 4 pairs and a rope block
+  static constexpr int ROPES = NH_ == 16 ? 2 : 1;
+  static constexpr int Q_B = 9 * NH_ * 128;
+  static constexpr int SMEM = Q_B + PAIRS * kPairB + ROPES * kRopeB + 1024;
+  static constexpr int COLS = NH_ == 16 ? 128 : NH_ == 32 ? 256 : 512;   // tensor memory
+  static constexpr int PIECE = NH_ * kLatDv + 2 * NH_;                   // floats: O, m, l
+};
+
+// ---- mbarriers and tcgen05 ------------------------------------------------------
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("{.reg .b64 t; mbarrier.arrive.shared::cta.b64 t, [%0];}" ::"r"(bar) : "memory");
+}
+// arrives once all copies this thread has issued so far are in shared memory
+__device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+constexpr long long kWaitClocks = 4000000000ll;   // about two seconds
+// Waits for the phase `parity` to end; false once a wait of the CTA has run out.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
+  long long since = 0;
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*gave_up) return false;
+    const long long now = clock64();
+    if (since == 0) since = now;
+    if (now - since > kWaitClocks) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a),
+      "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t addr, float *v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const float *v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand, 128-byte swizzle.  lbo: bytes between blocks of 64
+// elements along M (operands that are contiguous along M); sbo: between groups
+// of 8 rows of 128 bytes.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// 128 x n, 32-bit sums; a_m, b_n: the operand is contiguous along M (N) instead of K
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, int n, bool a_m, bool b_n) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_m ? 1u << 15 : 0u) | (b_n ? 1u << 16 : 0u) |
+         (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+
+// barriers of the four softmax warps
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  int r;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.s32 p, %1, 0; barrier.cta.red.or.pred q, 2, 128, p; selp.s32 %0, 1, 0, q;}"
+      : "=r"(r)
+      : "r"(int(x))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ int strips_of(int start, int len) {
+  return len > start ? (len + kStrip - 1) / kStrip - start / kStrip : 0;
+}
+
+// The pieces of a CTA's range of strips, in order.
+struct Pieces {
+  long long pos, hi;
+  long long skip;      // strips of sequence b before the range
+  int b;
+  // the current piece
+  int t_lo, t_hi, start, tiles;   // tokens [t_lo, t_hi) from t_lo = a multiple of kStrip; first token attended to
+  bool begins, ends;
+  __device__ __forceinline__ bool next(const DecodeParams &p) {
+    if (pos >= hi) return false;
+    int len, n;
+    for (;; ++b) {
+      seq_range(p, b, &start, &len);
+      n = strips_of(start, len);
+      if (skip < n || b + 1 >= p.B) break;
+      skip -= n;
+    }
+    const long long x1 = min((long long)n, skip + (hi - pos));
+    begins = skip == 0;
+    ends = x1 == n;
+    t_lo = (start / kStrip + int(skip)) * kStrip;
+    t_hi = min(len, (start / kStrip + int(x1)) * kStrip);
+    tiles = (int(x1 - skip) * kStrip + kTileTok - 1) / kTileTok;
+    pos += max(1ll, x1 - skip);
+    skip = 0;
+    ++b;
+    return true;
+  }
+  __device__ __forceinline__ int seq() const { return b - 1; }
+};
+
+template <class C>
+__global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __grid_constant__ DecodeParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  constexpr int NH = C::NH;
+  __shared__ long long prefix[kLatThreads + 1], scratch[kLatWarps];
+  __shared__ __align__(8) unsigned long long bars[2 * C::PAIRS + 2 * C::ROPES + 6];
+  __shared__ __align__(16) float m_s[NH], f_s[NH];
+  __shared__ float red[4][NH];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+
+  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_s = base, pair_s = base + C::Q_B, rope_s = pair_s + C::PAIRS * kPairB;
+  unsigned char *const rope_p = smem_raw + (rope_s - smem_u32(smem_raw));
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  constexpr int FULL = 0, EMPTY = C::PAIRS, RFULL = 2 * C::PAIRS, REMPTY = RFULL + C::ROPES, QFULL = REMPTY + C::ROPES,
+                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 3, PVDONE = QFULL + 4, LAST = QFULL + 5;
+
+  // the strips before each sequence
+  const int per = (p.B + kLatThreads - 1) / kLatThreads;
+  long long mine = 0, total = 0;
+  for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
+    int start, len;
+    seq_range(p, b, &start, &len);
+    mine += strips_of(start, len);
+  }
+  const long long ahead = block_prefix<kLatWarps>(mine, scratch, &total);
+  prefix[tid] = ahead;
+  if (tid == 0) {
+    prefix[kLatThreads] = total;
+    gave_up = 0;
+    for (int i = 0; i < C::PAIRS; ++i) {
+      mbar_init(bar(FULL + i), 128);
+      mbar_init(bar(EMPTY + i), 1);
+    }
+    for (int i = 0; i < C::ROPES; ++i) {
+      mbar_init(bar(RFULL + i), 128);
+      mbar_init(bar(REMPTY + i), 1);
+    }
+    mbar_init(bar(QFULL), 128);
+    mbar_init(bar(QEMPTY), 1);
+    mbar_init(bar(SFULL), 1);
+    mbar_init(bar(PFULL), 128);
+    mbar_init(bar(PVDONE), 1);
+    mbar_init(bar(LAST), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // sequences of which there is nothing to attend to
+  for (int b = int(blockIdx.x); b < p.B; b += int(gridDim.x)) {
+    int start, len;
+    seq_range(p, b, &start, &len);
+    if (len > start) continue;
+    for (int i = tid; i < p.Hq * kLatDv; i += kLatThreads) store_out(p, b, i / kLatDv, i % kLatDv, 0.f);
+    for (int h = tid; h < p.Hq; h += kLatThreads) store_lse(p, b, h, 0.f, 0.f);
+    if (tid == 0) p.seq_pieces[b] = make_int2(0, 0);
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // with fewer strips than groups, only as many groups take part
+  const long long groups = min((long long)(gridDim.x / unsigned(p.QB)), total);
+  const int group = int(blockIdx.x) / p.QB, qb = int(blockIdx.x) - group * p.QB;
+  if (group >= groups) return;
+  const int h0 = qb * NH, heads = min(NH, p.Hq - h0);
+
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "n"(C::COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t tmem_o = tmem, tmem_sc = tmem + 4 * NH;
+
+  Pieces pc;
+  pc.pos = total * group / groups;
+  pc.hi = total * (group + 1) / groups;
+  {
+    int a = 0, z = kLatThreads;                   // prefix[a] <= pos < prefix[z]
+    while (z - a > 1) {
+      const int mid = (a + z) >> 1;
+      if (prefix[mid] <= pc.pos) a = mid; else z = mid;
+    }
+    pc.b = a * per;
+    pc.skip = pc.pos - prefix[a];
+  }
+
+  if (warp >= 5) {
+    // ---- copies: rows of 128 bytes, 8 lanes a row, 16 rows at a time
+    const int pt = tid - 5 * 32, c = pt & 7, r0 = pt >> 3;
+    const char *kp = static_cast<const char *>(p.k);
+    int pair = 0, pair_ph = 1, rope = 0, rope_ph = 1, piece = 0;
+    bool ok = true;
+    while (ok && pc.next(p)) {
+      const int b = pc.seq();
+      if (piece > 0) ok = mbar_wait(bar(QEMPTY), uint32_t(piece - 1) & 1u, &gave_up);
+      if (!ok) break;
+      for (int i = 0; i < 9 * NH / 16; ++i) {
+        const int row = i * 16 + r0, blk = row / NH, r = row - blk * NH;
+        const bool have = r < heads;
+        const int64_t at = have ? 2 * (int64_t(b) * p.q_sb + int64_t(h0 + r) * p.q_sh) + blk * 128 + c * 16 : 0;
+        cp_async16(q_s + blk * (NH * 128) + r * 128 + ((c ^ (r & 7)) << 4), static_cast<const char *>(p.q) + at,
+                   have ? 16 : 0);
+      }
+      mbar_arrive_copies(bar(QFULL));
+      ++piece;
+      auto page_at = [&](int t, int *pg) {
+        int page = -1;
+        if (t >= pc.start && t < pc.t_hi) {
+          *pg = int(fast_div(uint32_t(t), p.fd_page));
+          page = __ldg(p.table + int64_t(b) * p.t_sb + *pg);
+        }
+        return page;
+      };
+      int pages[8], places[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pages[i] = page_at(pc.t_lo + i * 16 + r0, &places[i]);
+      for (int tile = 0; ok && tile < pc.tiles; ++tile) {
+        const int t0 = pc.t_lo + tile * kTileTok;
+        int64_t off[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = t0 + i * 16 + r0;
+          off[i] = -1;
+          if (page_present(pages[i], p.num_pages))
+            off[i] = (int64_t(pages[i]) * p.P + (t - places[i] * p.P)) * (kLatD * 2) + c * 16;
+        }
+        // the pages of the next tile, before the waits below
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pages[i] = page_at(t0 + kTileTok + i * 16 + r0, &places[i]);
+        for (int blk = 0; ok && blk < 4; ++blk) {
+          ok = mbar_wait(bar(EMPTY + pair), uint32_t(pair_ph), &gave_up);
+          if (!ok) break;
+          const uint32_t dst = pair_s + pair * kPairB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const char *src = kp + (off[i] >= 0 ? off[i] + blk * 256 : 0);
+            cp_async16(dst + i * 2048, src, off[i] >= 0 ? 16 : 0);
+            cp_async16(dst + i * 2048 + kPairB / 2, src + (off[i] >= 0 ? 128 : 0), off[i] >= 0 ? 16 : 0);
+          }
+          mbar_arrive_copies(bar(FULL + pair));
+          if (++pair == C::PAIRS) {
+            pair = 0;
+            pair_ph ^= 1;
+          }
+        }
+        if (ok) ok = mbar_wait(bar(REMPTY + rope), uint32_t(rope_ph), &gave_up);
+        if (!ok) break;
+        const uint32_t dst = rope_s + rope * kRopeB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          cp_async16(dst + i * 2048, kp + (off[i] >= 0 ? off[i] + 1024 : 0), off[i] >= 0 ? 16 : 0);
+        mbar_arrive_copies(bar(RFULL + rope));
+        if (++rope == C::ROPES) {
+          rope = 0;
+          rope_ph ^= 1;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 4) {
+    // ---- products
+    if (lane == 0) {
+      constexpr uint32_t kS = instr_desc(C::BF16, NH, false, false), kO = instr_desc(C::BF16, NH, true, true);
+      int pair = 0, pair_ph = 0, rope = 0, rope_ph = 0, piece = 0;
+      uint32_t tiles = 0;
+      bool ok = true;
+      while (ok && pc.next(p)) {
+        ok = mbar_wait(bar(QFULL), uint32_t(piece) & 1u, &gave_up);
+        ++piece;
+        for (int tile = 0; ok && tile < pc.tiles; ++tile, ++tiles) {
+          const int first_pair = pair;
+          for (int blk = 0; ok && blk < 4; ++blk) {
+            ok = mbar_wait(bar(FULL + pair), uint32_t(pair_ph), &gave_up);
+            if (!ok) break;
+            proxy_fence();
+            tc_fence_after();
+            const uint32_t a = pair_s + pair * kPairB;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              tc_mma(tmem_sc, smem_desc(a + (x >> 2) * (kPairB / 2) + (x & 3) * 32, 16, 1024),
+                     smem_desc(q_s + (2 * blk + (x >> 2)) * (NH * 128) + (x & 3) * 32, 16, 1024), kS, blk + x > 0);
+            if (++pair == C::PAIRS) {
+              pair = 0;
+              pair_ph ^= 1;
+            }
+          }
+          if (ok) ok = mbar_wait(bar(RFULL + rope), uint32_t(rope_ph), &gave_up);
+          if (!ok) break;
+          proxy_fence();
+          tc_fence_after();
+          const uint32_t ra = rope_s + rope * kRopeB;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            tc_mma(tmem_sc, smem_desc(ra + x * 32, 16, 1024), smem_desc(q_s + 8 * (NH * 128) + x * 32, 16, 1024), kS,
+                   true);
+          if (tile == pc.tiles - 1) tc_commit(bar(QEMPTY));
+          tc_commit(bar(SFULL));
+          ok = mbar_wait(bar(PFULL), tiles & 1u, &gave_up);
+          if (!ok) break;
+          tc_fence_after();
+          int pr = first_pair;
+          for (int blk = 0; blk < 4; ++blk) {
+            const uint32_t a = pair_s + pr * kPairB;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              tc_mma(tmem_o + blk * NH, smem_desc(a + x * 2048, kPairB / 2, 1024),
+                     smem_desc(ra + x * 2048, 1024, 1024), kO, tile > 0 || x > 0);
+            tc_commit(bar(EMPTY + pr));
+            if (++pr == C::PAIRS) pr = 0;
+          }
+          tc_commit(bar(REMPTY + rope));
+          tc_commit(bar(PVDONE));
+          if (++rope == C::ROPES) {
+            rope = 0;
+            rope_ph ^= 1;
+          }
+        }
+      }
+      // nothing is in flight when the tensor memory is given back
+      tc_commit(bar(LAST));
+      mbar_wait(bar(LAST), 0, &gave_up);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: thread = token
+    const uint32_t lanes = uint32_t(warp) << 21;  // this warp's 32 lanes of tensor memory
+    uint32_t tiles = 0, rope = 0;
+    bool fail = false;
+    while (!fail && pc.next(p)) {
+      const int b = pc.seq();
+      float l[NH];
+#pragma unroll
+      for (int j = 0; j < NH; ++j) l[j] = 0.f;
+      if (tid < NH) m_s[tid] = -INFINITY;
+      softmax_sync();
+      for (int tile = 0; tile < pc.tiles; ++tile, ++tiles) {
+        const int t = pc.t_lo + tile * kTileTok + tid;
+        const bool in = t >= pc.start && t < pc.t_hi;
+        bool present = false;
+        if (in) present = page_present(__ldg(p.table + int64_t(b) * p.t_sb + fast_div(uint32_t(t), p.fd_page)),
+                                       p.num_pages);
+        fail = !mbar_wait(bar(SFULL), tiles & 1u, &gave_up);
+        tc_fence_after();
+        float s[NH];
+#pragma unroll
+        for (int j = 0; j < NH; j += 16) tc_ld16(tmem_sc + lanes + j, s + j);
+        tc_wait_ld();
+        bool raise = false;
+#pragma unroll
+        for (int j = 0; j < NH; j += 4) {
+          const float4 m = *reinterpret_cast<const float4 *>(&m_s[j]);
+          const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[j + i] = present ? s[j + i] * p.scale2 : -INFINITY;
+            raise |= s[j + i] > mm[i] + 8.f;
+          }
+        }
+        if (p.weights && in) {
+          float *d = p.scores + (int64_t(b) * p.Hq + h0) * p.score_row + t;
+#pragma unroll
+          for (int j = 0; j < NH; ++j)
+            if (j < heads) __stcg(d + j * p.score_row, s[j]);
+        }
+        if (softmax_any(raise || fail)) {
+          // raise the maxima (all threads take this path, or none)
+          fail = softmax_any(fail);
+          if (fail) break;
+#pragma unroll
+          for (int j = 0; j < NH; ++j) {
+            float x = s[j];
+            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) red[warp][j] = x;
+          }
+          softmax_sync();
+          if (tid < NH) {
+            const float old = m_s[tid];
+            const float now = fmaxf(fmaxf(old, red[0][tid]), fmaxf(fmaxf(red[1][tid], red[2][tid]), red[3][tid]));
+            f_s[tid] = old == -INFINITY ? 0.f : exp2_fast(old - now);
+            m_s[tid] = now;
+          }
+          softmax_sync();
+#pragma unroll
+          for (int j = 0; j < NH; ++j) l[j] *= f_s[j];
+          // the product with V of the tile before has ended: S came after it
+          if (tile > 0) {
+#pragma unroll 1
+            for (int j = 0; j < 4 * NH; j += 16) {
+              float o[16];
+              tc_ld16(tmem_o + lanes + j, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f_s[(j + i) % NH];
+              tc_st16(tmem_o + lanes + j, o);
+            }
+            tc_wait_st();
+          }
+        }
+        // P, rounded to the cache's type for the tensor cores (the sums l keep all
+        // bits), over the rope block: a row of heads per token
+        unsigned char *prow = rope_p + rope * kRopeB + tid * 128;
+#pragma unroll
+        for (int j = 0; j < NH; j += 8) {
+          uint32_t w[4];
+          float e[8];
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(&m_s[j + i]);
+            const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e[i + x] = exp2_fast(s[j + i + x] - (mm[x] == -INFINITY ? 0.f : mm[x]));
+              l[j + i + x] += e[i + x];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack2<C::BF16>(e[2 * i], e[2 * i + 1]);
+          *reinterpret_cast<uint4 *>(prow + (((j >> 3) ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (++rope == C::ROPES) rope = 0;
+        proxy_fence();
+        tc_fence_before();
+        mbar_arrive(bar(PFULL));
+      }
+      if (fail) break;
+      // ---- the piece's end
+#pragma unroll
+      for (int j = 0; j < NH; ++j) {
+        float x = l[j];
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) red[warp][j] = x;
+      }
+      fail = !mbar_wait(bar(PVDONE), (tiles - 1) & 1u, &gave_up);
+      tc_fence_after();
+      fail = softmax_any(fail);
+      if (fail) break;
+      const bool whole = pc.begins && pc.ends;
+      float *part = p.cta_parts + (int64_t(blockIdx.x) * 2 + (pc.begins ? 1 : 0)) * C::PIECE;
+      if (tid < NH) {
+        const float sum = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+        f_s[tid] = !whole ? 1.f : sum == 0.f ? 0.f : p.v_scale / sum;
+        if (whole) {
+          if (tid < heads) store_lse(p, b, h0 + tid, m_s[tid], sum);
+        } else {
+          part[NH * kLatDv + tid] = m_s[tid];
+          part[NH * kLatDv + NH + tid] = sum;
+        }
+      }
+      if (tid == 0 && qb == 0 && pc.begins) {
+        // the group the sequence begins in, and the groups it lies in
+        int start, len;
+        seq_range(p, b, &start, &len);
+        const long long n = strips_of(start, len);
+        const long long first = pc.pos - max(1, (pc.t_hi + kStrip - 1) / kStrip - pc.t_lo / kStrip);
+        const int last = int(((first + n) * groups - 1) / total);
+        p.seq_pieces[b] = make_int2(group, whole ? 1 : last - group + 1);
+      }
+      softmax_sync();
+#pragma unroll 1
+      for (int blk = 0; blk < 4; ++blk)
+#pragma unroll 1
+        for (int j = 0; j < NH; j += 16) {
+          float o[16];
+          tc_ld16(tmem_o + lanes + blk * NH + j, o);
+          tc_wait_ld();
+          const int d = blk * 128 + tid;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (j + i >= heads) continue;
+            if (whole)
+              store_out(p, b, h0 + j + i, d, o[i] * f_s[j + i]);
+            else
+              part[(j + i) * kLatDv + d] = o[i];
+          }
+        }
+      tc_fence_before();
+      softmax_sync();                             // m_s, f_s, red are free
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+  }
+  if (tid == 0 && gave_up) p.counters[kDecodeCtas] = 1u;
+}
+
+// Adds the pieces of a sequence that several groups of CTAs share; one block
+// per sequence and head, a thread for 4 elements.
+template <int NH>
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ DecodeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int PIECE = NH * kLatDv + 2 * NH;
+  const int b = int(blockIdx.x) / p.Hq, h = int(blockIdx.x) - b * p.Hq;
+  const int2 at = __ldcg(p.seq_pieces + b);
+  if (at.y < 2) return;
+  const int qb = h / NH, r = h - qb * NH, tid = int(threadIdx.x);
+  auto slot = [&](int x) { return p.cta_parts + (int64_t((at.x + x) * p.QB + qb) * 2 + (x == 0 ? 1 : 0)) * PIECE; };
+  float m = -INFINITY;
+  for (int x = 0; x < at.y; ++x) m = fmaxf(m, __ldcg(slot(x) + NH * kLatDv + r));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int x = 0; x < at.y; ++x) {
+    const float *s = slot(x);
+    const float mx = __ldcg(s + NH * kLatDv + r);
+    const float f = mx == -INFINITY ? 0.f : exp2_fast(mx - m);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + r * kLatDv) + tid);
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+    sum += f * __ldcg(s + NH * kLatDv + NH + r);
+  }
+  const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+  store_out(p, b, h, tid * 4, acc.x * inv);
+  store_out(p, b, h, tid * 4 + 1, acc.y * inv);
+  store_out(p, b, h, tid * 4 + 2, acc.z * inv);
+  store_out(p, b, h, tid * 4 + 3, acc.w * inv);
+  if (tid == 0) store_lse(p, b, h, m, sum);
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int NH, bool BF16>
+int launch_lat(const DecodeParams &p, int device, cudaStream_t st) {
+  using C = LatConfig<NH, BF16>;
+  static std::atomic<bool> ready[kMaxDevices];
+  if (device >= kMaxDevices || !ready[device].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_latent_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return int(e);
+    if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
+  }
+  decode_latent_kernel<C><<<kDecodeCtas / p.QB * p.QB, kLatThreads, C::SMEM, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return int(e);
+  return launch_dependent(latent_join_kernel<NH>, dim3(unsigned(p.B) * unsigned(p.Hq)), kJoinThreads, st, p);
+}
+
+}  // namespace
+
+int launch_decode_latent(const DecodeParams &p, int device, void *stream, int *launches) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int rows = latent_rows(p.Hq);
+  const int e = rows == 16   ? (p.bf16 ? launch_lat<16, true>(p, device, st) : launch_lat<16, false>(p, device, st))
+                : rows == 32 ? (p.bf16 ? launch_lat<32, true>(p, device, st) : launch_lat<32, false>(p, device, st))
+                             : (p.bf16 ? launch_lat<64, true>(p, device, st) : launch_lat<64, false>(p, device, st));
+  if (e == 0) *launches += 2;
+  return e;
+}
+
+}  // namespace hicache

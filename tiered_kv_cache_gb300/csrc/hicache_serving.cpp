@@ -128,7 +128,8 @@ int decode_sizes(const Shape &s, int64_t batch, int64_t q_heads, int64_t head_di
   p->row = s.R;
   p->Hkv = int32_t(s.R / head_dim);
   p->G = p->Hq / p->Hkv;
-  p->QB = (p->G + hicache::decode_rows(p->G) - 1) / hicache::decode_rows(p->G);
+  const int rows = s.B == 1 ? hicache::latent_rows(p->Hq) : hicache::decode_rows(p->G);
+  p->QB = (p->G + rows - 1) / rows;
   p->P = int32_t(s.P);
   p->max_pages = int32_t(max_pages);
   p->e4m3 = s.es == 1;
@@ -312,6 +313,7 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.num_pages = kv->device_num_pages;
   p.counters = reinterpret_cast<unsigned int *>(ws);
   p.cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
+  p.seq_pieces = reinterpret_cast<int2 *>(ws + sp.seq_pieces);
   p.warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
   p.lse2 = reinterpret_cast<float *>(ws + sp.lse2);
   p.scores = reinterpret_cast<float *>(ws + sp.scores);

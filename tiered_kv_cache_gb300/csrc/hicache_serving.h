@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <vector_types.h>
+
 #include "hicache_internal.h"
 
 namespace hicache {
@@ -39,7 +41,8 @@ struct DecodeParams {
   int64_t num_pages;          // device pages
   int32_t QB;                 // units of a kv head: its G query heads by decode_rows(G)
   // workspace
-  unsigned int *counters;     // kDecodeCtas, zero between calls
+  unsigned int *counters;     // kDecodeCtas, zero between calls; then the error word
+  int2 *seq_pieces;           // latent: per sequence, the group it begins in and its pieces
   float *cta_parts, *warp_parts;
   float *scores;              // [batch, q_heads, score_row] in units of log2, if weights
   float *lse2;                // [batch, q_heads] base-2 logarithm, if weights
@@ -54,13 +57,16 @@ struct DecodeParams {
 // launch: one on each of a GB300's 152 SMs.
 HC_HD int decode_rows(int group) { return group <= 8 ? 8 : 16; }
 constexpr int kDecodeCtas = 152;
+// The heads (columns of a product) of a CTA over a latent cache.
+HC_HD int latent_rows(int q_heads) { return q_heads <= 16 ? 16 : q_heads <= 32 ? 32 : 64; }
 // The workspace of a call: byte offsets of its parts (from the sizes in p).
 struct DecodeSpace {
-  int64_t cta_parts, warp_parts, lse2, scores, bytes;
+  int64_t cta_parts, warp_parts, seq_pieces, lse2, scores, bytes;
   int64_t score_row;
 };
 DecodeSpace decode_space(const DecodeParams &p, bool weights);
 int launch_decode(const DecodeParams &p, int device, void *stream, int *launches);
+int launch_decode_latent(const DecodeParams &p, int device, void *stream, int *launches);
 
 // Whether a page table's entry is a page of the cache (else it counts as absent).
 HC_HD bool page_present(int32_t page, int64_t num_pages) { return page >= 0 && page < num_pages; }
