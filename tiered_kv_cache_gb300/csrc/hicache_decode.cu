@@ -394,8 +394,10 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
         }
     }
 
-    // ---- running maximum: raised only when a score passes it by 8 in log2, so
-    // that the sums are rarely rescaled; an exponential is then at most 256
+    // ---- running maximum: raised only when a score passes it by as much (in log2)
+    // as the products' type allows, so that the sums are rarely rescaled: fp16
+    // ends at 2^16, bf16 has room for 2^40 and its sums
+    constexpr float RAISE = MMA_BF16 ? 40.f : 14.f;
     uint32_t pf[4] = {0u, 0u, 0u, 0u};
     float top[2];
     bool raise = false;
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
       top[x] = t;
-      raise |= t > m[x] + 8.f;
+      raise |= t > m[x] + RAISE;
     }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll

@@ -4,17 +4,25 @@
 //
 // A cached byte serves all heads, so with many heads this is a pair of matrix
 // products: 16 heads do 30 multiply-adds per byte read, 128 heads 242.  The
-// tensor cores (tcgen05) take them with the TOKENS as the 128 rows and the
-// heads as the columns:
-//   S^T [128 tokens, heads] = K q^T       36 steps of 16 over the 576 elements
-//   O^T [512, heads]      += V^T P^T      4 blocks of 128 rows, 8 steps of 16 tokens
+// tensor cores (tcgen05) take them with the TOKENS as the rows and the heads as
+// the columns:
+//   S^T [64 tokens, heads] = K q^T        36 steps of 16 over the 576 elements
+//   O^T [512, heads]      += V^T P^T      4 blocks of 128 rows, 4 steps of 16 tokens
 // so that few heads cost few columns, and the cache tile, as it lies in shared
 // memory (rows of 128 bytes, 128-byte swizzle), is the first operand of both:
-// K-major for S, M-major for O.  Accumulators live in tensor memory (4 + 1
-// blocks of `heads` columns).  A thread of the softmax owns a token; the
-// running maximum of each head is raised only when some score passes it by 8 in
-// log2, so that the usual tile needs one barrier and no reduction, and row sums
-// stay per thread until the piece ends.
+// K-major for S, M-major for O.  Accumulators live in tensor memory: 4 blocks of
+// `heads` columns for O, 2 for S.
+//
+// A tile is 64 tokens (72 KiB), so that two and more fit beside q and the copies
+// of the next tile never stop for the products of this one.  S is double-buffered
+// and the two products are issued by a warp each, as their operands arrive: S of
+// tile n + 1 runs during the softmax of tile n, and a product with V whose P is
+// ready never waits behind one whose tile is still on its way.
+//
+// Softmax: a warp reads its 16 tokens as 16 x 8 fragments (2 tokens x heads / 4
+// a thread).  The running maximum of each head is raised only when some score
+// passes it by more than P's type can hold, so that the usual tile needs one
+// barrier and no reduction; sums stay per thread until the piece ends.
 //
 // The work is cut into strips of 32 tokens; the strips of all sequences, in
 // order, are dealt in equal contiguous ranges to the CTAs (one per SM; with more
@@ -23,8 +31,7 @@
 // a sequence is a piece; whole sequences are written out directly, the other
 // pieces go to the workspace and latent_join_kernel adds them in order.
 //
-// Warps: 0-3 softmax and epilogue (token = thread), 4 issues the products,
-// 5-8 copy the cache and q into shared memory (cp.async, 16 bytes per lane, so
+// Warps: 0-3 softmax and epilogue, 4 issues S, 5 O, 6-9 copy the cache and q into shared memory (cp.async, 16 bytes per lane, so
 // any page size, absent pages as zeros), signalling by mbarrier.  The tile's
 // rope block (elements 512..575) is free once S is there and then holds P.
 //
@@ -39,22 +46,26 @@ namespace hicache {
 namespace {
 
 constexpr int kLatD = 576, kLatDv = 512;
-constexpr int kTileTok = 128, kStrip = 32;
-constexpr int kPairB = 2 * kTileTok * 128;        // two 64-element column blocks
-constexpr int kRopeB = kTileTok * 128;
-constexpr int kLatWarps = 9, kLatThreads = kLatWarps * 32;
+constexpr int kTileTok = 64, kStrip = 32;
+constexpr int kAtomB = kTileTok * 128;            // 64 elements of a tile's tokens
+constexpr int kQuadB = 4 * kAtomB;                // 256 elements
+constexpr int kRopeB = kAtomB;                    // the last 64 elements
+constexpr int kLatWarps = 10, kLatThreads = kLatWarps * 32;
 constexpr int kJoinThreads = 128;
 
 template <int NH_, bool BF16_>
 struct LatConfig {
   static constexpr int NH = NH_;                  // heads (columns)
   static constexpr bool BF16 = BF16_;
-  static constexpr int PAIRS = NH_ == 64 ? 4 : 5; // a tile needs 4 pairs and a rope block
-  static constexpr int ROPES = NH_ == 16 ? 2 : 1;
+  static constexpr int QUADS = NH_ == 64 ? 4 : 5; // a tile is 2 quads and a rope block, and two
+  static constexpr int ROPES = NH_ == 16 ? 3 : 2; // tiles must fit (the products run a tile ahead)
   static constexpr int Q_B = 9 * NH_ * 128;
-  static constexpr int SMEM = Q_B + PAIRS * kPairB + ROPES * kRopeB + 1024;
+  static constexpr int SMEM = Q_B + QUADS * kQuadB + ROPES * kRopeB + 1024;
   static constexpr int COLS = NH_ == 16 ? 128 : NH_ == 32 ? 256 : 512;   // tensor memory
   static constexpr int PIECE = NH_ * kLatDv + 2 * NH_;                   // floats: O, m, l
+  // How far a score may pass the running maximum (log2) before it is raised: as
+  // far as P's type allows (fp16 ends at 2^16; bf16 has room for 2^40 and its sums)
+  static constexpr float RAISE = BF16_ ? 40.f : 14.f;
 };
 
 // ---- mbarriers and tcgen05 ------------------------------------------------------
@@ -89,6 +100,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
       return false;
     }
   }
+}
+
+// true in one lane of the (whole) warp, in a way the compiler can follow
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -135,10 +153,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
   return uint64_t((addr >> 4) & 0x3fff) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
          (uint64_t(2) << 61);
 }
-// 128 x n, 32-bit sums; a_m, b_n: the operand is contiguous along M (N) instead of K
-__device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, int n, bool a_m, bool b_n) {
+// m x n, 32-bit sums; a_m, b_n: the operand is contiguous along M (N) instead of K
+__device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, int m, int n, bool a_m, bool b_n) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_m ? 1u << 15 : 0u) | (b_n ? 1u << 16 : 0u) |
-         (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+         (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
 // barriers of the four softmax warps
@@ -151,6 +169,33 @@ __device__ __forceinline__ bool softmax_any(bool x) {
       : "r"(int(x))
       : "memory");
   return r != 0;
+}
+
+// The maximum or sum over a warp's 16 tokens of the columns a lane holds (8 n + 2 c
+// + i, in v[2 n + i]) into out.
+template <int NH, bool MAX>
+__device__ __forceinline__ void reduce_columns(float *v, int lane, float *out) {
+#pragma unroll
+  for (int j = 0; j < NH / 4; ++j) {
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, v[j], w);
+      v[j] = MAX ? fmaxf(v[j], y) : v[j] + y;
+    }
+    if (lane < 4) out[8 * (j >> 1) + 2 * lane + (j & 1)] = v[j];
+  }
+}
+
+// 16 lanes (tokens) x 16 columns: v[0..1] row lane / 4, columns 2 (lane % 4) + {0, 1};
+// v[2..3] row lane / 4 + 8; v[4..7] the same 8 columns on.
+__device__ __forceinline__ void tc_ld_16x16(uint32_t addr, float *v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ int strips_of(int start, int len) {
@@ -193,20 +238,22 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   extern __shared__ unsigned char smem_raw[];
   constexpr int NH = C::NH;
   __shared__ long long prefix[kLatThreads + 1], scratch[kLatWarps];
-  __shared__ __align__(8) unsigned long long bars[2 * C::PAIRS + 2 * C::ROPES + 6];
-  __shared__ __align__(16) float m_s[NH], f_s[NH];
+  __shared__ __align__(8) unsigned long long bars[2 * C::QUADS + 2 * C::ROPES + 9];
+  // per head: the maximum (and what scores are taken relative to: 0 while there is
+  // none), the factor and the shift of the last raise
+  __shared__ __align__(16) float m_s[NH], mu_s[NH], f_s[NH], d_s[NH];
   __shared__ float red[4][NH];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
 
-  const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_s = base, pair_s = base + C::Q_B, rope_s = pair_s + C::PAIRS * kPairB;
+  const uint32_t q_s = base, quad_s = base + C::Q_B, rope_s = quad_s + C::QUADS * kQuadB;
   unsigned char *const rope_p = smem_raw + (rope_s - smem_u32(smem_raw));
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
-  constexpr int FULL = 0, EMPTY = C::PAIRS, RFULL = 2 * C::PAIRS, REMPTY = RFULL + C::ROPES, QFULL = REMPTY + C::ROPES,
-                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 3, PVDONE = QFULL + 4, LAST = QFULL + 5;
+  constexpr int FULL = 0, EMPTY = C::QUADS, RFULL = 2 * C::QUADS, REMPTY = RFULL + C::ROPES, QFULL = REMPTY + C::ROPES,
+                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 4, PVDONE = QFULL + 6, LAST = QFULL + 8;
 
   // the strips before each sequence
   const int per = (p.B + kLatThreads - 1) / kLatThreads;
@@ -221,7 +268,7 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   if (tid == 0) {
     prefix[kLatThreads] = total;
     gave_up = 0;
-    for (int i = 0; i < C::PAIRS; ++i) {
+    for (int i = 0; i < C::QUADS; ++i) {
       mbar_init(bar(FULL + i), 128);
       mbar_init(bar(EMPTY + i), 1);
     }
@@ -231,10 +278,12 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
     }
     mbar_init(bar(QFULL), 128);
     mbar_init(bar(QEMPTY), 1);
-    mbar_init(bar(SFULL), 1);
-    mbar_init(bar(PFULL), 128);
-    mbar_init(bar(PVDONE), 1);
-    mbar_init(bar(LAST), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(SFULL + i), 1);
+      mbar_init(bar(PFULL + i), 128);
+      mbar_init(bar(PVDONE + i), 1);
+    }
+    mbar_init(bar(LAST), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // sequences of which there is nothing to attend to
@@ -264,7 +313,7 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
   const uint32_t tmem_o = tmem, tmem_sc = tmem + 4 * NH;
 
   Pieces pc;
@@ -280,11 +329,11 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
     pc.skip = pc.pos - prefix[a];
   }
 
-  if (warp >= 5) {
+  if (warp >= 6) {
     // ---- copies: rows of 128 bytes, 8 lanes a row, 16 rows at a time
-    const int pt = tid - 5 * 32, c = pt & 7, r0 = pt >> 3;
+    const int pt = tid - 6 * 32, c = pt & 7, r0 = pt >> 3;
     const char *kp = static_cast<const char *>(p.k);
-    int pair = 0, pair_ph = 1, rope = 0, rope_ph = 1, piece = 0;
+    int quad = 0, quad_ph = 1, rope = 0, rope_ph = 1, piece = 0;
     bool ok = true;
     while (ok && pc.next(p)) {
       const int b = pc.seq();
@@ -307,44 +356,44 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         }
         return page;
       };
-      int pages[8], places[8];
+      int pages[4], places[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pages[i] = page_at(pc.t_lo + i * 16 + r0, &places[i]);
+      for (int i = 0; i < 4; ++i) pages[i] = page_at(pc.t_lo + i * 16 + r0, &places[i]);
       for (int tile = 0; ok && tile < pc.tiles; ++tile) {
         const int t0 = pc.t_lo + tile * kTileTok;
-        int64_t off[8];
+        const char *src[4];
+        int bytes[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int t = t0 + i * 16 + r0;
-          off[i] = -1;
-          if (page_present(pages[i], p.num_pages))
-            off[i] = (int64_t(pages[i]) * p.P + (t - places[i] * p.P)) * (kLatD * 2) + c * 16;
+          const bool have = page_present(pages[i], p.num_pages);
+          bytes[i] = have ? 16 : 0;
+          src[i] = kp + (have ? (int64_t(pages[i]) * p.P + (t - places[i] * p.P)) * (kLatD * 2) + c * 16 : 0);
         }
         // the pages of the next tile, before the waits below
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pages[i] = page_at(t0 + kTileTok + i * 16 + r0, &places[i]);
-        for (int blk = 0; ok && blk < 4; ++blk) {
-          ok = mbar_wait(bar(EMPTY + pair), uint32_t(pair_ph), &gave_up);
-          if (!ok) break;
-          const uint32_t dst = pair_s + pair * kPairB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        for (int i = 0; i < 4; ++i) pages[i] = page_at(t0 + kTileTok + i * 16 + r0, &places[i]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const char *src = kp + (off[i] >= 0 ? off[i] + blk * 256 : 0);
-            cp_async16(dst + i * 2048, src, off[i] >= 0 ? 16 : 0);
-            cp_async16(dst + i * 2048 + kPairB / 2, src + (off[i] >= 0 ? 128 : 0), off[i] >= 0 ? 16 : 0);
-          }
-          mbar_arrive_copies(bar(FULL + pair));
-          if (++pair == C::PAIRS) {
-            pair = 0;
-            pair_ph ^= 1;
+        for (int half = 0; half < 2; ++half) {
+          if (ok) ok = mbar_wait(bar(EMPTY + quad), uint32_t(quad_ph), &gave_up);
+          if (!ok) break;
+          const uint32_t dst = quad_s + quad * kQuadB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              cp_async16(dst + a * kAtomB + i * 2048, src[i] + (bytes[i] ? half * 512 + a * 128 : 0), bytes[i]);
+          mbar_arrive_copies(bar(FULL + quad));
+          if (++quad == C::QUADS) {
+            quad = 0;
+            quad_ph ^= 1;
           }
         }
         if (ok) ok = mbar_wait(bar(REMPTY + rope), uint32_t(rope_ph), &gave_up);
         if (!ok) break;
         const uint32_t dst = rope_s + rope * kRopeB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          cp_async16(dst + i * 2048, kp + (off[i] >= 0 ? off[i] + 1024 : 0), off[i] >= 0 ? 16 : 0);
+        for (int i = 0; i < 4; ++i) cp_async16(dst + i * 2048, src[i] + (bytes[i] ? 1024 : 0), bytes[i]);
         mbar_arrive_copies(bar(RFULL + rope));
         if (++rope == C::ROPES) {
           rope = 0;
@@ -354,131 +403,187 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 4) {
-    // ---- products
-    if (lane == 0) {
-      constexpr uint32_t kS = instr_desc(C::BF16, NH, false, false), kO = instr_desc(C::BF16, NH, true, true);
-      int pair = 0, pair_ph = 0, rope = 0, rope_ph = 0, piece = 0;
-      uint32_t tiles = 0;
-      bool ok = true;
-      while (ok && pc.next(p)) {
-        ok = mbar_wait(bar(QFULL), uint32_t(piece) & 1u, &gave_up);
-        ++piece;
-        for (int tile = 0; ok && tile < pc.tiles; ++tile, ++tiles) {
-          const int first_pair = pair;
-          for (int blk = 0; ok && blk < 4; ++blk) {
-            ok = mbar_wait(bar(FULL + pair), uint32_t(pair_ph), &gave_up);
-            if (!ok) break;
-            proxy_fence();
-            tc_fence_after();
-            const uint32_t a = pair_s + pair * kPairB;
+    // ---- S^T = K q^T: the warp runs as one, and one elected lane issues (descriptors
+    // that the compiler knows to be the same in all lanes cost 1/6 of the issue
+    // time: with a branch on the lane an issue took 90 to 270 clocks)
+    constexpr uint32_t kS = instr_desc(C::BF16, kTileTok, NH, false, false);
+    int quad = 0, quad_ph = 0, rope = 0, rope_ph = 0, piece = 0;
+    uint32_t tiles = 0;
+    bool ok = true;
+    while (ok && pc.next(p)) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(QFULL), uint32_t(piece) & 1u, &gave_up));
+      ++piece;
+      for (int tile = 0; ok && tile < pc.tiles; ++tile, ++tiles) {
+        const uint32_t buf = tiles & 1u, s_at = tmem_sc + buf * NH;
+        // the softmax two tiles back has read this buffer
+        if (tiles >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(PFULL + buf), ((tiles - 2) >> 1) & 1u, &gave_up));
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              tc_mma(tmem_sc, smem_desc(a + (x >> 2) * (kPairB / 2) + (x & 3) * 32, 16, 1024),
-                     smem_desc(q_s + (2 * blk + (x >> 2)) * (NH * 128) + (x & 3) * 32, 16, 1024), kS, blk + x > 0);
-            if (++pair == C::PAIRS) {
-              pair = 0;
-              pair_ph ^= 1;
-            }
-          }
-          if (ok) ok = mbar_wait(bar(RFULL + rope), uint32_t(rope_ph), &gave_up);
+        for (int half = 0; half < 2; ++half) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(FULL + quad), uint32_t(quad_ph), &gave_up));
           if (!ok) break;
           proxy_fence();
           tc_fence_after();
-          const uint32_t ra = rope_s + rope * kRopeB;
+          const uint32_t a = __shfl_sync(0xffffffffu, quad_s + quad * kQuadB, 0);
+          if (elect_one()) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            tc_mma(tmem_sc, smem_desc(ra + x * 32, 16, 1024), smem_desc(q_s + 8 * (NH * 128) + x * 32, 16, 1024), kS,
-                   true);
-          if (tile == pc.tiles - 1) tc_commit(bar(QEMPTY));
-          tc_commit(bar(SFULL));
-          ok = mbar_wait(bar(PFULL), tiles & 1u, &gave_up);
-          if (!ok) break;
-          tc_fence_after();
-          int pr = first_pair;
-          for (int blk = 0; blk < 4; ++blk) {
-            const uint32_t a = pair_s + pr * kPairB;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              tc_mma(tmem_o + blk * NH, smem_desc(a + x * 2048, kPairB / 2, 1024),
-                     smem_desc(ra + x * 2048, 1024, 1024), kO, tile > 0 || x > 0);
-            tc_commit(bar(EMPTY + pr));
-            if (++pr == C::PAIRS) pr = 0;
+            for (int x = 0; x < 16; ++x)
+              tc_mma(s_at, smem_desc(a + (x >> 2) * kAtomB + (x & 3) * 32, 16, 1024),
+                     smem_desc(q_s + (4 * half + (x >> 2)) * (NH * 128) + (x & 3) * 32, 16, 1024), kS, half + x > 0);
           }
-          tc_commit(bar(REMPTY + rope));
-          tc_commit(bar(PVDONE));
-          if (++rope == C::ROPES) {
-            rope = 0;
-            rope_ph ^= 1;
+          __syncwarp();
+          if (++quad == C::QUADS) {
+            quad = 0;
+            quad_ph ^= 1;
           }
         }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(RFULL + rope), uint32_t(rope_ph), &gave_up));
+        if (!ok) break;
+        proxy_fence();
+        tc_fence_after();
+        const uint32_t ra = __shfl_sync(0xffffffffu, rope_s + rope * kRopeB, 0);
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            tc_mma(s_at, smem_desc(ra + x * 32, 16, 1024), smem_desc(q_s + 8 * (NH * 128) + x * 32, 16, 1024), kS, true);
+          if (tile == pc.tiles - 1) tc_commit(bar(QEMPTY));
+          tc_commit(bar(SFULL + buf));
+        }
+        __syncwarp();
+        if (++rope == C::ROPES) {
+          rope = 0;
+          rope_ph ^= 1;
+        }
       }
-      // nothing is in flight when the tensor memory is given back
-      tc_commit(bar(LAST));
-      mbar_wait(bar(LAST), 0, &gave_up);
     }
+    if (elect_one()) tc_commit(bar(LAST));
+    __syncwarp();
+  } else if (warp == 5) {
+    // ---- O^T += V^T P^T
+    constexpr uint32_t kO = instr_desc(C::BF16, 128, NH, true, true);
+    int quad = 0, rope = 0;
+    uint32_t tiles = 0;
+    bool ok = true;
+    while (ok && pc.next(p)) {
+      for (int tile = 0; tile < pc.tiles; ++tile, ++tiles) {
+        const uint32_t buf = tiles & 1u;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(PFULL + buf), (tiles >> 1) & 1u, &gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t pb = __shfl_sync(0xffffffffu, rope_s + rope * kRopeB, 0);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t a = __shfl_sync(0xffffffffu, quad_s + quad * kQuadB, 0);
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              tc_mma(tmem_o + (2 * half + (x >> 2)) * NH,
+                     smem_desc(a + (x >> 2) * 2 * kAtomB + (x & 3) * 2048, kAtomB, 1024),
+                     smem_desc(pb + (x & 3) * 2048, 1024, 1024), kO, tile > 0 || (x & 3) > 0);
+            tc_commit(bar(EMPTY + quad));
+            if (half == 1) {
+              tc_commit(bar(REMPTY + rope));
+              tc_commit(bar(PVDONE + buf));
+            }
+          }
+          __syncwarp();
+          if (++quad == C::QUADS) quad = 0;
+        }
+        if (++rope == C::ROPES) rope = 0;
+      }
+    }
+    if (elect_one()) tc_commit(bar(LAST));
     __syncwarp();
   } else {
-    // ---- softmax: thread = token
+    // ---- softmax: token rows warp * 16 + g and + 8, heads 8 n + 2 c and + 1
     const uint32_t lanes = uint32_t(warp) << 21;  // this warp's 32 lanes of tensor memory
+    const int g = lane >> 2, c = lane & 3, row0 = warp * 16 + g;
     uint32_t tiles = 0, rope = 0;
     bool fail = false;
     while (!fail && pc.next(p)) {
       const int b = pc.seq();
-      float l[NH];
+      float l[NH / 4];                            // sums of heads 8 (j / 2) + 2 c + j % 2
 #pragma unroll
-      for (int j = 0; j < NH; ++j) l[j] = 0.f;
-      if (tid < NH) m_s[tid] = -INFINITY;
+      for (int j = 0; j < NH / 4; ++j) l[j] = 0.f;
+      if (tid < NH) {
+        m_s[tid] = -INFINITY;
+        mu_s[tid] = 0.f;
+      }
+      bool unset = true;                          // a head has no maximum yet
       softmax_sync();
       for (int tile = 0; tile < pc.tiles; ++tile, ++tiles) {
-        const int t = pc.t_lo + tile * kTileTok + tid;
-        const bool in = t >= pc.start && t < pc.t_hi;
-        bool present = false;
-        if (in) present = page_present(__ldg(p.table + int64_t(b) * p.t_sb + fast_div(uint32_t(t), p.fd_page)),
-                                       p.num_pages);
-        fail = !mbar_wait(bar(SFULL), tiles & 1u, &gave_up);
+        const uint32_t buf = tiles & 1u;
+        bool in[2], present[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = pc.t_lo + tile * kTileTok + row0 + 8 * x;
+          in[x] = t >= pc.start && t < pc.t_hi;
+          present[x] = in[x] && page_present(__ldg(p.table + int64_t(b) * p.t_sb + fast_div(uint32_t(t), p.fd_page)),
+                                             p.num_pages);
+        }
+        fail = !mbar_wait(bar(SFULL + buf), (tiles >> 1) & 1u, &gave_up);
+        // O of two tiles back (long done), so that the waits for it below see each phase
+        if (!fail && tiles >= 2) fail = !mbar_wait(bar(PVDONE + buf), ((tiles - 2) >> 1) & 1u, &gave_up);
         tc_fence_after();
-        float s[NH];
+        float e[NH / 2];                          // scores less the running maxima, in log2: [4 n + 2 x + i]
 #pragma unroll
-        for (int j = 0; j < NH; j += 16) tc_ld16(tmem_sc + lanes + j, s + j);
+        for (int j = 0; j < NH; j += 16) tc_ld_16x16(tmem_sc + buf * NH + lanes + j, e + j / 2);
         tc_wait_ld();
-        bool raise = false;
+        float over = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NH; j += 4) {
-          const float4 m = *reinterpret_cast<const float4 *>(&m_s[j]);
-          const float mm[4] = {m.x, m.y, m.z, m.w};
+        for (int n = 0; n < NH / 8; ++n) {
+          const float2 mu = *reinterpret_cast<const float2 *>(&mu_s[8 * n + 2 * c]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            s[j + i] = present ? s[j + i] * p.scale2 : -INFINITY;
-            raise |= s[j + i] > mm[i] + 8.f;
+          for (int x = 0; x < 2; ++x) {
+            float *v = e + 4 * n + 2 * x;
+            v[0] = present[x] ? fmaf(v[0], p.scale2, -mu.x) : -INFINITY;
+            v[1] = present[x] ? fmaf(v[1], p.scale2, -mu.y) : -INFINITY;
+            over = fmaxf(over, fmaxf(v[0], v[1]));
           }
         }
-        if (p.weights && in) {
-          float *d = p.scores + (int64_t(b) * p.Hq + h0) * p.score_row + t;
+        if (p.weights) {
+          float *d = p.scores + (int64_t(b) * p.Hq + h0) * p.score_row + pc.t_lo + tile * kTileTok + row0;
 #pragma unroll
-          for (int j = 0; j < NH; ++j)
-            if (j < heads) __stcg(d + j * p.score_row, s[j]);
+          for (int n = 0; n < NH / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int h = 8 * n + 2 * c + i;
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                if (h < heads && in[x]) __stcg(d + h * p.score_row + 8 * x, e[4 * n + 2 * x + i] + mu_s[h]);
+            }
         }
-        if (softmax_any(raise || fail)) {
-          // raise the maxima (all threads take this path, or none)
+        if (softmax_any(unset || over > C::RAISE || fail)) {
+          // raise the maxima (all threads take this path, or none), once the
+          // product with V of the piece's tile before has ended
+          if (!fail && tile > 0) fail = !mbar_wait(bar(PVDONE + (buf ^ 1u)), ((tiles - 1) >> 1) & 1u, &gave_up);
           fail = softmax_any(fail);
           if (fail) break;
+          tc_fence_after();
+          float v[NH / 4];
 #pragma unroll
-          for (int j = 0; j < NH; ++j) {
-            float x = s[j];
-            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane == 0) red[warp][j] = x;
-          }
+          for (int j = 0; j < NH / 4; ++j)
+            v[j] = fmaxf(e[4 * (j >> 1) + (j & 1)], e[4 * (j >> 1) + 2 + (j & 1)]);
+          reduce_columns<NH, true>(v, lane, red[warp]);
           softmax_sync();
+          float now = 0.f;
           if (tid < NH) {
-            const float old = m_s[tid];
-            const float now = fmaxf(fmaxf(old, red[0][tid]), fmaxf(fmaxf(red[1][tid], red[2][tid]), red[3][tid]));
+            const float mu = mu_s[tid], old = m_s[tid];
+            const float top = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid])) + mu;
+            now = fmaxf(old, top);
             f_s[tid] = old == -INFINITY ? 0.f : exp2_fast(old - now);
             m_s[tid] = now;
+            const float use = now == -INFINITY ? 0.f : now;
+            d_s[tid] = mu - use;
+            mu_s[tid] = use;
           }
-          softmax_sync();
+          unset = softmax_any(now == -INFINITY);
 #pragma unroll
-          for (int j = 0; j < NH; ++j) l[j] *= f_s[j];
-          // the product with V of the tile before has ended: S came after it
+          for (int j = 0; j < NH / 4; ++j) {
+            const int h = 8 * (j >> 1) + 2 * c + (j & 1);
+            l[j] *= f_s[h];
+            e[4 * (j >> 1) + (j & 1)] += d_s[h];
+            e[4 * (j >> 1) + 2 + (j & 1)] += d_s[h];
+          }
           if (tile > 0) {
 #pragma unroll 1
             for (int j = 0; j < 4 * NH; j += 16) {
@@ -494,39 +599,26 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         }
         // P, rounded to the cache's type for the tensor cores (the sums l keep all
         // bits), over the rope block: a row of heads per token
-        unsigned char *prow = rope_p + rope * kRopeB + tid * 128;
+        unsigned char *prow = rope_p + rope * kRopeB + row0 * 128 + c * 4;
 #pragma unroll
-        for (int j = 0; j < NH; j += 8) {
-          uint32_t w[4];
-          float e[8];
+        for (int n = 0; n < NH / 8; ++n) {
 #pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            const float4 m = *reinterpret_cast<const float4 *>(&m_s[j + i]);
-            const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              e[i + x] = exp2_fast(s[j + i + x] - (mm[x] == -INFINITY ? 0.f : mm[x]));
-              l[j + i + x] += e[i + x];
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack2<C::BF16>(e[2 * i], e[2 * i + 1]);
-          *reinterpret_cast<uint4 *>(prow + (((j >> 3) ^ (tid & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) e[4 * n + i] = exp2_fast(e[4 * n + i]);
+          l[2 * n] += e[4 * n] + e[4 * n + 2];
+          l[2 * n + 1] += e[4 * n + 1] + e[4 * n + 3];
+          const int at = (n ^ (row0 & 7)) << 4;   // rows 8 apart share it
+          *reinterpret_cast<uint32_t *>(prow + at) = pack2<C::BF16>(e[4 * n], e[4 * n + 1]);
+          *reinterpret_cast<uint32_t *>(prow + at + 1024) = pack2<C::BF16>(e[4 * n + 2], e[4 * n + 3]);
         }
         if (++rope == C::ROPES) rope = 0;
         proxy_fence();
         tc_fence_before();
-        mbar_arrive(bar(PFULL));
+        mbar_arrive(bar(PFULL + buf));
       }
       if (fail) break;
       // ---- the piece's end
-#pragma unroll
-      for (int j = 0; j < NH; ++j) {
-        float x = l[j];
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) red[warp][j] = x;
-      }
-      fail = !mbar_wait(bar(PVDONE), (tiles - 1) & 1u, &gave_up);
+      reduce_columns<NH, false>(l, lane, red[warp]);
+      fail = !mbar_wait(bar(PVDONE + ((tiles - 1) & 1u)), ((tiles - 1) >> 1) & 1u, &gave_up);
       tc_fence_after();
       fail = softmax_any(fail);
       if (fail) break;
@@ -576,6 +668,9 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   }
   __syncthreads();
   if (warp == 4) {
+    // nothing is in flight when the tensor memory is given back
+    mbar_wait(bar(LAST), 0, &gave_up);
+    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
   }
