@@ -8,10 +8,13 @@
 // has more than one tile more than another.  A warp streams its range through a
 // ring of its own in shared memory (cp.async, page numbers read one tile ahead,
 // no block-wide barrier until the end) and keeps a running maximum and sum per
-// head.  The products are mma.sync m16n8k16 with the group's heads as the 16
-// rows (8 of them unused for groups up to 8): the tensor work is a fraction of
-// the time the tile's bytes take, and the exponentials of a tile are already in
-// the registers that the product with V wants them in.
+// head.  The products are mma.sync m16n8k16 with the 16 tokens (for V: 16 elements
+// of the head) as rows and the group's heads as columns, 8 at a time, so that a
+// group of 4 costs half of what heads as rows would; one 8 x 8 transposition per
+// 8 tokens takes the exponentials from one product to the other.  The running
+// maximum is raised only when a score passes it by as much (in log2) as the
+// products' type allows (fp16 ends at 2^16; bf16 has room for 2^40 and its sums):
+// the usual tile needs a vote and no reduction.
 //
 // A warp that has all tiles of a (sequence, kv head) writes the result itself.
 // The others leave a partial result, joined in tile order: first among the warps
@@ -43,17 +46,20 @@ struct KvConfig {
   static constexpr int TYPE = TYPE_;
   static constexpr int ROWS = ROWS_;              // query heads of a unit
   static constexpr int ES = TYPE_ == kE4m3 ? 1 : 2;
-  static constexpr int WARPS = DP_ == 256 && TYPE_ != kE4m3 ? 4 : 8;
+  // 192 KiB of ring a CTA, one CTA per SM, in as many warps as leave each three
+  // tiles or more (with few bytes to a tile it is the warps' own latency that
+  // binds) and registers enough: 128 e4m3 elements spill at 16 warps
+  static constexpr int WARPS = DP_ * ES >= 512 ? 4 : DP_ * ES >= 256 ? 8 : TYPE_ == kE4m3 && DP_ == 128 ? 12 : 16;
   static constexpr int CH = DP_ * ES / 16;        // 16-byte chunks of a row
   static constexpr int ROWB = DP_ * ES;
   static constexpr int TILE_B = 2 * kTok * ROWB;  // K and V
-  // 192 KiB of ring a CTA, one CTA per SM: all but one stage in flight
   static constexpr int RAW = 192 * 1024 / (WARPS * TILE_B);
   static constexpr int STAGES = RAW > 8 ? 8 : RAW;
   static constexpr int RING_B = STAGES * TILE_B;
   static constexpr int KS = DP_ / 16;             // k steps of q . k
-  static constexpr int NT = DP_ / 8;              // n tiles of the output
-  static constexpr int RH = ROWS_ / 8;            // 8-row halves in use
+  static constexpr int MT = DP_ / 16;             // m tiles of the output
+  static constexpr int NB = ROWS_ / 8;            // n tiles: 8 heads each
+  static constexpr float RAISE = TYPE_ == kBf16 ? 40.f : 14.f;
   static constexpr int PIECE = ROWS_ * DP_ + 2 * ROWS_;   // floats of a partial result: O, m, l
   static constexpr int SMEM = WARPS * RING_B;
   static_assert(STAGES >= 2 && RING_B >= ROWS_ * DP_ * 4, "ring");
@@ -72,20 +78,23 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t *r, uint32_t a) {
                : "memory");
 }
 
-// c += a b, 16 x 8 x 16.  RH == 1: rows 8..15 of a are zero and their sums unused.
-template <bool BF16, int RH>
+// c += a b, 16 x 8 x 16
+template <bool BF16>
 __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  float x = 0.f, y = 0.f;
-  float &c2 = RH == 2 ? c[2] : x, &c3 = RH == 2 ? c[3] : y;
-  const uint32_t a1 = RH == 2 ? a[1] : 0u, a3 = RH == 2 ? a[3] : 0u;
   if constexpr (BF16)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c2), "+f"(c3)
-        : "r"(a[0]), "r"(a1), "r"(a[2]), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c2), "+f"(c3)
-        : "r"(a[0]), "r"(a1), "r"(a[2]), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// an 8 x 8 matrix of 16-bit elements, a row per 4 lanes, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t u, bool bf16) {
@@ -114,12 +123,11 @@ __device__ __forceinline__ int swizzle(int c, int r) {
   return C::CH >= 8 ? c ^ (((r >> 1) & 3) << 1) : c ^ (((r >> 1) & 1) << 1);
 }
 
-// The output element (column of the head) of n tile `tile`, element e of a
-// lane with c = lane % 4.
+// The elements of the head that rows g and g + 8 of m tile t are.
 template <class C>
-__device__ __forceinline__ int column(int tile, int e, int c) {
-  if constexpr (C::TYPE != kE4m3) return tile * 8 + 2 * c + e;
-  return 32 * (tile >> 2) + 8 * c + 4 * e + (tile & 3);
+__device__ __forceinline__ int element(int t, int upper, int g) {
+  if constexpr (C::TYPE != kE4m3) return 16 * t + 8 * upper + g;
+  return 32 * (t >> 1) + 4 * g + 2 * (t & 1) + upper;
 }
 
 // A tile in a warp's ring.  flags: the tokens present (16 bits), then whether it
@@ -137,7 +145,7 @@ __device__ __forceinline__ int tiles_of(int start, int len) {
 template <class C>
 __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ __align__(128) unsigned char ring_all[];
-  constexpr int THREADS = C::WARPS * 32, ROWS = C::ROWS, RH = C::RH, DP = C::DP;
+  constexpr int THREADS = C::WARPS * 32, ROWS = C::ROWS, NB = C::NB, DP = C::DP;
   constexpr bool MMA_BF16 = C::TYPE == kBf16;
   __shared__ TileMeta meta_all[C::WARPS][C::STAGES];
   __shared__ long long prefix[THREADS + 1];
@@ -148,10 +156,13 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   __shared__ float piece_m[C::WARPS][2][ROWS], piece_l[C::WARPS][2][ROWS];
   __shared__ int piece_b[C::WARPS][2], piece_u[C::WARPS][2], piece_state[C::WARPS][2];
   __shared__ int last_flag;
+  __shared__ float factor[kDecodeCtas][ROWS], row_inv[ROWS];   // joining CTAs' pieces
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c4 = lane & 3;
   const int units = p.Hkv * p.QB;                 // units of a sequence
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
   // ---- the tiles before each sequence; thread i takes `per` sequences
   const int per = (p.B + THREADS - 1) / THREADS;
@@ -228,23 +239,38 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     const int t = t0 + (lane & 15);
     const int kvh = lu / p.QB;
     const bool ok = page_present(lpage, p.num_pages);
-    int64_t off = 0;
-    if (ok) off = ((int64_t(lpage) * p.P + (t - lpg * p.P)) * p.row + int64_t(kvh) * p.D) * C::ES;
     const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
     const uint32_t base = ring_s + lstage * C::TILE_B;
     constexpr int RPI = C::CH <= 32 ? 32 / C::CH : 1;         // rows per instruction
     static_assert(C::CH <= 32, "a row is at most a warp of chunks");
-    const int c = lane % C::CH;
+    const int c = lane % C::CH, r0 = lane / C::CH;
     const bool in_d = c * 16 < p.D * C::ES;
     const char *kp = static_cast<const char *>(p.k), *vp = static_cast<const char *>(p.v);
+    int64_t off = 0;
+    if (ok) off = ((int64_t(lpage) * p.P + (t - lpg * p.P)) * p.row + int64_t(kvh) * p.D) * C::ES;
+    if (mask == 0xffffu && (p.P & 15) == 0) {     // one page, every row: rows at a fixed distance
+      const int64_t first = __shfl_sync(0xffffffffu, off, 0) + r0 * p.row * C::ES + c * 16;
+      const char *ks = kp + (in_d ? first : 0), *vs = vp + (in_d ? first : 0);
+      const int64_t step = in_d ? RPI * p.row * C::ES : 0;
+      const int n = in_d ? 16 : 0;
 #pragma unroll
-    for (int i = 0; i < kTok / RPI; ++i) {
-      const int r = i * RPI + lane / C::CH;
-      const int64_t o = __shfl_sync(0xffffffffu, off, r);
-      const bool have = in_d && ((mask >> r) & 1u);
-      const int64_t at = have ? o + c * 16 : 0;
-      cp_async16(base + r * C::ROWB + swizzle<C, false>(c, r) * 16, kp + at, have ? 16 : 0);
-      cp_async16(base + kTok * C::ROWB + r * C::ROWB + swizzle<C, true>(c, r) * 16, vp + at, have ? 16 : 0);
+      for (int i = 0; i < kTok / RPI; ++i) {
+        const int r = i * RPI + r0;
+        cp_async16(base + r * C::ROWB + swizzle<C, false>(c, r) * 16, ks, n);
+        cp_async16(base + kTok * C::ROWB + r * C::ROWB + swizzle<C, true>(c, r) * 16, vs, n);
+        ks += step;
+        vs += step;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok / RPI; ++i) {
+        const int r = i * RPI + r0;
+        const int64_t o = __shfl_sync(0xffffffffu, off, r);
+        const bool have = in_d && ((mask >> r) & 1u);
+        const int64_t at = have ? o + c * 16 : 0;
+        cp_async16(base + r * C::ROWB + swizzle<C, false>(c, r) * 16, kp + at, have ? 16 : 0);
+        cp_async16(base + kTok * C::ROWB + r * C::ROWB + swizzle<C, true>(c, r) * 16, vp + at, have ? 16 : 0);
+      }
     }
     if (lane == 0) {
       uint32_t f = mask;
@@ -273,44 +299,46 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     if (lnext < hi) load();
     cp_commit();
   }
-  uint32_t qf[C::KS][4];                          // q as the A operand
-  float qmul[2] = {0.f, 0.f};                     // scale2, and for e4m3 the power of two taken out of q
-  float o[C::NT][RH * 2];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  uint32_t qf[C::KS][NB][2];                      // q as the B operand
+  // of heads 8 n + 2 c4 and + 1: the scale (for e4m3 with the power of two taken out
+  // of q), the maximum, what scores are taken relative to, the sum
+  float qmul[NB][2], m[NB][2], mu[NB][2], l[NB][2];
+  float o[C::MT][NB][4];
   int h0 = 0, rows = 0, pieces = 0, stage = 0;
 #pragma unroll 1
   for (long long it = lo; it < hi; ++it) {
     __syncwarp();                                 // everyone is done with the stage that is filled next
     if (lnext < hi) load();
     cp_commit();
-    cp_wait<C::STAGES - 1>();
-    __syncwarp();
-    const TileMeta tm = meta[stage];
+    const TileMeta tm = meta[stage];              // written a turn ago or more
     if (tm.flags & (1u << 16)) {                  // a new piece: its q
       const int kvh = tm.u / p.QB, qb = tm.u - kvh * p.QB;
       h0 = kvh * p.G + qb * ROWS;
       rows = min(ROWS, p.G - qb * ROWS);
 #pragma unroll
-      for (int i = 0; i < C::NT; ++i)
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-        for (int j = 0; j < RH * 2; ++j) o[i][j] = 0.f;
+        for (int t = 0; t < C::MT; ++t)
 #pragma unroll
-      for (int x = 0; x < RH; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.f;
-        qmul[x] = p.scale2;
-        const int r = g + 8 * x;
+          for (int i = 0; i < 4; ++i) o[t][n][i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qmul[n][i] = p.scale2;
+          m[n][i] = -INFINITY;
+          mu[n][i] = 0.f;
+          l[n][i] = 0.f;
+        }
+        const int r = 8 * n + g;
         const char *qp = static_cast<const char *>(p.q) + 2 * (int64_t(tm.b) * p.q_sb + int64_t(h0 + r) * p.q_sh);
         const bool live = r < rows;
-        if constexpr (C::TYPE != kE4m3) {
 #pragma unroll
-          for (int s = 0; s < C::KS; ++s)
+        for (int s = 0; s < C::KS; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int d = s * 16 + e * 8 + 2 * c4;
-              qf[s][x + 2 * e] = live && d < p.D ? __ldg(reinterpret_cast<const unsigned int *>(qp + 2 * d)) : 0u;
-            }
-        } else {
+          for (int e = 0; e < 2; ++e) {
+            const int d = C::TYPE != kE4m3 ? s * 16 + e * 8 + 2 * c4 : (s >> 2) * 64 + c4 * 16 + (s & 3) * 4 + 2 * e;
+            qf[s][n][e] = live && d < p.D ? __ldg(reinterpret_cast<const unsigned int *>(qp + 2 * d)) : 0u;
+          }
+        if constexpr (C::TYPE == kE4m3) {
           // fp16, after the power of two that brings the head's largest element
           // into [1, 2): bf16 and fp16 queries keep every bit down to 2^-14
           // of it, and below that are off by 2^-25 of it at most
@@ -319,132 +347,133 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
           for (int s = 0; s < C::KS; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int d = (s >> 2) * 64 + c4 * 16 + (s & 3) * 4 + 2 * e;
-              const uint32_t u = live && d < p.D ? __ldg(reinterpret_cast<const unsigned int *>(qp + 2 * d)) : 0u;
-              qf[s][x + 2 * e] = u;
-              const float2 f = unpack2(u, p.bf16);
+              const float2 f = unpack2(qf[s][n][e], p.bf16);
               top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int ex = top > 0.f && top < INFINITY ? max(-120, min(120, ilogbf(top))) : 0;
-          const float down = ldexpf(1.f, -ex);
-          qmul[x] = p.scale2 * ldexpf(1.f, ex);
+          const float down = ldexpf(1.f, -ex), up = p.scale2 * ldexpf(1.f, ex);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qmul[n][i] = __shfl_sync(0xffffffffu, up, (2 * c4 + i) * 4);
 #pragma unroll
           for (int s = 0; s < C::KS; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float2 f = unpack2(qf[s][x + 2 * e], p.bf16);
-              qf[s][x + 2 * e] = pack2<false>(f.x * down, f.y * down);
+              const float2 f = unpack2(qf[s][n][e], p.bf16);
+              qf[s][n][e] = pack2<false>(f.x * down, f.y * down);
             }
         }
       }
     }
+    cp_wait<C::STAGES - 1>();
+    __syncwarp();
 
-    // ---- scores: the unit's rows x 16 tokens
-    float sc[2][4] = {};
+    // ---- scores: 16 tokens x the unit's heads
+    float sc[NB][4] = {};
     const uint32_t kb = ring_s + stage * C::TILE_B, vb = kb + kTok * C::ROWB;
     if constexpr (C::TYPE != kE4m3) {
-      const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
+      const int r = lane & 15, cc = lane >> 4;
 #pragma unroll
       for (int s = 0; s < C::KS; ++s) {
         uint32_t f[4];
         ldmatrix4(f, kb + r * C::ROWB + ((2 * s + cc) ^ (r & 7)) * 16);
-        mma<MMA_BF16, RH>(sc[0], qf[s], f[0], f[1]);
-        mma<MMA_BF16, RH>(sc[1], qf[s], f[2], f[3]);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma<MMA_BF16>(sc[n], f, qf[s][n][0], qf[s][n][1]);
       }
     } else {
-      // a lane's 16 bytes of a token are the B operand of four k steps (which
+      // a lane's 16 bytes of a token are the A operand of four k steps (which
       // element of the head a k index stands for is free, as long as q agrees)
 #pragma unroll
-      for (int kk = 0; kk < C::KS / 4; ++kk)
+      for (int kk = 0; kk < C::KS / 4; ++kk) {
+        uint4 w[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int r = g + nt * 8;
-          const uint4 w = *reinterpret_cast<const uint4 *>(ring + stage * C::TILE_B + r * C::ROWB +
-                                                           swizzle<C, false>(kk * 4 + c4, r) * 16);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        for (int x = 0; x < 2; ++x)
+          w[x] = *reinterpret_cast<const uint4 *>(ring + stage * C::TILE_B + (g + 8 * x) * C::ROWB +
+                                                  swizzle<C, false>(kk * 4 + c4, g + 8 * x) * 16);
+        const uint32_t lo_w[4] = {w[0].x, w[0].y, w[0].z, w[0].w}, hi_w[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma<false, RH>(sc[nt], qf[kk * 4 + i], e4m3_lo(ws[i]), e4m3_hi(ws[i]));
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t f[4] = {e4m3_lo(lo_w[i]), e4m3_lo(hi_w[i]), e4m3_hi(lo_w[i]), e4m3_hi(hi_w[i])};
+#pragma unroll
+          for (int n = 0; n < NB; ++n) mma<false>(sc[n], f, qf[kk * 4 + i][n][0], qf[kk * 4 + i][n][1]);
         }
+      }
     }
+    bool raise = false;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
-      for (int x = 0; x < RH; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) sc[nt][2 * x + e] *= qmul[x];
+      for (int i = 0; i < 4; ++i) sc[n][i] = fmaf(sc[n][i], qmul[n][i & 1], -mu[n][i & 1]);
     if ((tm.flags & 0xffffu) != 0xffffu) {
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int x = 0; x < 2; ++x)
+        if (!((tm.flags >> (g + 8 * x)) & 1u)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!((tm.flags >> (nt * 8 + 2 * c4 + e)) & 1u)) {
-#pragma unroll
-            for (int x = 0; x < RH; ++x) sc[nt][2 * x + e] = -INFINITY;
-          }
+          for (int n = 0; n < NB; ++n) sc[n][2 * x] = sc[n][2 * x + 1] = -INFINITY;
+        }
     }
     if (p.weights) {
 #pragma unroll
-      for (int x = 0; x < RH; ++x)
-        if (g + 8 * x < rows) {
-          float *d = p.scores + (int64_t(tm.b) * p.Hq + h0 + g + 8 * x) * p.score_row + tm.t0 + 2 * c4;
-          __stcg(reinterpret_cast<float2 *>(d), make_float2(sc[0][2 * x], sc[0][2 * x + 1]));
-          __stcg(reinterpret_cast<float2 *>(d + 8), make_float2(sc[1][2 * x], sc[1][2 * x + 1]));
-        }
-    }
-
-    // ---- running maximum: raised only when a score passes it by as much (in log2)
-    // as the products' type allows, so that the sums are rarely rescaled: fp16
-    // ends at 2^16, bf16 has room for 2^40 and its sums
-    constexpr float RAISE = MMA_BF16 ? 40.f : 14.f;
-    uint32_t pf[4] = {0u, 0u, 0u, 0u};
-    float top[2];
-    bool raise = false;
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int x = 0; x < RH; ++x) {
-      float t = fmaxf(fmaxf(sc[0][2 * x], sc[0][2 * x + 1]), fmaxf(sc[1][2 * x], sc[1][2 * x + 1]));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-      t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      top[x] = t;
-      raise |= t > m[x] + RAISE;
+        for (int i = 0; i < 2; ++i)
+          if (8 * n + 2 * c4 + i < rows) {
+            float *d = p.scores + (int64_t(tm.b) * p.Hq + h0 + 8 * n + 2 * c4 + i) * p.score_row + tm.t0 + g;
+            __stcg(d, sc[n][i] + mu[n][i]);
+            __stcg(d + 8, sc[n][2 + i] + mu[n][i]);
+          }
     }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        raise |= fmaxf(sc[n][i], sc[n][2 + i]) > C::RAISE || m[n][i] == -INFINITY;
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int x = 0; x < RH; ++x) {
-        const float m2 = fmaxf(m[x], top[x]);
-        const float f = m[x] == -INFINITY ? 0.f : exp2_fast(m[x] - m2);
-        m[x] = m2;
-        l[x] *= f;
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < C::NT; ++i) {
-          o[i][2 * x] *= f;
-          o[i][2 * x + 1] *= f;
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(sc[n][i], sc[n][2 + i]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          const float m2 = fmaxf(m[n][i], top + mu[n][i]);
+          const float f = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - m2);
+          const float use = m2 == -INFINITY ? 0.f : m2, by = mu[n][i] - use;
+          m[n][i] = m2;
+          mu[n][i] = use;
+          sc[n][i] += by;
+          sc[n][2 + i] += by;
+          l[n][i] *= f;
+#pragma unroll
+          for (int t = 0; t < C::MT; ++t) {
+            o[t][n][i] *= f;
+            o[t][n][2 + i] *= f;
+          }
         }
-      }
     }
+    uint32_t pf[NB][2];                           // the exponentials as the B operand
 #pragma unroll
-    for (int x = 0; x < RH; ++x) {
-      const float mm = m[x] == -INFINITY ? 0.f : m[x];
-      float e[4];
+    for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = exp2_fast(sc[i >> 1][2 * x + (i & 1)] - mm);
-      l[x] += (e[0] + e[1]) + (e[2] + e[3]);
+      for (int i = 0; i < 4; ++i) sc[n][i] = exp2_fast(sc[n][i]);
+      l[n][0] += sc[n][0] + sc[n][2];
+      l[n][1] += sc[n][1] + sc[n][3];
       // rounded to the product's type for the tensor cores; the sum above keeps
       // all bits, and the rounding errors of many tokens average out
-      pf[x] = pack2<MMA_BF16>(e[0], e[1]);
-      pf[x + 2] = pack2<MMA_BF16>(e[2], e[3]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) pf[n][x] = transpose8(pack2<MMA_BF16>(sc[n][2 * x], sc[n][2 * x + 1]));
     }
 
-    // ---- O += P V
+    // ---- O^T += V^T P^T
     if constexpr (C::TYPE != kE4m3) {
-      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), cc = lane >> 4;
+      const int r = (lane & 7) + ((lane >> 4) << 3), cc = (lane >> 3) & 1;
 #pragma unroll
-      for (int n = 0; n < C::NT; n += 2) {
+      for (int t = 0; t < C::MT; ++t) {
         uint32_t f[4];
-        ldmatrix4_trans(f, vb + r * C::ROWB + ((n + cc) ^ (r & 7)) * 16);
-        mma<MMA_BF16, RH>(o[n], pf, f[0], f[1]);
-        mma<MMA_BF16, RH>(o[n + 1], pf, f[2], f[3]);
+        ldmatrix4_trans(f, vb + r * C::ROWB + ((2 * t + cc) ^ (r & 7)) * 16);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mma<MMA_BF16>(o[t][n], f, pf[n][0], pf[n][1]);
       }
     } else {
       const unsigned char *vr = ring + stage * C::TILE_B + kTok * C::ROWB;
@@ -457,13 +486,16 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
           w[i] = *reinterpret_cast<const uint32_t *>(vr + r * C::ROWB + swizzle<C, true>(2 * j + (g >> 2), r) * 16 +
                                                      (g & 3) * 4);
         }
-        // 4 tokens x 4 columns transposed: tokens (2c, 2c+1) and (2c+8, 2c+9) side by side
+        // 4 tokens x 4 elements transposed: tokens (2c, 2c+1) and (2c+8, 2c+9) side by side
         const uint32_t a01 = __byte_perm(w[0], w[1], 0x5140), a23 = __byte_perm(w[0], w[1], 0x7362);
         const uint32_t b01 = __byte_perm(w[2], w[3], 0x5140), b23 = __byte_perm(w[2], w[3], 0x7362);
-        mma<false, RH>(o[4 * j + 0], pf, e4m3_lo(a01), e4m3_lo(b01));
-        mma<false, RH>(o[4 * j + 1], pf, e4m3_hi(a01), e4m3_hi(b01));
-        mma<false, RH>(o[4 * j + 2], pf, e4m3_lo(a23), e4m3_lo(b23));
-        mma<false, RH>(o[4 * j + 3], pf, e4m3_hi(a23), e4m3_hi(b23));
+        const uint32_t f0[4] = {e4m3_lo(a01), e4m3_hi(a01), e4m3_lo(b01), e4m3_hi(b01)};
+        const uint32_t f1[4] = {e4m3_lo(a23), e4m3_hi(a23), e4m3_lo(b23), e4m3_hi(b23)};
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          mma<false>(o[2 * j][n], f0, pf[n][0], pf[n][1]);
+          mma<false>(o[2 * j + 1][n], f1, pf[n][0], pf[n][1]);
+        }
       }
     }
     if (++stage == C::STAGES) stage = 0;
@@ -472,21 +504,50 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     if (tm.flags & (1u << 17)) {
       const int whole = int(tm.flags >> 18) & 3;
 #pragma unroll
-      for (int x = 0; x < RH; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-      }
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], w);
       if (whole == 3) {
 #pragma unroll
-        for (int x = 0; x < RH; ++x) {
-          const int r = g + 8 * x;
-          if (r >= rows) continue;
-          const float inv = l[x] == 0.f ? 0.f : p.v_scale / l[x];
+        for (int n = 0; n < NB; ++n) {
+          float inv[2];
 #pragma unroll
-          for (int i = 0; i < C::NT; ++i)
+          for (int i = 0; i < 2; ++i) {
+            inv[i] = l[n][i] == 0.f ? 0.f : p.v_scale / l[n][i];
+            const int r = 8 * n + 2 * c4 + i;
+            if (g == 0 && r < rows) store_lse(p, tm.b, h0 + r, m[n][i], l[n][i]);
+          }
+          if constexpr (C::TYPE != kE4m3) {       // a head's pairs of elements, by a transposition
+            const int r = 8 * n + g;
+            char *dst = static_cast<char *>(p.out) + 2 * (int64_t(tm.b) * p.o_sb + int64_t(h0 + r) * p.o_sh);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) store_out(p, tm.b, h0 + r, column<C>(i, e, c4), o[i][2 * x + e] * inv);
-          if (c4 == 0) store_lse(p, tm.b, h0 + r, m[x], l[x]);
+            for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t w =
+                    transpose8(pack2<MMA_BF16>(o[t][n][2 * x] * inv[0], o[t][n][2 * x + 1] * inv[1]));
+                const int d = 16 * t + 8 * x + 2 * c4;
+                if (r < rows && d < p.D) *reinterpret_cast<uint32_t *>(dst + 2 * d) = w;
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 8 * n + 2 * c4 + i;
+              char *dst = static_cast<char *>(p.out) + 2 * (int64_t(tm.b) * p.o_sb + int64_t(h0 + r) * p.o_sh);
+#pragma unroll
+              for (int j = 0; j < DP / 32; ++j) { // 4 elements in a row
+                const int d = 32 * j + 4 * g;
+                const float v0 = o[2 * j][n][i] * inv[i], v1 = o[2 * j][n][2 + i] * inv[i];
+                const float v2 = o[2 * j + 1][n][i] * inv[i], v3 = o[2 * j + 1][n][2 + i] * inv[i];
+                if (r < rows && d < p.D)
+                  *reinterpret_cast<uint2 *>(dst + 2 * d) =
+                      p.bf16 ? make_uint2(pack2<true>(v0, v1), pack2<true>(v2, v3))
+                             : make_uint2(pack2<false>(v0, v1), pack2<false>(v2, v3));
+              }
+            }
+          }
         }
       } else {
         // the warp's last piece goes into its own ring, which nothing else will
@@ -499,17 +560,19 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
           __syncwarp();
         }
 #pragma unroll
-        for (int x = 0; x < RH; ++x) {
-          const int r = g + 8 * x;
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int i = 0; i < C::NT; ++i)
+          for (int i = 0; i < 2; ++i) {
+            const int r = 8 * n + 2 * c4 + i;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) dst[r * DP + column<C>(i, e, c4)] = o[i][2 * x + e];
-          if (c4 == 0) {
-            piece_m[warp][k][r] = m[x];
-            piece_l[warp][k][r] = l[x];
+            for (int t = 0; t < C::MT; ++t)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) dst[r * DP + element<C>(t, x, g)] = o[t][n][2 * x + i];
+            if (g == 0) {
+              piece_m[warp][k][r] = m[n][i];
+              piece_l[warp][k][r] = l[n][i];
+            }
           }
-        }
         if (lane == 0) {
           piece_o[warp][k] = dst;
           piece_b[warp][k] = tm.b;
@@ -586,21 +649,46 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
       __syncthreads();
       if (last_flag) {
         __threadfence();
-        // piece x of the unit: CTA c0 + x, its second slot where the unit begins
+        // piece x of the unit: CTA c0 + x, its second slot where the unit begins.
+        // First the factors of all pieces, a warp for a row; then O, by 4 columns
         auto slot = [&](int x) { return p.cta_parts + (int64_t(c0 + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
-        for (int i = tid; i < nr * DP; i += THREADS) {
-          const int r = i / DP, d = i - r * DP;
-          float mm = -INFINITY;
-          for (int x = 0; x < np; ++x) mm = fmaxf(mm, __ldcg(slot(x) + ROWS * DP + r));
-          float acc = 0.f, sum = 0.f;
-          for (int x = 0; x < np; ++x) {
+        for (int r = warp; r < nr; r += C::WARPS) {
+          float mm = -INFINITY, sum = 0.f;
+          for (int x = lane; x < np; x += 32) {
             const float mx = __ldcg(slot(x) + ROWS * DP + r);
-            const float f = mx == -INFINITY ? 0.f : exp2_fast(mx - mm);
-            acc += f * __ldcg(slot(x) + i);
+            factor[x][r] = mx;
+            mm = fmaxf(mm, mx);
+          }
+          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+          for (int x = lane; x < np; x += 32) {
+            const float f = factor[x][r] == -INFINITY ? 0.f : exp2_fast(factor[x][r] - mm);
+            factor[x][r] = f;
             sum += f * __ldcg(slot(x) + ROWS * DP + ROWS + r);
           }
-          store_out(p, b, hh + r, d, acc * (sum == 0.f ? 0.f : p.v_scale / sum));
-          if (d == 0) store_lse(p, b, hh + r, mm, sum);
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) {
+            row_inv[r] = sum == 0.f ? 0.f : p.v_scale / sum;
+            store_lse(p, b, hh + r, mm, sum);
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < nr * DP / 4; i += THREADS) {
+          const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int x = 0; x < np; ++x) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot(x)) + i);
+            const float f = factor[x][r];
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+          }
+          const float inv = row_inv[r];
+          store_out(p, b, hh + r, d, acc.x * inv);
+          store_out(p, b, hh + r, d + 1, acc.y * inv);
+          store_out(p, b, hh + r, d + 2, acc.z * inv);
+          store_out(p, b, hh + r, d + 3, acc.w * inv);
         }
       }
       __syncthreads();
@@ -612,41 +700,71 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
 // ---- page weights ----------------------------------------------------------------
 
 // weights[b, p] <- decay * weights[b, p] + sum over heads and tokens of
-// 2^(score - lse2).  A block takes as many whole pages as 256 tokens hold (one
-// page if it is longer); each thread sums a token over the heads, then each
-// page is summed in token order, so the result does not depend on timing.
-constexpr int kWeightThreads = 256;
+// 2^(score - lse2).  Bound by reading the scores (4 bytes a head and token).  A
+// block takes as many whole pages as 128 tokens hold (one page if it is longer),
+// a warp every eighth head, a lane four tokens of it, so that the loads of all
+// its heads are on their way together.  Then each token is summed over the warps
+// and each page over its tokens, in an order that does not depend on timing.
+constexpr int kWeightThreads = 256, kWeightTok = 128;
+
+HC_HD int weight_pages(int page) { return page < kWeightTok ? kWeightTok / page : 1; }
 
 __global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ DecodeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores and lse of the kernel before
-  __shared__ float val[kWeightThreads];
-  const int b = blockIdx.y, tid = int(threadIdx.x);
-  const int64_t cap = int64_t(p.max_pages) * p.P;
-  const int len = int(min(int64_t(max(0, p.lens[b])), cap));
-  const int start = p.window > 0 ? max(0, len - p.window) : 0;
-  const int per = max(1, kWeightThreads / p.P);            // pages of a block
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int WARPS = kWeightThreads / 32;
+  __shared__ float part[WARPS][kWeightTok], val[kWeightTok];
+  const int b = blockIdx.y, tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  int start, len;
+  seq_range(p, b, &start, &len);
+  const int per = weight_pages(p.P);                       // pages of a block
   const int first = int(blockIdx.x) * per;
   const int pages = int(len > 0 ? fast_div(uint32_t(len - 1), p.fd_page) + 1 : 0);
   if (first >= pages) return;
-  const int t0 = first * p.P, t1 = min(len, int(min(int64_t(len), (int64_t(first) + per) * p.P)));
+  const int t0 = first * p.P, t1 = int(min(int64_t(len), (int64_t(first) + per) * p.P));
   const float *lse2 = p.lse2 + int64_t(b) * p.Hq;
   const float *sc = p.scores + int64_t(b) * p.Hq * p.score_row;
-  float sum = 0.f;
-  for (int t = t0 + tid; t < t1; t += kWeightThreads) {
-    if (t < start) continue;
-    for (int h = 0; h < p.Hq; ++h) {
-      const float s = sc[h * p.score_row + t];
-      if (s != -INFINITY) sum += exp2f(s - __ldg(lse2 + h));
+  float whole = 0.f;                                       // a long page: this thread's tokens of it
+  for (int base = t0; base < t1; base += kWeightTok) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int h = warp; h < p.Hq; h += WARPS) {
+      const float z = __ldg(lse2 + h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = base + lane + 32 * j;
+        const float s = t >= start && t < t1 ? __ldcs(sc + h * p.score_row + t) : -INFINITY;
+        acc[j] += s == -INFINITY ? 0.f : exp2_fast(s - z);
+      }
+    }
+    __syncthreads();                                       // part is free again
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[warp][lane + 32 * j] = acc[j];
+    __syncthreads();
+    if (tid < kWeightTok) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) v += part[w][tid];
+      val[tid] = v;
+      whole += v;
     }
   }
-  val[tid] = sum;
+  if (p.P > kWeightTok) {
+    if (tid < kWeightTok) val[tid] = whole;
+    __syncthreads();
+  }
   __syncthreads();
-  if (p.P > kWeightThreads) {
-    for (int o = kWeightThreads / 2; o > 0; o >>= 1) {
-      if (tid < o) val[tid] += val[tid + o];
-      __syncthreads();
+  if (p.P >= 32) {                                         // a warp for a page
+    for (int pg = warp; pg < per && first + pg < pages; pg += WARPS) {
+      const int n = min(p.P, kWeightTok);
+      float s = 0.f;
+      for (int i = lane; i < n; i += 32) s += val[pg * n + i];
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) {
+        float *w = p.weights + b * p.w_sb + first + pg;
+        *w = p.decay * *w + s;
+      }
     }
-    if (tid == 0) p.weights[b * p.w_sb + first] = p.decay * p.weights[b * p.w_sb + first] + val[0];
   } else if (tid < per && first + tid < pages) {
     float s = 0.f;
     for (int i = 0; i < p.P; ++i) s += val[tid * p.P + i];
@@ -667,8 +785,7 @@ int launch_kv(const DecodeParams &p, int grid, int device, cudaStream_t st) {
     if (e != cudaSuccess) return int(e);
     if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
   }
-  decode_kv_kernel<C><<<unsigned(grid), C::WARPS * 32, C::SMEM, st>>>(p);
-  return int(cudaGetLastError());
+  return launch_dependent(decode_kv_kernel<C>, dim3(unsigned(grid)), C::WARPS * 32, st, p, C::SMEM);
 }
 
 template <int TYPE, int ROWS>
@@ -705,7 +822,7 @@ DecodeSpace decode_space(const DecodeParams &p, bool weights) {
     const int64_t rows = decode_rows(p.G), dp = p.D <= 64 ? 64 : p.D <= 128 ? 128 : 256;
     at = round_up(at + grid * 2 * (rows * dp + 2 * rows) * 4, 256);
     s.warp_parts = at;
-    at = round_up(at + grid * 8 * rows * dp * 4, 256);
+    at = round_up(at + grid * 16 * rows * dp * 4, 256);
   }
   s.score_row = round_up(int64_t(p.max_pages) * p.P, kTok);
   if (weights) {
@@ -729,7 +846,7 @@ int launch_decode(const DecodeParams &p, int device, void *stream, int *launches
     *launches += e == 0;
   }
   if (e || !p.weights) return e;
-  const int per = p.P < kWeightThreads ? kWeightThreads / p.P : 1;
+  const int per = weight_pages(p.P);
   e = launch_dependent(weights_kernel, dim3(unsigned((p.max_pages + per - 1) / per), unsigned(p.B)), kWeightThreads, st,
                        p);
   *launches += e == 0;

@@ -33,9 +33,10 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 2^x to two units of the last place; results under 2^-126 are zero
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -86,16 +87,17 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long *scr
   return before + inc - mine;
 }
 
-// Launches a kernel that may start while the one before it on the stream ends:
-// it must wait (griddepcontrol.wait) before it touches memory.
+// Launches a kernel that may start while the work before it on the stream ends:
+// it waits (griddepcontrol.wait) before it touches memory.
 inline int launch_dependent(void (*kernel)(const DecodeParams), dim3 grid, unsigned threads, cudaStream_t st,
-                            const DecodeParams &p) {
+                            const DecodeParams &p, size_t smem = 0) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
   c.gridDim = grid;
   c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
   c.stream = st;
   c.attrs = &at;
   c.numAttrs = 1;

@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   constexpr int FULL = 0, EMPTY = C::QUADS, RFULL = 2 * C::QUADS, REMPTY = RFULL + C::ROPES, QFULL = REMPTY + C::ROPES,
                 QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 4, PVDONE = QFULL + 6, LAST = QFULL + 8;
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
+
   // the strips before each sequence
   const int per = (p.B + kLatThreads - 1) / kLatThreads;
   long long mine = 0, total = 0;
@@ -724,9 +726,9 @@ int launch_lat(const DecodeParams &p, int device, cudaStream_t st) {
     if (e != cudaSuccess) return int(e);
     if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
   }
-  decode_latent_kernel<C><<<kDecodeCtas / p.QB * p.QB, kLatThreads, C::SMEM, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return int(e);
+  const int e = launch_dependent(decode_latent_kernel<C>, dim3(unsigned(kDecodeCtas / p.QB * p.QB)), kLatThreads, st, p,
+                                 C::SMEM);
+  if (e) return e;
   return launch_dependent(latent_join_kernel<NH>, dim3(unsigned(p.B) * unsigned(p.Hq)), kJoinThreads, st, p);
 }
 
