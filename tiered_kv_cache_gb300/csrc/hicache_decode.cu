@@ -153,10 +153,12 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   // the CTA's pieces, two per warp: where O lies, m and l, the unit, and
   // (4: present, 1: begins its unit, 2: ends it)
   __shared__ const float *piece_o[C::WARPS][2];
-  __shared__ float piece_m[C::WARPS][2][ROWS], piece_l[C::WARPS][2][ROWS];
+  __shared__ __align__(16) float piece_m[C::WARPS][2][ROWS], piece_l[C::WARPS][2][ROWS];
   __shared__ int piece_b[C::WARPS][2], piece_u[C::WARPS][2], piece_state[C::WARPS][2];
-  __shared__ int last_flag;
-  __shared__ float factor[kDecodeCtas][ROWS], row_inv[ROWS];   // joining CTAs' pieces
+  // joining CTAs' pieces: the two open units (first CTA, pieces if it falls to this
+  // CTA), factor and sum of each piece and row
+  __shared__ int join_cta[2], join_n[2];
+  __shared__ float factor[kDecodeCtas][ROWS], weight[kDecodeCtas][ROWS], row_inv[ROWS];
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c4 = lane & 3;
@@ -585,115 +587,150 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   cp_wait<0>();
   __syncthreads();
 
-  // ---- join the CTA's pieces: runs of pieces of one unit, in order
-  constexpr int PIECES = 2 * C::WARPS;
+  // ---- join the CTA's pieces.  A chain is a run of pieces of one unit: it starts
+  // at a piece that begins its unit, or at the CTA's first piece.
+  constexpr int PIECES = 2 * C::WARPS, COL4 = DP / 4;
+  static_assert(PIECES <= 32, "a lane for a piece");
   const int *state = &piece_state[0][0];
-  auto next = [&](int k) {                        // the first piece at or after k
-    while (k < PIECES && !state[k]) ++k;
-    return k;
+  const int mine_state = lane < PIECES ? state[lane] : 0;
+  const uint32_t present = __ballot_sync(0xffffffffu, mine_state & 4);
+  const uint32_t begin_m = __ballot_sync(0xffffffffu, mine_state & 1), end_m = __ballot_sync(0xffffffffu, mine_state & 2);
+  const uint32_t starts = begin_m | (present & (~present + 1u));
+  auto chain_of = [&](int k, int *k1) {           // the last piece of the chain that starts at k
+    const uint32_t later = k < 31 ? starts & (~0u << (k + 1)) : 0u;
+    const uint32_t upto = later ? (later & (~later + 1u)) - 1u : ~0u;
+    *k1 = 31 - __clz(int(present & upto));
+    return bool((begin_m >> k) & (end_m >> *k1) & 1u);
   };
-  int k0 = next(0);
-  while (k0 < PIECES) {
-    const int b = (&piece_b[0][0])[k0], u = (&piece_u[0][0])[k0];
-    const bool begins = state[k0] & 1;
-    int k1 = k0;                                  // the run's last piece
-    while (!(state[k1] & 2) && next(k1 + 1) < PIECES) k1 = next(k1 + 1);
-    const bool all = begins && (state[k1] & 2);
+  int chain = 0;
+  for (uint32_t left = starts; left; left &= left - 1u, ++chain) {
+    // a warp's worth of chains at a time: warps take elements, not chains
+    const int k0 = __ffs(int(left)) - 1;
+    int k1;
+    const bool all = chain_of(k0, &k1);
+    const int u = (&piece_u[0][0])[k0], b = (&piece_b[0][0])[k0];
     const int kvh = u / p.QB, qb = u - kvh * p.QB;
     const int hh = kvh * p.G + qb * ROWS, nr = min(ROWS, p.G - qb * ROWS);
-    float *part = p.cta_parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE;
-    for (int i = tid; i < nr * DP; i += THREADS) {
-      const int r = i / DP, d = i - r * DP;
+    float *part = p.cta_parts + (int64_t(blockIdx.x) * 2 + int((begin_m >> k0) & 1u)) * C::PIECE;
+    for (int i = (tid + chain * 128) % THREADS; i < nr * COL4; i += THREADS) {
+      const int r = i / COL4, d = (i - r * COL4) * 4;
       float mm = -INFINITY;
-      for (int k = k0; k <= k1; ++k)
-        if (state[k]) mm = fmaxf(mm, (&piece_m[0][0][0])[k * ROWS + r]);
-      float acc = 0.f, sum = 0.f;
-      for (int k = k0; k <= k1; ++k)
-        if (state[k]) {
-          const float mk = (&piece_m[0][0][0])[k * ROWS + r];
-          const float f = mk == -INFINITY ? 0.f : exp2_fast(mk - mm);
-          acc += f * (&piece_o[0][0])[k][i];
-          sum += f * (&piece_l[0][0][0])[k * ROWS + r];
-        }
+      for (uint32_t w = present & (~0u << k0); w; w &= w - 1u) {
+        const int k = __ffs(int(w)) - 1;
+        if (k > k1) break;
+        mm = fmaxf(mm, (&piece_m[0][0][0])[k * ROWS + r]);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+      for (uint32_t w = present & (~0u << k0); w; w &= w - 1u) {
+        const int k = __ffs(int(w)) - 1;
+        if (k > k1) break;
+        const float mk = (&piece_m[0][0][0])[k * ROWS + r];
+        const float f = mk == -INFINITY ? 0.f : exp2_fast(mk - mm);
+        const float4 v = *reinterpret_cast<const float4 *>((&piece_o[0][0])[k] + r * DP + d);
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+        sum += f * (&piece_l[0][0][0])[k * ROWS + r];
+      }
       if (all) {
-        store_out(p, b, hh + r, d, acc * (sum == 0.f ? 0.f : p.v_scale / sum));
+        store_out4(p, b, hh + r, d, acc, sum == 0.f ? 0.f : p.v_scale / sum);
         if (d == 0) store_lse(p, b, hh + r, mm, sum);
       } else {
-        __stcg(part + i, acc);
+        __stcg(reinterpret_cast<float4 *>(part + r * DP + d), acc);
         if (d == 0) {
           __stcg(part + ROWS * DP + r, mm);
           __stcg(part + ROWS * DP + ROWS + r, sum);
         }
       }
     }
-    if (!all) {
-      __threadfence();
-      __syncthreads();
-      // the unit's first tile, its tiles, and the CTAs they lie in
-      int start, len;
-      seq_range(p, b, &start, &len);
-      const int nt = tiles_of(start, len);
-      long long first = prefix[b / per];
-      for (int x = b / per * per; x < b; ++x) {
-        seq_range(p, x, &start, &len);
-        first += (long long)tiles_of(start, len) * units;
-      }
-      first += (long long)u * nt;
-      const int c0 = int(((first + 1) * n_cta - 1) / total), c1 = int(((first + nt) * n_cta - 1) / total);
-      const int np = c1 - c0 + 1;
-      if (tid == 0) {
-        const unsigned int was = atomicAdd(p.counters + c0, 1u);
-        last_flag = was == unsigned(np - 1);
-        if (last_flag) p.counters[c0] = 0u;       // ready for the next call
-      }
-      __syncthreads();
-      if (last_flag) {
-        __threadfence();
-        // piece x of the unit: CTA c0 + x, its second slot where the unit begins.
-        // First the factors of all pieces, a warp for a row; then O, by 4 columns
-        auto slot = [&](int x) { return p.cta_parts + (int64_t(c0 + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
-        for (int r = warp; r < nr; r += C::WARPS) {
-          float mm = -INFINITY, sum = 0.f;
-          for (int x = lane; x < np; x += 32) {
-            const float mx = __ldcg(slot(x) + ROWS * DP + r);
-            factor[x][r] = mx;
-            mm = fmaxf(mm, mx);
-          }
-          for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-          for (int x = lane; x < np; x += 32) {
-            const float f = factor[x][r] == -INFINITY ? 0.f : exp2_fast(factor[x][r] - mm);
-            factor[x][r] = f;
-            sum += f * __ldcg(slot(x) + ROWS * DP + ROWS + r);
-          }
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == 0) {
-            row_inv[r] = sum == 0.f ? 0.f : p.v_scale / sum;
-            store_lse(p, b, hh + r, mm, sum);
-          }
-        }
-        __syncthreads();
-        for (int i = tid; i < nr * DP / 4; i += THREADS) {
-          const int r = i / (DP / 4), d = (i - r * (DP / 4)) * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int x = 0; x < np; ++x) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot(x)) + i);
-            const float f = factor[x][r];
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-          }
-          const float inv = row_inv[r];
-          store_out(p, b, hh + r, d, acc.x * inv);
-          store_out(p, b, hh + r, d + 1, acc.y * inv);
-          store_out(p, b, hh + r, d + 2, acc.z * inv);
-          store_out(p, b, hh + r, d + 3, acc.w * inv);
-        }
-      }
-      __syncthreads();
+  }
+
+  // ---- join the CTAs' parts: of the first chain if it does not begin its unit, of
+  // the last if it does not end it.  Two warps see to the two counters at once.
+  const int first_k = starts ? __ffs(int(starts)) - 1 : 0, last_k = starts ? 31 - __clz(int(starts)) : 0;
+  int unused;
+  const bool open_first = starts && !chain_of(first_k, &unused);
+  const bool open_last = starts && last_k != first_k && !chain_of(last_k, &unused);
+  if (!open_first && !open_last) return;
+  __threadfence();
+  __syncthreads();
+  if (lane == 0 && (warp == 0 ? open_first : warp == 1 && open_last)) {
+    // the unit's first tile, its tiles, and the CTAs they lie in
+    const int k = warp == 0 ? first_k : last_k;
+    const int b = (&piece_b[0][0])[k], u = (&piece_u[0][0])[k];
+    int start, len;
+    seq_range(p, b, &start, &len);
+    const int nt = tiles_of(start, len);
+    long long first = prefix[b / per];
+    for (int x = b / per * per; x < b; ++x) {
+      seq_range(p, x, &start, &len);
+      first += (long long)tiles_of(start, len) * units;
     }
-    k0 = next(k1 + 1);
+    first += (long long)u * nt;
+    const int c0 = int(((first + 1) * n_cta - 1) / total), c1 = int(((first + nt) * n_cta - 1) / total);
+    const unsigned int was = atomicAdd(p.counters + c0, 1u);
+    const bool last = was == unsigned(c1 - c0);
+    if (last) p.counters[c0] = 0u;                // ready for the next call
+    join_cta[warp] = c0;
+    join_n[warp] = last ? c1 - c0 + 1 : 0;
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side) {
+    if (!(side == 0 ? open_first : open_last)) continue;
+    const int np = join_n[side], c0 = join_cta[side];
+    if (np == 0) continue;
+    __threadfence();
+    const int k = side == 0 ? first_k : last_k;
+    const int b = (&piece_b[0][0])[k], u = (&piece_u[0][0])[k];
+    const int kvh = u / p.QB, qb = u - kvh * p.QB;
+    const int hh = kvh * p.G + qb * ROWS, nr = min(ROWS, p.G - qb * ROWS);
+    // piece x of the unit: CTA c0 + x, its second slot where the unit begins.
+    // First the factors of all pieces, a warp for a row; then O, by 4 columns
+    auto slot = [&](int x) { return p.cta_parts + (int64_t(c0 + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
+    for (int r = warp; r < nr; r += C::WARPS) {
+      float mm = -INFINITY, sum = 0.f;
+      for (int x = lane; x < np; x += 32) {
+        const float mx = __ldcg(slot(x) + ROWS * DP + r);
+        weight[x][r] = __ldcg(slot(x) + ROWS * DP + ROWS + r);
+        factor[x][r] = mx;
+        mm = fmaxf(mm, mx);
+      }
+      for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+      for (int x = lane; x < np; x += 32) {
+        const float f = factor[x][r] == -INFINITY ? 0.f : exp2_fast(factor[x][r] - mm);
+        factor[x][r] = f;
+        sum += f * weight[x][r];
+      }
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) {
+        row_inv[r] = sum == 0.f ? 0.f : p.v_scale / sum;
+        store_lse(p, b, hh + r, mm, sum);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < nr * COL4; i += THREADS) {
+      const int r = i / COL4, d = (i - r * COL4) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int x0 = 0; x0 < np; x0 += 8) {        // 8 loads on their way at a time
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x0 + x < np) v[x] = __ldcg(reinterpret_cast<const float4 *>(slot(x0 + x)) + i);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x0 + x < np) {
+            const float f = factor[x0 + x][r];
+            acc.x += f * v[x].x;
+            acc.y += f * v[x].y;
+            acc.z += f * v[x].z;
+            acc.w += f * v[x].w;
+          }
+      }
+      store_out4(p, b, hh + r, d, acc, row_inv[r]);
+    }
+    __syncthreads();
   }
 }
 

@@ -59,6 +59,14 @@ __device__ __forceinline__ void store_out(const DecodeParams &p, int b, int h, i
   else
     static_cast<__half *>(p.out)[at] = __float2half_rn(v);
 }
+// four elements from a multiple of 4 on, times f
+__device__ __forceinline__ void store_out4(const DecodeParams &p, int b, int h, int col, float4 v, float f) {
+  if (col >= p.Dv) return;
+  char *at = static_cast<char *>(p.out) + 2 * (int64_t(b) * p.o_sb + int64_t(h) * p.o_sh + col);
+  *reinterpret_cast<uint2 *>(at) = p.bf16
+                                       ? make_uint2(pack2<true>(v.x * f, v.y * f), pack2<true>(v.z * f, v.w * f))
+                                       : make_uint2(pack2<false>(v.x * f, v.y * f), pack2<false>(v.z * f, v.w * f));
+}
 // l == 0: nothing attended to
 __device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int h, float m, float l) {
   const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);

@@ -691,26 +691,33 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
   if (at.y < 2) return;
   const int qb = h / NH, r = h - qb * NH, tid = int(threadIdx.x);
   auto slot = [&](int x) { return p.cta_parts + (int64_t((at.x + x) * p.QB + qb) * 2 + (x == 0 ? 1 : 0)) * PIECE; };
-  float m = -INFINITY;
-  for (int x = 0; x < at.y; ++x) m = fmaxf(m, __ldcg(slot(x) + NH * kLatDv + r));
+  float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int x = 0; x < at.y; ++x) {
-    const float *s = slot(x);
-    const float mx = __ldcg(s + NH * kLatDv + r);
-    const float f = mx == -INFINITY ? 0.f : exp2_fast(mx - m);
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + r * kLatDv) + tid);
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
-    sum += f * __ldcg(s + NH * kLatDv + NH + r);
+  for (int x0 = 0; x0 < at.y; x0 += 4) {          // 4 pieces on their way at a time
+    float4 v[4];
+    float mx[4], lx[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float *s = slot(min(x0 + x, at.y - 1));
+      v[x] = __ldcg(reinterpret_cast<const float4 *>(s + r * kLatDv) + tid);
+      mx[x] = __ldcg(s + NH * kLatDv + r);
+      lx[x] = __ldcg(s + NH * kLatDv + NH + r);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x0 + x >= at.y) break;
+      const float now = fmaxf(m, mx[x]);
+      const float was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = mx[x] == -INFINITY ? 0.f : exp2_fast(mx[x] - now);
+      acc.x = acc.x * was + f * v[x].x;
+      acc.y = acc.y * was + f * v[x].y;
+      acc.z = acc.z * was + f * v[x].z;
+      acc.w = acc.w * was + f * v[x].w;
+      sum = sum * was + f * lx[x];
+      m = now;
+    }
   }
   const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-  store_out(p, b, h, tid * 4, acc.x * inv);
-  store_out(p, b, h, tid * 4 + 1, acc.y * inv);
-  store_out(p, b, h, tid * 4 + 2, acc.z * inv);
-  store_out(p, b, h, tid * 4 + 3, acc.w * inv);
+  store_out4(p, b, h, tid * 4, acc, inv);
   if (tid == 0) store_lse(p, b, h, m, sum);
 }
 
