@@ -1,12 +1,15 @@
 // hicache_append.cu -- norms of the query and key heads, the position rotation
 // and the store of K and V into the paged cache, in one pass.
 //
-// Nothing is used twice, so memory binds: a head is read, normed, rotated and
-// written once.  A unit of work is one head of one token (of q, k or v), taken
-// by a group of lanes that each hold 16-byte vectors of it; the sum of squares
-// is reduced by shuffles, and the rotation's partner elements are exchanged
-// through shared memory, so that any rotation span and either pairing works on
-// whole vectors.
+// Nothing is used twice, so memory binds, once the arithmetic on the way (norm,
+// rotation, conversions) is short enough: 25 instructions a 16-byte vector.  A warp
+// takes a token, or a part of its heads.  8 lanes hold a head, 4 heads at a time: a
+// vector of each 128 bytes of it per lane, so that the sum of squares takes three
+// shuffles however long the head, and every access is whole 128-byte lines.  A
+// lane's cosines, sines and norm weights are read once for all heads of the token,
+// and the vectors of AHEAD heads are on their way before the first is used.
+// Partner elements half a rotation away come through shared memory, interleaved
+// ones are in the lane's own vector.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -18,7 +21,7 @@
 namespace hicache {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 &u, float *x) {
@@ -65,126 +68,252 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float *x, float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-// ITERS: 16-byte vectors of a head per lane of its group (lanes = 1 << lg).
-template <int ITERS, bool BF16>
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kLanes = 8, kGroups = 32 / kLanes;  // lanes of a head, heads of a warp
+
+__device__ __forceinline__ void load8(const float *p, float *x) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// The cosines and (signed) sines of the eight elements e0.. of a rotation, and which
+// of them belong to it.  WHOLE: all of them do, and they lie in one half.
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t rotation8(const AppendParams &p, const float *row, int e0, float *cs, float *sn) {
+  const int half = p.rot >> 1;
+  if constexpr (WHOLE) {
+    if (p.interleaved) {
+      const float4 c = __ldg(reinterpret_cast<const float4 *>(row + (e0 >> 1)));
+      const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half + (e0 >> 1)));
+      cs[0] = cs[1] = c.x, cs[2] = cs[3] = c.y, cs[4] = cs[5] = c.z, cs[6] = cs[7] = c.w;
+      sn[0] = -s.x, sn[1] = s.x, sn[2] = -s.y, sn[3] = s.y, sn[4] = -s.z, sn[5] = s.z, sn[6] = -s.w, sn[7] = s.w;
+    } else {
+      const bool second = e0 >= half;
+      load8(row + (second ? e0 - half : e0), cs);
+      load8(row + (second ? e0 : e0 + half), sn);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sn[i] = second ? sn[i] : -sn[i];
+    }
+    return 255u;
+  } else {
+    uint32_t in = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = e0 + i;
+      if (e < 0 || e >= p.rot) continue;
+      const bool second = p.interleaved ? (e & 1) : e >= half;
+      const int j = p.interleaved ? e >> 1 : second ? e - half : e;
+      in |= 1u << i;
+      cs[i] = __ldg(row + j);
+      sn[i] = second ? __ldg(row + half + j) : -__ldg(row + half + j);
+    }
+    return in;
+  }
+}
+
+// ITERS: 16-byte vectors of a head per lane; `segments` tasks per token, `reps`
+// times AHEAD heads of each group per task.  WHOLE: the rotation begins and ends at
+// whole vectors in either half, and the table's rows at 16 bytes.
+template <int ITERS, bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kAppendThreads)
-    append_kernel(const __grid_constant__ AppendParams p, int lg, FastDiv fd_units) {
-  __shared__ float stage[kAppendThreads * 8 * ITERS];
-  const int lanes = 1 << lg, group = int(threadIdx.x) >> lg, lane = int(threadIdx.x) & (lanes - 1);
-  const uint32_t unit = blockIdx.x * uint32_t(kAppendThreads >> lg) + uint32_t(group);
-  const uint32_t n = fast_div(unit, fd_units);
-  const int u = int(unit - n * fd_units.d);
-  const int kind = u < p.q_heads ? 0 : u < p.q_heads + p.kv_heads ? 1 : 2;   // q, k, v
-  const int head = kind == 0 ? u : kind == 1 ? u - p.q_heads : u - p.q_heads - p.kv_heads;
-  bool live = int64_t(n) < p.num_tokens;
-  int64_t pos = 0, slot = 0;
-  if (live && p.rot > 0) {
-    pos = p.positions[n];
-    live = pos >= 0 && pos < p.cos_sin_rows;
-  }
-  if (live && kind != 0) {
-    slot = p.slots[n];
-    live = slot >= 0 && slot < p.num_slots;
-  }
+    append_kernel(const __grid_constant__ AppendParams p, int reps, FastDiv fd_segments) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
+  constexpr int AHEAD = ITERS == 1 ? 4 : ITERS == 2 ? 2 : 1;
+  constexpr bool HOLD = ITERS <= 2;               // cosines, sines and weights in registers
+  constexpr int UPPER = 32 * ITERS;
+  __shared__ float4 stage_all[kAppendWarps][2 * 32 * ITERS];
+  const int warp = int(threadIdx.x) >> 5;
+  const uint32_t task = blockIdx.x * uint32_t(kAppendWarps) + uint32_t(warp);
+  const uint32_t n = fast_div(task, fd_segments);
+  if (int64_t(n) >= p.num_tokens) return;         // the whole warp
+  const int sub = (int(threadIdx.x) & 31) / kLanes, lane = int(threadIdx.x) & (kLanes - 1);
+  const int units = p.q_heads + p.kv_heads * (p.has_v ? 2 : 1);
+  const int u_first = int(task - n * fd_segments.d) * kGroups * AHEAD * reps;
+  const int u_end = min(units, u_first + kGroups * AHEAD * reps);
   const int chunks = p.D >> 3;
-  float x[ITERS][8];
-  const char *src = static_cast<const char *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v);
-  const int64_t off = kind == 0   ? int64_t(n) * p.q_st + int64_t(head) * p.q_sh
-                      : kind == 1 ? int64_t(n) * p.k_st + int64_t(head) * p.k_sh
-                                  : int64_t(n) * p.v_st + int64_t(head) * p.v_sh;
+  int64_t pos = 0, slot = -1;
+  if (p.kv_heads > 0) slot = p.slots[n];
+  if (p.rot > 0) {
+    pos = p.positions[n];
+    if (pos < 0 || pos >= p.cos_sin_rows) return; // the whole warp
+  }
+  const bool store_kv = slot >= 0 && slot < p.num_slots;
+  const float *row = p.cos_sin + pos * p.rot;
+  const int half = p.rot >> 1;
+  const bool exchange = half > 0 && !p.interleaved;
+
+  float cs[HOLD ? ITERS : 1][8], sn[HOLD ? ITERS : 1][8], qw[HOLD ? ITERS : 1][8], kw[HOLD ? ITERS : 1][8];
+  uint32_t turned[ITERS];                         // a bit per element
 #pragma unroll
   for (int it = 0; it < ITERS; ++it) {
-    const int c = lane + it * lanes;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live && c < chunks) w = __ldcs(reinterpret_cast<const uint4 *>(src + 2 * off) + c);
-    unpack8<BF16>(w, x[it]);
-  }
-  const int m = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : 0;
-  float sum = 0.f;
-#pragma unroll
-  for (int it = 0; it < ITERS; ++it)
-    if ((lane + it * lanes) * 8 < m) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(x[it][i], x[it][i], sum);
-    }
-  for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (m > 0) {
-    const float r = rsqrtf(sum / float(m) + p.eps);
-    const uint4 *wt = static_cast<const uint4 *>(kind == 0 ? p.q_weight : p.k_weight);
-#pragma unroll
-    for (int it = 0; it < ITERS; ++it) {
-      const int c = lane + it * lanes;
-      if (c * 8 < m) {
-        float w[8];
-        unpack8<BF16>(__ldg(wt + c), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[it][i] = x[it][i] * r * w[i];
-      }
+    const int c = lane + it * kLanes, e0 = c * 8 - p.rot_off;
+    turned[it] = c < chunks && e0 > -8 && e0 < p.rot ? 255u : 0u;
+    if constexpr (HOLD) {
+      if (turned[it]) turned[it] = rotation8<WHOLE>(p, row, e0, cs[it], sn[it]);
+      if (c * 8 < p.q_norm) unpack8<BF16>(__ldg(static_cast<const uint4 *>(p.q_weight) + c), qw[it]);
+      if (c * 8 < p.k_norm) unpack8<BF16>(__ldg(static_cast<const uint4 *>(p.k_weight) + c), kw[it]);
     }
   }
-  if (p.rot > 0) {
-    float *mine = stage + group * lanes * 8 * ITERS;
+  // the group's head in shared memory: the lower and the upper four of each vector
+  float4 *const stage = stage_all[warp] + sub * kLanes * ITERS;
+  const char *const q_n = static_cast<const char *>(p.q) + 2 * int64_t(n) * p.q_st;
+  const char *const k_n = static_cast<const char *>(p.k) + 2 * int64_t(n) * p.k_st;
+  const char *const v_n = static_cast<const char *>(p.v) + 2 * int64_t(n) * p.v_st;
+
+  for (int u0 = u_first; u0 < u_end; u0 += kGroups * AHEAD) {
+    uint4 raw[AHEAD][ITERS];
 #pragma unroll
-    for (int it = 0; it < ITERS; ++it) {
-      float4 *d = reinterpret_cast<float4 *>(mine + (lane + it * lanes) * 8);
-      d[0] = make_float4(x[it][0], x[it][1], x[it][2], x[it][3]);
-      d[1] = make_float4(x[it][4], x[it][5], x[it][6], x[it][7]);
-    }
-    __syncwarp();
-    if (live && kind != 2) {
-      const int half = p.rot >> 1;
-      const float *cs = p.cos_sin + pos * p.rot;
+    for (int x = 0; x < AHEAD; ++x) {
+      const int u = u0 + x * kGroups + sub;
+      const bool is_q = u < p.q_heads, is_k = !is_q && u < p.q_heads + p.kv_heads;
+      const bool live = u < u_end && (is_q || store_kv);
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          is_q ? q_n + 2 * u * p.q_sh
+               : is_k ? k_n + 2 * (u - p.q_heads) * p.k_sh : v_n + 2 * (u - p.q_heads - p.kv_heads) * p.v_sh);
 #pragma unroll
       for (int it = 0; it < ITERS; ++it) {
-        const int c = lane + it * lanes;
+        const int c = lane + it * kLanes;
+        raw[x][it] = live && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+      }
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = c * 8 + i - p.rot_off;
-          if (c < chunks && e >= 0 && e < p.rot) {
-            const bool second = p.interleaved ? (e & 1) : e >= half;
-            const int j = p.interleaved ? e >> 1 : second ? e - half : e;
-            const int mate = p.interleaved ? e ^ 1 : second ? e - half : e + half;
-            const float y = mine[mate + p.rot_off], co = __ldg(cs + j), si = __ldg(cs + half + j);
-            x[it][i] = second ? fmaf(x[it][i], co, y * si) : fmaf(x[it][i], co, -y * si);
+    for (int x = 0; x < AHEAD; ++x) {
+      if (u0 + x * kGroups >= u_end) break;       // the whole warp
+      const int u = u0 + x * kGroups + sub;
+      const bool is_q = u < p.q_heads, is_k = !is_q && u < p.q_heads + p.kv_heads;
+      const bool live = u < u_end && (is_q || store_kv);
+      const int m = is_q ? p.q_norm : is_k ? p.k_norm : 0;
+      float v[ITERS][8];
+      float sum = 0.f;
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        unpack8<BF16>(raw[x][it], v[it]);
+        if ((lane + it * kLanes) * 8 < m) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = fmaf(v[it][i], v[it][i], sum);
+        }
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (m > 0) {
+        const float r = rsqrtf(__fdividef(sum, float(m)) + p.eps);
+#pragma unroll
+        for (int it = 0; it < ITERS; ++it) {
+          const int c = lane + it * kLanes;
+          if (c * 8 >= m) continue;
+          if constexpr (HOLD) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[it][i] *= r * (is_q ? qw[it][i] : kw[it][i]);
+          } else {
+            float w[8];
+            unpack8<BF16>(__ldg(static_cast<const uint4 *>(is_q ? p.q_weight : p.k_weight) + c), w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[it][i] *= r * w[i];
           }
         }
       }
-    }
-  }
-  if (!live) return;
+      const bool turn = is_q || is_k;
+      if (exchange) {
+        __syncwarp();                             // the head before has been read
 #pragma unroll
-  for (int it = 0; it < ITERS; ++it) {
-    const int c = lane + it * lanes;
-    if (c >= chunks) continue;
-    if (kind == 0) {
-      char *dst = static_cast<char *>(p.q_out) + 2 * (int64_t(n) * p.o_st + int64_t(head) * p.o_sh);
-      reinterpret_cast<uint4 *>(dst)[c] = pack8<BF16>(x[it]);
-    } else {
-      const int64_t at = slot * p.row + int64_t(head) * p.D;
-      char *buf = static_cast<char *>(kind == 1 ? p.k_cache : p.v_cache);
-      if (p.e4m3)
-        reinterpret_cast<uint2 *>(buf + at)[c] = pack8_e4m3(x[it], kind == 1 ? p.k_scale : p.v_scale);
-      else
-        reinterpret_cast<uint4 *>(buf + 2 * at)[c] = pack8<BF16>(x[it]);
+        for (int it = 0; it < ITERS; ++it)
+          if (turned[it]) {
+            stage[lane + it * kLanes] = make_float4(v[it][0], v[it][1], v[it][2], v[it][3]);
+            stage[UPPER + lane + it * kLanes] = make_float4(v[it][4], v[it][5], v[it][6], v[it][7]);
+          }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        if (!turn || !turned[it]) continue;
+        const int e0 = (lane + it * kLanes) * 8 - p.rot_off;
+        float cl[8], sl[8];
+        uint32_t in = turned[it];
+        const float *cp = cl, *sp = sl;
+        if constexpr (HOLD)
+          cp = cs[it], sp = sn[it];
+        else
+          in = rotation8<WHOLE>(p, row, e0, cl, sl);
+        float y[8];
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = v[it][i ^ 1];
+        } else if constexpr (WHOLE) {
+          const int at = ((e0 < half ? e0 + half : e0 - half) + p.rot_off) >> 3;
+          const float4 a = stage[at], b = stage[UPPER + at];
+          y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i, at = ((in >> i) & 1u) ? (e < half ? e + half : e - half) + p.rot_off : 0;
+            y[i] = ((in >> i) & 1u) ? reinterpret_cast<const float *>(stage + ((at & 4) ? UPPER : 0) + (at >> 3))[at & 3]
+                                    : 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (WHOLE || ((in >> i) & 1u)) v[it][i] = fmaf(v[it][i], cp[i], y[i] * sp[i]);
+      }
+      if (!live) continue;
+      char *const dst = static_cast<char *>(p.q_out) + 2 * (int64_t(n) * p.o_st + int64_t(u) * p.o_sh);
+      const int64_t at = slot * p.row + (is_k ? u - p.q_heads : u - p.q_heads - p.kv_heads) * int64_t(p.D);
+      char *const buf = static_cast<char *>(is_k ? p.k_cache : p.v_cache);
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        const int c = lane + it * kLanes;
+        if (c >= chunks) continue;
+        if (is_q)
+          reinterpret_cast<uint4 *>(dst)[c] = pack8<BF16>(v[it]);
+        else if (p.e4m3)
+          reinterpret_cast<uint2 *>(buf + at)[c] = pack8_e4m3(v[it], is_k ? p.k_scale : p.v_scale);
+        else
+          reinterpret_cast<uint4 *>(buf + 2 * at)[c] = pack8<BF16>(v[it]);
+      }
     }
   }
+}
+
+template <int ITERS>
+auto append_kernel_of(const AppendParams &p) {
+  const int half = p.rot / 2;
+  const bool whole = p.rot_off % 8 == 0 && (p.interleaved ? p.rot : half) % 8 == 0 &&
+                     reinterpret_cast<uintptr_t>(p.cos_sin) % 16 == 0;
+  return p.bf16 ? (whole ? append_kernel<ITERS, true, true> : append_kernel<ITERS, true, false>)
+                : (whole ? append_kernel<ITERS, false, true> : append_kernel<ITERS, false, false>);
 }
 
 }  // namespace
 
 int launch_append(const AppendParams &p, void *stream) {
   const int units = p.q_heads + p.kv_heads * (p.has_v ? 2 : 1);
-  const int chunks = p.D / 8;
-  int lg = 0;
-  while (lg < 5 && (1 << lg) < chunks) ++lg;
-  const int per_block = kAppendThreads >> lg;
-  const int64_t total = p.num_tokens * units;
-  const unsigned grid = unsigned((total + per_block - 1) / per_block);
-  const FastDiv fd = make_fastdiv(uint32_t(units));
-  auto *k = chunks <= 32 ? (p.bf16 ? append_kernel<1, true> : append_kernel<1, false>)
-                         : (p.bf16 ? append_kernel<3, true> : append_kernel<3, false>);
-  k<<<grid, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, lg, fd);
-  return int(cudaGetLastError());
+  const int iters = (p.D / 8 + kLanes - 1) / kLanes;
+  auto *k = iters == 1   ? append_kernel_of<1>(p)
+            : iters == 2 ? append_kernel_of<2>(p)
+            : iters == 3 ? append_kernel_of<3>(p)
+            : iters == 4 ? append_kernel_of<4>(p)
+            : iters <= 9 ? append_kernel_of<9>(p)
+                         : append_kernel_of<12>(p);
+  // a warp per token, unless that leaves SMs with fewer than 16 warps: then its
+  // heads are dealt to as many warps as it takes (or as there are)
+  const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
+  const int most = (units + step - 1) / step;
+  int64_t segments = (int64_t(152) * 16 + p.num_tokens - 1) / p.num_tokens;
+  if (segments > most) segments = most;
+  const int reps = int((most + segments - 1) / segments);
+  segments = (most + reps - 1) / reps;
+  const int64_t tasks = p.num_tokens * segments;
+  const FastDiv fd = make_fastdiv(uint32_t(segments));
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(unsigned((tasks + kAppendWarps - 1) / kAppendWarps));
+  c.blockDim = dim3(kAppendThreads);
+  c.stream = static_cast<cudaStream_t>(stream);
+  c.attrs = &at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, k, p, reps, fd);
+  return int(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 }  // namespace hicache
