@@ -111,11 +111,295 @@ __device__ __forceinline__ uint32_t rotation8(const AppendParams &p, const float
   }
 }
 
+// ---- the usual shapes ------------------------------------------------------------
+// Where the head is whole 64 elements (ITERS vectors a lane), the norm covers whole
+// 64s and a vector's partners are one vector that the warp can reach without shared
+// memory, the sum is regrouped: with a partner z of element y
+//   out_y = r * (y * (w_y cos) + z * (w_z sin)),
+// the two coefficients are worked out once per token and kind, and an element costs
+// a multiply, a multiply-add, a multiply and its share of the sum of squares, all of
+// them on pairs (fma.rn.f32x2).  Against the general kernel below: a prefill chunk of
+// 8,191 tokens of 48 heads of 128 takes 47 us instead of 61.
+enum : int { kSelf = 0, kAcross = 1, kInside = 2 };   // where partners are: ITERS / 2 vectors
+                                                      // on, 4 lanes on, in the vector itself
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  if constexpr (BF16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return pair(f.x, f.y);
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t x) {
+  const float2 f = unpair(x);
+  return pair(f.y, f.x);
+}
+
+template <int ITERS, bool BF16, int MODE>
+__global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 3 : 2)
+    append_fast_kernel(const __grid_constant__ AppendParams p, int steps_per_task, FastDiv fd_segments) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
+  constexpr bool HOLD = ITERS <= 4;               // coefficients of every vector in registers
+  constexpr int AHEAD = ITERS <= 2 ? 2 : 1;       // steps on their way
+  const int warp = int(threadIdx.x) >> 5;
+  const uint32_t task = blockIdx.x * uint32_t(kAppendWarps) + uint32_t(warp);
+  const uint32_t n = fast_div(task, fd_segments);
+  if (int64_t(n) >= p.num_tokens) return;         // the whole warp
+  const int sub = (int(threadIdx.x) & 31) / kLanes, lane = int(threadIdx.x) & (kLanes - 1);
+  // a step: 4 heads of one kind
+  const int q_steps = (p.q_heads + kGroups - 1) / kGroups, kv_steps = (p.kv_heads + kGroups - 1) / kGroups;
+  const int first = int(task - n * fd_segments.d) * steps_per_task;
+  const int end = min(q_steps + kv_steps * (p.has_v ? 2 : 1), first + steps_per_task);
+  // the step to fetch next: its source, the step its kind ends at, heads of the kind
+  // from this one on
+  const char *f_src = nullptr;
+  int64_t f_step = 0;
+  int f_s = first, f_end = 0, f_left = 0;
+  auto seek = [&]() {
+    const int kind = f_s < q_steps ? 0 : f_s < q_steps + kv_steps ? 1 : 2;
+    const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
+    const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
+    const int h = (f_s - begin) * kGroups + sub;
+    f_src = static_cast<const char *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+            2 * (int64_t(n) * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) + h * sh) + lane * 16;
+    f_step = 2 * kGroups * sh;
+    f_end = min(end, begin + (kind == 0 ? q_steps : kv_steps));
+    f_left = (kind == 0 ? p.q_heads : p.kv_heads) - h;
+  };
+  uint4 ahead[AHEAD][ITERS];
+  auto fetch = [&](uint4 *to) {
+    if (f_s >= f_end && f_s < end) seek();
+    const bool have = f_s < f_end && f_left > 0;
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it)
+      to[it] = have ? __ldcs(reinterpret_cast<const uint4 *>(f_src) + it * kLanes) : make_uint4(0, 0, 0, 0);
+    ++f_s;
+    f_left -= kGroups;
+    f_src += f_step;
+  };
+  int64_t pos = 0, slot = -1;
+  if (p.kv_heads > 0) slot = p.slots[n];
+  if (p.rot > 0) pos = p.positions[n];
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) fetch(ahead[a]);
+  if (p.rot > 0 && (pos < 0 || pos >= p.cos_sin_rows)) return;   // the whole warp
+  const bool store_kv = slot >= 0 && slot < p.num_slots;
+  const float *row = p.cos_sin + pos * p.rot;
+  const int half = p.rot >> 1;
+
+  // coefficients of the current kind: of the element and of its partner
+  uint64_t own[HOLD ? ITERS : 1][4], mate[HOLD ? ITERS : 1][4];
+  uint4 wp[HOLD ? 1 : ITERS];                     // not held: the weights as they come
+  float cs1[HOLD ? 1 : 8], sn1[HOLD ? 1 : 8];     // and the rotation of the one vector it turns
+  int kind = 0, m = 0, s_end = 0, left = 0;       // the current kind, where it ends, heads from this one on
+  char *dst = nullptr;
+  int64_t dst_step = 0;
+  auto turned = [&](int it) {                     // whether vector `it` is rotated (the same in all lanes)
+    return p.rot > 0 && it * 64 >= p.rot_off && it * 64 < p.rot_off + p.rot;
+  };
+  auto prepare = [&](int kind) {
+    m = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : 0;
+    const uint4 *w = static_cast<const uint4 *>(kind == 0 ? p.q_weight : p.k_weight);
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        const int c = lane + it * kLanes;
+        const bool turn = kind != 2 && turned(it);
+        float a[8], z[8], cs[8], sn[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = z[i] = cs[i] = 1.f, sn[i] = 0.f;
+        if (it * 64 < m) {
+          unpack8<BF16>(__ldg(w + c), a);
+          if (MODE == kInside) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = a[i ^ 1];
+          } else {
+            unpack8<BF16>(__ldg(w + (MODE == kSelf ? c ^ (ITERS / 2 * kLanes) : c ^ 4)), z);
+          }
+        }
+        if (turn) rotation8<true>(p, row, c * 8 - p.rot_off, cs, sn);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          own[it][i] = pair(a[2 * i] * cs[2 * i], a[2 * i + 1] * cs[2 * i + 1]);
+          mate[it][i] = pair(z[2 * i] * sn[2 * i], z[2 * i + 1] * sn[2 * i + 1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        if (it * 64 < m) wp[it] = __ldg(w + lane + it * kLanes);
+        if (turned(it)) rotation8<true>(p, row, (lane + it * kLanes) * 8 - p.rot_off, cs1, sn1);
+      }
+    }
+  };
+
+#pragma unroll 1
+  for (int s = first; s < end; ++s) {
+    uint4 raw[ITERS];
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) raw[it] = ahead[0][it];
+#pragma unroll
+    for (int a = 0; a + 1 < AHEAD; ++a)
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) ahead[a][it] = ahead[a + 1][it];
+    fetch(ahead[AHEAD - 1]);
+    if (s >= s_end) {                             // on to the next kind: its coefficients and places
+      kind = s < q_steps ? 0 : s < q_steps + kv_steps ? 1 : 2;
+      const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
+      s_end = min(end, begin + (kind == 0 ? q_steps : kv_steps));
+      const int h = (s - begin) * kGroups + sub;
+      left = kind == 0 ? p.q_heads - h : store_kv ? p.kv_heads - h : 0;
+      const int vec = kind != 0 && p.e4m3 ? 8 : 16;              // bytes that 8 elements take
+      const int64_t sh = kind == 0 ? p.o_sh : p.D;
+      const int64_t at = kind == 0 ? int64_t(n) * p.o_st + h * sh : slot * p.row + h * sh;
+      dst = static_cast<char *>(kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + at * (vec / 8) + lane * vec;
+      dst_step = kGroups * sh * (vec / 8);
+      prepare(kind);
+    }
+    const bool live = left > 0;
+    char *const to = dst;
+    left -= kGroups;
+    dst += dst_step;
+    if (kind == 2 && !p.e4m3) {                   // as it came
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it)
+        if (live) reinterpret_cast<uint4 *>(to)[it * kLanes] = raw[it];
+      continue;
+    }
+    uint64_t v[ITERS][4];
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) {
+      const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[it][i] = widen<BF16>(w[i]);
+    }
+    float r = 1.f;
+    if (m > 0) {
+      uint64_t sq = 0;
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it)
+        if (it * 64 < m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sq = fma2(v[it][i], v[it][i], sq);
+        }
+      const float2 f = unpair(sq);
+      float sum = f.x + f.y;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      r = rsqrtf(__fdividef(sum, float(m)) + p.eps);
+    }
+    float out[ITERS][8];
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) {
+      const float rr = it * 64 < m ? r : 1.f;
+      const uint64_t r2 = pair(rr, rr);
+      const bool turn = kind != 2 && turned(it);
+      uint64_t x[4];
+      if constexpr (HOLD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = mul2(v[it][i], own[it][i]);
+      } else {
+        const uint32_t w[4] = {wp[it].x, wp[it].y, wp[it].z, wp[it].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = it * 64 < m ? mul2(v[it][i], widen<BF16>(w[i])) : v[it][i];
+      }
+      if (turn) {
+        uint64_t z[4];
+        if constexpr (MODE == kSelf) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = v[it ^ (ITERS / 2)][i];
+        } else if constexpr (MODE == kInside) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = swapped(HOLD ? v[it][i] : x[i]);
+        } else {
+          const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if constexpr (HOLD) {
+              z[i] = widen<BF16>(__shfl_xor_sync(0xffffffffu, w[i], 4));
+            } else {
+              const float2 f = unpair(x[i]);
+              z[i] = pair(__shfl_xor_sync(0xffffffffu, f.x, 4), __shfl_xor_sync(0xffffffffu, f.y, 4));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if constexpr (HOLD)
+            x[i] = fma2(z[i], mate[it][i], x[i]);
+          else
+            x[i] = fma2(z[i], pair(sn1[2 * i], sn1[2 * i + 1]), mul2(x[i], pair(cs1[2 * i], cs1[2 * i + 1])));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpair(mul2(x[i], r2));
+        out[it][2 * i] = f.x;
+        out[it][2 * i + 1] = f.y;
+      }
+    }
+    if (!live) continue;
+    if (kind != 0 && p.e4m3) {
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it)
+        reinterpret_cast<uint2 *>(to)[it * kLanes] = pack8_e4m3(out[it], kind == 1 ? p.k_scale : p.v_scale);
+    } else {
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) reinterpret_cast<uint4 *>(to)[it * kLanes] = pack8<BF16>(out[it]);
+    }
+  }
+}
+
+// The kernel for p's shape, or null where only the general one will do.
+using AppendKernel = void (*)(const AppendParams, int, FastDiv);
+template <int ITERS, int MODE>
+AppendKernel fast_of(const AppendParams &p) {
+  return p.bf16 ? append_fast_kernel<ITERS, true, MODE> : append_fast_kernel<ITERS, false, MODE>;
+}
+AppendKernel append_fast(const AppendParams &p) {
+  if (p.D % 64 || reinterpret_cast<uintptr_t>(p.cos_sin) % 16) return nullptr;
+  if (p.q_norm % 64 || p.k_norm % 64 || p.rot_off % 64) return nullptr;
+  const bool every = (p.q_norm == 0 || p.q_norm == p.D) && (p.k_norm == 0 || p.k_norm == p.D);
+  if (p.rot == 0 || (p.interleaved && p.rot % 64 == 0)) {
+    if (p.D == 64) return fast_of<1, kInside>(p);
+    if (p.D == 128) return fast_of<2, kInside>(p);
+    if (p.D == 256) return fast_of<4, kInside>(p);
+    if (p.D == 576 && p.rot <= 64) return fast_of<9, kInside>(p);
+  } else if (!p.interleaved && p.rot == 64) {
+    if (p.D == 64) return fast_of<1, kAcross>(p);
+    if (p.D == 128) return fast_of<2, kAcross>(p);
+    if (p.D == 256) return fast_of<4, kAcross>(p);
+    if (p.D == 576) return fast_of<9, kAcross>(p);
+  } else if (!p.interleaved && p.rot == p.D && every) {
+    if (p.D == 128) return fast_of<2, kSelf>(p);
+    if (p.D == 256) return fast_of<4, kSelf>(p);
+  }
+  return nullptr;
+}
+
+// ---- any shape -------------------------------------------------------------------
 // ITERS: 16-byte vectors of a head per lane; `segments` tasks per token, `reps`
 // times AHEAD heads of each group per task.  WHOLE: the rotation begins and ends at
 // whole vectors in either half, and the table's rows at 16 bytes.
 template <int ITERS, bool BF16, bool WHOLE>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, ITERS <= 4 ? 4 : 3)
     append_kernel(const __grid_constant__ AppendParams p, int reps, FastDiv fd_segments) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   constexpr int AHEAD = ITERS == 1 ? 4 : ITERS == 2 ? 2 : 1;
@@ -131,12 +415,32 @@ __global__ void __launch_bounds__(kAppendThreads)
   const int u_first = int(task - n * fd_segments.d) * kGroups * AHEAD * reps;
   const int u_end = min(units, u_first + kGroups * AHEAD * reps);
   const int chunks = p.D >> 3;
+  const char *const q_n = static_cast<const char *>(p.q) + 2 * int64_t(n) * p.q_st;
+  const char *const k_n = static_cast<const char *>(p.k) + 2 * int64_t(n) * p.k_st;
+  const char *const v_n = static_cast<const char *>(p.v) + 2 * int64_t(n) * p.v_st;
+  // the vectors of AHEAD heads; the next ones are fetched before these are used, the
+  // first ones before anything that depends on the token's position or slot
+  uint4 ahead[AHEAD][ITERS];
+  auto fetch = [&](int u0) {
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int u = u0 + x * kGroups + sub;
+      const bool is_q = u < p.q_heads, is_k = !is_q && u < p.q_heads + p.kv_heads;
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          is_q ? q_n + 2 * u * p.q_sh
+               : is_k ? k_n + 2 * (u - p.q_heads) * p.k_sh : v_n + 2 * (u - p.q_heads - p.kv_heads) * p.v_sh);
+#pragma unroll
+      for (int it = 0; it < ITERS; ++it) {
+        const int c = lane + it * kLanes;
+        ahead[x][it] = u < u_end && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
   int64_t pos = 0, slot = -1;
   if (p.kv_heads > 0) slot = p.slots[n];
-  if (p.rot > 0) {
-    pos = p.positions[n];
-    if (pos < 0 || pos >= p.cos_sin_rows) return; // the whole warp
-  }
+  if (p.rot > 0) pos = p.positions[n];
+  fetch(u_first);
+  if (p.rot > 0 && (pos < 0 || pos >= p.cos_sin_rows)) return;   // the whole warp
   const bool store_kv = slot >= 0 && slot < p.num_slots;
   const float *row = p.cos_sin + pos * p.rot;
   const int half = p.rot >> 1;
@@ -156,26 +460,13 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
   // the group's head in shared memory: the lower and the upper four of each vector
   float4 *const stage = stage_all[warp] + sub * kLanes * ITERS;
-  const char *const q_n = static_cast<const char *>(p.q) + 2 * int64_t(n) * p.q_st;
-  const char *const k_n = static_cast<const char *>(p.k) + 2 * int64_t(n) * p.k_st;
-  const char *const v_n = static_cast<const char *>(p.v) + 2 * int64_t(n) * p.v_st;
-
   for (int u0 = u_first; u0 < u_end; u0 += kGroups * AHEAD) {
     uint4 raw[AHEAD][ITERS];
 #pragma unroll
-    for (int x = 0; x < AHEAD; ++x) {
-      const int u = u0 + x * kGroups + sub;
-      const bool is_q = u < p.q_heads, is_k = !is_q && u < p.q_heads + p.kv_heads;
-      const bool live = u < u_end && (is_q || store_kv);
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          is_q ? q_n + 2 * u * p.q_sh
-               : is_k ? k_n + 2 * (u - p.q_heads) * p.k_sh : v_n + 2 * (u - p.q_heads - p.kv_heads) * p.v_sh);
+    for (int x = 0; x < AHEAD; ++x)
 #pragma unroll
-      for (int it = 0; it < ITERS; ++it) {
-        const int c = lane + it * kLanes;
-        raw[x][it] = live && c < chunks ? __ldcs(src + c) : make_uint4(0, 0, 0, 0);
-      }
-    }
+      for (int it = 0; it < ITERS; ++it) raw[x][it] = ahead[x][it];
+    if (u0 + kGroups * AHEAD < u_end) fetch(u0 + kGroups * AHEAD);
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) {
       if (u0 + x * kGroups >= u_end) break;       // the whole warp
@@ -274,7 +565,7 @@ __global__ void __launch_bounds__(kAppendThreads)
 }
 
 template <int ITERS>
-auto append_kernel_of(const AppendParams &p) {
+AppendKernel append_kernel_of(const AppendParams &p) {
   const int half = p.rot / 2;
   const bool whole = p.rot_off % 8 == 0 && (p.interleaved ? p.rot : half) % 8 == 0 &&
                      reinterpret_cast<uintptr_t>(p.cos_sin) % 16 == 0;
@@ -285,24 +576,34 @@ auto append_kernel_of(const AppendParams &p) {
 }  // namespace
 
 int launch_append(const AppendParams &p, void *stream) {
-  const int units = p.q_heads + p.kv_heads * (p.has_v ? 2 : 1);
-  const int iters = (p.D / 8 + kLanes - 1) / kLanes;
-  auto *k = iters == 1   ? append_kernel_of<1>(p)
-            : iters == 2 ? append_kernel_of<2>(p)
-            : iters == 3 ? append_kernel_of<3>(p)
-            : iters == 4 ? append_kernel_of<4>(p)
-            : iters <= 9 ? append_kernel_of<9>(p)
-                         : append_kernel_of<12>(p);
   // a warp per token, unless that leaves SMs with fewer than 16 warps: then its
   // heads are dealt to as many warps as it takes (or as there are)
-  const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
-  const int most = (units + step - 1) / step;
-  int64_t segments = (int64_t(152) * 16 + p.num_tokens - 1) / p.num_tokens;
-  if (segments > most) segments = most;
-  const int reps = int((most + segments - 1) / segments);
-  segments = (most + reps - 1) / reps;
-  const int64_t tasks = p.num_tokens * segments;
-  const FastDiv fd = make_fastdiv(uint32_t(segments));
+  auto deal = [&](int most, int *per_task, int64_t *tasks) {
+    int64_t segments = (int64_t(152) * 16 + p.num_tokens - 1) / p.num_tokens;
+    if (segments > most) segments = most;
+    *per_task = int((most + segments - 1) / segments);
+    segments = (most + *per_task - 1) / *per_task;
+    *tasks = p.num_tokens * segments;
+    return make_fastdiv(uint32_t(segments));
+  };
+  AppendKernel k = append_fast(p);
+  int most;
+  if (k) {
+    most = (p.q_heads + kGroups - 1) / kGroups + (p.kv_heads + kGroups - 1) / kGroups * (p.has_v ? 2 : 1);
+  } else {
+    const int iters = (p.D / 8 + kLanes - 1) / kLanes;
+    k = iters == 1   ? append_kernel_of<1>(p)
+        : iters == 2 ? append_kernel_of<2>(p)
+        : iters == 3 ? append_kernel_of<3>(p)
+        : iters == 4 ? append_kernel_of<4>(p)
+        : iters <= 9 ? append_kernel_of<9>(p)
+                     : append_kernel_of<12>(p);
+    const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
+    most = (p.q_heads + p.kv_heads * (p.has_v ? 2 : 1) + step - 1) / step;
+  }
+  int per_task = 0;
+  int64_t tasks = 0;
+  const FastDiv fd = deal(most, &per_task, &tasks);
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -312,7 +613,7 @@ int launch_append(const AppendParams &p, void *stream) {
   c.stream = static_cast<cudaStream_t>(stream);
   c.attrs = &at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, k, p, reps, fd);
+  const cudaError_t e = cudaLaunchKernelEx(&c, k, p, per_task, fd);
   return int(e != cudaSuccess ? e : cudaGetLastError());
 }
 
