@@ -1,20 +1,29 @@
 // hicache_evict.cu -- the pages of each sequence with the least accumulated
 // attention weight, and the page table without them.
 //
-// One CTA per sequence.  The count-th lowest key among the pages that may go is
-// found by a radix select (four 8-bit digits of an order-preserving integer key,
-// a shared-memory histogram each); then one pass over the pages in order splits
-// them into those that leave and those that stay, each place worked out by a
-// block-wide scan.  Among equal keys the first pages leave.  A page moves to
-// its own place or an earlier one, and a chunk is written only once it has been
-// read whole, so the outputs may be the inputs.
+// The count-th lowest key among the pages that may go is found by a radix select
+// (four 8-bit digits of an order-preserving integer key, a histogram each); then the
+// pages are split, in their order, into those that leave and those that stay, each
+// place worked out by a scan.  Among equal keys the first pages leave.
+//
+// A cluster of CTAs takes a sequence, each CTA a part of its pages, which it reads
+// once into shared memory; histograms and counts are summed over the cluster through
+// distributed shared memory.  Everything has been read before anything is written,
+// so the outputs may be the inputs.  Bound by the cluster's barriers: 131,071 pages
+// are 2 MB and take 25 us (198 us by one CTA).  Sequences too long for the cluster's shared memory take
+// one CTA that walks them chunk by chunk.
 
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "hicache_serving.h"
 
 namespace hicache {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kEvictThreads = 1024;
 
@@ -25,19 +34,182 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
+// A sequence's pages: n in all, those in [sink, last) may go, `count` of them do.
+struct EvictSeq {
+  int len, n, last, count;
+};
+__device__ __forceinline__ EvictSeq evict_seq(const EvictParams &p, int64_t b) {
+  EvictSeq s;
+  s.len = p.lens[b];
+  const int64_t pages = s.len > 0 ? (int64_t(s.len) + p.P - 1) / p.P : 0;
+  s.n = int(pages < p.max_pages ? pages : p.max_pages);
+  s.last = s.n - p.recent;
+  const int may = max(0, s.last - p.sink);
+  s.count = min(min(max(0, s.n - max(0, p.keep[b])), may), p.max_victims);
+  return s;
+}
+
+// The digit of the need-th lowest key in `hist` (256 counts) and the rank left within
+// it, into pick[0..1]; for one warp.
+__device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, uint32_t *pick, int lane) {
+  uint32_t c[8], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum += c[j] = hist[lane * 8 + j];
+  uint32_t before = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  before -= sum;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (before < need && need <= before + c[j]) {
+      pick[0] = uint32_t(lane * 8 + j);
+      pick[1] = need - before;
+    }
+    before += c[j];
+  }
+}
+
+// `cap`: pages that a CTA's dynamic shared memory holds (8 bytes each).
+__global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __grid_constant__ EvictParams p, int cap) {
+  extern __shared__ __align__(16) unsigned char pages_smem[];
+  __shared__ uint32_t hist[2][256], total[256], pick[2];
+  __shared__ uint32_t warp_below[32], warp_equal[32], cta_count[2], ahead[2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
+  float *const w_s = reinterpret_cast<float *>(pages_smem);
+  int32_t *const t_s = reinterpret_cast<int32_t *>(w_s + cap);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int64_t b = blockIdx.x / unsigned(cs);
+  const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  const EvictSeq q = evict_seq(p, b);
+  const int n = q.n, count = q.count;
+  const int slice = min(cap, ((n + cs - 1) / cs + 31) & ~31);
+  const int lo = min(n, rank * slice), mine = min(n, lo + slice) - lo;
+  for (int i = tid; i < mine; i += kEvictThreads) {
+    w_s[i] = p.weights[b * p.w_sb + lo + i];
+    t_s[i] = p.table[b * p.t_sb + lo + i];
+  }
+  if (tid < 512) hist[tid >> 8][tid & 255] = 0;
+  __syncthreads();
+
+  // the key of the last page that leaves, and how many pages with that key do
+  uint32_t key = 0, mask = 0, need = uint32_t(count);
+  if (count > 0) {
+    const int from = max(0, p.sink - lo), to = min(mine, q.last - lo);
+#pragma unroll 1
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      uint32_t *h = hist[pass & 1];
+      for (int i = from + tid; i < to; i += kEvictThreads) {
+        const uint32_t k = order_key(w_s[i]);
+        if ((k & mask) == key) atomicAdd(&h[(k >> shift) & 255], 1u);
+      }
+      cluster.sync();
+      if (tid < 256) {
+        uint32_t sum = 0;
+        for (int r = 0; r < cs; ++r) sum += cluster.map_shared_rank(h, r)[tid];
+        total[tid] = sum;
+        // the other histogram was last read before the barrier above
+        hist[(pass & 1) ^ 1][tid] = 0;
+      }
+      __syncthreads();
+      if (warp == 0) pick_digit(total, need, pick, lane);
+      __syncthreads();
+      key |= pick[0] << shift;
+      mask |= 255u << shift;
+      need = pick[1];
+    }
+  }
+
+  // keys below and equal: per warp (a run of pages each), CTA and cluster
+  const int run = ((slice + kEvictThreads - 1) / kEvictThreads) * 32;
+  const int w0 = min(mine, warp * run), w1 = min(mine, w0 + run);
+  auto flags = [&](int i, bool *below, bool *equal) {
+    *below = *equal = false;
+    if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last) {
+      const uint32_t k = order_key(w_s[i]);
+      *below = k < key;
+      *equal = k == key;
+    }
+  };
+  uint32_t below0 = 0, equal0 = 0;
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    bool below, equal;
+    flags(i, &below, &equal);
+    below0 += __popc(__ballot_sync(0xffffffffu, below));
+    equal0 += __popc(__ballot_sync(0xffffffffu, equal));
+  }
+  if (lane == 0) {
+    warp_below[warp] = below0;
+    warp_equal[warp] = equal0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t x = warp_below[lane], y = warp_equal[lane];
+    const uint32_t x0 = x, y0 = y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t xo = __shfl_up_sync(0xffffffffu, x, o), yo = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) x += xo, y += yo;
+    }
+    warp_below[lane] = x - x0;
+    warp_equal[lane] = y - y0;
+    if (lane == 31) cta_count[0] = x, cta_count[1] = y;
+  }
+  cluster.sync();                                 // and every CTA has read its pages
+  if (warp == 0) {
+    uint32_t x = 0, y = 0;
+    if (lane < rank) {
+      const uint32_t *c = cluster.map_shared_rank(cta_count, lane);
+      x = c[0];
+      y = c[1];
+    }
+    x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    if (lane == 0) ahead[0] = x, ahead[1] = y;
+  }
+  __syncthreads();
+  below0 = ahead[0] + warp_below[warp];
+  equal0 = ahead[1] + warp_equal[warp];
+  const uint32_t lower = (1u << lane) - 1u;
+  for (int i = w0 + lane; i - lane < w1; i += 32) {
+    bool below, equal;
+    flags(i, &below, &equal);
+    const uint32_t bm = __ballot_sync(0xffffffffu, below), em = __ballot_sync(0xffffffffu, equal);
+    const uint32_t nb = below0 + __popc(bm & lower), ne = equal0 + __popc(em & lower);
+    const uint32_t gone = nb + min(ne, need);     // pages before this one that leave
+    if (i < w1) {
+      if (below || (equal && ne < need)) {
+        p.victims[b * p.v_sb + gone] = t_s[i];
+      } else {
+        p.out_table[b * p.ot_sb + lo + i - gone] = t_s[i];
+        p.out_weights[b * p.ow_sb + lo + i - gone] = w_s[i];
+      }
+    }
+    below0 += __popc(bm);
+    equal0 += __popc(em);
+  }
+  for (int i = n - count + rank * kEvictThreads + tid; i < n; i += cs * kEvictThreads) {
+    p.out_table[b * p.ot_sb + i] = -1;
+    p.out_weights[b * p.ow_sb + i] = 0.f;
+  }
+  if (rank == 0 && tid == 0) {
+    p.num_victims[b] = count;
+    p.out_lens[b] = q.len - count * p.P;
+  }
+  cluster.sync();                                 // nobody reads this CTA's memory any more
+}
+
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t pick[2];              // digit, rank within it
   __shared__ unsigned long long warp_sum[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   const int64_t b = blockIdx.x;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-  const int len = p.lens[b];
-  const int64_t pages64 = len > 0 ? (int64_t(len) + p.P - 1) / p.P : 0;
-  const int n = int(pages64 < p.max_pages ? pages64 : p.max_pages);
-  const int keep = max(0, p.keep[b]);
-  const int last = n - p.recent;            // pages in [sink, last) may go
-  const int may = max(0, last - p.sink);
-  const int count = min(min(max(0, n - keep), may), p.max_victims);
+  const EvictSeq q = evict_seq(p, b);
+  const int n = q.n, count = q.count, last = q.last;
   const int32_t *table = p.table + b * p.t_sb;
   const float *weights = p.weights + b * p.w_sb;
 
@@ -52,23 +224,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
         if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & 255], 1u);
       }
       __syncthreads();
-      if (tid < 32) {
-        uint32_t c[8], sum = 0;
-        for (int j = 0; j < 8; ++j) sum += c[j] = hist[tid * 8 + j];
-        uint32_t before = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
-          if (tid >= o) before += y;
-        }
-        before -= sum;
-        for (int j = 0; j < 8; ++j) {
-          if (before < need && need <= before + c[j]) {
-            pick[0] = uint32_t(tid * 8 + j);
-            pick[1] = need - before;
-          }
-          before += c[j];
-        }
-      }
+      if (warp == 0) pick_digit(hist, need, pick, lane);
       __syncthreads();
       key |= pick[0] << shift;
       mask |= 255u << shift;
@@ -129,15 +285,48 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
   }
   if (tid == 0) {
     p.num_victims[b] = count;
-    p.out_lens[b] = len - count * p.P;
+    p.out_lens[b] = q.len - count * p.P;
   }
 }
 
 }  // namespace
 
-int launch_evict(const EvictParams &p, void *stream) {
-  evict_kernel<<<unsigned(p.B), kEvictThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return int(cudaGetLastError());
+int launch_evict(const EvictParams &p, int device, void *stream) {
+  constexpr int kMaxDevices = 64;
+  constexpr int kCap = 24576;                     // pages of a CTA: 192 KiB of shared memory
+  constexpr int kCluster = 8;
+  // one CTA up to 4,096 pages, four to a thread: there the cluster's barriers cost
+  // more than they save
+  const int cs = p.max_pages <= 4096 ? 1 : kCluster;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = unsigned(cs);
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.blockDim = dim3(kEvictThreads);
+  c.stream = static_cast<cudaStream_t>(stream);
+  c.attrs = at;
+  cudaError_t e;
+  if (p.max_pages > kCluster * kCap) {
+    c.gridDim = dim3(unsigned(p.B));
+    c.numAttrs = 1;
+    e = cudaLaunchKernelEx(&c, evict_kernel, p);
+  } else {
+    static std::atomic<bool> ready[kMaxDevices];
+    if (device >= kMaxDevices || !ready[device].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(evict_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap * 8);
+      if (e != cudaSuccess) return int(e);
+      if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
+    }
+    const int cap = ((p.max_pages + cs - 1) / cs + 31) & ~31;
+    c.gridDim = dim3(unsigned(p.B) * unsigned(cs));
+    c.dynamicSmemBytes = size_t(cap) * 8;
+    c.numAttrs = 2;
+    e = cudaLaunchKernelEx(&c, evict_cluster_kernel, p, cap);
+  }
+  return int(e != cudaSuccess ? e : cudaGetLastError());
 }
 
 }  // namespace hicache

@@ -334,7 +334,7 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
 int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {
   clear_error();
   if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the evict descriptor is NULL");
-  int rc = check_grid("batch", a->batch, INT32_MAX);
+  int rc = check_grid("batch", a->batch, (1 << 28) - 1);
   if (rc) return rc;
   if (a->page_size < 1 || a->max_pages < 1 || a->max_victims < 0 || a->sink < 0 || a->recent < 1)
     return set_error(HICACHE_ERR_INVALID_ARG,
@@ -383,7 +383,10 @@ int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {
   p.max_victims = a->max_victims;
   p.sink = a->sink;
   p.recent = a->recent;
-  const int e = hicache::launch_evict(p, stream);
+  int device = 0;
+  const cudaError_t de = cudaGetDevice(&device);
+  if (de != cudaSuccess) return cuda_error(de, "cudaGetDevice");
+  const int e = hicache::launch_evict(p, device, stream);
   return launched(e, e == 0, "evict kernel launch");
 }
 

@@ -80,6 +80,6 @@ struct EvictParams {
   int64_t t_sb, w_sb, v_sb, ot_sb, ow_sb;
   int32_t P, B, max_pages, max_victims, sink, recent;
 };
-int launch_evict(const EvictParams &p, void *stream);
+int launch_evict(const EvictParams &p, int device, void *stream);
 
 }  // namespace hicache
