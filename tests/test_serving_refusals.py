@@ -178,14 +178,19 @@ def test_tensors_are_checked():
         hc.append_kv(kv, desc(), 0, None, None, None, None)
     with pytest.raises(ValueError, match="current CUDA device"):
         hc.evict_pages(16, i32(3, 5), i32(3), torch.zeros((3, 5)), i32(3), i32(3, 5), i32(3))
-    cpu = torch.device("cpu")
-    for t, dtype, ndim in ((q, torch.float16, 3), (q, torch.bfloat16, 2), (q.transpose(1, 2), torch.bfloat16, 3)):
+    b16, cpu = torch.bfloat16, -1
+    assert hc._tensor("t", q, b16, (3, 4, 128), cpu) == (512, 128, 1)
+    for t, dtype, shape, device in ((q, torch.float16, (3, 4, 128), cpu), (q, b16, (3, 4, 64), cpu),
+                                    (q, b16, (3, 512), cpu), (q, b16, (3, 4, 128), 0),
+                                    (q.transpose(1, 2), b16, (3, 128, 4), cpu)):
         with pytest.raises(ValueError):
-            hc._tensor("t", t, dtype, ndim, cpu)
-    with pytest.raises(ValueError):
-        hc._tensor("t", q, torch.bfloat16, 3, torch.device("meta"))
-    with pytest.raises(ValueError):
+            hc._tensor("t", t, dtype, shape, device)
+    with pytest.raises(ValueError, match="buffers"):
         hc._check_cache(hc.DeviceKV([A] * 3, 10), desc(), 0, cpu)
     small = torch.zeros((10 * 16, 255), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="bytes"):
         hc._check_cache(hc.DeviceKV([small] * 4, 10), desc(), 0, cpu)
+    with pytest.raises(ValueError, match="expected device 0"):
+        hc._check_cache(hc.DeviceKV([small] * 4, 1), desc(), 0, 0)
+    with pytest.raises(ValueError, match="contiguous"):
+        hc._check_cache(hc.DeviceKV([torch.zeros((320, 512), dtype=b16)[:, ::2]] * 4, 10), desc(), 0, cpu)

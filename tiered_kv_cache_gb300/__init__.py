@@ -292,6 +292,7 @@ class DeviceKV:
         self.ref = ctypes.byref(self.struct)      # made once: every call passes it
         self.device_num_pages = device_num_pages
         self.num_buffers_total = len(ptrs)
+        self.checked = set()                      # pool shapes the tensors were checked for
 
 
 def _desc(num_layers, num_buffers, page_size, row_elems, host_num_pages, layout,
@@ -746,40 +747,51 @@ BF16 = 0
 FP16 = 1
 
 
-def _tensor(name, t, dtype, ndim, device):
-    """Checks a torch tensor argument: type, dimensions, a contiguous innermost
-    dimension, and the device the call runs on."""
-    if t.dtype != dtype:
+def _tensor(name, t, dtype, shape, device):
+    """Checks a torch tensor argument (type, shape, device index, a contiguous
+    innermost dimension) and returns its strides."""
+    strides = t.stride()
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == device
+            and (strides[-1] == 1 or shape[-1] <= 1)):
+        return strides
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected {ndim}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.stride(-1) != 1 and t.size(-1) > 1:
-        raise ValueError(f"{name}: the innermost dimension must be contiguous")
-    return t
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected device {device}")
+    raise ValueError(f"{name}: the innermost dimension must be contiguous")
 
 
-def _shape(name, t, shape):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+_torch = None
+
+
+def _import_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _activations(name, t):
-    """(dtype code, device) of the tensor that decides both for a call: a
+    """(dtype code, device index) of the tensor that decides both for a call: a
     [n, heads, dim] tensor on the current CUDA device."""
-    import torch
-    code = BF16 if t.dtype == torch.bfloat16 else FP16 if t.dtype == torch.float16 else -1
+    torch = _import_torch()
+    dt = t.dtype
+    code = BF16 if dt is torch.bfloat16 else FP16 if dt is torch.float16 else -1
     if code < 0:
-        raise ValueError(f"{name}: {t.dtype}, expected bfloat16 or float16")
-    _current(name, t)
-    return code, t.device
+        raise ValueError(f"{name}: {dt}, expected bfloat16 or float16")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected 3")
+    return code, _current(name, t)
 
 
 def _current(name, t):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    device = t.get_device()
+    if device < 0 or device != _import_torch().cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, expected the current CUDA device")
+    return device
 
 
 def _pool_desc(pool_or_desc) -> PoolDesc:
@@ -789,21 +801,23 @@ def _pool_desc(pool_or_desc) -> PoolDesc:
 def _check_cache(kv, desc, layer, device):
     """The cache must hold desc's buffers; its torch tensors must be on the
     call's device and hold the pages they are said to (raw addresses cannot be
-    checked)."""
-    if kv.num_buffers_total != desc.num_buffers * desc.num_layers:
-        raise ValueError(f"DeviceKV has {kv.num_buffers_total} buffers, the pool "
-                         f"{desc.num_buffers} x {desc.num_layers}")
-    if not 0 <= layer < desc.num_layers:
-        return                       # the library's own error
-    need = kv.device_num_pages * desc.page_size * desc.row_elems * desc.elem_bytes
-    for b in range(desc.num_buffers):
-        t = kv._tensors[b * desc.num_layers + layer]
+    checked).  A shape that kv has been checked for is not checked again."""
+    layers, buffers, row_bytes = desc.num_layers, desc.num_buffers, desc.page_size * desc.row_elems * desc.elem_bytes
+    shape = (layers, buffers, row_bytes, device)
+    if shape in kv.checked:
+        return buffers
+    if kv.num_buffers_total != buffers * layers:
+        raise ValueError(f"DeviceKV has {kv.num_buffers_total} buffers, the pool {buffers} x {layers}")
+    need = kv.device_num_pages * row_bytes
+    for t in kv._tensors:
         if isinstance(t, int):
             continue
-        if t.device != device:
-            raise ValueError(f"the cache is on {t.device}, expected {device}")
-        if t.numel() * t.element_size() < need:
-            raise ValueError(f"a cache buffer has {t.numel() * t.element_size()} bytes, its pages need {need}")
+        if t.get_device() != device:
+            raise ValueError(f"the cache is on {t.device}, expected device {device}")
+        if t.numel() * t.element_size() < need or not t.is_contiguous():
+            raise ValueError(f"a cache buffer has {t.numel() * t.element_size()} bytes, its pages need {need} contiguous")
+    kv.checked.add(shape)
+    return buffers
 
 
 def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=None, positions=None, cos_sin=None,
@@ -816,60 +830,62 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
 
     q [n, q_heads, dim] -> q_out (None: in place); k, v [n, kv_heads, dim] (v is
     None for a latent cache).  q, or k and v and slots, may be None."""
-    import torch
+    torch = _import_torch()
     first = q if q is not None else k
     if first is None:
         raise ValueError("q and k are both None")
     code, dev = _activations("q" if q is not None else "k", first)
     dt = first.dtype
     desc = _pool_desc(pool_or_desc)
-    _check_cache(kv, desc, layer, dev)
-    n, dim = first.shape[0], first.shape[-1]
-    qp = op = kp = vp = qst = qsh = ost = osh = kst = ksh = vst = vsh = hq = hk = 0
+    buffers = _check_cache(kv, desc, layer, dev)
+    n, hq, dim = first.shape
+    qp = op = kp = vp = qst = qsh = ost = osh = kst = ksh = vst = vsh = hk = sp = 0
     if q is not None:
-        _tensor("q", q, dt, 3, dev)
-        o = q if q_out is None else _tensor("q_out", q_out, dt, 3, dev)
-        hq = q.shape[1]
-        _shape("q_out", o, (n, hq, dim))
-        qp, op = q.data_ptr(), o.data_ptr()
-        qst, qsh, _ = q.stride()
-        ost, osh, _ = o.stride()
-    sp = 0
+        qst, qsh, _ = _tensor("q", q, dt, (n, hq, dim), dev)
+        qp = op = q.data_ptr()
+        ost, osh = qst, qsh
+        if q_out is not None:
+            ost, osh, _ = _tensor("q_out", q_out, dt, (n, hq, dim), dev)
+            op = q_out.data_ptr()
+    else:
+        hq = 0
     if k is not None:
-        hk = k.shape[1]
-        _tensor("k", k, dt, 3, dev)
-        _shape("k", k, (n, hk, dim))
+        hk = k.shape[1] if k.dim() == 3 else 0
+        kst, ksh, _ = _tensor("k", k, dt, (n, hk, dim), dev)
         kp = k.data_ptr()
-        kst, ksh, _ = k.stride()
-        if (v is None) != (desc.num_buffers == 1):
+        if (v is None) != (buffers == 1):
             raise ValueError("a K, V cache takes v, a latent cache none")
         if v is not None:
-            _tensor("v", v, dt, 3, dev)
-            _shape("v", v, (n, hk, dim))
+            vst, vsh, _ = _tensor("v", v, dt, (n, hk, dim), dev)
             vp = v.data_ptr()
-            vst, vsh, _ = v.stride()
-        _shape("slots", _tensor("slots", slots, torch.int64, 1, dev), (n,))
+        _tensor("slots", slots, torch.int64, (n,), dev)
         sp = slots.data_ptr()
     elif v is not None:
         raise ValueError("v without k")
     qw = kw = qn = kn = 0
     if q_weight is not None:
-        qw, qn = _tensor("q_weight", q_weight, dt, 1, dev).data_ptr(), q_weight.shape[0]
+        qn = q_weight.numel()
+        _tensor("q_weight", q_weight, dt, (qn,), dev)
+        qw = q_weight.data_ptr()
     if k_weight is not None:
-        kw, kn = _tensor("k_weight", k_weight, dt, 1, dev).data_ptr(), k_weight.shape[0]
+        kn = k_weight.numel()
+        _tensor("k_weight", k_weight, dt, (kn,), dev)
+        kw = k_weight.data_ptr()
     pp = cp = rows = rot = 0
     if cos_sin is not None:
-        _tensor("cos_sin", cos_sin, torch.float32, 2, dev)
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous, of two dimensions")
         rows, rot = cos_sin.shape
-        if rows > 1 and cos_sin.stride(0) != rot:
-            raise ValueError("cos_sin must be contiguous")
+        _tensor("cos_sin", cos_sin, torch.float32, (rows, rot), dev)
         if positions is None:
             raise ValueError("cos_sin without positions")
-        _shape("positions", _tensor("positions", positions, torch.int64, 1, dev), (n,))
+        _tensor("positions", positions, torch.int64, (n,), dev)
         pp, cp = positions.data_ptr(), cos_sin.data_ptr()
     a = _APPEND_DESC.pack(qp, op, kp, vp, qw, kw, sp, pp, cp, qst, qsh, ost, osh, kst, ksh, vst, vsh, n, rows,
                           code, hq, hk, dim, qn, kn, rot, rot_offset, bool(interleaved), eps, k_scale, v_scale)
-    _check(library().hicache_append_kv(kv.ref, ctypes.byref(desc), layer, a, _stream(stream)))
+    rc = library().hicache_append_kv(kv.ref, ctypes.byref(desc), layer, a, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def decode_workspace(pool_or_desc, batch: int, q_heads: int, head_dim: int, v_dim: int, max_pages: int,
@@ -891,36 +907,33 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     (optional) [batch, q_heads] the log of the softmax sums; weights (optional)
     [batch, max_pages] <- decay * weights + the attention each page received.
     scale: head_dim ** -0.5 unless given."""
-    import torch
+    torch = _import_torch()
     code, dev = _activations("q", q)
     dt = q.dtype
     desc = _pool_desc(pool_or_desc)
     _check_cache(kv, desc, layer, dev)
-    _tensor("q", q, dt, 3, dev)
     b, hq, d = q.shape
-    _tensor("out", out, dt, 3, dev)
-    dv = out.shape[-1]
-    _shape("out", out, (b, hq, dv))
-    _tensor("page_table", page_table, torch.int32, 2, dev)
-    width = page_table.shape[1]
-    _shape("page_table", page_table, (b, width))
-    _shape("seq_lens", _tensor("seq_lens", seq_lens, torch.int32, 1, dev), (b,))
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous and on {dev}")
+    qb, qh, _ = _tensor("q", q, dt, (b, hq, d), dev)
+    dv, width = out.shape[-1], page_table.shape[-1]
+    ob, oh, _ = _tensor("out", out, dt, (b, hq, dv), dev)
+    tst = _tensor("page_table", page_table, torch.int32, (b, width), dev)[0]
+    _tensor("seq_lens", seq_lens, torch.int32, (b,), dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on device {dev}")
     lp = wp = lst = wst = 0
     if lse is not None:
-        _shape("lse", _tensor("lse", lse, torch.float32, 2, dev), (b, hq))
-        lp, lst = lse.data_ptr(), lse.stride(0)
+        lst = _tensor("lse", lse, torch.float32, (b, hq), dev)[0]
+        lp = lse.data_ptr()
     if weights is not None:
-        _shape("weights", _tensor("weights", weights, torch.float32, 2, dev), (b, width))
-        wp, wst = weights.data_ptr(), weights.stride(0)
-    qb, qh, _ = q.stride()
-    ob, oh, _ = out.stride()
+        wst = _tensor("weights", weights, torch.float32, (b, width), dev)[0]
+        wp = weights.data_ptr()
     a = _DECODE_DESC.pack(q.data_ptr(), out.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), lp, wp,
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), qb, qh, ob, oh,
-                          page_table.stride(0), lst, wst, code, b, hq, d, dv, width, window, 0,
+                          tst, lst, wst, code, b, hq, d, dv, width, window, 0,
                           d ** -0.5 if scale is None else scale, k_scale, v_scale, decay)
-    _check(library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _stream(stream)))
+    rc = library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, num_victims, *, sink: int = 0,
@@ -929,33 +942,35 @@ def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, nu
     weights leave until keep[b] are left (or none may go, or victims is full):
     victims [batch, max_victims] receives their pages, num_victims their number,
     and out_table, out_lens, out_weights (None: in place) what stays."""
-    import torch
-    _current("page_table", page_table)
-    dev = page_table.device
-    i32 = torch.int32
-    _tensor("page_table", page_table, i32, 2, dev)
+    torch = _import_torch()
+    dev = _current("page_table", page_table)
+    i32, f32 = torch.int32, torch.float32
+    if page_table.dim() != 2 or victims.dim() != 2:
+        raise ValueError("page_table and victims must have two dimensions")
     b, width = page_table.shape
-    _shape("weights", _tensor("weights", weights, torch.float32, 2, dev), (b, width))
-    _shape("seq_lens", _tensor("seq_lens", seq_lens, i32, 1, dev), (b,))
-    _shape("keep", _tensor("keep", keep, i32, 1, dev), (b,))
-    _shape("num_victims", _tensor("num_victims", num_victims, i32, 1, dev), (b,))
-    _tensor("victims", victims, i32, 2, dev)
-    _shape("victims", victims, (b, victims.shape[1]))
-    if out_table is None:
-        out_table = page_table
-    else:
-        _shape("out_table", _tensor("out_table", out_table, i32, 2, dev), (b, width))
-    if out_weights is None:
-        out_weights = weights
-    else:
-        _shape("out_weights", _tensor("out_weights", out_weights, torch.float32, 2, dev), (b, width))
-    if out_lens is None:
-        out_lens = seq_lens
-    else:
-        _shape("out_lens", _tensor("out_lens", out_lens, i32, 1, dev), (b,))
-    a = _EVICT_DESC.pack(page_table.data_ptr(), weights.data_ptr(), seq_lens.data_ptr(), keep.data_ptr(),
-                         victims.data_ptr(), num_victims.data_ptr(), out_table.data_ptr(), out_weights.data_ptr(),
-                         out_lens.data_ptr(), page_table.stride(0), weights.stride(0), victims.stride(0),
-                         out_table.stride(0), out_weights.stride(0), page_size, b, width, victims.shape[1], sink,
-                         recent)
-    _check(library().hicache_evict_pages(a, _stream(stream)))
+    rows, one = (b, width), (b,)
+    cap = victims.shape[1]
+    tst = _tensor("page_table", page_table, i32, rows, dev)[0]
+    wst = _tensor("weights", weights, f32, rows, dev)[0]
+    _tensor("seq_lens", seq_lens, i32, one, dev)
+    _tensor("keep", keep, i32, one, dev)
+    _tensor("num_victims", num_victims, i32, one, dev)
+    vst = _tensor("victims", victims, i32, (b, cap), dev)[0]
+    tp = otp = page_table.data_ptr()
+    wp = owp = weights.data_ptr()
+    lp = olp = seq_lens.data_ptr()
+    otst, owst = tst, wst
+    if out_table is not None:
+        otst = _tensor("out_table", out_table, i32, rows, dev)[0]
+        otp = out_table.data_ptr()
+    if out_weights is not None:
+        owst = _tensor("out_weights", out_weights, f32, rows, dev)[0]
+        owp = out_weights.data_ptr()
+    if out_lens is not None:
+        _tensor("out_lens", out_lens, i32, one, dev)
+        olp = out_lens.data_ptr()
+    a = _EVICT_DESC.pack(tp, wp, lp, keep.data_ptr(), victims.data_ptr(), num_victims.data_ptr(), otp, owp, olp,
+                         tst, wst, vst, otst, owst, page_size, b, width, cap, sink, recent)
+    rc = library().hicache_evict_pages(a, _stream(stream))
+    if rc:
+        _check(rc)
