@@ -737,76 +737,88 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
 // ---- page weights ----------------------------------------------------------------
 
 // weights[b, p] <- decay * weights[b, p] + sum over heads and tokens of
-// 2^(score - lse2).  Bound by reading the scores (4 bytes a head and token).  A
-// block takes as many whole pages as 128 tokens hold (one page if it is longer),
-// a warp every eighth head, a lane four tokens of it, so that the loads of all
-// its heads are on their way together.  Then each token is summed over the warps
-// and each page over its tokens, in an order that does not depend on timing.
-constexpr int kWeightThreads = 256, kWeightTok = 128;
+// 2^(score - lse2).  Bound by reading the scores (4 bytes a head and token).  A warp
+// takes as many whole pages as 128 tokens hold, a lane four tokens, with the loads
+// of 8 heads on their way together and no barrier with other warps; a longer page
+// is dealt to the block's warps in chunks of 128 tokens.  Heads, then a page's
+// tokens are added in an order that does not depend on timing.
+constexpr int kWeightWarps = 4, kWeightTok = 128;
 
-HC_HD int weight_pages(int page) { return page < kWeightTok ? kWeightTok / page : 1; }
+HC_HD int weight_pages(int page) { return page <= kWeightTok ? kWeightTok / page : 1; }
+// blocks for a sequence of max_pages pages
+HC_HD int weight_blocks(int page, int max_pages) {
+  const int per = page <= kWeightTok ? kWeightWarps * weight_pages(page) : 1;
+  return (max_pages - 1) / per + 1;
+}
 
-__global__ void __launch_bounds__(kWeightThreads) weights_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kWeightWarps * 32) weights_kernel(const __grid_constant__ DecodeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the scores and lse of the kernel before
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int WARPS = kWeightThreads / 32;
-  __shared__ float part[WARPS][kWeightTok], val[kWeightTok];
-  const int b = blockIdx.y, tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  __shared__ float val_all[kWeightWarps][kWeightTok];
+  const int b = blockIdx.y, warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  float *const val = val_all[warp];
+  const bool shared_page = p.P > kWeightTok;
+  const int per = weight_pages(p.P);
+  const int first = shared_page ? int(blockIdx.x) : (int(blockIdx.x) * kWeightWarps + warp) * per;
   int start, len;
   seq_range(p, b, &start, &len);
-  const int per = weight_pages(p.P);                       // pages of a block
-  const int first = int(blockIdx.x) * per;
   const int pages = int(len > 0 ? fast_div(uint32_t(len - 1), p.fd_page) + 1 : 0);
-  if (first >= pages) return;
+  if (first >= pages) return;                     // the whole warp (of a long page: the whole block)
   const int t0 = first * p.P, t1 = int(min(int64_t(len), (int64_t(first) + per) * p.P));
   const float *lse2 = p.lse2 + int64_t(b) * p.Hq;
   const float *sc = p.scores + int64_t(b) * p.Hq * p.score_row;
-  float whole = 0.f;                                       // a long page: this thread's tokens of it
-  for (int base = t0; base < t1; base += kWeightTok) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int h = warp; h < p.Hq; h += WARPS) {
-      const float z = __ldg(lse2 + h);
+  float *const weights = p.weights + b * p.w_sb + first;
+  const int mine = min(per, pages - first);
+  // the old weights, on their way with the scores
+  const float old = lane < mine && !shared_page ? weights[lane] : 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int step = shared_page ? kWeightWarps * kWeightTok : kWeightTok;
+  for (int base = t0 + (shared_page ? warp * kWeightTok : 0); base < t1; base += step) {
+    for (int h0 = 0; h0 < p.Hq; h0 += 8) {
+      float s[8][4], z[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = base + lane + 32 * j;
-        const float s = t >= start && t < t1 ? __ldcs(sc + h * p.score_row + t) : -INFINITY;
-        acc[j] += s == -INFINITY ? 0.f : exp2_fast(s - z);
+      for (int h = 0; h < 8; ++h) {
+        z[h] = h0 + h < p.Hq ? __ldg(lse2 + h0 + h) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = base + lane + 32 * j;
+          s[h][j] = h0 + h < p.Hq && t >= start && t < t1 ? __ldcs(sc + (h0 + h) * p.score_row + t) : -INFINITY;
+        }
       }
-    }
-    __syncthreads();                                       // part is free again
 #pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][lane + 32 * j] = acc[j];
-    __syncthreads();
-    if (tid < kWeightTok) {
-      float v = 0.f;
+      for (int h = 0; h < 8; ++h)
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) v += part[w][tid];
-      val[tid] = v;
-      whole += v;
+        for (int j = 0; j < 4; ++j) acc[j] += s[h][j] == -INFINITY ? 0.f : exp2_fast(s[h][j] - z[h]);
     }
   }
-  if (p.P > kWeightTok) {
-    if (tid < kWeightTok) val[tid] = whole;
+  if (shared_page) {
+    float s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) val[0] = s;
     __syncthreads();
+    if (threadIdx.x == 0) {
+      s = 0.f;
+      for (int w = 0; w < kWeightWarps; ++w) s += val_all[w][0];
+      *weights = p.decay * *weights + s;
+    }
+    return;
   }
-  __syncthreads();
-  if (p.P >= 32) {                                         // a warp for a page
-    for (int pg = warp; pg < per && first + pg < pages; pg += WARPS) {
-      const int n = min(p.P, kWeightTok);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) val[lane + 32 * j] = acc[j];
+  __syncwarp();
+  if (p.P >= 16) {                                // the warp a page at a time (8 of them at most)
+    for (int pg = 0; pg < mine; ++pg) {
       float s = 0.f;
-      for (int i = lane; i < n; i += 32) s += val[pg * n + i];
+      for (int i = lane; i < p.P; i += 32) s += val[pg * p.P + i];
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) {
-        float *w = p.weights + b * p.w_sb + first + pg;
-        *w = p.decay * *w + s;
-      }
+      if (lane == pg) weights[pg] = p.decay * old + s;
     }
-  } else if (tid < per && first + tid < pages) {
-    float s = 0.f;
-    for (int i = 0; i < p.P; ++i) s += val[tid * p.P + i];
-    float *w = p.weights + b * p.w_sb + first + tid;
-    *w = p.decay * *w + s;
+  } else {                                        // a page a lane
+    for (int pg = lane; pg < mine; pg += 32) {
+      float s = 0.f;
+      for (int i = 0; i < p.P; ++i) s += val[pg * p.P + i];
+      weights[pg] = p.decay * (pg < 32 ? old : weights[pg]) + s;
+    }
   }
 }
 
@@ -883,9 +895,8 @@ int launch_decode(const DecodeParams &p, int device, void *stream, int *launches
     *launches += e == 0;
   }
   if (e || !p.weights) return e;
-  const int per = weight_pages(p.P);
-  e = launch_dependent(weights_kernel, dim3(unsigned((p.max_pages + per - 1) / per), unsigned(p.B)), kWeightThreads, st,
-                       p);
+  e = launch_dependent(weights_kernel, dim3(unsigned(weight_blocks(p.P, p.max_pages)), unsigned(p.B)),
+                       kWeightWarps * 32, st, p);
   *launches += e == 0;
   return e;
 }
