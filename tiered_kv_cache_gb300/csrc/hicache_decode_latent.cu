@@ -19,8 +19,8 @@
 // tile n + 1 runs during the softmax of tile n, and a product with V whose P is
 // ready never waits behind one whose tile is still on its way.
 //
-// Softmax: a warp reads its 16 tokens as 16 x 8 fragments (2 tokens x heads / 4
-// a thread).  The running maximum of each head is raised only when some score
+// Softmax: a set of four warps (two sets for 64 heads, 32 heads each) reads 16
+// tokens a warp as 16 x 8 fragments (2 tokens x heads / 4 a thread).  The running maximum of each head is raised only when some score
 // passes it by more than P's type can hold, so that the usual tile needs one
 // barrier and no reduction; sums stay per thread until the piece ends.
 //
@@ -31,7 +31,7 @@
 // a sequence is a piece; whole sequences are written out directly, the other
 // pieces go to the workspace and latent_join_kernel adds them in order.
 //
-// Warps: 0-3 softmax and epilogue, 4 issues S, 5 O, 6-9 copy the cache and q into shared memory (cp.async, 16 bytes per lane, so
+// Warps: first the softmax and epilogue, one issues S, one O, four copy the cache and q into shared memory (cp.async, 16 bytes per lane, so
 // any page size, absent pages as zeros), signalling by mbarrier.  The tile's
 // rope block (elements 512..575) is free once S is there and then holds P.
 //
@@ -48,19 +48,23 @@ namespace {
 constexpr int kLatD = 576, kLatDv = 512;
 constexpr int kTileTok = 64, kStrip = 32;
 constexpr int kAtomB = kTileTok * 128;            // 64 elements of a tile's tokens
-constexpr int kQuadB = 4 * kAtomB;                // 256 elements
+constexpr int kDuoB = 2 * kAtomB;                 // 128 elements
 constexpr int kRopeB = kAtomB;                    // the last 64 elements
-constexpr int kLatWarps = 10, kLatThreads = kLatWarps * 32;
 constexpr int kJoinThreads = 128;
 
 template <int NH_, bool BF16_>
 struct LatConfig {
   static constexpr int NH = NH_;                  // heads (columns)
   static constexpr bool BF16 = BF16_;
-  static constexpr int QUADS = NH_ == 64 ? 4 : 5; // a tile is 2 quads and a rope block, and two
-  static constexpr int ROPES = NH_ == 16 ? 3 : 2; // tiles must fit (the products run a tile ahead)
+  static constexpr int SETS = NH_ == 64 ? 2 : 1;  // of four softmax warps
+  static constexpr int NS = NH_ / SETS;           // heads of a set
+  static constexpr int S_WARP = 4 * SETS, O_WARP = S_WARP + 1, COPY_WARP = S_WARP + 2;
+  static constexpr int WARPS = COPY_WARP + 4, THREADS = WARPS * 32;
+  // A tile is 4 duos and a rope block; at least two tiles must fit.
+  static constexpr int DUOS = NH_ == 64 ? 8 : NH_ == 32 ? 10 : 11;
+  static constexpr int ROPES = NH_ == 16 ? 3 : 2;
   static constexpr int Q_B = 9 * NH_ * 128;
-  static constexpr int SMEM = Q_B + QUADS * kQuadB + ROPES * kRopeB + 1024;
+  static constexpr int SMEM = Q_B + DUOS * kDuoB + ROPES * kRopeB + 1024;
   static constexpr int COLS = NH_ == 16 ? 128 : NH_ == 32 ? 256 : 512;   // tensor memory
   static constexpr int PIECE = NH_ * kLatDv + 2 * NH_;                   // floats: O, m, l
   // How far a score may pass the running maximum (log2) before it is raised: as
@@ -159,14 +163,14 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(bool bf16, int m, int n
          (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
-// barriers of the four softmax warps
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool x) {
+// barriers of the four warps of a softmax set
+__device__ __forceinline__ void set_sync(int set) { asm volatile("bar.sync %0, 128;" ::"r"(1 + 2 * set) : "memory"); }
+__device__ __forceinline__ bool set_any(int set, bool x) {
   int r;
   asm volatile(
-      "{.reg .pred p, q; setp.ne.s32 p, %1, 0; barrier.cta.red.or.pred q, 2, 128, p; selp.s32 %0, 1, 0, q;}"
+      "{.reg .pred p, q; setp.ne.s32 p, %1, 0; barrier.cta.red.or.pred q, %2, 128, p; selp.s32 %0, 1, 0, q;}"
       : "=r"(r)
-      : "r"(int(x))
+      : "r"(int(x)), "r"(2 + 2 * set)
       : "memory");
   return r != 0;
 }
@@ -202,8 +206,17 @@ __device__ __forceinline__ int strips_of(int start, int len) {
   return len > start ? (len + kStrip - 1) / kStrip - start / kStrip : 0;
 }
 
+constexpr int kLens = 512;                        // lengths kept in shared memory
+
+__device__ __forceinline__ void seq_range(const DecodeParams &p, const int *lens, int b, int *start, int *len) {
+  if (b >= kLens) return seq_range(p, b, start, len);
+  *len = lens[b];
+  *start = p.window > 0 ? max(0, *len - p.window) : 0;
+}
+
 // The pieces of a CTA's range of strips, in order.
 struct Pieces {
+  const int *lens;
   long long pos, hi;
   long long skip;      // strips of sequence b before the range
   int b;
@@ -214,7 +227,7 @@ struct Pieces {
     if (pos >= hi) return false;
     int len, n;
     for (;; ++b) {
-      seq_range(p, b, &start, &len);
+      seq_range(p, lens, b, &start, &len);
       n = strips_of(start, len);
       if (skip < n || b + 1 >= p.B) break;
       skip -= n;
@@ -234,11 +247,12 @@ struct Pieces {
 };
 
 template <class C>
-__global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ unsigned char smem_raw[];
-  constexpr int NH = C::NH;
-  __shared__ long long prefix[kLatThreads + 1], scratch[kLatWarps];
-  __shared__ __align__(8) unsigned long long bars[2 * C::QUADS + 2 * C::ROPES + 9];
+  constexpr int NH = C::NH, NS = C::NS, THREADS = C::THREADS;
+  __shared__ long long prefix[THREADS + 1], scratch[C::WARPS];
+  __shared__ int lens_s[kLens];
+  __shared__ __align__(8) unsigned long long bars[4 + C::DUOS + C::ROPES + 9];
   // per head: the maximum (and what scores are taken relative to: 0 while there is
   // none), the factor and the shift of the last raise
   __shared__ __align__(16) float m_s[NH], mu_s[NH], f_s[NH], d_s[NH];
@@ -248,53 +262,53 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
 
   const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_s = base, quad_s = base + C::Q_B, rope_s = quad_s + C::QUADS * kQuadB;
+  const uint32_t q_s = base, duo_s = base + C::Q_B, rope_s = duo_s + C::DUOS * kDuoB;
   unsigned char *const rope_p = smem_raw + (rope_s - smem_u32(smem_raw));
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
-  constexpr int FULL = 0, EMPTY = C::QUADS, RFULL = 2 * C::QUADS, REMPTY = RFULL + C::ROPES, QFULL = REMPTY + C::ROPES,
-                QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 4, PVDONE = QFULL + 6, LAST = QFULL + 8;
+  // a tile's copies have landed: one barrier (of 4: never more tiles in flight) for the
+  // whole tile, since a wait and its fences cost the issuing warp what 8 to 14
+  // products do; a duo, a rope block is free again: one each
+  constexpr int FULL = 0, EMPTY = 4, REMPTY = EMPTY + C::DUOS, QFULL = REMPTY + C::ROPES, QEMPTY = QFULL + 1, SFULL = QFULL + 2, PFULL = QFULL + 4, PVDONE = QFULL + 6, LAST = QFULL + 8;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
-  // the strips before each sequence
-  const int per = (p.B + kLatThreads - 1) / kLatThreads;
+  // the strips before each sequence; above 2^48, the sequences without any
+  const int per = (p.B + THREADS - 1) / THREADS;
   long long mine = 0, total = 0;
   for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
     int start, len;
     seq_range(p, b, &start, &len);
-    mine += strips_of(start, len);
+    if (b < kLens) lens_s[b] = len;
+    mine += len > start ? strips_of(start, len) : 1ll << 48;
   }
-  const long long ahead = block_prefix<kLatWarps>(mine, scratch, &total);
+  constexpr long long kStrips = (1ll << 48) - 1;
+  const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total) & kStrips;
+  const bool idle = total > kStrips;
+  total &= kStrips;
   prefix[tid] = ahead;
   if (tid == 0) {
-    prefix[kLatThreads] = total;
+    prefix[THREADS] = total;
     gave_up = 0;
-    for (int i = 0; i < C::QUADS; ++i) {
-      mbar_init(bar(FULL + i), 128);
-      mbar_init(bar(EMPTY + i), 1);
-    }
-    for (int i = 0; i < C::ROPES; ++i) {
-      mbar_init(bar(RFULL + i), 128);
-      mbar_init(bar(REMPTY + i), 1);
-    }
+    for (int i = 0; i < 4; ++i) mbar_init(bar(FULL + i), 128);
+    for (int i = 0; i < C::DUOS + C::ROPES; ++i) mbar_init(bar(EMPTY + i), 1);
     mbar_init(bar(QFULL), 128);
     mbar_init(bar(QEMPTY), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(SFULL + i), 1);
-      mbar_init(bar(PFULL + i), 128);
+      mbar_init(bar(PFULL + i), 128 * C::SETS);
       mbar_init(bar(PVDONE + i), 1);
     }
     mbar_init(bar(LAST), 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // sequences of which there is nothing to attend to
-  for (int b = int(blockIdx.x); b < p.B; b += int(gridDim.x)) {
+  for (int b = int(blockIdx.x); idle && b < p.B; b += int(gridDim.x)) {
     int start, len;
     seq_range(p, b, &start, &len);
     if (len > start) continue;
-    for (int i = tid; i < p.Hq * kLatDv; i += kLatThreads) store_out(p, b, i / kLatDv, i % kLatDv, 0.f);
-    for (int h = tid; h < p.Hq; h += kLatThreads) store_lse(p, b, h, 0.f, 0.f);
+    for (int i = tid; i < p.Hq * kLatDv; i += THREADS) store_out(p, b, i / kLatDv, i % kLatDv, 0.f);
+    for (int h = tid; h < p.Hq; h += THREADS) store_lse(p, b, h, 0.f, 0.f);
     if (tid == 0) p.seq_pieces[b] = make_int2(0, 0);
   }
   __syncthreads();
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   if (group >= groups) return;
   const int h0 = qb * NH, heads = min(NH, p.Hq - h0);
 
-  if (warp == 4) {
+  if (warp == C::S_WARP) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
                  "n"(C::COLS)
                  : "memory");
@@ -319,10 +333,11 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
   const uint32_t tmem_o = tmem, tmem_sc = tmem + 4 * NH;
 
   Pieces pc;
+  pc.lens = lens_s;
   pc.pos = total * group / groups;
   pc.hi = total * (group + 1) / groups;
   {
-    int a = 0, z = kLatThreads;                   // prefix[a] <= pos < prefix[z]
+    int a = 0, z = THREADS;                   // prefix[a] <= pos < prefix[z]
     while (z - a > 1) {
       const int mid = (a + z) >> 1;
       if (prefix[mid] <= pc.pos) a = mid; else z = mid;
@@ -331,11 +346,11 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
     pc.skip = pc.pos - prefix[a];
   }
 
-  if (warp >= 6) {
+  if (warp >= C::COPY_WARP) {
     // ---- copies: rows of 128 bytes, 8 lanes a row, 16 rows at a time
-    const int pt = tid - 6 * 32, c = pt & 7, r0 = pt >> 3;
+    const int pt = tid - C::COPY_WARP * 32, c = pt & 7, r0 = pt >> 3;
     const char *kp = static_cast<const char *>(p.k);
-    int quad = 0, quad_ph = 1, rope = 0, rope_ph = 1, piece = 0;
+    int duo = 0, duo_ph = 1, rope = 0, rope_ph = 1, piece = 0, full = 0;
     bool ok = true;
     while (ok && pc.next(p)) {
       const int b = pc.seq();
@@ -376,19 +391,18 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
 #pragma unroll
         for (int i = 0; i < 4; ++i) pages[i] = page_at(t0 + kTileTok + i * 16 + r0, &places[i]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (ok) ok = mbar_wait(bar(EMPTY + quad), uint32_t(quad_ph), &gave_up);
+        for (int part = 0; part < 4; ++part) {
+          if (ok) ok = mbar_wait(bar(EMPTY + duo), uint32_t(duo_ph), &gave_up);
           if (!ok) break;
-          const uint32_t dst = quad_s + quad * kQuadB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+          const uint32_t dst = duo_s + duo * kDuoB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
 #pragma unroll
-          for (int a = 0; a < 4; ++a)
+          for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              cp_async16(dst + a * kAtomB + i * 2048, src[i] + (bytes[i] ? half * 512 + a * 128 : 0), bytes[i]);
-          mbar_arrive_copies(bar(FULL + quad));
-          if (++quad == C::QUADS) {
-            quad = 0;
-            quad_ph ^= 1;
+              cp_async16(dst + a * kAtomB + i * 2048, src[i] + (bytes[i] ? part * 256 + a * 128 : 0), bytes[i]);
+          if (++duo == C::DUOS) {
+            duo = 0;
+            duo_ph ^= 1;
           }
         }
         if (ok) ok = mbar_wait(bar(REMPTY + rope), uint32_t(rope_ph), &gave_up);
@@ -396,7 +410,8 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         const uint32_t dst = rope_s + rope * kRopeB + r0 * 128 + ((c ^ (r0 & 7)) << 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) cp_async16(dst + i * 2048, src[i] + (bytes[i] ? 1024 : 0), bytes[i]);
-        mbar_arrive_copies(bar(RFULL + rope));
+        mbar_arrive_copies(bar(FULL + full));
+        full = (full + 1) & 3;
         if (++rope == C::ROPES) {
           rope = 0;
           rope_ph ^= 1;
@@ -404,12 +419,12 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 4) {
+  } else if (warp == C::S_WARP) {
     // ---- S^T = K q^T: the warp runs as one, and one elected lane issues (descriptors
     // that the compiler knows to be the same in all lanes cost 1/6 of the issue
     // time: with a branch on the lane an issue took 90 to 270 clocks)
     constexpr uint32_t kS = instr_desc(C::BF16, kTileTok, NH, false, false);
-    int quad = 0, quad_ph = 0, rope = 0, rope_ph = 0, piece = 0;
+    int duo = 0, rope = 0, piece = 0;
     uint32_t tiles = 0;
     bool ok = true;
     while (ok && pc.next(p)) {
@@ -419,50 +434,35 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         const uint32_t buf = tiles & 1u, s_at = tmem_sc + buf * NH;
         // the softmax two tiles back has read this buffer
         if (tiles >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar(PFULL + buf), ((tiles - 2) >> 1) & 1u, &gave_up));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(FULL + quad), uint32_t(quad_ph), &gave_up));
-          if (!ok) break;
-          proxy_fence();
-          tc_fence_after();
-          const uint32_t a = __shfl_sync(0xffffffffu, quad_s + quad * kQuadB, 0);
-          if (elect_one()) {
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              tc_mma(s_at, smem_desc(a + (x >> 2) * kAtomB + (x & 3) * 32, 16, 1024),
-                     smem_desc(q_s + (4 * half + (x >> 2)) * (NH * 128) + (x & 3) * 32, 16, 1024), kS, half + x > 0);
-          }
-          __syncwarp();
-          if (++quad == C::QUADS) {
-            quad = 0;
-            quad_ph ^= 1;
-          }
-        }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(RFULL + rope), uint32_t(rope_ph), &gave_up));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(FULL + (tiles & 3u)), (tiles >> 2) & 1u, &gave_up));
         if (!ok) break;
+        uint32_t a[4];
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          a[part] = __shfl_sync(0xffffffffu, duo_s + duo * kDuoB, 0);
+          if (++duo == C::DUOS) duo = 0;
+        }
+        const uint32_t ra = __shfl_sync(0xffffffffu, rope_s + rope * kRopeB, 0);
+        if (++rope == C::ROPES) rope = 0;
         proxy_fence();
         tc_fence_after();
-        const uint32_t ra = __shfl_sync(0xffffffffu, rope_s + rope * kRopeB, 0);
         if (elect_one()) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            tc_mma(s_at, smem_desc(ra + x * 32, 16, 1024), smem_desc(q_s + 8 * (NH * 128) + x * 32, 16, 1024), kS, true);
+          for (int x = 0; x < 36; ++x)
+            tc_mma(s_at, smem_desc((x < 32 ? a[x >> 3] + ((x >> 2) & 1) * kAtomB : ra) + (x & 3) * 32, 16, 1024),
+                   smem_desc(q_s + (x >> 2) * (NH * 128) + (x & 3) * 32, 16, 1024), kS, x > 0);
           if (tile == pc.tiles - 1) tc_commit(bar(QEMPTY));
           tc_commit(bar(SFULL + buf));
         }
         __syncwarp();
-        if (++rope == C::ROPES) {
-          rope = 0;
-          rope_ph ^= 1;
-        }
       }
     }
     if (elect_one()) tc_commit(bar(LAST));
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == C::O_WARP) {
     // ---- O^T += V^T P^T
     constexpr uint32_t kO = instr_desc(C::BF16, 128, NH, true, true);
-    int quad = 0, rope = 0;
+    int duo = 0, rope = 0;
     uint32_t tiles = 0;
     bool ok = true;
     while (ok && pc.next(p)) {
@@ -472,46 +472,50 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         if (!ok) break;
         tc_fence_after();
         const uint32_t pb = __shfl_sync(0xffffffffu, rope_s + rope * kRopeB, 0);
+        uint32_t a[4], done[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t a = __shfl_sync(0xffffffffu, quad_s + quad * kQuadB, 0);
-          if (elect_one()) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              tc_mma(tmem_o + (2 * half + (x >> 2)) * NH,
-                     smem_desc(a + (x >> 2) * 2 * kAtomB + (x & 3) * 2048, kAtomB, 1024),
-                     smem_desc(pb + (x & 3) * 2048, 1024, 1024), kO, tile > 0 || (x & 3) > 0);
-            tc_commit(bar(EMPTY + quad));
-            if (half == 1) {
-              tc_commit(bar(REMPTY + rope));
-              tc_commit(bar(PVDONE + buf));
-            }
-          }
-          __syncwarp();
-          if (++quad == C::QUADS) quad = 0;
+        for (int part = 0; part < 4; ++part) {
+          a[part] = __shfl_sync(0xffffffffu, duo_s + duo * kDuoB, 0);
+          done[part] = __shfl_sync(0xffffffffu, bar(EMPTY + duo), 0);
+          if (++duo == C::DUOS) duo = 0;
         }
+        const uint32_t rope_done = __shfl_sync(0xffffffffu, bar(REMPTY + rope), 0);
         if (++rope == C::ROPES) rope = 0;
+        if (elect_one()) {
+#pragma unroll
+          for (int part = 0; part < 4; ++part) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              tc_mma(tmem_o + part * NH, smem_desc(a[part] + x * 2048, kAtomB, 1024),
+                     smem_desc(pb + x * 2048, 1024, 1024), kO, tile > 0 || x > 0);
+            tc_commit(done[part]);
+          }
+          tc_commit(rope_done);
+          tc_commit(bar(PVDONE + buf));
+        }
+        __syncwarp();
       }
     }
     if (elect_one()) tc_commit(bar(LAST));
     __syncwarp();
   } else {
     // ---- softmax: token rows warp * 16 + g and + 8, heads 8 n + 2 c and + 1
-    const uint32_t lanes = uint32_t(warp) << 21;  // this warp's 32 lanes of tensor memory
-    const int g = lane >> 2, c = lane & 3, row0 = warp * 16 + g;
+    const int set = warp >> 2, st = tid & 127, col0 = set * NS;   // this set and its first head
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const int g = lane >> 2, c = lane & 3, row0 = (warp & 3) * 16 + g;
     uint32_t tiles = 0, rope = 0;
     bool fail = false;
     while (!fail && pc.next(p)) {
       const int b = pc.seq();
-      float l[NH / 4];                            // sums of heads 8 (j / 2) + 2 c + j % 2
+      float l[NS / 4];                            // sums of heads 8 (j / 2) + 2 c + j % 2
 #pragma unroll
-      for (int j = 0; j < NH / 4; ++j) l[j] = 0.f;
-      if (tid < NH) {
-        m_s[tid] = -INFINITY;
-        mu_s[tid] = 0.f;
+      for (int j = 0; j < NS / 4; ++j) l[j] = 0.f;
+      if (st < NS) {
+        m_s[col0 + st] = -INFINITY;
+        mu_s[col0 + st] = 0.f;
       }
       bool unset = true;                          // a head has no maximum yet
-      softmax_sync();
+      set_sync(set);
       for (int tile = 0; tile < pc.tiles; ++tile, ++tiles) {
         const uint32_t buf = tiles & 1u;
         bool in[2], present[2];
@@ -526,14 +530,14 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         // O of two tiles back (long done), so that the waits for it below see each phase
         if (!fail && tiles >= 2) fail = !mbar_wait(bar(PVDONE + buf), ((tiles - 2) >> 1) & 1u, &gave_up);
         tc_fence_after();
-        float e[NH / 2];                          // scores less the running maxima, in log2: [4 n + 2 x + i]
+        float e[NS / 2];                          // scores less the running maxima, in log2: [4 n + 2 x + i]
 #pragma unroll
-        for (int j = 0; j < NH; j += 16) tc_ld_16x16(tmem_sc + buf * NH + lanes + j, e + j / 2);
+        for (int j = 0; j < NS; j += 16) tc_ld_16x16(tmem_sc + buf * NH + lanes + col0 + j, e + j / 2);
         tc_wait_ld();
         float over = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NH / 8; ++n) {
-          const float2 mu = *reinterpret_cast<const float2 *>(&mu_s[8 * n + 2 * c]);
+        for (int n = 0; n < NS / 8; ++n) {
+          const float2 mu = *reinterpret_cast<const float2 *>(&mu_s[col0 + 8 * n + 2 * c]);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float *v = e + 4 * n + 2 * x;
@@ -545,56 +549,58 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         if (p.weights) {
           float *d = p.scores + (int64_t(b) * p.Hq + h0) * p.score_row + pc.t_lo + tile * kTileTok + row0;
 #pragma unroll
-          for (int n = 0; n < NH / 8; ++n)
+          for (int n = 0; n < NS / 8; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int h = 8 * n + 2 * c + i;
+              const int h = col0 + 8 * n + 2 * c + i;
 #pragma unroll
               for (int x = 0; x < 2; ++x)
                 if (h < heads && in[x]) __stcg(d + h * p.score_row + 8 * x, e[4 * n + 2 * x + i] + mu_s[h]);
             }
         }
-        if (softmax_any(unset || over > C::RAISE || fail)) {
+        if (set_any(set, unset || over > C::RAISE || fail)) {
           // raise the maxima (all threads take this path, or none), once the
           // product with V of the piece's tile before has ended
           if (!fail && tile > 0) fail = !mbar_wait(bar(PVDONE + (buf ^ 1u)), ((tiles - 1) >> 1) & 1u, &gave_up);
-          fail = softmax_any(fail);
+          fail = set_any(set, fail);
           if (fail) break;
           tc_fence_after();
-          float v[NH / 4];
+          float v[NS / 4];
 #pragma unroll
-          for (int j = 0; j < NH / 4; ++j)
+          for (int j = 0; j < NS / 4; ++j)
             v[j] = fmaxf(e[4 * (j >> 1) + (j & 1)], e[4 * (j >> 1) + 2 + (j & 1)]);
-          reduce_columns<NH, true>(v, lane, red[warp]);
-          softmax_sync();
+          reduce_columns<NS, true>(v, lane, red[warp & 3] + col0);
+          set_sync(set);
           float now = 0.f;
-          if (tid < NH) {
-            const float mu = mu_s[tid], old = m_s[tid];
-            const float top = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid])) + mu;
+          if (st < NS) {
+            const int h = col0 + st;
+            const float mu = mu_s[h], old = m_s[h];
+            const float top = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h])) + mu;
             now = fmaxf(old, top);
-            f_s[tid] = old == -INFINITY ? 0.f : exp2_fast(old - now);
-            m_s[tid] = now;
+            f_s[h] = old == -INFINITY ? 0.f : exp2_fast(old - now);
+            m_s[h] = now;
             const float use = now == -INFINITY ? 0.f : now;
-            d_s[tid] = mu - use;
-            mu_s[tid] = use;
+            d_s[h] = mu - use;
+            mu_s[h] = use;
           }
-          unset = softmax_any(now == -INFINITY);
+          unset = set_any(set, now == -INFINITY);
 #pragma unroll
-          for (int j = 0; j < NH / 4; ++j) {
-            const int h = 8 * (j >> 1) + 2 * c + (j & 1);
+          for (int j = 0; j < NS / 4; ++j) {
+            const int h = col0 + 8 * (j >> 1) + 2 * c + (j & 1);
             l[j] *= f_s[h];
             e[4 * (j >> 1) + (j & 1)] += d_s[h];
             e[4 * (j >> 1) + 2 + (j & 1)] += d_s[h];
           }
           if (tile > 0) {
 #pragma unroll 1
-            for (int j = 0; j < 4 * NH; j += 16) {
+            for (int j = 0; j < 4 * NS; j += 16) {
+              const uint32_t at = tmem_o + lanes + (j / NS) * NH + col0 + j % NS;
               float o[16];
-              tc_ld16(tmem_o + lanes + j, o);
+              tc_ld16(at, o);
               tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f_s[(j + i) % NH];
-              tc_st16(tmem_o + lanes + j, o);
+              for (int i = 0; i < 16; ++i) o[i] *= f_s[col0 + j % NS + i];
+              tc_st16(at, o);
             }
             tc_wait_st();
           }
@@ -603,12 +609,12 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         // bits), over the rope block: a row of heads per token
         unsigned char *prow = rope_p + rope * kRopeB + row0 * 128 + c * 4;
 #pragma unroll
-        for (int n = 0; n < NH / 8; ++n) {
+        for (int n = 0; n < NS / 8; ++n) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) e[4 * n + i] = exp2_fast(e[4 * n + i]);
           l[2 * n] += e[4 * n] + e[4 * n + 2];
           l[2 * n + 1] += e[4 * n + 1] + e[4 * n + 3];
-          const int at = (n ^ (row0 & 7)) << 4;   // rows 8 apart share it
+          const int at = ((col0 / 8 + n) ^ (row0 & 7)) << 4;   // rows 8 apart share it
           *reinterpret_cast<uint32_t *>(prow + at) = pack2<C::BF16>(e[4 * n], e[4 * n + 1]);
           *reinterpret_cast<uint32_t *>(prow + at + 1024) = pack2<C::BF16>(e[4 * n + 2], e[4 * n + 3]);
         }
@@ -619,21 +625,22 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
       }
       if (fail) break;
       // ---- the piece's end
-      reduce_columns<NH, false>(l, lane, red[warp]);
+      reduce_columns<NS, false>(l, lane, red[warp & 3] + col0);
       fail = !mbar_wait(bar(PVDONE + ((tiles - 1) & 1u)), ((tiles - 1) >> 1) & 1u, &gave_up);
       tc_fence_after();
-      fail = softmax_any(fail);
+      fail = set_any(set, fail);
       if (fail) break;
       const bool whole = pc.begins && pc.ends;
       float *part = p.cta_parts + (int64_t(blockIdx.x) * 2 + (pc.begins ? 1 : 0)) * C::PIECE;
-      if (tid < NH) {
-        const float sum = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
-        f_s[tid] = !whole ? 1.f : sum == 0.f ? 0.f : p.v_scale / sum;
+      if (st < NS) {
+        const int h = col0 + st;
+        const float sum = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
+        f_s[h] = !whole ? 1.f : sum == 0.f ? 0.f : p.v_scale / sum;
         if (whole) {
-          if (tid < heads) store_lse(p, b, h0 + tid, m_s[tid], sum);
+          if (h < heads) store_lse(p, b, h0 + h, m_s[h], sum);
         } else {
-          part[NH * kLatDv + tid] = m_s[tid];
-          part[NH * kLatDv + NH + tid] = sum;
+          part[NH * kLatDv + h] = m_s[h];
+          part[NH * kLatDv + NH + h] = sum;
         }
       }
       if (tid == 0 && qb == 0 && pc.begins) {
@@ -645,31 +652,40 @@ __global__ void __launch_bounds__(kLatThreads, 1) decode_latent_kernel(const __g
         const int last = int(((first + n) * groups - 1) / total);
         p.seq_pieces[b] = make_int2(group, whole ? 1 : last - group + 1);
       }
-      softmax_sync();
+      set_sync(set);
+      // a thread has one element of the head for 16 heads; neighbours exchange halves,
+      // so that it has two for 8: even lanes the even heads, odd lanes the odd ones
+      const int odd = lane & 1;
+      char *const out = static_cast<char *>(p.out) + 2 * (int64_t(b) * p.o_sb + int64_t(h0 + odd) * p.o_sh);
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk)
 #pragma unroll 1
-        for (int j = 0; j < NH; j += 16) {
+        for (int j = 0; j < NS; j += 16) {
           float o[16];
-          tc_ld16(tmem_o + lanes + blk * NH + j, o);
+          tc_ld16(tmem_o + lanes + blk * NH + col0 + j, o);
           tc_wait_ld();
-          const int d = blk * 128 + tid;
+          const int d = (blk * 128 + st) & ~1;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (j + i >= heads) continue;
-            if (whole)
-              store_out(p, b, h0 + j + i, d, o[i] * f_s[j + i]);
-            else
-              part[(j + i) * kLatDv + d] = o[i];
+          for (int i = 0; i < 16; i += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 1], 1);
+            const int h = col0 + j + i;           // the pair's even head
+            const float x = odd ? got : o[i], y = odd ? o[i + 1] : got;
+            if (h + odd >= heads) continue;
+            if (whole) {
+              const float f = f_s[h + odd];
+              *reinterpret_cast<uint32_t *>(out + 2 * (h * p.o_sh + d)) = pack2<C::BF16>(x * f, y * f);
+            } else {
+              *reinterpret_cast<float2 *>(part + (h + odd) * kLatDv + d) = make_float2(x, y);
+            }
           }
         }
       tc_fence_before();
-      softmax_sync();                             // m_s, f_s, red are free
+      set_sync(set);                             // m_s, f_s, red are free
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == C::S_WARP) {
     // nothing is in flight when the tensor memory is given back
     mbar_wait(bar(LAST), 0, &gave_up);
     __syncwarp();
@@ -733,7 +749,7 @@ int launch_lat(const DecodeParams &p, int device, cudaStream_t st) {
     if (e != cudaSuccess) return int(e);
     if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
   }
-  const int e = launch_dependent(decode_latent_kernel<C>, dim3(unsigned(kDecodeCtas / p.QB * p.QB)), kLatThreads, st, p,
+  const int e = launch_dependent(decode_latent_kernel<C>, dim3(unsigned(kDecodeCtas / p.QB * p.QB)), C::THREADS, st, p,
                                  C::SMEM);
   if (e) return e;
   return launch_dependent(latent_join_kernel<NH>, dim3(unsigned(p.B) * unsigned(p.Hq)), kJoinThreads, st, p);
