@@ -373,9 +373,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
         }
         return page;
       };
-      int pages[4], places[4];
+      // page numbers are read two tiles ahead, and a tile's rows brought to the L2 cache
+      // one tile ahead: shared memory holds two tiles and a bit, which is less than
+      // HBM's latency times an SM's share of its bandwidth
+      int pages[4], places[4], next_pages[4], next_places[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pages[i] = page_at(pc.t_lo + i * 16 + r0, &places[i]);
+      for (int i = 0; i < 4; ++i) {
+        pages[i] = page_at(pc.t_lo + i * 16 + r0, &places[i]);
+        next_pages[i] = page_at(pc.t_lo + kTileTok + i * 16 + r0, &next_places[i]);
+      }
       for (int tile = 0; ok && tile < pc.tiles; ++tile) {
         const int t0 = pc.t_lo + tile * kTileTok;
         const char *src[4];
@@ -387,9 +393,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
           bytes[i] = have ? 16 : 0;
           src[i] = kp + (have ? (int64_t(pages[i]) * p.P + (t - places[i] * p.P)) * (kLatD * 2) + c * 16 : 0);
         }
-        // the pages of the next tile, before the waits below
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pages[i] = page_at(t0 + kTileTok + i * 16 + r0, &places[i]);
+        for (int i = 0; i < 4; ++i) {
+          pages[i] = next_pages[i];
+          places[i] = next_places[i];
+          if (page_present(pages[i], p.num_pages)) {
+            const int t = t0 + kTileTok + i * 16 + r0;
+            const char *row = kp + (int64_t(pages[i]) * p.P + (t - places[i] * p.P)) * (kLatD * 2);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c * 128));
+            if (c == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 1024));
+          }
+          next_pages[i] = page_at(t0 + 2 * kTileTok + i * 16 + r0, &next_places[i]);
+        }
 #pragma unroll
         for (int part = 0; part < 4; ++part) {
           if (ok) ok = mbar_wait(bar(EMPTY + duo), uint32_t(duo_ph), &gave_up);
