@@ -50,7 +50,6 @@ constexpr int kTileTok = 64, kStrip = 32;
 constexpr int kAtomB = kTileTok * 128;            // 64 elements of a tile's tokens
 constexpr int kDuoB = 2 * kAtomB;                 // 128 elements
 constexpr int kRopeB = kAtomB;                    // the last 64 elements
-constexpr int kJoinThreads = 128;
 
 template <int NH_, bool BF16_>
 struct LatConfig {
@@ -314,8 +313,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // with fewer strips than groups, only as many groups take part
-  const long long groups = min((long long)(gridDim.x / unsigned(p.QB)), total);
+  // with few strips, only as many groups take part as have a tile (two strips) each
+  const long long groups = min((long long)(gridDim.x / unsigned(p.QB)), (total + 1) / 2);
   const int group = int(blockIdx.x) / p.QB, qb = int(blockIdx.x) - group * p.QB;
   if (group >= groups) return;
   const int h0 = qb * NH, heads = min(NH, p.Hq - h0);
@@ -356,12 +355,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
       const int b = pc.seq();
       if (piece > 0) ok = mbar_wait(bar(QEMPTY), uint32_t(piece - 1) & 1u, &gave_up);
       if (!ok) break;
-      for (int i = 0; i < 9 * NH / 16; ++i) {
-        const int row = i * 16 + r0, blk = row / NH, r = row - blk * NH;
+#pragma unroll
+      for (int x = 0; x < NH / 16; ++x) {
+        const int r = x * 16 + r0;
         const bool have = r < heads;
-        const int64_t at = have ? 2 * (int64_t(b) * p.q_sb + int64_t(h0 + r) * p.q_sh) + blk * 128 + c * 16 : 0;
-        cp_async16(q_s + blk * (NH * 128) + r * 128 + ((c ^ (r & 7)) << 4), static_cast<const char *>(p.q) + at,
-                   have ? 16 : 0);
+        const char *src = static_cast<const char *>(p.q) +
+                          (have ? 2 * (int64_t(b) * p.q_sb + int64_t(h0 + r) * p.q_sh) + c * 16 : 0);
+        const uint32_t dst = q_s + r * 128 + ((c ^ (r & 7)) << 4);
+#pragma unroll
+        for (int blk = 0; blk < 9; ++blk)
+          cp_async16(dst + blk * (NH * 128), src + (have ? blk * 128 : 0), have ? 16 : 0);
       }
       mbar_arrive_copies(bar(QFULL));
       ++piece;
@@ -671,29 +674,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
       // a thread has one element of the head for 16 heads; neighbours exchange halves,
       // so that it has two for 8: even lanes the even heads, odd lanes the odd ones
       const int odd = lane & 1;
-      char *const out = static_cast<char *>(p.out) + 2 * (int64_t(b) * p.o_sb + int64_t(h0 + odd) * p.o_sh);
+      const int64_t step = whole ? 4 * p.o_sh : 8 * kLatDv;      // bytes, two heads on
+      const int size = whole ? 4 : 8;                            // bytes of two elements
 #pragma unroll 1
-      for (int blk = 0; blk < 4; ++blk)
+      for (int j = 0; j < NS; j += 16) {
+        const int h_even = col0 + j + odd;        // this lane's first head
+        char *const row = whole ? static_cast<char *>(p.out) + 2 * (int64_t(b) * p.o_sb + int64_t(h0 + h_even) * p.o_sh)
+                                : reinterpret_cast<char *>(part + h_even * kLatDv);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f_s[h_even + 2 * i];
 #pragma unroll 1
-        for (int j = 0; j < NS; j += 16) {
+        for (int blk = 0; blk < 4; ++blk) {
           float o[16];
           tc_ld16(tmem_o + lanes + blk * NH + col0 + j, o);
           tc_wait_ld();
-          const int d = (blk * 128 + st) & ~1;
+          float2 v[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 1], 1);
-            const int h = col0 + j + i;           // the pair's even head
-            const float x = odd ? got : o[i], y = odd ? o[i + 1] : got;
-            if (h + odd >= heads) continue;
-            if (whole) {
-              const float f = f_s[h + odd];
-              *reinterpret_cast<uint32_t *>(out + 2 * (h * p.o_sh + d)) = pack2<C::BF16>(x * f, y * f);
-            } else {
-              *reinterpret_cast<float2 *>(part + (h + odd) * kLatDv + d) = make_float2(x, y);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? o[2 * i] : o[2 * i + 1], 1);
+            v[i] = odd ? make_float2(got, o[2 * i + 1]) : make_float2(o[2 * i], got);
+          }
+          char *at = row + ((blk * 128 + st) >> 1) * size;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i, at += step)
+              if (h_even + 2 * i < heads) *reinterpret_cast<uint32_t *>(at) = pack2<C::BF16>(v[i].x * f[i], v[i].y * f[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i, at += step)
+              if (h_even + 2 * i < heads) *reinterpret_cast<float2 *>(at) = v[i];
           }
         }
+      }
       tc_fence_before();
       set_sync(set);                             // m_s, f_s, red are free
     }
@@ -710,45 +723,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
   if (tid == 0 && gave_up) p.counters[kDecodeCtas] = 1u;
 }
 
-// Adds the pieces of a sequence that several groups of CTAs share; one block
-// per sequence and head, a thread for 4 elements.
-template <int NH>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ DecodeParams p) {
+// Adds the pieces of a sequence that several groups of CTAs share; a block per
+// sequence and head, 128 threads with 4 elements each for every PARTS-th piece.
+template <int NH, int PARTS>
+__global__ void __launch_bounds__(128 * PARTS) latent_join_kernel(const __grid_constant__ DecodeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int PIECE = NH * kLatDv + 2 * NH;
+  __shared__ float4 acc_s[PARTS][128];
+  __shared__ float m_s[PARTS], l_s[PARTS];
   const int b = int(blockIdx.x) / p.Hq, h = int(blockIdx.x) - b * p.Hq;
   const int2 at = __ldcg(p.seq_pieces + b);
   if (at.y < 2) return;
-  const int qb = h / NH, r = h - qb * NH, tid = int(threadIdx.x);
+  const int qb = h / NH, r = h - qb * NH, tid = int(threadIdx.x) & 127, part = int(threadIdx.x) >> 7;
   auto slot = [&](int x) { return p.cta_parts + (int64_t((at.x + x) * p.QB + qb) * 2 + (x == 0 ? 1 : 0)) * PIECE; };
   float m = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int x0 = 0; x0 < at.y; x0 += 4) {          // 4 pieces on their way at a time
+  auto add = [&](float mx, float lx, float4 v) {
+    const float now = fmaxf(m, mx);
+    const float was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = mx == -INFINITY ? 0.f : exp2_fast(mx - now);
+    acc.x = acc.x * was + f * v.x;
+    acc.y = acc.y * was + f * v.y;
+    acc.z = acc.z * was + f * v.z;
+    acc.w = acc.w * was + f * v.w;
+    sum = sum * was + f * lx;
+    m = now;
+  };
+  for (int x0 = part; x0 < at.y; x0 += 4 * PARTS) {           // 4 pieces on their way at a time
     float4 v[4];
     float mx[4], lx[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const float *s = slot(min(x0 + x, at.y - 1));
+      if (x0 + x * PARTS >= at.y) break;
+      const float *s = slot(x0 + x * PARTS);
       v[x] = __ldcg(reinterpret_cast<const float4 *>(s + r * kLatDv) + tid);
       mx[x] = __ldcg(s + NH * kLatDv + r);
       lx[x] = __ldcg(s + NH * kLatDv + NH + r);
     }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      if (x0 + x >= at.y) break;
-      const float now = fmaxf(m, mx[x]);
-      const float was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = mx[x] == -INFINITY ? 0.f : exp2_fast(mx[x] - now);
-      acc.x = acc.x * was + f * v[x].x;
-      acc.y = acc.y * was + f * v[x].y;
-      acc.z = acc.z * was + f * v[x].z;
-      acc.w = acc.w * was + f * v[x].w;
-      sum = sum * was + f * lx[x];
-      m = now;
+      if (x0 + x * PARTS >= at.y) break;
+      add(mx[x], lx[x], v[x]);
     }
   }
-  const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
-  store_out4(p, b, h, tid * 4, acc, inv);
+  if constexpr (PARTS > 1) {
+    acc_s[part][tid] = acc;
+    if (tid == 0) m_s[part] = m, l_s[part] = sum;
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int x = 1; x < PARTS; ++x) add(m_s[x], l_s[x], acc_s[x][tid]);
+  }
+  store_out4(p, b, h, tid * 4, acc, sum == 0.f ? 0.f : p.v_scale / sum);
   if (tid == 0) store_lse(p, b, h, m, sum);
 }
 
@@ -767,7 +793,10 @@ int launch_lat(const DecodeParams &p, int device, cudaStream_t st) {
   const int e = launch_dependent(decode_latent_kernel<C>, dim3(unsigned(kDecodeCtas / p.QB * p.QB)), C::THREADS, st, p,
                                  C::SMEM);
   if (e) return e;
-  return launch_dependent(latent_join_kernel<NH>, dim3(unsigned(p.B) * unsigned(p.Hq)), kJoinThreads, st, p);
+  // few rows are cut into many pieces each: four at a time then
+  const unsigned rows = unsigned(p.B) * unsigned(p.Hq);
+  return rows < 1024 ? launch_dependent(latent_join_kernel<NH, 4>, dim3(rows), 512, st, p)
+                     : launch_dependent(latent_join_kernel<NH, 1>, dim3(rows), 128, st, p);
 }
 
 }  // namespace
