@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t rotation8(const AppendParams &p, const float
 // the two coefficients are worked out once per token and kind, and an element costs
 // a multiply, a multiply-add, a multiply and its share of the sum of squares, all of
 // them on pairs (fma.rn.f32x2).  Against the general kernel below: a prefill chunk of
-// 8,191 tokens of 48 heads of 128 takes 47 us instead of 61.
+// 8,191 tokens of 48 heads of 128 takes 45 us instead of 61.
 enum : int { kSelf = 0, kAcross = 1, kInside = 2 };   // where partners are: ITERS / 2 vectors
                                                       // on, 4 lanes on, in the vector itself
 
@@ -143,6 +143,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+// to two units of the last place
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 template <bool BF16>
 __device__ __forceinline__ uint64_t widen(uint32_t w) {
   if constexpr (BF16) return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -155,11 +161,11 @@ __device__ __forceinline__ uint64_t swapped(uint64_t x) {
 }
 
 template <int ITERS, bool BF16, int MODE>
-__global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 3 : 2)
+__global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 3 : 2)
     append_fast_kernel(const __grid_constant__ AppendParams p, int steps_per_task, FastDiv fd_segments) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   constexpr bool HOLD = ITERS <= 4;               // coefficients of every vector in registers
-  constexpr int AHEAD = ITERS <= 2 ? 2 : 1;       // steps on their way
+  constexpr bool EARLY = ITERS > 4;
   const int warp = int(threadIdx.x) >> 5;
   const uint32_t task = blockIdx.x * uint32_t(kAppendWarps) + uint32_t(warp);
   const uint32_t n = fast_div(task, fd_segments);
@@ -185,13 +191,13 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
     f_end = min(end, begin + (kind == 0 ? q_steps : kv_steps));
     f_left = (kind == 0 ? p.q_heads : p.kv_heads) - h;
   };
-  uint4 ahead[AHEAD][ITERS];
-  auto fetch = [&](uint4 *to) {
+  uint4 ahead[ITERS];                             // the next step's vectors, on their way
+  auto fetch = [&]() {
     if (f_s >= f_end && f_s < end) seek();
     const bool have = f_s < f_end && f_left > 0;
 #pragma unroll
     for (int it = 0; it < ITERS; ++it)
-      to[it] = have ? __ldcs(reinterpret_cast<const uint4 *>(f_src) + it * kLanes) : make_uint4(0, 0, 0, 0);
+      ahead[it] = have ? __ldcs(reinterpret_cast<const uint4 *>(f_src) + it * kLanes) : make_uint4(0, 0, 0, 0);
     ++f_s;
     f_left -= kGroups;
     f_src += f_step;
@@ -199,8 +205,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
   int64_t pos = 0, slot = -1;
   if (p.kv_heads > 0) slot = p.slots[n];
   if (p.rot > 0) pos = p.positions[n];
-#pragma unroll
-  for (int a = 0; a < AHEAD; ++a) fetch(ahead[a]);
+  fetch();
   if (p.rot > 0 && (pos < 0 || pos >= p.cos_sin_rows)) return;   // the whole warp
   const bool store_kv = slot >= 0 && slot < p.num_slots;
   const float *row = p.cos_sin + pos * p.rot;
@@ -211,6 +216,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
   uint4 wp[HOLD ? 1 : ITERS];                     // not held: the weights as they come
   float cs1[HOLD ? 1 : 8], sn1[HOLD ? 1 : 8];     // and the rotation of the one vector it turns
   int kind = 0, m = 0, s_end = 0, left = 0;       // the current kind, where it ends, heads from this one on
+  float inv_m = 0.f;
   char *dst = nullptr;
   int64_t dst_step = 0;
   auto turned = [&](int it) {                     // whether vector `it` is rotated (the same in all lanes)
@@ -218,6 +224,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
   };
   auto prepare = [&](int kind) {
     m = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : 0;
+    inv_m = m > 0 ? 1.f / float(m) : 0.f;
     const uint4 *w = static_cast<const uint4 *>(kind == 0 ? p.q_weight : p.k_weight);
     if constexpr (HOLD) {
 #pragma unroll
@@ -254,14 +261,15 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
 
 #pragma unroll 1
   for (int s = first; s < end; ++s) {
-    uint4 raw[ITERS];
+    // long heads: the next step is fetched at once, into registers of its own (40
+    // against 45 us for the latent prefill); short ones do without the copies
+    uint4 now[EARLY ? ITERS : 1];
+    if constexpr (EARLY) {
 #pragma unroll
-    for (int it = 0; it < ITERS; ++it) raw[it] = ahead[0][it];
-#pragma unroll
-    for (int a = 0; a + 1 < AHEAD; ++a)
-#pragma unroll
-      for (int it = 0; it < ITERS; ++it) ahead[a][it] = ahead[a + 1][it];
-    fetch(ahead[AHEAD - 1]);
+      for (int it = 0; it < ITERS; ++it) now[it] = ahead[it];
+      fetch();
+    }
+    const uint4 *const raw = EARLY ? now : ahead;
     if (s >= s_end) {                             // on to the next kind: its coefficients and places
       kind = s < q_steps ? 0 : s < q_steps + kv_steps ? 1 : 2;
       const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
       const int64_t at = kind == 0 ? int64_t(n) * p.o_st + h * sh : slot * p.row + h * sh;
       dst = static_cast<char *>(kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + at * (vec / 8) + lane * vec;
       dst_step = kGroups * sh * (vec / 8);
-      prepare(kind);
+      if (kind != 2 || p.e4m3) prepare(kind);
     }
     const bool live = left > 0;
     char *const to = dst;
@@ -283,15 +291,21 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
 #pragma unroll
       for (int it = 0; it < ITERS; ++it)
         if (live) reinterpret_cast<uint4 *>(to)[it * kLanes] = raw[it];
+      if constexpr (!EARLY) fetch();
       continue;
     }
     uint64_t v[ITERS][4];
+    uint32_t across[HOLD && MODE == kAcross ? ITERS : 1][4];      // the partners, as they come
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) {
       const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[it][i] = widen<BF16>(w[i]);
+      for (int i = 0; i < 4; ++i) {
+        v[it][i] = widen<BF16>(w[i]);
+        if constexpr (HOLD && MODE == kAcross) across[it][i] = __shfl_xor_sync(0xffffffffu, w[i], 4);
+      }
     }
+    if constexpr (!EARLY) fetch();
     float r = 1.f;
     if (m > 0) {
       uint64_t sq = 0;
@@ -305,7 +319,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
       float sum = f.x + f.y;
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = rsqrtf(__fdividef(sum, float(m)) + p.eps);
+      r = rsqrt_fast(fmaf(sum, inv_m, p.eps));
     }
     float out[ITERS][8];
 #pragma unroll
@@ -331,11 +345,10 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 4 : ITERS == 4 ? 
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[i] = swapped(HOLD ? v[it][i] : x[i]);
         } else {
-          const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if constexpr (HOLD) {
-              z[i] = widen<BF16>(__shfl_xor_sync(0xffffffffu, w[i], 4));
+              z[i] = widen<BF16>(across[it][i]);
             } else {
               const float2 f = unpair(x[i]);
               z[i] = pair(__shfl_xor_sync(0xffffffffu, f.x, 4), __shfl_xor_sync(0xffffffffu, f.y, 4));
