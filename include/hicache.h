@@ -723,6 +723,12 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
  * passes weights), on the current device. */
 int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32_t q_heads, int32_t head_dim,
                              int32_t v_dim, int32_t max_pages, int32_t with_weights, int64_t *bytes);
+/* Whether a call with this workspace has given up: the kernel over a latent cache
+ * waits for its own copies and products with a limit of about two seconds, and a
+ * wait that runs out (it never should) ends the call with its outputs undefined
+ * and marks the workspace, *gave_up = 1 until `clear`.  Reads device memory
+ * synchronously.  Errors: INVALID_ARG, CUDA. */
+int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
 
 /* Which pages of each sequence leave L1: those that received the least
  * attention.  With n = ceil(seq_lens[b] / page_size) pages, the pages in [sink,

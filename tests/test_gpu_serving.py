@@ -45,6 +45,15 @@ APPEND = [
     (3, 128, 1, 576, 64, "fp16", False, 576, 512, 64, 512, True, True),
     (11, 2, 1, 768, 4, "bf16", False, 768, 768, 768, 0, False, True),
     (1000, 14, 2, 128, 16, "fp16", False, 128, 128, 64, 64, False, False),
+    (9, 4, 2, 128, 16, "bf16", True, 128, 128, 128, 0, True, False),
+    (9, 5, 2, 256, 16, "fp16", False, 0, 256, 64, 192, True, False),
+    (10, 6, 2, 256, 16, "bf16", False, 256, 64, 64, 64, False, False),
+    (5, 3, 1, 64, 8, "fp16", True, 64, 0, 64, 0, True, False),
+    (5, 2, 1, 64, 8, "bf16", False, 64, 64, 6, 2, False, False),
+    (13, 9, 1, 128, 4, "bf16", False, 64, 128, 64, 0, False, False),
+    (13, 2, 1, 128, 4, "fp16", False, 8, 120, 128, 0, False, False),
+    (4000, 1, 1, 64, 4, "bf16", False, 64, 64, 0, 0, False, False),
+    (6, 3, 1, 384, 4, "fp16", False, 384, 384, 384, 0, False, True),
 ]
 
 
@@ -114,6 +123,21 @@ def test_append(c):
     hc.append_kv(kv, dd, 0, q, None, None, None, positions=pos if cs is not None else None, cos_sin=cs,
                  rot_offset=c[10], interleaved=c[11], q_weight=qw)
     assert torch.equal(raw(q), raw(keep))
+
+
+def test_append_tables_at_any_row():
+    """A table that starts between 16-byte boundaries, and token rows that are not
+    next to one another."""
+    c = (31, 4, 2, 128, 8, "bf16", False, 128, 128, 126, 2, False, False)
+    q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, 6)
+    wide = torch.zeros((5001, 126), device="cuda")
+    wide[1:] = cs
+    wide[0] = float("nan")
+    old = [b.clone() for b in bufs]
+    q_out = torch.zeros((31, 4, 128), dtype=q.dtype, device="cuda")
+    hc.append_kv(hc.DeviceKV(bufs, pages), desc(8, 256, 2), 0, q, k, v, slots, q_out=q_out, positions=pos,
+                 cos_sin=wide[1:], rot_offset=2, q_weight=qw, k_weight=kw)
+    check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, 1.0, 1.0)
 
 
 def test_append_skips_rows():
@@ -255,6 +279,21 @@ def test_decode(c):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_decode_latent(c, dtype):
     run_decode(c[0], c[1], 1, 576, c[2], dtype, latent=True, scale=192 ** -0.5)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_many_sequences(latent):
+    """More sequences than a CTA has threads, most of them short or empty."""
+    lens = [(7 * i) % 41 if i % 5 else 0 for i in range(700)]
+    lens[333] = 900
+    run_decode(lens, 4, 2, 576 if latent else 64, 16, "bf16", latent=latent)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("n", [16, 17, 100, 2400, 4864, 4880, 20000])
+def test_decode_one_sequence(latent, n):
+    """One sequence dealt to ever more CTAs: fewer tiles than CTAs, as many, more."""
+    run_decode([n], 8, 1, 576 if latent else 128, 64, "fp16", latent=latent)
 
 
 @pytest.mark.parametrize("latent,e4", [(False, False), (False, True), (True, False)])
@@ -432,6 +471,55 @@ def test_decode_graphs(latent):
                 assert torch.equal(o, a) and torch.equal(w, b)
 
 
+def test_first_calls_in_a_capture():
+    """Every operator's first call in a process, captured into a graph."""
+    import subprocess
+    import sys
+    code = """
+import torch, tiered_kv_cache_gb300 as hc, test_gpu_serving as t
+c = t.APPEND[0]
+q, k, v, slots, pos, cs, qw, kw, bufs, pages = t.append_inputs(c, 3)
+s = [t.decode_inputs([300, 40], 4, 2, 128, 16), t.decode_inputs([300, 40], 4, 2, 576, 16, latent=True)]
+dv = [128, 512]
+outs = [torch.zeros((2, 4, n), dtype=x['dt'], device='cuda') for x, n in zip(s, dv)]
+ws = [t.workspace(x, 4, x['q'].shape[2], n, True) for x, n in zip(s, dv)]
+w = [torch.zeros((2, x['width']), device='cuda') for x in s]
+table = torch.arange(12, dtype=torch.int32, device='cuda').view(2, 6)
+wt = torch.rand((2, 6), device='cuda')
+lens, keep = (torch.full((2,), n, dtype=torch.int32, device='cuda') for n in (96, 3))
+vic, cnt = torch.full((2, 6), -1, dtype=torch.int32, device='cuda'), torch.zeros(2, dtype=torch.int32, device='cuda')
+ot, ow, ol = torch.zeros_like(table), torch.zeros_like(wt), torch.zeros_like(lens)
+q_out = torch.zeros_like(q)
+torch.cuda.synchronize()
+def go(stream):
+    hc.append_kv(hc.DeviceKV(bufs, pages), t.desc(64, 1024, 2), 0, q, k, v, slots, q_out=q_out, positions=pos,
+                 cos_sin=cs, q_weight=qw, k_weight=kw, stream=stream)
+    for x, o, y, z in zip(s, outs, ws, w):
+        t.plain_call(x, o, y, weights=z, decay=0.0, stream=stream)
+    hc.evict_pages(16, table, lens, wt, keep, vic, cnt, out_table=ot, out_weights=ow, out_lens=ol, stream=stream)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    go(torch.cuda.current_stream())
+everything = [q_out, *bufs, *outs, *w, vic, cnt, ot, ow, ol]
+for x in everything: x.zero_()
+g.replay()
+torch.cuda.synchronize()
+first = [x.clone() for x in everything]
+for x in everything: x.zero_()
+go(None)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, everything))
+assert outs[0].any() and outs[1].any() and cnt.tolist() == [3, 3]
+assert not any(hc.decode_gave_up(x) for x in ws)
+print('ok')
+"""
+    import os
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(here), here]))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, env=env)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
 def test_decode_random_corpus():
     """Random shapes over the documented ranges."""
     rnd = random.Random(20)
@@ -498,7 +586,8 @@ def test_evict_small_and_special(in_place):
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("n,b,kinds", [(1, 3, 2), (31, 2, 3), (1023, 2, 5), (1024, 2, 0), (1025, 3, 0), (2049, 300, 4),
-                                       (5000, 2, 0), (40000, 2, 9), (131072, 3, 0), (300001, 1, 3)])
+                                       (4096, 2, 7), (4097, 2, 7), (5000, 2, 0), (40000, 2, 9), (131072, 3, 0),
+                                       (196608, 1, 50), (196609, 1, 50), (300001, 1, 3)])
 def test_evict_sizes(n, b, kinds, in_place):
     """kinds > 0: that many different weights only, so that most are equal."""
     rng = np.random.default_rng(n + b)

@@ -194,3 +194,33 @@ def test_tensors_are_checked():
         hc._check_cache(hc.DeviceKV([small] * 4, 1), desc(), 0, 0)
     with pytest.raises(ValueError, match="contiguous"):
         hc._check_cache(hc.DeviceKV([torch.zeros((320, 512), dtype=b16)[:, ::2]] * 4, 10), desc(), 0, cpu)
+    with pytest.raises(hc.HiCacheError, match="aligned"):
+        hc.decode_gave_up(q.view(-1)[1:])
+
+
+def test_page_predicate(tmp_path):
+    """The kernels' test of a page table's entry, at and around every edge."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "p.cpp"
+    src.write_text("""
+#include <cstdio>
+#include <climits>
+#include "hicache_serving.h"
+using namespace hicache;
+int main() {
+  const long long n[] = {1, 7, INT32_MAX - 1, INT32_MAX};
+  const int e[] = {INT32_MIN, -1, 0, 1, 6, 7, 8, INT32_MAX - 2, INT32_MAX - 1, INT32_MAX};
+  for (long long k : n)
+    for (int x : e)
+      if (page_present(x, k) != ((long long)x >= 0 && (long long)x < k)) return 1;
+  for (int g = 1; g <= 40; ++g) if (decode_rows(g) != (g <= 8 ? 8 : 16)) return 2;
+  for (int h = 1; h <= 300; ++h) { const int r = latent_rows(h); if (r != 16 && r != 32 && r != 64) return 3; if (h <= 64 && r < h) return 4; }
+  std::puts("ok");
+}
+""")
+    exe = tmp_path / "p"
+    subprocess.check_call(["g++", "-std=c++17", f"-I{root}/tiered_kv_cache_gb300/csrc", f"-I{root}/include",
+                           "-I/usr/local/cuda/include", str(src), "-o", str(exe)])
+    assert subprocess.run([str(exe)], capture_output=True, text=True).stdout.strip() == "ok"

@@ -13,7 +13,7 @@ Names follow the C ABI in ``include/hicache.h``:
     Engine (submission engine), PageAllocator (host pages)
     host_alloc / host_free, wait, prepass, segment_count, page_span, layer_checksum
     tp_share / tp_load_pipelined / Pool.layer_counters (tensor-parallel load of a replicated latent)
-    append_kv / decode_attention / decode_workspace / evict_pages (operators on the device pages)
+    append_kv / decode_attention / decode_workspace / decode_gave_up / evict_pages (operators on the device pages)
     stream_copy (roofline probe: plain zero-copy streaming copy)
     checked_build / check_status (the bounds-checked build, HICACHE_CHECKED=1)
 """
@@ -33,7 +33,7 @@ __all__ = [
     "MAX_GROUP", "PAGE_FIRST_DIRECT_KV",
     "host_alloc", "host_free", "wait", "prepass", "segment_count", "layer_checksum", "page_span",
     "launch_count", "version", "stream_copy", "tp_share", "tp_load_pipelined", "checked_build",
-    "check_status", "append_kv", "decode_attention", "decode_workspace", "evict_pages",
+    "check_status", "append_kv", "decode_attention", "decode_workspace", "decode_gave_up", "evict_pages",
 ]
 
 LAYOUT_POOL = -1
@@ -148,6 +148,7 @@ def _bind(lib):
         "hicache_append_kv": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
         "hicache_decode_attention": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
         "hicache_decode_workspace": (ctypes.c_int, [_P(PoolDesc), _i32, _i32, _i32, _i32, _i32, _i32, _P(_i64)]),
+        "hicache_decode_status": (ctypes.c_int, [_vp, _P(_i32), _i32]),
         "hicache_evict_pages": (ctypes.c_int, [ctypes.c_char_p, _vp]),
         "hicache_layer_checksum": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _vp, _i64, _i32,
                                                   _i32, _vp, _vp]),
@@ -934,6 +935,14 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     rc = library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _stream(stream))
     if rc:
         _check(rc)
+
+
+def decode_gave_up(workspace, clear: bool = False) -> bool:
+    """Whether a call with this workspace gave up waiting (it never should): its
+    outputs are undefined then.  Synchronous."""
+    out = ctypes.c_int32()
+    _check(library().hicache_decode_status(workspace.data_ptr(), ctypes.byref(out), int(clear)))
+    return bool(out.value)
 
 
 def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, num_victims, *, sink: int = 0,

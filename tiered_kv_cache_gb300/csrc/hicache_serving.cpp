@@ -331,6 +331,18 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   return launched(e, n, "decode kernel launch");
 }
 
+int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear) {
+  clear_error();
+  if (!workspace || !gave_up) return set_error(HICACHE_ERR_INVALID_ARG, "workspace or gave_up is NULL");
+  if (!aligned(workspace, 256)) return set_error(HICACHE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  unsigned int *word = static_cast<unsigned int *>(workspace) + hicache::kDecodeCtas, x = 0;
+  cudaError_t e = cudaMemcpy(&x, word, sizeof(x), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(x));
+  if (e != cudaSuccess) return cuda_error(e, "decode status");
+  *gave_up = x != 0;
+  return HICACHE_OK;
+}
+
 int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {
   clear_error();
   if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the evict descriptor is NULL");
