@@ -156,9 +156,10 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   __shared__ __align__(16) float piece_m[C::WARPS][2][ROWS], piece_l[C::WARPS][2][ROWS];
   __shared__ int piece_b[C::WARPS][2], piece_u[C::WARPS][2], piece_state[C::WARPS][2];
   // joining CTAs' pieces: the two open units (first CTA, pieces if it falls to this
-  // CTA), factor and sum of each piece and row
+  // CTA), and what the teams of threads beside the first have
   __shared__ int join_cta[2], join_n[2];
-  __shared__ float factor[kDecodeCtas][ROWS], weight[kDecodeCtas][ROWS], row_inv[ROWS];
+  __shared__ float4 team_o[THREADS];
+  __shared__ float2 team_ml[3][ROWS];
 
   const int tid = int(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c4 = lane & 3;
@@ -654,9 +655,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   const bool open_first = starts && !chain_of(first_k, &unused);
   const bool open_last = starts && last_k != first_k && !chain_of(last_k, &unused);
   if (!open_first && !open_last) return;
-  __threadfence();
-  __syncthreads();
-  if (lane == 0 && (warp == 0 ? open_first : warp == 1 && open_last)) {
+  int c0 = 0, c1 = 0;
+  const bool counts = lane == 0 && (warp == 0 ? open_first : warp == 1 && open_last);
+  if (counts) {
     // the unit's first tile, its tiles, and the CTAs they lie in
     const int k = warp == 0 ? first_k : last_k;
     const int b = (&piece_b[0][0])[k], u = (&piece_u[0][0])[k];
@@ -669,66 +670,79 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
       first += (long long)tiles_of(start, len) * units;
     }
     first += (long long)u * nt;
-    const int c0 = int(((first + 1) * n_cta - 1) / total), c1 = int(((first + nt) * n_cta - 1) / total);
+    c0 = int(((first + 1) * n_cta - 1) / total);
+    c1 = int(((first + nt) * n_cta - 1) / total);
+  }
+  __syncthreads();                                // the CTA's parts are written
+  if (counts) {
+    __threadfence();
     const unsigned int was = atomicAdd(p.counters + c0, 1u);
     const bool last = was == unsigned(c1 - c0);
     if (last) p.counters[c0] = 0u;                // ready for the next call
+    __threadfence();
     join_cta[warp] = c0;
     join_n[warp] = last ? c1 - c0 + 1 : 0;
   }
   __syncthreads();
   for (int side = 0; side < 2; ++side) {
     if (!(side == 0 ? open_first : open_last)) continue;
-    const int np = join_n[side], c0 = join_cta[side];
+    const int np = join_n[side], from = join_cta[side];
     if (np == 0) continue;
-    __threadfence();
     const int k = side == 0 ? first_k : last_k;
     const int b = (&piece_b[0][0])[k], u = (&piece_u[0][0])[k];
     const int kvh = u / p.QB, qb = u - kvh * p.QB;
     const int hh = kvh * p.G + qb * ROWS, nr = min(ROWS, p.G - qb * ROWS);
-    // piece x of the unit: CTA c0 + x, its second slot where the unit begins.
-    // First the factors of all pieces, a warp for a row; then O, by 4 columns
-    auto slot = [&](int x) { return p.cta_parts + (int64_t(c0 + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
-    for (int r = warp; r < nr; r += C::WARPS) {
-      float mm = -INFINITY, sum = 0.f;
-      for (int x = lane; x < np; x += 32) {
-        const float mx = __ldcg(slot(x) + ROWS * DP + r);
-        weight[x][r] = __ldcg(slot(x) + ROWS * DP + ROWS + r);
-        factor[x][r] = mx;
-        mm = fmaxf(mm, mx);
-      }
-      for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-      for (int x = lane; x < np; x += 32) {
-        const float f = factor[x][r] == -INFINITY ? 0.f : exp2_fast(factor[x][r] - mm);
-        factor[x][r] = f;
-        sum += f * weight[x][r];
-      }
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) {
-        row_inv[r] = sum == 0.f ? 0.f : p.v_scale / sum;
-        store_lse(p, b, hh + r, mm, sum);
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < nr * COL4; i += THREADS) {
+    // piece x of the unit: CTA from + x, its second slot where the unit begins
+    auto slot = [&](int x) { return p.cta_parts + (int64_t(from + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
+    // a thread takes four columns of a row; with threads to spare, every `teams`-th
+    // piece of them.  Maximum, sum and O of 8 pieces are on their way together.
+    const int cols = nr * COL4, teams = max(1, min(4, THREADS / cols));
+    const int team = teams > 1 ? tid / cols : 0;
+    for (int i0 = 0; i0 < cols; i0 += THREADS) {
+      const int i = teams > 1 ? tid - team * cols : i0 + tid;
+      const bool mine = team < teams && i < cols;
       const int r = i / COL4, d = (i - r * COL4) * 4;
+      float m_r = -INFINITY, l_r = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x0 = 0; x0 < np; x0 += 8) {        // 8 loads on their way at a time
+      auto add = [&](float mx, float lx, const float4 &v) {
+        const float now = fmaxf(m_r, mx);
+        const float was = m_r == -INFINITY ? 0.f : exp2_fast(m_r - now), f = mx == -INFINITY ? 0.f : exp2_fast(mx - now);
+        acc.x = acc.x * was + f * v.x;
+        acc.y = acc.y * was + f * v.y;
+        acc.z = acc.z * was + f * v.z;
+        acc.w = acc.w * was + f * v.w;
+        l_r = l_r * was + f * lx;
+        m_r = now;
+      };
+      for (int x0 = team; mine && x0 < np; x0 += 8 * teams) {
         float4 v[8];
+        float mx[8], lx[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          if (x0 + x < np) v[x] = __ldcg(reinterpret_cast<const float4 *>(slot(x0 + x)) + i);
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (x0 + x < np) {
-            const float f = factor[x0 + x][r];
-            acc.x += f * v[x].x;
-            acc.y += f * v[x].y;
-            acc.z += f * v[x].z;
-            acc.w += f * v[x].w;
+          if (x0 + x * teams < np) {
+            const float *s = slot(x0 + x * teams);
+            v[x] = __ldcg(reinterpret_cast<const float4 *>(s) + i);
+            mx[x] = __ldcg(s + ROWS * DP + r);
+            lx[x] = __ldcg(s + ROWS * DP + ROWS + r);
           }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (x0 + x * teams < np) add(mx[x], lx[x], v[x]);
       }
-      store_out4(p, b, hh + r, d, acc, row_inv[r]);
+      if (teams > 1) {
+        __syncthreads();
+        if (mine && team > 0) {
+          team_o[(team - 1) * cols + i] = acc;
+          if (d == 0) team_ml[team - 1][r] = make_float2(m_r, l_r);
+        }
+        __syncthreads();
+        if (mine && team == 0)
+          for (int t = 0; t + 1 < teams; ++t) add(team_ml[t][r].x, team_ml[t][r].y, team_o[t * cols + i]);
+      }
+      if (mine && team == 0) {
+        store_out4(p, b, hh + r, d, acc, l_r == 0.f ? 0.f : p.v_scale / l_r);
+        if (d == 0) store_lse(p, b, hh + r, m_r, l_r);
+      }
     }
     __syncthreads();
   }
