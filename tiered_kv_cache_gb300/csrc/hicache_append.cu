@@ -2,14 +2,17 @@
 // and the store of K and V into the paged cache, in one pass.
 //
 // Nothing is used twice, so memory binds, once the arithmetic on the way (norm,
-// rotation, conversions) is short enough: 25 instructions a 16-byte vector.  A warp
-// takes a token, or a part of its heads.  8 lanes hold a head, 4 heads at a time: a
-// vector of each 128 bytes of it per lane, so that the sum of squares takes three
-// shuffles however long the head, and every access is whole 128-byte lines.  A
-// lane's cosines, sines and norm weights are read once for all heads of the token,
-// and the vectors of AHEAD heads are on their way before the first is used.
-// Partner elements half a rotation away come through shared memory, interleaved
-// ones are in the lane's own vector.
+// rotation, conversions) is short enough.  A warp takes a token, or a part of its
+// heads.  8 lanes hold a head, 4 heads at a time: a vector of each 128 bytes of it
+// per lane, so that the sum of squares takes three shuffles however long the head,
+// and every access is whole 128-byte lines.  What depends on the token alone
+// (cosines, sines, norm weights) is read once for all its heads, and the next heads
+// are on their way while these are worked on.
+//
+// Two kernels: the usual shapes, where partners half a rotation away can be had
+// without shared memory, and any shape.  Measured, 8,191 tokens of 32 + 8 heads of
+// 128 (206 MB): 45.7 us, 4.5 TB/s; the same without norm and rotation, a plain copy,
+// runs at 5.7.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

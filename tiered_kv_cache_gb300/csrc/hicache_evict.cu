@@ -49,8 +49,8 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictParams &p, int64_t b) {
   return s;
 }
 
-// The digit of the need-th lowest key in `hist` (256 counts) and the rank left within
-// it, into pick[0..1]; for one warp.
+// The digit of the need-th lowest key in `hist` (256 counts), the rank left within it
+// and whether that is all the keys with this digit, into pick[0..2]; for one warp.
 __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, uint32_t *pick, int lane) {
   uint32_t c[8], sum = 0;
 #pragma unroll
@@ -66,6 +66,7 @@ __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, 
     if (before < need && need <= before + c[j]) {
       pick[0] = uint32_t(lane * 8 + j);
       pick[1] = need - before;
+      pick[2] = need - before == c[j];
     }
     before += c[j];
   }
@@ -74,7 +75,7 @@ __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, 
 // `cap`: pages that a CTA's dynamic shared memory holds (8 bytes each).
 __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __grid_constant__ EvictParams p, int cap) {
   extern __shared__ __align__(16) unsigned char pages_smem[];
-  __shared__ uint32_t hist[2][256], total[256], pick[2];
+  __shared__ uint32_t hist[2][256], total[256], pick[3];
   __shared__ uint32_t warp_below[32], warp_equal[32], cta_count[2], ahead[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   float *const w_s = reinterpret_cast<float *>(pages_smem);
@@ -83,6 +84,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
   const int cs = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int64_t b = blockIdx.x / unsigned(cs);
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+  auto sync = [&]() {
+    if (cs > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
   const EvictSeq q = evict_seq(p, b);
   const int n = q.n, count = q.count;
   const int slice = min(cap, ((n + cs - 1) / cs + 31) & ~31);
@@ -94,7 +101,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
   if (tid < 512) hist[tid >> 8][tid & 255] = 0;
   __syncthreads();
 
-  // the key of the last page that leaves, and how many pages with that key do
+  // the leading digits (mask) of the key of the last page that leaves, and how many
+  // pages with those digits do; once that is all of them, further digits do not matter
   uint32_t key = 0, mask = 0, need = uint32_t(count);
   if (count > 0) {
     const int from = max(0, p.sink - lo), to = min(mine, q.last - lo);
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
         const uint32_t k = order_key(w_s[i]);
         if ((k & mask) == key) atomicAdd(&h[(k >> shift) & 255], 1u);
       }
-      cluster.sync();
+      sync();
       if (tid < 256) {
         uint32_t sum = 0;
         for (int r = 0; r < cs; ++r) sum += cluster.map_shared_rank(h, r)[tid];
@@ -120,6 +128,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
       key |= pick[0] << shift;
       mask |= 255u << shift;
       need = pick[1];
+      if (pick[2]) break;
     }
   }
 
@@ -130,8 +139,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
     *below = *equal = false;
     if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last) {
       const uint32_t k = order_key(w_s[i]);
-      *below = k < key;
-      *equal = k == key;
+      *below = (k & mask) < key;
+      *equal = (k & mask) == key;
     }
   };
   uint32_t below0 = 0, equal0 = 0;
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
     warp_equal[lane] = y - y0;
     if (lane == 31) cta_count[0] = x, cta_count[1] = y;
   }
-  cluster.sync();                                 // and every CTA has read its pages
+  sync();                                         // and every CTA has read its pages
   if (warp == 0) {
     uint32_t x = 0, y = 0;
     if (lane < rank) {
@@ -198,12 +207,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
     p.num_victims[b] = count;
     p.out_lens[b] = q.len - count * p.P;
   }
-  cluster.sync();                                 // nobody reads this CTA's memory any more
+  if (cs > 1) cluster.sync();                     // nobody reads this CTA's memory any more
 }
 
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[2];              // digit, rank within it
+  __shared__ uint32_t pick[3];
   __shared__ unsigned long long warp_sum[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   const int64_t b = blockIdx.x;
