@@ -587,7 +587,7 @@ def test_evict_small_and_special(in_place):
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("n,b,kinds", [(1, 3, 2), (31, 2, 3), (1023, 2, 5), (1024, 2, 0), (1025, 3, 0), (2049, 300, 4),
                                        (4096, 2, 7), (4097, 2, 7), (5000, 2, 0), (40000, 2, 9), (131072, 3, 0),
-                                       (196608, 1, 50), (196609, 1, 50), (300001, 1, 3)])
+                                       (196608, 1, 50), (196609, 1, 50), (300001, 1, 3), (393216, 1, 20), (393217, 1, 20)])
 def test_evict_sizes(n, b, kinds, in_place):
     """kinds > 0: that many different weights only, so that most are equal."""
     rng = np.random.default_rng(n + b)

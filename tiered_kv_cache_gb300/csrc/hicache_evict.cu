@@ -10,7 +10,8 @@
 // once into shared memory; histograms and counts are summed over the cluster through
 // distributed shared memory.  Everything has been read before anything is written,
 // so the outputs may be the inputs.  Bound by the cluster's barriers: 131,071 pages
-// are 2 MB and take 25 us (198 us by one CTA).  Sequences too long for the cluster's shared memory take
+// are 2 MB and take 16 us (198 us by one CTA without
+// them).  Sequences too long for the cluster's shared memory take
 // one CTA that walks them chunk by chunk.
 
 #include <cooperative_groups.h>
@@ -303,10 +304,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
 int launch_evict(const EvictParams &p, int device, void *stream) {
   constexpr int kMaxDevices = 64;
   constexpr int kCap = 24576;                     // pages of a CTA: 192 KiB of shared memory
-  constexpr int kCluster = 8;
-  // one CTA up to 4,096 pages, four to a thread: there the cluster's barriers cost
-  // more than they save
-  const int cs = p.max_pages <= 4096 ? 1 : kCluster;
+  constexpr int kCluster = 16;
+  // One CTA a sequence up to 4,096 pages (9.7 us; 16 took 9.1 for one sequence, but 9.0
+  // against 6.0 at 1,024 pages and 80 against 11 for 64 sequences).  Beyond, as many
+  // as let every sequence's cluster run at once: large clusters find few places
+  // (8 sequences of 16,384 pages: 21.5 us by 16 CTAs each, 11.3 by 8, 22.4 by one;
+  // 64: 96 by 16, 17 by 2, 22 by one).  And no fewer than hold the pages.
+  int cs = 1;
+  if (p.max_pages > 4096) cs = p.B <= 4 ? 16 : p.B <= 9 ? 8 : p.B <= 32 ? 4 : p.B <= 76 ? 2 : 1;
+  while (cs < kCluster && int64_t(cs) * kCap < p.max_pages) cs *= 2;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -326,6 +332,8 @@ int launch_evict(const EvictParams &p, int device, void *stream) {
     static std::atomic<bool> ready[kMaxDevices];
     if (device >= kMaxDevices || !ready[device].load(std::memory_order_acquire)) {
       e = cudaFuncSetAttribute(evict_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap * 8);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(evict_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return int(e);
       if (device < kMaxDevices) ready[device].store(true, std::memory_order_release);
     }
