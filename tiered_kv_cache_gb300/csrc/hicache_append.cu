@@ -592,10 +592,14 @@ AppendKernel append_kernel_of(const AppendParams &p) {
 }  // namespace
 
 int launch_append(const AppendParams &p, void *stream) {
-  // a warp per token, unless that leaves SMs with fewer than 16 warps: then its
-  // heads are dealt to as many warps as it takes (or as there are)
-  auto deal = [&](int most, int *per_task, int64_t *tasks) {
-    int64_t segments = (int64_t(152) * 16 + p.num_tokens - 1) / p.num_tokens;
+  // a warp per token, unless the SMs hold several (`resident` each): then its heads
+  // are dealt to as many as there is room for, so that all tasks run at once.  One
+  // more than that, and the last wait for the first: 607 tokens of 17 heads of 576
+  // take 5.5 us as two tasks each and 8.3 as five, 450 of 16 + 4 heads of 256 4.4 us as
+  // three and 6.4 as six.
+  auto deal = [&](int most, int resident, int *per_task, int64_t *tasks) {
+    int64_t segments = int64_t(152) * resident / p.num_tokens;
+    if (segments < 1) segments = 1;
     if (segments > most) segments = most;
     *per_task = int((most + segments - 1) / segments);
     segments = (most + *per_task - 1) / *per_task;
@@ -603,8 +607,9 @@ int launch_append(const AppendParams &p, void *stream) {
     return make_fastdiv(uint32_t(segments));
   };
   AppendKernel k = append_fast(p);
-  int most;
+  int most, resident;
   if (k) {
+    resident = kAppendWarps * (p.D <= 128 ? 5 : p.D == 256 ? 3 : 2);
     most = (p.q_heads + kGroups - 1) / kGroups + (p.kv_heads + kGroups - 1) / kGroups * (p.has_v ? 2 : 1);
   } else {
     const int iters = (p.D / 8 + kLanes - 1) / kLanes;
@@ -614,12 +619,13 @@ int launch_append(const AppendParams &p, void *stream) {
         : iters == 4 ? append_kernel_of<4>(p)
         : iters <= 9 ? append_kernel_of<9>(p)
                      : append_kernel_of<12>(p);
+    resident = kAppendWarps * (iters <= 4 ? 4 : 3);
     const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
     most = (p.q_heads + p.kv_heads * (p.has_v ? 2 : 1) + step - 1) / step;
   }
   int per_task = 0;
   int64_t tasks = 0;
-  const FastDiv fd = deal(most, &per_task, &tasks);
+  const FastDiv fd = deal(most, resident, &per_task, &tasks);
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
