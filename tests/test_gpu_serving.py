@@ -156,6 +156,48 @@ def test_append_skips_rows():
     assert (q_out[skip] == 7.0).all()
 
 
+LONG_APPEND = [
+    # several tokens to a warp, and warps that begin and end within one
+    (3001, 5, 3, 64, 16, "bf16", False, 64, 64, 64, 0, False, False),
+    (4099, 1, 1, 64, 16, "fp16", True, 0, 64, 64, 0, True, False),
+    (2500, 9, 2, 128, 16, "fp16", False, 128, 128, 128, 0, False, False),
+    (1999, 4, 5, 128, 7, "bf16", True, 128, 64, 64, 64, False, False),
+    (2311, 6, 1, 128, 16, "bf16", False, 0, 0, 0, 0, False, False),
+    (1777, 3, 2, 256, 16, "bf16", False, 256, 256, 256, 0, False, False),
+    (1501, 5, 1, 256, 16, "fp16", True, 128, 256, 128, 64, True, False),
+    (1409, 7, 1, 576, 16, "bf16", False, 0, 512, 64, 512, False, True),
+    (911, 17, 1, 576, 64, "fp16", True, 576, 512, 64, 448, True, True),
+    (1205, 2, 1, 576, 64, "bf16", False, 512, 512, 0, 0, False, True),
+]
+
+
+@pytest.mark.parametrize("c", LONG_APPEND, ids=[f"{i}" for i in range(len(LONG_APPEND))])
+def test_append_many_tokens(c):
+    """Runs of tokens through each shape, some of whose slots or positions are outside."""
+    q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, 11)
+    n, hq, hk, d, P = c[:5]
+    slots[::5] = -1
+    slots[3::17] = pages * P
+    skip = torch.zeros(n, dtype=torch.bool, device="cuda")
+    if cs is not None:
+        skip[2::7] = True
+        skip[40:43] = True
+        pos[2::7] = -1
+        pos[40:43] = 5000
+    old = [b.clone() for b in bufs]
+    ks, vs = (0.03, 0.05) if c[6] else (1.0, 1.0)
+    q_out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    hc.append_kv(hc.DeviceKV(bufs, pages), desc(P, hk * d, bufs[0].element_size(), len(bufs)), 0, q, k, v, slots,
+                 q_out=q_out, positions=pos if cs is not None else None, cos_sin=cs, rot_offset=c[10],
+                 interleaved=c[11], q_weight=qw, k_weight=kw, k_scale=ks, v_scale=vs)
+    check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, ks, vs, skip)
+    assert (q_out[skip] == 7.0).all()
+    hc.append_kv(hc.DeviceKV(bufs, pages), desc(P, hk * d, bufs[0].element_size(), len(bufs)), 0, q, None, None, None,
+                 positions=pos if cs is not None else None, cos_sin=cs, rot_offset=c[10], interleaved=c[11],
+                 q_weight=qw)
+    assert torch.equal(raw(q)[~skip], raw(q_out)[~skip])
+
+
 def test_append_heads_outer_and_extremes():
     """Heads outside tokens, e4m3 saturation, infinities and NaN."""
     g = gen(9)

@@ -2,17 +2,16 @@
 // and the store of K and V into the paged cache, in one pass.
 //
 // Nothing is used twice, so memory binds, once the arithmetic on the way (norm,
-// rotation, conversions) is short enough.  A warp takes a token, or a part of its
-// heads.  8 lanes hold a head, 4 heads at a time: a vector of each 128 bytes of it
-// per lane, so that the sum of squares takes three shuffles however long the head,
-// and every access is whole 128-byte lines.  What depends on the token alone
-// (cosines, sines, norm weights) is read once for all its heads, and the next heads
-// are on their way while these are worked on.
+// rotation, conversions) is short enough.  A warp takes 4 heads of a token at a time,
+// 8 lanes a head: a vector of each 128 bytes of it per lane, so that the sum of
+// squares takes three shuffles however long the head, and every access is whole
+// 128-byte lines.  What depends on the token alone (cosines, sines, norm weights) is
+// read once for all its heads of a warp, and the next heads are on their way while
+// these are worked on.
 //
 // Two kernels: the usual shapes, where partners half a rotation away can be had
 // without shared memory, and any shape.  Measured, 8,191 tokens of 32 + 8 heads of
-// 128 (206 MB): 45.7 us, 4.5 TB/s; the same without norm and rotation, a plain copy,
-// runs at 5.7.
+// 128 (206 MB): 36 us, 5.7 TB/s, 85% of the rate of a plain copy.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -122,9 +121,29 @@ __device__ __forceinline__ uint32_t rotation8(const AppendParams &p, const float
 // the two coefficients are worked out once per token and kind, and an element costs
 // a multiply, a multiply-add, a multiply and its share of the sum of squares, all of
 // them on pairs (fma.rn.f32x2).  Against the general kernel below: a prefill chunk of
-// 8,191 tokens of 48 heads of 128 takes 45 us instead of 61.
+// 8,191 tokens of 48 heads of 128 takes 36 us instead of 61.
 enum : int { kSelf = 0, kAcross = 1, kInside = 2 };   // where partners are: ITERS / 2 vectors
                                                       // on, 4 lanes on, in the vector itself
+
+// Every warp that the SMs hold at once takes an even share of all steps (a step: 4
+// heads of one kind of a token), across tokens, so that none idles behind the last
+// ones, and copies of its next steps run ahead through a ring in shared memory.
+// Measured, 8,191 tokens of 32 + 8 heads of 128 and 4,096 of 16 + 1 heads of 576: a
+// warp per token with one step ahead in registers 45 and 40 us, shared out 42 and 35,
+// and 36 and 30 with the ring.
+//   heads of 64:  5 CTAs an SM, 2 steps ahead: 23.5 us for the 8,191 (4 CTAs 25)
+//            128: 4 CTAs, 3 steps: 35.6 (5 CTAs spill, 39; 3 CTAs 38.7; 2 steps 37.1)
+//            256: 3 CTAs, 2 steps: 68.1 (4 steps 69.0)
+//            576: 3 CTAs, 2 steps: 29.7 for the 4,096, 107 for 16,000 (4 CTAs spill, 28.9 and 118)
+constexpr int append_ctas(int iters) { return iters == 1 ? 5 : iters == 2 ? 4 : 3; }
+template <int ITERS>
+constexpr int kAppendSlots = ITERS == 2 ? 3 : 2;
+
+struct AppendDeal {
+  int steps;                                      // of each warp, one more of the first `longer`
+  uint32_t longer;
+  FastDiv fd_steps;                               // by a token's steps
+};
 
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -163,67 +182,98 @@ __device__ __forceinline__ uint64_t swapped(uint64_t x) {
   return pair(f.y, f.x);
 }
 
-template <int ITERS, bool BF16, int MODE>
-__global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 3 : 2)
-    append_fast_kernel(const __grid_constant__ AppendParams p, int steps_per_task, FastDiv fd_segments) {
+// E4M3: whether the cache is; the inlined divisions, in the way of the others, cost long
+// heads a sixth of their time (35 against 29.5 us for the 4,096).
+template <int ITERS, bool BF16, int MODE, bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads, append_ctas(ITERS))
+    append_fast_kernel(const __grid_constant__ AppendParams p, const AppendDeal deal) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   constexpr bool HOLD = ITERS <= 4;               // coefficients of every vector in registers
-  constexpr bool EARLY = ITERS > 4;
+  constexpr int SLOTS = kAppendSlots<ITERS>;
   const int warp = int(threadIdx.x) >> 5;
-  const uint32_t task = blockIdx.x * uint32_t(kAppendWarps) + uint32_t(warp);
-  const uint32_t n = fast_div(task, fd_segments);
-  if (int64_t(n) >= p.num_tokens) return;         // the whole warp
   const int sub = (int(threadIdx.x) & 31) / kLanes, lane = int(threadIdx.x) & (kLanes - 1);
   // a step: 4 heads of one kind
   const int q_steps = (p.q_heads + kGroups - 1) / kGroups, kv_steps = (p.kv_heads + kGroups - 1) / kGroups;
-  const int first = int(task - n * fd_segments.d) * steps_per_task;
-  const int end = min(q_steps + kv_steps * (p.has_v ? 2 : 1), first + steps_per_task);
+  const int all_steps = q_steps + kv_steps * (p.has_v ? 2 : 1);
+  // this warp's steps: `count` of them from step `s` of token n on
+  const uint32_t w = blockIdx.x * uint32_t(kAppendWarps) + uint32_t(warp);
+  const int count = deal.steps + (w < deal.longer ? 1 : 0);
+  const uint32_t past = w * uint32_t(deal.steps) + min(w, deal.longer);   // < 2^31 in all
+  int64_t n = fast_div(past, deal.fd_steps);
+  int s = int(past - uint32_t(n) * uint32_t(all_steps));
   // the step to fetch next: its source, the step its kind ends at, heads of the kind
   // from this one on
   const char *f_src = nullptr;
   int64_t f_step = 0;
-  int f_s = first, f_end = 0, f_left = 0;
+  int64_t f_n = n;
+  int f_s = s, f_end = 0, f_left = 0, f_count = count;
   auto seek = [&]() {
     const int kind = f_s < q_steps ? 0 : f_s < q_steps + kv_steps ? 1 : 2;
     const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
     const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
     const int h = (f_s - begin) * kGroups + sub;
     f_src = static_cast<const char *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-            2 * (int64_t(n) * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) + h * sh) + lane * 16;
+            2 * (f_n * (kind == 0 ? p.q_st : kind == 1 ? p.k_st : p.v_st) + h * sh) + lane * 16;
     f_step = 2 * kGroups * sh;
-    f_end = min(end, begin + (kind == 0 ? q_steps : kv_steps));
+    f_end = begin + (kind == 0 ? q_steps : kv_steps);
     f_left = (kind == 0 ? p.q_heads : p.kv_heads) - h;
   };
-  uint4 ahead[ITERS];                             // the next step's vectors, on their way
+  // a ring of steps; a lane reads only what it has copied itself
+  __shared__ uint4 ring[kAppendWarps][SLOTS][ITERS][32];
+  uint4 *const mine = &ring[warp][0][0][threadIdx.x & 31];
+  int f_slot = 0;                                 // to be read, then to be fetched into
   auto fetch = [&]() {
-    if (f_s >= f_end && f_s < end) seek();
-    const bool have = f_s < f_end && f_left > 0;
+    if (f_s == all_steps) f_s = f_end = 0, ++f_n;
+    if (f_s >= f_end && f_count > 0) seek();
+    const bool have = f_count > 0 && f_left > 0;
+    if (have) {
+      const uint32_t to = uint32_t(__cvta_generic_to_shared(mine + f_slot * (ITERS * 32)));
 #pragma unroll
-    for (int it = 0; it < ITERS; ++it)
-      ahead[it] = have ? __ldcs(reinterpret_cast<const uint4 *>(f_src) + it * kLanes) : make_uint4(0, 0, 0, 0);
+      for (int it = 0; it < ITERS; ++it)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + it * 512), "l"(f_src + it * (kLanes * 16))
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    f_slot = f_slot + 1 == SLOTS ? 0 : f_slot + 1;
     ++f_s;
+    --f_count;
     f_left -= kGroups;
     f_src += f_step;
   };
-  int64_t pos = 0, slot = -1;
-  if (p.kv_heads > 0) slot = p.slots[n];
-  if (p.rot > 0) pos = p.positions[n];
-  fetch();
-  if (p.rot > 0 && (pos < 0 || pos >= p.cos_sin_rows)) return;   // the whole warp
-  const bool store_kv = slot >= 0 && slot < p.num_slots;
-  const float *row = p.cos_sin + pos * p.rot;
-  const int half = p.rot >> 1;
+  int64_t slot = -1;
+  bool known = true;                              // whether the position is in the table
+  const float *row = nullptr;
+  auto place = [&]() {
+    slot = p.kv_heads > 0 ? p.slots[n] : -1;
+    if (slot >= p.num_slots) slot = -1;
+    if (p.rot == 0) return;
+    const int64_t pos = p.positions[n];
+    known = pos >= 0 && pos < p.cos_sin_rows;
+    row = p.cos_sin + pos * p.rot;
+  };
+  if (count > 0) place();
+#pragma unroll 1
+  for (int i = 0; i < SLOTS; ++i) fetch();
+  // long heads: the weights in shared memory, where they cost no registers
+  __shared__ uint4 weights[HOLD ? 1 : 2][HOLD ? 1 : kLanes * ITERS];
+  if constexpr (!HOLD) {
+    for (int i = int(threadIdx.x); i < kLanes * ITERS; i += kAppendThreads) {
+      if (i * 8 < p.q_norm) weights[0][i] = __ldg(static_cast<const uint4 *>(p.q_weight) + i);
+      if (i * 8 < p.k_norm) weights[1][i] = __ldg(static_cast<const uint4 *>(p.k_weight) + i);
+    }
+    __syncthreads();
+  }
+  if (count == 0) return;                         // the whole warp
 
   // coefficients of the current kind: of the element and of its partner
   uint64_t own[HOLD ? ITERS : 1][4], mate[HOLD ? ITERS : 1][4];
-  uint4 wp[HOLD ? 1 : ITERS];                     // not held: the weights as they come
   float cs1[HOLD ? 1 : 8], sn1[HOLD ? 1 : 8];     // and the rotation of the one vector it turns
   int kind = 0, m = 0, s_end = 0, left = 0;       // the current kind, where it ends, heads from this one on
   float inv_m = 0.f;
   char *dst = nullptr;
   int64_t dst_step = 0;
   auto turned = [&](int it) {                     // whether vector `it` is rotated (the same in all lanes)
-    return p.rot > 0 && it * 64 >= p.rot_off && it * 64 < p.rot_off + p.rot;
+    return known && p.rot > 0 && it * 64 >= p.rot_off && it * 64 < p.rot_off + p.rot;
   };
   auto prepare = [&](int kind) {
     m = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : 0;
@@ -256,67 +306,71 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 
     } else {
 #pragma unroll
       for (int it = 0; it < ITERS; ++it) {
-        if (it * 64 < m) wp[it] = __ldg(w + lane + it * kLanes);
         if (turned(it)) rotation8<true>(p, row, (lane + it * kLanes) * 8 - p.rot_off, cs1, sn1);
       }
     }
   };
 
 #pragma unroll 1
-  for (int s = first; s < end; ++s) {
-    // long heads: the next step is fetched at once, into registers of its own (40
-    // against 45 us for the latent prefill); short ones do without the copies
-    uint4 now[EARLY ? ITERS : 1];
-    if constexpr (EARLY) {
-#pragma unroll
-      for (int it = 0; it < ITERS; ++it) now[it] = ahead[it];
-      fetch();
+  for (int i = 0; i < count; ++i, ++s) {
+    if (s == all_steps) {                         // on to the next token
+      s = s_end = 0;
+      ++n;
+      place();
     }
-    const uint4 *const raw = EARLY ? now : ahead;
+    asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+    uint4 raw[ITERS];
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) raw[it] = mine[f_slot * (ITERS * 32) + it * 32];
     if (s >= s_end) {                             // on to the next kind: its coefficients and places
       kind = s < q_steps ? 0 : s < q_steps + kv_steps ? 1 : 2;
       const int begin = kind == 0 ? 0 : kind == 1 ? q_steps : q_steps + kv_steps;
-      s_end = min(end, begin + (kind == 0 ? q_steps : kv_steps));
+      s_end = begin + (kind == 0 ? q_steps : kv_steps);
       const int h = (s - begin) * kGroups + sub;
-      left = kind == 0 ? p.q_heads - h : store_kv ? p.kv_heads - h : 0;
-      const int vec = kind != 0 && p.e4m3 ? 8 : 16;              // bytes that 8 elements take
+      left = !known ? 0 : kind == 0 ? p.q_heads - h : slot >= 0 ? p.kv_heads - h : 0;
+      const int vec = kind != 0 && E4M3 ? 8 : 16;              // bytes that 8 elements take
       const int64_t sh = kind == 0 ? p.o_sh : p.D;
-      const int64_t at = kind == 0 ? int64_t(n) * p.o_st + h * sh : slot * p.row + h * sh;
+      const int64_t at = kind == 0 ? n * p.o_st + h * sh : slot * p.row + h * sh;
       dst = static_cast<char *>(kind == 0 ? p.q_out : kind == 1 ? p.k_cache : p.v_cache) + at * (vec / 8) + lane * vec;
       dst_step = kGroups * sh * (vec / 8);
-      if (kind != 2 || p.e4m3) prepare(kind);
+      if (kind != 2 || E4M3) prepare(kind);
     }
     const bool live = left > 0;
     char *const to = dst;
     left -= kGroups;
     dst += dst_step;
-    if (kind == 2 && !p.e4m3) {                   // as it came
+    if (kind == 2 && !E4M3) {                   // as it came
 #pragma unroll
       for (int it = 0; it < ITERS; ++it)
         if (live) reinterpret_cast<uint4 *>(to)[it * kLanes] = raw[it];
-      if constexpr (!EARLY) fetch();
+      fetch();
       continue;
     }
-    uint64_t v[ITERS][4];
+    uint64_t v[HOLD ? ITERS : 1][4];              // not held: widened again for the second pass
+    uint64_t sq = 0;
     uint32_t across[HOLD && MODE == kAcross ? ITERS : 1][4];      // the partners, as they come
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) {
       const uint32_t w[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[it][i] = widen<BF16>(w[i]);
+        if constexpr (HOLD) {
+          v[it][i] = widen<BF16>(w[i]);
+        } else if (it * 64 < m) {
+          const uint64_t x = widen<BF16>(w[i]);
+          sq = fma2(x, x, sq);
+        }
         if constexpr (HOLD && MODE == kAcross) across[it][i] = __shfl_xor_sync(0xffffffffu, w[i], 4);
       }
     }
-    if constexpr (!EARLY) fetch();
+    fetch();                                      // into the slot just read
     float r = 1.f;
     if (m > 0) {
-      uint64_t sq = 0;
 #pragma unroll
       for (int it = 0; it < ITERS; ++it)
-        if (it * 64 < m) {
+        if (HOLD && it * 64 < m) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sq = fma2(v[it][i], v[it][i], sq);
+          for (int i = 0; i < 4; ++i) sq = fma2(v[HOLD ? it : 0][i], v[HOLD ? it : 0][i], sq);
         }
       const float2 f = unpair(sq);
       float sum = f.x + f.y;
@@ -324,7 +378,13 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 
       for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       r = rsqrt_fast(fmaf(sum, inv_m, p.eps));
     }
-    float out[ITERS][8];
+    auto store = [&](int it, const float *x) {
+      if (kind != 0 && E4M3)
+        reinterpret_cast<uint2 *>(to)[it * kLanes] = pack8_e4m3(x, kind == 1 ? p.k_scale : p.v_scale);
+      else
+        reinterpret_cast<uint4 *>(to)[it * kLanes] = pack8<BF16>(x);
+    };
+    float out[HOLD ? ITERS : 1][8];
 #pragma unroll
     for (int it = 0; it < ITERS; ++it) {
       const float rr = it * 64 < m ? r : 1.f;
@@ -335,9 +395,12 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = mul2(v[it][i], own[it][i]);
       } else {
-        const uint32_t w[4] = {wp[it].x, wp[it].y, wp[it].z, wp[it].w};
+        const uint32_t y[4] = {raw[it].x, raw[it].y, raw[it].z, raw[it].w};
+        const uint4 f = weights[kind == 0 ? 0 : 1][lane + it * kLanes];
+        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = it * 64 < m ? mul2(v[it][i], widen<BF16>(w[i])) : v[it][i];
+        for (int i = 0; i < 4; ++i)
+          x[i] = it * 64 < m ? mul2(widen<BF16>(y[i]), widen<BF16>(w[i])) : widen<BF16>(y[i]);
       }
       if (turn) {
         uint64_t z[4];
@@ -346,7 +409,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 
           for (int i = 0; i < 4; ++i) z[i] = v[it ^ (ITERS / 2)][i];
         } else if constexpr (MODE == kInside) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = swapped(HOLD ? v[it][i] : x[i]);
+          for (int i = 0; i < 4; ++i) z[i] = swapped(HOLD ? v[HOLD ? it : 0][i] : x[i]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -364,32 +427,30 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 2 ? 5 : ITERS == 4 ? 
           else
             x[i] = fma2(z[i], pair(sn1[2 * i], sn1[2 * i + 1]), mul2(x[i], pair(cs1[2 * i], cs1[2 * i + 1])));
       }
+      float *const y = out[HOLD ? it : 0];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = unpair(mul2(x[i], r2));
-        out[it][2 * i] = f.x;
-        out[it][2 * i + 1] = f.y;
+        y[2 * i] = f.x;
+        y[2 * i + 1] = f.y;
       }
+      if (!HOLD && live) store(it, y);
     }
-    if (!live) continue;
-    if (kind != 0 && p.e4m3) {
+    if (HOLD && live) {
 #pragma unroll
-      for (int it = 0; it < ITERS; ++it)
-        reinterpret_cast<uint2 *>(to)[it * kLanes] = pack8_e4m3(out[it], kind == 1 ? p.k_scale : p.v_scale);
-    } else {
-#pragma unroll
-      for (int it = 0; it < ITERS; ++it) reinterpret_cast<uint4 *>(to)[it * kLanes] = pack8<BF16>(out[it]);
+      for (int it = 0; it < ITERS; ++it) store(it, out[HOLD ? it : 0]);
     }
   }
 }
 
 // The kernel for p's shape, or null where only the general one will do.
-using AppendKernel = void (*)(const AppendParams, int, FastDiv);
+using AppendFast = void (*)(const AppendParams, const AppendDeal);
 template <int ITERS, int MODE>
-AppendKernel fast_of(const AppendParams &p) {
-  return p.bf16 ? append_fast_kernel<ITERS, true, MODE> : append_fast_kernel<ITERS, false, MODE>;
+AppendFast fast_of(const AppendParams &p) {
+  return p.bf16 ? (p.e4m3 ? append_fast_kernel<ITERS, true, MODE, true> : append_fast_kernel<ITERS, true, MODE, false>)
+                : (p.e4m3 ? append_fast_kernel<ITERS, false, MODE, true> : append_fast_kernel<ITERS, false, MODE, false>);
 }
-AppendKernel append_fast(const AppendParams &p) {
+AppendFast append_fast(const AppendParams &p) {
   if (p.D % 64 || reinterpret_cast<uintptr_t>(p.cos_sin) % 16) return nullptr;
   if (p.q_norm % 64 || p.k_norm % 64 || p.rot_off % 64) return nullptr;
   const bool every = (p.q_norm == 0 || p.q_norm == p.D) && (p.k_norm == 0 || p.k_norm == p.D);
@@ -580,6 +641,7 @@ __global__ void __launch_bounds__(kAppendThreads, ITERS <= 4 ? 4 : 3)
   }
 }
 
+using AppendKernel = void (*)(const AppendParams, int, FastDiv);
 template <int ITERS>
 AppendKernel append_kernel_of(const AppendParams &p) {
   const int half = p.rot / 2;
@@ -592,50 +654,43 @@ AppendKernel append_kernel_of(const AppendParams &p) {
 }  // namespace
 
 int launch_append(const AppendParams &p, void *stream) {
-  // a warp per token, unless the SMs hold several (`resident` each): then its heads
-  // are dealt to as many as there is room for, so that all tasks run at once.  One
-  // more than that, and the last wait for the first: 607 tokens of 17 heads of 576
-  // take 5.5 us as two tasks each and 8.3 as five, 450 of 16 + 4 heads of 256 4.4 us as
-  // three and 6.4 as six.
-  auto deal = [&](int most, int resident, int *per_task, int64_t *tasks) {
-    int64_t segments = int64_t(152) * resident / p.num_tokens;
-    if (segments < 1) segments = 1;
-    if (segments > most) segments = most;
-    *per_task = int((most + segments - 1) / segments);
-    segments = (most + *per_task - 1) / *per_task;
-    *tasks = p.num_tokens * segments;
-    return make_fastdiv(uint32_t(segments));
-  };
-  AppendKernel k = append_fast(p);
-  int most, resident;
-  if (k) {
-    resident = kAppendWarps * (p.D <= 128 ? 5 : p.D == 256 ? 3 : 2);
-    most = (p.q_heads + kGroups - 1) / kGroups + (p.kv_heads + kGroups - 1) / kGroups * (p.has_v ? 2 : 1);
-  } else {
-    const int iters = (p.D / 8 + kLanes - 1) / kLanes;
-    k = iters == 1   ? append_kernel_of<1>(p)
-        : iters == 2 ? append_kernel_of<2>(p)
-        : iters == 3 ? append_kernel_of<3>(p)
-        : iters == 4 ? append_kernel_of<4>(p)
-        : iters <= 9 ? append_kernel_of<9>(p)
-                     : append_kernel_of<12>(p);
-    resident = kAppendWarps * (iters <= 4 ? 4 : 3);
-    const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
-    most = (p.q_heads + p.kv_heads * (p.has_v ? 2 : 1) + step - 1) / step;
-  }
-  int per_task = 0;
-  int64_t tasks = 0;
-  const FastDiv fd = deal(most, resident, &per_task, &tasks);
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(unsigned((tasks + kAppendWarps - 1) / kAppendWarps));
   c.blockDim = dim3(kAppendThreads);
   c.stream = static_cast<cudaStream_t>(stream);
   c.attrs = &at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, k, p, per_task, fd);
+  if (AppendFast k = append_fast(p)) {
+    const int steps = (p.q_heads + kGroups - 1) / kGroups + (p.kv_heads + kGroups - 1) / kGroups * (p.has_v ? 2 : 1);
+    const int64_t total = p.num_tokens * steps, most = 152 * append_ctas(p.D / 64);
+    const int64_t ctas = (total + kAppendWarps - 1) / kAppendWarps;
+    c.gridDim = dim3(unsigned(ctas < most ? ctas : most));
+    const int64_t warps = int64_t(c.gridDim.x) * kAppendWarps;
+    const AppendDeal deal{int(total / warps), uint32_t(total % warps), make_fastdiv(uint32_t(steps))};
+    const cudaError_t e = cudaLaunchKernelEx(&c, k, p, deal);
+    return int(e != cudaSuccess ? e : cudaGetLastError());
+  }
+  const int iters = (p.D / 8 + kLanes - 1) / kLanes;
+  AppendKernel k = iters == 1   ? append_kernel_of<1>(p)
+                   : iters == 2 ? append_kernel_of<2>(p)
+                   : iters == 3 ? append_kernel_of<3>(p)
+                   : iters == 4 ? append_kernel_of<4>(p)
+                   : iters <= 9 ? append_kernel_of<9>(p)
+                                : append_kernel_of<12>(p);
+  // a warp per token, unless the SMs hold several: then its heads are dealt to as many
+  // as there is room for, so that all tasks run at once.  One more than that, and the
+  // last wait for the first: 900 tokens of 32 + 8 heads of 96 take 8.6 us, where three
+  // tasks each took 11.4.
+  const int step = kGroups * (iters == 1 ? 4 : iters == 2 ? 2 : 1);
+  const int most = (p.q_heads + p.kv_heads * (p.has_v ? 2 : 1) + step - 1) / step;
+  int64_t segments = int64_t(152) * kAppendWarps * (iters <= 4 ? 4 : 3) / p.num_tokens;
+  segments = segments < 1 ? 1 : segments > most ? most : segments;
+  const int per_task = int((most + segments - 1) / segments);
+  segments = (most + per_task - 1) / per_task;
+  c.gridDim = dim3(unsigned((p.num_tokens * segments + kAppendWarps - 1) / kAppendWarps));
+  const cudaError_t e = cudaLaunchKernelEx(&c, k, p, per_task, make_fastdiv(uint32_t(segments)));
   return int(e != cudaSuccess ? e : cudaGetLastError());
 }
 
