@@ -10,9 +10,8 @@
 // once into shared memory; histograms and counts are summed over the cluster through
 // distributed shared memory.  Everything has been read before anything is written,
 // so the outputs may be the inputs.  Bound by the cluster's barriers: 131,071 pages
-// are 2 MB and take 16 us (198 us by one CTA without
-// them).  Sequences too long for the cluster's shared memory take
-// one CTA that walks them chunk by chunk.
+// are 2 MB and take 16 us (198 us by one CTA without them).  Sequences too long for the
+// cluster's shared memory take one CTA that walks them chunk by chunk.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
