@@ -739,7 +739,7 @@ int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
  *   num_victims[b]              count
  *   out_table[b, 0..n-count)    the other entries, in order; [n-count, n) -> -1
  *   out_weights[b, 0..n-count)  their weights, in order; [n-count, n) -> 0
- *   out_lens[b]                 seq_lens[b] - count * page_size
+ *   out_lens[b]                 seq_lens[b] (as given) - count * page_size
  * and everything else in those arrays is left as it was.  recent >= 1 keeps the
  * last page, which may not be full.  out_table, out_weights and out_lens may be
  * page_table, weights and seq_lens themselves (same strides), else nothing may

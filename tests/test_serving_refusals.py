@@ -107,6 +107,14 @@ def test_decode_refuses_pools(d, change, layer, status):
     assert call("hicache_decode_attention", hc._DECODE_DESC, {**DECODE, **change}, d, layer) == status
 
 
+def test_decode_refuses_scales_that_overflow_together():
+    """Each in range of 32 bits, their product (times log2 e) is not."""
+    d = desc(elem_bytes=1)
+    for scale, ks, status in ((1e38, 1e38, "INVALID_ARG"), (-3e38, 1.0, "INVALID_ARG"), (1e30, 1e9, "INVALID_ARG")):
+        assert call("hicache_decode_attention", hc._DECODE_DESC, {**DECODE, "scale": scale, "ks": ks}, d) == status
+        assert "scale" in hc.library().hicache_last_error().decode()
+
+
 def test_caches_are_checked():
     for fn, packer, f in (("hicache_append_kv", hc._APPEND_DESC, APPEND),
                           ("hicache_decode_attention", hc._DECODE_DESC, DECODE)):

@@ -274,6 +274,8 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   if ((rc = decode_sizes(s, a->batch, a->q_heads, a->head_dim, a->v_dim, a->max_pages, &p))) return rc;
   if (!std::isfinite(a->scale) || !std::isfinite(a->decay))
     return set_error(HICACHE_ERR_INVALID_ARG, "scale and decay must be finite");
+  p.scale2 = float(double(a->scale) * double(a->k_scale) * 1.4426950408889634);
+  if (!std::isfinite(p.scale2)) return set_error(HICACHE_ERR_INVALID_ARG, "scale * k_scale leaves 32 bits");
   if (a->window < 0) return set_error(HICACHE_ERR_INVALID_ARG, "window must be >= 0");
   if (a->batch == 0) return HICACHE_OK;
   if ((rc = check_heads("q", a->q, a->q_batch_stride, a->q_head_stride))) return rc;
@@ -321,7 +323,6 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.window = a->window;
   p.bf16 = a->dtype == HICACHE_BF16;
   p.fd_page = hicache::make_fastdiv(uint32_t(s.P));
-  p.scale2 = float(double(a->scale) * double(a->k_scale) * 1.4426950408889634);
   p.v_scale = a->v_scale;
   p.decay = a->decay;
   int n = 0, device = 0;
