@@ -66,8 +66,9 @@ struct KvConfig {
   static constexpr int NB = ROWS_ / 8;            // n tiles: 8 heads each
   static constexpr float RAISE = TYPE_ == kBf16 ? 40.f : 14.f;
   static constexpr int PIECE = ROWS_ * DP_ + 2 * ROWS_;   // floats of a partial result: O, m, l
+  static constexpr int LD = DP_ + 4;              // floats of a row of a warp's: no bank twice
   static constexpr int SMEM = WARPS * RING_B;
-  static_assert(STAGES >= 2 && RING_B >= ROWS_ * DP_ * 4, "ring");
+  static_assert(STAGES >= 2 && RING_B >= ROWS_ * LD * 4, "ring");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t *r, uint32_t a) {
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
         // fill; an earlier one (there is at most one) into the workspace
         const bool end = it == hi - 1;
         const int k = pieces++;
-        float *dst = end ? reinterpret_cast<float *>(ring) : p.warp_parts + w_id * (ROWS * DP);
+        float *dst = end ? reinterpret_cast<float *>(ring) : p.warp_parts + w_id * (ROWS * C::LD);
         if (end) {
           cp_wait<0>();
           __syncwarp();
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
 #pragma unroll
             for (int t = 0; t < C::MT; ++t)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) dst[r * DP + element<C>(t, x, g)] = o[t][n][2 * x + i];
+              for (int x = 0; x < 2; ++x) dst[r * C::LD + element<C>(t, x, g)] = o[t][n][2 * x + i];
             if (g == 0) {
               piece_m[warp][k][r] = m[n][i];
               piece_l[warp][k][r] = l[n][i];
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   // ---- join the CTA's pieces.  A chain is a run of pieces of one unit: it starts
   // at a piece that begins its unit, or at the CTA's first piece.
   constexpr int PIECES = 2 * C::WARPS, COL4 = DP / 4;
+  constexpr int COLS = ROWS * COL4 > THREADS ? 2 : 1;   // columns of a thread at a time
   static_assert(PIECES <= 32, "a lane for a piece");
   const int *state = &piece_state[0][0];
   const int mine_state = lane < PIECES ? state[lane] : 0;
@@ -608,6 +610,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     *k1 = 31 - __clz(int(present & upto));
     return bool((begin_m >> k) & (end_m >> *k1) & 1u);
   };
+  __shared__ unsigned char order[32];             // the pieces there are
+  if (warp == 0 && (mine_state & 4)) order[__popc(present & ((1u << lane) - 1u))] = (unsigned char)lane;
+  __syncthreads();
   int chain = 0;
   for (uint32_t left = starts; left; left &= left - 1u, ++chain) {
     // a warp's worth of chains at a time: warps take elements, not chains
@@ -618,36 +623,63 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     const int kvh = u / p.QB, qb = u - kvh * p.QB;
     const int hh = kvh * p.G + qb * ROWS, nr = min(ROWS, p.G - qb * ROWS);
     float *part = p.cta_parts + (int64_t(blockIdx.x) * 2 + int((begin_m >> k0) & 1u)) * C::PIECE;
-    for (int i = (tid + chain * 128) % THREADS; i < nr * COL4; i += THREADS) {
-      const int r = i / COL4, d = (i - r * COL4) * 4;
-      float mm = -INFINITY;
-      for (uint32_t w = present & (~0u << k0); w; w &= w - 1u) {
-        const int k = __ffs(int(w)) - 1;
-        if (k > k1) break;
-        mm = fmaxf(mm, (&piece_m[0][0][0])[k * ROWS + r]);
+    const int x0 = __popc(present & ((1u << k0) - 1u)), x1 = __popc(present & (k1 < 31 ? (2u << k1) - 1u : ~0u)) - 1;
+    const int cols = nr * COL4;
+    const bool more = cols > THREADS;             // two columns a thread, else one
+    for (int i0 = (tid + chain * 128) % THREADS; i0 < cols; i0 += COLS * THREADS) {
+      float mm[COLS], sum[COLS];
+      float4 acc[COLS];
+      int r[COLS], d[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const int i = min(i0 + c * THREADS, cols - 1);
+        r[c] = i / COL4, d[c] = (i - r[c] * COL4) * 4;
+        mm[c] = -INFINITY, sum[c] = 0.f;
+        acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-      for (uint32_t w = present & (~0u << k0); w; w &= w - 1u) {
-        const int k = __ffs(int(w)) - 1;
-        if (k > k1) break;
-        const float mk = (&piece_m[0][0][0])[k * ROWS + r];
-        const float f = mk == -INFINITY ? 0.f : exp2_fast(mk - mm);
-        const float4 v = *reinterpret_cast<const float4 *>((&piece_o[0][0])[k] + r * DP + d);
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
-        sum += f * (&piece_l[0][0][0])[k * ROWS + r];
+      const float *ms = &piece_m[0][0][0], *ls = &piece_l[0][0][0];
+      for (int x = x0; x <= x1; ++x)
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) mm[c] = fmaxf(mm[c], ms[order[x] * ROWS + r[c]]);
+      for (int xb = x0; xb <= x1; xb += 4) {      // 4 at a time: some come back from the workspace
+        float4 v[4][COLS];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (xb + x <= x1) {
+            const float *o = (&piece_o[0][0])[order[xb + x]];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+              if (c == 0 || more) v[x][c] = *reinterpret_cast<const float4 *>(o + r[c] * C::LD + d[c]);
+          }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (xb + x <= x1) {
+            const int k = order[xb + x] * ROWS;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+              if (c > 0 && !more) break;
+              const float mk = ms[k + r[c]];
+              const float f = mk == -INFINITY ? 0.f : exp2_fast(mk - mm[c]);
+              acc[c].x += f * v[x][c].x;
+              acc[c].y += f * v[x][c].y;
+              acc[c].z += f * v[x][c].z;
+              acc[c].w += f * v[x][c].w;
+              sum[c] += f * ls[k + r[c]];
+            }
+          }
       }
-      if (all) {
-        store_out4(p, b, hh + r, d, acc, sum == 0.f ? 0.f : p.v_scale / sum);
-        if (d == 0) store_lse(p, b, hh + r, mm, sum);
-      } else {
-        __stcg(reinterpret_cast<float4 *>(part + r * DP + d), acc);
-        if (d == 0) {
-          __stcg(part + ROWS * DP + r, mm);
-          __stcg(part + ROWS * DP + ROWS + r, sum);
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        if (i0 + c * THREADS >= cols) continue;
+        if (all) {
+          store_out4(p, b, hh + r[c], d[c], acc[c], sum[c] == 0.f ? 0.f : p.v_scale / sum[c]);
+          if (d[c] == 0) store_lse(p, b, hh + r[c], mm[c], sum[c]);
+        } else {
+          __stcg(reinterpret_cast<float4 *>(part + r[c] * DP + d[c]), acc[c]);
+          if (d[c] == 0) {
+            __stcg(part + ROWS * DP + r[c], mm[c]);
+            __stcg(part + ROWS * DP + ROWS + r[c], sum[c]);
+          }
         }
       }
     }
@@ -699,55 +731,73 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     const int hh = kvh * p.G + qb * ROWS, nr = min(ROWS, p.G - qb * ROWS);
     // piece x of the unit: CTA from + x, its second slot where the unit begins
     auto slot = [&](int x) { return p.cta_parts + (int64_t(from + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
-    // a thread takes four columns of a row; with threads to spare, every `teams`-th
-    // piece of them.  Maximum, sum and O of 8 pieces are on their way together.
+    constexpr int JOIN = ROWS > 8 ? COLS : 1;
+    // a thread takes four elements of a row (or JOIN times four); with threads to
+    // spare, every `teams`-th piece of them.  Maximum, sum and O of 8 pieces are on
+    // their way together.
     const int cols = nr * COL4, teams = max(1, min(4, THREADS / cols));
     const int team = teams > 1 ? tid / cols : 0;
-    for (int i0 = 0; i0 < cols; i0 += THREADS) {
+    for (int i0 = 0; i0 < cols; i0 += JOIN * THREADS) {
       const int i = teams > 1 ? tid - team * cols : i0 + tid;
-      const bool mine = team < teams && i < cols;
-      const int r = i / COL4, d = (i - r * COL4) * 4;
-      float m_r = -INFINITY, l_r = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](float mx, float lx, const float4 &v) {
-        const float now = fmaxf(m_r, mx);
-        const float was = m_r == -INFINITY ? 0.f : exp2_fast(m_r - now), f = mx == -INFINITY ? 0.f : exp2_fast(mx - now);
-        acc.x = acc.x * was + f * v.x;
-        acc.y = acc.y * was + f * v.y;
-        acc.z = acc.z * was + f * v.z;
-        acc.w = acc.w * was + f * v.w;
-        l_r = l_r * was + f * lx;
-        m_r = now;
+      float m_r[JOIN], l_r[JOIN];
+      float4 acc[JOIN];
+      auto add = [&](int c, float mx, float lx, const float4 &v) {
+        const float now = fmaxf(m_r[c], mx);
+        const float was = m_r[c] == -INFINITY ? 0.f : exp2_fast(m_r[c] - now);
+        const float f = mx == -INFINITY ? 0.f : exp2_fast(mx - now);
+        acc[c].x = acc[c].x * was + f * v.x;
+        acc[c].y = acc[c].y * was + f * v.y;
+        acc[c].z = acc[c].z * was + f * v.z;
+        acc[c].w = acc[c].w * was + f * v.w;
+        l_r[c] = l_r[c] * was + f * lx;
+        m_r[c] = now;
       };
-      for (int x0 = team; mine && x0 < np; x0 += 8 * teams) {
-        float4 v[8];
-        float mx[8], lx[8];
+      bool mine[JOIN];
+      int r[JOIN], d[JOIN];
+#pragma unroll
+      for (int c = 0; c < JOIN; ++c) {
+        mine[c] = team < teams && i + c * THREADS < cols;
+        const int j = min(i + c * THREADS, cols - 1);
+        r[c] = j / COL4, d[c] = (j - r[c] * COL4) * 4;
+        m_r[c] = -INFINITY, l_r[c] = 0.f;
+        acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      for (int x0 = team; mine[0] && x0 < np; x0 += 8 * teams) {
+        float4 v[8][JOIN];
+        float mx[8][JOIN], lx[8][JOIN];
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           if (x0 + x * teams < np) {
             const float *s = slot(x0 + x * teams);
-            v[x] = __ldcg(reinterpret_cast<const float4 *>(s) + i);
-            mx[x] = __ldcg(s + ROWS * DP + r);
-            lx[x] = __ldcg(s + ROWS * DP + ROWS + r);
+#pragma unroll
+            for (int c = 0; c < JOIN; ++c) {
+              v[x][c] = __ldcg(reinterpret_cast<const float4 *>(s + r[c] * DP + d[c]));
+              mx[x][c] = __ldcg(s + ROWS * DP + r[c]);
+              lx[x][c] = __ldcg(s + ROWS * DP + ROWS + r[c]);
+            }
           }
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          if (x0 + x * teams < np) add(mx[x], lx[x], v[x]);
+          if (x0 + x * teams < np)
+#pragma unroll
+            for (int c = 0; c < JOIN; ++c) add(c, mx[x][c], lx[x][c], v[x][c]);
       }
       if (teams > 1) {
         __syncthreads();
-        if (mine && team > 0) {
-          team_o[(team - 1) * cols + i] = acc;
-          if (d == 0) team_ml[team - 1][r] = make_float2(m_r, l_r);
+        if (mine[0] && team > 0) {
+          team_o[(team - 1) * cols + i] = acc[0];
+          if (d[0] == 0) team_ml[team - 1][r[0]] = make_float2(m_r[0], l_r[0]);
         }
         __syncthreads();
-        if (mine && team == 0)
-          for (int t = 0; t + 1 < teams; ++t) add(team_ml[t][r].x, team_ml[t][r].y, team_o[t * cols + i]);
+        if (mine[0] && team == 0)
+          for (int t = 0; t + 1 < teams; ++t) add(0, team_ml[t][r[0]].x, team_ml[t][r[0]].y, team_o[t * cols + i]);
       }
-      if (mine && team == 0) {
-        store_out4(p, b, hh + r, d, acc, l_r == 0.f ? 0.f : p.v_scale / l_r);
-        if (d == 0) store_lse(p, b, hh + r, m_r, l_r);
-      }
+#pragma unroll
+      for (int c = 0; c < JOIN; ++c)
+        if (mine[c] && team == 0) {
+          store_out4(p, b, hh + r[c], d[c], acc[c], l_r[c] == 0.f ? 0.f : p.v_scale / l_r[c]);
+          if (d[c] == 0) store_lse(p, b, hh + r[c], m_r[c], l_r[c]);
+        }
     }
     __syncthreads();
   }
@@ -890,7 +940,7 @@ DecodeSpace decode_space(const DecodeParams &p, bool weights) {
     const int64_t rows = decode_rows(p.G), dp = p.D <= 64 ? 64 : p.D <= 128 ? 128 : 256;
     at = round_up(at + grid * 2 * (rows * dp + 2 * rows) * 4, 256);
     s.warp_parts = at;
-    at = round_up(at + grid * 16 * rows * dp * 4, 256);
+    at = round_up(at + grid * 16 * rows * (dp + 4) * 4, 256);
   }
   s.score_row = round_up(int64_t(p.max_pages) * p.P, kTok);
   if (weights) {
