@@ -662,7 +662,8 @@ typedef enum { HICACHE_BF16 = 0, HICACHE_FP16 = 1 } hicache_dtype;
  * fill up a batch carry slot -1.  Two tokens of one call with the same slot
  * leave the row undefined.  q_out may be q itself (same strides), else it must
  * not overlap an input.  q may be NULL (q_heads 0), or k and v (kv_heads 0,
- * slots NULL).  Pointers and strides must be multiples of 16 bytes (ALIGNMENT);
+ * slots NULL); the norm of heads that are not there is left out, its weight not
+ * read.  Pointers and strides must be multiples of 16 bytes (ALIGNMENT);
  * head_dim a multiple of 8 (of 16 into an e4m3 cache), at most 768. */
 typedef struct {
   const void *q;            /* [num_tokens, q_heads, head_dim] of dtype */

@@ -748,3 +748,25 @@ def test_serving_step_through_both_tiers(latent):
             again = attend(1, q, torch.zeros((B, width), device="cuda"))
         torch.cuda.synchronize()
         assert torch.equal(whole, again)
+
+
+# ---- one side of an append -------------------------------------------------------
+
+@pytest.mark.parametrize("d", [96, 128, 576])
+def test_append_one_side_with_both_weights(d):
+    """Queries alone, or keys and values alone, with the other kind's weight given
+    all the same: what a call with both writes."""
+    c = (37, 5, 1, d, 16, "bf16", False, d, d, 64, 0, False, d == 576)
+    q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, 17)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    kv, dd = hc.DeviceKV(bufs, pages), desc(16, d, 2, len(bufs))
+    args = dict(positions=pos, cos_sin=cs, q_weight=qw, k_weight=kw)
+    hc.append_kv(kv, dd, 0, q, k, v, slots, q_out=q_out, **args)
+    want, stored = q_out.clone(), [raw(b).clone() for b in bufs]
+    q_out.zero_()
+    hc.append_kv(kv, dd, 0, q, None, None, None, q_out=q_out, **args)
+    assert torch.equal(q_out, want) and all(torch.equal(raw(b), s) for b, s in zip(bufs, stored))
+    for b in bufs:
+        b.view(torch.uint8)[:] = 0x5A
+    hc.append_kv(kv, dd, 0, None, k, v, slots, **args)
+    assert all(torch.equal(raw(b), s) for b, s in zip(bufs, stored))

@@ -1,0 +1,100 @@
+"""What hicache_append_kv hands its kernel, read on the CPU: the library's own
+objects, with a stand-in for the launch that prints the parameters.  Addresses
+are made up; nothing is read."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+MAIN = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include "hicache.h"
+#include "hicache_serving.h"
+namespace hicache {
+int launch_append(const AppendParams &p, void *) {
+  std::printf("q_norm=%d k_norm=%d q_st=%lld q_sh=%lld o_st=%lld o_sh=%lld k_st=%lld k_sh=%lld v_st=%lld v_sh=%lld ",
+              p.q_norm, p.k_norm, (long long)p.q_st, (long long)p.q_sh, (long long)p.o_st, (long long)p.o_sh,
+              (long long)p.k_st, (long long)p.k_sh, (long long)p.v_st, (long long)p.v_sh);
+  return 0;
+}
+}  // namespace hicache
+// arguments: name=value, over a plain call of 3 tokens, 4 query and 2 kv heads of 128
+int main(int argc, char **argv) {
+  const long long A = 1 << 20;
+  char *const base = reinterpret_cast<char *>(A);
+  hicache_pool_desc d{};
+  d.num_layers = 1, d.num_buffers = 2, d.page_size = 16, d.elem_bytes = 2, d.row_elems = 256, d.host_num_pages = 1;
+  void *bufs[2] = {base, base};
+  hicache_device_kv kv{};
+  kv.buf_ptrs = bufs, kv.device_num_pages = 10;
+  hicache_append_desc a{};
+  a.q = a.q_out = base, a.k = a.v = a.q_weight = a.k_weight = base;
+  a.slots = reinterpret_cast<int64_t *>(base);
+  a.q_token_stride = a.q_out_token_stride = 512, a.q_head_stride = a.q_out_head_stride = 128;
+  a.k_token_stride = a.v_token_stride = 256, a.k_head_stride = a.v_head_stride = 128;
+  a.num_tokens = 3, a.q_heads = 4, a.kv_heads = 2, a.head_dim = 128, a.q_norm_dim = a.k_norm_dim = 128;
+  a.eps = 1e-6f, a.k_scale = a.v_scale = 1.f;
+  for (int i = 1; i < argc; ++i) {
+    const char *eq = std::strchr(argv[i], '=');
+    const size_t n = size_t(eq - argv[i]);
+    const long long x = std::atoll(eq + 1);
+    auto is = [&](const char *s) { return std::strlen(s) == n && !std::strncmp(argv[i], s, n); };
+    if (is("q_heads")) a.q_heads = int(x);
+    else if (is("kv_heads")) a.kv_heads = int(x);
+    else if (is("row")) d.row_elems = x;
+    else if (is("n")) a.num_tokens = x;
+    else if (is("q_weight")) a.q_weight = reinterpret_cast<void *>(x);
+    else if (is("k_weight")) a.k_weight = reinterpret_cast<void *>(x);
+    else if (is("qst")) a.q_token_stride = x;
+    else if (is("qsh")) a.q_head_stride = x;
+    else if (is("ost")) a.q_out_token_stride = x;
+    else if (is("osh")) a.q_out_head_stride = x;
+    else if (is("kst")) a.k_token_stride = x;
+    else if (is("ksh")) a.k_head_stride = x;
+    else if (is("vst")) a.v_token_stride = x;
+    else if (is("vsh")) a.v_head_stride = x;
+    else return 1;
+  }
+  std::printf("rc=%d\n", hicache_append_kv(&kv, &d, 0, &a, nullptr));
+  return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def params(tmp_path_factory):
+    """Runs a call with some arguments changed: its return code and the kernel's parameters."""
+    from tiered_kv_cache_gb300 import build as b
+    b.build()
+    d = tmp_path_factory.mktemp("params")
+    (d / "m.cpp").write_text(MAIN)
+    cuda = "/usr/local/cuda"
+    objs = [os.path.join(b.BUILD, s + ".o") for s in b.SOURCES if s != "hicache_append.cu"]
+    subprocess.check_call(["g++", "-std=c++17", f"-I{ROOT}/tiered_kv_cache_gb300/csrc", f"-I{ROOT}/include",
+                           f"-I{cuda}/include", str(d / "m.cpp"), *objs, f"-L{cuda}/lib64", "-lcudart_static", "-ldl",
+                           "-lrt", "-lpthread", "-o", str(d / "m")])
+
+    def run(**change):
+        r = subprocess.run([str(d / "m")] + [f"{k}={v}" for k, v in change.items()], capture_output=True, text=True,
+                           check=True)
+        return {k: int(v) for k, v in (x.split("=") for x in r.stdout.split())}
+    return run
+
+
+def test_plain_call(params):
+    p = params()
+    assert (p["rc"], p["q_norm"], p["k_norm"]) == (0, 128, 128)
+
+
+@pytest.mark.parametrize("weight", [0, (1 << 20) + 2])
+def test_weights_of_absent_heads_are_not_read(params, weight):
+    """A call of queries alone, or of keys and values alone: the norm of the
+    other kind, whose weight may be NULL or at any address, is left out."""
+    p = params(kv_heads=0, k_weight=weight)
+    assert (p["rc"], p["q_norm"], p["k_norm"]) == (0, 128, 0)
+    p = params(q_heads=0, q_weight=weight)
+    assert (p["rc"], p["q_norm"], p["k_norm"]) == (0, 0, 128)

@@ -230,8 +230,8 @@ int hicache_append_kv(const hicache_device_kv *kv, const hicache_pool_desc *desc
   p.q_heads = a->q_heads;
   p.kv_heads = a->kv_heads;
   p.D = a->head_dim;
-  p.q_norm = a->q_norm_dim;
-  p.k_norm = a->k_norm_dim;
+  p.q_norm = a->q_heads > 0 ? a->q_norm_dim : 0;    // the kernels read the weights of a norm
+  p.k_norm = a->kv_heads > 0 ? a->k_norm_dim : 0;   // wherever there is one
   p.rot = a->rot_dim;
   p.rot_off = a->rot_offset;
   p.interleaved = a->interleaved != 0;
