@@ -770,3 +770,40 @@ def test_append_one_side_with_both_weights(d):
         b.view(torch.uint8)[:] = 0x5A
     hc.append_kv(kv, dd, 0, None, k, v, slots, **args)
     assert all(torch.equal(raw(b), s) for b, s in zip(bufs, stored))
+
+
+# ---- the largest batches ---------------------------------------------------------
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("batch", [32767, 32768, 40000, 65535])
+def test_decode_mostly_empty_large_batches(latent, batch):
+    """Tens of thousands of sequences, all but a few empty, on a workspace that a
+    call of another shape has filled."""
+    d, dv = (576, 512) if latent else (64, 64)
+    full = {0: 5, batch // 2: 130, batch - 1: 40}
+    lens = [full.get(i, 0) for i in (0, batch // 2, batch - 1)]
+    s = decode_inputs(lens, 2, 2, d, 16, latent=latent, seed=batch)
+    small = torch.empty((3, 2, dv), dtype=s["dt"], device="cuda")
+    plain_call(s, small, workspace(s, 2, d, dv, False))
+    q = torch.zeros((batch, 2, d), dtype=s["dt"], device="cuda")
+    table = torch.full((batch, s["width"]), -1, dtype=torch.int32, device="cuda")
+    n = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    at = list(full)
+    q[at], table[at], n[at] = s["q"], s["table"], s["lens"]
+    other = decode_inputs([3000, 900], 64, 2 if not latent else 1, d, 16, latent=latent, seed=1, width=400)
+    size = max(hc.decode_workspace(s["desc"], batch, 2, d, dv, s["width"], True),
+               hc.decode_workspace(other["desc"], 2, 64, d, dv, other["width"], True))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    plain_call(other, torch.empty((2, 64, dv), dtype=s["dt"], device="cuda"), ws,
+               weights=torch.zeros((2, other["width"]), device="cuda"))
+    out = torch.full((batch, 2, dv), 3.0, dtype=s["dt"], device="cuda")
+    lse = torch.full((batch, 2), 3.0, device="cuda")
+    s["q"], s["table"], s["lens"] = q, table, n
+    plain_call(s, out, ws, lse=lse)
+    empty = n == 0
+    assert (out[empty] == 0).all() and (lse[empty] == -torch.inf).all()
+    assert (lse[at] > -torch.inf).all()
+    # the few others as in a batch of their own, up to how they are cut: the
+    # exponentials' rounding, the sums' and the final one
+    bound = 2.0 ** -6 * max(b[b == b].abs().max().item() for b in s["bufs"])
+    assert ((out[at].float() - small.float()).abs() <= bound).all()

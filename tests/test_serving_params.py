@@ -98,3 +98,27 @@ def test_weights_of_absent_heads_are_not_read(params, weight):
     assert (p["rc"], p["q_norm"], p["k_norm"]) == (0, 128, 0)
     p = params(q_heads=0, q_weight=weight)
     assert (p["rc"], p["q_norm"], p["k_norm"]) == (0, 0, 128)
+
+
+def run_host(tmp_path, body):
+    """Compiles and runs a program over the kernels' header; its output."""
+    src, exe = tmp_path / "h.cpp", tmp_path / "h"
+    src.write_text('#include <climits>\n#include <cstdio>\n#include "hicache_serving.h"\nusing namespace hicache;\n'
+                   "int main() {\n" + body + '\n  std::puts("ok");\n}\n')
+    subprocess.check_call(["g++", "-std=c++17", f"-I{ROOT}/tiered_kv_cache_gb300/csrc", f"-I{ROOT}/include",
+                           "-I/usr/local/cuda/include", str(src), "-o", str(exe)])
+    return subprocess.run([str(exe)], capture_output=True, text=True).stdout.strip()
+
+
+def test_idle_sequences_are_counted_to_the_largest_batch(tmp_path):
+    """Strips and idle sequences of one sum, at and around 2^15 idle ones and at
+    the largest batch."""
+    assert run_host(tmp_path, """
+  const uint64_t idle[] = {0, 1, 2, 32767, 32768, 32769, 40000, 65534, 65535};
+  const int64_t strips[] = {0, 1, 5, (int64_t(1) << 42) + 3, (int64_t(1) << 48) - 1};
+  for (uint64_t i : idle)
+    for (int64_t s : strips) {
+      uint64_t sum = uint64_t(s);
+      for (uint64_t k = 0; k < i; ++k) sum += kIdleSeq;
+      if (idle_seqs(sum) != i || strips_in(sum) != s) return 1;
+    }""") == "ok"

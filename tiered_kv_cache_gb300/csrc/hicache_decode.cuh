@@ -76,17 +76,17 @@ __device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int h, f
 
 // Exclusive prefix sums over the CTA's threads (WARPS of them) of `mine`; the
 // total in *total.  Ends with every thread past its reads of `scratch`.
-template <int WARPS>
-__device__ __forceinline__ long long block_prefix(long long mine, long long *scratch, long long *total) {
+template <int WARPS, class T>
+__device__ __forceinline__ T block_prefix(T mine, T *scratch, T *total) {
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  long long inc = mine;
+  T inc = mine;
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    const T y = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += y;
   }
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  long long before = 0, all = 0;
+  T before = 0, all = 0;
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += scratch[w];
     all += scratch[w];

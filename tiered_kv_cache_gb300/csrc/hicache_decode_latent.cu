@@ -256,7 +256,8 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ unsigned char smem_raw[];
   constexpr int NH = C::NH, NS = C::NS, THREADS = C::THREADS;
-  __shared__ long long prefix[THREADS + 1], scratch[C::WARPS];
+  __shared__ long long prefix[THREADS + 1];
+  __shared__ unsigned long long scratch[C::WARPS];
   __shared__ int lens_s[kLens];
   __shared__ __align__(8) unsigned long long bars[4 + C::DUOS + C::ROPES + 9];
   // per head: the maximum (and what scores are taken relative to: 0 while there is
@@ -279,19 +280,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
-  // the strips before each sequence; above 2^48, the sequences without any
+  // the strips before each sequence, and whether there are sequences without any
   const int per = (p.B + THREADS - 1) / THREADS;
-  long long mine = 0, total = 0;
+  unsigned long long mine = 0, sum = 0;
   for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
     int start, len;
     seq_range(p, b, &start, &len);
     if (b < kLens) lens_s[b] = len;
-    mine += len > start ? strips_of(start, len) : 1ll << 48;
+    mine += len > start ? uint64_t(strips_of(start, len)) : kIdleSeq;
   }
-  constexpr long long kStrips = (1ll << 48) - 1;
-  const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total) & kStrips;
-  const bool idle = total > kStrips;
-  total &= kStrips;
+  const long long ahead = strips_in(block_prefix<C::WARPS>(mine, scratch, &sum));
+  const bool idle = idle_seqs(sum) > 0;
+  const long long total = strips_in(sum);
   prefix[tid] = ahead;
   if (tid == 0) {
     prefix[THREADS] = total;

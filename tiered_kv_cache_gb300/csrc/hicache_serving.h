@@ -68,6 +68,12 @@ DecodeSpace decode_space(const DecodeParams &p, bool weights);
 int launch_decode(const DecodeParams &p, int device, void *stream, int *launches);
 int launch_decode_latent(const DecodeParams &p, int device, void *stream, int *launches);
 
+// A sum over sequences of their strips of work, in which a sequence without any
+// counts kIdleSeq: unsigned, so that 65,535 of them and 2^48 - 1 strips fit.
+constexpr uint64_t kIdleSeq = uint64_t(1) << 48;
+HC_HD uint64_t idle_seqs(uint64_t sum) { return sum / kIdleSeq; }
+HC_HD int64_t strips_in(uint64_t sum) { return int64_t(sum % kIdleSeq); }
+
 // Whether a page table's entry is a page of the cache (else it counts as absent).
 HC_HD bool page_present(int32_t page, int64_t num_pages) { return page >= 0 && page < num_pages; }
 
