@@ -122,3 +122,19 @@ def test_idle_sequences_are_counted_to_the_largest_batch(tmp_path):
       for (uint64_t k = 0; k < i; ++k) sum += kIdleSeq;
       if (idle_seqs(sum) != i || strips_in(sum) != s) return 1;
     }""") == "ok"
+
+
+def test_pieces_to_join(tmp_path):
+    """Every piece that a join reads lies in the workspace, whatever the words say."""
+    assert run_host(tmp_path, """
+  const int e[] = {INT_MIN, INT_MIN + 1, -153, -152, -1, 0, 1, 2, 3, 37, 38, 75, 76, 77, 150, 151, 152, 153,
+                   0x3f800000, 0x7f800000, INT_MAX - 1, INT_MAX};
+  for (int QB = 1; QB <= 64; ++QB) {
+    const long long groups = kDecodeCtas / QB;
+    for (int x : e)
+      for (int y : e) {
+        const bool want = y >= 2 && x >= 0 && (long long)x + y <= groups;
+        if (pieces_to_join(x, y, QB) != want) return 1;
+        if (want && (((long long)x + y - 1) * QB + QB - 1) >= kDecodeCtas) return 2;
+      }
+  }""") == "ok"

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(128 * PARTS) latent_join_kernel(const __grid_c
   __shared__ float m_s[PARTS], l_s[PARTS];
   const int b = int(blockIdx.x) / p.Hq, h = int(blockIdx.x) - b * p.Hq;
   const int2 at = __ldcg(p.seq_pieces + b);
-  if (at.y < 2) return;
+  if (!pieces_to_join(at.x, at.y, p.QB)) return;
   const int qb = h / NH, r = h - qb * NH, tid = int(threadIdx.x) & 127, part = int(threadIdx.x) >> 7;
   auto slot = [&](int x) { return p.cta_parts + (int64_t((at.x + x) * p.QB + qb) * 2 + (x == 0 ? 1 : 0)) * PIECE; };
   float m = -INFINITY, sum = 0.f;

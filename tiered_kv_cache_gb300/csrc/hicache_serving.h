@@ -74,6 +74,14 @@ constexpr uint64_t kIdleSeq = uint64_t(1) << 48;
 HC_HD uint64_t idle_seqs(uint64_t sum) { return sum / kIdleSeq; }
 HC_HD int64_t strips_in(uint64_t sum) { return int64_t(sum % kIdleSeq); }
 
+// Whether a latent sequence's pieces are those of several of the call's groups of
+// CTAs, QB CTAs each: `first` the one it begins in, `count` of them.  A call that gave
+// up leaves the words of sequences it did not reach as another shape's call left them.
+HC_HD bool pieces_to_join(int32_t first, int32_t count, int32_t QB) {
+  const int32_t groups = kDecodeCtas / QB;
+  return count >= 2 && first >= 0 && first < groups && count <= groups - first;
+}
+
 // Whether a page table's entry is a page of the cache (else it counts as absent).
 HC_HD bool page_present(int32_t page, int64_t num_pages) { return page >= 0 && page < num_pages; }
 
