@@ -807,3 +807,21 @@ def test_decode_mostly_empty_large_batches(latent, batch):
     # exponentials' rounding, the sums' and the final one
     bound = 2.0 ** -6 * max(b[b == b].abs().max().item() for b in s["bufs"])
     assert ((out[at].float() - small.float()).abs() <= bound).all()
+
+
+# ---- the workspace's error word --------------------------------------------------
+
+def test_decode_status_and_clear():
+    """The error word (behind one counter per CTA), set by hand: reported until it
+    is cleared, left alone by calls in between, which are right all the same."""
+    s = decode_inputs([700, 90], 16, 1, 576, 16, latent=True)
+    ws = workspace(s, 16, 576, 512, False)
+    a, b, c = (torch.zeros((2, 16, 512), dtype=s["dt"], device="cuda") for _ in range(3))
+    plain_call(s, a, ws)
+    assert not hc.decode_gave_up(ws)
+    ws.view(torch.int32)[152] = 1
+    assert hc.decode_gave_up(ws)
+    plain_call(s, b, ws)
+    assert hc.decode_gave_up(ws) and hc.decode_gave_up(ws, clear=True) and not hc.decode_gave_up(ws)
+    plain_call(s, c, ws)
+    assert not hc.decode_gave_up(ws) and torch.equal(a, b) and torch.equal(a, c) and a.any()

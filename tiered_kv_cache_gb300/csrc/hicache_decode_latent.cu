@@ -91,7 +91,9 @@ __device__ __forceinline__ void mbar_arrive_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 constexpr long long kWaitClocks = 4000000000ll;   // about two seconds
-// Waits for the phase `parity` to end; false once a wait of the CTA has run out.
+// Waits for the phase `parity` to end; false once a wait of the CTA has run out (LAST:
+// only once this one has).
+template <bool LAST = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
   long long since = 0;
   for (;;) {
@@ -102,7 +104,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         : "r"(bar), "r"(parity)
         : "memory");
     if (done) return true;
-    if (*gave_up) return false;
+    if (!LAST && *gave_up) return false;
     const long long now = clock64();
     if (since == 0) since = now;
     if (now - since > kWaitClocks) {
@@ -721,13 +723,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
   }
   __syncthreads();
   if (warp == C::S_WARP) {
-    // nothing is in flight when the tensor memory is given back
-    mbar_wait(bar(LAST), 0, &gave_up);
+    // nothing is in flight when the tensor memory is given back, after a wait that ran
+    // out neither: the products that were issued end by themselves
+    mbar_wait<true>(bar(LAST), 0, &gave_up);
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::COLS) : "memory");
+    // every role has passed its waits, and this was the last one
+    if (lane == 0 && *static_cast<volatile int *>(&gave_up)) p.counters[kDecodeCtas] = 1u;
   }
-  if (tid == 0 && gave_up) p.counters[kDecodeCtas] = 1u;
 }
 
 // Adds the pieces of a sequence that several groups of CTAs share; a block per
