@@ -727,8 +727,9 @@ int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32
 /* Whether a call with this workspace has given up: the kernel over a latent cache
  * waits for its own copies and products with a limit of about two seconds, and a
  * wait that runs out (it never should) ends the call with its outputs undefined
- * and marks the workspace, *gave_up = 1 until `clear`.  Reads device memory
- * synchronously.  Errors: INVALID_ARG, CUDA. */
+ * and marks the workspace, *gave_up = 1 until `clear`.  Waits for all work of
+ * the current device, on every stream; not during a capture.  Errors:
+ * INVALID_ARG, ALIGNMENT, CUDA. */
 int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
 
 /* Which pages of each sequence leave L1: those that received the least

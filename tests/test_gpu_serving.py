@@ -825,3 +825,16 @@ def test_decode_status_and_clear():
     assert hc.decode_gave_up(ws) and hc.decode_gave_up(ws, clear=True) and not hc.decode_gave_up(ws)
     plain_call(s, c, ws)
     assert not hc.decode_gave_up(ws) and torch.equal(a, b) and torch.equal(a, c) and a.any()
+
+
+def test_decode_status_waits_for_every_stream():
+    """Work still to run on a stream that does not block the default one."""
+    ws = torch.zeros(1024, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(200_000_000)            # about a tenth of a second
+        ws.view(torch.int32)[152] = 1
+    assert hc.decode_gave_up(ws, clear=True)
+    with torch.cuda.stream(st):
+        assert ws.view(torch.int32)[152].item() == 0

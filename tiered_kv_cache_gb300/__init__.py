@@ -939,7 +939,7 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
 
 def decode_gave_up(workspace, clear: bool = False) -> bool:
     """Whether a call with this workspace gave up waiting (it never should): its
-    outputs are undefined then.  Synchronous."""
+    outputs are undefined then.  Waits for all work of the current device."""
     out = ctypes.c_int32()
     _check(library().hicache_decode_status(workspace.data_ptr(), ctypes.byref(out), int(clear)))
     return bool(out.value)

@@ -337,8 +337,11 @@ int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear) {
   if (!workspace || !gave_up) return set_error(HICACHE_ERR_INVALID_ARG, "workspace or gave_up is NULL");
   if (!aligned(workspace, 256)) return set_error(HICACHE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
   unsigned int *word = static_cast<unsigned int *>(workspace) + hicache::kDecodeCtas, x = 0;
-  cudaError_t e = cudaMemcpy(&x, word, sizeof(x), cudaMemcpyDeviceToHost);
+  // a copy on the default stream alone would pass calls on streams that do not block it
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&x, word, sizeof(x), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && clear) e = cudaMemset(word, 0, sizeof(x));
+  if (e == cudaSuccess && clear) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_error(e, "decode status");
   *gave_up = x != 0;
   return HICACHE_OK;
