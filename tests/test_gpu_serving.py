@@ -838,3 +838,17 @@ def test_decode_status_waits_for_every_stream():
     assert hc.decode_gave_up(ws, clear=True)
     with torch.cuda.stream(st):
         assert ws.view(torch.int32)[152].item() == 0
+
+
+# ---- eviction: the ends of the ranges --------------------------------------------
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_protects_everything(in_place):
+    """sink and recent at and near the largest 32-bit number."""
+    big = 2 ** 31 - 1
+    w = [[float((5 * i + j) % 7) for j in range(12)] for i in range(4)]
+    table = [[20 * i + j for j in range(12)] for i in range(4)]
+    for sink, recent in ((0, big), (4, big), (big, 1), (big, big), (5, big - 3), (big - 1, 2), (1 << 30, 1 << 30)):
+        run_evict(table, w, [48, 4, 8, 0], [0, 0, -1, 2], 4, sink, recent, 12, in_place)
+    rows = [[float((3 * j) % 11) for j in range(5000)]] * 2
+    run_evict([list(range(5000))] * 2, rows, [5000, 2], [1, 0], 1, 4, big, 5000, in_place)

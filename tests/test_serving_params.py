@@ -138,3 +138,24 @@ def test_pieces_to_join(tmp_path):
         if (want && (((long long)x + y - 1) * QB + QB - 1) >= kDecodeCtas) return 2;
       }
   }""") == "ok"
+
+
+def test_evict_count_at_the_ends_of_the_range(tmp_path):
+    """Pages that leave, against 128 bits, for sinks, recent pages and budgets up
+    to the largest; the first page that is too recent stays in 32 bits."""
+    assert run_host(tmp_path, """
+  const int e[] = {0, 1, 2, 3, 7, 100, 4096, INT_MAX / 2, INT_MAX - 1025, INT_MAX - 1, INT_MAX};
+  for (int n : e)
+    for (int sink : e)
+      for (int recent : e)
+        for (int keep : {INT_MIN, -1, 0, 1, 2, 3, 100, INT_MAX})
+          for (int cap : e) {
+            if (recent < 1) continue;
+            __int128 may = 0, over = (__int128)n - (keep > 0 ? keep : 0), want;
+            if ((__int128)n - recent > sink) may = (__int128)n - recent - sink;
+            want = over < 0 ? 0 : over;
+            if (may < want) want = may;
+            if (cap < want) want = cap;
+            if (evict_count(n, sink, recent, keep, cap) != want) return 1;
+            if ((__int128)n - recent < INT_MIN) return 2;
+          }""") == "ok"

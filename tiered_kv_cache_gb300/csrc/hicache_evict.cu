@@ -44,8 +44,7 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictParams &p, int64_t b) {
   const int64_t pages = s.len > 0 ? (int64_t(s.len) + p.P - 1) / p.P : 0;
   s.n = int(pages < p.max_pages ? pages : p.max_pages);
   s.last = s.n - p.recent;
-  const int may = max(0, s.last - p.sink);
-  s.count = min(min(max(0, s.n - max(0, p.keep[b])), may), p.max_victims);
+  s.count = evict_count(s.n, p.sink, p.recent, p.keep[b], p.max_victims);
   return s;
 }
 
