@@ -103,7 +103,7 @@ def test_weights_of_absent_heads_are_not_read(params, weight):
 def run_host(tmp_path, body):
     """Compiles and runs a program over the kernels' header; its output."""
     src, exe = tmp_path / "h.cpp", tmp_path / "h"
-    src.write_text('#include <climits>\n#include <cstdio>\n#include "hicache_serving.h"\nusing namespace hicache;\n'
+    src.write_text('#include <climits>\n#include <cstdio>\n#include <initializer_list>\n#include "hicache_serving.h"\nusing namespace hicache;\n'
                    "int main() {\n" + body + '\n  std::puts("ok");\n}\n')
     subprocess.check_call(["g++", "-std=c++17", f"-I{ROOT}/tiered_kv_cache_gb300/csrc", f"-I{ROOT}/include",
                            "-I/usr/local/cuda/include", str(src), "-o", str(exe)])
