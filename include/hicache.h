@@ -733,10 +733,12 @@ int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32
 int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
 
 /* Which pages of each sequence leave L1: those that received the least
- * attention.  With n = ceil(seq_lens[b] / page_size) pages, the pages in [sink,
- * n - recent) may go, and count = min(max(0, n - keep[b]), their number,
- * max_victims) of them do: those with the lowest weights[b, p], the lowest p
- * first among equals (-0 equals 0; NaN ranks above infinity).
+ * attention.  With n = ceil(seq_lens[b] / page_size) pages, those in [sink, n -
+ * recent) that are present (a negative entry of the table is an absent page)
+ * may go, and count = min(max(0, n - keep[b]), their number, max_victims) of
+ * them do: those with the lowest weights[b, p], the lowest p first among equals
+ * (-0 equals 0; NaN ranks above infinity).  Absent pages keep their place in the
+ * table and count among the n and the pages kept.
  *   victims[b, 0..count)        their page_table entries, in the order of p
  *   num_victims[b]              count
  *   out_table[b, 0..n-count)    the other entries, in order; [n-count, n) -> -1
@@ -751,7 +753,7 @@ typedef struct {
   const int32_t *page_table;  /* [batch, max_pages] */
   const float *weights;       /* [batch, max_pages] */
   const int32_t *seq_lens;    /* [batch] */
-  const int32_t *keep;        /* [batch]: pages to keep */
+  const int32_t *keep;        /* [batch]: pages to keep, absent ones among them */
   int32_t *victims;           /* [batch, max_victims] */
   int32_t *num_victims;       /* [batch] */
   int32_t *out_table;         /* [batch, max_pages] */

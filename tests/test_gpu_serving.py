@@ -852,3 +852,36 @@ def test_evict_protects_everything(in_place):
         run_evict(table, w, [48, 4, 8, 0], [0, 0, -1, 2], 4, sink, recent, 12, in_place)
     rows = [[float((3 * j) % 11) for j in range(5000)]] * 2
     run_evict([list(range(5000))] * 2, rows, [5000, 2], [1, 0], 1, 4, big, 5000, in_place)
+
+
+def evict_present(table, weights, lens, keep, page, sink, recent, cap):
+    """serving_reference.evict where absent pages (negative entries) stay."""
+    res = []
+    for t, w, n_t, k in zip(table, weights, lens, keep):
+        n = min(len(t), -(-n_t // page)) if n_t > 0 else 0
+        may = [p for p in range(sink, max(sink, n - recent)) if t[p] >= 0]
+        count = min(max(0, n - max(0, k)), len(may), cap)
+        gone = set(sorted(may, key=lambda p: (w[p] != w[p], w[p] if w[p] == w[p] else 0.0, p))[:count])
+        stay = [p for p in range(n) if p not in gone]
+        res.append(([t[p] for p in sorted(gone)], [t[p] for p in stay] + [-1] * count,
+                    [w[p] for p in stay] + [0.0] * count, n_t - count * page))
+    return res
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,b,share", [(1, 2, 0.5), (9, 6, 0.5), (40, 5, 0.9), (1025, 3, 0.3), (4096, 2, 1.0),
+                                       (5000, 3, 0.5), (40000, 2, 0.99), (196609, 1, 0.2), (393217, 1, 0.5)])
+def test_evict_absent_pages(monkeypatch, n, b, share, in_place):
+    """Pages that are not on the device never leave, whatever their weight: not
+    where fewer are present than asked for, nor where none is."""
+    monkeypatch.setattr(ref, "evict", evict_present)
+    rng = np.random.default_rng(n)
+    table = rng.integers(0, 10 ** 6, (b, n))
+    table[rng.random((b, n)) < share] = -1
+    table[0, 0] = -2 ** 31
+    w = rng.integers(0, 6, (b, n)).astype(np.float32)
+    w[table < 0] *= rng.integers(0, 2)            # an absent page receives no attention, as a rule
+    lens = [3 * n - 1] + [int(x) for x in rng.integers(0, 3 * n + 1, b - 1)]
+    for keep in (0, n // 3, n - 1):
+        run_evict(table.tolist(), w.tolist(), lens, [keep] * b, 3, 2, 1, n, in_place, pad=3)
+        run_evict(table.tolist(), w.tolist(), lens, [keep] * b, 3, 0, 1, max(1, n // 5), in_place)

@@ -947,7 +947,8 @@ def decode_gave_up(workspace, clear: bool = False) -> bool:
 
 def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, num_victims, *, sink: int = 0,
                 recent: int = 1, out_table=None, out_lens=None, out_weights=None, stream=None):
-    """Of each sequence's pages in [sink, n - recent), the ones with the lowest
+    """Of each sequence's pages in [sink, n - recent) that are present (entries
+    below 0 are absent pages, which keep their place), the ones with the lowest
     weights leave until keep[b] are left (or none may go, or victims is full):
     victims [batch, max_victims] receives their pages, num_victims their number,
     and out_table, out_lens, out_weights (None: in place) what stays."""

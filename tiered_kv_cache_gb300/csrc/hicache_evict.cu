@@ -34,7 +34,8 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-// A sequence's pages: n in all, those in [sink, last) may go, `count` of them do.
+// A sequence's pages: n in all, those present in [sink, last) may go, at most `count` of
+// them do (how many are present is known with the first histogram).
 struct EvictSeq {
   int len, n, last, count;
 };
@@ -48,8 +49,9 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictParams &p, int64_t b) {
   return s;
 }
 
-// The digit of the need-th lowest key in `hist` (256 counts), the rank left within it
-// and whether that is all the keys with this digit, into pick[0..2]; for one warp.
+// The digit of the need-th lowest key in `hist` (256 counts; the last one if there are
+// fewer), the rank left within it and whether that is all the keys with this digit, into
+// pick[0..2], min(need, keys) into pick[3]; for one warp.
 __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, uint32_t *pick, int lane) {
   uint32_t c[8], sum = 0;
 #pragma unroll
@@ -59,6 +61,8 @@ __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, 
     const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
     if (lane >= o) before += y;
   }
+  need = min(need, __shfl_sync(0xffffffffu, before, 31));
+  if (lane == 0) pick[3] = need;
   before -= sum;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -74,7 +78,7 @@ __device__ __forceinline__ void pick_digit(const uint32_t *hist, uint32_t need, 
 // `cap`: pages that a CTA's dynamic shared memory holds (8 bytes each).
 __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __grid_constant__ EvictParams p, int cap) {
   extern __shared__ __align__(16) unsigned char pages_smem[];
-  __shared__ uint32_t hist[2][256], total[256], pick[3];
+  __shared__ uint32_t hist[2][256], total[256], pick[4];
   __shared__ uint32_t warp_below[32], warp_equal[32], cta_count[2], ahead[2];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   float *const w_s = reinterpret_cast<float *>(pages_smem);
@@ -90,7 +94,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
       __syncthreads();
   };
   const EvictSeq q = evict_seq(p, b);
-  const int n = q.n, count = q.count;
+  const int n = q.n;
+  int count = q.count;
   const int slice = min(cap, ((n + cs - 1) / cs + 31) & ~31);
   const int lo = min(n, rank * slice), mine = min(n, lo + slice) - lo;
   for (int i = tid; i < mine; i += kEvictThreads) {
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
       uint32_t *h = hist[pass & 1];
       for (int i = from + tid; i < to; i += kEvictThreads) {
         const uint32_t k = order_key(w_s[i]);
-        if ((k & mask) == key) atomicAdd(&h[(k >> shift) & 255], 1u);
+        if (t_s[i] >= 0 && (k & mask) == key) atomicAdd(&h[(k >> shift) & 255], 1u);
       }
       sync();
       if (tid < 256) {
@@ -124,6 +129,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
       __syncthreads();
       if (warp == 0) pick_digit(total, need, pick, lane);
       __syncthreads();
+      if (pass == 0) count = int(pick[3]);
+      if (count == 0) break;
       key |= pick[0] << shift;
       mask |= 255u << shift;
       need = pick[1];
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
   const int w0 = min(mine, warp * run), w1 = min(mine, w0 + run);
   auto flags = [&](int i, bool *below, bool *equal) {
     *below = *equal = false;
-    if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last) {
+    if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last && t_s[i] >= 0) {
       const uint32_t k = order_key(w_s[i]);
       *below = (k & mask) < key;
       *equal = (k & mask) == key;
@@ -211,13 +218,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
 
 __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[3];
+  __shared__ uint32_t pick[4];
   __shared__ unsigned long long warp_sum[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
   const int64_t b = blockIdx.x;
   const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
   const EvictSeq q = evict_seq(p, b);
-  const int n = q.n, count = q.count, last = q.last;
+  const int n = q.n, last = q.last;
+  int count = q.count;
   const int32_t *table = p.table + b * p.t_sb;
   const float *weights = p.weights + b * p.w_sb;
 
@@ -229,11 +237,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       __syncthreads();
       for (int i = p.sink + tid; i < last; i += kEvictThreads) {
         const uint32_t k = order_key(weights[i]);
-        if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & 255], 1u);
+        if (table[i] >= 0 && (k & mask) == key) atomicAdd(&hist[(k >> shift) & 255], 1u);
       }
       __syncthreads();
       if (warp == 0) pick_digit(hist, need, pick, lane);
       __syncthreads();
+      if (shift == 24) count = int(pick[3]);
+      if (count == 0) break;
       key |= pick[0] << shift;
       mask |= 255u << shift;
       need = pick[1];
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     const int32_t page = in ? table[i] : 0;
     const float w = in ? weights[i] : 0.f;
     uint32_t below = 0, equal = 0;
-    if (count > 0 && i >= p.sink && i < last) {
+    if (count > 0 && i >= p.sink && i < last && page >= 0) {
       const uint32_t k = order_key(w);
       below = k < key;
       equal = k == key;
