@@ -98,12 +98,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
   int count = q.count;
   const int slice = min(cap, ((n + cs - 1) / cs + 31) & ~31);
   const int lo = min(n, rank * slice), mine = min(n, lo + slice) - lo;
+  int absent = 0;
+#pragma unroll 4
   for (int i = tid; i < mine; i += kEvictThreads) {
     w_s[i] = p.weights[b * p.w_sb + lo + i];
     t_s[i] = p.table[b * p.t_sb + lo + i];
+    absent |= t_s[i] < 0;
   }
   if (tid < 512) hist[tid >> 8][tid & 255] = 0;
-  __syncthreads();
+  const bool all_present = !__syncthreads_or(absent);   // of this CTA's: the usual case
 
   // the leading digits (mask) of the key of the last page that leaves, and how many
   // pages with those digits do; once that is all of them, further digits do not matter
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
       uint32_t *h = hist[pass & 1];
       for (int i = from + tid; i < to; i += kEvictThreads) {
         const uint32_t k = order_key(w_s[i]);
-        if (t_s[i] >= 0 && (k & mask) == key) atomicAdd(&h[(k >> shift) & 255], 1u);
+        if ((k & mask) == key && (all_present || t_s[i] >= 0)) atomicAdd(&h[(k >> shift) & 255], 1u);
       }
       sync();
       if (tid < 256) {
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_cluster_kernel(const __gr
   const int w0 = min(mine, warp * run), w1 = min(mine, w0 + run);
   auto flags = [&](int i, bool *below, bool *equal) {
     *below = *equal = false;
-    if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last && t_s[i] >= 0) {
+    if (count > 0 && i < w1 && lo + i >= p.sink && lo + i < q.last && (all_present || t_s[i] >= 0)) {
       const uint32_t k = order_key(w_s[i]);
       *below = (k & mask) < key;
       *equal = (k & mask) == key;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
       __syncthreads();
       for (int i = p.sink + tid; i < last; i += kEvictThreads) {
         const uint32_t k = order_key(weights[i]);
-        if (table[i] >= 0 && (k & mask) == key) atomicAdd(&hist[(k >> shift) & 255], 1u);
+        if ((k & mask) == key && table[i] >= 0) atomicAdd(&hist[(k >> shift) & 255], 1u);
       }
       __syncthreads();
       if (warp == 0) pick_digit(hist, need, pick, lane);

@@ -96,12 +96,13 @@ struct EvictParams {
 };
 int launch_evict(const EvictParams &p, int device, void *stream);
 
-// How many of a sequence's n pages leave: those in [sink, n - recent) may.  In 64 bits:
-// sink and recent go up to 2^31 - 1.
+// How many of a sequence's n pages leave: those in [sink, n - recent) may.  No step
+// leaves 32 bits: none of n, sink and recent is negative, and the second difference is
+// taken only where it is positive.
 HC_HD int32_t evict_count(int32_t n, int32_t sink, int32_t recent, int32_t keep, int32_t max_victims) {
-  const int64_t may = int64_t(n) - recent - sink, over = int64_t(n) - (keep > 0 ? keep : 0);
-  const int64_t most = may < over ? may : over;
-  return int32_t(most <= 0 ? 0 : most < max_victims ? most : max_victims);
+  const int32_t last = n - recent, may = last > sink ? last - sink : 0, over = n - (keep > 0 ? keep : 0);
+  const int32_t most = over < 0 ? 0 : may < over ? may : over;
+  return most < max_victims ? most : max_victims;
 }
 
 }  // namespace hicache
