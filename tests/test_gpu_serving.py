@@ -885,3 +885,65 @@ def test_evict_absent_pages(monkeypatch, n, b, share, in_place):
     for keep in (0, n // 3, n - 1):
         run_evict(table.tolist(), w.tolist(), lens, [keep] * b, 3, 2, 1, n, in_place, pad=3)
         run_evict(table.tolist(), w.tolist(), lens, [keep] * b, 3, 0, 1, max(1, n // 5), in_place)
+
+
+# ---- exponentials at the ends of the products' types ------------------------------
+
+def level_caches(lens, level, value, d, hk, dtype, e4, latent, ks=1.0, vs=1.0):
+    """Caches whose token t of sequence i has the score level(i, t) (log2, with a
+    query of ones at one element) and value(i, t) in every element of V, pages
+    of 16 in order; and the arguments of a call over them."""
+    P, at = 16, 570 if latent else 0
+    counts = [-(-n // P) for n in lens]
+    dp, width = sum(counts), max(counts)
+    row = d if latent else hk * d
+    cache = E4 if e4 else dtype
+    k, v = (torch.zeros((dp * P, hk, d), dtype=torch.float64, device="cuda") for _ in range(2))
+    table, first = [], 0
+    for i, n in enumerate(lens):
+        t = torch.arange(n)
+        lv, val = ([float(f(i, int(x))) for x in t] for f in (level, value))
+        rows = slice(first * P, first * P + n)
+        k[rows, :, at] = torch.tensor(lv, dtype=torch.float64, device="cuda")[:, None]
+        (k[..., :512] if latent else v)[rows] = torch.tensor(val, dtype=torch.float64, device="cuda")[:, None, None]
+        table.append(list(range(first, first + counts[i])) + [-1] * (width - counts[i]))
+        first += counts[i]
+    bufs = [x.reshape(-1, row).float().to(cache) for x in ((k,) if latent else (k, v))]
+    for b, x in zip(bufs, (k, v)):
+        assert torch.equal(b.double(), x.reshape(-1, row)), "not representable"
+    q = torch.zeros((len(lens), 2 * hk, d), dtype=dtype, device="cuda")
+    q[..., at] = 1
+    dd = desc(P, row, 1 if e4 else 2, len(bufs))
+    s = {"q": q, "desc": dd, "kv": hc.DeviceKV(bufs, dp), "width": width, "ks": ks, "vs": vs, "dt": dtype,
+         "table": torch.tensor(table, dtype=torch.int32, device="cuda"),
+         "lens": torch.tensor(lens, dtype=torch.int32, device="cuda")}
+    dv = 512 if latent else d
+    out = torch.empty((len(lens), 2 * hk, dv), dtype=dtype, device="cuda")
+    lse = torch.empty((len(lens), 2 * hk), device="cuda")
+    plain_call(s, out, workspace(s, 2 * hk, d, dv, False), scale=float(np.log(2.0)) / ks, lse=lse)
+    want, z = [], []
+    for i, n in enumerate(lens):
+        p = np.exp2(np.array([level(i, t) for t in range(n)], dtype=np.float64))
+        want.append(float((p * [value(i, t) for t in range(n)]).sum() / p.sum()) * vs)
+        z.append(float(np.log(p.sum())))
+    return out.double(), lse.double(), want, z
+
+
+@pytest.mark.parametrize("kind", ["fp16", "e4m3 fp16", "e4m3 bf16", "latent fp16"])
+@pytest.mark.parametrize("low", [-18, -22, -24, -26, -28, -30])
+def test_decode_small_weights_beside_a_large_one(kind, low):
+    """The first token takes nearly all the weight and has no value; the others,
+    2^low of it each, have a large one and decide the result."""
+    dt = torch.bfloat16 if "bf16" in kind else torch.float16
+    e4, latent = "e4m3" in kind, "latent" in kind
+    big = 448.0 if e4 else 57344.0
+    lens = [16, 17, 64, 200, 1000]
+    out, lse, want, z = level_caches(lens, lambda i, t: low if t else 0, lambda i, t: big if t else 0.0,
+                                     576 if latent else 64, 1 if latent else 2, dt, e4, latent, vs=128.0 if e4 else 1.0)
+    for i, n in enumerate(lens):
+        # exponentials: argument and function 2^-18, rounded to fp16's places below 2^8 of
+        # the largest (2^-33 of it at most); sums of n; the last rounding
+        tol = abs(want[i]) * (2.0 ** -17 + 2 * n * 2.0 ** -24 + ref.UNIT[dt] + 2.0 ** -11) + \
+            n * 2.0 ** -33 * 57344.0 + ref.TINY[dt]
+        assert (out[i] - want[i]).abs().max().item() <= tol, (n, out[i].flatten()[0].item(), want[i])
+        assert (lse[i] - z[i]).abs().max().item() <= 2.0 ** -17 + n * 2.0 ** -24

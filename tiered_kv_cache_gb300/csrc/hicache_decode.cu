@@ -11,10 +11,10 @@
 // head.  The products are mma.sync m16n8k16 with the 16 tokens (for V: 16 elements
 // of the head) as rows and the group's heads as columns, 8 at a time, so that a
 // group of 4 costs half of what heads as rows would; one 8 x 8 transposition per
-// 8 tokens takes the exponentials from one product to the other.  The running
-// maximum is raised only when a score passes it by as much (in log2) as the
-// products' type allows (fp16 ends at 2^16; bf16 has room for 2^40 and its sums):
-// the usual tile needs a vote and no reduction.
+// 8 tokens takes the exponentials from one product to the other.  What scores are
+// taken relative to follows the running maximum only when a score passes it by as
+// much (in log2) as the products' type allows: the usual tile needs a vote and no
+// reduction.
 //
 // A warp that has all tiles of a (sequence, kv head) writes the result itself.
 // The others leave a partial result, joined in tile order: first among the warps
@@ -64,7 +64,7 @@ struct KvConfig {
   static constexpr int KS = DP_ / 16;             // k steps of q . k
   static constexpr int MT = DP_ / 16;             // m tiles of the output
   static constexpr int NB = ROWS_ / 8;            // n tiles: 8 heads each
-  static constexpr float RAISE = TYPE_ == kBf16 ? 40.f : 14.f;
+  static constexpr float RAISE = kRaise<TYPE_ != kBf16>, ABOVE = kAbove<TYPE_ != kBf16>;
   static constexpr int PIECE = ROWS_ * DP_ + 2 * ROWS_;   // floats of a partial result: O, m, l
   static constexpr int LD = DP_ + 4;              // floats of a row of a warp's: no bank twice
   static constexpr int SMEM = WARPS * RING_B;
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
   }
   uint32_t qf[C::KS][NB][2];                      // q as the B operand
   // of heads 8 n + 2 c4 and + 1: the scale (for e4m3 with the power of two taken out
-  // of q), the maximum, what scores are taken relative to, the sum
+  // of q), the reference, what scores are taken relative to (0 while there is none),
+  // the sum
   float qmul[NB][2], m[NB][2], mu[NB][2], l[NB][2];
   float o[C::MT][NB][4];
   int h0 = 0, rows = 0, pieces = 0, stage = 0;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
           float top = fmaxf(sc[n][i], sc[n][2 + i]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-          const float m2 = fmaxf(m[n][i], top + mu[n][i]);
+          const float m2 = fmaxf(m[n][i], top + mu[n][i] - C::ABOVE);
           const float f = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - m2);
           const float use = m2 == -INFINITY ? 0.f : m2, by = mu[n][i] - use;
           m[n][i] = m2;
@@ -468,8 +469,9 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
       for (int i = 0; i < 4; ++i) sc[n][i] = exp2_fast(sc[n][i]);
       l[n][0] += sc[n][0] + sc[n][2];
       l[n][1] += sc[n][1] + sc[n][3];
-      // rounded to the product's type for the tensor cores; the sum above keeps
-      // all bits, and the rounding errors of many tokens average out
+      // rounded to the product's type for the tensor cores; the sum above keeps all
+      // bits, and the rounding errors of many tokens average out (those of the smallest,
+      // which become 0, do not: see kAbove)
 #pragma unroll
       for (int x = 0; x < 2; ++x) pf[n][x] = transpose8(pack2<MMA_BF16>(sc[n][2 * x], sc[n][2 * x + 1]));
     }

@@ -13,6 +13,19 @@ namespace {
 
 constexpr float kLn2 = 0.693147180559945309f;
 
+// Scores are taken relative to a reference per head that follows the running maximum:
+// it is put kAbove (log2) below the maximum whenever some score lies more than kRaise
+// above it.  The exponentials, 2^kAbove for the maximum then and 2^kRaise at most, are
+// rounded to the products' type.  fp16 has places from 2^-24 to 2^16: with the maximum
+// at 2^8, what lies below half its smallest number, and is lost to the product though
+// not to the sum of the exponentials, is under 2^-33 of the maximum: 1.2e-4 of the
+// weight for a million such tokens, a quarter of fp16's own rounding (at 2^0 it
+// was 2^-25, 3%).  bf16 has room for 2^40 and its sums.
+template <bool FP16>
+constexpr float kRaise = FP16 ? 15.f : 40.f;
+template <bool FP16>
+constexpr float kAbove = FP16 ? 8.f : 0.f;
+
 // The tokens [start, len) that sequence b attends to.
 __device__ __forceinline__ void seq_range(const DecodeParams &p, int b, int *start, int *len) {
   const int64_t cap = int64_t(p.max_pages) * p.P;

@@ -20,10 +20,10 @@
 // ready never waits behind one whose tile is still on its way.
 //
 // Softmax: a set of four warps (two sets for 64 heads, 32 heads each) reads 16
-// tokens a warp as 16 x 8 fragments (2 tokens x heads / 4 a thread).  The running
-// maximum of each head is raised only when some score passes it by more than P's
-// type can hold, so that the usual tile needs one barrier and no reduction; sums
-// stay per thread until the piece ends.
+// tokens a warp as 16 x 8 fragments (2 tokens x heads / 4 a thread).  What a head's
+// scores are taken relative to follows the running maximum only when some score
+// passes it by more than P's type can hold, so that the usual tile needs one barrier
+// and no reduction; sums stay per thread until the piece ends.
 //
 // The work is cut into strips of 32 tokens; the strips of all sequences, in
 // order, are dealt in equal contiguous ranges to the CTAs (one per SM; with more
@@ -73,9 +73,7 @@ struct LatConfig {
   static constexpr int SMEM = Q_B + DUOS * kDuoB + ROPES * kRopeB + 1024;
   static constexpr int COLS = NH_ == 16 ? 128 : NH_ == 32 ? 256 : 512;   // tensor memory
   static constexpr int PIECE = NH_ * kLatDv + 2 * NH_;                   // floats: O, m, l
-  // How far a score may pass the running maximum (log2) before it is raised: as
-  // far as P's type allows (fp16 ends at 2^16; bf16 has room for 2^40 and its sums)
-  static constexpr float RAISE = BF16_ ? 40.f : 14.f;
+  static constexpr float RAISE = kRaise<!BF16_>, ABOVE = kAbove<!BF16_>;
 };
 
 // ---- mbarriers and tcgen05 ------------------------------------------------------
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
   __shared__ unsigned long long scratch[C::WARPS];
   __shared__ int lens_s[kLens];
   __shared__ __align__(8) unsigned long long bars[4 + C::DUOS + C::ROPES + 9];
-  // per head: the maximum (and what scores are taken relative to: 0 while there is
+  // per head: the reference (and what scores are taken relative to: 0 while there is
   // none), the factor and the shift of the last raise
   __shared__ __align__(16) float m_s[NH], mu_s[NH], f_s[NH], d_s[NH];
   __shared__ float red[4][NH];
@@ -541,7 +539,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
         m_s[col0 + st] = -INFINITY;
         mu_s[col0 + st] = 0.f;
       }
-      bool unset = true;                          // a head has no maximum yet
+      bool unset = true;                          // a head has no reference yet
       set_sync(set);
       for (int tile = 0; tile < pc.tiles; ++tile, ++tiles) {
         const uint32_t buf = tiles & 1u;
@@ -557,7 +555,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
         // O of two tiles back (long done), so that the waits for it below see each phase
         if (!fail && tiles >= 2) fail = !mbar_wait(bar(PVDONE + buf), ((tiles - 2) >> 1) & 1u, &gave_up);
         tc_fence_after();
-        float e[NS / 2];                          // scores less the running maxima, in log2: [4 n + 2 x + i]
+        float e[NS / 2];                          // scores less the references, in log2: [4 n + 2 x + i]
 #pragma unroll
         for (int j = 0; j < NS; j += 16) tc_ld_16x16(tmem_sc + buf * NH + lanes + col0 + j, e + j / 2);
         tc_wait_ld();
@@ -586,7 +584,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
             }
         }
         if (set_any(set, unset || over > C::RAISE || fail)) {
-          // raise the maxima (all threads take this path, or none), once the
+          // raise the references (all threads take this path, or none), once the
           // product with V of the piece's tile before has ended
           if (!fail && tile > 0) fail = !mbar_wait(bar(PVDONE + (buf ^ 1u)), ((tiles - 1) >> 1) & 1u, &gave_up);
           fail = set_any(set, fail);
@@ -603,7 +601,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
             const int h = col0 + st;
             const float mu = mu_s[h], old = m_s[h];
             const float top = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h])) + mu;
-            now = fmaxf(old, top);
+            now = fmaxf(old, top - C::ABOVE);
             f_s[h] = old == -INFINITY ? 0.f : exp2_fast(old - now);
             m_s[h] = now;
             const float use = now == -INFINITY ? 0.f : now;
