@@ -947,3 +947,18 @@ def test_decode_small_weights_beside_a_large_one(kind, low):
             n * 2.0 ** -33 * 57344.0 + ref.TINY[dt]
         assert (out[i] - want[i]).abs().max().item() <= tol, (n, out[i].flatten()[0].item(), want[i])
         assert (lse[i] - z[i]).abs().max().item() <= 2.0 ** -17 + n * 2.0 ** -24
+
+
+@pytest.mark.parametrize("latent", [False, True])
+@pytest.mark.parametrize("power", [-100, 0, 85, 100, 115])
+def test_decode_rising_scores_with_large_values(latent, power):
+    """bf16 values near both ends of their range, under scores that rise by 39 (log2)
+    between tiles of the same piece: exponentials that used the type's whole range
+    would overflow their sums."""
+    tile, n, b = (64, 1024, 60) if latent else (16, 256, 300)
+    value = 2.0 ** power
+    out, lse, want, z = level_caches([n] * b, lambda i, t: 39 * (t // tile % 2), lambda i, t: value,
+                                     576 if latent else 64, 1 if latent else 2, torch.bfloat16, False, latent)
+    # 2^-8 of each exponential, sums of n, the last rounding
+    assert ((out / value - 1).abs() <= 2.0 ** -8 + 2 * n * 2.0 ** -24 + 2.0 ** -17 + 2.0 ** -8).all()
+    assert ((lse - z[0]).abs() <= 2.0 ** -17 + n * 2.0 ** -24 + 4 * z[0] * 2.0 ** -24).all()
