@@ -941,8 +941,9 @@ def test_decode_small_weights_beside_a_large_one(kind, low):
     out, lse, want, z = level_caches(lens, lambda i, t: low if t else 0, lambda i, t: big if t else 0.0,
                                      576 if latent else 64, 1 if latent else 2, dt, e4, latent, vs=128.0 if e4 else 1.0)
     for i, n in enumerate(lens):
-        # exponentials: argument and function 2^-18, rounded to fp16's places below 2^8 of
-        # the largest (2^-33 of it at most); sums of n; the last rounding
+        # exponentials: argument and function 2^-18 (powers of two, so that fp16's places
+        # take nothing more from 2^-30 of the largest on; 2^-33 for each is left); sums of
+        # n; the last rounding
         tol = abs(want[i]) * (2.0 ** -17 + 2 * n * 2.0 ** -24 + ref.UNIT[dt] + 2.0 ** -11) + \
             n * 2.0 ** -33 * 57344.0 + ref.TINY[dt]
         assert (out[i] - want[i]).abs().max().item() <= tol, (n, out[i].flatten()[0].item(), want[i])

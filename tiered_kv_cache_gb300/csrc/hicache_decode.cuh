@@ -17,9 +17,9 @@ constexpr float kLn2 = 0.693147180559945309f;
 // it is put kAbove (log2) below the maximum whenever some score lies more than kRaise
 // above it.  The exponentials, 2^kAbove for the maximum then and 2^kRaise at most, are
 // rounded to the products' type.  fp16 has places from 2^-24 to 2^16: with the maximum
-// at 2^8, what lies below half its smallest number, and is lost to the product though
-// not to the sum of the exponentials, is under 2^-33 of the maximum: 1.2e-4 of the
-// weight for a million such tokens, a quarter of fp16's own rounding (at 2^0 it
+// at 2^6, what lies below half its smallest number, and is lost to the product though
+// not to the sum of the exponentials, is under 2^-31 of the maximum: 2^-11 of the
+// weight for a million such tokens, as much as fp16's own rounding (at 2^0 it
 // was 2^-25, 3%).  bf16 has the exponents of the sums themselves, and exponentials
 // above 1 would only take room from V: 2^40, which its places allow, times elements of
 // 2^90 left 32 bits.  They stay under 1, so that the sum over a piece fits wherever that
@@ -27,7 +27,7 @@ constexpr float kLn2 = 0.693147180559945309f;
 template <bool FP16>
 constexpr float kRaise = FP16 ? 15.f : 0.f;
 template <bool FP16>
-constexpr float kAbove = FP16 ? 8.f : -14.f;
+constexpr float kAbove = FP16 ? 6.f : -14.f;
 
 // The tokens [start, len) that sequence b attends to.
 __device__ __forceinline__ void seq_range(const DecodeParams &p, int b, int *start, int *len) {
