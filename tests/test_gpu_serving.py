@@ -963,3 +963,18 @@ def test_decode_rising_scores_with_large_values(latent, power):
     # 2^-8 of each exponential, sums of n, the last rounding
     assert ((out / value - 1).abs() <= 2.0 ** -8 + 2 * n * 2.0 ** -24 + 2.0 ** -17 + 2.0 ** -8).all()
     assert ((lse - z[0]).abs() <= 2.0 ** -17 + n * 2.0 ** -24 + 4 * z[0] * 2.0 ** -24).all()
+
+
+# ---- the binding's checks on the device --------------------------------------------
+
+def test_caches_of_another_type_are_refused():
+    s = decode_inputs([40], 4, 2, 64, 16, "bf16")
+    ws = workspace(s, 4, 64, 64, False)
+    out, before = torch.zeros((1, 4, 64), dtype=torch.float16, device="cuda"), hc.launch_count()
+    slots = torch.zeros(1, dtype=torch.int64, device="cuda")
+    s["q"] = s["q"].to(torch.float16)
+    with pytest.raises(ValueError, match="expected torch.float16"):
+        plain_call(s, out, ws)
+    with pytest.raises(ValueError, match="expected torch.float16"):
+        hc.append_kv(s["kv"], s["desc"], 0, None, s["q"][:, :2], s["q"][:, :2], slots)
+    assert hc.launch_count() == before

@@ -232,3 +232,28 @@ int main() {
     subprocess.check_call(["g++", "-std=c++17", f"-I{root}/tiered_kv_cache_gb300/csrc", f"-I{root}/include",
                            "-I/usr/local/cuda/include", str(src), "-o", str(exe)])
     assert subprocess.run([str(exe)], capture_output=True, text=True).stdout.strip() == "ok"
+
+
+def test_cache_types_are_checked():
+    """A cache of another floating-point type than the call's; storage without one is taken."""
+    torch = pytest.importorskip("torch")
+    bf, fp, e4, e5 = torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float8_e5m2
+    for cache, dtype, es, ok in ((bf, bf, 2, True), (fp, fp, 2, True), (bf, fp, 2, False), (fp, bf, 2, False),
+                                 (torch.int16, bf, 2, True), (torch.uint8, fp, 2, True), (torch.float32, bf, 2, False),
+                                 (e4, bf, 1, True), (e4, fp, 1, True), (e5, bf, 1, False), (torch.uint8, bf, 1, True),
+                                 (bf, bf, 1, False)):
+        kv = hc.DeviceKV([torch.zeros((160, 256 * 4), dtype=cache)] * 4, 10)
+        for _ in range(2):
+            if ok:
+                assert hc._check_cache(kv, desc(elem_bytes=es), 0, -1, dtype) == 2
+            else:
+                with pytest.raises(ValueError, match="expected torch"):
+                    hc._check_cache(kv, desc(elem_bytes=es), 0, -1, dtype)
+    # one cache, calls of both types
+    kv = hc.DeviceKV([torch.zeros((160, 256), dtype=bf)] * 4, 10)
+    assert hc._check_cache(kv, desc(), 0, -1, bf) == 2
+    with pytest.raises(ValueError, match="expected torch.float16"):
+        hc._check_cache(kv, desc(), 0, -1, fp)
+    # and of one-byte elements in rows of as many bytes
+    with pytest.raises(ValueError, match="expected torch.float8_e4m3fn"):
+        hc._check_cache(kv, desc(elem_bytes=1, row_elems=512), 0, -1, bf)

@@ -799,16 +799,20 @@ def _pool_desc(pool_or_desc) -> PoolDesc:
     return pool_or_desc.desc if isinstance(pool_or_desc, Pool) else pool_or_desc
 
 
-def _check_cache(kv, desc, layer, device):
+def _check_cache(kv, desc, layer, device, dtype=None):
     """The cache must hold desc's buffers; its torch tensors must be on the
-    call's device and hold the pages they are said to (raw addresses cannot be
-    checked).  A shape that kv has been checked for is not checked again."""
+    call's device, hold the pages they are said to (raw addresses cannot be
+    checked) and have elements of dtype, e4m3 in a 1-byte cache (or of no
+    floating-point type: plain storage).  What kv has been checked for is not
+    checked again."""
     layers, buffers, row_bytes = desc.num_layers, desc.num_buffers, desc.page_size * desc.row_elems * desc.elem_bytes
-    shape = (layers, buffers, row_bytes, device)
+    shape = (layers, buffers, row_bytes, desc.elem_bytes, device, dtype)
     if shape in kv.checked:
         return buffers
     if kv.num_buffers_total != buffers * layers:
         raise ValueError(f"DeviceKV has {kv.num_buffers_total} buffers, the pool {buffers} x {layers}")
+    if desc.elem_bytes == 1:
+        dtype = _import_torch().float8_e4m3fn
     need = kv.device_num_pages * row_bytes
     for t in kv._tensors:
         if isinstance(t, int):
@@ -817,6 +821,8 @@ def _check_cache(kv, desc, layer, device):
             raise ValueError(f"the cache is on {t.device}, expected device {device}")
         if t.numel() * t.element_size() < need or not t.is_contiguous():
             raise ValueError(f"a cache buffer has {t.numel() * t.element_size()} bytes, its pages need {need} contiguous")
+        if dtype is not None and t.dtype is not dtype and t.dtype.is_floating_point:
+            raise ValueError(f"a cache buffer is {t.dtype}, expected {dtype}")
     kv.checked.add(shape)
     return buffers
 
@@ -838,7 +844,7 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
     code, dev = _activations("q" if q is not None else "k", first)
     dt = first.dtype
     desc = _pool_desc(pool_or_desc)
-    buffers = _check_cache(kv, desc, layer, dev)
+    buffers = _check_cache(kv, desc, layer, dev, dt)
     n, hq, dim = first.shape
     qp = op = kp = vp = qst = qsh = ost = osh = kst = ksh = vst = vsh = hk = sp = 0
     if q is not None:
@@ -912,7 +918,7 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     code, dev = _activations("q", q)
     dt = q.dtype
     desc = _pool_desc(pool_or_desc)
-    _check_cache(kv, desc, layer, dev)
+    _check_cache(kv, desc, layer, dev, dt)
     b, hq, d = q.shape
     qb, qh, _ = _tensor("q", q, dt, (b, hq, d), dev)
     dv, width = out.shape[-1], page_table.shape[-1]
