@@ -978,3 +978,36 @@ def test_caches_of_another_type_are_refused():
     with pytest.raises(ValueError, match="expected torch.float16"):
         hc.append_kv(s["kv"], s["desc"], 0, None, s["q"][:, :2], s["q"][:, :2], slots)
     assert hc.launch_count() == before
+
+
+def test_tensors_that_autograd_records_are_not_written():
+    s = decode_inputs([40], 4, 2, 64, 16, "bf16")
+    ws = workspace(s, 4, 64, 64, True)
+    out = torch.zeros((1, 4, 64), dtype=s["dt"], device="cuda")
+    w, lse = torch.zeros((1, s["width"]), device="cuda"), torch.zeros((1, 4), device="cuda")
+    k = torch.ones((1, 2, 64), dtype=s["dt"], device="cuda")
+    slots = torch.full((1,), -1, dtype=torch.int64, device="cuda")
+    i32 = lambda *x: torch.zeros(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    calls = {
+        "q": lambda x: hc.append_kv(s["kv"], s["desc"], 0, x, k, k, slots),
+        "q_out": lambda x: hc.append_kv(s["kv"], s["desc"], 0, s["q"], k, k, slots, q_out=x),
+        "out": lambda x: plain_call(s, x, ws),
+        "lse": lambda x: plain_call(s, out, ws, lse=x),
+        "weights": lambda x: plain_call(s, out, ws, weights=x),
+        "weights ": lambda x: hc.evict_pages(16, s["table"], s["lens"], x, i32(1), i32(1, 2), i32(1)),
+        "out_weights": lambda x: hc.evict_pages(16, s["table"], s["lens"], w, i32(1), i32(1, 2), i32(1), out_weights=x),
+    }
+    like = {"q": s["q"], "q_out": out, "out": out, "lse": lse, "weights": w, "weights ": w, "out_weights": w}
+    for name, call in calls.items():
+        t = torch.zeros_like(like[name]).requires_grad_()
+        before = hc.launch_count()
+        for x in (t, t * 1):                      # a leaf, and a tensor that was computed
+            with pytest.raises(ValueError, match=f"{name.strip()}: written"):
+                call(x)
+        assert hc.launch_count() == before
+        with torch.no_grad():
+            call(t)
+        assert hc.launch_count() > before
+    # inputs that are only read may
+    plain_call({**s, "q": s["q"].clone().requires_grad_()}, out, ws)
+    torch.cuda.synchronize()

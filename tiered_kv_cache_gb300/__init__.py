@@ -764,6 +764,12 @@ def _tensor(name, t, dtype, shape, device):
     raise ValueError(f"{name}: the innermost dimension must be contiguous")
 
 
+def _written(name, t):
+    """Refuses to write a tensor that autograd records: it would not see it."""
+    if t.requires_grad and _import_torch().is_grad_enabled():
+        raise ValueError(f"{name}: written, but requires grad (these operators have no backward pass; use torch.no_grad())")
+
+
 _torch = None
 
 
@@ -854,6 +860,7 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
         if q_out is not None:
             ost, osh, _ = _tensor("q_out", q_out, dt, (n, hq, dim), dev)
             op = q_out.data_ptr()
+        _written("q" if q_out is None else "q_out", q if q_out is None else q_out)
     else:
         hq = 0
     if k is not None:
@@ -923,6 +930,7 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     qb, qh, _ = _tensor("q", q, dt, (b, hq, d), dev)
     dv, width = out.shape[-1], page_table.shape[-1]
     ob, oh, _ = _tensor("out", out, dt, (b, hq, dv), dev)
+    _written("out", out)
     tst = _tensor("page_table", page_table, torch.int32, (b, width), dev)[0]
     _tensor("seq_lens", seq_lens, torch.int32, (b,), dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -930,9 +938,11 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     lp = wp = lst = wst = 0
     if lse is not None:
         lst = _tensor("lse", lse, torch.float32, (b, hq), dev)[0]
+        _written("lse", lse)
         lp = lse.data_ptr()
     if weights is not None:
         wst = _tensor("weights", weights, torch.float32, (b, width), dev)[0]
+        _written("weights", weights)
         wp = weights.data_ptr()
     a = _DECODE_DESC.pack(q.data_ptr(), out.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), lp, wp,
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), qb, qh, ob, oh,
@@ -982,6 +992,7 @@ def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, nu
     if out_weights is not None:
         owst = _tensor("out_weights", out_weights, f32, rows, dev)[0]
         owp = out_weights.data_ptr()
+    _written("weights" if out_weights is None else "out_weights", weights if out_weights is None else out_weights)
     if out_lens is not None:
         _tensor("out_lens", out_lens, i32, one, dev)
         olp = out_lens.data_ptr()
