@@ -1011,3 +1011,51 @@ def test_tensors_that_autograd_records_are_not_written():
     # inputs that are only read may
     plain_call({**s, "q": s["q"].clone().requires_grad_()}, out, ws)
     torch.cuda.synchronize()
+
+
+def test_calls_follow_the_current_stream():
+    """Without a stream each operator runs on torch's current one, behind inputs that
+    are still being made there, and is captured with it; with 0 on the default one."""
+    s = decode_inputs([300, 40], 4, 2, 64, 16)
+    ws = workspace(s, 4, 64, 64, True)
+    q, lens, weight = s["q"].clone(), s["lens"].clone(), torch.rand((2, s["width"]), device="cuda")
+    k = torch.randn((2, 2, 64), generator=gen(3), device="cuda").to(s["dt"])
+    slots = torch.tensor([3, 700], device="cuda")
+    kw = torch.ones(64, dtype=s["dt"], device="cuda")
+    keep = torch.full((2,), 2, dtype=torch.int32, device="cuda")
+    kv = hc.DeviceKV([torch.zeros_like(b) for b in s["bufs"]], s["Dp"])
+
+    def step(late, stream=None):
+        bufs = kv._tensors
+        new = {"q": torch.zeros_like(q), "k": torch.zeros_like(k), "lens": torch.zeros_like(lens)}
+        out = torch.zeros((2, 4, 64), dtype=s["dt"], device="cuda")
+        w, t, n = torch.zeros_like(weight), s["table"].clone(), torch.zeros_like(lens)
+        vic, cnt = torch.full_like(t, -1), torch.zeros_like(lens)
+        for b, x in zip(bufs, s["bufs"]):
+            b.copy_(x)
+        torch.cuda.synchronize()
+        if late:
+            torch.cuda._sleep(50_000_000)
+        new["q"].copy_(q), new["k"].copy_(k), new["lens"].copy_(lens), n.copy_(lens)
+        hc.append_kv(kv, s["desc"], 0, new["q"], new["k"], new["k"], slots, q_weight=kw, stream=stream)
+        hc.decode_attention(kv, s["desc"], 0, new["q"], s["table"], new["lens"], out, ws, weights=w, stream=stream)
+        w.add_(weight)
+        hc.evict_pages(16, t, n, w, keep, vic, cnt, stream=stream)
+        return [new["q"], out, w, t, n, vic, cnt]
+    want = step(False)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = step(True)
+        torch.cuda.current_stream().synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and want[-1].tolist() == [17, 1]
+    got = step(False, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    out = torch.zeros_like(want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        hc.decode_attention(kv, s["desc"], 0, want[0], s["table"], lens, out, ws)
+    assert not out.any()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[1])

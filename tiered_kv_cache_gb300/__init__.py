@@ -801,6 +801,13 @@ def _current(name, t):
     return device
 
 
+def _launch_stream(stream, device):
+    """The handle of a stream as _stream() takes it, but for None: these calls take
+    tensors that torch has just made, so torch's current stream (without its
+    wrapper object, which costs a microsecond)."""
+    return _torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def _pool_desc(pool_or_desc) -> PoolDesc:
     return pool_or_desc.desc if isinstance(pool_or_desc, Pool) else pool_or_desc
 
@@ -842,7 +849,8 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
     store of k and v into rows slots[n] of the layer's buffers.
 
     q [n, q_heads, dim] -> q_out (None: in place); k, v [n, kv_heads, dim] (v is
-    None for a latent cache).  q, or k and v and slots, may be None."""
+    None for a latent cache).  q, or k and v and slots, may be None.  stream: torch's
+    current stream unless given."""
     torch = _import_torch()
     first = q if q is not None else k
     if first is None:
@@ -897,7 +905,7 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
         pp, cp = positions.data_ptr(), cos_sin.data_ptr()
     a = _APPEND_DESC.pack(qp, op, kp, vp, qw, kw, sp, pp, cp, qst, qsh, ost, osh, kst, ksh, vst, vsh, n, rows,
                           code, hq, hk, dim, qn, kn, rot, rot_offset, bool(interleaved), eps, k_scale, v_scale)
-    rc = library().hicache_append_kv(kv.ref, ctypes.byref(desc), layer, a, _stream(stream))
+    rc = library().hicache_append_kv(kv.ref, ctypes.byref(desc), layer, a, _launch_stream(stream, dev))
     if rc:
         _check(rc)
 
@@ -920,7 +928,8 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     `window` of them if window > 0) into out [batch, q_heads, v_dim]; lse
     (optional) [batch, q_heads] the log of the softmax sums; weights (optional)
     [batch, max_pages] <- decay * weights + the attention each page received.
-    scale: head_dim ** -0.5 unless given."""
+    scale: head_dim ** -0.5 unless given; stream: torch's current stream unless
+    given."""
     torch = _import_torch()
     code, dev = _activations("q", q)
     dt = q.dtype
@@ -948,7 +957,7 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), qb, qh, ob, oh,
                           tst, lst, wst, code, b, hq, d, dv, width, window, 0,
                           d ** -0.5 if scale is None else scale, k_scale, v_scale, decay)
-    rc = library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _stream(stream))
+    rc = library().hicache_decode_attention(kv.ref, ctypes.byref(desc), layer, a, _launch_stream(stream, dev))
     if rc:
         _check(rc)
 
@@ -967,7 +976,8 @@ def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, nu
     below 0 are absent pages, which keep their place), the ones with the lowest
     weights leave until keep[b] are left (or none may go, or victims is full):
     victims [batch, max_victims] receives their pages, num_victims their number,
-    and out_table, out_lens, out_weights (None: in place) what stays."""
+    and out_table, out_lens, out_weights (None: in place) what stays.  stream:
+    torch's current stream unless given."""
     torch = _import_torch()
     dev = _current("page_table", page_table)
     i32, f32 = torch.int32, torch.float32
@@ -998,6 +1008,6 @@ def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, nu
         olp = out_lens.data_ptr()
     a = _EVICT_DESC.pack(tp, wp, lp, keep.data_ptr(), victims.data_ptr(), num_victims.data_ptr(), otp, owp, olp,
                          tst, wst, vst, otst, owst, page_size, b, width, cap, sink, recent)
-    rc = library().hicache_evict_pages(a, _stream(stream))
+    rc = library().hicache_evict_pages(a, _launch_stream(stream, dev))
     if rc:
         _check(rc)
