@@ -765,8 +765,9 @@ def _tensor(name, t, dtype, shape, device):
 
 
 def _written(name, t):
-    """Refuses to write a tensor that autograd records: it would not see it."""
-    if t.requires_grad and _import_torch().is_grad_enabled():
+    """Refuses to write a tensor that requires grad while autograd records: it would
+    not see it."""
+    if _torch.is_grad_enabled():
         raise ValueError(f"{name}: written, but requires grad (these operators have no backward pass; use torch.no_grad())")
 
 
@@ -796,7 +797,7 @@ def _activations(name, t):
 
 def _current(name, t):
     device = t.get_device()
-    if device < 0 or device != _import_torch().cuda.current_device():
+    if device < 0 or device != _torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, expected the current CUDA device")
     return device
 
@@ -868,7 +869,10 @@ def append_kv(kv: DeviceKV, pool_or_desc, layer: int, q, k, v, slots, *, q_out=N
         if q_out is not None:
             ost, osh, _ = _tensor("q_out", q_out, dt, (n, hq, dim), dev)
             op = q_out.data_ptr()
-        _written("q" if q_out is None else "q_out", q if q_out is None else q_out)
+            if q_out.requires_grad:
+                _written("q_out", q_out)
+        elif q.requires_grad:
+            _written("q", q)
     else:
         hq = 0
     if k is not None:
@@ -939,7 +943,8 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     qb, qh, _ = _tensor("q", q, dt, (b, hq, d), dev)
     dv, width = out.shape[-1], page_table.shape[-1]
     ob, oh, _ = _tensor("out", out, dt, (b, hq, dv), dev)
-    _written("out", out)
+    if out.requires_grad:
+        _written("out", out)
     tst = _tensor("page_table", page_table, torch.int32, (b, width), dev)[0]
     _tensor("seq_lens", seq_lens, torch.int32, (b,), dev)
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -947,11 +952,13 @@ def decode_attention(kv: DeviceKV, pool_or_desc, layer: int, q, page_table, seq_
     lp = wp = lst = wst = 0
     if lse is not None:
         lst = _tensor("lse", lse, torch.float32, (b, hq), dev)[0]
-        _written("lse", lse)
+        if lse.requires_grad:
+            _written("lse", lse)
         lp = lse.data_ptr()
     if weights is not None:
         wst = _tensor("weights", weights, torch.float32, (b, width), dev)[0]
-        _written("weights", weights)
+        if weights.requires_grad:
+            _written("weights", weights)
         wp = weights.data_ptr()
     a = _DECODE_DESC.pack(q.data_ptr(), out.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), lp, wp,
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), qb, qh, ob, oh,
@@ -1002,7 +1009,10 @@ def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, nu
     if out_weights is not None:
         owst = _tensor("out_weights", out_weights, f32, rows, dev)[0]
         owp = out_weights.data_ptr()
-    _written("weights" if out_weights is None else "out_weights", weights if out_weights is None else out_weights)
+        if out_weights.requires_grad:
+            _written("out_weights", out_weights)
+    elif weights.requires_grad:
+        _written("weights", weights)
     if out_lens is not None:
         _tensor("out_lens", out_lens, i32, one, dev)
         olp = out_lens.data_ptr()
