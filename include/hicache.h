@@ -638,7 +638,8 @@ int hicache_layer_checksum(const hicache_device_kv *kv, const hicache_pool_desc 
  *     [0, device_num_pages) counts as absent, a slot outside the buffers or a
  *     position outside the table stores nothing, a length counts as clamped
  *     to [0, max_pages * page_size].
- *   - Strides are in elements; the innermost dimension is contiguous.
+ *   - Strides are in elements; the innermost dimension is contiguous.  The
+ *     stride of a dimension of one is not used, whatever it is.
  *   - Everything is computed in 32 bits and rounded once to the output's type,
  *     except as noted.  The same call on the same data gives the same bits.
  *   - A call that returns an error has enqueued nothing. */

@@ -1059,3 +1059,34 @@ def test_calls_follow_the_current_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want[1])
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_single_rows_with_odd_strides(latent):
+    """One sequence, one head, one token, as views whose unused strides are odd."""
+    d, dv = (576, 512) if latent else (64, 64)
+    s = decode_inputs([90], 1, 1, d, 16, latent=latent)
+    ws = workspace(s, 1, d, dv, True)
+    odd = lambda t, *st: torch.as_strided(t, t.shape, (*st, 1))  # noqa: E731
+    a, b = (torch.zeros((1, 1, dv), dtype=s["dt"], device="cuda") for _ in range(2))
+    w, lse = [torch.zeros((1, s["width"]), device="cuda") for _ in range(2)], torch.zeros((1, 1), device="cuda")
+    q, table = s["q"], s["table"]
+    plain_call(s, a, ws, weights=w[0])
+    s["q"], s["table"] = odd(q, 13, 7), odd(table, 1)
+    plain_call(s, odd(b, 3, 5), ws, weights=odd(w[1], 3), lse=odd(lse, 9))
+    assert torch.equal(a, b) and torch.equal(*w) and a.any()
+    k = torch.randn((1, 1, d), generator=gen(2), device="cuda").to(s["dt"])
+    for x in (k, odd(k, 11, 3)):
+        for buf in s["bufs"]:
+            buf[5] = 0
+        got = torch.zeros((1, 1, d), dtype=s["dt"], device="cuda")
+        hc.append_kv(s["kv"], s["desc"], 0, odd(q, 9, 1), x, None if latent else x,
+                     torch.tensor([5], device="cuda"), q_out=odd(got, 1, 1))
+        assert torch.equal(got, q) and all(torch.equal(buf[5], k.view(-1)) for buf in s["bufs"])
+    n = [torch.tensor([90], dtype=torch.int32, device="cuda") for _ in range(4)]
+    vic = [torch.full((1, 4), -1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    keep, cnt = torch.full((1,), 3, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    t = [table.clone(), table.clone()]
+    hc.evict_pages(16, t[0], n[0], w[0], keep, vic[0], cnt)
+    hc.evict_pages(16, odd(t[1], 2), n[1], odd(w[1], 1), keep, odd(vic[1], 1), cnt)
+    assert torch.equal(*t) and torch.equal(*w) and torch.equal(*vic) and cnt.item() == 3

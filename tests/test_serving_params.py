@@ -159,3 +159,22 @@ def test_evict_count_at_the_ends_of_the_range(tmp_path):
             if (evict_count(n, sink, recent, keep, cap) != want) return 1;
             if ((__int128)n - recent < INT_MIN) return 2;
           }""") == "ok"
+
+
+def test_strides_of_single_tokens_and_heads_are_not_used(params):
+    """A dimension of one may have any stride, odd, negative or huge; of several it is
+    checked and passed on."""
+    strides = ["qst", "qsh", "ost", "osh", "kst", "ksh", "vst", "vsh"]
+    names = ["q_st", "q_sh", "o_st", "o_sh", "k_st", "k_sh", "v_st", "v_sh"]
+    given = [512, 128, 512, 128, 256, 128, 256, 128]
+    p = params()
+    assert p["rc"] == 0 and [p[x] for x in names] == given
+    for odd in (1, 3, -7, 2 ** 50, 132):
+        p = params(n=1, q_heads=1, kv_heads=1, row=128, **{x: odd for x in strides})
+        assert p["rc"] == 0 and [p[x] for x in names] == [0] * 8
+        p = params(n=1, **{x: odd for x in strides[::2]})
+        assert p["rc"] == 0 and [p[x] for x in names] == [0, 128] * 4
+        p = params(q_heads=1, kv_heads=1, row=128, **{x: odd for x in strides[1::2]})
+        assert p["rc"] == 0 and [p[x] for x in names] == [512, 0, 512, 0, 256, 0, 256, 0]
+        for x in strides:
+            assert params(**{x: odd})["rc"] != 0

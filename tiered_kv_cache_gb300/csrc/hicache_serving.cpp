@@ -31,6 +31,9 @@ bool positive(float x) { return std::isfinite(x) && x > 0.f; }
 // out here or in a kernel leaves 64 bits.
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 bool stride_ok(int64_t s) { return s >= 0 && s < kMaxStride; }
+// The stride of a dimension of n: of one element (or none) it is never used, and
+// tensors have all kinds there.
+int64_t used(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
 
 // The shape and the layer's buffers of an operator on the device pages.
 int check_pages(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer, Shape *s,
@@ -180,22 +183,24 @@ int hicache_append_kv(const hicache_device_kv *kv, const hicache_pool_desc *desc
   if (a->rot_dim > 0 && (!aligned(a->positions, 8) || !aligned(a->cos_sin, 4)))
     return set_error(HICACHE_ERR_ALIGNMENT, "positions or cos_sin is not aligned to its elements");
   if (N == 0) return HICACHE_OK;
+  const int64_t q_st = used(a->q_token_stride, N), q_sh = used(a->q_head_stride, a->q_heads);
+  const int64_t o_st = used(a->q_out_token_stride, N), o_sh = used(a->q_out_head_stride, a->q_heads);
+  const int64_t k_st = used(a->k_token_stride, N), k_sh = used(a->k_head_stride, a->kv_heads);
+  const int64_t v_st = used(a->v_token_stride, N), v_sh = used(a->v_head_stride, a->kv_heads);
   if (a->q_heads > 0) {
-    if ((rc = check_heads("q", a->q, a->q_token_stride, a->q_head_stride))) return rc;
-    if ((rc = check_heads("q_out", a->q_out, a->q_out_token_stride, a->q_out_head_stride))) return rc;
-    if (!rows_disjoint(N, a->q_out_token_stride, a->q_heads, a->q_out_head_stride, D))
+    if ((rc = check_heads("q", a->q, q_st, q_sh))) return rc;
+    if ((rc = check_heads("q_out", a->q_out, o_st, o_sh))) return rc;
+    if (!rows_disjoint(N, o_st, a->q_heads, o_sh, D))
       return set_error(HICACHE_ERR_INVALID_ARG, "q_out: heads overlap one another");
-    if (a->q_out == a->q &&
-        ((N > 1 && a->q_out_token_stride != a->q_token_stride) ||
-         (a->q_heads > 1 && a->q_out_head_stride != a->q_head_stride)))
+    if (a->q_out == a->q && (o_st != q_st || o_sh != q_sh))
       return set_error(HICACHE_ERR_INVALID_ARG, "q_out is q with other strides");
     if (a->q_norm_dim > 0 && (!a->q_weight || !aligned(a->q_weight, 16)))
       return set_error(a->q_weight ? HICACHE_ERR_ALIGNMENT : HICACHE_ERR_INVALID_ARG,
                        "q_weight is NULL or not 16-byte aligned");
   }
   if (a->kv_heads > 0) {
-    if ((rc = check_heads("k", a->k, a->k_token_stride, a->k_head_stride))) return rc;
-    if (has_v && (rc = check_heads("v", a->v, a->v_token_stride, a->v_head_stride))) return rc;
+    if ((rc = check_heads("k", a->k, k_st, k_sh))) return rc;
+    if (has_v && (rc = check_heads("v", a->v, v_st, v_sh))) return rc;
     if (!has_v && a->v) return set_error(HICACHE_ERR_INVALID_ARG, "a latent cache takes no v");
     if (!a->slots) return set_error(HICACHE_ERR_INVALID_ARG, "slots is NULL");
     if (!aligned(a->slots, 8)) return set_error(HICACHE_ERR_ALIGNMENT, "slots is not aligned to its elements");
@@ -215,14 +220,14 @@ int hicache_append_kv(const hicache_device_kv *kv, const hicache_pool_desc *desc
   p.cos_sin = a->cos_sin;
   p.k_cache = k;
   p.v_cache = v;
-  p.q_st = a->q_token_stride;
-  p.q_sh = a->q_head_stride;
-  p.o_st = a->q_out_token_stride;
-  p.o_sh = a->q_out_head_stride;
-  p.k_st = a->k_token_stride;
-  p.k_sh = a->k_head_stride;
-  p.v_st = a->v_token_stride;
-  p.v_sh = a->v_head_stride;
+  p.q_st = q_st;
+  p.q_sh = q_sh;
+  p.o_st = o_st;
+  p.o_sh = o_sh;
+  p.k_st = k_st;
+  p.k_sh = k_sh;
+  p.v_st = v_st;
+  p.v_sh = v_sh;
   p.num_tokens = N;
   p.cos_sin_rows = a->cos_sin_rows;
   p.num_slots = kv->device_num_pages * s.P;
@@ -278,16 +283,23 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   if (!std::isfinite(p.scale2)) return set_error(HICACHE_ERR_INVALID_ARG, "scale * k_scale leaves 32 bits");
   if (a->window < 0) return set_error(HICACHE_ERR_INVALID_ARG, "window must be >= 0");
   if (a->batch == 0) return HICACHE_OK;
-  if ((rc = check_heads("q", a->q, a->q_batch_stride, a->q_head_stride))) return rc;
-  if ((rc = check_heads("out", a->out, a->out_batch_stride, a->out_head_stride))) return rc;
-  if (!rows_disjoint(a->batch, a->out_batch_stride, a->q_heads, a->out_head_stride, a->v_dim))
+  p.q_sb = used(a->q_batch_stride, a->batch);
+  p.q_sh = used(a->q_head_stride, a->q_heads);
+  p.o_sb = used(a->out_batch_stride, a->batch);
+  p.o_sh = used(a->out_head_stride, a->q_heads);
+  p.t_sb = used(a->table_stride, a->batch);
+  p.lse_sb = used(a->lse_stride, a->batch);
+  p.w_sb = used(a->weights_stride, a->batch);
+  if ((rc = check_heads("q", a->q, p.q_sb, p.q_sh))) return rc;
+  if ((rc = check_heads("out", a->out, p.o_sb, p.o_sh))) return rc;
+  if (!rows_disjoint(a->batch, p.o_sb, a->q_heads, p.o_sh, a->v_dim))
     return set_error(HICACHE_ERR_INVALID_ARG, "out: heads overlap one another");
   if (!a->page_table || !a->seq_lens || !a->workspace)
     return set_error(HICACHE_ERR_INVALID_ARG, "page_table, seq_lens or workspace is NULL");
-  if (!stride_ok(a->table_stride)) return set_error(HICACHE_ERR_INVALID_ARG, "table_stride must be in [0, 2^40)");
-  if (a->lse && (!stride_ok(a->lse_stride) || !rows_disjoint(a->batch, a->lse_stride, 1, 0, a->q_heads)))
+  if (!stride_ok(p.t_sb)) return set_error(HICACHE_ERR_INVALID_ARG, "table_stride must be in [0, 2^40)");
+  if (a->lse && (!stride_ok(p.lse_sb) || !rows_disjoint(a->batch, p.lse_sb, 1, 0, a->q_heads)))
     return set_error(HICACHE_ERR_INVALID_ARG, "lse_stride must be at least q_heads");
-  if (a->weights && (!stride_ok(a->weights_stride) || !rows_disjoint(a->batch, a->weights_stride, 1, 0, a->max_pages)))
+  if (a->weights && (!stride_ok(p.w_sb) || !rows_disjoint(a->batch, p.w_sb, 1, 0, a->max_pages)))
     return set_error(HICACHE_ERR_INVALID_ARG, "weights_stride must be at least max_pages");
   if (!aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->lse, 4) || !aligned(a->weights, 4))
     return set_error(HICACHE_ERR_ALIGNMENT, "page_table, seq_lens, lse or weights is not aligned to its elements");
@@ -305,13 +317,6 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.lens = a->seq_lens;
   p.lse = a->lse;
   p.weights = a->weights;
-  p.q_sb = a->q_batch_stride;
-  p.q_sh = a->q_head_stride;
-  p.o_sb = a->out_batch_stride;
-  p.o_sh = a->out_head_stride;
-  p.t_sb = a->table_stride;
-  p.lse_sb = a->lse_stride;
-  p.w_sb = a->weights_stride;
   p.num_pages = kv->device_num_pages;
   p.counters = reinterpret_cast<unsigned int *>(ws);
   p.cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
@@ -369,16 +374,18 @@ int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {
                         static_cast<const void *>(a->out_table), static_cast<const void *>(a->out_weights),
                         static_cast<const void *>(a->out_lens)})
     if (!aligned(q, 4)) return set_error(HICACHE_ERR_ALIGNMENT, "an array is not aligned to its elements");
-  for (const int64_t t : {a->table_stride, a->weights_stride, a->victims_stride, a->out_table_stride,
-                          a->out_weights_stride})
-    if (!stride_ok(t)) return set_error(HICACHE_ERR_INVALID_ARG, "strides must be in [0, 2^40)");
-  if (a->batch > 1 && (a->victims_stride < a->max_victims || a->out_table_stride < a->max_pages ||
-                       a->out_weights_stride < a->max_pages))
-    return set_error(HICACHE_ERR_INVALID_ARG, "the rows of an output overlap");
-  if (a->batch > 1 && ((a->out_table == a->page_table && a->out_table_stride != a->table_stride) ||
-                       (a->out_weights == a->weights && a->out_weights_stride != a->weights_stride)))
-    return set_error(HICACHE_ERR_INVALID_ARG, "an output is its input with another stride");
   hicache::EvictParams p{};
+  p.t_sb = used(a->table_stride, a->batch);
+  p.w_sb = used(a->weights_stride, a->batch);
+  p.v_sb = used(a->victims_stride, a->batch);
+  p.ot_sb = used(a->out_table_stride, a->batch);
+  p.ow_sb = used(a->out_weights_stride, a->batch);
+  for (const int64_t t : {p.t_sb, p.w_sb, p.v_sb, p.ot_sb, p.ow_sb})
+    if (!stride_ok(t)) return set_error(HICACHE_ERR_INVALID_ARG, "strides must be in [0, 2^40)");
+  if (a->batch > 1 && (p.v_sb < a->max_victims || p.ot_sb < a->max_pages || p.ow_sb < a->max_pages))
+    return set_error(HICACHE_ERR_INVALID_ARG, "the rows of an output overlap");
+  if ((a->out_table == a->page_table && p.ot_sb != p.t_sb) || (a->out_weights == a->weights && p.ow_sb != p.w_sb))
+    return set_error(HICACHE_ERR_INVALID_ARG, "an output is its input with another stride");
   p.table = a->page_table;
   p.weights = a->weights;
   p.lens = a->seq_lens;
@@ -388,11 +395,6 @@ int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {
   p.out_table = a->out_table;
   p.out_lens = a->out_lens;
   p.out_weights = a->out_weights;
-  p.t_sb = a->table_stride;
-  p.w_sb = a->weights_stride;
-  p.v_sb = a->victims_stride;
-  p.ot_sb = a->out_table_stride;
-  p.ow_sb = a->out_weights_stride;
   p.P = a->page_size;
   p.B = a->batch;
   p.max_pages = a->max_pages;
