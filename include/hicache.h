@@ -662,9 +662,11 @@ typedef enum { HICACHE_BF16 = 0, HICACHE_FP16 = 1 } hicache_dtype;
  * 0); one whose slot lies outside the buffers stores no K and V: rows that only
  * fill up a batch carry slot -1.  Two tokens of one call with the same slot
  * leave the row undefined.  q_out may be q itself (same strides), else it must
- * not overlap an input.  q may be NULL (q_heads 0), or k and v (kv_heads 0,
- * slots NULL); the norm of heads that are not there is left out, its weight not
- * read.  Pointers and strides must be multiples of 16 bytes (ALIGNMENT);
+ * not overlap an input.  A latent cache may be e4m3 too (to be moved, or read by a
+ * kernel of the caller's: hicache_decode_attention does not).  q may be NULL
+ * (q_heads 0), or k and v (kv_heads 0, slots NULL); the norm of heads that are
+ * not there is left out, its weight not read.  Pointers and strides must be
+ * multiples of 16 bytes (ALIGNMENT);
  * head_dim a multiple of 8 (of 16 into an e4m3 cache), at most 768. */
 typedef struct {
   const void *q;            /* [num_tokens, q_heads, head_dim] of dtype */
@@ -703,6 +705,7 @@ int hicache_append_kv(const hicache_device_kv *kv, const hicache_pool_desc *desc
  * zero-filled before its first use; every call leaves it ready for the next
  * call of any shape it is large enough for.  Calls that may run at the same
  * time (other streams, graphs replayed together) need one each.
+ * out, lse and weights must not overlap an input or one another.
  * head_dim: a multiple of 8 (of 16 for e4m3) up to 256; a latent cache has 576,
  * v_dim 512 and elem_bytes 2.  max_pages * page_size < 2^31. */
 typedef struct {

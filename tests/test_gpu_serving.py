@@ -1090,3 +1090,46 @@ def test_single_rows_with_odd_strides(latent):
     hc.evict_pages(16, t[0], n[0], w[0], keep, vic[0], cnt)
     hc.evict_pages(16, odd(t[1], 2), n[1], odd(w[1], 1), keep, odd(vic[1], 1), cnt)
     assert torch.equal(*t) and torch.equal(*w) and torch.equal(*vic) and cnt.item() == 3
+
+
+@pytest.mark.parametrize("c", [(40, 16, 1, 576, 64, "bf16", True, 0, 512, 64, 512, False, True),
+                               (700, 3, 1, 576, 16, "fp16", True, 576, 512, 64, 512, True, True),
+                               (9, 2, 1, 384, 4, "bf16", True, 384, 384, 96, 10, False, True)], ids=["0", "1", "2"])
+def test_append_latent_e4m3(c):
+    """Latent rows in e4m3: stored like those of K."""
+    test_append(c)
+
+
+# ---- how far off on the whole ------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "e4m3 fp16", "latent bf16", "latent fp16"])
+def test_decode_error_as_a_root_mean_square(kind):
+    """Thousands of tokens of about the same weight, where a bound on each element's worst
+    case is as large as the element: a tile of V left out, or counted twice, would
+    pass it.  Rounding the exponentials p shifts an output, sum p v, by errors that are
+    independent and uniform over half a step either way, u p / sqrt 3 at most as a root
+    mean square: u / sqrt 3 sqrt(sum p^2 v^2) together, where sqrt(sum p^2 v^2) is the
+    outputs' own root mean square (v of mean zero).  The last rounding adds as much of
+    the output's type.  A token left out of 4,096 alone would be 2^-6."""
+    dt = torch.bfloat16 if "bf16" in kind else torch.float16
+    e4, latent = "e4m3" in kind, "latent" in kind
+    lens, P = [4096, 1000, 2777], 16
+    hq, hk, d = (16, 1, 576) if latent else (8, 2, 128)
+    s = decode_inputs(lens, hq, hk, d, P, "bf16" if "bf16" in kind else "fp16", e4, latent, seed=31, sharp=0.5)
+    dv = 512 if latent else d
+    out = torch.empty((3, hq, dv), dtype=dt, device="cuda")
+    w = torch.zeros((3, s["width"]), device="cuda")
+    plain_call(s, out, workspace(s, hq, d, dv, True), weights=w, scale=d ** -0.5)
+    k = s["bufs"][0].view(s["Dp"] * P, -1, d)
+    v = k[..., :512] if latent else s["bufs"][1].view(s["Dp"] * P, -1, d)
+    want = ref.decode(s["q"], k, v, s["clean"], lens, P, d ** -0.5, 0, s["ks"], s["vs"])
+    p_unit = ref.UNIT[torch.float16 if e4 else dt]
+    for i, (o, z, share, _) in enumerate(want):
+        rms = lambda x: x.double().pow(2).mean().sqrt().item()  # noqa: E731
+        # sqrt 3 above that, for chance
+        off = rms(out[i].double() - o) / rms(o)
+        assert off <= (p_unit ** 2 + ref.UNIT[dt] ** 2) ** 0.5, (i, off)
+        # scores: d / 16 <= 36 sums in 32 bits, each off by at most a step (2^-23) of less
+        # than 4; arguments under 16 by 2^-21, the function by 2^-22
+        pages = share.numel()
+        assert rms(w[i, :pages].double() - share) / rms(share) <= 2.0 ** -15
