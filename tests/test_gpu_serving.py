@@ -1133,3 +1133,55 @@ def test_decode_error_as_a_root_mean_square(kind):
         # than 4; arguments under 16 by 2^-21, the function by 2^-22
         pages = share.numel()
         assert rms(w[i, :pages].double() - share) / rms(share) <= 2.0 ** -15
+
+
+# ---- random shapes -----------------------------------------------------------------
+
+def test_append_random_corpus():
+    """Random shapes over the documented ranges, some slots and positions outside."""
+    rnd = random.Random(41)
+    for i in range(120):
+        e4, latent, il = rnd.random() < 0.4, rnd.random() < 0.25, rnd.random() < 0.5
+        unit = 16 if e4 else 8
+        d = rnd.choice((64, 128, 256, 576, unit * rnd.randint(1, 768 // unit), unit * rnd.randint(1, 256 // unit)))
+        hk = 1 if latent else rnd.randint(1, 5)
+        norms = [rnd.choice((0, d, 8 * rnd.randint(0, d // 8), d // 128 * 64)) for _ in range(2)]
+        rot = rnd.choice((0, d, 64 if d >= 64 else 2, 2 * rnd.randint(0, d // 2), d // 4 // 2 * 2))
+        off = rnd.choice((0, d - rot, 2 * rnd.randint(0, (d - rot) // 2), (d - rot) // 64 * 64))
+        n = int(2 ** rnd.uniform(0, 11))
+        c = (n, rnd.randint(1, 17), hk, d, rnd.choice((1, 5, 16, 64)), rnd.choice(("bf16", "fp16")), e4, *norms, rot,
+             off, il, latent)
+        q, k, v, slots, pos, cs, qw, kw, bufs, pages = append_inputs(c, i)
+        skip = torch.zeros(n, dtype=torch.bool, device="cuda")
+        if rnd.random() < 0.5:
+            slots[::3] = rnd.choice((-1, pages * c[4], 2 ** 40))
+            if cs is not None:
+                skip[1::4] = True
+                pos[1::4] = rnd.choice((-1, 5000, -2 ** 50))
+        old = [b.clone() for b in bufs]
+        ks, vs = (0.03, 0.05) if e4 else (1.0, 1.0)
+        q_out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+        hc.append_kv(hc.DeviceKV(bufs, pages), desc(c[4], hk * d, bufs[0].element_size(), len(bufs)), 0, q, k, v, slots,
+                     q_out=q_out, positions=pos if cs is not None else None, cos_sin=cs, rot_offset=off, interleaved=il,
+                     q_weight=qw, k_weight=kw, k_scale=ks, v_scale=vs)
+        try:
+            check_append(c, q, k, v, slots, pos, cs, qw, kw, bufs, q_out, old, ks, vs, skip)
+            assert (q_out[skip] == 7.0).all()
+        except AssertionError as e:
+            raise AssertionError(f"{i}: {c}: {e}") from None
+
+
+def test_evict_random_corpus(monkeypatch):
+    """Random tables, weights, budgets and protected pages, absent pages among them."""
+    monkeypatch.setattr(ref, "evict", evict_present)
+    rng = np.random.default_rng(7)
+    for i in range(80):
+        n, b, P = int(2 ** rng.uniform(0, 13.5)), int(rng.integers(1, 7)), int(rng.choice((1, 4, 16, 100)))
+        w = rng.standard_normal((b, n)).astype(np.float32) if i % 2 else rng.integers(0, 4, (b, n)).astype(np.float32)
+        table = rng.integers(0, 10 ** 6, (b, n))
+        table[rng.random((b, n)) < rng.choice((0.0, 0.0, 0.3, 1.0))] = -1
+        lens = [int(x) for x in rng.integers(-1, n * P + 2 * P, b)]
+        keep = [int(x) for x in rng.integers(-1, n + 2, b)]
+        run_evict(table.tolist(), w.tolist(), lens, keep, P, int(rng.choice((0, 1, 4, n, 2 ** 31 - 1))),
+                  int(rng.choice((1, 2, 8, n + 1, 2 ** 31 - 1), p=(0.4, 0.2, 0.2, 0.1, 0.1))),
+                  int(rng.choice((0, 1, n, 2 * n))), bool(rng.integers(0, 2)), pad=int(rng.integers(0, 3)))
