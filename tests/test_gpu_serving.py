@@ -1185,3 +1185,70 @@ def test_evict_random_corpus(monkeypatch):
         run_evict(table.tolist(), w.tolist(), lens, keep, P, int(rng.choice((0, 1, 4, n, 2 ** 31 - 1))),
                   int(rng.choice((1, 2, 8, n + 1, 2 ** 31 - 1), p=(0.4, 0.2, 0.2, 0.1, 0.1))),
                   int(rng.choice((0, 1, n, 2 * n))), bool(rng.integers(0, 2)), pad=int(rng.integers(0, 3)))
+
+
+# ---- at once, and shared pages -----------------------------------------------------
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_from_threads_at_once(latent):
+    """Calls from several host threads on a stream and a workspace each, over one
+    cache: the bits of a call alone."""
+    import threading
+    d, dv = (576, 512) if latent else (128, 128)
+    s = decode_inputs([3000, 40, 700, 0, 1111], 16, 4, d, 16, latent=latent, seed=9)
+    want, w0 = torch.empty((5, 16, dv), dtype=s["dt"], device="cuda"), torch.zeros((5, s["width"]), device="cuda")
+    plain_call(s, want, workspace(s, 16, d, dv, True), weights=w0)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        st, ws = torch.cuda.Stream(), workspace(s, 16, d, dv, True)
+        with torch.cuda.stream(st):
+            for _ in range(30):
+                out, w = torch.zeros_like(want), torch.zeros_like(w0)
+                st.synchronize()
+                plain_call(s, out, ws, weights=w)
+                st.synchronize()
+                if not (torch.equal(out, want) and torch.equal(w, w0)):
+                    bad.append(1)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_decode_pages_of_several_sequences(latent):
+    """Sequences that share a prefix's pages, one page twice in a sequence, a table that
+    all sequences share (stride 0): as over copies of the pages."""
+    d, dv, P = (576, 512, 16) if latent else (64, 64, 16)
+    s = decode_inputs([160], 4, 2, d, P, latent=latent, spare=0)
+    base = s["table"][0].clone()
+    tables = [base.tolist(), base.tolist()[:4] + base.tolist()[7:] + [-1] * 3, [int(base[2])] * 10]
+    lens = [160, 100, 150]
+    q = torch.randn((3, 4, d), generator=gen(3), device="cuda").to(s["dt"])
+    total = sum(-(-n // P) for n in lens)
+    copies, at, apart = [torch.zeros((total * P, b.shape[1]), dtype=b.dtype, device="cuda") for b in s["bufs"]], 0, []
+    for t, n in zip(tables, lens):
+        row = []
+        for p in t[:-(-n // P)]:
+            for c, b in zip(copies, s["bufs"]):
+                c[at * P:at * P + P] = b[p * P:p * P + P]
+            row.append(at)
+            at += 1
+        apart.append(row + [-1] * (10 - len(row)))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(hc.decode_workspace(s["desc"], 3, 4, d, dv, 10, True), dtype=torch.uint8, device="cuda")
+
+    def call(kv, table):
+        out, w = torch.zeros((3, 4, dv), dtype=s["dt"], device="cuda"), torch.zeros((3, 10), device="cuda")
+        hc.decode_attention(kv, s["desc"], 0, q, table, i32(lens), out, ws, weights=w)
+        return out, w
+    for a, b in zip(call(s["kv"], i32(tables)), call(hc.DeviceKV(copies, total), i32(apart))):
+        assert torch.equal(a, b) and a.any()
+    one = i32([tables[0]])
+    for a, b in zip(call(s["kv"], one.expand(3, 10)), call(s["kv"], one.repeat(3, 1))):
+        assert torch.equal(a, b)

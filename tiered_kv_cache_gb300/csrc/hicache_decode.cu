@@ -24,9 +24,9 @@
 // timing cannot change the result.
 //
 // Measured: 16 sequences of 32,768 tokens, 32 heads on 8 of 128 in bf16 (2.15 GB),
-// 331 us, 6.5 TB/s, 96% of a copy's rate; 64 sequences of 33 to 8,192 tokens, pages of
+// 335 us, 6.4 TB/s, 94% of a copy's rate; 64 sequences of 33 to 8,192 tokens, pages of
 // 16, 84 us (59 streaming, the rest start, joins and SMs that get 12% less of HBM
-// than others); one of 4,097, 12 us, all of it latency.
+// than others); one of 4,097, 11.3 us, all of it latency.
 //
 // Latent caches: hicache_decode_latent.cu.
 
@@ -734,8 +734,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     // piece x of the unit: CTA from + x, its second slot where the unit begins
     auto slot = [&](int x) { return p.cta_parts + (int64_t(from + x) * 2 + (x == 0 ? 1 : 0)) * C::PIECE; };
     // a thread takes four elements of a row, or twice four where there are 16 rows (one
-    // sequence of 4,096 with 12 heads of 256 on each of 4: 41 -> 33 us; with 8 rows,
-    // 8 heads on each, 28.6 -> 32); with threads to spare, every `teams`-th piece of
+    // sequence of 4,096 with 12 heads of 256 on each of 4: 41 -> 34 us; with 8 rows,
+    // 8 heads on each, 28.1 -> 32); with threads to spare, every `teams`-th piece of
     // them.  Maximum, sum and O of 8 pieces are on their way together.
     constexpr int JOIN = ROWS > 8 ? COLS : 1;
     const int cols = nr * COL4, teams = max(1, min(4, THREADS / cols));

@@ -9,9 +9,10 @@
 // A cluster of CTAs takes a sequence, each CTA a part of its pages, which it reads
 // once into shared memory; histograms and counts are summed over the cluster through
 // distributed shared memory.  Everything has been read before anything is written,
-// so the outputs may be the inputs.  Bound by the cluster's barriers: 131,071 pages
-// are 2 MB and take 16 us (198 us by one CTA without them).  Sequences too long for the
-// cluster's shared memory take one CTA that walks them chunk by chunk.
+// so the outputs may be the inputs.  Bound by the cluster's barriers: two sequences of
+// 131,071 and 100,000 pages take 17 us (198 us by one CTA each).  Sequences too long
+// for the cluster's shared memory (393,216 pages) take one CTA that walks them chunk by
+// chunk: 400,000 pages 671 us.
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -316,11 +317,11 @@ int launch_evict(const EvictParams &p, int device, void *stream) {
   constexpr int kMaxDevices = 64;
   constexpr int kCap = 24576;                     // pages of a CTA: 192 KiB of shared memory
   constexpr int kCluster = 16;
-  // One CTA a sequence up to 4,096 pages (9.7 us; 16 took 9.1 for one sequence, but 9.0
-  // against 6.0 at 1,024 pages and 80 against 11 for 64 sequences).  Beyond, as many
-  // as let every sequence's cluster run at once: large clusters find few places
-  // (8 sequences of 16,384 pages: 21.5 us by 16 CTAs each, 11.3 by 8, 22.4 by one;
-  // 64: 96 by 16, 17 by 2, 22 by one).  And no fewer than hold the pages.
+  // One CTA a sequence up to 4,096 pages (one sequence of 4,000: 8.9 us, 7.7 by 16 CTAs;
+  // but 5.6 against 7.5 at 1,000 pages and 10.2 against 83 for 64 sequences).  Beyond,
+  // as many as let every sequence's cluster run at once: large clusters find few places
+  // (8 sequences of 16,384 pages: 18.7 us by 16 CTAs each, 10.3 by 8, 22.0 by one;
+  // 64: 97 by 16, 17.7 by 2, 23.8 by one).  And no fewer than hold the pages.
   int cs = 1;
   if (p.max_pages > 4096) cs = p.B <= 4 ? 16 : p.B <= 9 ? 8 : p.B <= 32 ? 4 : p.B <= 76 ? 2 : 1;
   while (cs < kCluster && int64_t(cs) * kCap < p.max_pages) cs *= 2;
