@@ -616,7 +616,7 @@ int hicache_layer_checksum(const hicache_device_kv *kv, const hicache_pool_desc 
                            const int64_t *device_pages, int64_t n, int32_t layer_id,
                            int32_t reps, uint64_t *out_sum_dev, void *stream);
 
-/* ---- operators on the device pages: append, decode attention, eviction ---------
+/* ---- operators on the device pages: append, attention, eviction -----------------
  * What a serving step runs on the L1 pages between the moves above: new keys
  * and values are stored into their slots, the new token attends to the cached
  * ones, and pages that received little attention leave L1 (their page numbers
@@ -735,6 +735,107 @@ int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32
  * the current device, on every stream; not during a capture.  Errors:
  * INVALID_ARG, ALIGNMENT, CUDA. */
 int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
+
+/* Attention of several query tokens per sequence over its pages.  Sequence b has
+ * the query tokens [q_starts[b], q_starts[b+1]) of q, nq of them, and kv_lens[b]
+ * cached tokens; query i of the sequence (from 0) attends
+ *   causal == 0   to all of them: cross attention to an encoder's states, whose
+ *                 number has nothing to do with that of the queries;
+ *   causal != 0   to the tokens up to kv_lens[b] - nq + i (the last `window` of
+ *                 those if window > 0): a chunk of a prompt, whose own keys and
+ *                 values hicache_append_kv has stored behind the cached prefix;
+ * of which those on absent pages are left out, with scores, lse and out as in
+ * hicache_decode_attention (K and V of kv head h / (q_heads / kv_heads)).  A query
+ * without any such token gives out = 0 and lse = -infinity.  Rows of q that belong to
+ * no sequence (in front of q_starts[0], behind q_starts[batch]) are not read, and
+ * theirs of out and lse left as they were.  q_starts must ascend; its values count
+ * as clamped to [0, num_tokens], those of a sequence that descend as no query.
+ * Pages behind the lengths may hold anything.  V of the cached tokens must be finite:
+ * a causal query's weight of a token it does not see is 0, and 0 times infinity is
+ * not.
+ * The products run on the tensor cores with 32-bit sums, exponentials rounded as in
+ * hicache_decode_attention.
+ * workspace: hicache_query_workspace bytes, under the rules of
+ * hicache_decode_attention's; hicache_decode_status tells whether a call with it gave
+ * up.  out and lse must not overlap an input or one another.
+ * K, V caches (num_buffers 2); head_dim: a multiple of 8 (of 16 for e4m3) up to 256;
+ * num_tokens * q_heads < 2^31 - 4096; batch up to 65,535. */
+typedef struct {
+  const void *q;              /* [num_tokens, q_heads, head_dim] of dtype */
+  void *out;                  /* as q */
+  const int32_t *q_starts;    /* [batch + 1] */
+  const int32_t *page_table;  /* [batch, max_pages] */
+  const int32_t *kv_lens;     /* [batch] */
+  float *lse;                 /* [num_tokens, q_heads], or NULL */
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+  int64_t table_stride, lse_stride;
+  int64_t num_tokens;
+  int32_t dtype, batch, q_heads, head_dim, max_pages, window, causal, reserved;
+  float scale, k_scale, v_scale;
+} hicache_query_desc;
+int hicache_query_attention(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                            const hicache_query_desc *a, void *stream);
+/* The workspace bytes of a call with these sizes, on the current device. */
+int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_t num_tokens, int32_t q_heads,
+                            int32_t head_dim, int32_t max_pages, int64_t *bytes);
+
+/* Attention of one new token per sequence where sequences share a prefix: group g,
+ * the sequences [group_starts[g], group_starts[g+1]), shares the first
+ * prefix_lens[g] tokens on the pages prefix_table[g], and each sequence has
+ * seq_lens[b] tokens of its own, on page_table[b], behind them.  The result is that of
+ * hicache_decode_attention over the prefix's tokens and then the sequence's, but a
+ * group's prefix is read once for all of its sequences.  Sequences of no group (in front
+ * of group_starts[0], behind group_starts[groups]) have their own tokens alone, and
+ * groups may be 0 (the three arrays NULL).  group_starts must ascend, as q_starts of
+ * hicache_query_attention.  Absent pages, lengths, strides, types and the workspace
+ * (hicache_prefix_workspace bytes; hicache_decode_status) as there; the prefixes'
+ * part of a row is kept in 32 bits until it is joined with the rest.
+ * Of several levels of shared prefixes, each is a hicache_query_attention (the queries
+ * of the sequences below it), and hicache_merge_attention joins them. */
+typedef struct {
+  const void *q;                /* [batch, q_heads, head_dim] of dtype */
+  void *out;                    /* as q */
+  const int32_t *group_starts;  /* [groups + 1] */
+  const int32_t *prefix_table;  /* [groups, max_prefix_pages] */
+  const int32_t *prefix_lens;   /* [groups] */
+  const int32_t *page_table;    /* [batch, max_pages] */
+  const int32_t *seq_lens;      /* [batch] */
+  float *lse;                   /* [batch, q_heads], or NULL */
+  void *workspace;
+  int64_t workspace_bytes;
+  int64_t q_batch_stride, q_head_stride, out_batch_stride, out_head_stride;
+  int64_t prefix_stride, table_stride, lse_stride;
+  int32_t dtype, batch, groups, q_heads, head_dim, max_prefix_pages, max_pages, reserved;
+  float scale, k_scale, v_scale;
+} hicache_prefix_desc;
+int hicache_prefix_attention(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                             const hicache_prefix_desc *a, void *stream);
+int hicache_prefix_workspace(const hicache_pool_desc *desc, int32_t batch, int32_t groups, int32_t q_heads,
+                             int32_t head_dim, int32_t max_prefix_pages, int32_t max_pages, int64_t *bytes);
+
+/* Results of attention over parts of the tokens, joined: with part i's out_i and lse_i
+ * (as the calls above return them),
+ *   lse = log sum exp(lse_i),   out = sum exp(lse_i - lse) out_i,
+ * row by row.  A part whose lse is -infinity counts for nothing, whatever its out
+ * holds (it is not read); a row without any part gives out = 0 and lse = -infinity.
+ * out may be a part itself (same strides), else it must not overlap an input; lse
+ * must not overlap one.  head_dim: a multiple of 8; num_tokens * heads *
+ * head_dim / 8 < 2^31 - 4096. */
+#define HICACHE_MERGE_PARTS 8
+typedef struct {
+  const void *part_outs[HICACHE_MERGE_PARTS];   /* [num_tokens, heads, head_dim] of dtype */
+  const float *part_lses[HICACHE_MERGE_PARTS];  /* [num_tokens, heads] */
+  void *out;                                    /* [num_tokens, heads, head_dim] of dtype */
+  float *lse;                                   /* [num_tokens, heads], or NULL */
+  int64_t part_token_strides[HICACHE_MERGE_PARTS], part_head_strides[HICACHE_MERGE_PARTS];
+  int64_t part_lse_strides[HICACHE_MERGE_PARTS];
+  int64_t out_token_stride, out_head_stride, lse_stride;
+  int64_t num_tokens;
+  int32_t dtype, parts, heads, head_dim;
+} hicache_merge_desc;
+int hicache_merge_attention(const hicache_merge_desc *a, void *stream);
 
 /* Which pages of each sequence leave L1: those that received the least
  * attention.  With n = ceil(seq_lens[b] / page_size) pages, those in [sink, n -

@@ -136,3 +136,37 @@ def evict(table, weights, lens, keep, page, sink, recent, cap):
         res.append(([t[p] for p in sorted(gone)], [t[p] for p in stay] + [-1] * count,
                     [w[p] for p in stay] + [0.0] * count, n_t - count * page))
     return res
+
+
+def attend(q, k, v, rows, scale, k_scale=1.0, v_scale=1.0, joins=0):
+    """q [n, hq, d], k and v [slots, hk, d] (values without their scales), rows: for
+    each query the cache rows it attends to.  Results and bounds as decode()'s, for
+    check_decode.  joins: how many results were joined by log-sums kept in 32 bits."""
+    res = []
+    hk, (_, hq, d) = k.shape[1], q.shape
+    for i, at in enumerate(rows):
+        if at.numel() == 0:
+            res.append((torch.zeros(hq, d, dtype=torch.float64, device=q.device),
+                        torch.full((hq,), -torch.inf, dtype=torch.float64, device=q.device), None, None))
+            continue
+        kk, vv = k[at].double() * k_scale, v[at].double() * v_scale
+        qq = q[i].double().view(hk, hq // hk, d)
+        x = torch.einsum("kgd,tkd->kgt", qq, kk) * scale
+        # the errors of scores, exponentials and sums as in decode(); a join by log-sums
+        # adds, for each result, the rounding of its log-sum (in units of log2) and of the
+        # exponential of its distance
+        mass = torch.einsum("kgd,tkd->kgt", qq.abs(), kk.abs()) * abs(scale)
+        big = qq.abs().amax(-1)[..., None] * kk.abs().sum(-1).T[:, None, :] * abs(scale)
+        ds = (mass * (2 * d + 4) * U32 + big * 2.0 ** -25 + 2 * x.abs() * U32).amax(-1)
+        z = torch.logsumexp(x, -1, keepdim=True)
+        p = torch.exp(x - z)
+        out = torch.einsum("kgt,tkd->kgd", p, vv)
+        spread = torch.einsum("kgt,tkd->kgd", p, vv.abs())
+        far = joins * (2 * x.abs().amax(-1) * U32 + 2.0 ** -20)
+        de = 2 * ds + 2.0 ** -19 + far
+        n_t = at.numel()
+        dl = de + n_t * U32
+        res.append((out.reshape(hq, -1), z.flatten(), None,
+                    {"spread": spread.reshape(hq, -1), "de": (de + dl).flatten(), "dl": dl.flatten(),
+                     "n": n_t, "vmax": vv.abs().max().item()}))
+    return res

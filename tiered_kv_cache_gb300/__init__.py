@@ -13,7 +13,9 @@ Names follow the C ABI in ``include/hicache.h``:
     Engine (submission engine), PageAllocator (host pages)
     host_alloc / host_free, wait, prepass, segment_count, page_span, layer_checksum
     tp_share / tp_load_pipelined / Pool.layer_counters (tensor-parallel load of a replicated latent)
-    append_kv / decode_attention / decode_workspace / decode_gave_up / evict_pages (operators on the device pages)
+    append_kv / decode_attention / decode_workspace / decode_gave_up / evict_pages,
+    query_attention / query_workspace / prefix_attention / prefix_workspace / merge_attention
+    (operators on the device pages)
     stream_copy (roofline probe: plain zero-copy streaming copy)
     checked_build / check_status (the bounds-checked build, HICACHE_CHECKED=1)
 """
@@ -34,6 +36,7 @@ __all__ = [
     "host_alloc", "host_free", "wait", "prepass", "segment_count", "layer_checksum", "page_span",
     "launch_count", "version", "stream_copy", "tp_share", "tp_load_pipelined", "checked_build",
     "check_status", "append_kv", "decode_attention", "decode_workspace", "decode_gave_up", "evict_pages",
+    "query_attention", "query_workspace", "prefix_attention", "prefix_workspace", "merge_attention", "MERGE_PARTS",
 ]
 
 LAYOUT_POOL = -1
@@ -149,6 +152,11 @@ def _bind(lib):
         "hicache_decode_attention": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
         "hicache_decode_workspace": (ctypes.c_int, [_P(PoolDesc), _i32, _i32, _i32, _i32, _i32, _i32, _P(_i64)]),
         "hicache_decode_status": (ctypes.c_int, [_vp, _P(_i32), _i32]),
+        "hicache_query_attention": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
+        "hicache_query_workspace": (ctypes.c_int, [_P(PoolDesc), _i32, _i64, _i32, _i32, _i32, _P(_i64)]),
+        "hicache_prefix_attention": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _i32, ctypes.c_char_p, _vp]),
+        "hicache_prefix_workspace": (ctypes.c_int, [_P(PoolDesc), _i32, _i32, _i32, _i32, _i32, _i32, _P(_i64)]),
+        "hicache_merge_attention": (ctypes.c_int, [ctypes.c_char_p, _vp]),
         "hicache_evict_pages": (ctypes.c_int, [ctypes.c_char_p, _vp]),
         "hicache_layer_checksum": (ctypes.c_int, [_P(_DeviceKVStruct), _P(PoolDesc), _vp, _i64, _i32,
                                                   _i32, _vp, _vp]),
@@ -744,6 +752,10 @@ class Plan:
 _APPEND_DESC = struct.Struct("9P10q9i3f")
 _DECODE_DESC = struct.Struct("7P8q8i4f")
 _EVICT_DESC = struct.Struct("9P5q6i")
+_QUERY_DESC = struct.Struct("7P8q8i3f")
+_PREFIX_DESC = struct.Struct("9P8q8i3f")
+_MERGE_DESC = struct.Struct("18P28q4i")
+MERGE_PARTS = 8
 BF16 = 0
 FP16 = 1
 
@@ -975,6 +987,143 @@ def decode_gave_up(workspace, clear: bool = False) -> bool:
     out = ctypes.c_int32()
     _check(library().hicache_decode_status(workspace.data_ptr(), ctypes.byref(out), int(clear)))
     return bool(out.value)
+
+
+def query_workspace(pool_or_desc, batch: int, tokens: int, q_heads: int, head_dim: int, max_pages: int) -> int:
+    """Bytes of workspace a query_attention of these sizes needs.  Zero-fill it
+    once; calls that may run at the same time need one each."""
+    out = ctypes.c_int64()
+    _check(library().hicache_query_workspace(ctypes.byref(_pool_desc(pool_or_desc)), batch, tokens, q_heads, head_dim,
+                                             max_pages, ctypes.byref(out)))
+    return out.value
+
+
+def query_attention(kv: DeviceKV, pool_or_desc, layer: int, q, q_starts, page_table, kv_lens, out, workspace, *,
+                    causal: bool = False, scale=None, window: int = 0, lse=None, k_scale: float = 1.0,
+                    v_scale: float = 1.0, stream=None):
+    """Attention of several query tokens per sequence: sequence b has the tokens
+    [q_starts[b], q_starts[b + 1]) (int32 [batch + 1]) of q [tokens, q_heads,
+    head_dim] and kv_lens[b] cached ones on the pages page_table[b].  Each query
+    attends to all of these (cross attention), or, causal, to those up to its own
+    place when the sequence's queries are its last tokens (the last `window` of them
+    if window > 0).  out as q; lse (optional) [tokens, q_heads]; rows of no sequence
+    are left as they were.  scale: head_dim ** -0.5 unless given; stream: torch's
+    current stream unless given."""
+    torch = _import_torch()
+    code, dev = _activations("q", q)
+    dt = q.dtype
+    desc = _pool_desc(pool_or_desc)
+    _check_cache(kv, desc, layer, dev, dt)
+    n, hq, d = q.shape
+    qt, qh, _ = _tensor("q", q, dt, (n, hq, d), dev)
+    b, width = kv_lens.shape[0], page_table.shape[-1]
+    ot, oh, _ = _tensor("out", out, dt, (n, hq, d), dev)
+    if out.requires_grad:
+        _written("out", out)
+    tst = _tensor("page_table", page_table, torch.int32, (b, width), dev)[0]
+    _tensor("q_starts", q_starts, torch.int32, (b + 1,), dev)
+    _tensor("kv_lens", kv_lens, torch.int32, (b,), dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on device {dev}")
+    lp = lst = 0
+    if lse is not None:
+        lst = _tensor("lse", lse, torch.float32, (n, hq), dev)[0]
+        if lse.requires_grad:
+            _written("lse", lse)
+        lp = lse.data_ptr()
+    a = _QUERY_DESC.pack(q.data_ptr(), out.data_ptr(), q_starts.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+                         lp, workspace.data_ptr(), workspace.numel() * workspace.element_size(), qt, qh, ot, oh, tst,
+                         lst, n, code, b, hq, d, width, window, bool(causal), 0, d ** -0.5 if scale is None else scale,
+                         k_scale, v_scale)
+    rc = library().hicache_query_attention(kv.ref, ctypes.byref(desc), layer, a, _launch_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def prefix_workspace(pool_or_desc, batch: int, groups: int, q_heads: int, head_dim: int, max_prefix_pages: int,
+                     max_pages: int) -> int:
+    """Bytes of workspace a prefix_attention of these sizes needs.  Zero-fill it
+    once; calls that may run at the same time need one each."""
+    out = ctypes.c_int64()
+    _check(library().hicache_prefix_workspace(ctypes.byref(_pool_desc(pool_or_desc)), batch, groups, q_heads, head_dim,
+                                              max_prefix_pages, max_pages, ctypes.byref(out)))
+    return out.value
+
+
+def prefix_attention(kv: DeviceKV, pool_or_desc, layer: int, q, group_starts, prefix_table, prefix_lens, page_table,
+                     seq_lens, out, workspace, *, scale=None, lse=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                     stream=None):
+    """decode_attention where sequences share a prefix: the sequences
+    [group_starts[g], group_starts[g + 1]) (int32 [groups + 1]) attend to the
+    prefix_lens[g] tokens on the pages prefix_table[g], read once for all of them,
+    and each to the seq_lens[b] tokens on its own pages page_table[b].  Sequences of
+    no group have their own tokens alone.  out as q [batch, q_heads, head_dim]; lse
+    (optional) [batch, q_heads] over both.  scale: head_dim ** -0.5 unless given;
+    stream: torch's current stream unless given."""
+    torch = _import_torch()
+    code, dev = _activations("q", q)
+    dt, i32 = q.dtype, torch.int32
+    desc = _pool_desc(pool_or_desc)
+    _check_cache(kv, desc, layer, dev, dt)
+    b, hq, d = q.shape
+    qb, qh, _ = _tensor("q", q, dt, (b, hq, d), dev)
+    groups, wide, width = prefix_lens.shape[0], prefix_table.shape[-1], page_table.shape[-1]
+    ob, oh, _ = _tensor("out", out, dt, (b, hq, d), dev)
+    if out.requires_grad:
+        _written("out", out)
+    pst = _tensor("prefix_table", prefix_table, i32, (groups, wide), dev)[0]
+    _tensor("group_starts", group_starts, i32, (groups + 1,), dev)
+    _tensor("prefix_lens", prefix_lens, i32, (groups,), dev)
+    tst = _tensor("page_table", page_table, i32, (b, width), dev)[0]
+    _tensor("seq_lens", seq_lens, i32, (b,), dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on device {dev}")
+    lp = lst = 0
+    if lse is not None:
+        lst = _tensor("lse", lse, torch.float32, (b, hq), dev)[0]
+        if lse.requires_grad:
+            _written("lse", lse)
+        lp = lse.data_ptr()
+    a = _PREFIX_DESC.pack(q.data_ptr(), out.data_ptr(), group_starts.data_ptr(), prefix_table.data_ptr(),
+                          prefix_lens.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), lp, workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), qb, qh, ob, oh, pst, tst, lst, code, b, groups,
+                          hq, d, wide, width, 0, d ** -0.5 if scale is None else scale, k_scale, v_scale)
+    rc = library().hicache_prefix_attention(kv.ref, ctypes.byref(desc), layer, a, _launch_stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def merge_attention(outs, lses, out, *, lse=None, stream=None):
+    """Results over parts of the tokens, joined: outs and lses are sequences of up
+    to MERGE_PARTS results [tokens, heads, dim] and their log-sums [tokens, heads];
+    out (which may be one of outs) and lse (optional) are those over all parts.  A part whose
+    log-sum is -infinity counts for nothing.  stream: torch's current stream unless
+    given."""
+    torch = _import_torch()
+    parts = len(outs)
+    if not 1 <= parts <= MERGE_PARTS or len(lses) != parts:
+        raise ValueError(f"{parts} outs and {len(lses)} lses, expected 1 to {MERGE_PARTS} of each")
+    code, dev = _activations("out", out)
+    dt = out.dtype
+    n, h, d = shape = out.shape
+    ot, oh, _ = _tensor("out", out, dt, (n, h, d), dev)
+    if out.requires_grad:
+        _written("out", out)
+    rest = [0] * (MERGE_PARTS - parts)
+    strides = [_tensor("a part of outs", x, dt, shape, dev) for x in outs]
+    rows = [_tensor("a part of lses", x, torch.float32, (n, h), dev)[0] for x in lses]
+    lp = lst = 0
+    if lse is not None:
+        lst = _tensor("lse", lse, torch.float32, (n, h), dev)[0]
+        if lse.requires_grad:
+            _written("lse", lse)
+        lp = lse.data_ptr()
+    a = _MERGE_DESC.pack(*[x.data_ptr() for x in outs], *rest, *[x.data_ptr() for x in lses], *rest, out.data_ptr(), lp,
+                         *[s[0] for s in strides], *rest, *[s[1] for s in strides], *rest, *rows, *rest, ot, oh, lst, n,
+                         code, parts, h, d)
+    rc = library().hicache_merge_attention(a, _launch_stream(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def evict_pages(page_size: int, page_table, seq_lens, weights, keep, victims, num_victims, *, sink: int = 0,

@@ -1,0 +1,856 @@
+// hicache_query.cuh -- attention of many query tokens over a paged K, V cache:
+// cross attention, chunks of prompts, and a prefix shared by a batch.
+//
+// The rows of a product are pairs of a query token and one of the G query heads of
+// a kv head, 128 of them, so that a token of the cache serves all that need it:
+//   S [128 rows, 128 tokens] = Q K^T      head_dim / 16 steps
+//   O [128 rows, head_dim]  += P V        8 steps of 16 tokens
+// on the tensor cores (tcgen05), sums in tensor memory.  Two such tiles of rows (a unit
+// of 256) share every block of the cache: while one's scores become exponentials, the
+// tensor cores work for the other.  P goes back to tensor memory in the place of its
+// scores, as the first operand of the second product; K and V lie in shared memory as
+// they came (rows of 128 bytes, 128-byte swizzle).  A head of more than 128 leaves room
+// for one tile of rows and blocks of 64 tokens, and a unit of up to 128 rows has only
+// one: there the two score buffers are filled in turn.
+//
+// Bounds: with N rows a byte of the cache takes N multiply-adds of 2-byte elements, so
+// from 280 rows on the tensor cores bind, below that HBM.
+//
+// Softmax: a thread per row, so that maximum and sum need no other thread.  What a row's
+// scores are taken relative to follows the running maximum only when some score passes
+// it by more than P's type can hold; O is rescaled then, and only then, by the same
+// thread.
+//
+// The work is cut into blocks; the blocks of all units (sequences, kv heads, groups of
+// rows, in order) are dealt in equal contiguous ranges, chunks, to the CTAs (one per
+// SM), whatever the lengths.  A chunk's part of a unit is a piece; whole units are
+// written out directly, the other pieces go to the workspace and query_join_kernel adds
+// them in order, so that timing cannot change the result.
+//
+// Warps: softmax and epilogue (four for each tile of rows), four that copy the cache
+// into shared memory (cp.async, 16 bytes a lane, so any page size, absent tokens as
+// zeros; e4m3 through registers, to fp16), one that issues the products.  Every wait
+// has a limit of about two seconds, after which the CTA gives up, sets the workspace's
+// error word and returns.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <atomic>
+
+#include "hicache_decode.cuh"
+#include "hicache_tcgen05.cuh"
+
+namespace hicache {
+namespace {
+
+enum : int { kQBf16 = 0, kQFp16 = 1, kQE4m3 = 2 };   // element types of the cache
+
+template <int DP_, int TYPE_>
+struct QueryConfig {
+  static constexpr int DP = DP_;                  // head_dim, padded
+  static constexpr int TYPE = TYPE_;
+  static constexpr bool BF16 = TYPE_ == kQBf16;   // the products' type, else fp16
+  static constexpr int ES = TYPE_ == kQE4m3 ? 1 : 2;
+  static constexpr int QT = DP_ <= 128 ? 2 : 1;   // tiles of rows
+  static constexpr int BN = DP_ <= 128 ? 128 : 64;
+  static constexpr int ROWS = QT * kQueryRows;    // of a unit
+  static constexpr int ATOMS = DP_ / 64;          // of 64 elements: 128 bytes a row
+  static constexpr int QATOM_B = kQueryRows * 128, ATOM_B = BN * 128;
+  static constexpr int QTILE_B = ATOMS * QATOM_B, TILE_B = ATOMS * ATOM_B;
+  static constexpr int STAGES = DP_ == 64 ? 8 : 5;
+  static constexpr int SMEM = QT * QTILE_B + STAGES * TILE_B;
+  static constexpr int SOFT_WARPS = 4 * QT, COPY_WARP = SOFT_WARPS, MMA_WARP = COPY_WARP + 4;
+  static constexpr int WARPS = MMA_WARP + 4, THREADS = WARPS * 32;
+  // registers of a thread of each group of four warps: what the launch has, dealt anew
+  static constexpr int SOFT_REGS = QT == 2 ? 200 : 240, COPY_REGS = QT == 2 ? 72 : 168, MMA_REGS = QT == 2 ? 40 : 96;
+  static_assert(4 * QT * SOFT_REGS + 4 * COPY_REGS + 4 * MMA_REGS <= WARPS * (65536 / THREADS / 8 * 8), "registers");
+  static constexpr int O_COL = 2 * BN;            // tensor memory: two score buffers, then O of each tile
+  static constexpr int PIECE = ROWS * DP_ + 2 * ROWS;   // floats: O [tile][element][row], m, l
+  static constexpr float RAISE = kRaise<!BF16>, ABOVE = kAbove<!BF16>;
+  static_assert(O_COL + QT * DP_ <= 512, "tensor memory");
+};
+
+// d += a b, a in tensor memory
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a),
+      "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t addr, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+// The loads so far are there; the registers pass through, so that no use of them moves up.
+__device__ __forceinline__ void tc_loaded32(float *v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tc_st16u(uint32_t addr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+template <int REGS, bool MORE>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+__device__ __forceinline__ uint32_t q_e4m3(uint32_t two) {   // two e4m3 in the low 16 bits -> two fp16, exactly
+  uint32_t r;
+  asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ float2 q_unpack2(uint32_t u, bool bf16) {
+  return bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u))
+              : __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// A sequence's queries and tokens; starts that do not ascend, or leave the rows there
+// are, hold no query.
+struct QuerySeq {
+  int32_t q0, nq, kv;
+};
+__device__ __forceinline__ QuerySeq query_seq(const QueryParams &p, int b) {
+  QuerySeq s;
+  s.q0 = min(max(__ldg(p.starts + b), 0), p.N);
+  s.nq = min(max(__ldg(p.starts + b + 1), s.q0), p.N) - s.q0;
+  s.kv = int(min(int64_t(max(0, __ldg(p.lens + b))), int64_t(p.max_pages) * p.P));
+  return s;
+}
+
+// The pieces of a chunk, in order.
+template <class C>
+struct QueryPieces {
+  long long pos, hi;
+  int b, h, m, units, off;         // the unit: sequence, kv head, group of rows (of `units`); blocks of it done
+  QuerySeq s;
+  QueryUnit u;
+  // the current piece: blocks [x0, x1) of the unit
+  int x0, x1;
+  __device__ __forceinline__ bool begins() const { return x0 == 0; }
+  __device__ __forceinline__ bool ends() const { return x1 == u.blocks; }
+  // one tile of rows, or two that share the blocks
+  __device__ __forceinline__ bool dual() const { return C::QT == 2 && u.rows > kQueryRows; }
+  __device__ __forceinline__ QueryUnit unit(const QueryParams &p, int i) const {
+    return query_unit(i, s.nq, s.kv, p.fd_group, C::ROWS, C::BN, p.causal, p.window);
+  }
+  __device__ __forceinline__ void sequence(const QueryParams &p) {
+    s = query_seq(p, b);
+    units = query_units(s.nq, p.G, C::ROWS);
+  }
+  // the blocks of a kv head of the sequence (a whole warp calls)
+  __device__ __forceinline__ long long blocks(const QueryParams &p) const {
+    const int lane = int(threadIdx.x) & 31;
+    if (units == 0) return 0;
+    if (!p.causal) return (long long)units * unit(p, 0).blocks;
+    long long n = 0;
+    for (int i = lane; i < units; i += 32) n += unit(p, i).blocks;
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+  }
+  // at block `at` of all, `rest` blocks from the first of sequence b (a whole warp calls)
+  __device__ __forceinline__ void start(const QueryParams &p, long long at, long long end, int b0, long long rest) {
+    const int lane = int(threadIdx.x) & 31;
+    pos = at;
+    hi = end;
+    b = b0;
+    long long n;
+    for (;; ++b) {
+      sequence(p);
+      n = blocks(p);
+      if (rest < n * p.Hkv || b + 1 >= p.B) break;
+      rest -= n * p.Hkv;
+    }
+    h = n > 0 ? int(rest / n) : 0;
+    rest -= h * n;
+    m = 0;
+    if (!p.causal) {
+      const int each = unit(p, 0).blocks;
+      m = each > 0 ? int(rest / each) : 0;
+      rest -= (long long)m * each;
+    } else {
+      for (;; m += 32) {           // 32 units at a time
+        const int mine = m + lane < units ? unit(p, m + lane).blocks : 0;
+        int inc = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        const int all = __shfl_sync(0xffffffffu, inc, 31);
+        if (rest >= all && m + 32 < units) {
+          rest -= all;
+          continue;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, inc > rest);
+        const int at_lane = past ? __ffs(int(past)) - 1 : 31;
+        rest -= __shfl_sync(0xffffffffu, inc - mine, at_lane);
+        m += at_lane;
+        break;
+      }
+    }
+    u = unit(p, m);
+    off = int(rest);
+  }
+  __device__ __forceinline__ bool next(const QueryParams &p) {
+    if (pos >= hi) return false;
+    while (off >= u.blocks) {
+      if (++m >= units) {
+        m = 0;
+        if (++h >= p.Hkv) {
+          h = 0;
+          do {
+            if (++b >= p.B) return false;
+            sequence(p);
+          } while (units == 0 || s.kv == 0);
+        }
+      }
+      u = unit(p, m);
+      off = 0;
+    }
+    x0 = off;
+    x1 = int(min((long long)u.blocks, off + (hi - pos)));
+    pos += x1 - x0;
+    off = x1;
+    return true;
+  }
+};
+
+// The output's row of row r of a unit: the query token and head.
+struct QueryRow {
+  int64_t token;
+  int head;
+  int i;                           // query of the sequence
+};
+__device__ __forceinline__ QueryRow query_row(const QueryParams &p, const QuerySeq &s, int h, int r) {
+  QueryRow x;
+  x.i = int(fast_div(uint32_t(r), p.fd_group));
+  x.token = int64_t(s.q0) + x.i;
+  x.head = h * p.G + (r - x.i * p.G);
+  return x;
+}
+__device__ __forceinline__ void query_lse(const QueryParams &p, const QueryRow &x, float m, float l) {
+  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+  if (p.lse2) p.lse2[x.token * p.Hq + x.head] = lse2;
+  if (p.lse) p.lse[x.token * p.lse_st + x.head] = lse2 * kLn2;
+}
+// 8 elements of a row from a multiple of 8 on
+__device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRow &x, int col, const float *v) {
+  if (p.out32) {
+    float4 *at = reinterpret_cast<float4 *>(p.out32 + (x.token * p.Hq + x.head) * p.D + col);
+    at[0] = make_float4(v[0], v[1], v[2], v[3]);
+    at[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  char *at = static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh + col);
+  uint4 w;
+  if (p.bf16)
+    w = make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]), pack2<true>(v[6], v[7]));
+  else
+    w = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+  *reinterpret_cast<uint4 *>(at) = w;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_constant__ QueryParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = 8;
+  __shared__ long long scratch[C::WARPS];
+  __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
+  __shared__ int first_seq;
+  __shared__ __align__(8) unsigned long long bars[2 * C::STAGES + INFO + 12];
+  __shared__ int64_t offs[2][BN];                 // where a block's tokens lie, in bytes; -1: absent
+  __shared__ uint32_t there[INFO][WORDS];         // which of them are present
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+
+  const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t q_s = smem_u32(smem_raw), ring_s = q_s + C::QT * C::QTILE_B;
+  unsigned char *const q_p = smem_raw, *const ring_p = smem_raw + C::QT * C::QTILE_B;
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
+  // a stage is full, empty; what of a block is present; Q of a tile is there; scores,
+  // exponentials of a lane are there, their product with V is done; the last product.
+  // A lane is a score buffer with the warps that take it: 0 and 1 the two tiles of a unit,
+  // 0 and 2 the buffers that one tile fills in turn.  The second tile's warps sit units of one
+  // tile out, so no barrier that they wait on may count there: a phase's parity would pass
+  // for that of a phase two on.
+  constexpr int FULL = 0, EMPTY = C::STAGES, KNOWN = 2 * C::STAGES, QFULL = KNOWN + INFO, SFULL = QFULL + 2,
+                PFULL = SFULL + 3, PVDONE = PFULL + 3, LAST = PVDONE + 3;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
+
+  // ---- the blocks before each sequence; thread i takes `per` sequences
+  const int per = (p.B + THREADS - 1) / THREADS;
+  long long mine = 0;
+  for (int x = 0; x < per; ++x) {
+    const int b = tid * per + x;
+    QueryPieces<C> t;
+    t.s = b < p.B ? query_seq(p, b) : QuerySeq{0, 0, 0};
+    t.units = query_units(t.s.nq, p.G, C::ROWS);
+    long long n = 0;
+    const bool many = p.causal && t.units > 4;    // counted by the whole warp
+    if (!many)
+      for (int i = 0; i < (p.causal ? t.units : min(t.units, 1)); ++i) n += t.unit(p, i).blocks;
+    if (!p.causal) n *= t.units;
+    for (unsigned todo = __ballot_sync(0xffffffffu, many); todo; todo &= todo - 1u) {
+      const int src = __ffs(int(todo)) - 1;
+      QueryPieces<C> o;
+      o.s.nq = __shfl_sync(0xffffffffu, t.s.nq, src);
+      o.s.kv = __shfl_sync(0xffffffffu, t.s.kv, src);
+      o.units = __shfl_sync(0xffffffffu, t.units, src);
+      const long long all = o.blocks(p);
+      if (lane == src) n = all;
+    }
+    mine += n * p.Hkv;
+  }
+  long long total = 0;
+  const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total);
+  // with fewer blocks than CTAs, only as many CTAs take part: each has one then
+  const long long chunks = min((long long)gridDim.x, total);
+  if (blockIdx.x < chunks) {
+    const long long lo = total * int(blockIdx.x) / chunks;
+    if (ahead <= lo && lo < ahead + mine) {       // one thread
+      first_seq = tid * per;
+      first_rest = lo - ahead;
+    }
+  }
+  if (tid == 0) {
+    gave_up = 0;
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(bar(FULL + i), 128);
+      mbar_init(bar(EMPTY + i), 1);
+    }
+    for (int i = 0; i < INFO; ++i) mbar_init(bar(KNOWN + i), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), 128);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bar(SFULL + i), 1);
+      mbar_init(bar(PFULL + i), 128);
+      mbar_init(bar(PVDONE + i), 1);
+    }
+    mbar_init(bar(LAST), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    p.open[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  // rows of which there is nothing to attend to and that no unit holds: of sequences
+  // without tokens, and of queries before the first token
+  for (int b = int(blockIdx.x); b < p.B; b += int(gridDim.x)) {
+    const QuerySeq s = query_seq(p, b);
+    int rows = s.nq * p.G;
+    if (s.kv > 0) rows = p.causal ? max(0, min(s.nq, s.nq - s.kv)) * p.G / C::ROWS * C::ROWS : 0;
+    for (int64_t i = tid; i < int64_t(rows) * p.Hkv; i += THREADS) {
+      const QueryRow x = query_row(p, s, int(i / rows), int(i % rows));
+      const float zero[8] = {};
+      for (int c = 0; c < p.D; c += 8) query_store8(p, x, c, zero);
+      query_lse(p, x, 0.f, 0.f);
+    }
+  }
+  if (p.lse2) {                                   // rows of no sequence
+    const int s0 = min(max(__ldg(p.starts), 0), p.N), s1 = min(max(__ldg(p.starts + p.B), s0), p.N);
+    for (int64_t i = int64_t(blockIdx.x) * THREADS + tid; i < int64_t(p.N) * p.Hq; i += int64_t(gridDim.x) * THREADS)
+      if (i / p.Hq < s0 || i / p.Hq >= s1) p.lse2[i] = -INFINITY;
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (blockIdx.x >= chunks) return;
+  if (q_s & 1023u) {                              // the tiles' swizzle counts on it
+    if (tid == 0) *p.error = 1u;
+    return;
+  }
+
+  if (warp == C::MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)), "n"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+
+  const int d16 = (p.D + 15) & ~15;
+  auto begin = [&](QueryPieces<C> &pc) {
+    pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+  };
+
+  if (warp >= C::MMA_WARP) {
+    set_registers<C::MMA_REGS, false>();
+    if (warp == C::MMA_WARP) {
+      // ---- the products: the warp runs as one, one elected lane issues.  In the order
+      // QK(0) QK(1) PV(0) QK(2) PV(1) QK(3) ...: products of one CTA run in order, so
+      // QK(s + 2) may overwrite the buffer that PV(s) reads.
+      QueryPieces<C> pc;
+      begin(pc);
+      const uint32_t s_desc = instr_desc(C::BF16, kQueryRows, BN, false, false);
+      const uint32_t o_desc = instr_desc(C::BF16, kQueryRows, d16, false, true);
+      const int ksteps = d16 / 16;
+      int kst = 0, kph = 0, vst = 1, vph = 0;     // stage and phase of the next block's K, V
+      uint32_t used[3] = {0, 0, 0}, duals = 0, pieces = 0;
+      bool ok = true;
+      auto wait = [&](int b, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, &gave_up));
+      };
+      while (ok && pc.next(p)) {
+        const bool dual = pc.dual();
+        const int steps = (pc.x1 - pc.x0) << int(dual);
+        wait(QFULL, pieces++);
+        if (ok && dual) wait(QFULL + 1, duals++);
+        auto qk = [&](int s) {
+          const int x = s & 1, tile = dual ? x : 0, way = dual ? x : 2 * x;
+          if (!dual || x == 0) wait(FULL + kst, uint32_t(kph));
+          if (!ok) return;
+          proxy_fence();
+          tc_fence_after();
+          const uint32_t a = __shfl_sync(0xffffffffu, q_s + tile * C::QTILE_B, 0);
+          const uint32_t k = __shfl_sync(0xffffffffu, ring_s + kst * C::TILE_B, 0);
+          const bool release = !dual || x == 1;
+          if (elect_one()) {
+            for (int i = 0; i < ksteps; ++i)
+              tc_mma(tmem + x * BN, smem_desc(a + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
+                     smem_desc(k + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
+            if (release) tc_commit(bar(EMPTY + kst));
+            tc_commit(bar(SFULL + way));
+          }
+          __syncwarp();
+          if (release && (kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
+        };
+        auto pv = [&](int s) {
+          const int x = s & 1, tile = dual ? x : 0, way = dual ? x : 2 * x;
+          wait(PFULL + way, used[way] + (s >> 1));
+          if (ok && (!dual || x == 0)) wait(FULL + vst, uint32_t(vph));
+          if (!ok) return;
+          proxy_fence();
+          tc_fence_after();
+          const uint32_t v = __shfl_sync(0xffffffffu, ring_s + vst * C::TILE_B, 0);
+          const bool release = !dual || x == 1, add = s >= (dual ? 2 : 1);
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < BN / 16; ++i)
+              tc_mma_ta(tmem + C::O_COL + tile * C::DP, tmem + x * BN + i * 8, smem_desc(v + i * 2048, C::ATOM_B, 1024),
+                        o_desc, add || i > 0);
+            if (release) tc_commit(bar(EMPTY + vst));
+            tc_commit(bar(PVDONE + way));
+          }
+          __syncwarp();
+          if (release && (vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
+        };
+        qk(0);
+        if (ok && steps > 1) qk(1);
+        for (int s = 0; ok && s < steps; ++s) {
+          pv(s);
+          if (ok && s + 2 < steps) qk(s + 2);
+        }
+        used[0] += uint32_t(steps + 1) >> 1;
+        used[dual ? 1 : 2] += uint32_t(steps) >> 1;
+      }
+      if (elect_one()) tc_commit(bar(LAST));
+      __syncwarp();
+    }
+  } else if (warp >= C::COPY_WARP) {
+    set_registers<C::COPY_REGS, false>();
+    // ---- copies
+    QueryPieces<C> pc;
+    begin(pc);
+    const int pt = tid - C::COPY_WARP * 32;
+    int stage = 0, phase = 1;
+    uint32_t blk = 0;
+    bool ok = true;
+    while (ok && pc.next(p)) {
+      int t = (pc.u.blk0 + pc.x0) * BN + pt, pg = 0, page = -1;
+      // the tokens that some row of the unit sees
+      int lo, hi, unused;
+      query_sees(int(fast_div(uint32_t(pc.u.row0), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window, &lo, &unused);
+      query_sees(int(fast_div(uint32_t(pc.u.row0 + pc.u.rows - 1), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window,
+                 &unused, &hi);
+      auto lookup = [&]() {
+        page = -1;
+        if (pt < BN && t >= lo && t < hi) {
+          pg = int(fast_div(uint32_t(t), p.fd_page));
+          page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
+        }
+      };
+      lookup();
+      for (int x = pc.x0; ok && x < pc.x1; ++x, ++blk) {
+        const bool have = page_present(page, p.num_pages);
+        int64_t *const at = offs[blk & 1u];
+        if (pt < BN)
+          at[pt] = have ? ((int64_t(page) * p.P + (t - pg * p.P)) * p.row + int64_t(pc.h) * p.D) * C::ES : -1;
+        const uint32_t word = __ballot_sync(0xffffffffu, have);
+        if (lane == 0) {
+          if (pt < BN) there[blk % INFO][pt >> 5] = word;
+          mbar_arrive(bar(KNOWN + blk % INFO));
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        t += BN;
+        if (x + 1 < pc.x1) lookup();
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up);
+          if (!ok) break;
+          const char *src = static_cast<const char *>(kv ? p.v : p.k);
+          if constexpr (C::TYPE != kQE4m3) {
+            const int c = pt & 7, r0 = pt >> 3;   // 8 lanes a row of 128 bytes, 16 rows at a time
+            const uint32_t dst = ring_s + stage * C::TILE_B + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+#pragma unroll
+            for (int i = 0; i < BN / 16; ++i) {
+              const int64_t o = at[i * 16 + r0];
+#pragma unroll
+              for (int a = 0; a < C::ATOMS; ++a) {
+                const int col = a * 64 + c * 8;
+                if (col < d16) {
+                  const bool in = o >= 0 && col < p.D;
+                  cp_async16(dst + a * C::ATOM_B + i * 2048, src + (in ? o + col * 2 : 0), in ? 16 : 0);
+                }
+              }
+            }
+            mbar_arrive_copies(bar(FULL + stage));
+          } else {
+            constexpr int RC = C::DP / 16, RP = 128 / RC;   // 16-byte chunks of a row, rows at a time
+            const int c = pt % RC, r0 = pt / RC;
+            unsigned char *const dst = ring_p + stage * C::TILE_B + (c >> 2) * C::ATOM_B;
+            if (c * 16 < p.D) {
+              uint4 w[BN / RP];
+#pragma unroll
+              for (int i = 0; i < BN / RP; ++i) {
+                const int64_t o = at[i * RP + r0];
+                w[i] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + o + c * 16)) : make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int i = 0; i < BN / RP; ++i) {
+                const int r = i * RP + r0, j = 2 * (c & 3);
+                *reinterpret_cast<uint4 *>(dst + r * 128 + ((j ^ (r & 7)) << 4)) =
+                    make_uint4(q_e4m3(w[i].x), q_e4m3(w[i].x >> 16), q_e4m3(w[i].y), q_e4m3(w[i].y >> 16));
+                *reinterpret_cast<uint4 *>(dst + r * 128 + (((j + 1) ^ (r & 7)) << 4)) =
+                    make_uint4(q_e4m3(w[i].z), q_e4m3(w[i].z >> 16), q_e4m3(w[i].w), q_e4m3(w[i].w >> 16));
+              }
+            }
+            proxy_fence();
+            mbar_arrive(bar(FULL + stage));
+          }
+          if (++stage == C::STAGES) stage = 0, phase ^= 1;
+        }
+      }
+    }
+    if constexpr (C::TYPE != kQE4m3) asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    set_registers<C::SOFT_REGS, true>();
+    // ---- softmax: a thread per row
+    QueryPieces<C> pc;
+    begin(pc);
+    const int tile = warp >> 2, r = tid & 127;
+    const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t o_at = tmem + C::O_COL + tile * C::DP + lanes;
+    uint32_t used0 = 0, used2 = 0, blk = 0;       // of this tile's lane, of lane 2
+    bool ok = true;
+    while (ok && pc.next(p)) {
+      const bool dual = pc.dual();
+      const int n = pc.x1 - pc.x0;
+      if (tile == 1 && !dual) {                   // the other tile's
+        blk += uint32_t(n);
+        continue;
+      }
+      // where block j's scores are, and how often its lane was used before
+      auto way = [&](int j) { return dual ? tile : 2 * (j & 1); };
+      auto turn = [&](int j) { return dual ? used0 + uint32_t(j) : ((j & 1) ? used2 : used0) + (uint32_t(j) >> 1); };
+      // ---- Q: this thread's row into shared memory (the products that read the one
+      // before it are done: their scores were)
+      const int row = tile * kQueryRows + r;
+      const bool live = row < pc.u.rows;
+      const QueryRow out = query_row(p, pc.s, pc.h, pc.u.row0 + (live ? row : 0));
+      int lo = 0, hi = 0;
+      if (live) query_sees(out.i, pc.s.nq, pc.s.kv, p.causal, p.window, &lo, &hi);
+      float mul = p.scale2;
+      {
+        const char *src = static_cast<const char *>(p.q) + 2 * (out.token * p.q_st + int64_t(out.head) * p.q_sh);
+        unsigned char *dst = q_p + tile * C::QTILE_B + r * 128;
+        float down = 1.f;
+        if constexpr (C::TYPE == kQE4m3) {
+          // fp16, after the power of two that brings the row's largest element into
+          // [1, 2): bf16 and fp16 queries keep every bit down to 2^-14 of it, and
+          // below that are off by 2^-25 of it at most
+          float top = 0.f;
+          for (int c = 0; live && c < p.D; c += 8) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 2 * c));
+            for (const uint32_t y : {w.x, w.y, w.z, w.w}) {
+              const float2 f = q_unpack2(y, p.bf16);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          const int ex = top > 0.f && top < INFINITY ? max(-120, min(120, ilogbf(top))) : 0;
+          down = ldexpf(1.f, -ex);
+          mul = p.scale2 * ldexpf(1.f, ex);
+        }
+#pragma unroll 4
+        for (int c = 0; c < d16; c += 8) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (live && c < p.D) w = __ldg(reinterpret_cast<const uint4 *>(src + 2 * c));
+          if constexpr (C::TYPE == kQE4m3) {
+            auto lower = [&](uint32_t y) {
+              const float2 f = q_unpack2(y, p.bf16);
+              return pack2<false>(f.x * down, f.y * down);
+            };
+            w = make_uint4(lower(w.x), lower(w.y), lower(w.z), lower(w.w));
+          }
+          *reinterpret_cast<uint4 *>(dst + (c >> 6) * C::QATOM_B + ((((c >> 3) & 7) ^ (r & 7)) << 4)) = w;
+        }
+        proxy_fence();
+        mbar_arrive(bar(QFULL + tile));
+      }
+      const bool any = __any_sync(0xffffffffu, live);   // of a warp without rows, nothing is looked at
+      float m = -INFINITY, mu = 0.f, l0 = 0.f, l1 = 0.f;
+      for (int j = 0; j < n; ++j, ++blk) {
+        const int x = dual ? tile : j & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(j)), turn(j) & 1u, &gave_up));
+        if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(bar(KNOWN + blk % INFO), (blk / INFO) & 1u, &gave_up));
+        if (!ok) break;
+        if (!any) {
+          mbar_arrive(bar(PFULL + way(j)));
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t s_at = tmem + x * BN + lanes;
+        float e[BN];                              // scores less the reference, in log2
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) tc_ld32(s_at + w * 32, e + w * 32);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) tc_loaded32(e + w * 32);
+#pragma unroll
+        for (int i = 0; i < BN; ++i) e[i] = fmaf(e[i], mul, -mu);
+        // what this row does not see
+        const int t0 = (pc.u.blk0 + pc.x0 + j) * BN;
+        bool mask = lo > t0 || hi < t0 + BN;
+        uint32_t words[WORDS];
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          words[w] = there[blk % INFO][w];
+          mask |= words[w] != ~0u;
+        }
+        if (__any_sync(0xffffffffu, mask)) {
+#pragma unroll
+          for (int w = 0; w < WORDS; ++w) {
+            const int a = min(32, max(0, lo - t0 - 32 * w)), z = min(32, max(0, hi - t0 - 32 * w));
+            const uint32_t in = words[w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
+          }
+        }
+        float over = e[0];
+#pragma unroll
+        for (int i = 1; i < BN; ++i) over = fmaxf(over, e[i]);
+        const bool raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
+        if (__any_sync(0xffffffffu, raise)) {
+          float f = 1.f;
+          if (raise) {
+            const float now = fmaxf(m, over + mu - C::ABOVE), by = mu - now;
+            f = m == -INFINITY ? 0.f : exp2_fast(m - now);
+            m = mu = now;
+            l0 *= f;
+            l1 *= f;
+#pragma unroll
+            for (int i = 0; i < BN; ++i) e[i] += by;
+          }
+          __syncwarp();
+          if (j > 0) {                            // O, once the product with V before this is done
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + way(j - 1)), turn(j - 1) & 1u, &gave_up));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < d16; c += 16) {
+              float o[16];
+              tc_ld16(o_at + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tc_st16(o_at + c, o);
+            }
+          }
+        }
+        // P, rounded to the products' type for the tensor cores (the sums keep all bits)
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
+            l0 += a;
+            l1 += z;
+            pk[i] = pack2<C::BF16>(a, z);
+          }
+          tc_st16u(s_at + w * 16, pk);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(PFULL + way(j)));
+      }
+      if (!ok) break;
+      // ---- the piece's end
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + way(n - 1)), turn(n - 1) & 1u, &gave_up));
+      if (!ok) break;
+      used0 += dual ? uint32_t(n) : uint32_t(n + 1) >> 1;
+      used2 += dual ? 0u : uint32_t(n) >> 1;
+      const float l = l0 + l1;
+      const bool whole = pc.begins() && pc.ends();
+      float *const part = p.parts + (int64_t(blockIdx.x) * 2 + (pc.begins() ? 1 : 0)) * C::PIECE;
+      if (any) {
+        tc_fence_after();
+        const float f = l == 0.f ? 0.f : p.v_scale / l;
+#pragma unroll 1
+        for (int c = 0; c < d16; c += 16) {
+          float o[16];
+          __syncwarp();
+          tc_ld16(o_at + c, o);
+          tc_wait_ld();
+          if (!live) continue;
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * f;
+            query_store8(p, out, c, o);
+            if (c + 8 < p.D) query_store8(p, out, c + 8, o + 8);
+          } else {
+            float *at = part + (tile * C::DP + c) * kQueryRows + r;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(at + i * kQueryRows, o[i]);
+          }
+        }
+        if (live && whole) query_lse(p, out, m, l);
+        if (live && !whole) {
+          __stcg(part + C::ROWS * C::DP + row, m);
+          __stcg(part + C::ROWS * C::DP + C::ROWS + row, l);
+        }
+        tc_fence_before();
+      }
+      if (tid == 0 && pc.begins() && !pc.ends()) {
+        // the chunks that the unit lies in
+        const long long first = pc.pos - pc.x1;
+        const int last = int(((first + pc.u.blocks) * chunks - 1) / total);
+        p.open[blockIdx.x] = make_int4(pc.b, pc.h, pc.m, last - int(blockIdx.x) + 1);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    // nothing is in flight when the tensor memory is given back, after a wait that ran
+    // out neither: the products that were issued end by themselves
+    mbar_wait<true>(bar(LAST), 0, &gave_up);
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512) : "memory");
+    // every role has passed its waits, and this was the last one
+    const int which = *static_cast<volatile int *>(&gave_up);
+    if (lane == 0 && which) *p.error = 1u + ((uint32_t(which) - bar0) >> 3) + (blockIdx.x << 8);
+  }
+}
+
+// Adds the pieces of the units that several chunks share: a block per chunk in which
+// such a unit may begin, tile of rows and 8 elements; a thread per row.
+template <int DP, int QT>
+__global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_constant__ QueryParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int ROWS = QT * kQueryRows, PIECE = ROWS * DP + 2 * ROWS, BN = DP <= 128 ? 128 : 64;
+  const int chunk = int(blockIdx.x), col = int(blockIdx.y) * 8;
+  if (col >= p.D) return;
+  const int4 at = __ldcg(p.open + chunk);
+  if (!query_open(chunk, at.w, int(gridDim.x)) || at.x < 0 || at.x >= p.B || at.y < 0 || at.y >= p.Hkv || at.z < 0) return;
+  const QuerySeq s = query_seq(p, at.x);
+  if (at.z >= query_units(s.nq, p.G, ROWS)) return;
+  const QueryUnit u = query_unit(at.z, s.nq, s.kv, p.fd_group, ROWS, BN, p.causal, p.window);
+  const int row = int(blockIdx.z) * kQueryRows + int(threadIdx.x);
+  if (row >= u.rows) return;
+  auto slot = [&](int x) { return p.parts + (int64_t(chunk + x) * 2 + (x == 0 ? 1 : 0)) * PIECE; };
+  float m = -INFINITY, sum = 0.f, acc[8] = {};
+  constexpr int AT_ONCE = 4;
+  for (int x0 = 0; x0 < at.w; x0 += AT_ONCE) {
+    float v[AT_ONCE][8], mx[AT_ONCE], lx[AT_ONCE];
+#pragma unroll
+    for (int x = 0; x < AT_ONCE; ++x) {
+      mx[x] = -INFINITY;
+      if (x0 + x >= at.w) continue;
+      const float *d = slot(x0 + x);
+      mx[x] = __ldcg(d + ROWS * DP + row);
+      lx[x] = __ldcg(d + ROWS * DP + ROWS + row);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[x][i] = __ldcg(d + (int(blockIdx.z) * DP + col + i) * kQueryRows + int(threadIdx.x));
+    }
+#pragma unroll
+    for (int x = 0; x < AT_ONCE; ++x) {
+      if (mx[x] == -INFINITY) {                   // nothing seen there (or only NaN, which its sum then is)
+        if (x0 + x < at.w && lx[x] != lx[x]) sum = lx[x];
+        continue;
+      }
+      const float now = fmaxf(m, mx[x]);
+      const float was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = exp2_fast(mx[x] - now);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = acc[i] * was + f * v[x][i];
+      sum = sum * was + f * lx[x];
+      m = now;
+    }
+  }
+  const float f = sum == 0.f ? 0.f : p.v_scale / sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = sum == 0.f ? 0.f : acc[i] * f;
+  const QueryRow out = query_row(p, s, at.y, u.row0 + row);
+  query_store8(p, out, col, acc);
+  if (col == 0) query_lse(p, out, m, sum);
+}
+
+template <class P>
+int query_launch(void (*kernel)(const P), dim3 grid, unsigned threads, cudaStream_t st, const P &p, size_t smem) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, p);
+  return int(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+constexpr int kQueryDevices = 64;
+
+// The kernel (its shared memory is raised once per device, on first use) and the join.
+template <class C>
+int launch_query_as(const QueryParams &p, int device, cudaStream_t st, int *launches) {
+  static std::atomic<bool> ready[kQueryDevices];
+  if (device >= kQueryDevices || !ready[device].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(query_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return int(e);
+    if (device < kQueryDevices) ready[device].store(true, std::memory_order_release);
+  }
+  int e = query_launch(query_kernel<C>, dim3(kQueryCtas), C::THREADS, st, p, C::SMEM);
+  if (e) return e;
+  ++*launches;
+  e = query_launch(query_join_kernel<C::DP, C::QT>, dim3(kQueryCtas, C::DP / 8, C::QT), kQueryRows, st, p, 0);
+  *launches += e == 0;
+  return e;
+}
+
+}  // namespace
+}  // namespace hicache

@@ -1,7 +1,8 @@
 // hicache_serving.cpp -- argument checks and launches of the operators on the
-// device pages: hicache_append_kv, hicache_decode_attention and
-// hicache_evict_pages.  The kernels are in hicache_append.cu, hicache_decode.cu
-// and hicache_evict.cu.
+// device pages: hicache_append_kv, hicache_decode_attention,
+// hicache_query_attention, hicache_prefix_attention, hicache_merge_attention and
+// hicache_evict_pages.  The kernels are in hicache_append.cu, hicache_decode.cu,
+// hicache_query.cu, hicache_merge.cu and hicache_evict.cu.
 //
 // No call allocates, waits for the GPU or reads device memory.  Like every
 // call of the library, each checks its arguments before it enqueues anything.
@@ -12,6 +13,7 @@
 
 #include <cmath>
 #include <cstdlib>
+#include <initializer_list>
 
 #include "hicache.h"
 #include "hicache_host.h"
@@ -138,6 +140,105 @@ int decode_sizes(const Shape &s, int64_t batch, int64_t q_heads, int64_t head_di
   p->e4m3 = s.es == 1;
   p->latent = s.B == 1;
   return HICACHE_OK;
+}
+
+// What calls with many queries have in common.
+int check_query_dtype(int32_t dtype, int32_t reserved, const Shape &s, float k_scale, float v_scale) {
+  if (dtype != HICACHE_BF16 && dtype != HICACHE_FP16) return set_error(HICACHE_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (reserved != 0) return set_error(HICACHE_ERR_INVALID_ARG, "reserved must be 0");
+  return check_scales(s, k_scale, v_scale);
+}
+
+// Checks the sizes of a call with `tokens` queries of `batch` sequences.
+int query_sizes(const Shape &s, int64_t batch, int64_t tokens, int64_t q_heads, int64_t head_dim, int64_t max_pages,
+                hicache::QueryParams *p) {
+  if (s.B != 2) return set_error(HICACHE_ERR_INVALID_ARG, "calls with many queries take K, V caches (num_buffers 2)");
+  hicache::DecodeParams d{};
+  const int rc = decode_sizes(s, batch, q_heads, head_dim, head_dim, max_pages, &d);
+  if (rc) return rc;
+  if (tokens < 0 || tokens > ((int64_t(1) << 31) - 4096) / q_heads)
+    return set_error(HICACHE_ERR_INVALID_ARG, "num_tokens = %lld times q_heads = %lld must be in [0, 2^31 - 4096]",
+                     (long long)tokens, (long long)q_heads);
+  p->B = d.B;
+  p->N = int32_t(tokens);
+  p->Hq = d.Hq;
+  p->Hkv = d.Hkv;
+  p->G = d.G;
+  p->D = d.D;
+  p->P = d.P;
+  p->max_pages = d.max_pages;
+  p->row = d.row;
+  p->e4m3 = d.e4m3;
+  p->fd_page = hicache::make_fastdiv(uint32_t(s.P));
+  p->fd_group = hicache::make_fastdiv(uint32_t(d.G));
+  return HICACHE_OK;
+}
+
+// Places the workspace of a query kernel at `at`; its error word is the call's.
+void query_place(char *at, void *error, hicache::QueryParams *p) {
+  const hicache::QuerySpace sp = hicache::query_space(p->D, 1);
+  p->error = static_cast<unsigned int *>(error) + hicache::kDecodeCtas;
+  p->open = reinterpret_cast<int4 *>(at + sp.open);
+  p->parts = reinterpret_cast<float *>(at + sp.parts);
+}
+
+// Scores' factor in log2.
+int check_scale(float scale, float k_scale, float *scale2) {
+  if (!std::isfinite(scale)) return set_error(HICACHE_ERR_INVALID_ARG, "scale must be finite");
+  *scale2 = float(double(scale) * double(k_scale) * 1.4426950408889634);
+  if (!std::isfinite(*scale2)) return set_error(HICACHE_ERR_INVALID_ARG, "scale * k_scale leaves 32 bits");
+  return HICACHE_OK;
+}
+
+int check_ints(std::initializer_list<const void *> arrays, const char *what) {
+  for (const void *a : arrays) {
+    if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "%s is NULL", what);
+    if (!aligned(a, 4)) return set_error(HICACHE_ERR_ALIGNMENT, "%s is not aligned to its elements", what);
+  }
+  return HICACHE_OK;
+}
+
+int check_lse(const float *lse, int64_t stride, int64_t n, int64_t heads) {
+  if (!lse) return HICACHE_OK;
+  if (!stride_ok(stride) || !rows_disjoint(n, stride, 1, 0, heads))
+    return set_error(HICACHE_ERR_INVALID_ARG, "lse_stride must be at least the number of heads");
+  if (!aligned(lse, 4)) return set_error(HICACHE_ERR_ALIGNMENT, "lse is not aligned to its elements");
+  return HICACHE_OK;
+}
+
+int check_workspace(const void *ws, int64_t have, int64_t need) {
+  if (!ws) return set_error(HICACHE_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned(ws, 256)) return set_error(HICACHE_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  if (have < need)
+    return set_error(HICACHE_ERR_INVALID_ARG, "workspace of %lld bytes is below the %lld needed", (long long)have,
+                     (long long)need);
+  return HICACHE_OK;
+}
+
+// The workspace of a call over prefixes: decode attention's, the prefixes' part of every
+// row and its log-sum, the query kernel's.
+struct PrefixSpace {
+  int64_t prior, prior_lse2, query, bytes;
+};
+PrefixSpace prefix_space(const hicache::DecodeParams &d) {
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  PrefixSpace s{};
+  s.prior = up(hicache::decode_space(d, false).bytes);
+  s.prior_lse2 = up(s.prior + int64_t(d.B) * d.Hq * d.D * 4);
+  s.query = up(s.prior_lse2 + int64_t(d.B) * d.Hq * 4);
+  s.bytes = s.query + hicache::query_space(d.D, 1).bytes;
+  return s;
+}
+
+// Points a decode call into its workspace.
+void decode_place(char *ws, const hicache::DecodeSpace &sp, hicache::DecodeParams *p) {
+  p->counters = reinterpret_cast<unsigned int *>(ws);
+  p->cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
+  p->seq_pieces = reinterpret_cast<int2 *>(ws + sp.seq_pieces);
+  p->warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
+  p->lse2 = reinterpret_cast<float *>(ws + sp.lse2);
+  p->scores = reinterpret_cast<float *>(ws + sp.scores);
+  p->score_row = sp.score_row;
 }
 
 }  // namespace
@@ -308,7 +409,6 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   if (a->workspace_bytes < sp.bytes)
     return set_error(HICACHE_ERR_INVALID_ARG, "workspace of %lld bytes is below the %lld needed",
                      (long long)a->workspace_bytes, (long long)sp.bytes);
-  char *ws = static_cast<char *>(a->workspace);
   p.q = a->q;
   p.k = k;
   p.v = v;
@@ -318,13 +418,7 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.lse = a->lse;
   p.weights = a->weights;
   p.num_pages = kv->device_num_pages;
-  p.counters = reinterpret_cast<unsigned int *>(ws);
-  p.cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
-  p.seq_pieces = reinterpret_cast<int2 *>(ws + sp.seq_pieces);
-  p.warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
-  p.lse2 = reinterpret_cast<float *>(ws + sp.lse2);
-  p.scores = reinterpret_cast<float *>(ws + sp.scores);
-  p.score_row = sp.score_row;
+  decode_place(static_cast<char *>(a->workspace), sp, &p);
   p.window = a->window;
   p.bf16 = a->dtype == HICACHE_BF16;
   p.fd_page = hicache::make_fastdiv(uint32_t(s.P));
@@ -350,6 +444,202 @@ int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear) {
   if (e != cudaSuccess) return cuda_error(e, "decode status");
   *gave_up = x != 0;
   return HICACHE_OK;
+}
+
+int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_t num_tokens, int32_t q_heads,
+                            int32_t head_dim, int32_t max_pages, int64_t *bytes) {
+  clear_error();
+  Shape s{};
+  int rc = check_desc(desc, &s, true);
+  if (rc) return rc;
+  if (!bytes) return set_error(HICACHE_ERR_INVALID_ARG, "bytes is NULL");
+  hicache::QueryParams p{};
+  if ((rc = query_sizes(s, batch, num_tokens, q_heads, head_dim, max_pages, &p))) return rc;
+  *bytes = hicache::query_space(p.D, 1).bytes;
+  return HICACHE_OK;
+}
+
+int hicache_query_attention(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                            const hicache_query_desc *a, void *stream) {
+  clear_error();
+  Shape s{};
+  void *k = nullptr, *v = nullptr;
+  int rc = check_pages(kv, desc, layer_id, &s, &k, &v);
+  if (rc) return rc;
+  if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the query descriptor is NULL");
+  if ((rc = check_query_dtype(a->dtype, a->reserved, s, a->k_scale, a->v_scale))) return rc;
+  hicache::QueryParams p{};
+  if ((rc = query_sizes(s, a->batch, a->num_tokens, a->q_heads, a->head_dim, a->max_pages, &p))) return rc;
+  if ((rc = check_scale(a->scale, a->k_scale, &p.scale2))) return rc;
+  if (a->window < 0 || (a->window > 0 && !a->causal))
+    return set_error(HICACHE_ERR_INVALID_ARG, "window must be >= 0, and 0 unless causal");
+  if (a->batch == 0 || a->num_tokens == 0) return HICACHE_OK;
+  p.q_st = used(a->q_token_stride, a->num_tokens);
+  p.q_sh = used(a->q_head_stride, a->q_heads);
+  p.o_st = used(a->out_token_stride, a->num_tokens);
+  p.o_sh = used(a->out_head_stride, a->q_heads);
+  p.t_sb = used(a->table_stride, a->batch);
+  p.lse_st = used(a->lse_stride, a->num_tokens);
+  if ((rc = check_heads("q", a->q, p.q_st, p.q_sh))) return rc;
+  if ((rc = check_heads("out", a->out, p.o_st, p.o_sh))) return rc;
+  if (!rows_disjoint(a->num_tokens, p.o_st, a->q_heads, p.o_sh, a->head_dim))
+    return set_error(HICACHE_ERR_INVALID_ARG, "out: heads overlap one another");
+  if ((rc = check_ints({a->q_starts, a->page_table, a->kv_lens}, "q_starts, page_table or kv_lens"))) return rc;
+  if (!stride_ok(p.t_sb)) return set_error(HICACHE_ERR_INVALID_ARG, "table_stride must be in [0, 2^40)");
+  if ((rc = check_lse(a->lse, p.lse_st, a->num_tokens, a->q_heads))) return rc;
+  if ((rc = check_workspace(a->workspace, a->workspace_bytes, hicache::query_space(p.D, 1).bytes))) return rc;
+  p.q = a->q;
+  p.k = k;
+  p.v = v;
+  p.out = a->out;
+  p.starts = a->q_starts;
+  p.table = a->page_table;
+  p.lens = a->kv_lens;
+  p.lse = a->lse;
+  p.num_pages = kv->device_num_pages;
+  p.window = a->window;
+  p.causal = a->causal != 0;
+  p.bf16 = a->dtype == HICACHE_BF16;
+  p.v_scale = a->v_scale;
+  query_place(static_cast<char *>(a->workspace), a->workspace, &p);
+  int n = 0, device = 0;
+  const cudaError_t de = cudaGetDevice(&device);
+  if (de != cudaSuccess) return cuda_error(de, "cudaGetDevice");
+  const int e = hicache::launch_query(p, device, stream, &n);
+  return launched(e, n, "query kernel launch");
+}
+
+int hicache_prefix_workspace(const hicache_pool_desc *desc, int32_t batch, int32_t groups, int32_t q_heads,
+                             int32_t head_dim, int32_t max_prefix_pages, int32_t max_pages, int64_t *bytes) {
+  clear_error();
+  Shape s{};
+  int rc = check_desc(desc, &s, true);
+  if (rc) return rc;
+  if (!bytes) return set_error(HICACHE_ERR_INVALID_ARG, "bytes is NULL");
+  hicache::QueryParams q{};
+  hicache::DecodeParams d{};
+  if ((rc = query_sizes(s, groups, batch, q_heads, head_dim, max_prefix_pages, &q))) return rc;
+  if ((rc = decode_sizes(s, batch, q_heads, head_dim, head_dim, max_pages, &d))) return rc;
+  *bytes = prefix_space(d).bytes;
+  return HICACHE_OK;
+}
+
+int hicache_prefix_attention(const hicache_device_kv *kv, const hicache_pool_desc *desc, int32_t layer_id,
+                             const hicache_prefix_desc *a, void *stream) {
+  clear_error();
+  Shape s{};
+  void *k = nullptr, *v = nullptr;
+  int rc = check_pages(kv, desc, layer_id, &s, &k, &v);
+  if (rc) return rc;
+  if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the prefix descriptor is NULL");
+  if ((rc = check_query_dtype(a->dtype, a->reserved, s, a->k_scale, a->v_scale))) return rc;
+  hicache::QueryParams q{};
+  hicache::DecodeParams d{};
+  if ((rc = query_sizes(s, a->groups, a->batch, a->q_heads, a->head_dim, a->max_prefix_pages, &q))) return rc;
+  if ((rc = decode_sizes(s, a->batch, a->q_heads, a->head_dim, a->head_dim, a->max_pages, &d))) return rc;
+  if ((rc = check_scale(a->scale, a->k_scale, &q.scale2))) return rc;
+  if (a->batch == 0) return HICACHE_OK;
+  q.q_st = d.q_sb = used(a->q_batch_stride, a->batch);
+  q.q_sh = d.q_sh = used(a->q_head_stride, a->q_heads);
+  d.o_sb = used(a->out_batch_stride, a->batch);
+  d.o_sh = used(a->out_head_stride, a->q_heads);
+  q.t_sb = used(a->prefix_stride, a->groups);
+  d.t_sb = used(a->table_stride, a->batch);
+  d.lse_sb = used(a->lse_stride, a->batch);
+  if ((rc = check_heads("q", a->q, d.q_sb, d.q_sh))) return rc;
+  if ((rc = check_heads("out", a->out, d.o_sb, d.o_sh))) return rc;
+  if (!rows_disjoint(a->batch, d.o_sb, a->q_heads, d.o_sh, a->head_dim))
+    return set_error(HICACHE_ERR_INVALID_ARG, "out: heads overlap one another");
+  if ((rc = check_ints({a->page_table, a->seq_lens}, "page_table or seq_lens"))) return rc;
+  if (a->groups > 0 &&
+      (rc = check_ints({a->group_starts, a->prefix_table, a->prefix_lens}, "group_starts, prefix_table or prefix_lens")))
+    return rc;
+  if (!stride_ok(q.t_sb) || !stride_ok(d.t_sb))
+    return set_error(HICACHE_ERR_INVALID_ARG, "prefix_stride and table_stride must be in [0, 2^40)");
+  if ((rc = check_lse(a->lse, d.lse_sb, a->batch, a->q_heads))) return rc;
+  const PrefixSpace sp = prefix_space(d);
+  if ((rc = check_workspace(a->workspace, a->workspace_bytes, sp.bytes))) return rc;
+  char *const ws = static_cast<char *>(a->workspace);
+  q.q = d.q = a->q;
+  q.k = d.k = k;
+  q.v = d.v = v;
+  q.num_pages = d.num_pages = kv->device_num_pages;
+  q.bf16 = d.bf16 = a->dtype == HICACHE_BF16;
+  q.v_scale = d.v_scale = a->v_scale;
+  q.starts = a->group_starts;
+  q.table = a->prefix_table;
+  q.lens = a->prefix_lens;
+  q.out32 = reinterpret_cast<float *>(ws + sp.prior);
+  q.lse2 = reinterpret_cast<float *>(ws + sp.prior_lse2);
+  query_place(ws + sp.query, ws, &q);
+  d.out = a->out;
+  d.table = a->page_table;
+  d.lens = a->seq_lens;
+  d.lse = a->lse;
+  d.scale2 = q.scale2;
+  d.decay = 1.f;
+  d.fd_page = q.fd_page;
+  decode_place(ws, hicache::decode_space(d, false), &d);
+  int n = 0, device = 0;
+  const cudaError_t de = cudaGetDevice(&device);
+  if (de != cudaSuccess) return cuda_error(de, "cudaGetDevice");
+  int e = 0;
+  if (a->groups > 0) {
+    d.prior = q.out32;
+    d.prior_lse2 = q.lse2;
+    e = hicache::launch_query(q, device, stream, &n);
+  }
+  if (!e) e = hicache::launch_decode(d, device, stream, &n);
+  return launched(e, n, "prefix kernel launch");
+}
+
+int hicache_merge_attention(const hicache_merge_desc *a, void *stream) {
+  clear_error();
+  if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the merge descriptor is NULL");
+  if (a->dtype != HICACHE_BF16 && a->dtype != HICACHE_FP16)
+    return set_error(HICACHE_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
+  if (a->parts < 1 || a->parts > hicache::kMergeParts)
+    return set_error(HICACHE_ERR_INVALID_ARG, "parts = %d must be in [1, %d]", a->parts, hicache::kMergeParts);
+  if (a->heads < 1 || a->head_dim < 8 || a->head_dim % 8 || a->head_dim > (1 << 20))
+    return set_error(HICACHE_ERR_INVALID_ARG, "heads %d must be >= 1, head_dim %d a multiple of 8 in [8, 2^20]", a->heads,
+                     a->head_dim);
+  const int64_t vecs = a->head_dim / 8;
+  if (a->num_tokens < 0 || a->num_tokens > ((int64_t(1) << 31) - 4096) / (a->heads * vecs))
+    return set_error(HICACHE_ERR_INVALID_ARG, "num_tokens * heads * head_dim / 8 must be in [0, 2^31 - 4096]");
+  if (a->num_tokens == 0) return HICACHE_OK;
+  hicache::MergeParams p{};
+  int rc;
+  p.out_st = used(a->out_token_stride, a->num_tokens);
+  p.out_sh = used(a->out_head_stride, a->heads);
+  p.lse_st = used(a->lse_stride, a->num_tokens);
+  if ((rc = check_heads("out", a->out, p.out_st, p.out_sh))) return rc;
+  if (!rows_disjoint(a->num_tokens, p.out_st, a->heads, p.out_sh, a->head_dim))
+    return set_error(HICACHE_ERR_INVALID_ARG, "out: heads overlap one another");
+  if ((rc = check_lse(a->lse, p.lse_st, a->num_tokens, a->heads))) return rc;
+  for (int i = 0; i < a->parts; ++i) {
+    p.o_st[i] = used(a->part_token_strides[i], a->num_tokens);
+    p.o_sh[i] = used(a->part_head_strides[i], a->heads);
+    p.l_st[i] = used(a->part_lse_strides[i], a->num_tokens);
+    if ((rc = check_heads("a part", a->part_outs[i], p.o_st[i], p.o_sh[i]))) return rc;
+    if ((rc = check_ints({a->part_lses[i]}, "a part's lse"))) return rc;
+    if (!stride_ok(p.l_st[i])) return set_error(HICACHE_ERR_INVALID_ARG, "a part's lse stride must be in [0, 2^40)");
+    if (a->part_outs[i] == a->out && (p.o_st[i] != p.out_st || p.o_sh[i] != p.out_sh))
+      return set_error(HICACHE_ERR_INVALID_ARG, "out is a part with other strides");
+    if (a->part_lses[i] == a->lse) return set_error(HICACHE_ERR_INVALID_ARG, "lse is a part's");
+    p.outs[i] = a->part_outs[i];
+    p.lses[i] = a->part_lses[i];
+  }
+  p.out = a->out;
+  p.lse = a->lse;
+  p.rows = a->num_tokens * a->heads;
+  p.parts = a->parts;
+  p.heads = a->heads;
+  p.D = a->head_dim;
+  p.bf16 = a->dtype == HICACHE_BF16;
+  p.fd_heads = hicache::make_fastdiv(uint32_t(a->heads));
+  p.fd_vecs = hicache::make_fastdiv(uint32_t(vecs));
+  const int e = hicache::launch_merge(p, stream);
+  return launched(e, e == 0, "merge kernel launch");
 }
 
 int hicache_evict_pages(const hicache_evict_desc *a, void *stream) {

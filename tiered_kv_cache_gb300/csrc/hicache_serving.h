@@ -1,6 +1,7 @@
 // hicache_serving.h -- kernel parameters shared by the operators on the device
-// pages (hicache_append.cu, hicache_decode.cu, hicache_evict.cu) and their
-// argument checks (hicache_serving.cpp).  Not part of the public ABI.
+// pages (hicache_append.cu, hicache_decode.cu, hicache_query.cu, hicache_merge.cu,
+// hicache_evict.cu) and their argument checks (hicache_serving.cpp).  Not part of
+// the public ABI.
 #pragma once
 
 #include <cstddef>
@@ -52,6 +53,9 @@ struct DecodeParams {
   FastDiv fd_page;            // tokens per page
   float scale2;               // scale * k_scale * log2(e)
   float v_scale, decay;
+  // K/V: what the rows attended to before these tokens, or null: [batch, q_heads, D] and
+  // its base-2 logarithm [batch, q_heads].  The results cover both.
+  const float *prior, *prior_lse2;
 };
 // Query heads of a unit of work (the rows of a product), and the CTAs of a
 // launch: one on each of a GB300's 152 SMs.
@@ -84,6 +88,88 @@ HC_HD bool pieces_to_join(int32_t first, int32_t count, int32_t QB) {
 
 // Whether a page table's entry is a page of the cache (else it counts as absent).
 HC_HD bool page_present(int32_t page, int64_t num_pages) { return page >= 0 && page < num_pages; }
+
+// ---- many queries: hicache_query_attention, hicache_prefix_attention ----------------
+
+struct QueryParams {
+  const void *q, *k, *v;      // k, v: the layer's buffers
+  void *out;
+  const int32_t *starts, *table, *lens;
+  float *lse;                 // natural logarithm, or null
+  // a prefix's part of a call, instead of out and lse: [tokens, Hq, D] and [tokens, Hq]
+  float *out32, *lse2;
+  int64_t q_st, q_sh, o_st, o_sh, t_sb, lse_st;
+  int64_t row;                // elements of a cache row
+  int64_t num_pages;          // device pages
+  // workspace
+  unsigned int *error;        // set by a call that gave up waiting
+  int4 *open;                 // per chunk of work: the unit that begins in it and goes on, and in how many chunks it lies
+  float *parts;               // two per chunk
+  int32_t B, N, Hq, Hkv, G, D, P, max_pages, window, causal;
+  int32_t bf16, e4m3;
+  FastDiv fd_page, fd_group;  // tokens per page, query heads per kv head
+  float scale2;               // scale * k_scale * log2(e)
+  float v_scale;
+};
+// The rows of a product (query tokens times their heads of one kv head), products
+// that share a tile of the cache, and tokens of that tile.
+constexpr int kQueryRows = 128;
+HC_HD int query_tiles(int D) { return D <= 128 ? 2 : 1; }
+HC_HD int query_block(int D) { return D <= 128 ? 128 : 64; }
+HC_HD int query_cols(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+constexpr int kQueryCtas = 152;                   // one on each of a GB300's SMs
+constexpr int kQueryPhases = 8;                   // chunks of work for each of them, at most
+struct QuerySpace {
+  int64_t open, parts, bytes;
+};
+QuerySpace query_space(int D, int phases);
+int launch_query(const QueryParams &p, int device, void *stream, int *launches);
+
+// A unit of work: rows [row0, row0 + rows) of a sequence's nq * G query rows, over
+// blocks [blk0, blk0 + blocks) of the tokens.  Causal: query i of nq sees the tokens up
+// to kv - nq + i, the last `window` of them if window > 0.
+struct QueryUnit {
+  int32_t row0, rows, blk0, blocks;
+};
+HC_HD int32_t query_units(int32_t nq, int32_t G, int32_t unit_rows) { return (nq * G + unit_rows - 1) / unit_rows; }
+// The tokens [lo, hi) that query i sees.
+HC_HD void query_sees(int32_t i, int32_t nq, int32_t kv, int32_t causal, int32_t window, int32_t *lo, int32_t *hi) {
+  const int32_t end = causal ? kv - nq + i + 1 : kv;
+  *hi = end < 0 ? 0 : end;
+  *lo = window > 0 && end > window ? end - window : 0;
+}
+HC_HD QueryUnit query_unit(int32_t m, int32_t nq, int32_t kv, const FastDiv &group, int32_t unit_rows, int32_t block,
+                           int32_t causal, int32_t window) {
+  QueryUnit u;
+  const int32_t all = nq * int32_t(group.d);
+  u.row0 = m * unit_rows;
+  u.rows = all - u.row0 < unit_rows ? all - u.row0 : unit_rows;
+  int32_t lo, hi, unused;
+  query_sees(int32_t(fast_div(uint32_t(u.row0), group)), nq, kv, causal, window, &lo, &unused);
+  query_sees(int32_t(fast_div(uint32_t(u.row0 + u.rows - 1), group)), nq, kv, causal, window, &unused, &hi);
+  u.blk0 = lo / block;
+  u.blocks = hi > lo ? (hi + block - 1) / block - u.blk0 : 0;
+  return u;
+}
+// Whether a record of the workspace is a unit of this call to join: its pieces lie in
+// chunks of it.
+HC_HD bool query_open(int32_t chunk, int32_t pieces, int32_t chunks) {
+  return pieces >= 2 && chunk >= 0 && chunk < chunks && pieces <= chunks - chunk;
+}
+
+constexpr int kMergeParts = 8;
+struct MergeParams {
+  const void *outs[kMergeParts];
+  const float *lses[kMergeParts];
+  int64_t o_st[kMergeParts], o_sh[kMergeParts], l_st[kMergeParts];
+  void *out;
+  float *lse;
+  int64_t out_st, out_sh, lse_st;
+  int64_t rows;               // tokens times heads
+  int32_t parts, heads, D, bf16;
+  FastDiv fd_heads, fd_vecs;
+};
+int launch_merge(const MergeParams &p, void *stream);
 
 struct EvictParams {
   const int32_t *table;
