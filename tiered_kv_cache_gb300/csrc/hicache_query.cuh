@@ -34,6 +34,8 @@
 // error word and returns.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -63,7 +65,7 @@ struct QueryConfig {
   static constexpr int SOFT_WARPS = 4 * QT, COPY_WARP = SOFT_WARPS, MMA_WARP = COPY_WARP + 4;
   static constexpr int WARPS = MMA_WARP + 4, THREADS = WARPS * 32;
   // registers of a thread of each group of four warps: what the launch has, dealt anew
-  static constexpr int SOFT_REGS = QT == 2 ? 200 : 240, COPY_REGS = QT == 2 ? 72 : 168, MMA_REGS = QT == 2 ? 40 : 96;
+  static constexpr int SOFT_REGS = QT == 2 ? 192 : 240, COPY_REGS = QT == 2 ? 72 : 168, MMA_REGS = QT == 2 ? 56 : 96;
   static_assert(4 * QT * SOFT_REGS + 4 * COPY_REGS + 4 * MMA_REGS <= WARPS * (65536 / THREADS / 8 * 8), "registers");
   static constexpr int O_COL = 2 * BN;            // tensor memory: two score buffers, then O of each tile
   static constexpr int PIECE = ROWS * DP_ + 2 * ROWS;   // floats: O [tile][element][row], m, l
@@ -71,12 +73,34 @@ struct QueryConfig {
   static_assert(O_COL + QT * DP_ <= 512, "tensor memory");
 };
 
-// d += a b, a in tensor memory
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// d += a b in one lane of a warp that runs as one: predicated, since behind a branch the
+// compiler no longer knows that the operands are the same in all lanes, and takes each
+// from vector registers (an issue then cost 75 clocks)
+__device__ __forceinline__ void tc_mma_in(uint32_t lane, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{.reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a),
-      "l"(b), "r"(idesc), "r"(uint32_t(add))
+      "{.reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lane)
       : "memory");
+}
+// the same with a in tensor memory
+__device__ __forceinline__ void tc_mma_ta(uint32_t lane, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lane)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_in(uint32_t lane, uint32_t bar) {
+  asm volatile(
+      "{.reg .pred q; setp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];}" ::"r"(bar), "r"(lane)
+      : "memory");
+}
+// what is the same in all lanes, in a register that the compiler knows to be
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t r;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p;}" : "=r"(r));
+  return r;
 }
 __device__ __forceinline__ void tc_ld32(uint32_t addr, float *v) {
   asm volatile(
@@ -110,6 +134,28 @@ __device__ __forceinline__ void tc_st16u(uint32_t addr, const uint32_t *r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// two floats at a time
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t x, float *v) { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <int REGS, bool MORE>
 __device__ __forceinline__ void set_registers() {
   if constexpr (MORE)
@@ -125,6 +171,22 @@ __device__ __forceinline__ uint32_t q_e4m3(uint32_t two) {   // two e4m3 in the 
 __device__ __forceinline__ float2 q_unpack2(uint32_t u, bool bf16) {
   return bf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u))
               : __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// The layer's buffers as TMA sees them, rows of elements of 2 bytes in boxes of 64 elements
+// (128 bytes) by `box` rows; box 0: not at all.
+struct QueryMaps {
+  CUtensorMap k, v;
+  int32_t box;
+};
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {   // and arrives
+  asm volatile("{.reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;}" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // A sequence's queries and tokens; starts that do not ascend, or leave the rows there
@@ -273,14 +335,14 @@ __device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRo
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_constant__ QueryParams p) {
+__global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_constant__ QueryParams p, const __grid_constant__ QueryMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = 8;
+  constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = 8, PARTS = BN / 64;
   __shared__ long long scratch[C::WARPS];
   __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
   __shared__ int first_seq;
-  __shared__ __align__(8) unsigned long long bars[2 * C::STAGES + INFO + 12];
-  __shared__ int64_t offs[2][BN];                 // where a block's tokens lie, in bytes; -1: absent
+  __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 19];
+  __shared__ int64_t offs[2][BN];                 // the rows a block's tokens lie in; -1: absent
   __shared__ uint32_t there[INFO][WORDS];         // which of them are present
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
@@ -290,14 +352,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   unsigned char *const q_p = smem_raw, *const ring_p = smem_raw + C::QT * C::QTILE_B;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
-  // a stage is full, empty; what of a block is present; Q of a tile is there; scores,
+  // a stage is full, its copies are visible to the products, it is empty; what of a block is present, the copying
+  // warps are together; Q of a tile is there; scores,
   // exponentials of a lane are there, their product with V is done; the last product.
   // A lane is a score buffer with the warps that take it: 0 and 1 the two tiles of a unit,
   // 0 and 2 the buffers that one tile fills in turn.  The second tile's warps sit units of one
   // tile out, so no barrier that they wait on may count there: a phase's parity would pass
   // for that of a phase two on.
-  constexpr int FULL = 0, EMPTY = C::STAGES, KNOWN = 2 * C::STAGES, QFULL = KNOWN + INFO, SFULL = QFULL + 2,
-                PFULL = SFULL + 3, PVDONE = PFULL + 3, LAST = PVDONE + 3;
+  constexpr int FULL = 0, EMPTY = C::STAGES, READY = 2 * C::STAGES, KNOWN = 3 * C::STAGES, QFULL = KNOWN + INFO, SFULL = QFULL + 2,
+                PFULL = SFULL + 3, PVDONE = PFULL + 6, LAST = PVDONE + 6, GROUP = LAST + 1;   // PFULL, PVDONE: + 3 for a block's second half
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
@@ -341,15 +404,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(bar(FULL + i), 128);
       mbar_init(bar(EMPTY + i), 1);
+      mbar_init(bar(READY + i), 1);
     }
     for (int i = 0; i < INFO; ++i) mbar_init(bar(KNOWN + i), 4);
     for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), 128);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(SFULL + i), 1);
-      mbar_init(bar(PFULL + i), 128);
-      mbar_init(bar(PVDONE + i), 1);
+      for (int part = 0; part < 6; part += 3) {
+        mbar_init(bar(PFULL + part + i), 4);
+        mbar_init(bar(PVDONE + part + i), 1);
+      }
     }
     mbar_init(bar(LAST), 1);
+    mbar_init(bar(GROUP), 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     p.open[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -388,9 +455,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+  const uint32_t tmem = uniform(tmem_base);
 
   const int d16 = (p.D + 15) & ~15;
+  // rows that cp.async brings tile after tile: a warp makes them visible to the products
+  const bool relayed = C::TYPE != kQE4m3 && maps.box == 0;
   auto begin = [&](QueryPieces<C> &pc) {
     pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
   };
@@ -407,66 +476,121 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       const uint32_t o_desc = instr_desc(C::BF16, kQueryRows, d16, false, true);
       const int ksteps = d16 / 16;
       int kst = 0, kph = 0, vst = 1, vph = 0;     // stage and phase of the next block's K, V
-      uint32_t used[3] = {0, 0, 0}, duals = 0, pieces = 0;
+      uint32_t used0 = 0, used1 = 0, used2 = 0, duals = 0, pieces = 0;
       bool ok = true;
+      const uint32_t one = elected();             // all products and commits are this lane's
       auto wait = [&](int b, uint32_t parity) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, &gave_up));
       };
-      while (ok && pc.next(p)) {
-        const bool dual = pc.dual();
-        const int steps = (pc.x1 - pc.x0) << int(dual);
+      while (ok && __all_sync(0xffffffffu, pc.next(p))) {
+        const bool dual = __all_sync(0xffffffffu, pc.dual());
+        const int steps = int(__reduce_max_sync(0xffffffffu, uint32_t(pc.x1 - pc.x0))) << int(dual);
         wait(QFULL, pieces++);
         if (ok && dual) wait(QFULL + 1, duals++);
-        auto qk = [&](int s) {
-          const int x = s & 1, tile = dual ? x : 0, way = dual ? x : 2 * x;
-          if (!dual || x == 0) wait(FULL + kst, uint32_t(kph));
-          if (!ok) return;
-          proxy_fence();
-          tc_fence_after();
-          const uint32_t a = __shfl_sync(0xffffffffu, q_s + tile * C::QTILE_B, 0);
-          const uint32_t k = __shfl_sync(0xffffffffu, ring_s + kst * C::TILE_B, 0);
-          const bool release = !dual || x == 1;
-          if (elect_one()) {
-            for (int i = 0; i < ksteps; ++i)
-              tc_mma(tmem + x * BN, smem_desc(a + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
-                     smem_desc(k + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
-            if (release) tc_commit(bar(EMPTY + kst));
-            tc_commit(bar(SFULL + way));
-          }
-          __syncwarp();
-          if (release && (kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
-        };
-        auto pv = [&](int s) {
-          const int x = s & 1, tile = dual ? x : 0, way = dual ? x : 2 * x;
-          wait(PFULL + way, used[way] + (s >> 1));
-          if (ok && (!dual || x == 0)) wait(FULL + vst, uint32_t(vph));
-          if (!ok) return;
-          proxy_fence();
-          tc_fence_after();
-          const uint32_t v = __shfl_sync(0xffffffffu, ring_s + vst * C::TILE_B, 0);
-          const bool release = !dual || x == 1, add = s >= (dual ? 2 : 1);
-          if (elect_one()) {
+        // The next block's K, the next V to come: waited for ahead of the exponentials where
+        // two tiles share them, so that PV(s) and QK(s + 2) follow one another without a pause.
+        auto arrived = [&](int stage, int parity) { wait((relayed ? READY : FULL) + stage, uint32_t(parity)); };
+        // x: the score buffer
+        auto qk = [&](int x, bool both) {
+          const int way = both ? x : 2 * x;
+          const uint32_t a = q_s + (both ? x : 0) * C::QTILE_B, at = tmem + x * BN;
+          const uint32_t k = uniform(ring_s + kst * C::TILE_B);
+          auto product = [&](int i) {
+            tc_mma_in(one, at, smem_desc(a + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
+                      smem_desc(k + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
+          };
+          if (ksteps == C::DP / 16) {
 #pragma unroll
-            for (int i = 0; i < BN / 16; ++i)
-              tc_mma_ta(tmem + C::O_COL + tile * C::DP, tmem + x * BN + i * 8, smem_desc(v + i * 2048, C::ATOM_B, 1024),
-                        o_desc, add || i > 0);
-            if (release) tc_commit(bar(EMPTY + vst));
-            tc_commit(bar(PVDONE + way));
+            for (int i = 0; i < C::DP / 16; ++i) product(i);
+          } else {
+            for (int i = 0; i < ksteps; ++i) product(i);
           }
-          __syncwarp();
-          if (release && (vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
+          tc_commit_in(one, bar(SFULL + way));
+          if (!both || x == 1) {
+            tc_commit_in(one, bar(EMPTY + kst));
+            if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
+          }
         };
-        qk(0);
-        if (ok && steps > 1) qk(1);
-        for (int s = 0; ok && s < steps; ++s) {
-          pv(s);
-          if (ok && s + 2 < steps) qk(s + 2);
+        auto pv = [&](int x, bool both, int s) {
+          const int way = both ? x : 2 * x;
+          const uint32_t at = tmem + C::O_COL + (both ? x : 0) * C::DP, pa = tmem + x * BN;
+          const uint32_t v = uniform(ring_s + vst * C::TILE_B);
+          const uint32_t add = uniform(uint32_t(s >= (both ? 2 : 1)));
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            wait(PFULL + 3 * part + way, (way == 0 ? used0 : way == 1 ? used1 : used2) + (s >> 1));
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 4 * part; i < 4 * part + 4; ++i)
+              tc_mma_ta(one, at, pa + i * 8, smem_desc(v + i * 2048, C::ATOM_B, 1024), o_desc, i > 0 ? 1u : add);
+            tc_commit_in(one, bar(PVDONE + 3 * part + way));
+          }
+          if (!both || x == 1) {
+            tc_commit_in(one, bar(EMPTY + vst));
+            if ((vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
+          }
+        };
+        arrived(kst, kph);
+        if (!ok) break;
+        tc_fence_after();
+        if (dual) {
+          qk(0, true);
+          qk(1, true);
+          for (int s = 0; s < steps; s += 2) {
+            const bool more = s + 2 < steps;
+            arrived(vst, vph);
+            if (ok && more) arrived(kst, kph);
+            if (ok) pv(0, true, s);
+            if (!ok) break;
+            if (more) qk(0, true);
+            pv(1, true, s + 1);
+            if (!ok) break;
+            if (more) qk(1, true);
+          }
+          used0 += uint32_t(steps) >> 1;
+          used1 += uint32_t(steps) >> 1;
+        } else {
+          qk(0, false);
+          if (steps > 1) {
+            arrived(kst, kph);
+            if (!ok) break;
+            qk(1, false);
+          }
+          auto step = [&](int x, int s) {
+            arrived(vst, vph);
+            if (ok) pv(x, false, s);
+            if (ok && s + 2 < steps) {
+              arrived(kst, kph);
+              if (ok) qk(x, false);
+            }
+          };
+          for (int s = 0; ok && s < steps; s += 2) {
+            step(0, s);
+            if (ok && s + 1 < steps) step(1, s + 1);
+          }
+          used0 += uint32_t(steps + 1) >> 1;
+          used2 += uint32_t(steps) >> 1;
         }
-        used[0] += uint32_t(steps + 1) >> 1;
-        used[dual ? 1 : 2] += uint32_t(steps) >> 1;
       }
-      if (elect_one()) tc_commit(bar(LAST));
+      tc_commit_in(one, bar(LAST));
       __syncwarp();
+    } else if (relayed && warp == C::MMA_WARP + 1) {
+      // ---- copies that have landed are made visible to the products: the fence takes
+      // hundreds of clocks, which the warp that issues them does not have
+      QueryPieces<C> pc;
+      begin(pc);
+      int stage = 0, phase = 0;
+      bool ok = true;
+      while (ok && pc.next(p)) {
+        for (int x = 2 * pc.x0; ok && x < 2 * pc.x1; ++x) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(FULL + stage), uint32_t(phase), &gave_up));
+          if (!ok) break;
+          proxy_fence();
+          if (lane == 0) mbar_arrive(bar(READY + stage));
+          if (++stage == C::STAGES) stage = 0, phase ^= 1;
+        }
+      }
     }
   } else if (warp >= C::COPY_WARP) {
     set_registers<C::COPY_REGS, false>();
@@ -474,57 +598,118 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     QueryPieces<C> pc;
     begin(pc);
     const int pt = tid - C::COPY_WARP * 32;
+    // boxes: lane i of the first warp takes rows from box_r on, 64 elements from box_c on
+    const int columns = (p.D + 63) >> 6, box_r = lane / columns * maps.box, box_c = lane % columns * 64;
     int stage = 0, phase = 1;
     uint32_t blk = 0;
     bool ok = true;
+    auto advance = [&]() {
+      if (++stage == C::STAGES) stage = 0, phase ^= 1;
+    };
+    uint32_t turns = 0;
+    auto together = [&]() {                       // the four warps, with a limit as for every wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(GROUP));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(GROUP), turns++ & 1u, &gave_up));
+    };
     while (ok && pc.next(p)) {
-      int t = (pc.u.blk0 + pc.x0) * BN + pt, pg = 0, page = -1;
       // the tokens that some row of the unit sees
       int lo, hi, unused;
       query_sees(int(fast_div(uint32_t(pc.u.row0), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window, &lo, &unused);
       query_sees(int(fast_div(uint32_t(pc.u.row0 + pc.u.rows - 1), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window,
                  &unused, &hi);
-      auto lookup = [&]() {
+      int page = -1, pg = 0;
+      auto lookup = [&](int t) {
         page = -1;
-        if (pt < BN && t >= lo && t < hi) {
+        if (t >= lo && t < hi) {
           pg = int(fast_div(uint32_t(t), p.fd_page));
           page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
         }
       };
-      lookup();
+      // Whole boxes, present or not (one that is not lies behind the rows and reads as
+      // zeros), are the first warp's; a block in which the range of tokens cuts a box is
+      // copied row by row by all four.
+      auto boxes = [&](int x) {
+        const int t0 = (pc.u.blk0 + x) * BN;
+        return C::TYPE != kQE4m3 && maps.box > 0 && (max(lo - t0, 0) & (maps.box - 1)) == 0 &&
+               (min(hi - t0, BN) & (maps.box - 1)) == 0;
+      };
+      auto mine = [&](int x) { return (pc.u.blk0 + x) * BN + (maps.box > 0 && boxes(x) ? box_r : pt); };
+      lookup(mine(pc.x0));
       for (int x = pc.x0; ok && x < pc.x1; ++x, ++blk) {
-        const bool have = page_present(page, p.num_pages);
+        if (boxes(x)) {
+          if (pt < 32) {
+            const bool have = box_r < BN && page_present(page, p.num_pages);
+            const int y = have ? int(int64_t(page) * p.P + (mine(x) - pg * p.P)) : int(p.num_pages * p.P);
+            const uint32_t bits = __ballot_sync(0xffffffffu, have);
+            if (lane < WORDS) {                   // tokens lane * 32 on
+              const int at = lane * 32 / maps.box * columns;
+              uint32_t word = (bits >> at) & 1u ? ~0u : 0u;
+              if (maps.box == 16) word = (word & 0xffffu) | ((bits >> (at + columns)) & 1u ? 0xffff0000u : 0u);
+              there[blk % INFO][lane] = word;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(KNOWN + blk % INFO), 4);
+            if (x + 1 < pc.x1) lookup(mine(x + 1));
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
+              if (!ok) break;
+              if (lane == 0) mbar_expect(bar(FULL + stage), uint32_t(columns) * C::ATOM_B);
+              if (lane == 1) mbar_arrive(bar(FULL + stage), 127);
+              __syncwarp();
+              if (box_r < BN)
+                tma_box(ring_s + stage * C::TILE_B + (box_c >> 6) * C::ATOM_B + box_r * 128, kv ? &maps.v : &maps.k,
+                        pc.h * p.D + box_c, y, bar(FULL + stage));
+              advance();
+            }
+          } else {
+            if (x + 1 < pc.x1 && !boxes(x + 1)) lookup(mine(x + 1));
+            advance();
+            advance();
+          }
+          continue;
+        }
+        // the other three warps pass over whole boxes: they wait here for the first, whose
+        // blocks before this one still use the barriers and the words
+        if (maps.box > 0) together();
+        if (!ok) break;
+        const bool have = pt < BN && page_present(page, p.num_pages);
         int64_t *const at = offs[blk & 1u];
-        if (pt < BN)
-          at[pt] = have ? ((int64_t(page) * p.P + (t - pg * p.P)) * p.row + int64_t(pc.h) * p.D) * C::ES : -1;
+        if (pt < BN) at[pt] = have ? int64_t(page) * p.P + (mine(x) - pg * p.P) : -1;
         const uint32_t word = __ballot_sync(0xffffffffu, have);
         if (lane == 0) {
           if (pt < BN) there[blk % INFO][pt >> 5] = word;
           mbar_arrive(bar(KNOWN + blk % INFO));
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        t += BN;
-        if (x + 1 < pc.x1) lookup();
+        together();
+        if (x + 1 < pc.x1) lookup(mine(x + 1));
         for (int kv = 0; kv < 2; ++kv) {
-          ok = mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up);
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
           if (!ok) break;
-          const char *src = static_cast<const char *>(kv ? p.v : p.k);
+          const char *src = static_cast<const char *>(kv ? p.v : p.k) + int64_t(pc.h) * p.D * C::ES;
           if constexpr (C::TYPE != kQE4m3) {
             const int c = pt & 7, r0 = pt >> 3;   // 8 lanes a row of 128 bytes, 16 rows at a time
             const uint32_t dst = ring_s + stage * C::TILE_B + r0 * 128 + ((c ^ (r0 & 7)) << 4);
 #pragma unroll
             for (int i = 0; i < BN / 16; ++i) {
-              const int64_t o = at[i * 16 + r0];
+              const int64_t y = at[i * 16 + r0], o = y * p.row * 2;
 #pragma unroll
               for (int a = 0; a < C::ATOMS; ++a) {
                 const int col = a * 64 + c * 8;
                 if (col < d16) {
-                  const bool in = o >= 0 && col < p.D;
+                  const bool in = y >= 0 && col < p.D;
                   cp_async16(dst + a * C::ATOM_B + i * 2048, src + (in ? o + col * 2 : 0), in ? 16 : 0);
                 }
               }
             }
-            mbar_arrive_copies(bar(FULL + stage));
+            if (relayed) {
+              mbar_arrive_copies(bar(FULL + stage));
+            } else {                              // a block among boxes: here and visible at once
+              asm volatile("cp.async.wait_all;" ::: "memory");
+              proxy_fence();
+              mbar_arrive(bar(FULL + stage));
+            }
           } else {
             constexpr int RC = C::DP / 16, RP = 128 / RC;   // 16-byte chunks of a row, rows at a time
             const int c = pt % RC, r0 = pt / RC;
@@ -533,8 +718,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               uint4 w[BN / RP];
 #pragma unroll
               for (int i = 0; i < BN / RP; ++i) {
-                const int64_t o = at[i * RP + r0];
-                w[i] = o >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + o + c * 16)) : make_uint4(0u, 0u, 0u, 0u);
+                const int64_t y = at[i * RP + r0];
+                w[i] = y >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + y * p.row + c * 16)) : make_uint4(0u, 0u, 0u, 0u);
               }
 #pragma unroll
               for (int i = 0; i < BN / RP; ++i) {
@@ -548,11 +733,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             proxy_fence();
             mbar_arrive(bar(FULL + stage));
           }
-          if (++stage == C::STAGES) stage = 0, phase ^= 1;
+          advance();
         }
       }
     }
-    if constexpr (C::TYPE != kQE4m3) asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (C::TYPE != kQE4m3) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      // after a wait that ran out, boxes may be on their way still: the last of each stage
+      for (int i = 0; !ok && i < C::STAGES; ++i) {
+        mbar_wait<true>(bar(FULL + stage), uint32_t(phase), &gave_up);
+        advance();
+      }
+    }
   } else {
     set_registers<C::SOFT_REGS, true>();
     // ---- softmax: a thread per row
@@ -618,98 +810,131 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         mbar_arrive(bar(QFULL + tile));
       }
       const bool any = __any_sync(0xffffffffu, live);   // of a warp without rows, nothing is looked at
-      float m = -INFINITY, mu = 0.f, l0 = 0.f, l1 = 0.f;
+      float m = -INFINITY, mu = 0.f, l = 0.f;
       for (int j = 0; j < n; ++j, ++blk) {
         const int x = dual ? tile : j & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(j)), turn(j) & 1u, &gave_up));
-        if (ok && any) ok = __all_sync(0xffffffffu, mbar_wait(bar(KNOWN + blk % INFO), (blk / INFO) & 1u, &gave_up));
+        uint32_t words[WORDS];
+        bool mask = false;
+        const int t0 = (pc.u.blk0 + pc.x0 + j) * BN;
+        // (after units that these warps sat out, the copies may be many blocks behind: then the
+        // scores come first, before a word's barrier could have turned around)
+        if (j == 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(0)), turn(0) & 1u, &gave_up));
+        if (ok && any) {                          // what this row does not see
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(KNOWN + blk % INFO), (blk / INFO) & 1u, &gave_up));
+          mask = lo > t0 || hi < t0 + BN;
+#pragma unroll
+          for (int w = 0; w < WORDS; ++w) {
+            words[w] = there[blk % INFO][w];
+            mask |= words[w] != ~0u;
+          }
+          mask = __any_sync(0xffffffffu, mask);
+        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(j)), turn(j) & 1u, &gave_up));
         if (!ok) break;
         if (!any) {
-          mbar_arrive(bar(PFULL + way(j)));
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+            if (lane == 0) mbar_arrive(bar(PFULL + 3 * part + way(j)));
           continue;
         }
         tc_fence_after();
         const uint32_t s_at = tmem + x * BN + lanes;
+        // 64 tokens at a time, whose product with V starts while the next ones are taken.  The
+        // usual 64 are done in one pass, 32 at a time, the scores of the next 32 on their
+        // way: exponentials against the reference there is, the largest score beside them.
+        // Only when that turns out too large are they taken again.
         float e[BN];                              // scores less the reference, in log2
+        tc_ld32(s_at, e);
+        tc_ld32(s_at + 32, e + 32);
+        tc_loaded32(e);
+        tc_loaded32(e + 32);
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) tc_ld32(s_at + w * 32, e + w * 32);
+        for (int part = 0; part < PARTS; ++part) {
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint64_t sum[2] = {0, 0};               // two pairs of sums
+          auto exponentials = [&](int w) {        // P, rounded to the products' type; the sums keep all bits
+            uint32_t pk[16];
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) tc_loaded32(e + w * 32);
+            for (int i = 0; i < 16; ++i) {
+              const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
+              sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
+              pk[i] = pack2<C::BF16>(a, z);
+            }
+            tc_st16u(s_at + w * 16, pk);
+          };
+          const uint64_t mul2 = f32x2(mul, mul), mu2 = f32x2(-mu, -mu);
+          bool raise = false, any_raise = false;
+          float over = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < BN; ++i) e[i] = fmaf(e[i], mul, -mu);
-        // what this row does not see
-        const int t0 = (pc.u.blk0 + pc.x0 + j) * BN;
-        bool mask = lo > t0 || hi < t0 + BN;
-        uint32_t words[WORDS];
+          for (int w = 2 * part; w < 2 * part + 2; ++w) {
+            if (w + 2 < WORDS) tc_ld32(s_at + (w + 2) * 32, e + (w + 2) * 32);
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          words[w] = there[blk % INFO][w];
-          mask |= words[w] != ~0u;
-        }
-        if (__any_sync(0xffffffffu, mask)) {
+            for (int i = 0; i < 32; i += 2) {
+              float *v = e + 32 * w + i;
+              unpack(fma2(f32x2(v[0], v[1]), mul2, mu2), v);
+            }
+            if (__builtin_expect(mask, 0)) {
+              const int a = min(32, max(0, lo - t0 - 32 * w)), z = min(32, max(0, hi - t0 - 32 * w));
+              const uint32_t in = words[w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
 #pragma unroll
-          for (int w = 0; w < WORDS; ++w) {
-            const int a = min(32, max(0, lo - t0 - 32 * w)), z = min(32, max(0, hi - t0 - 32 * w));
-            const uint32_t in = words[w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
+              for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
+            }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
+            for (int i = 0; i < 32; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[32 * w + i], e[32 * w + i + 1]);
+            if (w & 1) {                          // asked here, so that the answer comes during the exponentials
+              over = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+              raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
+              any_raise = __any_sync(0xffffffffu, raise);
+            }
+            exponentials(w);                      // over scores that are here: P of word w takes half of word w / 2's place
+            if (w + 2 < WORDS) tc_loaded32(e + (w + 2) * 32);
           }
-        }
-        float over = e[0];
+          if (__builtin_expect(any_raise, 0)) {
+            float f = 1.f;
+            if (raise) {
+              const float now = fmaxf(m, over + mu - C::ABOVE), by = mu - now;
+              f = m == -INFINITY ? 0.f : exp2_fast(m - now);
+              m = mu = now;
+              l *= f;
 #pragma unroll
-        for (int i = 1; i < BN; ++i) over = fmaxf(over, e[i]);
-        const bool raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-          float f = 1.f;
-          if (raise) {
-            const float now = fmaxf(m, over + mu - C::ABOVE), by = mu - now;
-            f = m == -INFINITY ? 0.f : exp2_fast(m - now);
-            m = mu = now;
-            l0 *= f;
-            l1 *= f;
-#pragma unroll
-            for (int i = 0; i < BN; ++i) e[i] += by;
-          }
-          __syncwarp();
-          if (j > 0) {                            // O, once the product with V before this is done
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + way(j - 1)), turn(j - 1) & 1u, &gave_up));
-            if (!ok) break;
-            tc_fence_after();
+              for (int i = 64 * part; i < 64 * part + 64; ++i) e[i] += by;
+            }
+            __syncwarp();
+            sum[0] = sum[1] = 0;
+            exponentials(2 * part);
+            exponentials(2 * part + 1);
+            if (j > 0 || part > 0) {              // O, once the product with V before this is done
+              const int last = part > 0 ? j : j - 1;
+              ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 3 * PARTS - 3) + way(last)), turn(last) & 1u, &gave_up));
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < d16; c += 16) {
-              float o[16];
-              tc_ld16(o_at + c, o);
-              tc_wait_ld();
+              for (int c = 0; c < d16; c += 16) {
+                float o[16];
+                tc_ld16(o_at + c, o);
+                tc_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= f;
-              tc_st16(o_at + c, o);
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tc_st16(o_at + c, o);
+              }
             }
           }
+          float x[2];
+          unpack(add2(sum[0], sum[1]), x);
+          l += x[0] + x[1];
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(PFULL + 3 * part + way(j)));
         }
-        // P, rounded to the products' type for the tensor cores (the sums keep all bits)
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
-            l0 += a;
-            l1 += z;
-            pk[i] = pack2<C::BF16>(a, z);
-          }
-          tc_st16u(s_at + w * 16, pk);
-        }
-        tc_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(PFULL + way(j)));
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- the piece's end
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + way(n - 1)), turn(n - 1) & 1u, &gave_up));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 3 * PARTS - 3 + way(n - 1)), turn(n - 1) & 1u, &gave_up));
       if (!ok) break;
       used0 += dual ? uint32_t(n) : uint32_t(n + 1) >> 1;
       used2 += dual ? 0u : uint32_t(n) >> 1;
-      const float l = l0 + l1;
       const bool whole = pc.begins() && pc.ends();
       float *const part = p.parts + (int64_t(blockIdx.x) * 2 + (pc.begins() ? 1 : 0)) * C::PIECE;
       if (any) {
@@ -817,8 +1042,8 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   if (col == 0) query_lse(p, out, m, sum);
 }
 
-template <class P>
-int query_launch(void (*kernel)(const P), dim3 grid, unsigned threads, cudaStream_t st, const P &p, size_t smem) {
+template <class... A, class... B>
+int query_launch(void (*kernel)(A...), dim3 grid, unsigned threads, cudaStream_t st, size_t smem, const B &...args) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
@@ -829,8 +1054,45 @@ int query_launch(void (*kernel)(const P), dim3 grid, unsigned threads, cudaStrea
   c.stream = st;
   c.attrs = &at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
   return int(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+// The driver's call that describes a tensor to TMA, or null.
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_call() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 call = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r);
+    if (e != cudaSuccess || r != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return call;
+}
+
+// Describes the layer's buffers to TMA where its boxes fit: pages of whole boxes of 16 rows
+// or more (with fewer, rows copied by threads are as fast), heads that the products'
+// steps of 16 cover (what a box holds behind the head is not used), rows within a
+// coordinate.  Else, or where the driver will not, the copies go row by row.
+inline void query_maps(const QueryParams &p, int block, QueryMaps *m) {
+  m->box = 0;
+  int box = 1;
+  while (box < 64 && p.P % (2 * box) == 0) box *= 2;
+  const int64_t rows = p.num_pages * p.P;
+  const PFN_cuTensorMapEncodeTiled_v12000 call = tensor_map_call();
+  if (!call || box < 16 || p.D % 16 || rows >= INT32_MAX) return;
+  const cuuint64_t dims[2] = {cuuint64_t(p.row), cuuint64_t(rows)}, strides[1] = {cuuint64_t(p.row) * 2};
+  const cuuint32_t sizes[2] = {64, cuuint32_t(box < block ? box : block)}, steps[2] = {1, 1};
+  const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  for (int i = 0; i < 2; ++i)
+    if (call(i ? &m->v : &m->k, type, 2, const_cast<void *>(i ? p.v : p.k), dims, strides, sizes, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return;
+  m->box = int(sizes[1]);
 }
 
 constexpr int kQueryDevices = 64;
@@ -844,10 +1106,12 @@ int launch_query_as(const QueryParams &p, int device, cudaStream_t st, int *laun
     if (e != cudaSuccess) return int(e);
     if (device < kQueryDevices) ready[device].store(true, std::memory_order_release);
   }
-  int e = query_launch(query_kernel<C>, dim3(kQueryCtas), C::THREADS, st, p, C::SMEM);
+  QueryMaps maps{};
+  if (C::TYPE != kQE4m3) query_maps(p, C::BN, &maps);
+  int e = query_launch(query_kernel<C>, dim3(kQueryCtas), C::THREADS, st, C::SMEM, p, maps);
   if (e) return e;
   ++*launches;
-  e = query_launch(query_join_kernel<C::DP, C::QT>, dim3(kQueryCtas, C::DP / 8, C::QT), kQueryRows, st, p, 0);
+  e = query_launch(query_join_kernel<C::DP, C::QT>, dim3(kQueryCtas, C::DP / 8, C::QT), kQueryRows, st, 0, p);
   *launches += e == 0;
   return e;
 }
