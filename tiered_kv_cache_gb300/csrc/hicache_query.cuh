@@ -146,6 +146,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -299,16 +304,25 @@ struct QueryPieces {
   }
 };
 
+// A piece as the roles see it; n == 0: there is none any more.
+struct alignas(16) QueryPiece {
+  int32_t b, h, n, t0;             // sequence, kv head, blocks, the first one's first token
+  int32_t row0, rows, q0, nq;      // rows of the unit; the sequence's first query and their number
+  int32_t kv, lo, hi, flags;       // tokens of the sequence; those [lo, hi) that some row of the unit sees
+};
+enum : int { kTwoTiles = 1, kBegins = 2, kWhole = 4 };
+constexpr int kPieceRing = 4;
+
 // The output's row of row r of a unit: the query token and head.
 struct QueryRow {
   int64_t token;
   int head;
   int i;                           // query of the sequence
 };
-__device__ __forceinline__ QueryRow query_row(const QueryParams &p, const QuerySeq &s, int h, int r) {
+__device__ __forceinline__ QueryRow query_row(const QueryParams &p, int q0, int h, int r) {
   QueryRow x;
   x.i = int(fast_div(uint32_t(r), p.fd_group));
-  x.token = int64_t(s.q0) + x.i;
+  x.token = int64_t(q0) + x.i;
   x.head = h * p.G + (r - x.i * p.G);
   return x;
 }
@@ -316,6 +330,13 @@ __device__ __forceinline__ void query_lse(const QueryParams &p, const QueryRow &
   const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
   if (p.lse2) p.lse2[x.token * p.Hq + x.head] = lse2;
   if (p.lse) p.lse[x.token * p.lse_st + x.head] = lse2 * kLn2;
+}
+// the call's type is the cache's, but for e4m3
+template <class C>
+__device__ __forceinline__ uint4 query_pack8(const QueryParams &p, const float *v) {
+  if (C::TYPE == kQE4m3 ? p.bf16 : C::BF16)
+    return make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]), pack2<true>(v[6], v[7]));
+  return make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
 }
 // 8 elements of a row from a multiple of 8 on
 __device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRow &x, int col, const float *v) {
@@ -326,12 +347,7 @@ __device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRo
     return;
   }
   char *at = static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh + col);
-  uint4 w;
-  if (p.bf16)
-    w = make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]), pack2<true>(v[6], v[7]));
-  else
-    w = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-  *reinterpret_cast<uint4 *>(at) = w;
+  *reinterpret_cast<uint4 *>(at) = p.bf16 ? query_pack8<QueryConfig<64, kQBf16>>(p, v) : query_pack8<QueryConfig<64, kQFp16>>(p, v);
 }
 
 template <class C>
@@ -341,9 +357,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   __shared__ long long scratch[C::WARPS];
   __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
   __shared__ int first_seq;
-  __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 19];
+  __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 19 + 2 * kPieceRing];
   __shared__ int64_t offs[2][BN];                 // the rows a block's tokens lie in; -1: absent
   __shared__ uint32_t there[INFO][WORDS];         // which of them are present
+  __shared__ QueryPiece ring_of_pieces[kPieceRing];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
 
@@ -352,15 +369,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   unsigned char *const q_p = smem_raw, *const ring_p = smem_raw + C::QT * C::QTILE_B;
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8u * uint32_t(i); };
-  // a stage is full, its copies are visible to the products, it is empty; what of a block is present, the copying
-  // warps are together; Q of a tile is there; scores,
-  // exponentials of a lane are there, their product with V is done; the last product.
+  // A stage is full, its copies are visible to the products, it is empty; what of a block
+  // is present; Q of a tile is there; a lane's scores, exponentials are there, their product with V
+  // is done; the last product; the copying warps are together; a piece is there, is read.
   // A lane is a score buffer with the warps that take it: 0 and 1 the two tiles of a unit,
   // 0 and 2 the buffers that one tile fills in turn.  The second tile's warps sit units of one
   // tile out, so no barrier that they wait on may count there: a phase's parity would pass
   // for that of a phase two on.
-  constexpr int FULL = 0, EMPTY = C::STAGES, READY = 2 * C::STAGES, KNOWN = 3 * C::STAGES, QFULL = KNOWN + INFO, SFULL = QFULL + 2,
-                PFULL = SFULL + 3, PVDONE = PFULL + 6, LAST = PVDONE + 6, GROUP = LAST + 1;   // PFULL, PVDONE: + 3 for a block's second half
+  constexpr int FULL = 0, EMPTY = C::STAGES, READY = 2 * C::STAGES, KNOWN = 3 * C::STAGES, QFULL = KNOWN + INFO,
+                SFULL = QFULL + 2, PFULL = SFULL + 3, PVDONE = PFULL + 6, LAST = PVDONE + 6, GROUP = LAST + 1,
+                PIECE = GROUP + 1, TAKEN = PIECE + kPieceRing;   // PFULL, PVDONE: + 3 for a block's second half
+  // rows that cp.async brings tile after tile: a warp makes them visible to the products
+  const bool relayed = C::TYPE != kQE4m3 && maps.box == 0;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
@@ -407,7 +427,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       mbar_init(bar(READY + i), 1);
     }
     for (int i = 0; i < INFO; ++i) mbar_init(bar(KNOWN + i), 4);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), 128);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(SFULL + i), 1);
       for (int part = 0; part < 6; part += 3) {
@@ -417,6 +437,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     }
     mbar_init(bar(LAST), 1);
     mbar_init(bar(GROUP), 4);
+    for (int i = 0; i < kPieceRing; ++i) {
+      mbar_init(bar(PIECE + i), 1);
+      mbar_init(bar(TAKEN + i), C::SOFT_WARPS + 5 + int(relayed));
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     p.open[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -427,7 +451,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     int rows = s.nq * p.G;
     if (s.kv > 0) rows = p.causal ? max(0, min(s.nq, s.nq - s.kv)) * p.G / C::ROWS * C::ROWS : 0;
     for (int64_t i = tid; i < int64_t(rows) * p.Hkv; i += THREADS) {
-      const QueryRow x = query_row(p, s, int(i / rows), int(i % rows));
+      const QueryRow x = query_row(p, s.q0, int(i / rows), int(i % rows));
       const float zero[8] = {};
       for (int c = 0; c < p.D; c += 8) query_store8(p, x, c, zero);
       query_lse(p, x, 0.f, 0.f);
@@ -458,10 +482,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   const uint32_t tmem = uniform(tmem_base);
 
   const int d16 = (p.D + 15) & ~15;
-  // rows that cp.async brings tile after tile: a warp makes them visible to the products
-  const bool relayed = C::TYPE != kQE4m3 && maps.box == 0;
-  auto begin = [&](QueryPieces<C> &pc) {
-    pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+  // The next piece, in order: every warp but the planner's takes each of them.
+  uint32_t taken = 0;
+  bool ok = true;
+  auto take = [&](QueryPiece &x) {
+    const uint32_t i = taken % kPieceRing;
+    ok = __all_sync(0xffffffffu, mbar_wait(bar(PIECE + i), (taken / kPieceRing) & 1u, &gave_up));
+    if (!ok) return false;
+    x = ring_of_pieces[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(TAKEN + i));
+    ++taken;
+    return __any_sync(0xffffffffu, x.n > 0) != 0;
   };
 
   if (warp >= C::MMA_WARP) {
@@ -470,158 +502,164 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       // ---- the products: the warp runs as one, one elected lane issues.  In the order
       // QK(0) QK(1) PV(0) QK(2) PV(1) QK(3) ...: products of one CTA run in order, so
       // QK(s + 2) may overwrite the buffer that PV(s) reads.
-      QueryPieces<C> pc;
-      begin(pc);
       const uint32_t s_desc = instr_desc(C::BF16, kQueryRows, BN, false, false);
       const uint32_t o_desc = instr_desc(C::BF16, kQueryRows, d16, false, true);
       const int ksteps = d16 / 16;
+      const uint32_t one = elected();             // all products and commits are this lane's
       int kst = 0, kph = 0, vst = 1, vph = 0;     // stage and phase of the next block's K, V
       uint32_t used0 = 0, used1 = 0, used2 = 0, duals = 0, pieces = 0;
-      bool ok = true;
-      const uint32_t one = elected();             // all products and commits are this lane's
       auto wait = [&](int b, uint32_t parity) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, &gave_up));
       };
-      while (ok && __all_sync(0xffffffffu, pc.next(p))) {
-        const bool dual = __all_sync(0xffffffffu, pc.dual());
-        const int steps = int(__reduce_max_sync(0xffffffffu, uint32_t(pc.x1 - pc.x0))) << int(dual);
+      auto arrived = [&](int stage, int parity) { wait((relayed ? READY : FULL) + stage, uint32_t(parity)); };
+      QueryPiece pc;
+      while (take(pc)) {
+        const bool dual = __all_sync(0xffffffffu, pc.flags & kTwoTiles);
+        const int steps = int(uniform(uint32_t(pc.n))) << int(dual);
         wait(QFULL, pieces++);
         if (ok && dual) wait(QFULL + 1, duals++);
-        // The next block's K, the next V to come: waited for ahead of the exponentials where
-        // two tiles share them, so that PV(s) and QK(s + 2) follow one another without a pause.
-        auto arrived = [&](int stage, int parity) { wait((relayed ? READY : FULL) + stage, uint32_t(parity)); };
-        // x: the score buffer
-        auto qk = [&](int x, bool both) {
-          const int way = both ? x : 2 * x;
-          const uint32_t a = q_s + (both ? x : 0) * C::QTILE_B, at = tmem + x * BN;
-          const uint32_t k = uniform(ring_s + kst * C::TILE_B);
-          auto product = [&](int i) {
-            tc_mma_in(one, at, smem_desc(a + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
-                      smem_desc(k + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
-          };
-          if (ksteps == C::DP / 16) {
-#pragma unroll
-            for (int i = 0; i < C::DP / 16; ++i) product(i);
-          } else {
-            for (int i = 0; i < ksteps; ++i) product(i);
-          }
-          tc_commit_in(one, bar(SFULL + way));
-          if (!both || x == 1) {
-            tc_commit_in(one, bar(EMPTY + kst));
-            if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
-          }
-        };
-        auto pv = [&](int x, bool both, int s) {
-          const int way = both ? x : 2 * x;
-          const uint32_t at = tmem + C::O_COL + (both ? x : 0) * C::DP, pa = tmem + x * BN;
-          const uint32_t v = uniform(ring_s + vst * C::TILE_B);
-          const uint32_t add = uniform(uint32_t(s >= (both ? 2 : 1)));
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) {
-            wait(PFULL + 3 * part + way, (way == 0 ? used0 : way == 1 ? used1 : used2) + (s >> 1));
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 4 * part; i < 4 * part + 4; ++i)
-              tc_mma_ta(one, at, pa + i * 8, smem_desc(v + i * 2048, C::ATOM_B, 1024), o_desc, i > 0 ? 1u : add);
-            tc_commit_in(one, bar(PVDONE + 3 * part + way));
-          }
-          if (!both || x == 1) {
-            tc_commit_in(one, bar(EMPTY + vst));
-            if ((vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
-          }
-        };
-        arrived(kst, kph);
         if (!ok) break;
-        tc_fence_after();
-        if (dual) {
-          qk(0, true);
-          qk(1, true);
-          for (int s = 0; s < steps; s += 2) {
-            const bool more = s + 2 < steps;
-            arrived(vst, vph);
-            if (ok && more) arrived(kst, kph);
-            if (ok) pv(0, true, s);
-            if (!ok) break;
-            if (more) qk(0, true);
-            pv(1, true, s + 1);
-            if (!ok) break;
-            if (more) qk(1, true);
+        for (int s = -2; s < steps; ++s) {
+          const int x = s & 1, way = dual ? x : 2 * x;   // the score buffer, the lane
+          const bool last_of_tile = !dual || x == 1, more = s + 2 < steps;
+          const uint32_t s_at = uniform(tmem + x * BN), o_at = uniform(tmem + C::O_COL + (dual ? x : 0) * C::DP);
+          const uint32_t q_at = uniform(q_s + (dual ? x : 0) * C::QTILE_B);
+          const uint32_t k_at = uniform(ring_s + kst * C::TILE_B), v_at = uniform(ring_s + vst * C::TILE_B);
+          // what two tiles share is waited for ahead of the exponentials, so that PV(s) and
+          // QK(s + 2) follow one another without a pause
+          if (!dual || x == 0) {
+            if (s >= 0) arrived(vst, vph);
+            if (ok && dual && more) arrived(kst, kph);
           }
-          used0 += uint32_t(steps) >> 1;
-          used1 += uint32_t(steps) >> 1;
-        } else {
-          qk(0, false);
-          if (steps > 1) {
-            arrived(kst, kph);
-            if (!ok) break;
-            qk(1, false);
-          }
-          auto step = [&](int x, int s) {
-            arrived(vst, vph);
-            if (ok) pv(x, false, s);
-            if (ok && s + 2 < steps) {
-              arrived(kst, kph);
-              if (ok) qk(x, false);
+          if (s >= 0) {
+            const uint32_t turn = (way == 0 ? used0 : way == 1 ? used1 : used2) + uint32_t(s >> 1);
+            const uint32_t add = uniform(uint32_t(s >= (dual ? 2 : 1)));
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+              if (ok) wait(PFULL + 3 * part + way, turn);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int i = 4 * part; i < 4 * part + 4; ++i)
+                tc_mma_ta(one, o_at, s_at + i * 8, smem_desc(v_at + i * 2048, C::ATOM_B, 1024), o_desc, i > 0 ? 1u : add);
+              tc_commit_in(one, bar(PVDONE + 3 * part + way));
             }
-          };
-          for (int s = 0; ok && s < steps; s += 2) {
-            step(0, s);
-            if (ok && s + 1 < steps) step(1, s + 1);
+            if (last_of_tile) {
+              tc_commit_in(one, bar(EMPTY + vst));
+              if ((vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
+            }
           }
-          used0 += uint32_t(steps + 1) >> 1;
-          used2 += uint32_t(steps) >> 1;
+          if (ok && !dual && more) arrived(kst, kph);
+          if (!ok) break;
+          if (more) {
+            tc_fence_after();
+            auto product = [&](int i) {
+              tc_mma_in(one, s_at, smem_desc(q_at + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
+                        smem_desc(k_at + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
+            };
+            if (ksteps == C::DP / 16) {
+#pragma unroll
+              for (int i = 0; i < C::DP / 16; ++i) product(i);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < ksteps; ++i) product(i);
+            }
+            tc_commit_in(one, bar(SFULL + way));
+            if (last_of_tile) {
+              tc_commit_in(one, bar(EMPTY + kst));
+              if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
+            }
+          }
         }
+        if (!ok) break;
+        used0 += uint32_t(steps + 1) >> 1;
+        (dual ? used1 : used2) += uint32_t(steps) >> 1;
       }
       tc_commit_in(one, bar(LAST));
       __syncwarp();
     } else if (relayed && warp == C::MMA_WARP + 1) {
       // ---- copies that have landed are made visible to the products: the fence takes
       // hundreds of clocks, which the warp that issues them does not have
-      QueryPieces<C> pc;
-      begin(pc);
       int stage = 0, phase = 0;
-      bool ok = true;
-      while (ok && pc.next(p)) {
-        for (int x = 2 * pc.x0; ok && x < 2 * pc.x1; ++x) {
+      QueryPiece pc;
+      while (take(pc)) {
+        for (int x = 0; ok && x < 2 * pc.n; ++x) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar(FULL + stage), uint32_t(phase), &gave_up));
           if (!ok) break;
           proxy_fence();
+          __syncwarp();
           if (lane == 0) mbar_arrive(bar(READY + stage));
           if (++stage == C::STAGES) stage = 0, phase ^= 1;
         }
+        if (!ok) break;
+      }
+    } else if (warp == C::MMA_WARP + 2) {
+      // ---- the planner: the chunk's pieces, a few ahead of the other warps.  (With this in
+      // every role the kernel was 200 KB, more than the instruction cache holds: whatever was
+      // not the inner loop ran at 8 clocks an instruction and more.)
+      QueryPieces<C> pc;
+      pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+      bool more = true;
+      for (uint32_t i = 0; more; ++i) {
+        more = __any_sync(0xffffffffu, pc.next(p)) != 0;
+        const uint32_t slot = i % kPieceRing;
+        if (i >= kPieceRing) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + slot), (i / kPieceRing - 1u) & 1u, &gave_up));
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          QueryPiece x{};
+          if (more) {
+            const bool begins = pc.begins(), whole = begins && pc.ends();
+            int unused;
+            query_sees(int(fast_div(uint32_t(pc.u.row0), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window, &x.lo, &unused);
+            query_sees(int(fast_div(uint32_t(pc.u.row0 + pc.u.rows - 1), p.fd_group)), pc.s.nq, pc.s.kv, p.causal,
+                       p.window, &unused, &x.hi);
+            x.b = pc.b;
+            x.h = pc.h;
+            x.n = pc.x1 - pc.x0;
+            x.t0 = (pc.u.blk0 + pc.x0) * BN;
+            x.row0 = pc.u.row0;
+            x.rows = pc.u.rows;
+            x.q0 = pc.s.q0;
+            x.nq = pc.s.nq;
+            x.kv = pc.s.kv;
+            x.flags = (pc.dual() ? kTwoTiles : 0) | (begins ? kBegins : 0) | (whole ? kWhole : 0);
+            if (begins && !whole) {
+              // the chunks that the unit lies in
+              const long long first = pc.pos - pc.x1;
+              const int last = int(((first + pc.u.blocks) * chunks - 1) / total);
+              p.open[blockIdx.x] = make_int4(pc.b, pc.h, pc.m, last - int(blockIdx.x) + 1);
+            }
+          }
+          ring_of_pieces[slot] = x;
+          mbar_arrive(bar(PIECE + slot));
+        }
+        __syncwarp();
       }
     }
   } else if (warp >= C::COPY_WARP) {
     set_registers<C::COPY_REGS, false>();
     // ---- copies
-    QueryPieces<C> pc;
-    begin(pc);
     const int pt = tid - C::COPY_WARP * 32;
     // boxes: lane i of the first warp takes rows from box_r on, 64 elements from box_c on
     const int columns = (p.D + 63) >> 6, box_r = lane / columns * maps.box, box_c = lane % columns * 64;
     int stage = 0, phase = 1;
-    uint32_t blk = 0;
-    bool ok = true;
+    uint32_t blk = 0, turns = 0;
     auto advance = [&]() {
       if (++stage == C::STAGES) stage = 0, phase ^= 1;
     };
-    uint32_t turns = 0;
     auto together = [&]() {                       // the four warps, with a limit as for every wait
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(GROUP));
       ok = __all_sync(0xffffffffu, mbar_wait(bar(GROUP), turns++ & 1u, &gave_up));
     };
-    while (ok && pc.next(p)) {
-      // the tokens that some row of the unit sees
-      int lo, hi, unused;
-      query_sees(int(fast_div(uint32_t(pc.u.row0), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window, &lo, &unused);
-      query_sees(int(fast_div(uint32_t(pc.u.row0 + pc.u.rows - 1), p.fd_group)), pc.s.nq, pc.s.kv, p.causal, p.window,
-                 &unused, &hi);
+    QueryPiece pc;
+    while (take(pc)) {
       int page = -1, pg = 0;
       auto lookup = [&](int t) {
         page = -1;
-        if (t >= lo && t < hi) {
+        if (t >= pc.lo && t < pc.hi) {
           pg = int(fast_div(uint32_t(t), p.fd_page));
           page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
         }
@@ -629,18 +667,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       // Whole boxes, present or not (one that is not lies behind the rows and reads as
       // zeros), are the first warp's; a block in which the range of tokens cuts a box is
       // copied row by row by all four.
-      auto boxes = [&](int x) {
-        const int t0 = (pc.u.blk0 + x) * BN;
-        return C::TYPE != kQE4m3 && maps.box > 0 && (max(lo - t0, 0) & (maps.box - 1)) == 0 &&
-               (min(hi - t0, BN) & (maps.box - 1)) == 0;
+      auto boxes = [&](int t0) {
+        return C::TYPE != kQE4m3 && maps.box > 0 && (max(pc.lo - t0, 0) & (maps.box - 1)) == 0 &&
+               (min(pc.hi - t0, BN) & (maps.box - 1)) == 0;
       };
-      auto mine = [&](int x) { return (pc.u.blk0 + x) * BN + (maps.box > 0 && boxes(x) ? box_r : pt); };
-      lookup(mine(pc.x0));
-      for (int x = pc.x0; ok && x < pc.x1; ++x, ++blk) {
-        if (boxes(x)) {
+      bool boxed = boxes(pc.t0);
+      lookup(pc.t0 + (boxed ? box_r : pt));
+      for (int x = 0; ok && x < pc.n; ++x, ++blk) {
+        const int t0 = pc.t0 + x * BN;
+        const bool next_boxed = boxes(t0 + BN);
+        const int next_t = t0 + BN + (next_boxed ? box_r : pt);
+        if (boxed) {
           if (pt < 32) {
             const bool have = box_r < BN && page_present(page, p.num_pages);
-            const int y = have ? int(int64_t(page) * p.P + (mine(x) - pg * p.P)) : int(p.num_pages * p.P);
+            const int y = have ? int(int64_t(page) * p.P + (t0 + box_r - pg * p.P)) : int(p.num_pages * p.P);
             const uint32_t bits = __ballot_sync(0xffffffffu, have);
             if (lane < WORDS) {                   // tokens lane * 32 on
               const int at = lane * 32 / maps.box * columns;
@@ -650,8 +690,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(KNOWN + blk % INFO), 4);
-            if (x + 1 < pc.x1) lookup(mine(x + 1));
-#pragma unroll
+            if (x + 1 < pc.n) lookup(next_t);
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
               if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
               if (!ok) break;
@@ -664,10 +704,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               advance();
             }
           } else {
-            if (x + 1 < pc.x1 && !boxes(x + 1)) lookup(mine(x + 1));
+            if (x + 1 < pc.n && !next_boxed) lookup(next_t);
             advance();
             advance();
           }
+          boxed = next_boxed;
           continue;
         }
         // the other three warps pass over whole boxes: they wait here for the first, whose
@@ -676,14 +717,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (!ok) break;
         const bool have = pt < BN && page_present(page, p.num_pages);
         int64_t *const at = offs[blk & 1u];
-        if (pt < BN) at[pt] = have ? int64_t(page) * p.P + (mine(x) - pg * p.P) : -1;
+        if (pt < BN) at[pt] = have ? int64_t(page) * p.P + (t0 + pt - pg * p.P) : -1;
         const uint32_t word = __ballot_sync(0xffffffffu, have);
         if (lane == 0) {
           if (pt < BN) there[blk % INFO][pt >> 5] = word;
           mbar_arrive(bar(KNOWN + blk % INFO));
         }
         together();
-        if (x + 1 < pc.x1) lookup(mine(x + 1));
+        if (x + 1 < pc.n) lookup(next_t);
+        boxed = next_boxed;
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
           if (!ok) break;
@@ -736,10 +779,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           advance();
         }
       }
+      if (!ok) break;
     }
     if constexpr (C::TYPE != kQE4m3) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       // after a wait that ran out, boxes may be on their way still: the last of each stage
+#pragma unroll 1
       for (int i = 0; !ok && i < C::STAGES; ++i) {
         mbar_wait<true>(bar(FULL + stage), uint32_t(phase), &gave_up);
         advance();
@@ -748,74 +793,112 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   } else {
     set_registers<C::SOFT_REGS, true>();
     // ---- softmax: a thread per row
-    QueryPieces<C> pc;
-    begin(pc);
-    const int tile = warp >> 2, r = tid & 127;
+    const int tile = warp >> 2, r = tid & 127, w0 = (warp & 3) * 32, row = tile * kQueryRows + r;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t o_at = tmem + C::O_COL + tile * C::DP + lanes;
     uint32_t used0 = 0, used2 = 0, blk = 0;       // of this tile's lane, of lane 2
-    bool ok = true;
-    while (ok && pc.next(p)) {
-      const bool dual = pc.dual();
-      const int n = pc.x1 - pc.x0;
-      if (tile == 1 && !dual) {                   // the other tile's
-        blk += uint32_t(n);
-        continue;
+    QueryPiece pc;
+    // this tile's next piece: units of one tile of rows are the first tile's
+    auto next = [&]() {
+      for (;;) {
+        if (!take(pc)) return false;
+        if (tile == 0 || __any_sync(0xffffffffu, pc.flags & kTwoTiles)) return true;
+        blk += uint32_t(pc.n);
       }
+    };
+    // Between global and shared memory a warp moves its 32 rows of Q, and of the result, by
+    // 16 bytes a lane: LPR lanes a row, RPI rows at a time.  A warp alone on its scheduler
+    // takes 4 to 5 clocks an instruction, so what counts here is their number: each lane
+    // works out where its own row lies, and the others ask it.
+    constexpr int LPR = C::DP / 8, RPI = 32 / LPR, QI = 32 / RPI;
+    const int qc = lane % LPR, qr = lane / LPR;
+    unsigned char *const q_w = q_p + tile * C::QTILE_B + w0 * 128;   // this warp's part of Q's tile
+    // in it, elements 8 qc on of row i * RPI + qr (whose swizzle is that of qr and of i * RPI)
+    unsigned char *const q_mine = q_w + (qc >> 3) * C::QATOM_B + qr * 128;
+    auto slot = [&](int i) { return q_mine + i * RPI * 128 + ((((qc & 7) ^ qr) ^ (i * RPI & 7)) << 4); };
+    auto ask = [&](int64_t x, int i) { return __shfl_sync(0xffffffffu, (long long)x, i * RPI + qr); };
+    bool more = false, live = false;
+    int64_t out_at = -1, out32_at = 0;            // where this thread's row lies in out, in lse; -1: nowhere
+    int64_t lse_at = 0;
+    int lo = 0, hi = 0;                           // the tokens it sees
+    uint4 qv[QI];
+    // the row's places, and Q on its way
+    auto load_q = [&]() {
+      live = more && row < pc.rows;
+      int64_t own = -1;
+      lo = hi = 0;
+      out_at = -1;
+      if (live) {
+        const QueryRow x = query_row(p, pc.q0, pc.h, pc.row0 + row);
+        own = x.token * p.q_st + int64_t(x.head) * p.q_sh;
+        out_at = x.token * p.o_st + int64_t(x.head) * p.o_sh;
+        out32_at = x.token * p.Hq + x.head;
+        lse_at = x.token * p.lse_st + x.head;
+        query_sees(x.i, pc.nq, pc.kv, p.causal, p.window, &lo, &hi);
+      }
+      const char *const src = static_cast<const char *>(p.q) + qc * 16;
+#pragma unroll
+      for (int i = 0; i < QI; ++i) {
+        const int64_t at = ask(own, i);
+        qv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0 && qc * 8 < p.D) qv[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * at));
+      }
+    };
+    // Q into shared memory (the products that read the one before it are done: their scores
+    // were there); returns the scores' factor of this thread's row
+    auto store_q = [&]() {
+      float mul = p.scale2;
+      if (C::TYPE == kQE4m3 && p.bf16) {
+        // fp16, after the power of two that brings the row's largest element into [1, 2):
+        // queries keep every bit down to 2^-14 of it, and below that are off by 2^-25 of it
+        // at most
+#pragma unroll
+        for (int i = 0; i < QI; ++i) {
+          uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+          float top = 0.f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = q_unpack2(w[y], true);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int ex = top < INFINITY ? max(-120, min(120, (__float_as_int(top) >> 23) - 127)) : 0;
+          const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = q_unpack2(w[y], true);
+            w[y] = pack2<false>(f.x * down, f.y * down);
+          }
+          qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          const int mine = __shfl_sync(0xffffffffu, ex, lane % RPI * LPR);
+          if (i == lane / RPI) mul = p.scale2 * __int_as_float((127 + mine) << 23);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < QI; ++i)
+        if (qc * 8 < d16) *reinterpret_cast<uint4 *>(slot(i)) = qv[i];
+      proxy_fence();
+      __syncwarp();
+      if (more && lane == 0) mbar_arrive(bar(QFULL + tile));
+      return mul;
+    };
+    // One pass per piece, the first for the first piece's Q alone: the code is here once.
+    // (qv lives within a pass only; behind a branch the compiler would keep it through all blocks.)
+    bool any = false, dual = false, begins = false, whole = false;
+    int n = 0, t_first = 0;
+    float mul = 0.f, m = -INFINITY, l = 0.f;
+    for (;;) {
       // where block j's scores are, and how often its lane was used before
       auto way = [&](int j) { return dual ? tile : 2 * (j & 1); };
       auto turn = [&](int j) { return dual ? used0 + uint32_t(j) : ((j & 1) ? used2 : used0) + (uint32_t(j) >> 1); };
-      // ---- Q: this thread's row into shared memory (the products that read the one
-      // before it are done: their scores were)
-      const int row = tile * kQueryRows + r;
-      const bool live = row < pc.u.rows;
-      const QueryRow out = query_row(p, pc.s, pc.h, pc.u.row0 + (live ? row : 0));
-      int lo = 0, hi = 0;
-      if (live) query_sees(out.i, pc.s.nq, pc.s.kv, p.causal, p.window, &lo, &hi);
-      float mul = p.scale2;
-      {
-        const char *src = static_cast<const char *>(p.q) + 2 * (out.token * p.q_st + int64_t(out.head) * p.q_sh);
-        unsigned char *dst = q_p + tile * C::QTILE_B + r * 128;
-        float down = 1.f;
-        if constexpr (C::TYPE == kQE4m3) {
-          // fp16, after the power of two that brings the row's largest element into
-          // [1, 2): bf16 and fp16 queries keep every bit down to 2^-14 of it, and
-          // below that are off by 2^-25 of it at most
-          float top = 0.f;
-          for (int c = 0; live && c < p.D; c += 8) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 2 * c));
-            for (const uint32_t y : {w.x, w.y, w.z, w.w}) {
-              const float2 f = q_unpack2(y, p.bf16);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          const int ex = top > 0.f && top < INFINITY ? max(-120, min(120, ilogbf(top))) : 0;
-          down = ldexpf(1.f, -ex);
-          mul = p.scale2 * ldexpf(1.f, ex);
-        }
-#pragma unroll 4
-        for (int c = 0; c < d16; c += 8) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (live && c < p.D) w = __ldg(reinterpret_cast<const uint4 *>(src + 2 * c));
-          if constexpr (C::TYPE == kQE4m3) {
-            auto lower = [&](uint32_t y) {
-              const float2 f = q_unpack2(y, p.bf16);
-              return pack2<false>(f.x * down, f.y * down);
-            };
-            w = make_uint4(lower(w.x), lower(w.y), lower(w.z), lower(w.w));
-          }
-          *reinterpret_cast<uint4 *>(dst + (c >> 6) * C::QATOM_B + ((((c >> 3) & 7) ^ (r & 7)) << 4)) = w;
-        }
-        proxy_fence();
-        mbar_arrive(bar(QFULL + tile));
-      }
-      const bool any = __any_sync(0xffffffffu, live);   // of a warp without rows, nothing is looked at
-      float m = -INFINITY, mu = 0.f, l = 0.f;
+      m = -INFINITY, l = 0.f;
+      float mu = 0.f;
+#pragma unroll 1
       for (int j = 0; j < n; ++j, ++blk) {
-        const int x = dual ? tile : j & 1;
         uint32_t words[WORDS];
         bool mask = false;
-        const int t0 = (pc.u.blk0 + pc.x0 + j) * BN;
+        const int t0 = t_first + j * BN;
         // (after units that these warps sat out, the copies may be many blocks behind: then the
         // scores come first, before a word's barrier could have turned around)
         if (j == 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(0)), turn(0) & 1u, &gave_up));
@@ -832,17 +915,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(j)), turn(j) & 1u, &gave_up));
         if (!ok) break;
         if (!any) {
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-            if (lane == 0) mbar_arrive(bar(PFULL + 3 * part + way(j)));
+          if (lane < PARTS) mbar_arrive(bar(PFULL + 3 * lane + way(j)));
           continue;
         }
         tc_fence_after();
-        const uint32_t s_at = tmem + x * BN + lanes;
-        // 64 tokens at a time, whose product with V starts while the next ones are taken.  The
-        // usual 64 are done in one pass, 32 at a time, the scores of the next 32 on their
-        // way: exponentials against the reference there is, the largest score beside them.
-        // Only when that turns out too large are they taken again.
+        const uint32_t s_at = tmem + (dual ? tile : j & 1) * BN + lanes;
+        // 64 tokens at a time, whose product with V starts while the next ones are taken
         float e[BN];                              // scores less the reference, in log2
         tc_ld32(s_at, e);
         tc_ld32(s_at + 32, e + 32);
@@ -850,46 +928,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         tc_loaded32(e + 32);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
+          if (part + 1 < PARTS) {                 // the next scores on their way
+            tc_ld32(s_at + 64 * part + 64, e + 64 * part + 64);
+            tc_ld32(s_at + 64 * part + 96, e + 64 * part + 96);
+          }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint64_t sum[2] = {0, 0};               // two pairs of sums
-          auto exponentials = [&](int w) {        // P, rounded to the products' type; the sums keep all bits
-            uint32_t pk[16];
+          const uint64_t times = f32x2(mul, mul), less = f32x2(-mu, -mu);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
-              sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
-              pk[i] = pack2<C::BF16>(a, z);
-            }
-            tc_st16u(s_at + w * 16, pk);
-          };
-          const uint64_t mul2 = f32x2(mul, mul), mu2 = f32x2(-mu, -mu);
-          bool raise = false, any_raise = false;
-          float over = -INFINITY;
+          for (int i = 64 * part; i < 64 * part + 64; i += 2) unpack(fma2(f32x2(e[i], e[i + 1]), times, less), e + i);
+          if (__builtin_expect(mask, 0)) {
 #pragma unroll
-          for (int w = 2 * part; w < 2 * part + 2; ++w) {
-            if (w + 2 < WORDS) tc_ld32(s_at + (w + 2) * 32, e + (w + 2) * 32);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float *v = e + 32 * w + i;
-              unpack(fma2(f32x2(v[0], v[1]), mul2, mu2), v);
-            }
-            if (__builtin_expect(mask, 0)) {
+            for (int w = 2 * part; w < 2 * part + 2; ++w) {
               const int a = min(32, max(0, lo - t0 - 32 * w)), z = min(32, max(0, hi - t0 - 32 * w));
               const uint32_t in = words[w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
 #pragma unroll
               for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[32 * w + i], e[32 * w + i + 1]);
-            if (w & 1) {                          // asked here, so that the answer comes during the exponentials
-              over = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-              raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
-              any_raise = __any_sync(0xffffffffu, raise);
-            }
-            exponentials(w);                      // over scores that are here: P of word w takes half of word w / 2's place
-            if (w + 2 < WORDS) tc_loaded32(e + (w + 2) * 32);
           }
-          if (__builtin_expect(any_raise, 0)) {
+#pragma unroll
+          for (int i = 64 * part; i < 64 * part + 64; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[i], e[i + 1]);
+          const float over = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          const bool raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
+          if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
             float f = 1.f;
             if (raise) {
               const float now = fmaxf(m, over + mu - C::ABOVE), by = mu - now;
@@ -900,9 +960,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               for (int i = 64 * part; i < 64 * part + 64; ++i) e[i] += by;
             }
             __syncwarp();
-            sum[0] = sum[1] = 0;
-            exponentials(2 * part);
-            exponentials(2 * part + 1);
             if (j > 0 || part > 0) {              // O, once the product with V before this is done
               const int last = part > 0 ? j : j - 1;
               ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 3 * PARTS - 3) + way(last)), turn(last) & 1u, &gave_up));
@@ -919,9 +976,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               }
             }
           }
+          // P, rounded to the products' type; the sums keep all bits.  P of word w takes half of
+          // the place of the scores of word w / 2, which are here
+          uint64_t sum[2] = {0, 0};               // two pairs of sums
+#pragma unroll
+          for (int w = 2 * part; w < 2 * part + 2; ++w) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
+              sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
+              pk[i] = pack2<C::BF16>(a, z);
+            }
+            tc_st16u(s_at + w * 16, pk);
+          }
           float x[2];
           unpack(add2(sum[0], sum[1]), x);
           l += x[0] + x[1];
+          if (part + 1 < PARTS) {
+            tc_loaded32(e + 64 * part + 64);
+            tc_loaded32(e + 64 * part + 96);
+          }
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -930,47 +1005,83 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (!ok) break;
       }
       if (!ok) break;
-      // ---- the piece's end
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 3 * PARTS - 3 + way(n - 1)), turn(n - 1) & 1u, &gave_up));
-      if (!ok) break;
+      // ---- the piece's end; the next one's Q is on its way meanwhile
+      const int last_way = way(n - 1);
+      const uint32_t last_turn = turn(n - 1);
       used0 += dual ? uint32_t(n) : uint32_t(n + 1) >> 1;
       used2 += dual ? 0u : uint32_t(n) >> 1;
-      const bool whole = pc.begins() && pc.ends();
-      float *const part = p.parts + (int64_t(blockIdx.x) * 2 + (pc.begins() ? 1 : 0)) * C::PIECE;
+      const bool was_live = live;
+      const int64_t was_out = out_at, was_out32 = out32_at, was_lse = lse_at;
+      more = next();
+      load_q();
+      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 3 * PARTS - 3 + last_way), last_turn & 1u, &gave_up));
+      if (!ok) break;
       if (any) {
         tc_fence_after();
-        const float f = l == 0.f ? 0.f : p.v_scale / l;
+        // a row that saw nothing is 0, whatever 0 times V was
+        const bool none = whole && __any_sync(0xffffffffu, l == 0.f);
+        const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
+        const uint64_t f2 = f32x2(f, f);
+        const bool direct = whole && !p.out32;
+        float *part = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + tile * C::DP * kQueryRows + r;
+        float *row32 = p.out32 + was_out32 * p.D;
+        unsigned char *const mine = q_w + lane * 128;
 #pragma unroll 1
-        for (int c = 0; c < d16; c += 16) {
-          float o[16];
+        for (int c = 0; c < d16; c += 32) {
+          float o[32];
           __syncwarp();
-          tc_ld16(o_at + c, o);
-          tc_wait_ld();
-          if (!live) continue;
-          if (whole) {
+          tc_ld32(o_at + c, o);
+          tc_loaded32(o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * f;
-            query_store8(p, out, c, o);
-            if (c + 8 < p.D) query_store8(p, out, c + 8, o + 8);
-          } else {
-            float *at = part + (tile * C::DP + c) * kQueryRows + r;
+          for (int i = 0; i < 32; i += 2) unpack(mul2(f32x2(o[i], o[i + 1]), f2), o + i);
+          if (__builtin_expect(none, 0)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) __stcg(at + i * kQueryRows, o[i]);
+            for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
+          }
+          if (direct) {                           // by way of Q's place, so that lanes write rows together
+            unsigned char *const to = mine + (c >> 6) * C::QATOM_B;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4 *>(to + ((((c & 32) + i) * 2) ^ ((lane & 7) << 4))) = query_pack8<C>(p, o + i);
+          } else if (whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              if (was_live && c + i < p.D) *reinterpret_cast<float4 *>(row32 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else if (was_live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) __stcg(part + i * kQueryRows, o[i]);
+            part += 32 * kQueryRows;
           }
         }
-        if (live && whole) query_lse(p, out, m, l);
-        if (live && !whole) {
-          __stcg(part + C::ROWS * C::DP + row, m);
-          __stcg(part + C::ROWS * C::DP + C::ROWS + row, l);
-        }
         tc_fence_before();
+        if (direct) {
+          __syncwarp();
+          char *const to = static_cast<char *>(p.out) + qc * 16;
+#pragma unroll
+          for (int i = 0; i < QI; ++i) {
+            const int64_t at = ask(was_out, i);
+            if (at >= 0 && qc * 8 < p.D) *reinterpret_cast<uint4 *>(to + 2 * at) = *reinterpret_cast<const uint4 *>(slot(i));
+          }
+          __syncwarp();
+        }
+        if (was_live && whole) {
+          const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+          if (p.lse2) p.lse2[was_out32] = lse2;
+          if (p.lse) p.lse[was_lse] = lse2 * kLn2;
+        } else if (was_live) {
+          float *const ml = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + C::ROWS * C::DP + row;
+          __stcg(ml, m);
+          __stcg(ml + C::ROWS, l);
+        }
       }
-      if (tid == 0 && pc.begins() && !pc.ends()) {
-        // the chunks that the unit lies in
-        const long long first = pc.pos - pc.x1;
-        const int last = int(((first + pc.u.blocks) * chunks - 1) / total);
-        p.open[blockIdx.x] = make_int4(pc.b, pc.h, pc.m, last - int(blockIdx.x) + 1);
-      }
+      mul = store_q();
+      if (!more) break;
+      dual = pc.flags & kTwoTiles;
+      begins = pc.flags & kBegins;
+      whole = pc.flags & kWhole;
+      n = pc.n;
+      t_first = pc.t0;
+      any = __any_sync(0xffffffffu, live);        // of a warp without rows, nothing is looked at
     }
     tc_fence_before();
   }
@@ -1037,7 +1148,7 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   const float f = sum == 0.f ? 0.f : p.v_scale / sum;
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = sum == 0.f ? 0.f : acc[i] * f;
-  const QueryRow out = query_row(p, s, at.y, u.row0 + row);
+  const QueryRow out = query_row(p, s.q0, at.y, u.row0 + row);
   query_store8(p, out, col, acc);
   if (col == 0) query_lse(p, out, m, sum);
 }
