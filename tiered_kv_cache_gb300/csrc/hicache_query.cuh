@@ -17,9 +17,8 @@
 // from 280 rows on the tensor cores bind, below that HBM.
 //
 // Softmax: a thread per row, so that maximum and sum need no other thread.  What a row's
-// scores are taken relative to follows the running maximum only when some score passes
-// it by more than P's type can hold; O is rescaled then, and only then, by the same
-// thread.
+// scores are taken relative to follows the running maximum only when exponentials pass
+// what P's type can hold; O is rescaled then, and only then, by the same thread.
 //
 // The work is cut into blocks; the blocks of all units (sequences, kv heads, groups of
 // rows, in order) are dealt in equal contiguous ranges, chunks, to the CTAs (one per
@@ -69,24 +68,32 @@ struct QueryConfig {
   static_assert(4 * QT * SOFT_REGS + 4 * COPY_REGS + 4 * MMA_REGS <= WARPS * (65536 / THREADS / 8 * 8), "registers");
   static constexpr int O_COL = 2 * BN;            // tensor memory: two score buffers, then O of each tile
   static constexpr int PIECE = ROWS * DP_ + 2 * ROWS;   // floats: O [tile][element][row], m, l
-  static constexpr float RAISE = kRaise<!BF16>, ABOVE = kAbove<!BF16>;
+  static constexpr float LIMIT = BF16 ? 1.f : 32768.f, ABOVE = kAbove<!BF16>;   // 2^kRaise
+  static_assert(kRaise<false> == 0.f && kRaise<true> == 15.f, "the sums' limit");
   static_assert(O_COL + QT * DP_ <= 512, "tensor memory");
 };
 
-// d += a b in one lane of a warp that runs as one: predicated, since behind a branch the
-// compiler no longer knows that the operands are the same in all lanes, and takes each
-// from vector registers (an issue then cost 75 clocks)
-__device__ __forceinline__ void tc_mma_in(uint32_t lane, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// A shared-memory operand's descriptor in two halves (see smem_desc): the upper is the same
+// for all, the lower moves by an address over 16, so that a product costs an addition.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;   // 8 rows of 128 bytes, 128-byte swizzle
+// d += a b in one lane of a warp that runs as one: predicated, not behind a branch, where the
+// compiler takes each operand from vector registers
+__device__ __forceinline__ void tc_mma_in(uint32_t lane, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{.reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lane)
+      "{.reg .pred p, q; .reg .b64 x, y; setp.ne.u32 p, %5, 0; setp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc),
+      "r"(add), "r"(lane)
       : "memory");
 }
 // the same with a in tensor memory
-__device__ __forceinline__ void tc_mma_ta(uint32_t lane, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t lane, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{.reg .pred p, q; setp.ne.u32 p, %4, 0; setp.ne.u32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lane)
+      "{.reg .pred p, q; .reg .b64 y; setp.ne.u32 p, %5, 0; setp.ne.u32 q, %6, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc),
+      "r"(add), "r"(lane)
       : "memory");
 }
 __device__ __forceinline__ void tc_commit_in(uint32_t lane, uint32_t bar) {
@@ -516,32 +523,35 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       while (take(pc)) {
         const bool dual = __all_sync(0xffffffffu, pc.flags & kTwoTiles);
         const int steps = int(uniform(uint32_t(pc.n))) << int(dual);
-        wait(QFULL, pieces++);
-        if (ok && dual) wait(QFULL + 1, duals++);
-        if (!ok) break;
-        for (int s = -2; s < steps; ++s) {
-          const int x = s & 1, way = dual ? x : 2 * x;   // the score buffer, the lane
+        uint32_t k_at = 0, v_at = 0;              // of the block's K, V
+        // PV(s), QK(s + 2) with score buffer x
+        auto step = [&](int s, int x) {
+          const int way = dual ? x : 2 * x;       // the lane
           const bool last_of_tile = !dual || x == 1, more = s + 2 < steps;
-          const uint32_t s_at = uniform(tmem + x * BN), o_at = uniform(tmem + C::O_COL + (dual ? x : 0) * C::DP);
-          const uint32_t q_at = uniform(q_s + (dual ? x : 0) * C::QTILE_B);
-          const uint32_t k_at = uniform(ring_s + kst * C::TILE_B), v_at = uniform(ring_s + vst * C::TILE_B);
+          const uint32_t s_at = tmem + x * BN, o_at = tmem + C::O_COL + (dual ? x : 0) * C::DP;
           // what two tiles share is waited for ahead of the exponentials, so that PV(s) and
           // QK(s + 2) follow one another without a pause
           if (!dual || x == 0) {
-            if (s >= 0) arrived(vst, vph);
-            if (ok && dual && more) arrived(kst, kph);
+            if (s >= 0) {
+              arrived(vst, vph);
+              v_at = uniform(desc_low(ring_s + vst * C::TILE_B, C::ATOM_B));
+            }
+            if (ok && dual && more) {
+              arrived(kst, kph);
+              k_at = uniform(desc_low(ring_s + kst * C::TILE_B, 16));
+            }
           }
           if (s >= 0) {
             const uint32_t turn = (way == 0 ? used0 : way == 1 ? used1 : used2) + uint32_t(s >> 1);
-            const uint32_t add = uniform(uint32_t(s >= (dual ? 2 : 1)));
+            const uint32_t add = s >= (dual ? 2 : 1);
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
               if (ok) wait(PFULL + 3 * part + way, turn);
-              if (!ok) break;
+              if (!ok) return;
               tc_fence_after();
 #pragma unroll
               for (int i = 4 * part; i < 4 * part + 4; ++i)
-                tc_mma_ta(one, o_at, s_at + i * 8, smem_desc(v_at + i * 2048, C::ATOM_B, 1024), o_desc, i > 0 ? 1u : add);
+                tc_mma_ta(one, o_at, s_at + i * 8, v_at + i * (2048 >> 4), o_desc, i > 0 ? 1u : add);
               tc_commit_in(one, bar(PVDONE + 3 * part + way));
             }
             if (last_of_tile) {
@@ -549,27 +559,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               if ((vst += 2) >= C::STAGES) vst -= C::STAGES, vph ^= 1;
             }
           }
-          if (ok && !dual && more) arrived(kst, kph);
-          if (!ok) break;
-          if (more) {
-            tc_fence_after();
-            auto product = [&](int i) {
-              tc_mma_in(one, s_at, smem_desc(q_at + (i >> 2) * C::QATOM_B + (i & 3) * 32, 16, 1024),
-                        smem_desc(k_at + (i >> 2) * C::ATOM_B + (i & 3) * 32, 16, 1024), s_desc, i > 0);
-            };
-            if (ksteps == C::DP / 16) {
-#pragma unroll
-              for (int i = 0; i < C::DP / 16; ++i) product(i);
-            } else {
-#pragma unroll 1
-              for (int i = 0; i < ksteps; ++i) product(i);
-            }
-            tc_commit_in(one, bar(SFULL + way));
-            if (last_of_tile) {
-              tc_commit_in(one, bar(EMPTY + kst));
-              if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
-            }
+          if (!ok || !more) return;
+          if (!dual) {
+            arrived(kst, kph);
+            if (!ok) return;
+            k_at = uniform(desc_low(ring_s + kst * C::TILE_B, 16));
           }
+          tc_fence_after();
+          const uint32_t q_at = desc_low(q_s + (dual ? x : 0) * C::QTILE_B, 16);
+          auto product = [&](int i) {
+            tc_mma_in(one, s_at, q_at + ((i >> 2) * C::QATOM_B + (i & 3) * 32) / 16, k_at + ((i >> 2) * C::ATOM_B + (i & 3) * 32) / 16,
+                      s_desc, i > 0);
+          };
+          if (ksteps == C::DP / 16) {
+#pragma unroll
+            for (int i = 0; i < C::DP / 16; ++i) product(i);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < ksteps; ++i) product(i);
+          }
+          tc_commit_in(one, bar(SFULL + way));
+          if (last_of_tile) {
+            tc_commit_in(one, bar(EMPTY + kst));
+            if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
+          }
+        };
+#pragma unroll 1
+        for (int s = -2; ok && s < steps; s += 2) {
+          if (s < 0) {
+            wait(QFULL, pieces++);
+            if (!ok) break;
+          }
+          step(s, 0);
+          if (!ok || s + 1 >= steps) break;
+          if (s < 0 && dual) {
+            wait(QFULL + 1, duals++);
+            if (!ok) break;
+          }
+          step(s + 1, 1);
         }
         if (!ok) break;
         used0 += uint32_t(steps + 1) >> 1;
@@ -892,8 +919,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       // where block j's scores are, and how often its lane was used before
       auto way = [&](int j) { return dual ? tile : 2 * (j & 1); };
       auto turn = [&](int j) { return dual ? used0 + uint32_t(j) : ((j & 1) ? used2 : used0) + (uint32_t(j) >> 1); };
-      m = -INFINITY, l = 0.f;
+      m = live ? -INFINITY : 0.f, l = 0.f;
       float mu = 0.f;
+      bool unset = true;                          // a row of the warp has no reference yet
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++blk) {
         uint32_t words[WORDS];
@@ -920,19 +948,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         }
         tc_fence_after();
         const uint32_t s_at = tmem + (dual ? tile : j & 1) * BN + lanes;
-        // 64 tokens at a time, whose product with V starts while the next ones are taken
+        // 64 tokens at a time, whose product with V starts while the next ones are taken.  No
+        // maximum is looked for in the usual 64: an exponential above 2^RAISE shows in their sum,
+        // and only then (or while a row has no reference) the scores are gone through again,
+        // a reference put kAbove from the maximum, and the exponentials taken anew.
         float e[BN];                              // scores less the reference, in log2
-        tc_ld32(s_at, e);
-        tc_ld32(s_at + 32, e + 32);
-        tc_loaded32(e);
-        tc_loaded32(e + 32);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) tc_ld32(s_at + 32 * w, e + 32 * w);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) tc_loaded32(e + 32 * w);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
-          if (part + 1 < PARTS) {                 // the next scores on their way
-            tc_ld32(s_at + 64 * part + 64, e + 64 * part + 64);
-            tc_ld32(s_at + 64 * part + 96, e + 64 * part + 96);
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           const uint64_t times = f32x2(mul, mul), less = f32x2(-mu, -mu);
 #pragma unroll
           for (int i = 64 * part; i < 64 * part + 64; i += 2) unpack(fma2(f32x2(e[i], e[i + 1]), times, less), e + i);
@@ -945,58 +971,59 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
             }
           }
+          float all;
+          for (bool again = unset;;) {
+            if (__builtin_expect(again, 0)) {
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 64 * part; i < 64 * part + 64; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[i], e[i + 1]);
-          const float over = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-          const bool raise = over > C::RAISE || (m == -INFINITY && over > -INFINITY);
-          if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
-            float f = 1.f;
-            if (raise) {
-              const float now = fmaxf(m, over + mu - C::ABOVE), by = mu - now;
-              f = m == -INFINITY ? 0.f : exp2_fast(m - now);
-              m = mu = now;
+              for (int i = 64 * part; i < 64 * part + 64; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[i], e[i + 1]);
+              const float now = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) + mu - C::ABOVE);
+              const float f = m == -INFINITY ? 0.f : exp2_fast(m - now), use = now == -INFINITY ? 0.f : now, by = mu - use;
+              m = now;
+              mu = use;
               l *= f;
 #pragma unroll
               for (int i = 64 * part; i < 64 * part + 64; ++i) e[i] += by;
-            }
-            __syncwarp();
-            if (j > 0 || part > 0) {              // O, once the product with V before this is done
-              const int last = part > 0 ? j : j - 1;
-              ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 3 * PARTS - 3) + way(last)), turn(last) & 1u, &gave_up));
-              if (!ok) break;
-              tc_fence_after();
+              unset = __any_sync(0xffffffffu, m == -INFINITY);
+              if (j > 0 || part > 0) {            // O, once the product with V before this is done
+                const int last = part > 0 ? j : j - 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 3 * PARTS - 3) + way(last)), turn(last) & 1u, &gave_up));
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < d16; c += 16) {
-                float o[16];
-                tc_ld16(o_at + c, o);
-                tc_wait_ld();
+                for (int c = 0; c < d16; c += 16) {
+                  float o[16];
+                  tc_ld16(o_at + c, o);
+                  tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= f;
-                tc_st16(o_at + c, o);
+                  for (int i = 0; i < 16; ++i) o[i] *= f;
+                  tc_st16(o_at + c, o);
+                }
               }
             }
-          }
-          // P, rounded to the products' type; the sums keep all bits.  P of word w takes half of
-          // the place of the scores of word w / 2, which are here
-          uint64_t sum[2] = {0, 0};               // two pairs of sums
+            // P, rounded to the products' type; the sums keep all bits.  P of word w takes half
+            // of the place of the scores of word w / 2
+            uint64_t sum[2] = {0, 0};             // two pairs of sums
 #pragma unroll
-          for (int w = 2 * part; w < 2 * part + 2; ++w) {
-            uint32_t pk[16];
+            for (int w = 2 * part; w < 2 * part + 2; ++w) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
-              sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
-              pk[i] = pack2<C::BF16>(a, z);
+              for (int i = 0; i < 16; ++i) {
+                const float a = exp2_fast(e[32 * w + 2 * i]), z = exp2_fast(e[32 * w + 2 * i + 1]);
+                sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
+                pk[i] = pack2<C::BF16>(a, z);
+              }
+              tc_st16u(s_at + w * 16, pk);
             }
-            tc_st16u(s_at + w * 16, pk);
+            float x[2];
+            unpack(add2(sum[0], sum[1]), x);
+            all = x[0] + x[1];
+            if (again) break;
+            again = __any_sync(0xffffffffu, all > C::LIMIT);
+            if (__builtin_expect(!again, 1)) break;
           }
-          float x[2];
-          unpack(add2(sum[0], sum[1]), x);
-          l += x[0] + x[1];
-          if (part + 1 < PARTS) {
-            tc_loaded32(e + 64 * part + 64);
-            tc_loaded32(e + 64 * part + 96);
-          }
+          if (!ok) break;
+          l += all;
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -1057,10 +1084,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (direct) {
           __syncwarp();
           char *const to = static_cast<char *>(p.out) + qc * 16;
+          constexpr int AT_ONCE = QI < 16 ? QI : 16;
+#pragma unroll 1
+          for (int i0 = 0; i0 < QI; i0 += AT_ONCE) {
+            uint4 w[AT_ONCE];
 #pragma unroll
-          for (int i = 0; i < QI; ++i) {
-            const int64_t at = ask(was_out, i);
-            if (at >= 0 && qc * 8 < p.D) *reinterpret_cast<uint4 *>(to + 2 * at) = *reinterpret_cast<const uint4 *>(slot(i));
+            for (int i = 0; i < AT_ONCE; ++i) w[i] = *reinterpret_cast<const uint4 *>(slot(i0 + i));
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+              const int64_t at = ask(was_out, i0 + i);
+              if (at >= 0 && qc * 8 < p.D) *reinterpret_cast<uint4 *>(to + 2 * at) = w[i];
+            }
           }
           __syncwarp();
         }
