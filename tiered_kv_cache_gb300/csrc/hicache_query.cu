@@ -14,11 +14,12 @@ int launch_query_type(const QueryParams &p, int device, cudaStream_t st, int *la
 
 }  // namespace
 
-QuerySpace query_space(int D, int phases) {
+QuerySpace query_space(int D) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  const int64_t rows = kQueryRows * query_tiles(D), chunks = int64_t(kQueryCtas) * phases;
+  const int64_t rows = kQueryRows * query_tiles(D), chunks = kQueryCtas;
   QuerySpace s;
-  s.open = up((kDecodeCtas + 1) * 4);             // the error word lies where decode attention's does
+  s.next = up((kDecodeCtas + 1) * 4);             // the error word lies where decode attention's does
+  s.open = s.next + 256;
   s.parts = up(s.open + chunks * 16);
   s.bytes = up(s.parts + chunks * 2 * (rows * query_cols(D) + 2 * rows) * 4);
   return s;

@@ -20,11 +20,12 @@
 // scores are taken relative to follows the running maximum only when exponentials pass
 // what P's type can hold; O is rescaled then, and only then, by the same thread.
 //
-// The work is cut into blocks; the blocks of all units (sequences, kv heads, groups of
-// rows, in order) are dealt in equal contiguous ranges, chunks, to the CTAs (one per
-// SM), whatever the lengths.  A chunk's part of a unit is a piece; whole units are
+// The work of few units is cut into blocks; the blocks of all units (sequences, kv heads,
+// groups of rows, in order) are dealt in equal contiguous ranges, chunks, to the CTAs (one
+// per SM), whatever the lengths.  A chunk's part of a unit is a piece; whole units are
 // written out directly, the other pieces go to the workspace and query_join_kernel adds
-// them in order, so that timing cannot change the result.
+// them in order, so that timing cannot change the result.  Of many units each CTA takes one
+// after another.
 //
 // Warps: softmax and epilogue (four for each tile of rows), four that copy the cache
 // into shared memory (cp.async, 16 bytes a lane, so any page size, absent tokens as
@@ -187,10 +188,18 @@ __device__ __forceinline__ float2 q_unpack2(uint32_t u, bool bf16) {
 
 // The layer's buffers as TMA sees them, rows of elements of 2 bytes in boxes of 64 elements
 // (128 bytes) by `box` rows; box 0: not at all.
+// q, as [token, kv head, head of the group, element], in boxes of 64 elements by 128 rows of a
+// tile; q_boxes 0: not at all.
 struct QueryMaps {
-  CUtensorMap k, v;
-  int32_t box;
+  CUtensorMap k, v, q;
+  int32_t box, q_boxes;
 };
+__device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 
   // ---- the blocks before each sequence; thread i takes `per` sequences
   const int per = (p.B + THREADS - 1) / THREADS;
-  long long mine = 0;
+  long long mine = 0, units = 0;
   for (int x = 0; x < per; ++x) {
     const int b = tid * per + x;
     QueryPieces<C> t;
@@ -414,11 +423,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       if (lane == src) n = all;
     }
     mine += n * p.Hkv;
+    units += (long long)t.units * p.Hkv;
   }
-  long long total = 0;
+  long long total = 0, all_units = 0;
+  block_prefix<C::WARPS>(units, scratch, &all_units);
+  __syncthreads();
   const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total);
   // with fewer blocks than CTAs, only as many CTAs take part: each has one then
   const long long chunks = min((long long)gridDim.x, total);
+  // With many units to a CTA, whole units one after another (see the planner)
+  const bool whole_units = all_units >= kQueryWhole * (long long)gridDim.x;
   if (blockIdx.x < chunks) {
     const long long lo = total * int(blockIdx.x) / chunks;
     if (ahead <= lo && lo < ahead + mine) {       // one thread
@@ -434,7 +448,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       mbar_init(bar(READY + i), 1);
     }
     for (int i = 0; i < INFO; ++i) mbar_init(bar(KNOWN + i), 4);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), 4);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), maps.q_boxes > 0 ? 1 : 4);
     for (int i = 0; i < 3; ++i) {
       mbar_init(bar(SFULL + i), 1);
       for (int part = 0; part < 6; part += 3) {
@@ -621,19 +635,66 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (!ok) break;
       }
     } else if (warp == C::MMA_WARP + 2) {
-      // ---- the planner: the chunk's pieces, a few ahead of the other warps.  (With this in
+      // ---- the planner: this CTA's pieces, a few ahead of the other warps.  (With this in
       // every role the kernel was 200 KB, more than the instruction cache holds: whatever was
       // not the inner loop ran at 8 clocks an instruction and more.)
+      // Few units: the chunk's pieces.  Many: whole units, taken from a counter as they are
+      // needed, those of one kv head one after another, so that the CTAs read the same part of
+      // the cache at the same time, the longest first; which CTA has a unit does not change
+      // its result.
       QueryPieces<C> pc;
-      pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+      int base = 0;                               // the sequences of this and 31 more, one a lane
+      long long before = 0, upto = 0;             // units before them; this lane's and those before it
+      QuerySeq seq{0, 0, 0};
+      auto group = [&]() {
+        seq = base + lane < p.B ? query_seq(p, base + lane) : QuerySeq{0, 0, 0};
+        upto = (long long)query_units(seq.nq, p.G, C::ROWS) * p.Hkv;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+      };
+      auto claim = [&]() {                        // the next whole unit with something to attend to
+        for (;;) {
+          long long at = lane == 0 ? (long long)atomicAdd(p.next, 1u) : 0;
+          at = __shfl_sync(0xffffffffu, at, 0);
+          if (at >= all_units) return false;
+          for (;;) {
+            const long long here = __shfl_sync(0xffffffffu, upto, 31);
+            if (at < before + here) break;
+            before += here;
+            base += 32;
+            group();
+          }
+          const int src = __ffs(int(__ballot_sync(0xffffffffu, before + upto > at))) - 1;
+          pc.b = base + src;
+          pc.s.q0 = __shfl_sync(0xffffffffu, seq.q0, src);
+          pc.s.nq = __shfl_sync(0xffffffffu, seq.nq, src);
+          pc.s.kv = __shfl_sync(0xffffffffu, seq.kv, src);
+          pc.units = query_units(pc.s.nq, p.G, C::ROWS);
+          const int i = int(at - (before + __shfl_sync(0xffffffffu, upto, src) - (long long)pc.units * p.Hkv));
+          pc.h = i / pc.units;
+          pc.m = pc.units - 1 - (i - pc.h * pc.units);
+          pc.u = pc.unit(p, pc.m);
+          pc.x0 = 0;
+          pc.x1 = pc.u.blocks;
+          if (pc.x1 > 0) return true;
+        }
+      };
+      if (whole_units)
+        group();
+      else
+        pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+      const uint32_t ahead = whole_units ? 1 : kPieceRing;   // a unit is taken when the one before it is begun
       bool more = true;
       for (uint32_t i = 0; more; ++i) {
-        more = __any_sync(0xffffffffu, pc.next(p)) != 0;
         const uint32_t slot = i % kPieceRing;
-        if (i >= kPieceRing) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + slot), (i / kPieceRing - 1u) & 1u, &gave_up));
+        if (i >= ahead) {
+          const uint32_t last = i - ahead;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + last % kPieceRing), (last / kPieceRing) & 1u, &gave_up));
           if (!ok) break;
         }
+        more = __any_sync(0xffffffffu, whole_units ? claim() : pc.next(p)) != 0;
         if (lane == 0) {
           QueryPiece x{};
           if (more) {
@@ -833,59 +894,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         blk += uint32_t(pc.n);
       }
     };
-    // Between global and shared memory a warp moves its 32 rows of Q, and of the result, by
-    // 16 bytes a lane: LPR lanes a row, RPI rows at a time.  A warp alone on its scheduler
-    // takes 4 to 5 clocks an instruction, so what counts here is their number: each lane
-    // works out where its own row lies, and the others ask it.
-    constexpr int LPR = C::DP / 8, RPI = 32 / LPR, QI = 32 / RPI;
-    const int qc = lane % LPR, qr = lane / LPR;
-    unsigned char *const q_w = q_p + tile * C::QTILE_B + w0 * 128;   // this warp's part of Q's tile
-    // in it, elements 8 qc on of row i * RPI + qr (whose swizzle is that of qr and of i * RPI)
-    unsigned char *const q_mine = q_w + (qc >> 3) * C::QATOM_B + qr * 128;
-    auto slot = [&](int i) { return q_mine + i * RPI * 128 + ((((qc & 7) ^ qr) ^ (i * RPI & 7)) << 4); };
-    auto ask = [&](int64_t x, int i) { return __shfl_sync(0xffffffffu, (long long)x, i * RPI + qr); };
     bool more = false, live = false;
-    int64_t out_at = -1, out32_at = 0;            // where this thread's row lies in out, in lse; -1: nowhere
-    int64_t lse_at = 0;
+    int64_t out_at = 0, out32_at = 0, lse_at = 0; // where this thread's row lies in out, out32 and lse2, lse
     int lo = 0, hi = 0;                           // the tokens it sees
-    uint4 qv[QI];
-    // the row's places, and Q on its way
-    auto load_q = [&]() {
+    uint32_t asked = 0;                           // tiles of Q by TMA
+    // The next piece's row, and its Q into shared memory (the products that read the one
+    // before it are done: their scores were there).  Returns the scores' factor.
+    auto begin = [&]() {
       live = more && row < pc.rows;
-      int64_t own = -1;
-      lo = hi = 0;
-      out_at = -1;
+      float mul = 0.f;
+      int64_t q_at = -1;
+      lo = 0, hi = INT32_MAX;                     // of no row: nothing to mask, and 0 times its scores
       if (live) {
         const QueryRow x = query_row(p, pc.q0, pc.h, pc.row0 + row);
-        own = x.token * p.q_st + int64_t(x.head) * p.q_sh;
+        q_at = x.token * p.q_st + int64_t(x.head) * p.q_sh;
         out_at = x.token * p.o_st + int64_t(x.head) * p.o_sh;
         out32_at = x.token * p.Hq + x.head;
         lse_at = x.token * p.lse_st + x.head;
         query_sees(x.i, pc.nq, pc.kv, p.causal, p.window, &lo, &hi);
+        mul = p.scale2;
       }
-      const char *const src = static_cast<const char *>(p.q) + qc * 16;
-#pragma unroll
+      if (!more) return mul;
+      if (maps.q_boxes > 0) {
+        if (r == 0) {
+          mbar_expect(bar(QFULL + tile), uint32_t(maps.q_boxes) * C::QATOM_B);
+          const int token = pc.q0 + (pc.row0 + tile * kQueryRows) / p.G;
+          for (int a = 0; a < maps.q_boxes; ++a)
+            tma_box4(q_s + tile * C::QTILE_B + a * C::QATOM_B, &maps.q, a * 64, 0, pc.h, token, bar(QFULL + tile));
+        }
+        ++asked;
+        __syncwarp();
+        return mul;
+      }
+      // row by row, LPR lanes each: every lane knows where its own lies, and the others ask it
+      constexpr int LPR = C::DP / 8, RPI = 32 / LPR, QI = 32 / RPI;
+      const int qc = lane % LPR, qr = lane / LPR;
+#pragma unroll 4
       for (int i = 0; i < QI; ++i) {
-        const int64_t at = ask(own, i);
-        qv[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0 && qc * 8 < p.D) qv[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * at));
-      }
-    };
-    // Q into shared memory (the products that read the one before it are done: their scores
-    // were there); returns the scores' factor of this thread's row
-    auto store_q = [&]() {
-      float mul = p.scale2;
-      if (C::TYPE == kQE4m3 && p.bf16) {
-        // fp16, after the power of two that brings the row's largest element into [1, 2):
-        // queries keep every bit down to 2^-14 of it, and below that are off by 2^-25 of it
-        // at most
-#pragma unroll
-        for (int i = 0; i < QI; ++i) {
-          uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        const int rr = i * RPI + qr;
+        const int64_t at = __shfl_sync(0xffffffffu, (long long)q_at, rr);
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0 && qc * 8 < p.D) w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(p.q) + 2 * at + qc * 16));
+        if (C::TYPE == kQE4m3 && p.bf16) {
+          // fp16, after the power of two that brings the row's largest element into [1, 2):
+          // queries keep every bit down to 2^-14 of it, and below that are off by 2^-25 of
+          // it at most
           float top = 0.f;
+          uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = q_unpack2(w[y], true);
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = q_unpack2(y[k], true);
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
 #pragma unroll
@@ -893,34 +951,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           const int ex = top < INFINITY ? max(-120, min(120, (__float_as_int(top) >> 23) - 127)) : 0;
           const float down = __int_as_float((127 - ex) << 23);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = q_unpack2(w[y], true);
-            w[y] = pack2<false>(f.x * down, f.y * down);
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = q_unpack2(y[k], true);
+            y[k] = pack2<false>(f.x * down, f.y * down);
           }
-          qv[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          w = make_uint4(y[0], y[1], y[2], y[3]);
           const int mine = __shfl_sync(0xffffffffu, ex, lane % RPI * LPR);
-          if (i == lane / RPI) mul = p.scale2 * __int_as_float((127 + mine) << 23);
+          if (i == lane / RPI) mul *= __int_as_float((127 + mine) << 23);
         }
+        if (qc * 8 < d16)
+          *reinterpret_cast<uint4 *>(q_p + tile * C::QTILE_B + (qc >> 3) * C::QATOM_B + (w0 + rr) * 128 + (((qc & 7) ^ (rr & 7)) << 4)) = w;
       }
-#pragma unroll
-      for (int i = 0; i < QI; ++i)
-        if (qc * 8 < d16) *reinterpret_cast<uint4 *>(slot(i)) = qv[i];
       proxy_fence();
       __syncwarp();
-      if (more && lane == 0) mbar_arrive(bar(QFULL + tile));
+      if (lane == 0) mbar_arrive(bar(QFULL + tile));
       return mul;
     };
     // One pass per piece, the first for the first piece's Q alone: the code is here once.
-    // (qv lives within a pass only; behind a branch the compiler would keep it through all blocks.)
     bool any = false, dual = false, begins = false, whole = false;
     int n = 0, t_first = 0;
-    float mul = 0.f, m = -INFINITY, l = 0.f;
+    float mul = 0.f, m = 0.f, l = 0.f;
     for (;;) {
       // where block j's scores are, and how often its lane was used before
       auto way = [&](int j) { return dual ? tile : 2 * (j & 1); };
       auto turn = [&](int j) { return dual ? used0 + uint32_t(j) : ((j & 1) ? used2 : used0) + (uint32_t(j) >> 1); };
       m = live ? -INFINITY : 0.f, l = 0.f;
-      float mu = 0.f;
+      float mu = live ? 0.f : 1000.f;             // (no row: exponentials of 0)
       bool unset = true;                          // a row of the warp has no reference yet
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++blk) {
@@ -1032,27 +1088,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (!ok) break;
       }
       if (!ok) break;
-      // ---- the piece's end; the next one's Q is on its way meanwhile
+      // ---- the piece's end; the next one's first products run meanwhile
       const int last_way = way(n - 1);
       const uint32_t last_turn = turn(n - 1);
       used0 += dual ? uint32_t(n) : uint32_t(n + 1) >> 1;
       used2 += dual ? 0u : uint32_t(n) >> 1;
-      const bool was_live = live;
+      const bool was_live = live, was_any = any;
       const int64_t was_out = out_at, was_out32 = out32_at, was_lse = lse_at;
       more = next();
-      load_q();
+      mul = begin();
       if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 3 * PARTS - 3 + last_way), last_turn & 1u, &gave_up));
       if (!ok) break;
-      if (any) {
+      if (was_any) {
         tc_fence_after();
         // a row that saw nothing is 0, whatever 0 times V was
-        const bool none = whole && __any_sync(0xffffffffu, l == 0.f);
+        const bool none = whole && __any_sync(0xffffffffu, was_live && l == 0.f);
         const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
         const uint64_t f2 = f32x2(f, f);
-        const bool direct = whole && !p.out32;
         float *part = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + tile * C::DP * kQueryRows + r;
-        float *row32 = p.out32 + was_out32 * p.D;
-        unsigned char *const mine = q_w + lane * 128;
+        float *const row32 = p.out32 + was_out32 * p.D;
+        char *const row16 = static_cast<char *>(p.out) + 2 * was_out;
 #pragma unroll 1
         for (int c = 0; c < d16; c += 32) {
           float o[32];
@@ -1065,39 +1120,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
           }
-          if (direct) {                           // by way of Q's place, so that lanes write rows together
-            unsigned char *const to = mine + (c >> 6) * C::QATOM_B;
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4 *>(to + ((((c & 32) + i) * 2) ^ ((lane & 7) << 4))) = query_pack8<C>(p, o + i);
-          } else if (whole) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              if (was_live && c + i < p.D) *reinterpret_cast<float4 *>(row32 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-          } else if (was_live) {
+          if (!was_live) continue;
+          if (!whole) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) __stcg(part + i * kQueryRows, o[i]);
             part += 32 * kQueryRows;
+          } else if (p.out32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              if (c + i < p.D) *reinterpret_cast<float4 *>(row32 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              if (c + i < p.D) *reinterpret_cast<uint4 *>(row16 + 2 * (c + i)) = query_pack8<C>(p, o + i);
           }
         }
         tc_fence_before();
-        if (direct) {
-          __syncwarp();
-          char *const to = static_cast<char *>(p.out) + qc * 16;
-          constexpr int AT_ONCE = QI < 16 ? QI : 16;
-#pragma unroll 1
-          for (int i0 = 0; i0 < QI; i0 += AT_ONCE) {
-            uint4 w[AT_ONCE];
-#pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i) w[i] = *reinterpret_cast<const uint4 *>(slot(i0 + i));
-#pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i) {
-              const int64_t at = ask(was_out, i0 + i);
-              if (at >= 0 && qc * 8 < p.D) *reinterpret_cast<uint4 *>(to + 2 * at) = w[i];
-            }
-          }
-          __syncwarp();
-        }
         if (was_live && whole) {
           const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
           if (p.lse2) p.lse2[was_out32] = lse2;
@@ -1108,7 +1146,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           __stcg(ml + C::ROWS, l);
         }
       }
-      mul = store_q();
       if (!more) break;
       dual = pc.flags & kTwoTiles;
       begins = pc.flags & kBegins;
@@ -1117,6 +1154,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       t_first = pc.t0;
       any = __any_sync(0xffffffffu, live);        // of a warp without rows, nothing is looked at
     }
+    // after a wait that ran out, a tile of Q may be on its way still
+    if (!ok && asked > 0 && r == 0) mbar_wait<true>(bar(QFULL + tile), (asked - 1u) & 1u, &gave_up);
     tc_fence_before();
   }
   __syncthreads();
@@ -1141,6 +1180,7 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int ROWS = QT * kQueryRows, PIECE = ROWS * DP + 2 * ROWS, BN = DP <= 128 ? 128 : 64;
   const int chunk = int(blockIdx.x), col = int(blockIdx.y) * 8;
+  if (chunk == 0 && col == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next = 0u;   // ready for the next call
   if (col >= p.D) return;
   const int4 at = __ldcg(p.open + chunk);
   if (!query_open(chunk, at.w, int(gridDim.x)) || at.x < 0 || at.x >= p.B || at.y < 0 || at.y >= p.Hkv || at.z < 0) return;
@@ -1218,20 +1258,34 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_call() {
   return call;
 }
 
-// Describes the layer's buffers to TMA where its boxes fit: pages of whole boxes of 16 rows
+// Describes q and the layer's buffers to TMA where its boxes fit: pages of whole boxes of 16 rows
 // or more (with fewer, rows copied by threads are as fast), heads that the products'
 // steps of 16 cover (what a box holds behind the head is not used), rows within a
 // coordinate.  Else, or where the driver will not, the copies go row by row.
-inline void query_maps(const QueryParams &p, int block, QueryMaps *m) {
-  m->box = 0;
+inline void query_maps(const QueryParams &p, int block, bool cache, QueryMaps *m) {
+  const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const PFN_cuTensorMapEncodeTiled_v12000 call = tensor_map_call();
+  m->box = m->q_boxes = 0;
+  if (!call) return;
+  // Q: groups that fill a tile's rows, queries that the products take as they are.  (A
+  // dimension of one has a stride that nothing uses.)
+  if (kQueryRows % p.G == 0 && !(p.e4m3 && p.bf16)) {
+    const int64_t sh = p.Hq > 1 ? p.q_sh : p.D, st = p.N > 1 ? p.q_st : int64_t(p.Hq) * sh;
+    const cuuint64_t dims[4] = {cuuint64_t(p.D), cuuint64_t(p.G), cuuint64_t(p.Hkv), cuuint64_t(p.N)};
+    const cuuint64_t strides[3] = {cuuint64_t(sh) * 2, cuuint64_t(sh) * 2 * p.G, cuuint64_t(st) * 2};
+    const cuuint32_t sizes[4] = {64, cuuint32_t(p.G), 1, cuuint32_t(kQueryRows / p.G)}, steps[4] = {1, 1, 1, 1};
+    if (sh > 0 && st > 0 &&
+        call(&m->q, type, 4, const_cast<void *>(p.q), dims, strides, sizes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS)
+      m->q_boxes = (p.D + 63) / 64;
+  }
+  if (!cache) return;
   int box = 1;
   while (box < 64 && p.P % (2 * box) == 0) box *= 2;
   const int64_t rows = p.num_pages * p.P;
-  const PFN_cuTensorMapEncodeTiled_v12000 call = tensor_map_call();
-  if (!call || box < 16 || p.D % 16 || rows >= INT32_MAX) return;
+  if (box < 16 || p.D % 16 || rows >= INT32_MAX) return;
   const cuuint64_t dims[2] = {cuuint64_t(p.row), cuuint64_t(rows)}, strides[1] = {cuuint64_t(p.row) * 2};
   const cuuint32_t sizes[2] = {64, cuuint32_t(box < block ? box : block)}, steps[2] = {1, 1};
-  const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   for (int i = 0; i < 2; ++i)
     if (call(i ? &m->v : &m->k, type, 2, const_cast<void *>(i ? p.v : p.k), dims, strides, sizes, steps,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1252,7 +1306,7 @@ int launch_query_as(const QueryParams &p, int device, cudaStream_t st, int *laun
     if (device < kQueryDevices) ready[device].store(true, std::memory_order_release);
   }
   QueryMaps maps{};
-  if (C::TYPE != kQE4m3) query_maps(p, C::BN, &maps);
+  query_maps(p, C::BN, C::TYPE != kQE4m3, &maps);
   int e = query_launch(query_kernel<C>, dim3(kQueryCtas), C::THREADS, st, C::SMEM, p, maps);
   if (e) return e;
   ++*launches;

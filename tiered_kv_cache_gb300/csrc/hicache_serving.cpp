@@ -176,8 +176,9 @@ int query_sizes(const Shape &s, int64_t batch, int64_t tokens, int64_t q_heads, 
 
 // Places the workspace of a query kernel at `at`; its error word is the call's.
 void query_place(char *at, void *error, hicache::QueryParams *p) {
-  const hicache::QuerySpace sp = hicache::query_space(p->D, 1);
+  const hicache::QuerySpace sp = hicache::query_space(p->D);
   p->error = static_cast<unsigned int *>(error) + hicache::kDecodeCtas;
+  p->next = reinterpret_cast<unsigned int *>(at + sp.next);
   p->open = reinterpret_cast<int4 *>(at + sp.open);
   p->parts = reinterpret_cast<float *>(at + sp.parts);
 }
@@ -226,7 +227,7 @@ PrefixSpace prefix_space(const hicache::DecodeParams &d) {
   s.prior = up(hicache::decode_space(d, false).bytes);
   s.prior_lse2 = up(s.prior + int64_t(d.B) * d.Hq * d.D * 4);
   s.query = up(s.prior_lse2 + int64_t(d.B) * d.Hq * 4);
-  s.bytes = s.query + hicache::query_space(d.D, 1).bytes;
+  s.bytes = s.query + hicache::query_space(d.D).bytes;
   return s;
 }
 
@@ -455,7 +456,7 @@ int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_
   if (!bytes) return set_error(HICACHE_ERR_INVALID_ARG, "bytes is NULL");
   hicache::QueryParams p{};
   if ((rc = query_sizes(s, batch, num_tokens, q_heads, head_dim, max_pages, &p))) return rc;
-  *bytes = hicache::query_space(p.D, 1).bytes;
+  *bytes = hicache::query_space(p.D).bytes;
   return HICACHE_OK;
 }
 
@@ -487,7 +488,7 @@ int hicache_query_attention(const hicache_device_kv *kv, const hicache_pool_desc
   if ((rc = check_ints({a->q_starts, a->page_table, a->kv_lens}, "q_starts, page_table or kv_lens"))) return rc;
   if (!stride_ok(p.t_sb)) return set_error(HICACHE_ERR_INVALID_ARG, "table_stride must be in [0, 2^40)");
   if ((rc = check_lse(a->lse, p.lse_st, a->num_tokens, a->q_heads))) return rc;
-  if ((rc = check_workspace(a->workspace, a->workspace_bytes, hicache::query_space(p.D, 1).bytes))) return rc;
+  if ((rc = check_workspace(a->workspace, a->workspace_bytes, hicache::query_space(p.D).bytes))) return rc;
   p.q = a->q;
   p.k = k;
   p.v = v;

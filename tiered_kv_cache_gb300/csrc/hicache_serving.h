@@ -103,6 +103,7 @@ struct QueryParams {
   int64_t num_pages;          // device pages
   // workspace
   unsigned int *error;        // set by a call that gave up waiting
+  unsigned int *next;         // the next whole unit; zero between calls
   int4 *open;                 // per chunk of work: the unit that begins in it and goes on, and in how many chunks it lies
   float *parts;               // two per chunk
   int32_t B, N, Hq, Hkv, G, D, P, max_pages, window, causal;
@@ -118,11 +119,12 @@ HC_HD int query_tiles(int D) { return D <= 128 ? 2 : 1; }
 HC_HD int query_block(int D) { return D <= 128 ? 128 : 64; }
 HC_HD int query_cols(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 constexpr int kQueryCtas = 152;                   // one on each of a GB300's SMs
-constexpr int kQueryPhases = 8;                   // chunks of work for each of them, at most
+// From so many units for each of them on, CTAs take whole units.
+constexpr int kQueryWhole = 4;
 struct QuerySpace {
-  int64_t open, parts, bytes;
+  int64_t next, open, parts, bytes;
 };
-QuerySpace query_space(int D, int phases);
+QuerySpace query_space(int D);
 int launch_query(const QueryParams &p, int device, void *stream, int *launches);
 
 // A unit of work: rows [row0, row0 + rows) of a sequence's nq * G query rows, over
