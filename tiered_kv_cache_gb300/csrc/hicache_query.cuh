@@ -223,6 +223,12 @@ __device__ __forceinline__ QuerySeq query_seq(const QueryParams &p, int b) {
   return s;
 }
 
+// a / b of what is not negative, in 32 bits where they fit: a division of 64 takes 400 clocks
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
+}
+
 // The pieces of a chunk, in order.
 template <class C>
 struct QueryPieces {
@@ -266,12 +272,12 @@ struct QueryPieces {
       if (rest < n * p.Hkv || b + 1 >= p.B) break;
       rest -= n * p.Hkv;
     }
-    h = n > 0 ? int(rest / n) : 0;
+    h = n > 0 ? int(quotient(rest, n)) : 0;
     rest -= h * n;
     m = 0;
     if (!p.causal) {
       const int each = unit(p, 0).blocks;
-      m = each > 0 ? int(rest / each) : 0;
+      m = each > 0 ? int(quotient(rest, each)) : 0;
       rest -= (long long)m * each;
     } else {
       for (;; m += 32) {           // 32 units at a time
@@ -370,7 +376,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_constant__ QueryParams p, const __grid_constant__ QueryMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = 8, PARTS = BN / 64;
-  __shared__ long long scratch[C::WARPS];
+  __shared__ long long scratch[C::WARPS], units_of[C::WARPS];
   __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
   __shared__ int first_seq;
   __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 19 + 2 * kPieceRing];
@@ -403,6 +409,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   // ---- the blocks before each sequence; thread i takes `per` sequences
   const int per = (p.B + THREADS - 1) / THREADS;
   long long mine = 0, units = 0;
+  bool zero = false;                              // a sequence has rows that no unit holds
   for (int x = 0; x < per; ++x) {
     const int b = tid * per + x;
     QueryPieces<C> t;
@@ -424,17 +431,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     }
     mine += n * p.Hkv;
     units += (long long)t.units * p.Hkv;
+    zero |= t.s.nq > 0 && (t.s.kv == 0 || (p.causal && t.s.nq > t.s.kv));
   }
   long long total = 0, all_units = 0;
-  block_prefix<C::WARPS>(units, scratch, &all_units);
-  __syncthreads();
+  const bool zeros = __syncthreads_or(zero);
+  for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+  if (lane == 0) units_of[warp] = units;          // read behind block_prefix's barrier
   const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total);
+  for (int w = 0; w < C::WARPS; ++w) all_units += units_of[w];
   // with fewer blocks than CTAs, only as many CTAs take part: each has one then
   const long long chunks = min((long long)gridDim.x, total);
   // With many units to a CTA, whole units one after another (see the planner)
   const bool whole_units = all_units >= kQueryWhole * (long long)gridDim.x;
   if (blockIdx.x < chunks) {
-    const long long lo = total * int(blockIdx.x) / chunks;
+    const long long lo = quotient(total * int(blockIdx.x), chunks);
     if (ahead <= lo && lo < ahead + mine) {       // one thread
       first_seq = tid * per;
       first_rest = lo - ahead;
@@ -467,7 +477,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   }
   // rows of which there is nothing to attend to and that no unit holds: of sequences
   // without tokens, and of queries before the first token
-  for (int b = int(blockIdx.x); b < p.B; b += int(gridDim.x)) {
+  for (int b = int(blockIdx.x); zeros && b < p.B; b += int(gridDim.x)) {
     const QuerySeq s = query_seq(p, b);
     int rows = s.nq * p.G;
     if (s.kv > 0) rows = p.causal ? max(0, min(s.nq, s.nq - s.kv)) * p.G / C::ROWS * C::ROWS : 0;
@@ -684,7 +694,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       if (whole_units)
         group();
       else
-        pc.start(p, total * int(blockIdx.x) / chunks, total * (int(blockIdx.x) + 1) / chunks, first_seq, first_rest);
+        pc.start(p, quotient(total * int(blockIdx.x), chunks), quotient(total * (int(blockIdx.x) + 1), chunks), first_seq, first_rest);
       const uint32_t ahead = whole_units ? 1 : kPieceRing;   // a unit is taken when the one before it is begun
       bool more = true;
       for (uint32_t i = 0; more; ++i) {
@@ -716,7 +726,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             if (begins && !whole) {
               // the chunks that the unit lies in
               const long long first = pc.pos - pc.x1;
-              const int last = int(((first + pc.u.blocks) * chunks - 1) / total);
+              const int last = int(quotient((first + pc.u.blocks) * chunks - 1, total));
               p.open[blockIdx.x] = make_int4(pc.b, pc.h, pc.m, last - int(blockIdx.x) + 1);
             }
           }
@@ -730,8 +740,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     set_registers<C::COPY_REGS, false>();
     // ---- copies
     const int pt = tid - C::COPY_WARP * 32;
-    // boxes: lane i of the first warp takes rows from box_r on, 64 elements from box_c on
+    // boxes: lane i takes rows from box_r on, 64 elements from box_c on.  A block's take a
+    // warp 2,500 clocks, so three take turns.  (No more: each waits for the stages of its own
+    // blocks only, and with 5 stages a fourth's could be two phases behind.)
     const int columns = (p.D + 63) >> 6, box_r = lane / columns * maps.box, box_c = lane % columns * 64;
+    const int boxes_all = maps.box > 0 ? BN / maps.box * columns : 0;
     int stage = 0, phase = 1;
     uint32_t blk = 0, turns = 0;
     auto advance = [&]() {
@@ -752,22 +765,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
         }
       };
-      // Whole boxes, present or not (one that is not lies behind the rows and reads as
-      // zeros), are the first warp's; a block in which the range of tokens cuts a box is
-      // copied row by row by all four.
+      // Whole boxes come by TMA, present or not (one that is not lies behind the rows and
+      // reads as zeros); a block in which the range of tokens cuts a box, row by row.
       auto boxes = [&](int t0) {
         return C::TYPE != kQE4m3 && maps.box > 0 && (max(pc.lo - t0, 0) & (maps.box - 1)) == 0 &&
                (min(pc.hi - t0, BN) & (maps.box - 1)) == 0;
       };
       bool boxed = boxes(pc.t0);
-      lookup(pc.t0 + (boxed ? box_r : pt));
+      if (!boxed) lookup(pc.t0 + pt);
       for (int x = 0; ok && x < pc.n; ++x, ++blk) {
         const int t0 = pc.t0 + x * BN;
         const bool next_boxed = boxes(t0 + BN);
-        const int next_t = t0 + BN + (next_boxed ? box_r : pt);
         if (boxed) {
-          if (pt < 32) {
-            const bool have = box_r < BN && page_present(page, p.num_pages);
+          if (blk % 3u == uint32_t(pt >> 5)) {
+            lookup(t0 + box_r);
+            const bool have = lane < boxes_all && page_present(page, p.num_pages);
             const int y = have ? int(int64_t(page) * p.P + (t0 + box_r - pg * p.P)) : int(p.num_pages * p.P);
             const uint32_t bits = __ballot_sync(0xffffffffu, have);
             if (lane < WORDS) {                   // tokens lane * 32 on
@@ -778,7 +790,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(KNOWN + blk % INFO), 4);
-            if (x + 1 < pc.n) lookup(next_t);
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv) {
               if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
@@ -786,21 +797,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               if (lane == 0) mbar_expect(bar(FULL + stage), uint32_t(columns) * C::ATOM_B);
               if (lane == 1) mbar_arrive(bar(FULL + stage), 127);
               __syncwarp();
-              if (box_r < BN)
+              if (lane < boxes_all)
                 tma_box(ring_s + stage * C::TILE_B + (box_c >> 6) * C::ATOM_B + box_r * 128, kv ? &maps.v : &maps.k,
                         pc.h * p.D + box_c, y, bar(FULL + stage));
               advance();
             }
           } else {
-            if (x + 1 < pc.n && !next_boxed) lookup(next_t);
             advance();
             advance();
           }
           boxed = next_boxed;
+          if (!boxed && x + 1 < pc.n) lookup(t0 + BN + pt);
           continue;
         }
-        // the other three warps pass over whole boxes: they wait here for the first, whose
-        // blocks before this one still use the barriers and the words
+        // among boxes the warps are not together: none may still read the places of two blocks ago
         if (maps.box > 0) together();
         if (!ok) break;
         const bool have = pt < BN && page_present(page, p.num_pages);
@@ -812,8 +822,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           mbar_arrive(bar(KNOWN + blk % INFO));
         }
         together();
-        if (x + 1 < pc.n) lookup(next_t);
         boxed = next_boxed;
+        if (!boxed && x + 1 < pc.n) lookup(t0 + BN + pt);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
