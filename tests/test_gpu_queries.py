@@ -195,6 +195,40 @@ def test_query_long(hq, hk, d, dtype, e4, causal, window):
     check_query(cache, q, q_lens, out, lse, causal, window, pick=[0, 1, 63, 64, 127, 128, 700, 1023, 1499])
 
 
+@pytest.mark.parametrize("hq,hk,d,P,dtype,e4", [
+    (8, 8, 128, 16, "bf16", False), (16, 8, 64, 64, "fp16", False), (24, 8, 128, 5, "bf16", False),
+    (8, 8, 64, 16, "bf16", True), (8, 4, 256, 32, "fp16", False), (8, 8, 128, 16, "fp16", True),
+    (16, 8, 80, 128, "bf16", False)])
+def test_query_few_rows_many_blocks(hq, hk, d, P, dtype, e4):
+    """Units of one tile of rows, long enough that a chunk has many of their blocks, and of
+    lengths that end within a box of rows."""
+    kv_lens, q_lens = [9001, 17, 20000, 4100, 128], [1, 3, 5, 20, 2]
+    cache = Cache([kv_lens], hk, d, P, dtype, e4, seed=8)
+    q = queries(sum(q_lens), hq, d, dtype)
+    for causal in (False, True):
+        out, lse = run_query(cache, q, q_lens, kv_lens, causal)
+        check_query(cache, q, q_lens, out, lse, causal, pick=[0, 4, 19])
+
+
+@pytest.mark.parametrize("hq,hk,d,P,causal,dtype", [
+    (4, 4, 64, 16, False, "bf16"), (6, 2, 128, 64, True, "fp16"), (16, 16, 128, 16, False, "bf16")])
+def test_query_many_units(hq, hk, d, P, causal, dtype):
+    """Whole units from the counter: more sequences than a warp has lanes, some without
+    queries, some without tokens; the counter is back at zero for the next call."""
+    rnd = random.Random(3)
+    kv_lens = [rnd.choice((0, 1, 50, 128, 300, 513)) for _ in range(150)]
+    q_lens = [rnd.choice((0, 1, 7, 40, 300)) for _ in range(150)]
+    if causal:
+        kv_lens = [max(k, n) if k else 0 for k, n in zip(kv_lens, q_lens)]
+    cache = Cache([kv_lens], hk, d, P, dtype, seed=9)
+    q = queries(sum(q_lens), hq, d, dtype)
+    ws = workspace(hc.query_workspace(cache.desc, len(q_lens), q.shape[0], hq, d, cache.tables[0].shape[1]))
+    out, lse = run_query(cache, q, q_lens, kv_lens, causal, ws=ws)
+    check_query(cache, q, q_lens, out, lse, causal, pick=[0, 6, 150])
+    again, lse2 = run_query(cache, q, q_lens, kv_lens, causal, ws=ws)
+    assert torch.equal(raw(out), raw(again)) and torch.equal(raw(lse), raw(lse2))
+
+
 PREFIX = [
     # members, prefix_lens, own_lens of all, hq, hk, d, P, dtype, e4m3
     ([1], [1], [0], 1, 1, 64, 16, "bf16", False),

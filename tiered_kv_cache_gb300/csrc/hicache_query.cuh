@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   __shared__ long long scratch[C::WARPS], units_of[C::WARPS];
   __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
   __shared__ int first_seq;
-  __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 19 + 2 * kPieceRing];
+  __shared__ __align__(8) unsigned long long bars[3 * C::STAGES + INFO + 16 + 2 * kPieceRing];
   __shared__ int64_t offs[2][BN];                 // the rows a block's tokens lie in; -1: absent
   __shared__ uint32_t there[INFO][WORDS];         // which of them are present
   __shared__ QueryPiece ring_of_pieces[kPieceRing];
@@ -394,13 +394,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   // A stage is full, its copies are visible to the products, it is empty; what of a block
   // is present; Q of a tile is there; a lane's scores, exponentials are there, their product with V
   // is done; the last product; the copying warps are together; a piece is there, is read.
-  // A lane is a score buffer with the warps that take it: 0 and 1 the two tiles of a unit,
-  // 0 and 2 the buffers that one tile fills in turn.  The second tile's warps sit units of one
-  // tile out, so no barrier that they wait on may count there: a phase's parity would pass
-  // for that of a phase two on.
+  // A lane is a score buffer, of a tile of rows, or, in a unit with one tile, of every other
+  // block: the two sets of softmax warps share its blocks then, each with sums of its own,
+  // which the first set adds up when the second has put its (OTHER) and until when it leaves
+  // them (ADDED).
   constexpr int FULL = 0, EMPTY = C::STAGES, READY = 2 * C::STAGES, KNOWN = 3 * C::STAGES, QFULL = KNOWN + INFO,
-                SFULL = QFULL + 2, PFULL = SFULL + 3, PVDONE = PFULL + 6, LAST = PVDONE + 6, GROUP = LAST + 1,
-                PIECE = GROUP + 1, TAKEN = PIECE + kPieceRing;   // PFULL, PVDONE: + 3 for a block's second half
+                SFULL = QFULL + 2, PFULL = SFULL + 2, PVDONE = PFULL + 4, LAST = PVDONE + 4, GROUP = LAST + 1,
+                OTHER = GROUP + 1, ADDED = OTHER + 1, PIECE = ADDED + 1,
+                TAKEN = PIECE + kPieceRing;       // PFULL, PVDONE: + 2 for a block's second half
   // rows that cp.async brings tile after tile: a warp makes them visible to the products
   const bool relayed = C::TYPE != kQE4m3 && maps.box == 0;
 
@@ -459,9 +460,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     }
     for (int i = 0; i < INFO; ++i) mbar_init(bar(KNOWN + i), 4);
     for (int i = 0; i < 2; ++i) mbar_init(bar(QFULL + i), maps.q_boxes > 0 ? 1 : 4);
-    for (int i = 0; i < 3; ++i) {
+    mbar_init(bar(OTHER), 4);
+    mbar_init(bar(ADDED), 4);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(SFULL + i), 1);
-      for (int part = 0; part < 6; part += 3) {
+      for (int part = 0; part < 4; part += 2) {
         mbar_init(bar(PFULL + part + i), 4);
         mbar_init(bar(PVDONE + part + i), 1);
       }
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       const int ksteps = d16 / 16;
       const uint32_t one = elected();             // all products and commits are this lane's
       int kst = 0, kph = 0, vst = 1, vph = 0;     // stage and phase of the next block's K, V
-      uint32_t used0 = 0, used1 = 0, used2 = 0, duals = 0, pieces = 0;
+      uint32_t used0 = 0, used1 = 0, duals = 0, pieces = 0;
       auto wait = [&](int b, uint32_t parity) {
         ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, &gave_up));
       };
@@ -550,9 +553,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         uint32_t k_at = 0, v_at = 0;              // of the block's K, V
         // PV(s), QK(s + 2) with score buffer x
         auto step = [&](int s, int x) {
-          const int way = dual ? x : 2 * x;       // the lane
           const bool last_of_tile = !dual || x == 1, more = s + 2 < steps;
-          const uint32_t s_at = tmem + x * BN, o_at = tmem + C::O_COL + (dual ? x : 0) * C::DP;
+          const uint32_t s_at = tmem + x * BN, o_at = tmem + C::O_COL + (C::QT == 2 ? x : 0) * C::DP;
           // what two tiles share is waited for ahead of the exponentials, so that PV(s) and
           // QK(s + 2) follow one another without a pause
           if (!dual || x == 0) {
@@ -566,17 +568,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             }
           }
           if (s >= 0) {
-            const uint32_t turn = (way == 0 ? used0 : way == 1 ? used1 : used2) + uint32_t(s >> 1);
-            const uint32_t add = s >= (dual ? 2 : 1);
+            const uint32_t turn = (x == 0 ? used0 : used1) + uint32_t(s >> 1);
+            const uint32_t add = s >= C::QT;
 #pragma unroll
             for (int part = 0; part < PARTS; ++part) {
-              if (ok) wait(PFULL + 3 * part + way, turn);
+              if (ok) wait(PFULL + 2 * part + x, turn);
               if (!ok) return;
               tc_fence_after();
 #pragma unroll
               for (int i = 4 * part; i < 4 * part + 4; ++i)
                 tc_mma_ta(one, o_at, s_at + i * 8, v_at + i * (2048 >> 4), o_desc, i > 0 ? 1u : add);
-              tc_commit_in(one, bar(PVDONE + 3 * part + way));
+              tc_commit_in(one, bar(PVDONE + 2 * part + x));
             }
             if (last_of_tile) {
               tc_commit_in(one, bar(EMPTY + vst));
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll 1
             for (int i = 0; i < ksteps; ++i) product(i);
           }
-          tc_commit_in(one, bar(SFULL + way));
+          tc_commit_in(one, bar(SFULL + x));
           if (last_of_tile) {
             tc_commit_in(one, bar(EMPTY + kst));
             if ((kst += 2) >= C::STAGES) kst -= C::STAGES, kph ^= 1;
@@ -624,7 +626,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         }
         if (!ok) break;
         used0 += uint32_t(steps + 1) >> 1;
-        (dual ? used1 : used2) += uint32_t(steps) >> 1;
+        used1 += uint32_t(steps) >> 1;
       }
       tc_commit_in(one, bar(LAST));
       __syncwarp();
@@ -891,19 +893,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   } else {
     set_registers<C::SOFT_REGS, true>();
     // ---- softmax: a thread per row
-    const int tile = warp >> 2, r = tid & 127, w0 = (warp & 3) * 32, row = tile * kQueryRows + r;
+    const int tile = warp >> 2, r = tid & 127, w0 = (warp & 3) * 32;
     const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t o_at = tmem + C::O_COL + tile * C::DP + lanes;
-    uint32_t used0 = 0, used2 = 0, blk = 0;       // of this tile's lane, of lane 2
+    uint32_t used0 = 0, used1 = 0, blk = 0;       // uses of this set's lane (of one set: of both); blocks before the piece
+    uint32_t shares = 0;                          // pieces whose blocks the sets shared
+    int row = 0;
     QueryPiece pc;
-    // this tile's next piece: units of one tile of rows are the first tile's
-    auto next = [&]() {
-      for (;;) {
-        if (!take(pc)) return false;
-        if (tile == 0 || __any_sync(0xffffffffu, pc.flags & kTwoTiles)) return true;
-        blk += uint32_t(pc.n);
-      }
-    };
     bool more = false, live = false;
     int64_t out_at = 0, out32_at = 0, lse_at = 0; // where this thread's row lies in out, out32 and lse2, lse
     int lo = 0, hi = 0;                           // the tokens it sees
@@ -911,6 +907,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     // The next piece's row, and its Q into shared memory (the products that read the one
     // before it are done: their scores were there).  Returns the scores' factor.
     auto begin = [&]() {
+      const bool two = pc.flags & kTwoTiles;
+      row = two ? tile * kQueryRows + r : r;
       live = more && row < pc.rows;
       float mul = 0.f;
       int64_t q_at = -1;
@@ -924,11 +922,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         query_sees(x.i, pc.nq, pc.kv, p.causal, p.window, &lo, &hi);
         mul = p.scale2;
       }
-      if (!more) return mul;
-      if (maps.q_boxes > 0) {
+      const bool loads = tile == 0 || two;        // one tile's Q is the first set's to bring
+      if (!more || !(loads || (C::TYPE == kQE4m3 && p.bf16))) return mul;
+      if (loads && maps.q_boxes > 0) {
         if (r == 0) {
           mbar_expect(bar(QFULL + tile), uint32_t(maps.q_boxes) * C::QATOM_B);
-          const int token = pc.q0 + (pc.row0 + tile * kQueryRows) / p.G;
+          const int token = pc.q0 + (pc.row0 + tile * kQueryRows) / p.G;   // a whole number of queries
           for (int a = 0; a < maps.q_boxes; ++a)
             tma_box4(q_s + tile * C::QTILE_B + a * C::QATOM_B, &maps.q, a * 64, 0, pc.h, token, bar(QFULL + tile));
         }
@@ -969,9 +968,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           const int mine = __shfl_sync(0xffffffffu, ex, lane % RPI * LPR);
           if (i == lane / RPI) mul *= __int_as_float((127 + mine) << 23);
         }
-        if (qc * 8 < d16)
+        if (loads && qc * 8 < d16)
           *reinterpret_cast<uint4 *>(q_p + tile * C::QTILE_B + (qc >> 3) * C::QATOM_B + (w0 + rr) * 128 + (((qc & 7) ^ (rr & 7)) << 4)) = w;
       }
+      if (!loads) return mul;                     // it needed the rows' factors alone
       proxy_fence();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(QFULL + tile));
@@ -982,26 +982,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     int n = 0, t_first = 0;
     float mul = 0.f, m = 0.f, l = 0.f;
     for (;;) {
-      // where block j's scores are, and how often its lane was used before
-      auto way = [&](int j) { return dual ? tile : 2 * (j & 1); };
-      auto turn = [&](int j) { return dual ? used0 + uint32_t(j) : ((j & 1) ? used2 : used0) + (uint32_t(j) >> 1); };
+      // this set's blocks: j0, j0 + each, ...; of one tile with two sets every other
+      const bool shared = C::QT == 2 && !dual;
+      const int j0 = shared ? tile : 0, each = shared ? 2 : 1;
+      // the lane of block j, and how often it was used before
+      auto way = [&](int j) { return C::QT == 2 ? tile : j & 1; };
+      auto turn = [&](int j) {
+        return C::QT == 2 ? used0 + uint32_t(shared ? j >> 1 : j) : ((j & 1) ? used1 : used0) + (uint32_t(j) >> 1);
+      };
       m = live ? -INFINITY : 0.f, l = 0.f;
       float mu = live ? 0.f : 1000.f;             // (no row: exponentials of 0)
       bool unset = true;                          // a row of the warp has no reference yet
 #pragma unroll 1
-      for (int j = 0; j < n; ++j, ++blk) {
+      for (int j = j0; j < n; j += each) {
+        const uint32_t info = (blk + uint32_t(j)) % INFO;
         uint32_t words[WORDS];
         bool mask = false;
         const int t0 = t_first + j * BN;
-        // (after units that these warps sat out, the copies may be many blocks behind: then the
-        // scores come first, before a word's barrier could have turned around)
-        if (j == 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(0)), turn(0) & 1u, &gave_up));
-        if (ok && any) {                          // what this row does not see
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(KNOWN + blk % INFO), (blk / INFO) & 1u, &gave_up));
+        if (any) {                                // what this row does not see
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(KNOWN + info), ((blk + uint32_t(j)) / INFO) & 1u, &gave_up));
           mask = lo > t0 || hi < t0 + BN;
 #pragma unroll
           for (int w = 0; w < WORDS; ++w) {
-            words[w] = there[blk % INFO][w];
+            words[w] = there[info][w];
             mask |= words[w] != ~0u;
           }
           mask = __any_sync(0xffffffffu, mask);
@@ -1009,11 +1012,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + way(j)), turn(j) & 1u, &gave_up));
         if (!ok) break;
         if (!any) {
-          if (lane < PARTS) mbar_arrive(bar(PFULL + 3 * lane + way(j)));
+          if (lane < PARTS) mbar_arrive(bar(PFULL + 2 * lane + way(j)));
           continue;
         }
         tc_fence_after();
-        const uint32_t s_at = tmem + (dual ? tile : j & 1) * BN + lanes;
+        const uint32_t s_at = tmem + way(j) * BN + lanes;
         // 64 tokens at a time, whose product with V starts while the next ones are taken.  No
         // maximum is looked for in the usual 64: an exponential above 2^RAISE shows in their sum,
         // and only then (or while a row has no reference) the scores are gone through again,
@@ -1051,9 +1054,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll
               for (int i = 64 * part; i < 64 * part + 64; ++i) e[i] += by;
               unset = __any_sync(0xffffffffu, m == -INFINITY);
-              if (j > 0 || part > 0) {            // O, once the product with V before this is done
-                const int last = part > 0 ? j : j - 1;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 3 * PARTS - 3) + way(last)), turn(last) & 1u, &gave_up));
+              if (j > j0 || part > 0) {           // O, once the product with V before this is done
+                const int last = part > 0 ? j : j - each;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + (part > 0 ? 0 : 2 * PARTS - 2) + way(last)), turn(last) & 1u, &gave_up));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -1093,28 +1096,56 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(PFULL + 3 * part + way(j)));
+          if (lane == 0) mbar_arrive(bar(PFULL + 2 * part + way(j)));
         }
         if (!ok) break;
       }
       if (!ok) break;
       // ---- the piece's end; the next one's first products run meanwhile
-      const int last_way = way(n - 1);
-      const uint32_t last_turn = turn(n - 1);
-      used0 += dual ? uint32_t(n) : uint32_t(n + 1) >> 1;
-      used2 += dual ? 0u : uint32_t(n) >> 1;
+      const int mine = (n - j0 + each - 1) / each, j1 = j0 + (mine - 1) * each;   // blocks, the last one
+      const int last_way = way(j1);
+      const uint32_t last_turn = turn(j1);
+      used0 += uint32_t(C::QT == 2 ? mine : (n + 1) >> 1);
+      used1 += uint32_t(n) >> 1;
+      blk += uint32_t(n);
       const bool was_live = live, was_any = any;
+      const int was_row = row;
       const int64_t was_out = out_at, was_out32 = out32_at, was_lse = lse_at;
-      more = next();
-      mul = begin();
-      if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 3 * PARTS - 3 + last_way), last_turn & 1u, &gave_up));
+      if (mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 2 * PARTS - 2 + last_way), last_turn & 1u, &gave_up));
+      tc_fence_after();
+      float take0 = 1.f, take1 = 0.f;             // of O, of the other set's
+      if (ok && shared && n > 0) {
+        float2 *const other = reinterpret_cast<float2 *>(q_p + C::QTILE_B) + r;   // in the place of a second tile's Q
+        if (tile == 1) {
+          *other = make_float2(m, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(OTHER));
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(ADDED), shares & 1u, &gave_up));
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(OTHER), shares & 1u, &gave_up));
+          tc_fence_after();
+          if (n > 1) {
+            const float2 x = *other;
+            const float now = fmaxf(m, x.x), base = now == -INFINITY ? 0.f : now;
+            take0 = exp2_fast(m - base);
+            take1 = exp2_fast(x.x - base);
+            l = l * take0 + x.y * take1;
+            m = now;
+          }
+        }
+        ++shares;
+      }
       if (!ok) break;
-      if (was_any) {
-        tc_fence_after();
+      more = take(pc);
+      mul = begin();
+      if (!ok) break;
+      if (was_any && !(shared && tile == 1)) {
         // a row that saw nothing is 0, whatever 0 times V was
         const bool none = whole && __any_sync(0xffffffffu, was_live && l == 0.f);
         const float f = whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
-        const uint64_t f2 = f32x2(f, f);
+        const uint64_t f2 = f32x2(f * take0, f * take0), g2 = f32x2(f * take1, f * take1);
+        const bool both = shared && n > 1;
         float *part = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + tile * C::DP * kQueryRows + r;
         float *const row32 = p.out32 + was_out32 * p.D;
         char *const row16 = static_cast<char *>(p.out) + 2 * was_out;
@@ -1126,6 +1157,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           tc_loaded32(o);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) unpack(mul2(f32x2(o[i], o[i + 1]), f2), o + i);
+          if (both) {
+            float z[32];
+            tc_ld32(o_at + C::DP + c, z);
+            tc_loaded32(z);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) unpack(fma2(f32x2(z[i], z[i + 1]), g2, f32x2(o[i], o[i + 1])), o + i);
+          }
           if (__builtin_expect(none, 0)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
@@ -1151,10 +1189,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           if (p.lse2) p.lse2[was_out32] = lse2;
           if (p.lse) p.lse[was_lse] = lse2 * kLn2;
         } else if (was_live) {
-          float *const ml = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + C::ROWS * C::DP + row;
+          float *const ml = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + C::ROWS * C::DP + was_row;
           __stcg(ml, m);
           __stcg(ml + C::ROWS, l);
         }
+      }
+      if (shared && tile == 0 && n > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ADDED));
       }
       if (!more) break;
       dual = pc.flags & kTwoTiles;
