@@ -229,11 +229,12 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
-// The pieces of a chunk, in order.
+// The pieces of a chunk, in order.  A unit counts its blocks and kQueryStart more, what
+// beginning and ending it takes.
 template <class C>
 struct QueryPieces {
   long long pos, hi;
-  int b, h, m, units, off;         // the unit: sequence, kv head, group of rows (of `units`); blocks of it done
+  int b, h, m, units, off;         // the unit: sequence, kv head, group of rows (of `units`); how much of it is done
   QuerySeq s;
   QueryUnit u;
   // the current piece: blocks [x0, x1) of the unit
@@ -249,17 +250,18 @@ struct QueryPieces {
     s = query_seq(p, b);
     units = query_units(s.nq, p.G, C::ROWS);
   }
-  // the blocks of a kv head of the sequence (a whole warp calls)
-  __device__ __forceinline__ long long blocks(const QueryParams &p) const {
+  __device__ __forceinline__ int cost(const QueryParams &p, int i) const { return query_cost(unit(p, i).blocks); }
+  // what a kv head of the sequence counts (a whole warp calls)
+  __device__ __forceinline__ long long head(const QueryParams &p) const {
     const int lane = int(threadIdx.x) & 31;
     if (units == 0) return 0;
-    if (!p.causal) return (long long)units * unit(p, 0).blocks;
+    if (!p.causal) return (long long)units * cost(p, 0);
     long long n = 0;
-    for (int i = lane; i < units; i += 32) n += unit(p, i).blocks;
+    for (int i = lane; i < units; i += 32) n += cost(p, i);
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
     return n;
   }
-  // at block `at` of all, `rest` blocks from the first of sequence b (a whole warp calls)
+  // at `at` of all, `rest` from the first of sequence b (a whole warp calls)
   __device__ __forceinline__ void start(const QueryParams &p, long long at, long long end, int b0, long long rest) {
     const int lane = int(threadIdx.x) & 31;
     pos = at;
@@ -268,7 +270,7 @@ struct QueryPieces {
     long long n;
     for (;; ++b) {
       sequence(p);
-      n = blocks(p);
+      n = head(p);
       if (rest < n * p.Hkv || b + 1 >= p.B) break;
       rest -= n * p.Hkv;
     }
@@ -276,12 +278,12 @@ struct QueryPieces {
     rest -= h * n;
     m = 0;
     if (!p.causal) {
-      const int each = unit(p, 0).blocks;
+      const int each = cost(p, 0);
       m = each > 0 ? int(quotient(rest, each)) : 0;
       rest -= (long long)m * each;
     } else {
       for (;; m += 32) {           // 32 units at a time
-        const int mine = m + lane < units ? unit(p, m + lane).blocks : 0;
+        const int mine = m + lane < units ? cost(p, m + lane) : 0;
         int inc = mine;
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -303,25 +305,28 @@ struct QueryPieces {
     off = int(rest);
   }
   __device__ __forceinline__ bool next(const QueryParams &p) {
-    if (pos >= hi) return false;
-    while (off >= u.blocks) {
-      if (++m >= units) {
-        m = 0;
-        if (++h >= p.Hkv) {
-          h = 0;
-          do {
-            if (++b >= p.B) return false;
-            sequence(p);
-          } while (units == 0 || s.kv == 0);
+    do {
+      if (pos >= hi) return false;
+      while (off >= query_cost(u.blocks)) {
+        if (++m >= units) {
+          m = 0;
+          if (++h >= p.Hkv) {
+            h = 0;
+            do {
+              if (++b >= p.B) return false;
+              sequence(p);
+            } while (units == 0 || s.kv == 0);
+          }
         }
+        u = unit(p, m);
+        off = 0;
       }
-      u = unit(p, m);
-      off = 0;
-    }
-    x0 = off;
-    x1 = int(min((long long)u.blocks, off + (hi - pos)));
-    pos += x1 - x0;
-    off = x1;
+      const int end = int(min((long long)query_cost(u.blocks), off + (hi - pos)));
+      pos += end - off;
+      x0 = max(0, off - kQueryStart);
+      x1 = max(0, end - kQueryStart);
+      off = end;
+    } while (x1 == x0);
     return true;
   }
 };
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the work before this call
 
-  // ---- the blocks before each sequence; thread i takes `per` sequences
+  // ---- what lies before each sequence; thread i takes `per` sequences
   const int per = (p.B + THREADS - 1) / THREADS;
   long long mine = 0, units = 0;
   bool zero = false;                              // a sequence has rows that no unit holds
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     long long n = 0;
     const bool many = p.causal && t.units > 4;    // counted by the whole warp
     if (!many)
-      for (int i = 0; i < (p.causal ? t.units : min(t.units, 1)); ++i) n += t.unit(p, i).blocks;
+      for (int i = 0; i < (p.causal ? t.units : min(t.units, 1)); ++i) n += t.cost(p, i);
     if (!p.causal) n *= t.units;
     for (unsigned todo = __ballot_sync(0xffffffffu, many); todo; todo &= todo - 1u) {
       const int src = __ffs(int(todo)) - 1;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       o.s.nq = __shfl_sync(0xffffffffu, t.s.nq, src);
       o.s.kv = __shfl_sync(0xffffffffu, t.s.kv, src);
       o.units = __shfl_sync(0xffffffffu, t.units, src);
-      const long long all = o.blocks(p);
+      const long long all = o.head(p);
       if (lane == src) n = all;
     }
     mine += n * p.Hkv;
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   if (lane == 0) units_of[warp] = units;          // read behind block_prefix's barrier
   const long long ahead = block_prefix<C::WARPS>(mine, scratch, &total);
   for (int w = 0; w < C::WARPS; ++w) all_units += units_of[w];
-  // with fewer blocks than CTAs, only as many CTAs take part: each has one then
+  // with less than that for each CTA, only as many CTAs take part
   const long long chunks = min((long long)gridDim.x, total);
   // With many units to a CTA, whole units one after another (see the planner)
   const bool whole_units = all_units >= kQueryWhole * (long long)gridDim.x;
@@ -727,8 +732,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             x.flags = (pc.dual() ? kTwoTiles : 0) | (begins ? kBegins : 0) | (whole ? kWhole : 0);
             if (begins && !whole) {
               // the chunks that the unit lies in
-              const long long first = pc.pos - pc.x1;
-              const int last = int(quotient((first + pc.u.blocks) * chunks - 1, total));
+              const long long first = pc.pos - pc.off;
+              const int last = int(quotient((first + query_cost(pc.u.blocks)) * chunks - 1, total));
               p.open[blockIdx.x] = make_int4(pc.b, pc.h, pc.m, last - int(blockIdx.x) + 1);
             }
           }
@@ -767,21 +772,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
         }
       };
-      // Whole boxes come by TMA, present or not (one that is not lies behind the rows and
-      // reads as zeros); a block in which the range of tokens cuts a box, row by row.
+      // By TMA, K and V of whole boxes, present or not (one that is not lies behind the rows
+      // and reads as zeros).  Of a block in which the range of tokens cuts a box only K: what
+      // it holds beyond the range is masked, but V there might be no number, and 0 times that is
+      // none either.  That V comes row by row.
       auto boxes = [&](int t0) {
-        return C::TYPE != kQE4m3 && maps.box > 0 && (max(pc.lo - t0, 0) & (maps.box - 1)) == 0 &&
-               (min(pc.hi - t0, BN) & (maps.box - 1)) == 0;
+        return (max(pc.lo - t0, 0) & (maps.box - 1)) == 0 && (min(pc.hi - t0, BN) & (maps.box - 1)) == 0;
       };
-      bool boxed = boxes(pc.t0);
-      if (!boxed) lookup(pc.t0 + pt);
+      const bool by_box = C::TYPE != kQE4m3 && maps.box > 0;
+      if (!by_box) lookup(pc.t0 + pt);
       for (int x = 0; ok && x < pc.n; ++x, ++blk) {
         const int t0 = pc.t0 + x * BN;
-        const bool next_boxed = boxes(t0 + BN);
-        if (boxed) {
+        int kv0 = 0;                              // the tiles from which on rows are copied one by one
+        if (by_box) {
+          kv0 = boxes(t0) ? 2 : 1;
           if (blk % 3u == uint32_t(pt >> 5)) {
-            lookup(t0 + box_r);
-            const bool have = lane < boxes_all && page_present(page, p.num_pages);
+            // the page of the box's first token that is in the range
+            const int t = max(t0 + box_r, pc.lo);
+            page = -1;
+            if (lane < boxes_all && t < t0 + box_r + maps.box) lookup(t);
+            const bool have = page_present(page, p.num_pages);
             const int y = have ? int(int64_t(page) * p.P + (t0 + box_r - pg * p.P)) : int(p.num_pages * p.P);
             const uint32_t bits = __ballot_sync(0xffffffffu, have);
             if (lane < WORDS) {                   // tokens lane * 32 on
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(KNOWN + blk % INFO), 4);
 #pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
+            for (int kv = 0; kv < kv0; ++kv) {
               if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
               if (!ok) break;
               if (lane == 0) mbar_expect(bar(FULL + stage), uint32_t(columns) * C::ATOM_B);
@@ -805,29 +815,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
               advance();
             }
           } else {
-            advance();
-            advance();
+            for (int kv = 0; kv < kv0; ++kv) advance();
           }
-          boxed = next_boxed;
-          if (!boxed && x + 1 < pc.n) lookup(t0 + BN + pt);
-          continue;
+          if (!ok) break;
+          if (kv0 == 2) continue;
+          lookup(t0 + pt);
+          // among boxes the warps are not together: none may still read the places of two blocks ago
+          together();
+          if (!ok) break;
         }
-        // among boxes the warps are not together: none may still read the places of two blocks ago
-        if (maps.box > 0) together();
-        if (!ok) break;
         const bool have = pt < BN && page_present(page, p.num_pages);
         int64_t *const at = offs[blk & 1u];
         if (pt < BN) at[pt] = have ? int64_t(page) * p.P + (t0 + pt - pg * p.P) : -1;
-        const uint32_t word = __ballot_sync(0xffffffffu, have);
-        if (lane == 0) {
-          if (pt < BN) there[blk % INFO][pt >> 5] = word;
-          mbar_arrive(bar(KNOWN + blk % INFO));
+        if (!by_box) {
+          const uint32_t word = __ballot_sync(0xffffffffu, have);
+          if (lane == 0) {
+            if (pt < BN) there[blk % INFO][pt >> 5] = word;
+            mbar_arrive(bar(KNOWN + blk % INFO));
+          }
         }
         together();
-        boxed = next_boxed;
-        if (!boxed && x + 1 < pc.n) lookup(t0 + BN + pt);
+        if (!by_box && x + 1 < pc.n) lookup(t0 + BN + pt);
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
+        for (int kv = kv0; kv < 2; ++kv) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
           if (!ok) break;
           const char *src = static_cast<const char *>(kv ? p.v : p.k) + int64_t(pc.h) * p.D * C::ES;
@@ -1106,15 +1116,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       const int last_way = way(j1);
       const uint32_t last_turn = turn(j1);
       used0 += uint32_t(C::QT == 2 ? mine : (n + 1) >> 1);
-      used1 += uint32_t(n) >> 1;
+      used1 += uint32_t(dual ? n : n >> 1);       // of the second lane, whoever's
       blk += uint32_t(n);
       const bool was_live = live, was_any = any;
       const int was_row = row;
       const int64_t was_out = out_at, was_out32 = out32_at, was_lse = lse_at;
-      if (mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 2 * PARTS - 2 + last_way), last_turn & 1u, &gave_up));
-      tc_fence_after();
       float take0 = 1.f, take1 = 0.f;             // of O, of the other set's
-      if (ok && shared && n > 0) {
+      // The next piece begins, its Q on its way, before the wait for the last product; but the
+      // second set of a unit with one tile leaves its sums where its next Q would come.  (A
+      // loop of two turns, so that the code is here once.)
+      const bool early = !(shared && tile == 1);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        if ((k == 0) == early) {
+          // of one tile, Q is still read for the other set's last block
+          if (shared && n > 1 && !(n & 1) && tile == 0)
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(SFULL + 1), (used1 - 1u) & 1u, &gave_up));
+          if (!ok) break;
+          more = take(pc);
+          mul = begin();
+        }
+        if (!ok) break;
+        if (k == 1) continue;
+        if (mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(PVDONE + 2 * PARTS - 2 + last_way), last_turn & 1u, &gave_up));
+        tc_fence_after();
+        if (!(ok && shared && n > 0)) continue;
         float2 *const other = reinterpret_cast<float2 *>(q_p + C::QTILE_B) + r;   // in the place of a second tile's Q
         if (tile == 1) {
           *other = make_float2(m, l);
@@ -1136,9 +1162,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         }
         ++shares;
       }
-      if (!ok) break;
-      more = take(pc);
-      mul = begin();
       if (!ok) break;
       if (was_any && !(shared && tile == 1)) {
         // a row that saw nothing is 0, whatever 0 times V was

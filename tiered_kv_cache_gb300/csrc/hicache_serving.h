@@ -119,6 +119,9 @@ HC_HD int query_tiles(int D) { return D <= 128 ? 2 : 1; }
 HC_HD int query_block(int D) { return D <= 128 ? 128 : 64; }
 HC_HD int query_cols(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 constexpr int kQueryCtas = 152;                   // one on each of a GB300's SMs
+// What beginning and ending a unit takes, in blocks.
+constexpr int kQueryStart = 4;
+HC_HD int32_t query_cost(int32_t blocks) { return blocks > 0 ? blocks + kQueryStart : 0; }
 // From so many units for each of them on, CTAs take whole units.
 constexpr int kQueryWhole = 4;
 struct QuerySpace {
