@@ -265,7 +265,7 @@ def check_prefix(c, q, members, out, lse, lead=0, pick=None):
     owner += [-1] * (q.shape[0] - len(owner))
     rows = [present((c.rows[0][g] if g >= 0 else []) + c.rows[1][b]) for b, g in enumerate(owner)]
     some = list(range(q.shape[0])) if pick is None else pick
-    want = ref.attend(q[some], k, v, [rows[i] for i in some], q.shape[2] ** -0.5, c.k_scale, c.v_scale, joins=2)
+    want = ref.attend(q[some], k, v, [rows[i] for i in some], q.shape[2] ** -0.5, c.k_scale, c.v_scale, joins=5)
     p_type = torch.bfloat16 if c.bufs[0].dtype == torch.bfloat16 else torch.float16
     ref.check_decode(out[some], want, q.dtype, p_type, lse=lse[some])
 
@@ -282,18 +282,36 @@ def test_prefix(c, holes):
     assert torch.equal(raw(out), raw(again)) and torch.equal(raw(lse), raw(lse2))
 
 
-def test_prefix_is_decode_without_groups():
-    """Without groups, or with empty ones, the bits of decode_attention."""
+def test_prefix_without_groups():
+    """Without groups, with groups of no sequence, with empty prefixes: decode_attention's
+    results, within the bounds of both."""
     own = [0, 3, 700, 65]
     cache = Cache([[1], own], 2, 128, 16)
     q = queries(4, 8, 128, "bf16")
+    ws = workspace(hc.prefix_workspace(cache.desc, 4, 0, 8, 128, 1, cache.tables[1].shape[1]))
+    out, lse = torch.full_like(q, 7.0), torch.full((4, 8), 5.0, device="cuda")
+    hc.prefix_attention(cache.kv, cache.desc, 0, q, i32([0]), cache.tables[0][:0], i32([]), cache.tables[1], i32(own), out,
+                        ws, lse=lse)
+    check_prefix(cache, q, [], out, lse)
+    for members, prefix, lead in (([0], [1], 2), ([4], [0], 0)):
+        again, lse2 = run_prefix(cache, q, members, prefix, own, lead=lead)
+        assert torch.equal(raw(out), raw(again)) and torch.equal(raw(lse), raw(lse2))
     want, want_lse = torch.zeros_like(q), torch.zeros((4, 8), device="cuda")
     ws = workspace(hc.decode_workspace(cache.desc, 4, 8, 128, 128, cache.tables[1].shape[1]))
     hc.decode_attention(cache.kv, cache.desc, 0, q, cache.tables[1], i32(own), want, ws, lse=want_lse)
-    out, lse = run_prefix(cache, q, [0], [1], own, lead=2)
-    assert torch.equal(raw(out), raw(want)) and torch.equal(lse, want_lse)
-    out, lse = run_prefix(cache, q, [4], [0], own)
-    assert torch.equal(raw(out), raw(want)) and torch.equal(lse, want_lse)
+    check_prefix(cache, q, [], want, want_lse)
+
+
+@pytest.mark.parametrize("hq,hk,d,P,dtype,e4", [(8, 2, 128, 16, "bf16", False), (6, 2, 64, 5, "fp16", False),
+                                                (4, 1, 256, 64, "bf16", True)])
+def test_prefix_long_own(hq, hk, d, P, dtype, e4):
+    """Own tokens of several parts, around their limits."""
+    members, prefix = [2, 3], [5000, 300]
+    own = [9000, 4096, 4097, 8192, 1, 0, 12289]
+    cache = Cache([prefix, own], hk, d, P, dtype, e4, seed=12)
+    q = queries(len(own), hq, d, dtype)
+    out, lse = run_prefix(cache, q, members, prefix, own)
+    check_prefix(cache, q, members, out, lse)
 
 
 # ---- merge ----------------------------------------------------------------------------

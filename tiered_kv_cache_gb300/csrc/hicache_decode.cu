@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
     int start, len;
     seq_range(p, b, &start, &len);
     if (len > start) continue;
-    for (int i = tid; i < p.Hq * DP; i += THREADS) store_none(p, b, i / DP, i % DP);
+    for (int i = tid; i < p.Hq * DP; i += THREADS) store_out(p, b, i / DP, i % DP, 0.f);
     for (int h = tid; h < p.Hq; h += THREADS) store_lse(p, b, h, 0.f, 0.f);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -526,20 +526,8 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
           float inv[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+            inv[i] = l[n][i] == 0.f ? 0.f : p.v_scale / l[n][i];
             const int r = 8 * n + 2 * c4 + i;
-            const Ending end = row_ending(p, tm.b, h0 + min(r, rows - 1), m[n][i], l[n][i]);
-            inv[i] = end.own;
-            if (end.prior != 0.f) {               // O as it will be, but for its factor
-              const float *x = prior_row(p, tm.b, h0 + min(r, rows - 1));
-#pragma unroll
-              for (int t = 0; t < C::MT; ++t)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int d = element<C>(t, y, g);
-                  if (d < p.D) o[t][n][2 * y + i] = o[t][n][2 * y + i] * end.own + end.prior * __ldg(x + d);
-                }
-              inv[i] = 1.f;
-            }
             if (g == 0 && r < rows) store_lse(p, tm.b, h0 + r, m[n][i], l[n][i]);
           }
           if constexpr (C::TYPE != kE4m3) {       // a head's pairs of elements, by a transposition
@@ -686,7 +674,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
       for (int c = 0; c < COLS; ++c) {
         if (i0 + c * THREADS >= cols) continue;
         if (all) {
-          store_out4(p, b, hh + r[c], d[c], acc[c], mm[c], sum[c]);
+          store_out4(p, b, hh + r[c], d[c], acc[c], sum[c] == 0.f ? 0.f : p.v_scale / sum[c]);
           if (d[c] == 0) store_lse(p, b, hh + r[c], mm[c], sum[c]);
         } else {
           __stcg(reinterpret_cast<float4 *>(part + r[c] * DP + d[c]), acc[c]);
@@ -810,7 +798,7 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) decode_kv_kernel(const __gri
 #pragma unroll
       for (int c = 0; c < JOIN; ++c)
         if (mine[c] && team == 0) {
-          store_out4(p, b, hh + r[c], d[c], acc[c], m_r[c], l_r[c]);
+          store_out4(p, b, hh + r[c], d[c], acc[c], l_r[c] == 0.f ? 0.f : p.v_scale / l_r[c]);
           if (d[c] == 0) store_lse(p, b, hh + r[c], m_r[c], l_r[c]);
         }
     }

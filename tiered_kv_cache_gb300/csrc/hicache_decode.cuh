@@ -67,27 +67,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// What a row's result is made of: its own sums times `own`, and, where the call carries on
-// from what the row attended to before (p.prior), that times `prior`.  l == 0: nothing
-// attended to.
-struct Ending {
-  float own, prior, lse2;
-};
-__device__ __forceinline__ Ending row_ending(const DecodeParams &p, int b, int h, float m, float l) {
-  Ending e{l == 0.f ? 0.f : p.v_scale / l, 0.f, 0.f};
-  if (!p.prior) return e;
-  const float mine = l == 0.f ? -INFINITY : m + log2f(l), before = __ldg(p.prior_lse2 + int64_t(b) * p.Hq + h);
-  const float top = fmaxf(mine, before), base = top == -INFINITY ? 0.f : top;
-  const float w = exp2_fast(mine - base), y = exp2_fast(before - base), all = w + y;
-  e.own *= l == 0.f ? 0.f : w / all;
-  e.prior = before == -INFINITY ? 0.f : y / all;
-  e.lse2 = all == 0.f ? -INFINITY : base + log2f(all);
-  return e;
-}
-__device__ __forceinline__ const float *prior_row(const DecodeParams &p, int b, int h) {
-  return p.prior + (int64_t(b) * p.Hq + h) * p.D;
-}
-
 __device__ __forceinline__ void store_out(const DecodeParams &p, int b, int h, int col, float v) {
   if (col >= p.Dv) return;
   const int64_t at = int64_t(b) * p.o_sb + int64_t(h) * p.o_sh + col;
@@ -96,30 +75,17 @@ __device__ __forceinline__ void store_out(const DecodeParams &p, int b, int h, i
   else
     static_cast<__half *>(p.out)[at] = __float2half_rn(v);
 }
-// element col of a row that attends to none of the call's tokens
-__device__ __forceinline__ void store_none(const DecodeParams &p, int b, int h, int col) {
+// four elements from a multiple of 4 on, times f
+__device__ __forceinline__ void store_out4(const DecodeParams &p, int b, int h, int col, float4 v, float f) {
   if (col >= p.Dv) return;
-  float v = 0.f;
-  if (p.prior && __ldg(p.prior_lse2 + int64_t(b) * p.Hq + h) != -INFINITY) v = __ldg(prior_row(p, b, h) + col);
-  store_out(p, b, h, col, v);
-}
-// four elements from a multiple of 4 on, of a row with the maximum m and the sum l
-__device__ __forceinline__ void store_out4(const DecodeParams &p, int b, int h, int col, float4 v, float m, float l) {
-  if (col >= p.Dv) return;
-  const Ending e = row_ending(p, b, h, m, l);
-  const float f = e.own;
-  float4 r = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-  if (e.prior != 0.f) {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(prior_row(p, b, h) + col));
-    r = make_float4(r.x + e.prior * x.x, r.y + e.prior * x.y, r.z + e.prior * x.z, r.w + e.prior * x.w);
-  }
   char *at = static_cast<char *>(p.out) + 2 * (int64_t(b) * p.o_sb + int64_t(h) * p.o_sh + col);
-  *reinterpret_cast<uint2 *>(at) = p.bf16 ? make_uint2(pack2<true>(r.x, r.y), pack2<true>(r.z, r.w))
-                                          : make_uint2(pack2<false>(r.x, r.y), pack2<false>(r.z, r.w));
+  *reinterpret_cast<uint2 *>(at) = p.bf16
+                                       ? make_uint2(pack2<true>(v.x * f, v.y * f), pack2<true>(v.z * f, v.w * f))
+                                       : make_uint2(pack2<false>(v.x * f, v.y * f), pack2<false>(v.z * f, v.w * f));
 }
 // l == 0: nothing attended to
 __device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int h, float m, float l) {
-  const float lse2 = p.prior ? row_ending(p, b, h, m, l).lse2 : l == 0.f ? -INFINITY : m + log2f(l);
+  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
   if (p.lse) p.lse[int64_t(b) * p.lse_sb + h] = lse2 * kLn2;
   if (p.weights) p.lse2[int64_t(b) * p.Hq + h] = lse2;
 }

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) decode_latent_kernel(const __gr
     int start, len;
     seq_range(p, b, &start, &len);
     if (len > start) continue;
-    for (int i = tid; i < p.Hq * kLatDv; i += THREADS) store_none(p, b, i / kLatDv, i % kLatDv);
+    for (int i = tid; i < p.Hq * kLatDv; i += THREADS) store_out(p, b, i / kLatDv, i % kLatDv, 0.f);
     for (int h = tid; h < p.Hq; h += THREADS) store_lse(p, b, h, 0.f, 0.f);
     if (tid == 0) p.seq_pieces[b] = make_int2(0, 0);
   }
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(128 * PARTS) latent_join_kernel(const __grid_c
 #pragma unroll
     for (int x = 1; x < PARTS; ++x) add(m_s[x], l_s[x], acc_s[x][tid]);
   }
-  store_out4(p, b, h, tid * 4, acc, m, sum);
+  store_out4(p, b, h, tid * 4, acc, sum == 0.f ? 0.f : p.v_scale / sum);
   if (tid == 0) store_lse(p, b, h, m, sum);
 }
 

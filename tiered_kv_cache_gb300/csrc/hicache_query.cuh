@@ -65,7 +65,14 @@ struct QueryConfig {
   static constexpr int SOFT_WARPS = 4 * QT, COPY_WARP = SOFT_WARPS, MMA_WARP = COPY_WARP + 4;
   static constexpr int WARPS = MMA_WARP + 4, THREADS = WARPS * 32;
   // registers of a thread of each group of four warps: what the launch has, dealt anew
-  static constexpr int SOFT_REGS = QT == 2 ? 192 : 240, COPY_REGS = QT == 2 ? 72 : 168, MMA_REGS = QT == 2 ? 56 : 96;
+  static constexpr bool E4 = TYPE_ == kQE4m3;
+  // Halves of a block whose scores are loaded together, and whose code is there twice: 8% for
+  // what the products bind (2,048 queries at 32,768: 740 -> 683 us), but 18 to 20% against
+  // what copies and starts do (32 ragged encoders 59 -> 72, e4m3 197 -> 247), for
+  // the instruction cache.
+  static constexpr int AT_ONCE = BN == 128 && DP_ == 128 && !E4 ? 2 : 1;
+  static constexpr int SOFT_REGS = QT == 1 ? 240 : E4 ? 184 : 192, COPY_REGS = QT == 1 ? 152 : E4 ? 72 : 72,
+                       MMA_REGS = QT == 1 ? 112 : E4 ? 72 : 56;
   static_assert(4 * QT * SOFT_REGS + 4 * COPY_REGS + 4 * MMA_REGS <= WARPS * (65536 / THREADS / 8 * 8), "registers");
   static constexpr int O_COL = 2 * BN;            // tensor memory: two score buffers, then O of each tile
   static constexpr int PIECE = ROWS * DP_ + 2 * ROWS;   // floats: O [tile][element][row], m, l
@@ -255,11 +262,12 @@ struct QueryPieces {
   __device__ __forceinline__ long long head(const QueryParams &p) const {
     const int lane = int(threadIdx.x) & 31;
     if (units == 0) return 0;
-    if (!p.causal) return (long long)units * cost(p, 0);
     long long n = 0;
-    for (int i = lane; i < units; i += 32) n += cost(p, i);
+#pragma unroll 1
+    for (int i = lane; i < (p.causal ? units : 1); i += 32) n += cost(p, i);
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    return p.causal ? n : n * units;              // alike, then
   }
   // at `at` of all, `rest` from the first of sequence b (a whole warp calls)
   __device__ __forceinline__ void start(const QueryParams &p, long long at, long long end, int b0, long long rest) {
@@ -278,13 +286,15 @@ struct QueryPieces {
     rest -= h * n;
     m = 0;
     if (!p.causal) {
-      const int each = cost(p, 0);
+      const int each = units > 0 ? int(quotient(n, units)) : 0;   // (a head's count: of units that are alike)
       m = each > 0 ? int(quotient(rest, each)) : 0;
       rest -= (long long)m * each;
     } else {
+#pragma unroll 1
       for (;; m += 32) {           // 32 units at a time
         const int mine = m + lane < units ? cost(p, m + lane) : 0;
         int inc = mine;
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, inc, o);
           if (lane >= o) inc += y;
@@ -337,7 +347,7 @@ struct alignas(16) QueryPiece {
   int32_t row0, rows, q0, nq;      // rows of the unit; the sequence's first query and their number
   int32_t kv, lo, hi, flags;       // tokens of the sequence; those [lo, hi) that some row of the unit sees
 };
-enum : int { kTwoTiles = 1, kBegins = 2, kWhole = 4 };
+enum : int { kTwoTiles = 1, kBegins = 2, kWhole = 4, kOwn = 8 };   // kOwn: over the sequence's own tokens
 constexpr int kPieceRing = 4;
 
 // The output's row of row r of a unit: the query token and head.
@@ -356,7 +366,7 @@ __device__ __forceinline__ QueryRow query_row(const QueryParams &p, int q0, int 
 __device__ __forceinline__ void query_lse(const QueryParams &p, const QueryRow &x, float m, float l) {
   const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
   if (p.lse2) p.lse2[x.token * p.Hq + x.head] = lse2;
-  if (p.lse) p.lse[x.token * p.lse_st + x.head] = lse2 * kLn2;
+  else if (p.lse) p.lse[x.token * p.lse_st + x.head] = lse2 * kLn2;
 }
 // the call's type is the cache's, but for e4m3
 template <class C>
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   const int per = (p.B + THREADS - 1) / THREADS;
   long long mine = 0, units = 0;
   bool zero = false;                              // a sequence has rows that no unit holds
+#pragma unroll 1
   for (int x = 0; x < per; ++x) {
     const int b = tid * per + x;
     QueryPieces<C> t;
@@ -423,9 +434,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     t.units = query_units(t.s.nq, p.G, C::ROWS);
     long long n = 0;
     const bool many = p.causal && t.units > 4;    // counted by the whole warp
-    if (!many)
-      for (int i = 0; i < (p.causal ? t.units : min(t.units, 1)); ++i) n += t.cost(p, i);
+#pragma unroll 1
+    for (int i = 0; !many && i < (p.causal ? t.units : min(t.units, 1)); ++i) n += t.cost(p, i);
     if (!p.causal) n *= t.units;
+#pragma unroll 1
     for (unsigned todo = __ballot_sync(0xffffffffu, many); todo; todo &= todo - 1u) {
       const int src = __ffs(int(todo)) - 1;
       QueryPieces<C> o;
@@ -485,26 +497,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   }
   // rows of which there is nothing to attend to and that no unit holds: of sequences
   // without tokens, and of queries before the first token
+#pragma unroll 1
   for (int b = int(blockIdx.x); zeros && b < p.B; b += int(gridDim.x)) {
     const QuerySeq s = query_seq(p, b);
-    int rows = s.nq * p.G;
-    if (s.kv > 0) rows = p.causal ? max(0, min(s.nq, s.nq - s.kv)) * p.G / C::ROWS * C::ROWS : 0;
-    for (int64_t i = tid; i < int64_t(rows) * p.Hkv; i += THREADS) {
+    uint32_t rows = uint32_t(s.nq) * p.G;         // times Hkv under 2^31, as N * Hq is
+    if (s.kv > 0) rows = p.causal ? uint32_t(max(0, min(s.nq, s.nq - s.kv))) * p.G / C::ROWS * C::ROWS : 0;
+#pragma unroll 1
+    for (uint32_t i = tid; i < rows * p.Hkv; i += THREADS) {
       const QueryRow x = query_row(p, s.q0, int(i / rows), int(i % rows));
-      const float zero[8] = {};
-      for (int c = 0; c < p.D; c += 8) query_store8(p, x, c, zero);
+      char *const at = p.out32 ? reinterpret_cast<char *>(p.out32 + (x.token * p.Hq + x.head) * p.D)
+                               : static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh);
+#pragma unroll 1
+      for (int c = 0; c < p.D * (p.out32 ? 4 : 2); c += 16) *reinterpret_cast<uint4 *>(at + c) = make_uint4(0u, 0u, 0u, 0u);
       query_lse(p, x, 0.f, 0.f);
     }
   }
   if (p.lse2) {                                   // rows of no sequence
-    const int s0 = min(max(__ldg(p.starts), 0), p.N), s1 = min(max(__ldg(p.starts + p.B), s0), p.N);
-    for (int64_t i = int64_t(blockIdx.x) * THREADS + tid; i < int64_t(p.N) * p.Hq; i += int64_t(gridDim.x) * THREADS)
-      if (i / p.Hq < s0 || i / p.Hq >= s1) p.lse2[i] = -INFINITY;
+    const int s0 = p.B > 0 ? min(max(__ldg(p.starts), 0), p.N) : 0;
+    const int s1 = p.B > 0 ? min(max(__ldg(p.starts + p.B), s0), p.N) : 0;
+#pragma unroll 1
+    for (uint32_t i = blockIdx.x * THREADS + tid; i < uint32_t(p.N) * p.Hq; i += gridDim.x * THREADS)
+      if (int(i / p.Hq) < s0 || int(i / p.Hq) >= s1) p.lse2[i] = -INFINITY;
   }
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (blockIdx.x >= chunks) return;
+  if (blockIdx.x >= chunks && !p.own_lens) return;
   if (q_s & 1023u) {                              // the tiles' swizzle counts on it
     if (tid == 0) *p.error = 1u;
     return;
@@ -660,12 +678,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       // the cache at the same time, the longest first; which CTA has a unit does not change
       // its result.
       QueryPieces<C> pc;
-      int base = 0;                               // the sequences of this and 31 more, one a lane
+      int list = 0;                               // 1: of the sequences' own tokens, when the prefixes are dealt
+      int base = -32, part = 0;                   // the sequences of this and 31 more, one a lane; kOwnTokens of them
       long long before = 0, upto = 0;             // units before them; this lane's and those before it
       QuerySeq seq{0, 0, 0};
+      const int own_units = query_units(1, p.G, C::ROWS);
       auto group = [&]() {
-        seq = base + lane < p.B ? query_seq(p, base + lane) : QuerySeq{0, 0, 0};
-        upto = (long long)query_units(seq.nq, p.G, C::ROWS) * p.Hkv;
+        const int b = base + lane;
+        seq = QuerySeq{0, 0, 0};
+        if (list == 0) {
+          if (b < p.B) seq = query_seq(p, b);
+          upto = (long long)query_units(seq.nq, p.G, C::ROWS) * p.Hkv;
+        } else {
+          if (b < p.N) seq = QuerySeq{b, 1, int(min(int64_t(max(0, __ldg(p.own_lens + b))), int64_t(p.own_pages) * p.P))};
+          upto = (long long)((seq.kv + kOwnTokens - 1) / kOwnTokens) * own_units * p.Hkv;
+        }
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += y;
@@ -673,14 +701,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       };
       auto claim = [&]() {                        // the next whole unit with something to attend to
         for (;;) {
-          long long at = lane == 0 ? (long long)atomicAdd(p.next, 1u) : 0;
+          long long at = lane == 0 ? (long long)atomicAdd(p.next + list, 1u) : 0;
           at = __shfl_sync(0xffffffffu, at, 0);
-          if (at >= all_units) return false;
+#pragma unroll 1
           for (;;) {
-            const long long here = __shfl_sync(0xffffffffu, upto, 31);
+            const long long here = __shfl_sync(0xffffffffu, upto, 31);   // 0 at first
             if (at < before + here) break;
             before += here;
             base += 32;
+            if (base >= (list == 0 ? p.B : p.N)) return false;
             group();
           }
           const int src = __ffs(int(__ballot_sync(0xffffffffu, before + upto > at))) - 1;
@@ -688,30 +717,42 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           pc.s.q0 = __shfl_sync(0xffffffffu, seq.q0, src);
           pc.s.nq = __shfl_sync(0xffffffffu, seq.nq, src);
           pc.s.kv = __shfl_sync(0xffffffffu, seq.kv, src);
-          pc.units = query_units(pc.s.nq, p.G, C::ROWS);
+          pc.x0 = 0;
+          const int parts = (pc.s.kv + kOwnTokens - 1) / kOwnTokens;
+          pc.units = list == 0 ? query_units(pc.s.nq, p.G, C::ROWS) : own_units * parts;
           const int i = int(at - (before + __shfl_sync(0xffffffffu, upto, src) - (long long)pc.units * p.Hkv));
           pc.h = i / pc.units;
-          pc.m = pc.units - 1 - (i - pc.h * pc.units);
+          const int m = i - pc.h * pc.units;
+          part = list == 0 ? 0 : m / own_units;
+          pc.m = list == 0 ? pc.units - 1 - m : m - part * own_units;
           pc.u = pc.unit(p, pc.m);
-          pc.x0 = 0;
+          if (list == 1) {
+            pc.u.blk0 = part * (kOwnTokens / BN);
+            pc.u.blocks = (min(pc.s.kv - part * kOwnTokens, kOwnTokens) + BN - 1) / BN;
+          }
           pc.x1 = pc.u.blocks;
           if (pc.x1 > 0) return true;
         }
       };
-      if (whole_units)
-        group();
-      else
+      pc.pos = pc.hi = 0;
+      if (!whole_units && blockIdx.x < chunks)
         pc.start(p, quotient(total * int(blockIdx.x), chunks), quotient(total * (int(blockIdx.x) + 1), chunks), first_seq, first_rest);
-      const uint32_t ahead = whole_units ? 1 : kPieceRing;   // a unit is taken when the one before it is begun
       bool more = true;
+#pragma unroll 1
       for (uint32_t i = 0; more; ++i) {
         const uint32_t slot = i % kPieceRing;
-        if (i >= ahead) {
-          const uint32_t last = i - ahead;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + last % kPieceRing), (last / kPieceRing) & 1u, &gave_up));
+#pragma unroll 1
+        for (;;) {
+          const bool counted = whole_units || list == 1;
+          // a whole unit is taken when the one before it is begun
+          const uint32_t ahead = counted ? 1 : kPieceRing, j = i - ahead;
+          if (i >= ahead) ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + j % kPieceRing), (j / kPieceRing) & 1u, &gave_up));
           if (!ok) break;
+          more = __any_sync(0xffffffffu, counted ? claim() : pc.next(p)) != 0;
+          if (more || list == 1 || !p.own_lens) break;
+          list = 1, base = -32, before = upto = 0;
         }
-        more = __any_sync(0xffffffffu, whole_units ? claim() : pc.next(p)) != 0;
+        if (!ok) break;
         if (lane == 0) {
           QueryPiece x{};
           if (more) {
@@ -730,6 +771,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             x.nq = pc.s.nq;
             x.kv = pc.s.kv;
             x.flags = (pc.dual() ? kTwoTiles : 0) | (begins ? kBegins : 0) | (whole ? kWhole : 0);
+            if (list == 1) {
+              x.flags |= kOwn;
+              x.lo = part * kOwnTokens;
+              x.hi = min(x.lo + kOwnTokens, pc.s.kv);
+            }
             if (begins && !whole) {
               // the chunks that the unit lies in
               const long long first = pc.pos - pc.off;
@@ -769,7 +815,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         page = -1;
         if (t >= pc.lo && t < pc.hi) {
           pg = int(fast_div(uint32_t(t), p.fd_page));
-          page = __ldg(p.table + int64_t(pc.b) * p.t_sb + pg);
+          const bool own = pc.flags & kOwn;
+          page = __ldg((own ? p.own_table : p.table) + int64_t(pc.b) * (own ? p.own_t_sb : p.t_sb) + pg);
         }
       };
       // By TMA, K and V of whole boxes, present or not (one that is not lies behind the rows
@@ -911,7 +958,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     int row = 0;
     QueryPiece pc;
     bool more = false, live = false;
-    int64_t out_at = 0, out32_at = 0, lse_at = 0; // where this thread's row lies in out, out32 and lse2, lse
+    // where this thread's row lies in out, in out32 and lse2, in lse: in local memory, since
+    // the blocks need every register
+    volatile int64_t places[3] = {0, 0, 0};
     int lo = 0, hi = 0;                           // the tokens it sees
     uint32_t asked = 0;                           // tiles of Q by TMA
     // The next piece's row, and its Q into shared memory (the products that read the one
@@ -926,9 +975,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       if (live) {
         const QueryRow x = query_row(p, pc.q0, pc.h, pc.row0 + row);
         q_at = x.token * p.q_st + int64_t(x.head) * p.q_sh;
-        out_at = x.token * p.o_st + int64_t(x.head) * p.o_sh;
-        out32_at = x.token * p.Hq + x.head;
-        lse_at = x.token * p.lse_st + x.head;
+        places[0] = x.token * p.o_st + int64_t(x.head) * p.o_sh;
+        places[1] = (int64_t(pc.flags & kOwn ? 1 + pc.t0 / kOwnTokens : 0) * p.N + x.token) * p.Hq + x.head;
+        places[2] = x.token * p.lse_st + x.head;
         query_sees(x.i, pc.nq, pc.kv, p.causal, p.window, &lo, &hi);
         mul = p.scale2;
       }
@@ -1006,7 +1055,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll 1
       for (int j = j0; j < n; j += each) {
         const uint32_t info = (blk + uint32_t(j)) % INFO;
-        uint32_t words[WORDS];
         bool mask = false;
         const int t0 = t_first + j * BN;
         if (any) {                                // what this row does not see
@@ -1014,8 +1062,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           mask = lo > t0 || hi < t0 + BN;
 #pragma unroll
           for (int w = 0; w < WORDS; ++w) {
-            words[w] = there[info][w];
-            mask |= words[w] != ~0u;
+            mask |= there[info][w] != ~0u;
           }
           mask = __any_sync(0xffffffffu, mask);
         }
@@ -1031,21 +1078,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         // maximum is looked for in the usual 64: an exponential above 2^RAISE shows in their sum,
         // and only then (or while a row has no reference) the scores are gone through again,
         // a reference put kAbove from the maximum, and the exponentials taken anew.
-        float e[BN];                              // scores less the reference, in log2
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) tc_ld32(s_at + 32 * w, e + 32 * w);
-#pragma unroll
-        for (int w = 0; w < WORDS; ++w) tc_loaded32(e + 32 * w);
-#pragma unroll
+        float e_all[C::AT_ONCE * 64];             // scores less the reference, in log2
+#pragma unroll C::AT_ONCE
         for (int part = 0; part < PARTS; ++part) {
+          float *const e = e_all + part % C::AT_ONCE * 64;
+          if (part % C::AT_ONCE == 0) {
+#pragma unroll
+            for (int w = 0; w < 2 * C::AT_ONCE; ++w) tc_ld32(s_at + 64 * part + 32 * w, e_all + 32 * w);
+#pragma unroll
+            for (int w = 0; w < 2 * C::AT_ONCE; ++w) tc_loaded32(e_all + 32 * w);
+          }
           const uint64_t times = f32x2(mul, mul), less = f32x2(-mu, -mu);
 #pragma unroll
-          for (int i = 64 * part; i < 64 * part + 64; i += 2) unpack(fma2(f32x2(e[i], e[i + 1]), times, less), e + i);
+          for (int i = 0; i < 64; i += 2) unpack(fma2(f32x2(e[i], e[i + 1]), times, less), e + i);
           if (__builtin_expect(mask, 0)) {
 #pragma unroll
-            for (int w = 2 * part; w < 2 * part + 2; ++w) {
-              const int a = min(32, max(0, lo - t0 - 32 * w)), z = min(32, max(0, hi - t0 - 32 * w));
-              const uint32_t in = words[w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
+            for (int w = 0; w < 2; ++w) {
+              const int a = min(32, max(0, lo - t0 - 64 * part - 32 * w)), z = min(32, max(0, hi - t0 - 64 * part - 32 * w));
+              const uint32_t in = there[info][2 * part + w] & uint32_t((uint64_t(1) << z) - 1u) & ~uint32_t((uint64_t(1) << a) - 1u);
 #pragma unroll
               for (int i = 0; i < 32; ++i) e[32 * w + i] = (in >> i) & 1u ? e[32 * w + i] : -INFINITY;
             }
@@ -1055,14 +1105,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             if (__builtin_expect(again, 0)) {
               float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 64 * part; i < 64 * part + 64; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[i], e[i + 1]);
+              for (int i = 0; i < 64; i += 2) top[(i >> 1) & 3] = max3(top[(i >> 1) & 3], e[i], e[i + 1]);
               const float now = fmaxf(m, fmaxf(max3(top[0], top[1], top[2]), top[3]) + mu - C::ABOVE);
               const float f = m == -INFINITY ? 0.f : exp2_fast(m - now), use = now == -INFINITY ? 0.f : now, by = mu - use;
               m = now;
               mu = use;
               l *= f;
 #pragma unroll
-              for (int i = 64 * part; i < 64 * part + 64; ++i) e[i] += by;
+              for (int i = 0; i < 64; ++i) e[i] += by;
               unset = __any_sync(0xffffffffu, m == -INFINITY);
               if (j > j0 || part > 0) {           // O, once the product with V before this is done
                 const int last = part > 0 ? j : j - each;
@@ -1084,7 +1134,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             // of the place of the scores of word w / 2
             uint64_t sum[2] = {0, 0};             // two pairs of sums
 #pragma unroll
-            for (int w = 2 * part; w < 2 * part + 2; ++w) {
+            for (int w = 0; w < 2; ++w) {
               uint32_t pk[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -1092,7 +1142,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
                 sum[i & 1] = add2(sum[i & 1], f32x2(a, z));
                 pk[i] = pack2<C::BF16>(a, z);
               }
-              tc_st16u(s_at + w * 16, pk);
+              tc_st16u(s_at + (2 * part + w) * 16, pk);
             }
             float x[2];
             unpack(add2(sum[0], sum[1]), x);
@@ -1120,7 +1170,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       blk += uint32_t(n);
       const bool was_live = live, was_any = any;
       const int was_row = row;
-      const int64_t was_out = out_at, was_out32 = out32_at, was_lse = lse_at;
+      const int64_t was_out = places[0], was_out32 = places[1], was_lse = places[2];
       float take0 = 1.f, take1 = 0.f;             // of O, of the other set's
       // The next piece begins, its Q on its way, before the wait for the last product; but the
       // second set of a unit with one tile leaves its sums where its next Q would come.  (A
@@ -1210,7 +1260,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         if (was_live && whole) {
           const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
           if (p.lse2) p.lse2[was_out32] = lse2;
-          if (p.lse) p.lse[was_lse] = lse2 * kLn2;
+          else if (p.lse) p.lse[was_lse] = lse2 * kLn2;
         } else if (was_live) {
           float *const ml = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + C::ROWS * C::DP + was_row;
           __stcg(ml, m);
@@ -1255,7 +1305,7 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int ROWS = QT * kQueryRows, PIECE = ROWS * DP + 2 * ROWS, BN = DP <= 128 ? 128 : 64;
   const int chunk = int(blockIdx.x), col = int(blockIdx.y) * 8;
-  if (chunk == 0 && col == 0 && blockIdx.z == 0 && threadIdx.x == 0) *p.next = 0u;   // ready for the next call
+  if (chunk == 0 && col == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.next[0] = p.next[1] = 0u;   // ready for the next call
   if (col >= p.D) return;
   const int4 at = __ldcg(p.open + chunk);
   if (!query_open(chunk, at.w, int(gridDim.x)) || at.x < 0 || at.x >= p.B || at.y < 0 || at.y >= p.Hkv || at.z < 0) return;
@@ -1300,6 +1350,37 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   const QueryRow out = query_row(p, s.q0, at.y, u.row0 + row);
   query_store8(p, out, col, acc);
   if (col == 0) query_lse(p, out, m, sum);
+}
+
+// Joins the prefix's part of a row with those of its own tokens; a thread for 4 elements.
+constexpr int kEndThreads = 256;
+template <bool BF16>
+__global__ void __launch_bounds__(kEndThreads) prefix_end_kernel(const __grid_constant__ QueryParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t at = int64_t(blockIdx.x) * kEndThreads + threadIdx.x, vecs = p.D / 4;
+  const int64_t rows = int64_t(p.N) * p.Hq, row = at / vecs;
+  if (row >= rows) return;
+  const int col = int(at - row * vecs) * 4, b = int(row / p.Hq), h = int(row - int64_t(b) * p.Hq);
+  const int kv = int(min(int64_t(max(0, __ldg(p.own_lens + b))), int64_t(p.own_pages) * p.P));
+  const int parts = (kv + kOwnTokens - 1) / kOwnTokens;
+  float m = __ldcg(p.lse2 + row), sum = m == -INFINITY ? 0.f : 1.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != -INFINITY) acc = __ldcg(reinterpret_cast<const float4 *>(p.out32 + row * p.D + col));
+  for (int i = 0; i < parts; ++i) {
+    const int64_t x = int64_t(1 + i) * rows + row;
+    const float z = __ldcg(p.lse2 + x);
+    if (z == -INFINITY) continue;
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.out32 + x * p.D + col));
+    const float now = fmaxf(m, z), was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = exp2_fast(z - now);
+    acc = make_float4(acc.x * was + f * v.x, acc.y * was + f * v.y, acc.z * was + f * v.z, acc.w * was + f * v.w);
+    sum = sum * was + f;
+    m = now;
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2 *>(static_cast<char *>(p.out) + 2 * (b * p.o_st + h * p.o_sh + col)) =
+      make_uint2(pack2<BF16>(acc.x * f, acc.y * f), pack2<BF16>(acc.z * f, acc.w * f));
+  if (p.lse && col == 0) p.lse[b * p.lse_st + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 template <class... A, class... B>

@@ -216,30 +216,32 @@ int check_workspace(const void *ws, int64_t have, int64_t need) {
   return HICACHE_OK;
 }
 
-// The workspace of a call over prefixes: decode attention's, the prefixes' part of every
-// row and its log-sum, the query kernel's.
+// The workspace of a call over prefixes: the query kernel's, then in 32 bits the prefixes'
+// part of every row and its log-sum, and those of every kOwnTokens of the sequences' own.
 struct PrefixSpace {
-  int64_t prior, prior_lse2, query, bytes;
+  int64_t out32, lse2, bytes;
 };
-PrefixSpace prefix_space(const hicache::DecodeParams &d) {
+int prefix_space(const hicache::QueryParams &q, PrefixSpace *s) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  PrefixSpace s{};
-  s.prior = up(hicache::decode_space(d, false).bytes);
-  s.prior_lse2 = up(s.prior + int64_t(d.B) * d.Hq * d.D * 4);
-  s.query = up(s.prior_lse2 + int64_t(d.B) * d.Hq * 4);
-  s.bytes = s.query + hicache::query_space(d.D).bytes;
-  return s;
+  const int64_t rows = int64_t(q.N) * q.Hq;       // < 2^31, of at most 256 elements
+  const int64_t parts = 1 + (int64_t(q.own_pages) * q.P + hicache::kOwnTokens - 1) / hicache::kOwnTokens;   // <= 2^19
+  if (parts * rows > (int64_t(1) << 50))
+    return set_error(HICACHE_ERR_INVALID_ARG, "batch * q_heads * max_pages * page_size is too large");
+  s->out32 = hicache::query_space(q.D).bytes;
+  s->lse2 = up(s->out32 + parts * rows * q.D * 4);
+  s->bytes = up(s->lse2 + parts * rows * 4);
+  return HICACHE_OK;
 }
 
-// Points a decode call into its workspace.
-void decode_place(char *ws, const hicache::DecodeSpace &sp, hicache::DecodeParams *p) {
-  p->counters = reinterpret_cast<unsigned int *>(ws);
-  p->cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
-  p->seq_pieces = reinterpret_cast<int2 *>(ws + sp.seq_pieces);
-  p->warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
-  p->lse2 = reinterpret_cast<float *>(ws + sp.lse2);
-  p->scores = reinterpret_cast<float *>(ws + sp.scores);
-  p->score_row = sp.score_row;
+// Checks the sizes of a call over prefixes.
+int prefix_sizes(const Shape &s, int64_t batch, int64_t groups, int64_t q_heads, int64_t head_dim, int64_t max_prefix_pages,
+                 int64_t max_pages, hicache::QueryParams *q) {
+  int rc = query_sizes(s, groups, batch, q_heads, head_dim, max_prefix_pages, q);
+  if (rc) return rc;
+  hicache::DecodeParams d{};
+  if ((rc = decode_sizes(s, batch, q_heads, head_dim, head_dim, max_pages, &d))) return rc;
+  q->own_pages = d.max_pages;
+  return HICACHE_OK;
 }
 
 }  // namespace
@@ -410,6 +412,7 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   if (a->workspace_bytes < sp.bytes)
     return set_error(HICACHE_ERR_INVALID_ARG, "workspace of %lld bytes is below the %lld needed",
                      (long long)a->workspace_bytes, (long long)sp.bytes);
+  char *ws = static_cast<char *>(a->workspace);
   p.q = a->q;
   p.k = k;
   p.v = v;
@@ -419,7 +422,13 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
   p.lse = a->lse;
   p.weights = a->weights;
   p.num_pages = kv->device_num_pages;
-  decode_place(static_cast<char *>(a->workspace), sp, &p);
+  p.counters = reinterpret_cast<unsigned int *>(ws);
+  p.cta_parts = reinterpret_cast<float *>(ws + sp.cta_parts);
+  p.seq_pieces = reinterpret_cast<int2 *>(ws + sp.seq_pieces);
+  p.warp_parts = reinterpret_cast<float *>(ws + sp.warp_parts);
+  p.lse2 = reinterpret_cast<float *>(ws + sp.lse2);
+  p.scores = reinterpret_cast<float *>(ws + sp.scores);
+  p.score_row = sp.score_row;
   p.window = a->window;
   p.bf16 = a->dtype == HICACHE_BF16;
   p.fd_page = hicache::make_fastdiv(uint32_t(s.P));
@@ -518,10 +527,10 @@ int hicache_prefix_workspace(const hicache_pool_desc *desc, int32_t batch, int32
   if (rc) return rc;
   if (!bytes) return set_error(HICACHE_ERR_INVALID_ARG, "bytes is NULL");
   hicache::QueryParams q{};
-  hicache::DecodeParams d{};
-  if ((rc = query_sizes(s, groups, batch, q_heads, head_dim, max_prefix_pages, &q))) return rc;
-  if ((rc = decode_sizes(s, batch, q_heads, head_dim, head_dim, max_pages, &d))) return rc;
-  *bytes = prefix_space(d).bytes;
+  if ((rc = prefix_sizes(s, batch, groups, q_heads, head_dim, max_prefix_pages, max_pages, &q))) return rc;
+  PrefixSpace sp{};
+  if ((rc = prefix_space(q, &sp))) return rc;
+  *bytes = sp.bytes;
   return HICACHE_OK;
 }
 
@@ -535,62 +544,51 @@ int hicache_prefix_attention(const hicache_device_kv *kv, const hicache_pool_des
   if (!a) return set_error(HICACHE_ERR_INVALID_ARG, "the prefix descriptor is NULL");
   if ((rc = check_query_dtype(a->dtype, a->reserved, s, a->k_scale, a->v_scale))) return rc;
   hicache::QueryParams q{};
-  hicache::DecodeParams d{};
-  if ((rc = query_sizes(s, a->groups, a->batch, a->q_heads, a->head_dim, a->max_prefix_pages, &q))) return rc;
-  if ((rc = decode_sizes(s, a->batch, a->q_heads, a->head_dim, a->head_dim, a->max_pages, &d))) return rc;
+  if ((rc = prefix_sizes(s, a->batch, a->groups, a->q_heads, a->head_dim, a->max_prefix_pages, a->max_pages, &q))) return rc;
   if ((rc = check_scale(a->scale, a->k_scale, &q.scale2))) return rc;
+  PrefixSpace sp{};
+  if ((rc = prefix_space(q, &sp))) return rc;
   if (a->batch == 0) return HICACHE_OK;
-  q.q_st = d.q_sb = used(a->q_batch_stride, a->batch);
-  q.q_sh = d.q_sh = used(a->q_head_stride, a->q_heads);
-  d.o_sb = used(a->out_batch_stride, a->batch);
-  d.o_sh = used(a->out_head_stride, a->q_heads);
+  q.q_st = used(a->q_batch_stride, a->batch);
+  q.q_sh = used(a->q_head_stride, a->q_heads);
+  q.o_st = used(a->out_batch_stride, a->batch);
+  q.o_sh = used(a->out_head_stride, a->q_heads);
   q.t_sb = used(a->prefix_stride, a->groups);
-  d.t_sb = used(a->table_stride, a->batch);
-  d.lse_sb = used(a->lse_stride, a->batch);
-  if ((rc = check_heads("q", a->q, d.q_sb, d.q_sh))) return rc;
-  if ((rc = check_heads("out", a->out, d.o_sb, d.o_sh))) return rc;
-  if (!rows_disjoint(a->batch, d.o_sb, a->q_heads, d.o_sh, a->head_dim))
+  q.own_t_sb = used(a->table_stride, a->batch);
+  q.lse_st = used(a->lse_stride, a->batch);
+  if ((rc = check_heads("q", a->q, q.q_st, q.q_sh))) return rc;
+  if ((rc = check_heads("out", a->out, q.o_st, q.o_sh))) return rc;
+  if (!rows_disjoint(a->batch, q.o_st, a->q_heads, q.o_sh, a->head_dim))
     return set_error(HICACHE_ERR_INVALID_ARG, "out: heads overlap one another");
   if ((rc = check_ints({a->page_table, a->seq_lens}, "page_table or seq_lens"))) return rc;
   if (a->groups > 0 &&
       (rc = check_ints({a->group_starts, a->prefix_table, a->prefix_lens}, "group_starts, prefix_table or prefix_lens")))
     return rc;
-  if (!stride_ok(q.t_sb) || !stride_ok(d.t_sb))
+  if (!stride_ok(q.t_sb) || !stride_ok(q.own_t_sb))
     return set_error(HICACHE_ERR_INVALID_ARG, "prefix_stride and table_stride must be in [0, 2^40)");
-  if ((rc = check_lse(a->lse, d.lse_sb, a->batch, a->q_heads))) return rc;
-  const PrefixSpace sp = prefix_space(d);
+  if ((rc = check_lse(a->lse, q.lse_st, a->batch, a->q_heads))) return rc;
   if ((rc = check_workspace(a->workspace, a->workspace_bytes, sp.bytes))) return rc;
   char *const ws = static_cast<char *>(a->workspace);
-  q.q = d.q = a->q;
-  q.k = d.k = k;
-  q.v = d.v = v;
-  q.num_pages = d.num_pages = kv->device_num_pages;
-  q.bf16 = d.bf16 = a->dtype == HICACHE_BF16;
-  q.v_scale = d.v_scale = a->v_scale;
+  q.q = a->q;
+  q.k = k;
+  q.v = v;
+  q.out = a->out;
+  q.lse = a->lse;
+  q.num_pages = kv->device_num_pages;
+  q.bf16 = a->dtype == HICACHE_BF16;
+  q.v_scale = a->v_scale;
   q.starts = a->group_starts;
   q.table = a->prefix_table;
   q.lens = a->prefix_lens;
-  q.out32 = reinterpret_cast<float *>(ws + sp.prior);
-  q.lse2 = reinterpret_cast<float *>(ws + sp.prior_lse2);
-  query_place(ws + sp.query, ws, &q);
-  d.out = a->out;
-  d.table = a->page_table;
-  d.lens = a->seq_lens;
-  d.lse = a->lse;
-  d.scale2 = q.scale2;
-  d.decay = 1.f;
-  d.fd_page = q.fd_page;
-  decode_place(ws, hicache::decode_space(d, false), &d);
+  q.own_table = a->page_table;
+  q.own_lens = a->seq_lens;
+  q.out32 = reinterpret_cast<float *>(ws + sp.out32);
+  q.lse2 = reinterpret_cast<float *>(ws + sp.lse2);
+  query_place(ws, ws, &q);
   int n = 0, device = 0;
   const cudaError_t de = cudaGetDevice(&device);
   if (de != cudaSuccess) return cuda_error(de, "cudaGetDevice");
-  int e = 0;
-  if (a->groups > 0) {
-    d.prior = q.out32;
-    d.prior_lse2 = q.lse2;
-    e = hicache::launch_query(q, device, stream, &n);
-  }
-  if (!e) e = hicache::launch_decode(d, device, stream, &n);
+  const int e = hicache::launch_prefix(q, device, stream, &n);
   return launched(e, n, "prefix kernel launch");
 }
 

@@ -53,9 +53,6 @@ struct DecodeParams {
   FastDiv fd_page;            // tokens per page
   float scale2;               // scale * k_scale * log2(e)
   float v_scale, decay;
-  // K/V: what the rows attended to before these tokens, or null: [batch, q_heads, D] and
-  // its base-2 logarithm [batch, q_heads].  The results cover both.
-  const float *prior, *prior_lse2;
 };
 // Query heads of a unit of work (the rows of a product), and the CTAs of a
 // launch: one on each of a GB300's 152 SMs.
@@ -96,14 +93,20 @@ struct QueryParams {
   void *out;
   const int32_t *starts, *table, *lens;
   float *lse;                 // natural logarithm, or null
-  // a prefix's part of a call, instead of out and lse: [tokens, Hq, D] and [tokens, Hq]
-  float *out32, *lse2;
+  // Calls over prefixes: the sequences above are the groups, their queries one of each
+  // sequence, which has tokens of its own besides.  Results in 32 bits and their base-2
+  // logarithms, to be joined: [0] of the prefix [N, Hq, D], [1 + i] of each kOwnTokens of the
+  // sequence's own.
+  float *out32, *lse2;        // else null
+  const int32_t *own_table, *own_lens;
+  int64_t own_t_sb;
+  int32_t own_pages;          // max_pages of own_table
   int64_t q_st, q_sh, o_st, o_sh, t_sb, lse_st;
   int64_t row;                // elements of a cache row
   int64_t num_pages;          // device pages
   // workspace
   unsigned int *error;        // set by a call that gave up waiting
-  unsigned int *next;         // the next whole unit; zero between calls
+  unsigned int *next;         // the next whole unit, the next of the sequences' own; zero between calls
   int4 *open;                 // per chunk of work: the unit that begins in it and goes on, and in how many chunks it lies
   float *parts;               // two per chunk
   int32_t B, N, Hq, Hkv, G, D, P, max_pages, window, causal;
@@ -122,6 +125,8 @@ constexpr int kQueryCtas = 152;                   // one on each of a GB300's SM
 // What beginning and ending a unit takes, in blocks.
 constexpr int kQueryStart = 4;
 HC_HD int32_t query_cost(int32_t blocks) { return blocks > 0 ? blocks + kQueryStart : 0; }
+// The tokens of a unit over a sequence's own.
+constexpr int kOwnTokens = 4096;
 // From so many units for each of them on, CTAs take whole units.
 constexpr int kQueryWhole = 4;
 struct QuerySpace {
@@ -129,6 +134,7 @@ struct QuerySpace {
 };
 QuerySpace query_space(int D);
 int launch_query(const QueryParams &p, int device, void *stream, int *launches);
+int launch_prefix(const QueryParams &p, int device, void *stream, int *launches);
 
 // A unit of work: rows [row0, row0 + rows) of a sequence's nq * G query rows, over
 // blocks [blk0, blk0 + blocks) of the tokens.  Causal: query i of nq sees the tokens up
