@@ -744,7 +744,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll 1
         for (;;) {
           const bool counted = whole_units || list == 1;
-          // a whole unit is taken when the one before it is begun
+          // a whole unit is taken when the one before it is begun, so that none waits at the
+          // end for a CTA that has another to do
           const uint32_t ahead = counted ? 1 : kPieceRing, j = i - ahead;
           if (i >= ahead) ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + j % kPieceRing), (j / kPieceRing) & 1u, &gave_up));
           if (!ok) break;
