@@ -380,3 +380,297 @@ def test_merge_of_parts_is_the_whole():
             want.abs() * ref.UNIT[q.dtype] * 1.01
         assert ((out[i].double() - want).abs() <= tol).all()
         assert ((lse[i].double() - zz).abs() <= bd["dl"] + 4 * zz.abs() * ref.U32 + 2.0 ** -20).all()
+
+
+# ---- what the calls allow beyond the usual one -------------------------------------------
+
+@pytest.mark.parametrize("d,e4,dtype", [(128, False, "bf16"), (64, True, "bf16"), (256, False, "fp16")])
+def test_query_strides(d, e4, dtype):
+    """Heads outside tokens, rows apart, a slice of a wider table, one token, one head."""
+    kv_lens, q_lens, hq, hk = [700, 130], [60, 9], 4, 2
+    cache = Cache([kv_lens], hk, d, 16, dtype, e4, seed=3)
+    n = sum(q_lens)
+    q = queries(n, hq, d, dtype)
+    want, want_z = run_query(cache, q, q_lens, kv_lens, True)
+    check_query(cache, q, q_lens, want, want_z, True)
+    q2 = q.transpose(0, 1).contiguous().transpose(0, 1)                  # [heads][tokens] in memory
+    wide = torch.zeros((n, hq, d + 24), dtype=q.dtype, device="cuda")
+    wide[:, :, :d] = q
+    table = torch.full((2, cache.tables[0].shape[1] + 5), -7, dtype=torch.int32, device="cuda")
+    table[:, 2:-3] = cache.tables[0]
+    ws = workspace(hc.query_workspace(cache.desc, 2, n, hq, d, cache.tables[0].shape[1]))
+    for x in (q2, wide[:, :, :d]):
+        out = torch.full((hq, n, d), 7.0, dtype=q.dtype, device="cuda").transpose(0, 1)
+        lse = torch.full((n, hq + 3), 5.0, device="cuda")
+        hc.query_attention(cache.kv, cache.desc, 0, x, i32([0, 60, 69]), table[:, 2:-3], i32(kv_lens), out, ws, causal=True,
+                           lse=lse[:, :hq], k_scale=cache.k_scale, v_scale=cache.v_scale)
+        assert same(out.contiguous(), want) and same(lse[:, :hq].contiguous(), want_z)
+        assert (lse[:, hq:] == 5.0).all()
+    # one query head of one token, whatever its strides
+    one = q[:1, :1].as_strided((1, 1, d), (3, 1, 1))
+    small = Cache([[300]], 1, d, 16, dtype, e4, seed=5)
+    out, lse = run_query(small, one, [1], [300])
+    check_query(small, one, [1], out, lse)
+
+
+@pytest.mark.parametrize("dtype,e4", [("bf16", False), ("fp16", False), ("fp16", True), ("bf16", True)])
+@pytest.mark.parametrize("k_size,order", [(1.0, 0), (6.0, 0), (6.0, 1), (6.0, -1)])
+def test_query_references(dtype, e4, k_size, order):
+    """Scores that leave the reference far behind, in falling and rising order of the
+    tokens, so that every block moves it."""
+    kv, nq, hq, d = 900, 140, 2, 128
+    cache = Cache([[kv]], 1, d, 16, dtype, e4, seed=7, k_size=k_size)
+    q = queries(nq, hq, d, dtype, sharp=4.0)
+    q[:] = q[:1, :1]                              # all alike, so that one order of the keys serves them
+    if order:
+        k, v = cache.bufs
+        at = present(cache.rows[0][0])
+        s = k.float()[at] @ q[0, 0].float()
+        raw(k)[at] = raw(k)[at][s.argsort(descending=order < 0)]
+    for causal in (False, True):
+        out, lse = run_query(cache, q, [nq], [kv], causal)
+        check_query(cache, q, [nq], out, lse, causal)
+
+
+def same(a, b):
+    return a.shape == b.shape and bool((raw(a) == raw(b)).all())
+
+
+def test_query_infinities():
+    """A key of +-infinity: its weight is none, or everything is NaN, for the queries that
+    see it alone; a NaN key or value is seen by its kv head alone.  The rows of a warp move
+    their references together, so a query before the key can be rounded otherwise than
+    without it: it is held to the bounds against 64 bits."""
+    kv, nq, hq, d = 300, 100, 4, 64
+    cache = Cache([[kv]], 2, d, 16, seed=2)
+    q = queries(nq, hq, d, "bf16").abs()          # positive: scores with +inf are +inf
+    k, v = cache.bufs
+    row = cache.rows[0][0]
+    clean, z = run_query(cache, q, [nq], [kv], causal=True)
+    check_query(cache, q, [nq], clean, z, causal=True)
+    first = [seen(cache.rows[0][0], nq, i, True, 0) for i in range(50)]
+    want = ref.attend(q[:50], *cache.plain(), first, d ** -0.5)
+    for x in (float("inf"), -float("inf"), float("nan")):
+        k[row[250], d:] = x                       # of kv head 1, seen by queries from 50 on
+        out, lse = run_query(cache, q, [nq], [kv], causal=True)
+        assert same(out[:, :2].contiguous(), clean[:, :2].contiguous()) and same(lse[:, :2].contiguous(), z[:, :2].contiguous())
+        ref.check_decode(out[:50], want, q.dtype, torch.bfloat16, lse=lse[:50])
+        if x == -float("inf"):                    # weight 0: as if the token were absent
+            gone = [torch.tensor([r for r in seen(row, nq, i, True, 0).tolist() if r != row[250]], device="cuda")
+                    for i in range(50, nq)]
+            k[row[250], d:] = 0
+            less = ref.attend(q[50:, 2:], *[t[:, 1:] for t in cache.plain()], gone, d ** -0.5)
+            ref.check_decode(out[50:, 2:], less, q.dtype, torch.bfloat16, lse=lse[50:, 2:])
+        else:
+            assert out[50:, 2:].isnan().all() and lse[50:, 2:].isnan().all()
+
+
+def test_bad_starts_and_lengths():
+    """What the host cannot see: starts that descend or leave the rows, lengths below 0 and
+    beyond the table.  Nothing outside the rows is written."""
+    cache = Cache([[200, 200, 200]], 2, 64, 16)
+    q = queries(20, 4, 64, "bf16")
+    ws = workspace(hc.query_workspace(cache.desc, 3, 20, 4, 64, cache.tables[0].shape[1]))
+    guard = torch.full((24, 4, 64), 7.0, dtype=q.dtype, device="cuda")
+    for starts, lens in (([-5, 4, 9, 30], [200, 200, 200]), ([2 ** 31 - 1, 3, -2 ** 31, 5], [200, 200, 200]),
+                         ([0, 10, 5, 20], [200, -1, 200]), ([0, 5, 10, 15], [-2 ** 31, 2 ** 31 - 1, 0])):
+        out = guard.clone()
+        for causal in (False, True):
+            hc.query_attention(cache.kv, cache.desc, 0, q, i32(starts), cache.tables[0], i32(lens), out[2:22], ws,
+                               causal=causal)
+            assert not hc.decode_gave_up(ws)
+            assert (out[:2] == 7.0).all() and (out[22:] == 7.0).all()
+    out = guard.clone()
+    hc.query_attention(cache.kv, cache.desc, 0, q, i32([0, 5, 10, 15]), cache.tables[0], i32([-9, 2 ** 31 - 1, 0]), out[:20], ws)
+    assert (out[:5] == 0).all() and (out[10:15] == 0).all() and (out[15:] == 7.0).all()
+
+
+def test_far_pages():
+    """Pages whose elements lie beyond 2^32 of the buffer's first, by boxes and row by row."""
+    for P, d in ((64, 128), (3, 128)):
+        pages = 5_700_000_000 // (P * d)
+        bufs = [torch.empty((pages * P, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        kv = 5 * P + 2
+        table = i32([[pages - 1 - 7 * i for i in range(6)]])
+        rows = torch.tensor([table[0, t // P].item() * P + t % P for t in range(kv)], device="cuda")
+        for i, b in enumerate(bufs):
+            b[(table[0].long()[:, None] * P + torch.arange(P, device="cuda")).flatten()] = float("nan")
+            b[rows] = torch.randn((kv, d), generator=gen(i), device="cuda").bfloat16()
+        q = queries(30, 4, d, "bf16")
+        dd = desc(P, d, 2)
+        ws = workspace(hc.query_workspace(dd, 1, 30, 4, d, 6))
+        out, lse = torch.zeros_like(q), torch.zeros((30, 4), device="cuda")
+        hc.query_attention(hc.DeviceKV(bufs, pages), dd, 0, q, i32([0, 30]), table, i32([kv]), out, ws, lse=lse)
+        assert not hc.decode_gave_up(ws)
+        k, v = (b[rows].view(kv, 1, d) for b in bufs)
+        want = ref.attend(q, k, v, [torch.arange(kv, device="cuda")] * 30, d ** -0.5)
+        ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)
+        del bufs, k, v
+        torch.cuda.empty_cache()
+
+
+def test_one_workspace_for_many_shapes():
+    """Calls of different shapes one after another over one workspace."""
+    cache = Cache([[900, 40, 3000]], 2, 128, 16, seed=1)
+    shapes = [([700, 1, 300], False), ([1, 1, 1], False), ([300, 40, 1], True), ([2000, 40, 2500], False)]
+    n = max(hc.query_workspace(cache.desc, 3, sum(l), 8, 128, cache.tables[0].shape[1]) for l, _ in shapes)
+    ws = workspace(n)
+    first = []
+    for _ in range(2):
+        got = []
+        for lens, causal in shapes:
+            q = queries(sum(lens), 8, 128, "bf16", seed=sum(lens))
+            got.append((q, lens, causal) + run_query(cache, q, lens, [900, 40, 3000], causal, ws=ws))
+        if first:
+            for a, b in zip(first, got):
+                assert same(a[3], b[3]) and same(a[4], b[4])
+        first = got
+    for q, lens, causal, out, lse in first:
+        check_query(cache, q, lens, out, lse, causal, pick=[0, 1, 39, 200])
+
+
+def test_captured_calls():
+    """All three in a CUDA graph, replayed with other starts, lengths, tables and values."""
+    hq, hk, d, P = 8, 2, 128, 16
+    own, prefix = [40, 0, 300], [600]
+    cache = Cache([prefix, own], hk, d, P, seed=6)
+    q = queries(3, hq, d, "bf16")
+    starts, lens, shared = i32([0, 3]), i32(own), i32(prefix)
+    t0, t1 = cache.tables[0].clone(), cache.tables[1].clone()
+    ws = workspace(hc.prefix_workspace(cache.desc, 3, 1, hq, d, t0.shape[1], t1.shape[1]))
+    ws2 = workspace(hc.query_workspace(cache.desc, 1, 3, hq, d, t0.shape[1]))
+    outs = [torch.zeros_like(q) for _ in range(3)]
+    lses = [torch.zeros((3, hq), device="cuda") for _ in range(3)]
+
+    def calls():
+        hc.prefix_attention(cache.kv, cache.desc, 0, q, starts, t0, shared, t1, lens, outs[0], ws, lse=lses[0])
+        hc.query_attention(cache.kv, cache.desc, 0, q, starts, t0, shared, outs[1], ws2, lse=lses[1])
+        hc.merge_attention(outs[:2], lses[:2], outs[2], lse=lses[2])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for i, (s, n, l) in enumerate((([0, 3], [600], own), ([1, 2], [77], [1, 299, 0]), ([0, 0], [600], [40, 0, 300]),
+                                   ([0, 3], [0], [0, 0, 0]))):
+        starts.copy_(i32(s))
+        shared.copy_(i32(n))
+        lens.copy_(i32(l))
+        q.copy_(queries(3, hq, d, "bf16", seed=20 + i))
+        for x in outs[:2]:
+            x.fill_(3.0)
+        for z in lses[:2]:
+            z.fill_(-INF)
+        graph.replay()
+        got = [x.clone() for x in outs + lses]
+        for x in outs[:2]:
+            x.fill_(3.0)
+        for z in lses[:2]:
+            z.fill_(-INF)
+        calls()
+        for a, b in zip(got, outs + lses):
+            assert same(a, b)
+
+
+def test_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    cache = Cache([[2000, 700]], 2, 128, 16, seed=2)
+    lens = [2000, 700]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    q = [queries(900, 8, 128, "bf16", seed=i) for i in range(2)]
+    ws = [workspace(hc.query_workspace(cache.desc, 2, 900, 8, 128, cache.tables[0].shape[1])) for _ in range(2)]
+    outs = [[torch.zeros_like(q[0]) for _ in range(6)] for _ in range(2)]
+    starts, kl = i32([0, 300, 900]), i32(lens)
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i, st in enumerate(streams):
+            hc.query_attention(cache.kv, cache.desc, 0, q[i], starts, cache.tables[0], kl, outs[i][r], ws[i], causal=i == 0,
+                               stream=st)
+    torch.cuda.synchronize()
+    for i in range(2):
+        want, z = run_query(cache, q[i], [300, 600], lens, i == 0)
+        check_query(cache, q[i], [300, 600], want, z, i == 0, pick=[0, 299, 400])
+        for x in outs[i]:
+            assert same(x, want)
+
+
+def test_grad_is_refused():
+    cache = Cache([[100]], 2, 64, 16)
+    q = queries(4, 4, 64, "bf16")
+    ws = workspace(hc.query_workspace(cache.desc, 1, 4, 4, 64, cache.tables[0].shape[1]))
+    out = torch.zeros_like(q).requires_grad_()
+    with pytest.raises(ValueError, match="requires grad"):
+        hc.query_attention(cache.kv, cache.desc, 0, q, i32([0, 4]), cache.tables[0], i32([100]), out, ws)
+    with pytest.raises(ValueError, match="requires grad"):
+        hc.merge_attention([q], [torch.zeros((4, 4), device="cuda")], out)
+    with torch.no_grad():
+        hc.query_attention(cache.kv, cache.desc, 0, q, i32([0, 4]), cache.tables[0], i32([100]), out, ws)
+
+
+def test_serving_run():
+    """A prompt whose prefix is in L2: the prefix is loaded, the rest appended and attended
+    to in chunks; then samples that share the prompt are decoded, their own tokens
+    appended; a two-level tree by queries and merge gives the same."""
+    hq, hk, d, P, dt = 8, 2, 128, 16, torch.bfloat16
+    prompt, cached, samples, steps = 300, 160, 3, 4
+    g = gen(11)
+    pages = 64
+    bufs = [torch.full((pages * P, hk * d), float("nan"), dtype=dt, device="cuda") for _ in range(2)]
+    kv = hc.DeviceKV(bufs, pages)
+    k_all = torch.randn((prompt + samples * steps, hk, d), generator=g, device="cuda").to(dt)
+    v_all = torch.randn((prompt + samples * steps, hk, d), generator=g, device="cuda").to(dt)
+    with hc.Pool(1, 2, P, hk * d, 32, "page_first") as pool:
+        # the prefix was computed before, backed up, and comes back into other pages
+        first = list(range(40, 40 + cached // P))
+        slots = torch.tensor([first[t // P] * P + t % P for t in range(cached)], device="cuda")
+        hc.append_kv(kv, pool, 0, None, k_all[:cached], v_all[:cached], slots)
+        torch.cuda.synchronize()
+        pool.backup(kv, first, list(range(len(first))))
+        torch.cuda.synchronize()
+        for b in bufs:
+            b.fill_(float("nan"))
+        mine = [3, 9, 1, 30, 22, 5, 6, 17, 8, 11, 2, 33, 21, 50, 51, 52, 53, 54, 55]
+        pool.load(kv, mine[:len(first)], list(range(len(first))))
+        torch.cuda.synchronize()
+        table = i32([mine])
+        q = torch.randn((prompt - cached, hq, d), generator=g, device="cuda").to(dt)
+        out, lse = torch.zeros_like(q), torch.zeros((prompt - cached, hq), device="cuda")
+        ws = workspace(hc.query_workspace(pool, 1, 140, hq, d, len(mine)))
+        for a, z in ((cached, 230), (230, prompt)):
+            slots = torch.tensor([mine[t // P] * P + t % P for t in range(a, z)], device="cuda")
+            hc.append_kv(kv, pool, 0, None, k_all[a:z], v_all[a:z], slots)
+            part = slice(a - cached, z - cached)
+            hc.query_attention(kv, pool, 0, q[part], i32([0, z - a]), table, i32([z]), out[part], ws, causal=True, lse=lse[part])
+        want = ref.attend(q, k_all, v_all, [torch.arange(cached + i + 1, device="cuda") for i in range(prompt - cached)], d ** -0.5)
+        ref.check_decode(out, want, dt, dt, lse=lse)
+        # samples: each step stores one token of each, then attends
+        own = i32([[40 + s] for s in range(samples)])
+        wp = workspace(hc.prefix_workspace(pool, samples, 1, hq, d, len(mine), 1))
+        for step in range(steps):
+            rows = prompt + torch.arange(samples, device="cuda") * steps + step
+            hc.append_kv(kv, pool, 0, None, k_all[rows], v_all[rows], (own[:, 0] * P + step).long())
+            x = torch.randn((samples, hq, d), generator=g, device="cuda").to(dt)
+            o, z = torch.zeros_like(x), torch.zeros((samples, hq), device="cuda")
+            hc.prefix_attention(kv, pool, 0, x, i32([0, samples]), table, i32([prompt]), own, i32([step + 1] * samples), o, wp,
+                                lse=z)
+            seen_rows = [torch.cat([torch.arange(prompt, device="cuda"), prompt + s * steps + torch.arange(step + 1, device="cuda")])
+                         for s in range(samples)]
+            want = ref.attend(x, k_all, v_all, seen_rows, d ** -0.5, joins=2)
+            ref.check_decode(o, want, dt, dt, lse=z)
+        # the same from two levels, joined
+        parts, sums = [torch.zeros_like(x) for _ in range(2)], [torch.zeros((samples, hq), device="cuda") for _ in range(2)]
+        hc.query_attention(kv, pool, 0, x, i32([0, samples]), table, i32([prompt]), parts[0], ws, lse=sums[0])
+        wd = workspace(hc.decode_workspace(pool, samples, hq, d, d, 1))
+        hc.decode_attention(kv, pool, 0, x, own, i32([steps] * samples), parts[1], wd, lse=sums[1])
+        both, z2 = torch.zeros_like(x), torch.zeros((samples, hq), device="cuda")
+        hc.merge_attention(parts, sums, both, lse=z2)
+        for i, (w, zz, _, bd) in enumerate(want):
+            tol = bd["spread"] * (2 * ref.UNIT[dt] * 1.01 + bd["de"][:, None] + 2 * bd["n"] * ref.U32) + w.abs() * ref.UNIT[dt] * 1.01
+            assert ((both[i].double() - w).abs() <= tol).all()
+            assert ((z2[i].double() - zz).abs() <= bd["dl"] + 4 * zz.abs() * ref.U32 + 2.0 ** -20).all()
+        for w in (ws, wp, wd):
+            assert not hc.decode_gave_up(w)
