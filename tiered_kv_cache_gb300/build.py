@@ -1,6 +1,6 @@
 """Build libhicache.so in-tree with nvcc for sm_103a (GB300).
 
-Sixteen translation units, compiled in parallel, linked with the static CUDA
+Seventeen translation units, compiled in parallel, linked with the static CUDA
 runtime so the library loads on a machine without a GPU driver (and the
 kernel file a second time with HICACHE_CHECKED=1 for libhicache_checked.so,
 the bounds-checked build):
@@ -18,6 +18,7 @@ the bounds-checked build):
   csrc/hicache_decode.cu     attention of one new token over a paged cache
   csrc/hicache_decode_latent.cu  the same over a latent cache
   csrc/hicache_query.cu      attention of many queries over a paged cache
+  csrc/hicache_prefix.cu     the same of groups that share a prefix
   csrc/hicache_merge.cu      results over parts of the tokens, joined
   csrc/hicache_evict.cu      eviction of pages by accumulated attention weight
 """
@@ -42,7 +43,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 SOURCES = ["hicache_kernels.cu", "hicache_api.cpp", "hicache_index.cpp", "hicache_pipeline.cpp",
            "hicache_plan.cpp", "hicache_group.cpp", "hicache_alloc.cpp", "hicache_engine.cpp",
            "hicache_tp.cpp", "hicache_serving.cpp", "hicache_append.cu", "hicache_decode.cu",
-           "hicache_decode_latent.cu", "hicache_query.cu", "hicache_merge.cu", "hicache_evict.cu"]
+           "hicache_decode_latent.cu", "hicache_query.cu", "hicache_prefix.cu", "hicache_merge.cu", "hicache_evict.cu"]
 
 
 def _nvcc() -> str:

@@ -32,14 +32,4 @@ int launch_query(const QueryParams &p, int device, void *stream, int *launches) 
   return launch_query_type<kQFp16>(p, device, st, launches);
 }
 
-int launch_prefix(const QueryParams &p, int device, void *stream, int *launches) {
-  int e = launch_query(p, device, stream, launches);
-  if (e) return e;
-  const int64_t blocks = (int64_t(p.N) * p.Hq * (p.D / 4) + kEndThreads - 1) / kEndThreads;
-  e = query_launch(p.bf16 ? prefix_end_kernel<true> : prefix_end_kernel<false>, dim3(unsigned(blocks)), kEndThreads,
-                   static_cast<cudaStream_t>(stream), 0, p);
-  *launches += e == 0;
-  return e;
-}
-
 }  // namespace hicache

@@ -48,10 +48,14 @@ namespace {
 
 enum : int { kQBf16 = 0, kQFp16 = 1, kQE4m3 = 2 };   // element types of the cache
 
-template <int DP_, int TYPE_>
+// OWN: a prefix call's, whose units are the groups' prefixes and then the sequences' own
+// tokens, with results in 32 bits for prefix_end_kernel; of its own, since the code for both in one
+// kernel costs a call without groups 5 to 9% (8,192 queries at themselves: 411 -> 445 us).
+template <int DP_, int TYPE_, bool OWN_ = false>
 struct QueryConfig {
   static constexpr int DP = DP_;                  // head_dim, padded
   static constexpr int TYPE = TYPE_;
+  static constexpr bool OWN = OWN_;
   static constexpr bool BF16 = TYPE_ == kQBf16;   // the products' type, else fp16
   static constexpr int ES = TYPE_ == kQE4m3 ? 1 : 2;
   static constexpr int QT = DP_ <= 128 ? 2 : 1;   // tiles of rows
@@ -505,14 +509,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll 1
     for (uint32_t i = tid; i < rows * p.Hkv; i += THREADS) {
       const QueryRow x = query_row(p, s.q0, int(i / rows), int(i % rows));
-      char *const at = p.out32 ? reinterpret_cast<char *>(p.out32 + (x.token * p.Hq + x.head) * p.D)
-                               : static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh);
+      char *const at = C::OWN ? reinterpret_cast<char *>(p.out32 + (x.token * p.Hq + x.head) * p.D)
+                              : static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh);
 #pragma unroll 1
-      for (int c = 0; c < p.D * (p.out32 ? 4 : 2); c += 16) *reinterpret_cast<uint4 *>(at + c) = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < p.D * (C::OWN ? 4 : 2); c += 16) *reinterpret_cast<uint4 *>(at + c) = make_uint4(0u, 0u, 0u, 0u);
       query_lse(p, x, 0.f, 0.f);
     }
   }
-  if (p.lse2) {                                   // rows of no sequence
+  if (C::OWN) {                                   // rows of no sequence
     const int s0 = p.B > 0 ? min(max(__ldg(p.starts), 0), p.N) : 0;
     const int s1 = p.B > 0 ? min(max(__ldg(p.starts + p.B), s0), p.N) : 0;
 #pragma unroll 1
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (blockIdx.x >= chunks && !p.own_lens) return;
+  if (blockIdx.x >= chunks && !C::OWN) return;
   if (q_s & 1023u) {                              // the tiles' swizzle counts on it
     if (tid == 0) *p.error = 1u;
     return;
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       auto group = [&]() {
         const int b = base + lane;
         seq = QuerySeq{0, 0, 0};
-        if (list == 0) {
+        if (!C::OWN || list == 0) {
           if (b < p.B) seq = query_seq(p, b);
           upto = (long long)query_units(seq.nq, p.G, C::ROWS) * p.Hkv;
         } else {
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       };
       auto claim = [&]() {                        // the next whole unit with something to attend to
         for (;;) {
-          long long at = lane == 0 ? (long long)atomicAdd(p.next + list, 1u) : 0;
+          long long at = lane == 0 ? (long long)atomicAdd(p.next + (C::OWN ? list : 0), 1u) : 0;
           at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll 1
           for (;;) {
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             if (at < before + here) break;
             before += here;
             base += 32;
-            if (base >= (list == 0 ? p.B : p.N)) return false;
+            if (base >= (!C::OWN || list == 0 ? p.B : p.N)) return false;
             group();
           }
           const int src = __ffs(int(__ballot_sync(0xffffffffu, before + upto > at))) - 1;
@@ -718,15 +722,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           pc.s.nq = __shfl_sync(0xffffffffu, seq.nq, src);
           pc.s.kv = __shfl_sync(0xffffffffu, seq.kv, src);
           pc.x0 = 0;
-          const int parts = (pc.s.kv + kOwnTokens - 1) / kOwnTokens;
-          pc.units = list == 0 ? query_units(pc.s.nq, p.G, C::ROWS) : own_units * parts;
+          const int parts = C::OWN ? (pc.s.kv + kOwnTokens - 1) / kOwnTokens : 0;
+          pc.units = !C::OWN || list == 0 ? query_units(pc.s.nq, p.G, C::ROWS) : own_units * parts;
           const int i = int(at - (before + __shfl_sync(0xffffffffu, upto, src) - (long long)pc.units * p.Hkv));
           pc.h = i / pc.units;
           const int m = i - pc.h * pc.units;
-          part = list == 0 ? 0 : m / own_units;
-          pc.m = list == 0 ? pc.units - 1 - m : m - part * own_units;
+          part = !C::OWN || list == 0 ? 0 : m / own_units;
+          pc.m = !C::OWN || list == 0 ? pc.units - 1 - m : m - part * own_units;
           pc.u = pc.unit(p, pc.m);
-          if (list == 1) {
+          if (C::OWN && list == 1) {
             pc.u.blk0 = part * (kOwnTokens / BN);
             pc.u.blocks = (min(pc.s.kv - part * kOwnTokens, kOwnTokens) + BN - 1) / BN;
           }
@@ -743,14 +747,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         const uint32_t slot = i % kPieceRing;
 #pragma unroll 1
         for (;;) {
-          const bool counted = whole_units || list == 1;
+          const bool counted = whole_units || (C::OWN && list == 1);
           // a whole unit is taken when the one before it is begun, so that none waits at the
           // end for a CTA that has another to do
           const uint32_t ahead = counted ? 1 : kPieceRing, j = i - ahead;
           if (i >= ahead) ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + j % kPieceRing), (j / kPieceRing) & 1u, &gave_up));
           if (!ok) break;
           more = __any_sync(0xffffffffu, counted ? claim() : pc.next(p)) != 0;
-          if (more || list == 1 || !p.own_lens) break;
+          if (!C::OWN || more || list == 1) break;
           list = 1, base = -32, before = upto = 0;
         }
         if (!ok) break;
@@ -772,7 +776,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             x.nq = pc.s.nq;
             x.kv = pc.s.kv;
             x.flags = (pc.dual() ? kTwoTiles : 0) | (begins ? kBegins : 0) | (whole ? kWhole : 0);
-            if (list == 1) {
+            if (C::OWN && list == 1) {
               x.flags |= kOwn;
               x.lo = part * kOwnTokens;
               x.hi = min(x.lo + kOwnTokens, pc.s.kv);
@@ -816,7 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         page = -1;
         if (t >= pc.lo && t < pc.hi) {
           pg = int(fast_div(uint32_t(t), p.fd_page));
-          const bool own = pc.flags & kOwn;
+          const bool own = C::OWN && (pc.flags & kOwn);
           page = __ldg((own ? p.own_table : p.table) + int64_t(pc.b) * (own ? p.own_t_sb : p.t_sb) + pg);
         }
       };
@@ -957,11 +961,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     uint32_t used0 = 0, used1 = 0, blk = 0;       // uses of this set's lane (of one set: of both); blocks before the piece
     uint32_t shares = 0;                          // pieces whose blocks the sets shared
     int row = 0;
-    QueryPiece pc;
+    QueryPiece pc{};
     bool more = false, live = false;
-    // where this thread's row lies in out, in out32 and lse2, in lse: in local memory, since
-    // the blocks need every register
-    volatile int64_t places[3] = {0, 0, 0};
+    // where this thread's row lies in out and in lse, or in out32 and lse2: in local memory,
+    // since the blocks need every register
+    volatile int64_t places[2] = {0, 0};
     int lo = 0, hi = 0;                           // the tokens it sees
     uint32_t asked = 0;                           // tiles of Q by TMA
     // The next piece's row, and its Q into shared memory (the products that read the one
@@ -976,9 +980,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       if (live) {
         const QueryRow x = query_row(p, pc.q0, pc.h, pc.row0 + row);
         q_at = x.token * p.q_st + int64_t(x.head) * p.q_sh;
-        places[0] = x.token * p.o_st + int64_t(x.head) * p.o_sh;
-        places[1] = (int64_t(pc.flags & kOwn ? 1 + pc.t0 / kOwnTokens : 0) * p.N + x.token) * p.Hq + x.head;
-        places[2] = x.token * p.lse_st + x.head;
+        if constexpr (C::OWN) {
+          places[0] = (int64_t(pc.flags & kOwn ? 1 + pc.t0 / kOwnTokens : 0) * p.N + x.token) * p.Hq + x.head;
+        } else {
+          places[0] = x.token * p.o_st + int64_t(x.head) * p.o_sh;
+          places[1] = x.token * p.lse_st + x.head;
+        }
         query_sees(x.i, pc.nq, pc.kv, p.causal, p.window, &lo, &hi);
         mul = p.scale2;
       }
@@ -1171,7 +1178,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       blk += uint32_t(n);
       const bool was_live = live, was_any = any;
       const int was_row = row;
-      const int64_t was_out = places[0], was_out32 = places[1], was_lse = places[2];
+      const int64_t was_out = places[0], was_lse = places[C::OWN ? 0 : 1];
       float take0 = 1.f, take1 = 0.f;             // of O, of the other set's
       // The next piece begins, its Q on its way, before the wait for the last product; but the
       // second set of a unit with one tile leaves its sums where its next Q would come.  (A
@@ -1221,8 +1228,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         const uint64_t f2 = f32x2(f * take0, f * take0), g2 = f32x2(f * take1, f * take1);
         const bool both = shared && n > 1;
         float *part = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + tile * C::DP * kQueryRows + r;
-        float *const row32 = p.out32 + was_out32 * p.D;
-        char *const row16 = static_cast<char *>(p.out) + 2 * was_out;
+        char *const line = C::OWN ? reinterpret_cast<char *>(p.out32 + was_out * p.D) : static_cast<char *>(p.out) + 2 * was_out;
 #pragma unroll 1
         for (int c = 0; c < d16; c += 32) {
           float o[32];
@@ -1247,20 +1253,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) __stcg(part + i * kQueryRows, o[i]);
             part += 32 * kQueryRows;
-          } else if (p.out32) {
+          } else if (C::OWN) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              if (c + i < p.D) *reinterpret_cast<float4 *>(row32 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              if (c + i < p.D) *reinterpret_cast<float4 *>(line + 4 * (c + i)) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
-              if (c + i < p.D) *reinterpret_cast<uint4 *>(row16 + 2 * (c + i)) = query_pack8<C>(p, o + i);
+              if (c + i < p.D) *reinterpret_cast<uint4 *>(line + 2 * (c + i)) = query_pack8<C>(p, o + i);
           }
         }
         tc_fence_before();
         if (was_live && whole) {
           const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-          if (p.lse2) p.lse2[was_out32] = lse2;
+          if (C::OWN) p.lse2[was_lse] = lse2;
           else if (p.lse) p.lse[was_lse] = lse2 * kLn2;
         } else if (was_live) {
           float *const ml = p.parts + (int64_t(blockIdx.x) * 2 + (begins ? 1 : 0)) * C::PIECE + C::ROWS * C::DP + was_row;
