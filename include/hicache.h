@@ -728,9 +728,9 @@ int hicache_decode_attention(const hicache_device_kv *kv, const hicache_pool_des
  * passes weights), on the current device. */
 int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32_t q_heads, int32_t head_dim,
                              int32_t v_dim, int32_t max_pages, int32_t with_weights, int64_t *bytes);
-/* Whether a call with this workspace has given up: the kernel over a latent cache
- * waits for its own copies and products with a limit of about two seconds, and a
- * wait that runs out (it never should) ends the call with its outputs undefined
+/* Whether a call with this workspace has given up: the kernels over a latent cache
+ * and those of hicache_query_attention and hicache_prefix_attention wait for their
+ * own copies and products with a limit of about two seconds, and a wait that runs out (it never should) ends the call with its outputs undefined
  * and marks the workspace, *gave_up = 1 until `clear`.  Waits for all work of
  * the current device, on every stream; not during a capture.  Errors:
  * INVALID_ARG, ALIGNMENT, CUDA. */
@@ -790,8 +790,9 @@ int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_
  * of group_starts[0], behind group_starts[groups]) have their own tokens alone, and
  * groups may be 0 (the three arrays NULL).  group_starts must ascend, as q_starts of
  * hicache_query_attention.  Absent pages, lengths, strides, types and the workspace
- * (hicache_prefix_workspace bytes; hicache_decode_status) as there; the prefixes'
- * part of a row is kept in 32 bits until it is joined with the rest.
+ * (hicache_prefix_workspace bytes; hicache_decode_status) as there; the prefix's part
+ * of a row and those of each 4,096 tokens of its own are kept in the workspace, in 32
+ * bits, until they are joined.
  * Of several levels of shared prefixes, each is a hicache_query_attention (the queries
  * of the sequences below it), and hicache_merge_attention joins them. */
 typedef struct {
