@@ -756,8 +756,8 @@ int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
  * The products run on the tensor cores with 32-bit sums, exponentials rounded as in
  * hicache_decode_attention.
  * workspace: hicache_query_workspace bytes, under the rules of
- * hicache_decode_attention's; hicache_decode_status tells whether a call with it gave
- * up.  out and lse must not overlap an input or one another.
+ * hicache_decode_attention's, with which it can be shared, one call after another;
+ * hicache_decode_status tells whether a call with it gave up.  out and lse must not overlap an input or one another.
  * K, V caches (num_buffers 2); head_dim: a multiple of 8 (of 16 for e4m3) up to 256;
  * num_tokens * q_heads < 2^31 - 4096; batch up to 65,535. */
 typedef struct {

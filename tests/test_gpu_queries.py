@@ -529,6 +529,80 @@ def test_one_workspace_for_many_shapes():
         check_query(cache, q, lens, out, lse, causal, pick=[0, 1, 39, 200])
 
 
+def test_workspace_shared_with_decode():
+    """One workspace for decode, query and prefix attention, one call after another: what
+    each counts in is zero for the others, whatever their parts hold."""
+    cache = Cache([[900] * 60, [200] * 60], 4, 128, 16, seed=3)
+    hq, d, n = 8, 128, 60
+    q = queries(n, hq, d, "bf16")
+    many = queries(n * 300, hq, d, "bf16", seed=4)          # more units than whole ones need
+    ws = workspace(max(hc.decode_workspace(cache.desc, n, hq, d, d, cache.tables[0].shape[1], True),
+                       hc.query_workspace(cache.desc, n, n * 300, hq, d, cache.tables[0].shape[1]),
+                       hc.prefix_workspace(cache.desc, n, 1, hq, d, cache.tables[0].shape[1], cache.tables[1].shape[1])))
+
+    def calls(w):
+        out, lse = torch.zeros_like(q), torch.zeros((n, hq), device="cuda")
+        weight = torch.zeros(cache.tables[0].shape, device="cuda")
+        hc.decode_attention(cache.kv, cache.desc, 0, q, cache.tables[0], i32([900] * n), out, w[0], lse=lse, weights=weight)
+        big, big_lse = run_query(cache, many, [300] * n, [900] * n, ws=w[1])
+        both, both_lse = torch.zeros_like(q), torch.zeros((n, hq), device="cuda")
+        hc.prefix_attention(cache.kv, cache.desc, 0, q, i32([0, n]), cache.tables[0][:1], i32([900]), cache.tables[1],
+                            i32([200] * n), both, w[2], lse=both_lse)
+        return out, lse, weight, big, big_lse, both, both_lse
+
+    want = calls([workspace(ws.numel()) for _ in range(3)])
+    check_query(cache, many, [300] * n, want[3], want[4], pick=[0, 33])
+    for _ in range(2):
+        assert all(same(a, b) for a, b in zip(calls([ws] * 3), want))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30, 3.0])
+@pytest.mark.parametrize("d,e4", [(64, False), (128, True), (256, False)])
+def test_scales(scale, d, e4):
+    cache = Cache([[300, 40]], 2, d, 16, "bf16", e4, seed=5)
+    q = queries(70, 4, d, "bf16", sharp=0.5)
+    out, lse = run_query(cache, q, [60, 10], [300, 40], True, scale=scale)
+    check_query(cache, q, [60, 10], out, lse, True, scale=scale)
+
+
+@pytest.mark.parametrize("hq,hk,d,causal", [(160, 1, 64, True), (300, 2, 128, False), (129, 1, 256, True)])
+def test_many_heads_a_kv_head(hq, hk, d, causal):
+    """More query heads on a kv head than a tile has rows."""
+    cache = Cache([[200, 140]], hk, d, 16, seed=6)
+    q = queries(13, hq, d, "bf16")
+    out, lse = run_query(cache, q, [3, 10], [200, 140], causal)
+    check_query(cache, q, [3, 10], out, lse, causal)
+
+
+def test_largest_batch():
+    """65,535 sequences of one query, most without tokens."""
+    n, hq, d, P = 65535, 2, 64, 16
+    cache = Cache([[33, 5, 16, 0]], 1, d, P, seed=7)
+    width = cache.tables[0].shape[1]
+    table, lens = torch.full((n, width), -1, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    at = [0, 31, 32, 4095, 4096, 40000, 65534]
+    for j, i in enumerate(at):
+        table[i], lens[i] = cache.tables[0][j % 4], [33, 5, 16, 0][j % 4]
+    q = queries(n, hq, d, "bf16")
+    out, lse = torch.full_like(q, 7.0), torch.full((n, hq), 5.0, device="cuda")
+    ws = workspace(hc.query_workspace(cache.desc, n, n, hq, d, width))
+    starts = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        hc.query_attention(cache.kv, cache.desc, 0, q, starts, table, lens, out, ws, lse=lse)
+        assert not hc.decode_gave_up(ws)
+    want = ref.attend(q[at], *cache.plain(), [present(cache.rows[0][j % 4]) for j in range(len(at))], d ** -0.5)
+    ref.check_decode(out[at], want, q.dtype, torch.bfloat16, lse=lse[at])
+    none = torch.ones(n, dtype=torch.bool, device="cuda")
+    none[at] = False
+    assert (out[none] == 0).all() and (lse[none] == -INF).all()
+    # the same as sequences with tokens of their own, in no group
+    wp = workspace(hc.prefix_workspace(cache.desc, n, 0, hq, d, width, width))
+    out2, lse2 = torch.full_like(q, 7.0), torch.full((n, hq), 5.0, device="cuda")
+    hc.prefix_attention(cache.kv, cache.desc, 0, q, i32([0]), table[:0], i32([]), table, lens, out2, wp, lse=lse2)
+    ref.check_decode(out2[at], want, q.dtype, torch.bfloat16, lse=lse2[at])
+    assert (out2[none] == 0).all() and (lse2[none] == -INF).all()
+
+
 def test_captured_calls():
     """All three in a CUDA graph, replayed with other starts, lengths, tables and values."""
     hq, hk, d, P = 8, 2, 128, 16

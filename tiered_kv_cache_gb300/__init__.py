@@ -1057,7 +1057,8 @@ def prefix_attention(kv: DeviceKV, pool_or_desc, layer: int, q, group_starts, pr
     [group_starts[g], group_starts[g + 1]) (int32 [groups + 1]) attend to the
     prefix_lens[g] tokens on the pages prefix_table[g], read once for all of them,
     and each to the seq_lens[b] tokens on its own pages page_table[b].  Sequences of
-    no group have their own tokens alone.  out as q [batch, q_heads, head_dim]; lse
+    no group have their own tokens alone, and there may be no group (arrays of 0 rows, and
+    one start).  out as q [batch, q_heads, head_dim]; lse
     (optional) [batch, q_heads] over both.  scale: head_dim ** -0.5 unless given;
     stream: torch's current stream unless given."""
     torch = _import_torch()

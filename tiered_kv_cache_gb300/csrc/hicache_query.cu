@@ -18,8 +18,12 @@ QuerySpace query_space(int D) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t rows = kQueryRows * query_tiles(D), chunks = kQueryCtas;
   QuerySpace s;
-  s.next = up((kDecodeCtas + 1) * 4);             // the error word lies where decode attention's does
-  s.open = s.next + 256;
+  // Decode attention's counters and error word come first, and what is zero between calls lies
+  // behind them where it has nothing: one workspace can serve both, one call after another.
+  constexpr int64_t counters = (kDecodeCtas + 1) * 4, next = (counters + 63) / 64 * 64;
+  static_assert(next + 8 <= (counters + 255) / 256 * 256, "the counters lie before decode attention's parts");
+  s.next = next;
+  s.open = up(counters);
   s.parts = up(s.open + chunks * 16);
   s.bytes = up(s.parts + chunks * 2 * (rows * query_cols(D) + 2 * rows) * 4);
   return s;
