@@ -16,7 +16,7 @@
 // Bounds: with N rows a byte of the cache takes N multiply-adds of 2-byte elements, so
 // from 280 rows on the tensor cores bind, below that HBM.  8 sequences of 2,048 queries over
 // 4,001 tokens, 32 heads of 128 on 8: 700 us, 1,530 TFLOP/s, 80% of a large library product's
-// rate; 8,191 queries of one prompt at themselves: 421 us, 1,300 TFLOP/s.  A step of the tensor
+// rate; 8,191 queries of one prompt at themselves: 415 us, 1,320 TFLOP/s.  A step of the tensor
 // cores for 128 rows takes 64 clocks whatever its operands come from, and the exponentials of
 // two tiles 60% of the products' time on the units that compute them, so each hides behind the other
 // as long as nobody waits.
@@ -418,6 +418,30 @@ __device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRo
   }
   char *at = static_cast<char *>(p.out) + 2 * (x.token * p.o_st + int64_t(x.head) * p.o_sh + col);
   *reinterpret_cast<uint4 *>(at) = p.bf16 ? query_pack8<QueryConfig<64, kQBf16>>(p, v) : query_pack8<QueryConfig<64, kQFp16>>(p, v);
+}
+
+// The boxes of V in `rows` row by row, zeros beyond [lo, hi); by one warp.  Not inlined: it is rare,
+// and with it inlined what the products bind lost 3% (8 x 2,048 queries 700 -> 721 us).
+__device__ __noinline__ void copy_cut_boxes(uint32_t rows, const char *v, int64_t pitch, int y, int box_r, int box_c, int box, int d,
+                                            uint32_t at, uint32_t atom, int t_lo, int t_hi) {
+  const int lane = int(threadIdx.x) & 31;
+#pragma unroll 1
+  for (; rows; rows &= rows - 1u) {
+    const int src = __ffs(int(rows)) - 1;
+    const int64_t y0 = __shfl_sync(0xffffffffu, y, src);
+    const int r0 = __shfl_sync(0xffffffffu, box_r, src), c0 = __shfl_sync(0xffffffffu, box_c, src);
+    const int c = lane & 7, col = c0 + c * 8;     // 8 lanes a row of 128 bytes
+#pragma unroll 1
+    for (int i = lane >> 3; i < box; i += 4) {
+      const int x = r0 + i;
+      const bool in = x >= t_lo && x < t_hi;
+      if (col < d)
+        cp_async16(at + uint32_t(c0 >> 6) * atom + x * 128 + ((c ^ (x & 7)) << 4), in ? v + (y0 + i) * pitch + col * 2 : v,
+                   in ? 16 : 0);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  proxy_fence();
 }
 
 template <class C>
@@ -853,13 +877,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           page = __ldg((own ? p.own_table : p.table) + int64_t(pc.b) * (own ? p.own_t_sb : p.t_sb) + pg);
         }
       };
-      // By TMA, K and V of whole boxes, present or not (one that is not lies behind the rows
-      // and reads as zeros).  Of a block in which the range of tokens cuts a box only K: what
-      // it holds beyond the range is masked, but V there might be no number, and 0 times that is
-      // none either.  That V comes row by row.
-      auto boxes = [&](int t0) {
-        return (max(pc.lo - t0, 0) & (maps.box - 1)) == 0 && (min(pc.hi - t0, BN) & (maps.box - 1)) == 0;
-      };
+      // By TMA, boxes present or not (one that is not lies behind the rows and reads as zeros).
+      // Where the range of tokens cuts a box, what it holds beyond the range is masked in K, but V
+      // there might be no number, and 0 times that is none either: that box of V comes row by row,
+      // zeros beyond the range, by the warp whose turn it is (by all four together, which had to
+      // meet for it, 32 ragged encoders took 53 us in place of 49; heads of 256, whose boxes are the largest, lose 2%).
       const bool by_box = C::TYPE != kQE4m3 && maps.box > 0;
       if (!by_box) lookup(pc.t0 + pt);
       if constexpr (C::TYPE == kQE4m3) {
@@ -925,9 +947,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       }
       for (int x = 0; ok && x < pc.n; ++x, ++blk) {
         const int t0 = pc.t0 + x * BN;
-        int kv0 = 0;                              // the tiles from which on rows are copied one by one
         if (by_box) {
-          kv0 = boxes(t0) ? 2 : 1;
           if (blk % 3u == uint32_t(pt >> 5)) {
             // the page of the box's first token that is in the range
             const int t = max(t0 + box_r, pc.lo);
@@ -944,42 +964,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(KNOWN + blk % INFO), 4);
+            const uint32_t cut = __ballot_sync(0xffffffffu, have && (t0 + box_r < pc.lo || t0 + box_r + maps.box > pc.hi));
 #pragma unroll 1
-            for (int kv = 0; kv < kv0; ++kv) {
+            for (int kv = 0; kv < 2; ++kv) {
               if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
               if (!ok) break;
-              if (lane == 0) mbar_expect(bar(FULL + stage), uint32_t(columns) * C::ATOM_B);
-              if (lane == 1) mbar_arrive(bar(FULL + stage), 127);
+              uint32_t rows = kv ? cut : 0u;      // boxes that come row by row
+              const uint32_t full = bar(FULL + stage), at = ring_s + stage * C::TILE_B;
+              if (lane == 0) mbar_expect(full, uint32_t(boxes_all - __popc(rows)) * uint32_t(maps.box) * 128u);
+              if (lane == 1 && !rows) mbar_arrive(full, 127);
               __syncwarp();
-              if (lane < boxes_all)
-                tma_box(ring_s + stage * C::TILE_B + (box_c >> 6) * C::ATOM_B + box_r * 128, kv ? &maps.v : &maps.k,
-                        pc.h * p.D + box_c, y, bar(FULL + stage));
+              if (lane < boxes_all && !(rows >> lane & 1u))
+                tma_box(at + (box_c >> 6) * C::ATOM_B + box_r * 128, kv ? &maps.v : &maps.k, pc.h * p.D + box_c, y, full);
+              if (rows) {
+                copy_cut_boxes(rows, static_cast<const char *>(p.v) + int64_t(pc.h) * p.D * 2, p.row * 2, y, box_r, box_c, maps.box,
+                               p.D, at, C::ATOM_B, pc.lo - t0, pc.hi - t0);
+                mbar_arrive(full, lane == 0 ? 3 : 4);
+              }
               advance();
             }
           } else {
-            for (int kv = 0; kv < kv0; ++kv) advance();
+            advance();
+            advance();
           }
           if (!ok) break;
-          if (kv0 == 2) continue;
-          lookup(t0 + pt);
-          // among boxes the warps are not together: none may still read the places of two blocks ago
-          together();
-          if (!ok) break;
+          continue;
         }
         const bool have = pt < BN && page_present(page, p.num_pages);
         int64_t *const at = offs[blk & 1u];
         if (pt < BN) at[pt] = have ? int64_t(page) * p.P + (t0 + pt - pg * p.P) : -1;
-        if (!by_box) {
-          const uint32_t word = __ballot_sync(0xffffffffu, have);
-          if (lane == 0) {
-            if (pt < BN) there[blk % INFO][pt >> 5] = word;
-            mbar_arrive(bar(KNOWN + blk % INFO));
-          }
+        const uint32_t word = __ballot_sync(0xffffffffu, have);
+        if (lane == 0) {
+          if (pt < BN) there[blk % INFO][pt >> 5] = word;
+          mbar_arrive(bar(KNOWN + blk % INFO));
         }
         together();
-        if (!by_box && x + 1 < pc.n) lookup(t0 + BN + pt);
+        if (x + 1 < pc.n) lookup(t0 + BN + pt);
 #pragma unroll 1
-        for (int kv = kv0; kv < 2; ++kv) {
+        for (int kv = 0; kv < 2; ++kv) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(EMPTY + stage), uint32_t(phase), &gave_up));
           if (!ok) break;
           const char *src = static_cast<const char *>(kv ? p.v : p.k) + int64_t(pc.h) * p.D * C::ES;
@@ -998,13 +1020,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
                 }
               }
             }
-            if (relayed) {
-              mbar_arrive_copies(bar(FULL + stage));
-            } else {                              // a block among boxes: here and visible at once
-              asm volatile("cp.async.wait_all;" ::: "memory");
-              proxy_fence();
-              mbar_arrive(bar(FULL + stage));
-            }
+            mbar_arrive_copies(bar(FULL + stage));
           }
           advance();
         }
@@ -1490,7 +1506,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_call() {
 }
 
 // Describes q and the layer's buffers to TMA where its boxes fit: pages of whole boxes of 16 rows
-// or more (32 ragged encoders on pages of 16: 54 us, 71 row by row; 64 sequences on a prefix
+// or more (32 ragged encoders on pages of 16: 49 us, 71 row by row; 64 sequences on a prefix
 // of 32,768: 91, 100; with fewer rows a block would take more requests than a warp has lanes), heads that the products'
 // steps of 16 cover (what a box holds behind the head is not used), rows within a
 // coordinate.  Else, or where the driver will not, the copies go row by row.
