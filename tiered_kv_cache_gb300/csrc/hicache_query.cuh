@@ -18,7 +18,7 @@
 // 4,001 tokens, 32 heads of 128 on 8: 700 us, 1,530 TFLOP/s, 80% of a large library product's
 // rate; 8,191 queries of one prompt at themselves: 415 us, 1,320 TFLOP/s.  A step of the tensor
 // cores for 128 rows takes 64 clocks whatever its operands come from, and the exponentials of
-// two tiles 60% of the products' time on the units that compute them, so each hides behind the other
+// two tiles half of the products' time on the units that compute them, so each hides behind the other
 // as long as nobody waits.
 //
 // Softmax: a thread per row, so that maximum and sum need no other thread.  What a row's
