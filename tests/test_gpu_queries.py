@@ -465,6 +465,22 @@ def test_query_infinities():
             assert out[50:, 2:].isnan().all() and lse[50:, 2:].isnan().all()
 
 
+@pytest.mark.parametrize("d,P,dtype,e4", [(128, 16, "bf16", False), (128, 64, "fp16", False), (256, 128, "bf16", False),
+                                          (64, 5, "fp16", False), (80, 32, "bf16", False), (128, 16, "fp16", True)])
+def test_anything_before_the_windows(d, P, dtype, e4):
+    """Tokens that no query's window reaches, K and V, hold NaN: in the box, block and page of
+    the first one that counts too."""
+    kv, nq, window = 500, 20, 100
+    cache = Cache([[kv]], 2, d, P, dtype, e4, seed=4)
+    q = queries(nq, 4, d, dtype)
+    want, z = run_query(cache, q, [nq], [kv], causal=True, window=window)
+    check_query(cache, q, [nq], want, z, causal=True, window=window)
+    for buf in cache.bufs:
+        raw(buf)[present(cache.rows[0][0][:kv - nq - window + 1])] = 0x7F if e4 else -1
+    out, lse = run_query(cache, q, [nq], [kv], causal=True, window=window)
+    assert same(out, want) and same(lse, z)
+
+
 def test_bad_starts_and_lengths():
     """What the host cannot see: starts that descend or leave the rows, lengths below 0 and
     beyond the table.  Nothing outside the rows is written."""
