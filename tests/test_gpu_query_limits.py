@@ -1,0 +1,42 @@
+"""Query and prefix attention at the limits of what the calls accept, against plain 64-bit forms."""
+import pytest
+import torch
+
+import serving_reference as ref
+import tiered_kv_cache_gb300 as hc
+from test_gpu_queries import Cache, check_prefix, desc, gen, i32, present, queries, raw, run_query, same, workspace
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def far_apart(P, d, width, at, lens):
+    """A small cache, and tables of `width` pages of which those of the lists `at` are there:
+    (kv, descriptor, table, rows of each sequence's tokens, k, v)."""
+    pages = sum(map(len, at))
+    bufs = [torch.randn((pages * P, d), generator=gen(i), device="cuda").bfloat16() for i in range(2)]
+    table = torch.full((len(at), width), -1, dtype=torch.int32, device="cuda")
+    rows, page = [], 0
+    for b, some in enumerate(at):
+        mine = []
+        for x in some:
+            table[b, x] = page
+            mine += [page * P + t for t in range(P) if x * P + t < lens[b]]
+            page += 1
+        rows.append(torch.tensor(mine, dtype=torch.long, device="cuda"))
+    return hc.DeviceKV(bufs, pages), desc(P, d, 2), table, rows, *[b.view(-1, 1, d) for b in bufs]
+
+
+def test_prefix_own_tokens_of_the_longest_table():
+    """As many own tokens as a table can have, most on absent pages, between sequences of a few."""
+    P, d, hq, width = 1000, 64, 2, 2_147_482
+    lens = [1500, width * P, 700, 2 ** 31 - 1, 0, 3]
+    at = [[0, 1], [0, 4, 1_000_000, width - 1], [0], [5, width - 1], [], [0]]
+    kv, dd, table, rows, k, v = far_apart(P, d, width, at, [min(n, width * P) for n in lens])
+    q = queries(len(lens), hq, d, "bf16")
+    ws = workspace(hc.prefix_workspace(dd, len(lens), 0, hq, d, 1, width))
+    out, lse = torch.full_like(q, 7.0), torch.full((len(lens), hq), 5.0, device="cuda")
+    hc.prefix_attention(kv, dd, 0, q, i32([0]), table[:0], i32([]), table, i32(lens), out, ws, lse=lse)
+    assert not hc.decode_gave_up(ws)
+    want = ref.attend(q, k, v, rows, d ** -0.5, joins=5)
+    ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)

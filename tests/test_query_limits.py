@@ -1,0 +1,47 @@
+"""The arithmetic of query, prefix and merge attention at the limits of the sizes that the
+calls accept, without a GPU."""
+import ctypes
+
+import pytest
+
+import tiered_kv_cache_gb300 as hc
+from test_query_refusals import desc, run_host
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from tiered_kv_cache_gb300 import build
+    build.build()
+
+
+def test_parts_of_own_tokens(tmp_path):
+    """A sequence's own tokens lie in parts of kOwnTokens, each token in one, up to the longest
+    table; the workspace holds as many."""
+    assert run_host(tmp_path, """
+  const long long most = INT_MAX - 1024ll;            // max_pages * page_size
+  for (long long n : {0ll, 1ll, 4095ll, 4096ll, 4097ll, 8192ll, 1000000007ll, most - 4096, most - 3072, most - 3071, most - 1, most}) {
+    const long long want = (n + kOwnTokens - 1) / kOwnTokens;
+    if (own_parts(int32_t(n)) != want) return 1;
+    long long next = 0;
+    for (long long i = want > 3 ? want - 3 : 0; i < want; ++i) {
+      const int32_t lo = int32_t(i) * kOwnTokens;
+      if (i == (want > 3 ? want - 3 : 0)) next = lo;
+      const int32_t hi = own_end(lo, int32_t(n));
+      if (lo != next || hi <= lo || hi - lo > kOwnTokens || hi > n) return 2;
+      next = hi;
+    }
+    if (next != n) return 3;
+  }""") == "ok"
+
+
+def test_workspace_of_the_longest_tables():
+    out = ctypes.c_int64()
+    d = desc(page_size=1000)
+    ask = lambda own: hc.library().hicache_prefix_workspace(ctypes.byref(d), 1, 1, 4, 128, 1, own, ctypes.byref(out))  # noqa: E731
+    sizes = []
+    for pages in (2_147_480, 2_147_482):
+        assert ask(pages) == 0
+        sizes.append(out.value)
+    # 524,288 parts and the prefix's, each of 4 rows of 128 elements and a log-sum in 32 bits
+    assert sizes[0] <= sizes[1] and sizes[1] >= 524_289 * 4 * 129 * 4
+    assert ask(2_147_483) == -1

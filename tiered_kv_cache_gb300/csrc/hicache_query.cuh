@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           upto = (long long)query_units(seq.nq, p.G, C::ROWS) * p.Hkv;
         } else {
           if (b < p.N) seq = QuerySeq{b, 1, int(min(int64_t(max(0, __ldg(p.own_lens + b))), int64_t(p.own_pages) * p.P))};
-          upto = (long long)((seq.kv + kOwnTokens - 1) / kOwnTokens) * own_units * p.Hkv;
+          upto = (long long)own_parts(seq.kv) * own_units * p.Hkv;
         }
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           pc.s.nq = __shfl_sync(0xffffffffu, seq.nq, src);
           pc.s.kv = __shfl_sync(0xffffffffu, seq.kv, src);
           pc.x0 = 0;
-          const int parts = C::OWN ? (pc.s.kv + kOwnTokens - 1) / kOwnTokens : 0;
+          const int parts = C::OWN ? own_parts(pc.s.kv) : 0;
           pc.units = !C::OWN || list == 0 ? query_units(pc.s.nq, p.G, C::ROWS) : own_units * parts;
           const int i = int(at - (before + __shfl_sync(0xffffffffu, upto, src) - (long long)pc.units * p.Hkv));
           pc.h = i / pc.units;
@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           pc.u = pc.unit(p, pc.m);
           if (C::OWN && list == 1) {
             pc.u.blk0 = part * (kOwnTokens / BN);
-            pc.u.blocks = (min(pc.s.kv - part * kOwnTokens, kOwnTokens) + BN - 1) / BN;
+            pc.u.blocks = (own_end(part * kOwnTokens, pc.s.kv) - part * kOwnTokens + BN - 1) / BN;
           }
           pc.x1 = pc.u.blocks;
           if (pc.x1 > 0) return true;
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
             if (C::OWN && list == 1) {
               x.flags |= kOwn;
               x.lo = part * kOwnTokens;
-              x.hi = min(x.lo + kOwnTokens, pc.s.kv);
+              x.hi = own_end(x.lo, pc.s.kv);
             }
             if (begins && !whole) {
               // the chunks that the unit lies in
@@ -1454,7 +1454,7 @@ __global__ void __launch_bounds__(kEndThreads) prefix_end_kernel(const __grid_co
   if (row >= rows) return;
   const int col = int(at - row * vecs) * 4, b = int(row / p.Hq), h = int(row - int64_t(b) * p.Hq);
   const int kv = int(min(int64_t(max(0, __ldg(p.own_lens + b))), int64_t(p.own_pages) * p.P));
-  const int parts = (kv + kOwnTokens - 1) / kOwnTokens;
+  const int parts = own_parts(kv);
   float m = __ldcg(p.lse2 + row), sum = m == -INFINITY ? 0.f : 1.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (m != -INFINITY) acc = __ldcg(reinterpret_cast<const float4 *>(p.out32 + row * p.D + col));

@@ -224,7 +224,7 @@ struct PrefixSpace {
 int prefix_space(const hicache::QueryParams &q, PrefixSpace *s) {
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t rows = int64_t(q.N) * q.Hq;       // < 2^31, of at most 256 elements
-  const int64_t parts = 1 + (int64_t(q.own_pages) * q.P + hicache::kOwnTokens - 1) / hicache::kOwnTokens;   // <= 2^19
+  const int64_t parts = 1 + hicache::own_parts(q.own_pages * q.P);   // <= 2^19 + 1
   if (parts * rows > (int64_t(1) << 50))
     return set_error(HICACHE_ERR_INVALID_ARG, "batch * q_heads * max_pages * page_size is too large");
   s->out32 = hicache::query_space(q.D).bytes;

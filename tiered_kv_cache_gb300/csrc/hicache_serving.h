@@ -130,6 +130,10 @@ HC_HD int32_t query_cost(int32_t blocks) { return blocks > 0 ? blocks + kQuerySt
 // The tokens of a unit over a sequence's own: 16 sequences of 8,000 to 20,000, 32 heads on 8, take
 // 194 us with 1,024, 177 with 4,096, 208 with 32,768; 200 of 100 to 6,000 306, 272, 274.
 constexpr int kOwnTokens = 4096;
+// The parts of so many, and the end of the one that begins at `lo`: no step leaves 32 bits, up to
+// the longest table's 2^31 - 1,025 tokens.
+HC_HD int32_t own_parts(int32_t tokens) { return tokens / kOwnTokens + (tokens % kOwnTokens != 0); }
+HC_HD int32_t own_end(int32_t lo, int32_t tokens) { return tokens - lo < kOwnTokens ? tokens : lo + kOwnTokens; }
 // From so many units for each of them on, CTAs take whole units.  8 x 2,048 queries of 32 heads
 // on 8 (13 for each): 772 us in chunks, 698 whole.  With 2 as the limit 1,500 queries of
 // heads of 256 on 6,001 tokens (2.5 for each) would take 251 us in place of 211, chunks at
