@@ -1286,6 +1286,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
         float2 *const other = reinterpret_cast<float2 *>(q_p + C::QTILE_B) + r;   // in the place of a second tile's Q
         if (tile == 1) {
           *other = make_float2(m, l);
+          proxy_fence();                          // before the next piece's Q comes there by TMA
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(OTHER));
