@@ -4,10 +4,9 @@ import torch
 
 import serving_reference as ref
 import tiered_kv_cache_gb300 as hc
-from test_gpu_queries import Cache, check_prefix, desc, gen, i32, present, queries, raw, run_query, same, workspace
+from test_gpu_queries import desc, gen, i32, queries, workspace
 
 pytestmark = pytest.mark.gpu
-INF = float("inf")
 
 
 def far_apart(P, d, width, at, lens):
@@ -39,4 +38,23 @@ def test_prefix_own_tokens_of_the_longest_table():
     hc.prefix_attention(kv, dd, 0, q, i32([0]), table[:0], i32([]), table, i32(lens), out, ws, lse=lse)
     assert not hc.decode_gave_up(ws)
     want = ref.attend(q, k, v, rows, d ** -0.5, joins=5)
+    ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_query_unit_of_seconds(causal):
+    """One sequence whose tokens keep its CTA busy for longer than any wait may last, among so many
+    that CTAs take whole units."""
+    P, d, hq, n, long = 1024, 64, 1, 700, 600_000_000
+    width = -(-long // P)
+    kv, dd, table, rows, k, v = far_apart(P, d, width, [[0, 3, 300_000, width - 2]], [long])
+    lens = [10] * n
+    lens[5] = long
+    q = queries(n, hq, d, "bf16")
+    ws = workspace(hc.query_workspace(dd, n, n, hq, d, width))
+    out, lse = torch.full_like(q, 7.0), torch.full((n, hq), 5.0, device="cuda")
+    hc.query_attention(kv, dd, 0, q, torch.arange(n + 1, dtype=torch.int32, device="cuda"), table.expand(n, -1), i32(lens), out,
+                       ws, causal=causal, lse=lse)
+    assert not hc.decode_gave_up(ws)
+    want = ref.attend(q, k, v, [rows[0] if x == long else rows[0][:10] for x in lens], d ** -0.5)
     ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)

@@ -249,6 +249,33 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {   // and arrives
   asm volatile("{.reg .b64 t; mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;}" ::"r"(bar), "r"(bytes) : "memory");
 }
+// mbar_wait for what takes as long as the work in hand does: the limit runs from the last end of a
+// phase of `moves`, a barrier that the work in hand ends again and again.
+__device__ __forceinline__ bool mbar_wait_moving(uint32_t bar, uint32_t parity, uint32_t moves, volatile int *gave_up) {
+  auto ended = [](uint32_t b, uint32_t phase) {
+    uint32_t done;
+    asm volatile("{.reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+                 : "=r"(done)
+                 : "r"(b), "r"(phase)
+                 : "memory");
+    return done != 0;
+  };
+  long long since = clock64();
+  for (uint32_t turn = 0; !ended(bar, parity);) {
+    if (*gave_up) return false;
+    const long long now = clock64();
+    if (ended(moves, turn)) {
+      turn ^= 1u;
+      since = now;
+    }
+    if (now - since > kWaitClocks) {
+      *gave_up = int(bar);
+      return false;
+    }
+    __nanosleep(100);
+  }
+  return true;
+}
 
 // A sequence's queries and tokens; starts that do not ascend, or leave the rows there
 // are, hold no query.
@@ -599,15 +626,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   // The next piece, in order: every warp but the planner's takes each of them.
   uint32_t taken = 0;
   bool ok = true;
-  auto take = [&](QueryPiece &x) {
+  auto took = [&](QueryPiece &x, bool there_is) {
     const uint32_t i = taken % kPieceRing;
-    ok = __all_sync(0xffffffffu, mbar_wait(bar(PIECE + i), (taken / kPieceRing) & 1u, &gave_up));
+    ok = __all_sync(0xffffffffu, there_is);
     if (!ok) return false;
     x = ring_of_pieces[i];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(TAKEN + i));
     ++taken;
     return __any_sync(0xffffffffu, x.n > 0) != 0;
+  };
+  auto take = [&](QueryPiece &x) {
+    return took(x, mbar_wait(bar(PIECE + taken % kPieceRing), (taken / kPieceRing) & 1u, &gave_up));
   };
 
   if (warp >= C::MMA_WARP) {
@@ -804,7 +834,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
           // a whole unit is taken when the one before it is begun, so that none waits at the
           // end for a CTA that has another to do
           const uint32_t ahead = counted ? 1 : kPieceRing, j = i - ahead;
-          if (i >= ahead) ok = __all_sync(0xffffffffu, mbar_wait(bar(TAKEN + j % kPieceRing), (j / kPieceRing) & 1u, &gave_up));
+          // (for as long as a piece takes, which nothing bounds)
+          if (i >= ahead)
+            ok = __all_sync(0xffffffffu, mbar_wait_moving(bar(TAKEN + j % kPieceRing), (j / kPieceRing) & 1u, bar(EMPTY), &gave_up));
           if (!ok) break;
           more = __any_sync(0xffffffffu, counted ? claim() : pc.next(p)) != 0;
           if (!C::OWN || more || list == 1) break;
@@ -867,7 +899,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       ok = __all_sync(0xffffffffu, mbar_wait(bar(GROUP), turns++ & 1u, &gave_up));
     };
     QueryPiece pc;
-    while (take(pc)) {
+    // (a warp that has no block's boxes to bring is there a piece ahead of the others, for as long as theirs takes)
+    while (took(pc, mbar_wait_moving(bar(PIECE + taken % kPieceRing), (taken / kPieceRing) & 1u, bar(EMPTY), &gave_up))) {
       int page = -1, pg = 0;
       auto lookup = [&](int t) {
         page = -1;
