@@ -252,29 +252,26 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {   //
 // mbar_wait for what takes as long as the work in hand does: the limit runs from the last end of a
 // phase of `moves`, a barrier that the work in hand ends again and again.
 __device__ __forceinline__ bool mbar_wait_moving(uint32_t bar, uint32_t parity, uint32_t moves, volatile int *gave_up) {
-  auto ended = [](uint32_t b, uint32_t phase) {
-    uint32_t done;
-    asm volatile("{.reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
-                 : "=r"(done)
-                 : "r"(b), "r"(phase)
-                 : "memory");
-    return done != 0;
-  };
-  long long since = clock64();
-  for (uint32_t turn = 0; !ended(bar, parity);) {
+  uint32_t turn = 0;
+  long long since = 0;
+  for (;;) {
+    uint32_t done, moved;
+    asm volatile(
+        "{.reg .pred p, q; mbarrier.try_wait.parity.shared::cta.b64 p, [%2], %3; selp.u32 %0, 1, 0, p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%4], %5; selp.u32 %1, 1, 0, q;}"
+        : "=r"(done), "=r"(moved)
+        : "r"(bar), "r"(parity), "r"(moves), "r"(turn)
+        : "memory");
+    if (done) return true;
     if (*gave_up) return false;
     const long long now = clock64();
-    if (ended(moves, turn)) {
-      turn ^= 1u;
-      since = now;
-    }
+    if (since == 0 || moved) since = now;
+    turn ^= moved;
     if (now - since > kWaitClocks) {
       *gave_up = int(bar);
       return false;
     }
-    __nanosleep(100);
   }
-  return true;
 }
 
 // A sequence's queries and tokens; starts that do not ascend, or leave the rows there
