@@ -45,3 +45,13 @@ def test_workspace_of_the_longest_tables():
     # 524,288 parts and the prefix's, each of 4 rows of 128 elements and a log-sum in 32 bits
     assert sizes[0] <= sizes[1] and sizes[1] >= 524_289 * 4 * 129 * 4
     assert ask(2_147_483) == -1
+
+
+def test_counters_of_units_do_not_wrap(tmp_path):
+    """A call may have more units than 32 bits count: behind 2^32 the counter would begin anew, with
+    units whose place in their sequence is negative."""
+    assert run_host(tmp_path, """
+  const long long parts = own_parts(INT_MAX - 1024), units = 65535ll * parts * query_units(1, 1, 256);
+  QueryParams p{};
+  if (units <= (1ll << 32)) return 1;
+  if (sizeof(*p.next) * CHAR_BIT < 64) return 2;""") == "ok"

@@ -21,7 +21,7 @@ QuerySpace query_space(int D) {
   // Decode attention's counters and error word come first, and what is zero between calls lies
   // behind them where it has nothing: one workspace can serve both, one call after another.
   constexpr int64_t counters = (kDecodeCtas + 1) * 4, next = (counters + 63) / 64 * 64;
-  static_assert(next + 8 <= (counters + 255) / 256 * 256, "the counters lie before decode attention's parts");
+  static_assert(next % 8 == 0 && next + 16 <= (counters + 255) / 256 * 256, "the counters lie before decode attention's parts");
   s.next = next;
   s.open = up(counters);
   s.parts = up(s.open + chunks * 16);

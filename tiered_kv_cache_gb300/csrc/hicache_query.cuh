@@ -785,7 +785,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       };
       auto claim = [&]() {                        // the next whole unit with something to attend to
         for (;;) {
-          long long at = lane == 0 ? (long long)atomicAdd(p.next + (C::OWN ? list : 0), 1u) : 0;
+          long long at = lane == 0 ? (long long)atomicAdd(p.next + (C::OWN ? list : 0), 1ull) : 0;
           at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll 1
           for (;;) {
@@ -1427,7 +1427,7 @@ __global__ void __launch_bounds__(kQueryRows) query_join_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int ROWS = QT * kQueryRows, PIECE = ROWS * DP + 2 * ROWS, BN = DP <= 128 ? 128 : 64;
   const int chunk = int(blockIdx.x), col = int(blockIdx.y) * 8;
-  if (chunk == 0 && col == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.next[0] = p.next[1] = 0u;   // ready for the next call
+  if (chunk == 0 && col == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.next[0] = p.next[1] = 0ull;   // ready for the next call
   if (col >= p.D) return;
   const int4 at = __ldcg(p.open + chunk);
   if (!query_open(chunk, at.w, int(gridDim.x)) || at.x < 0 || at.x >= p.B || at.y < 0 || at.y >= p.Hkv || at.z < 0) return;

@@ -178,7 +178,7 @@ int query_sizes(const Shape &s, int64_t batch, int64_t tokens, int64_t q_heads, 
 void query_place(char *at, void *error, hicache::QueryParams *p) {
   const hicache::QuerySpace sp = hicache::query_space(p->D);
   p->error = static_cast<unsigned int *>(error) + hicache::kDecodeCtas;
-  p->next = reinterpret_cast<unsigned int *>(at + sp.next);
+  p->next = reinterpret_cast<unsigned long long *>(at + sp.next);
   p->open = reinterpret_cast<int4 *>(at + sp.open);
   p->parts = reinterpret_cast<float *>(at + sp.parts);
 }

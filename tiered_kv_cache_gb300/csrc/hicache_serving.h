@@ -106,7 +106,10 @@ struct QueryParams {
   int64_t num_pages;          // device pages
   // workspace
   unsigned int *error;        // set by a call that gave up waiting
-  unsigned int *next;         // the next whole unit, the next of the sequences' own; zero between calls
+  // The next whole unit, the next of the sequences' own; zero between calls.  In 64 bits: own parts
+  // of up to 2^19 for each kv head of 65,535 sequences are more units than 32 bits count, and starts
+  // that descend let sequences share queries.
+  unsigned long long *next;
   int4 *open;                 // per chunk of work: the unit that begins in it and goes on, and in how many chunks it lies
   float *parts;               // two per chunk
   int32_t B, N, Hq, Hkv, G, D, P, max_pages, window, causal;
