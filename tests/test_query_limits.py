@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import tiered_kv_cache_gb300 as hc
-from test_query_refusals import desc, run_host
+from test_query_refusals import desc, merge, run_host
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -55,3 +55,13 @@ def test_counters_of_units_do_not_wrap(tmp_path):
   QueryParams p{};
   if (units <= (1ll << 32)) return 1;
   if (sizeof(*p.next) * CHAR_BIT < 64) return 2;""") == "ok"
+
+
+@pytest.mark.parametrize("heads,stride", [((1 << 25) + 1, 1 << 39), ((1 << 27) - 300, 1 << 38), ((1 << 24) + 1, 1 << 39)])
+def test_merge_refuses_heads_that_overlap(heads, stride):
+    """Rows that lie on one another, of strides that leave 64 bits times the number of heads."""
+    change = dict(n=2, heads=heads, d=8, out_t=stride, out_h=stride, ot=[stride] * 3, oh=[stride] * 3, lt=[heads] * 3, lse_t=heads)
+    assert merge(**change) == "INVALID_ARG"
+    # apart, the call goes on to what is checked next
+    assert merge(**{**change, "out_h": 8, "lse": 4 << 20 | 2}) == "ALIGNMENT"
+    assert merge(**{**change, "out_t": 8, "out_h": 16, "lse": 4 << 20 | 2}) == "ALIGNMENT"

@@ -82,7 +82,7 @@ bool rows_disjoint(int64_t n, int64_t st, int64_t h, int64_t sh, int64_t d) {
   if (n <= 1 && h <= 1) return true;
   if (n <= 1) return sh >= d;
   if (h <= 1) return st >= d;
-  if (st >= sh) return sh >= d && st >= (h - 1) * sh + d;      // h <= 2^20, sh < 2^40
+  if (st >= sh) return sh >= d && st >= d && (st - d) / sh >= h - 1;   // (by quotients: products leave 64 bits)
   return st >= d && (sh - d) / st >= n - 1;
 }
 
