@@ -4,7 +4,7 @@ import torch
 
 import serving_reference as ref
 import tiered_kv_cache_gb300 as hc
-from test_gpu_queries import desc, gen, i32, queries, workspace
+from test_gpu_queries import DT, desc, gen, i32, queries, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,21 @@ def test_query_unit_of_seconds(causal):
     assert not hc.decode_gave_up(ws)
     want = ref.attend(q, k, v, [rows[0] if x == long else rows[0][:10] for x in lens], d ** -0.5)
     ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)
+
+
+@pytest.mark.parametrize("dtype,big", [("bf16", 3.38e38), ("fp16", 65504.0)])
+@pytest.mark.parametrize("parts", [1, 2, 3, 4, 5, 8])
+def test_merge_of_the_largest_values(parts, dtype, big):
+    """A weighted mean of elements near the type's largest lies among them."""
+    n, h, d, dt = 33, 3, 72, DT[dtype]
+    outs = [((1.0 - 0.3 * torch.rand((n, h, d), generator=gen(i), device="cuda")) * big).to(dt) for i in range(parts)]
+    lses = [(0.0 if i % 2 else 3.0) * torch.randn((n, h), generator=gen(9 + i), device="cuda") for i in range(parts)]
+    z = torch.stack(lses).double()
+    w = torch.softmax(z, 0)[..., None]
+    want = (w * torch.stack(outs).double()).sum(0)
+    out, lse = torch.zeros((n, h, d), dtype=dt, device="cuda"), torch.zeros((n, h), device="cuda")
+    hc.merge_attention(outs, lses, out, lse=lse)
+    # weights as in test_merge, of log-sums up to 20 apart; then their sums and the rounding
+    rel = 2 * (2 * 20 * 1.45 * ref.U32 + 2.0 ** -22) + (2 * parts + 4) * ref.U32
+    assert ((out.double() - want).abs() <= want.abs() * (rel + ref.UNIT[dt] * (1 + rel))).all()
+    assert ((lse.double() - torch.logsumexp(z, 0)).abs() <= rel + 4 * 20 * ref.U32 + 2.0 ** -21).all()

@@ -38,10 +38,12 @@ __global__ void __launch_bounds__(kMergeThreads, PARTS <= 4 ? 8 : 5) merge_kerne
                                               2 * (token * p.o_st[i] + head * p.o_sh[i] + col)));
   }
   const float base = top == -INFINITY ? 0.f : top;
+  // weights in eighths (exactly): the sum of as many parts near the largest bf16 would leave 32 bits,
+  // though their mean does not
   float acc[8] = {}, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < PARTS; ++i) {
-    const float w = exp2_fast((z[i] - base) * 1.4426950408889634f);   // 0 for a part that is not there
+    const float w = 0.125f * exp2_fast((z[i] - base) * 1.4426950408889634f);   // 0 for a part that is not there
     sum += w;
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
@@ -53,12 +55,13 @@ __global__ void __launch_bounds__(kMergeThreads, PARTS <= 4 ? 8 : 5) merge_kerne
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
+  static_assert(kMergeParts == 8, "eighths");
   uint32_t r[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) r[j] = pack2<BF16>(acc[2 * j] * f, acc[2 * j + 1] * f);
   __stcs(reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + 2 * (token * p.out_st + head * p.out_sh + col)),
          make_uint4(r[0], r[1], r[2], r[3]));
-  if (p.lse && col == 0) p.lse[token * p.lse_st + head] = sum == 0.f ? -INFINITY : base + log2f(sum) * kLn2;
+  if (p.lse && col == 0) p.lse[token * p.lse_st + head] = sum == 0.f ? -INFINITY : base + log2f(8.f * sum) * kLn2;
 }
 
 template <int PARTS>
