@@ -4,7 +4,7 @@ import torch
 
 import serving_reference as ref
 import tiered_kv_cache_gb300 as hc
-from test_gpu_queries import DT, desc, gen, i32, queries, workspace
+from test_gpu_queries import Cache, DT, check_prefix, desc, gen, i32, queries, run_prefix, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,16 @@ def test_merge_of_the_largest_values(parts, dtype, big):
     rel = 2 * (2 * 20 * 1.45 * ref.U32 + 2.0 ** -22) + (2 * parts + 4) * ref.U32
     assert ((out.double() - want).abs() <= want.abs() * (rel + ref.UNIT[dt] * (1 + rel))).all()
     assert ((lse.double() - torch.logsumexp(z, 0)).abs() <= rel + 4 * 20 * ref.U32 + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("own", [[0, 1, 40, 700], [9000, 0, 4097, 3]])
+def test_prefix_of_the_largest_values(own):
+    """Values near bf16's largest in the prefix and in every part of the sequences' own tokens."""
+    prefix, members = [500, 90], [2, 1]
+    cache = Cache([prefix, own], 2, 128, 16, seed=15)
+    v = cache.bufs[1]
+    big = (1.0 - 0.3 * torch.rand(v.shape, generator=gen(3), device="cuda")) * 3.38e38
+    v.copy_(torch.where(v.isnan(), v, big.bfloat16()))
+    q = queries(4, 8, 128, "bf16", sharp=0.3)
+    out, lse = run_prefix(cache, q, members, prefix, own)
+    check_prefix(cache, q, members, out, lse)

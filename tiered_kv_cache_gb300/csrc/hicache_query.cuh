@@ -1486,15 +1486,19 @@ __global__ void __launch_bounds__(kEndThreads) prefix_end_kernel(const __grid_co
   const int col = int(at - row * vecs) * 4, b = int(row / p.Hq), h = int(row - int64_t(b) * p.Hq);
   const int kv = int(min(int64_t(max(0, __ldg(p.own_lens + b))), int64_t(p.own_pages) * p.P));
   const int parts = own_parts(kv);
-  float m = __ldcg(p.lse2 + row), sum = m == -INFINITY ? 0.f : 1.f;
+  // weights over a power of two (exactly): the sum of as many parts near the largest bf16 would leave
+  // 32 bits, though their mean does not
+  const float unit = __int_as_float((127 - (32 - __clz(parts))) << 23);
+  float m = __ldcg(p.lse2 + row), sum = m == -INFINITY ? 0.f : unit;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (m != -INFINITY) acc = __ldcg(reinterpret_cast<const float4 *>(p.out32 + row * p.D + col));
+  acc = make_float4(acc.x * unit, acc.y * unit, acc.z * unit, acc.w * unit);
   for (int i = 0; i < parts; ++i) {
     const int64_t x = int64_t(1 + i) * rows + row;
     const float z = __ldcg(p.lse2 + x);
     if (z == -INFINITY) continue;
     const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.out32 + x * p.D + col));
-    const float now = fmaxf(m, z), was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = exp2_fast(z - now);
+    const float now = fmaxf(m, z), was = m == -INFINITY ? 0.f : exp2_fast(m - now), f = unit * exp2_fast(z - now);
     acc = make_float4(acc.x * was + f * v.x, acc.y * was + f * v.y, acc.z * was + f * v.z, acc.w * was + f * v.w);
     sum = sum * was + f;
     m = now;
@@ -1502,7 +1506,7 @@ __global__ void __launch_bounds__(kEndThreads) prefix_end_kernel(const __grid_co
   const float f = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint2 *>(static_cast<char *>(p.out) + 2 * (b * p.o_st + h * p.o_sh + col)) =
       make_uint2(pack2<BF16>(acc.x * f, acc.y * f), pack2<BF16>(acc.z * f, acc.w * f));
-  if (p.lse && col == 0) p.lse[b * p.lse_st + h] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+  if (p.lse && col == 0) p.lse[b * p.lse_st + h] = sum == 0.f ? -INFINITY : (m + log2f(sum / unit)) * kLn2;
 }
 
 template <class... A, class... B>
