@@ -81,7 +81,7 @@ struct QueryConfig {
   static constexpr int ATOMS = DP_ / 64;          // of 64 elements: 128 bytes a row
   static constexpr int QATOM_B = kQueryRows * 128, ATOM_B = BN * 128;
   static constexpr int QTILE_B = ATOMS * QATOM_B, TILE_B = ATOMS * ATOM_B;
-  static constexpr int STAGES = DP_ == 64 ? 8 : 5;   // tiles of K or V: what shared memory holds beside Q (2 x 32 KB + 5 x 32 KB at 128)
+  static constexpr int STAGES = query_stages(DP_);   // tiles of K or V
   static constexpr int SMEM = QT * QTILE_B + STAGES * TILE_B;
   static constexpr int SOFT_WARPS = 4 * QT, COPY_WARP = SOFT_WARPS, MMA_WARP = COPY_WARP + 4;
   static constexpr int WARPS = MMA_WARP + 4, THREADS = WARPS * 32;
@@ -102,6 +102,8 @@ struct QueryConfig {
   static constexpr float LIMIT = BF16 ? 1.f : 32768.f, ABOVE = kAbove<!BF16>;   // 2^kRaise
   static_assert(kRaise<false> == 0.f && kRaise<true> == 15.f, "the sums' limit");
   static_assert(O_COL + QT * DP_ <= 512, "tensor memory");
+  static_assert(query_turns_hold(kQueryTurns, STAGES), "a parity wait of the copies could pass two phases early");
+  static_assert(query_info_holds(kQueryInfo, kQueryTurns, STAGES), "what is present of a block could be overwritten");
 };
 
 // A shared-memory operand's descriptor in two halves (see smem_desc): the upper is the same
@@ -405,7 +407,7 @@ struct alignas(16) QueryPiece {
   int32_t kv, lo, hi, flags;       // tokens of the sequence; those [lo, hi) that some row of the unit sees
 };
 enum : int { kTwoTiles = 1, kBegins = 2, kWhole = 4, kOwn = 8 };   // kOwn: over the sequence's own tokens
-constexpr int kPieceRing = 4;
+constexpr int kPieceRing = kQueryPieces;
 
 // The output's row of row r of a unit: the query token and head.
 struct QueryRow {
@@ -471,7 +473,7 @@ __device__ __noinline__ void copy_cut_boxes(uint32_t rows, const char *v, int64_
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_constant__ QueryParams p, const __grid_constant__ QueryMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = 8, PARTS = BN / 64;
+  constexpr int BN = C::BN, THREADS = C::THREADS, WORDS = BN / 32, INFO = kQueryInfo, PARTS = BN / 64;
   __shared__ long long scratch[C::WARPS], units_of[C::WARPS];
   __shared__ long long first_rest;                // where the chunk starts: blocks from the first of a sequence on
   __shared__ int first_seq;
@@ -481,6 +483,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
   __shared__ QueryPiece ring_of_pieces[kPieceRing];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
+  // (static variables, up to the tiles' alignment)
+  static_assert(C::SMEM + (sizeof(scratch) + sizeof(units_of) + sizeof(bars) + sizeof(offs) + sizeof(there) +
+                           sizeof(ring_of_pieces) + 64 + 1023) / 1024 * 1024 <= 227 * 1024, "a block's shared memory");
 
   const int tid = int(threadIdx.x), warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t q_s = smem_u32(smem_raw), ring_s = q_s + C::QT * C::QTILE_B;
@@ -881,8 +886,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
     // ---- copies
     const int pt = tid - C::COPY_WARP * 32;
     // boxes: lane i takes rows from box_r on, 64 elements from box_c on.  A block's take a
-    // warp 2,500 clocks, so three take turns.  (No more: each waits for the stages of its own
-    // blocks only, and with 5 stages a fourth's could be two phases behind.)
+    // warp 2,500 clocks, so three take turns.  (No more: see query_turns_hold.)
     const int columns = (p.D + 63) >> 6, box_r = lane / columns * maps.box, box_c = lane % columns * 64;
     const int boxes_all = maps.box > 0 ? BN / maps.box * columns : 0;
     int stage = 0, phase = 1;
@@ -978,7 +982,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
       for (int x = 0; ok && x < pc.n; ++x, ++blk) {
         const int t0 = pc.t0 + x * BN;
         if (by_box) {
-          if (blk % 3u == uint32_t(pt >> 5)) {
+          if (blk % uint32_t(kQueryTurns) == uint32_t(pt >> 5)) {
             // the page of the box's first token that is in the range
             const int t = max(t0 + box_r, pc.lo);
             page = -1;

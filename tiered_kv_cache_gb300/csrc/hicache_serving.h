@@ -124,6 +124,22 @@ constexpr int kQueryRows = 128;
 HC_HD int query_tiles(int D) { return D <= 128 ? 2 : 1; }
 HC_HD int query_block(int D) { return D <= 128 ? 128 : 64; }
 HC_HD int query_cols(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// Who may be how far ahead of whom: stages of K or V tiles in shared memory, blocks whose present
+// tokens are kept, copying warps that take turns, pieces that are planned ahead.
+constexpr int query_stages(int D) { return D <= 64 ? 8 : 5; }   // what fits beside Q (2 x 32 KB + 5 x 32 KB at 128)
+constexpr int kQueryInfo = 8;
+constexpr int kQueryTurns = 3;
+constexpr int kQueryPieces = 4;
+// A copying warp waits for the stages of its own blocks only, by a phase's parity, which tells one
+// phase from the next but not from the one after that.  At block b it has seen the tile 2 (b - turns) + 1 -
+// stages used up, its last one's, and next waits for tile 2 b - stages: tile 2 b - 2 stages, which used
+// that stage before it, must be known to be used up by then.
+constexpr bool query_turns_hold(int turns, int stages) { return 2 * (-turns) + 1 - stages >= -2 * stages; }
+// What it writes of block b must not be read as block b - info's any more.  If the tile it has seen used
+// up is K's (an odd number of stages), the products with V two blocks before that are done, if V's, its own.
+constexpr bool query_info_holds(int info, int turns, int stages) {
+  return info >= turns + (stages % 2 ? (stages - 1) / 2 + 2 : stages / 2);
+}
 constexpr int kQueryCtas = 152;                   // one on each of a GB300's SMs
 // What beginning and ending a unit takes, in blocks: without it CTAs with many short units end
 // last (32 ragged encoders 71 us, 54 with 4, 55 with 8; chunks of up to 1,000 queries at e4m3 188,
