@@ -4,7 +4,7 @@ import torch
 
 import serving_reference as ref
 import tiered_kv_cache_gb300 as hc
-from test_gpu_queries import Cache, DT, check_prefix, desc, gen, i32, queries, run_prefix, workspace
+from test_gpu_queries import Cache, DT, check_prefix, desc, gen, i32, present, queries, run_prefix, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,43 @@ def test_prefix_of_the_largest_values(own):
     q = queries(4, 8, 128, "bf16", sharp=0.3)
     out, lse = run_prefix(cache, q, members, prefix, own)
     check_prefix(cache, q, members, out, lse)
+
+
+@pytest.mark.parametrize("starts,sure", [
+    ([-5, 4, 9, 30], range(20)), ([0, 10, 5, 20], [*range(5), *range(10, 20)]), ([4, 4, 3, 4], [*range(3), *range(4, 20)]),
+    ([2 ** 31 - 1, 3, -2 ** 31, 5], range(5, 20)), ([-2 ** 31, -1, 2 ** 31 - 1, 0], []), ([25, 24, 23, 22], range(20)),
+])
+@pytest.mark.parametrize("bad", [False, True])
+def test_prefix_bad_starts_and_lengths(starts, sure, bad):
+    """What the host cannot see: starts that descend or leave the rows, lengths below 0 and beyond
+    the tables.  Nothing outside the rows is written, and rows in one group at most are right.  (Where
+    starts descend, rows may lie in two groups or behind the last start.)"""
+    n, hq, d, P = 20, 4, 64, 16
+    prefix, own = [96, 96, 96], [(0, 16, 48, 33)[i % 4] for i in range(n)]
+    cache = Cache([prefix, own], 2, d, P, seed=16)
+    q = queries(n, hq, d, "bf16")
+    lens, own_lens = list(prefix), list(own)
+    if bad:
+        lens[0], lens[2] = -1, 2 ** 31 - 1
+        prefix[0] = 0
+        for i in range(0, n, 4):                  # nothing, and a table's 3 pages
+            own_lens[i] = -2 ** 31
+            own_lens[i + 2] = 2 ** 31 - 1
+    out = torch.full((n + 4, hq, d), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((n + 4, hq), 5.0, device="cuda")
+    ws = workspace(hc.prefix_workspace(cache.desc, n, 3, hq, d, cache.tables[0].shape[1], cache.tables[1].shape[1]))
+    hc.prefix_attention(cache.kv, cache.desc, 0, q, i32(starts), cache.tables[0], i32(lens), cache.tables[1], i32(own_lens),
+                        out[2:-2], ws, lse=lse[2:-2])
+    assert not hc.decode_gave_up(ws)
+    for x, v in ((out, 7.0), (lse, 5.0)):
+        assert (x[:2] == v).all() and (x[-2:] == v).all()
+    at = [min(max(s, 0), n) for s in starts]
+    owner = [-1] * n
+    for g in range(3):
+        for b in range(at[g], max(at[g], at[g + 1])):
+            owner[b] = g
+    k, v = cache.plain()
+    sure = list(sure)
+    rows = [present((cache.rows[0][owner[b]][:prefix[owner[b]]] if owner[b] >= 0 else []) + cache.rows[1][b]) for b in sure]
+    want = ref.attend(q[sure], k, v, rows, d ** -0.5, joins=5)
+    ref.check_decode(out[2:-2][sure], want, q.dtype, torch.bfloat16, lse=lse[2:-2][sure])
