@@ -730,10 +730,11 @@ int hicache_decode_workspace(const hicache_pool_desc *desc, int32_t batch, int32
                              int32_t v_dim, int32_t max_pages, int32_t with_weights, int64_t *bytes);
 /* Whether a call with this workspace has given up: the kernels over a latent cache
  * and those of hicache_query_attention and hicache_prefix_attention wait for their
- * own copies and products with a limit of about two seconds, and a wait that runs out (it never should) ends the call with its outputs undefined
- * and marks the workspace, *gave_up = 1 until `clear`.  Waits for all work of
- * the current device, on every stream; not during a capture.  Errors:
- * INVALID_ARG, ALIGNMENT, CUDA. */
+ * own copies and products with a limit of about two seconds (for a unit of work as
+ * long as it takes, while its products go on), and a wait that runs out (it never
+ * should) ends the call with its outputs undefined and marks the workspace,
+ * *gave_up = 1 until `clear`.  Waits for all work of the current device, on every
+ * stream; not during a capture.  Errors: INVALID_ARG, ALIGNMENT, CUDA. */
 int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
 
 /* Attention of several query tokens per sequence over its pages.  Sequence b has
@@ -747,17 +748,20 @@ int hicache_decode_status(void *workspace, int32_t *gave_up, int32_t clear);
  * of which those on absent pages are left out, with scores, lse and out as in
  * hicache_decode_attention (K and V of kv head h / (q_heads / kv_heads)).  A query
  * without any such token gives out = 0 and lse = -infinity.  Rows of q that belong to
- * no sequence (in front of q_starts[0], behind q_starts[batch]) are not read, and
- * theirs of out and lse left as they were.  q_starts must ascend; its values count
- * as clamped to [0, num_tokens], those of a sequence that descend as no query.
+ * no sequence (in front of q_starts[0], behind q_starts[batch]) have no effect, though
+ * a copy of 128 rows may read them, and theirs of out and lse are left as they were.
+ * q_starts must ascend; its values count as clamped to [0, num_tokens], those of a
+ * sequence that descend as no query, and a row in several sequences is undefined.
  * Pages behind the lengths may hold anything.  V of the cached tokens must be finite:
  * a causal query's weight of a token it does not see is 0, and 0 times infinity is
- * not.
+ * not.  Where V is not, queries in front of that token can be NaN, as far as the
+ * kernel works on them together with one that sees it.
  * The products run on the tensor cores with 32-bit sums, exponentials rounded as in
  * hicache_decode_attention.
  * workspace: hicache_query_workspace bytes, under the rules of
  * hicache_decode_attention's, with which it can be shared, one call after another;
- * hicache_decode_status tells whether a call with it gave up.  out and lse must not overlap an input or one another.
+ * hicache_decode_status tells whether a call with it gave up.  out and lse must not
+ * overlap an input or one another.
  * K, V caches (num_buffers 2); head_dim: a multiple of 8 (of 16 for e4m3) up to 256;
  * num_tokens * q_heads < 2^31 - 4096; batch up to 65,535. */
 typedef struct {
@@ -789,7 +793,10 @@ int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_
  * group's prefix is read once for all of its sequences.  Sequences of no group (in front
  * of group_starts[0], behind group_starts[groups]) have their own tokens alone, and
  * groups may be 0 (the three arrays NULL).  group_starts must ascend, as q_starts of
- * hicache_query_attention.  Absent pages, lengths, strides, types and the workspace
+ * hicache_query_attention.
+ * It is the faster call where reading the prefix for each sequence would take over
+ * some 270 MB: with cache rows of 2 KB each of K and V from 32 sequences on 2,048
+ * shared tokens, 8 on 8,192 or 4 on 32,768; below that hicache_decode_attention is.  Absent pages, lengths, strides, types and the workspace
  * (hicache_prefix_workspace bytes; hicache_decode_status) as there; the prefix's part
  * of a row and those of each 4,096 tokens of its own are kept in the workspace, in 32
  * bits, until they are joined.

@@ -7,7 +7,7 @@
 // an SM holds (8 blocks: 54 -> 48 us for 8,191 tokens of 32 heads of 128 from 4 parts of which a
 // quarter is empty; two or four rows a thread instead took 62 and 113), and loads and stores
 // that leave L2 to others (48 -> 45.4; 2 parts 37 -> 32.5): nothing is read twice.  4 parts without
-// an empty one: 50.8 us, 8 parts 91, 97% and more of a plain copy's rate, 2 parts 91%.
+// an empty one: 50.8 us, 8 parts 91, 97% and more of a plain copy's rate, 2 parts 92%.
 
 #include "hicache_decode.cuh"
 

@@ -13,10 +13,11 @@
 // for one tile of rows and blocks of 64 tokens, and a unit of up to 128 rows has only
 // one: there the two score buffers are filled in turn.
 //
-// Bounds: with N rows a byte of the cache takes N multiply-adds of 2-byte elements, so
-// from 280 rows on the tensor cores bind, below that HBM.  8 sequences of 2,048 queries over
-// 4,001 tokens, 32 heads of 128 on 8: 700 us, 1,530 TFLOP/s, 80% of a large library product's
-// rate; 8,191 queries of one prompt at themselves: 415 us, 1,320 TFLOP/s.  A step of the tensor
+// Bounds: with N rows a byte of the cache takes N operations (2-byte elements, N / 2
+// multiply-adds), so from 280 rows on the tensor cores bind, below that HBM.  8 sequences of 2,048
+// queries over 4,001 tokens, 32 heads of 128 on 8: 695 us in a burst, 1,540 TFLOP/s, 81% of a large
+// library product's burst rate, and 737 us once the power cap lowers the clock; 8,191 queries of
+// one prompt at themselves: 415 and 420 us, 1,320 TFLOP/s.  A step of the tensor
 // cores for 128 rows takes 64 clocks whatever its operands come from, and the exponentials of
 // two tiles half of the products' time on the units that compute them, so each hides behind the other
 // as long as nobody waits.
@@ -24,8 +25,8 @@
 // Softmax: a thread per row, so that maximum and sum need no other thread.  What a row's
 // scores are taken relative to follows the running maximum only when the sum of a block's
 // exponentials passes what P's type can hold; O is rescaled then, and only then, by the same
-// thread.  (With a maximum per block in place of that sum: 2,048 queries at 32,768
-// tokens 732 us where this took 691.)
+// thread.  (With a maximum per block in place of that sum, 2,048 queries at 32,768
+// tokens took 732 us when this took 691, now 655.)
 //
 // Units of one tile of rows (a decode batch's prefix, short queries) would leave the second set of
 // softmax warps idle: the two sets share its blocks there, even and odd, with sums of
@@ -86,12 +87,12 @@ struct QueryConfig {
   static constexpr int SOFT_WARPS = 4 * QT, COPY_WARP = SOFT_WARPS, MMA_WARP = COPY_WARP + 4;
   static constexpr int WARPS = MMA_WARP + 4, THREADS = WARPS * 32;
   // Registers of a thread of each group of four warps: what the launch has, dealt anew.  The
-  // softmax holds up to 64 scores, e4m3 copies two tiles' parts (with 88 registers for them 237 us
+  // softmax holds up to 64 scores, e4m3 copies two tiles' parts (with 88 registers for them 239 us
   // in place of 172, with 120 the same).
   static constexpr bool E4 = TYPE_ == kQE4m3;
-  // Halves of a block whose scores are loaded together, and whose code is there twice: 8% for
-  // what the products bind (2,048 queries at 32,768: 740 -> 683 us), but 18 to 20% against
-  // what copies and starts do (32 ragged encoders 59 -> 72, e4m3 172 -> 200), for
+  // Halves of a block whose scores are loaded together, and whose code is there twice: 4 to 6% for
+  // what the products bind (2,048 queries at 32,768: 689 -> 659 us, 8 x 2,048 740 -> 695), but 23 to
+  // 29% against what copies and starts do (32 ragged encoders 50 -> 64, e4m3 172 -> 212), for
   // the instruction cache.
   static constexpr int AT_ONCE = BN == 128 && DP_ == 128 && !E4 ? 2 : 1;
   static constexpr int SOFT_REGS = QT == 1 ? 240 : E4 ? 176 : 192, COPY_REGS = QT == 1 ? 152 : E4 ? 104 : 72,
@@ -447,7 +448,7 @@ __device__ __forceinline__ void query_store8(const QueryParams &p, const QueryRo
 }
 
 // The boxes of V in `rows` row by row, zeros beyond [lo, hi); by one warp.  Not inlined: it is rare,
-// and with it inlined what the products bind lost 3% (8 x 2,048 queries 700 -> 721 us).
+// and with it inlined what the products bind loses 2% (8 x 2,048 queries 695 -> 710 us).
 __device__ __noinline__ void copy_cut_boxes(uint32_t rows, const char *v, int64_t pitch, int y, int box_r, int box_c, int box, int d,
                                             uint32_t at, uint32_t atom, int t_lo, int t_hi) {
   const int lane = int(threadIdx.x) & 31;
@@ -1256,8 +1257,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) query_kernel(const __grid_const
                 }
               }
             }
-            // P, rounded to the products' type; the sums keep all bits.  P of word w takes half
-            // of the place of the scores of word w / 2
+            // P, rounded to the products' type as in decode attention, since the tensor cores take 16-bit
+            // operands of one type (outputs in bf16 are 0.0024 off in place of 0.0017, in fp16 0.0003
+            // in place of 0.0002); the sums keep all bits.  P of word w takes half of the place of the
+            // scores of word w / 2
             uint64_t sum[2] = {0, 0};             // two pairs of sums
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -1545,7 +1548,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_call() {
 }
 
 // Describes q and the layer's buffers to TMA where its boxes fit: pages of whole boxes of 16 rows
-// or more (32 ragged encoders on pages of 16: 49 us, 71 row by row; 64 sequences on a prefix
+// or more (32 ragged encoders on pages of 16: 50 us, 70 row by row; 64 sequences on a prefix
 // of 32,768: 91, 100; with fewer rows a block would take more requests than a warp has lanes), heads that the products'
 // steps of 16 cover (what a box holds behind the head is not used), rows within a
 // coordinate.  Else, or where the driver will not, the copies go row by row.

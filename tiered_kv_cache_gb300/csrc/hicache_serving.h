@@ -142,21 +142,22 @@ constexpr bool query_info_holds(int info, int turns, int stages) {
 }
 constexpr int kQueryCtas = 152;                   // one on each of a GB300's SMs
 // What beginning and ending a unit takes, in blocks: without it CTAs with many short units end
-// last (32 ragged encoders 71 us, 54 with 4, 55 with 8; chunks of up to 1,000 queries at e4m3 188,
-// 172, 180).
+// last (32 ragged encoders 66 us, 50 with 4, 52 with 8; chunks of up to 1,000 queries at e4m3 188,
+// 172, 175).
 constexpr int kQueryStart = 4;
 HC_HD int32_t query_cost(int32_t blocks) { return blocks > 0 ? blocks + kQueryStart : 0; }
 // The tokens of a unit over a sequence's own: 16 sequences of 8,000 to 20,000, 32 heads on 8, take
-// 194 us with 1,024, 177 with 4,096, 208 with 32,768; 200 of 100 to 6,000 306, 272, 274.
+// 198 us with 1,024, 177 with 4,096, 206 with 32,768; 200 of 100 to 6,000 306, 278, 280.
 constexpr int kOwnTokens = 4096;
 // The parts of so many, and the end of the one that begins at `lo`: no step leaves 32 bits, up to
 // the longest table's 2^31 - 1,025 tokens.
 HC_HD int32_t own_parts(int32_t tokens) { return tokens / kOwnTokens + (tokens % kOwnTokens != 0); }
 HC_HD int32_t own_end(int32_t lo, int32_t tokens) { return tokens - lo < kOwnTokens ? tokens : lo + kOwnTokens; }
 // From so many units for each of them on, CTAs take whole units.  8 x 2,048 queries of 32 heads
-// on 8 (13 for each): 772 us in chunks, 698 whole.  With 2 as the limit 1,500 queries of
-// heads of 256 on 6,001 tokens (2.5 for each) would take 251 us in place of 211, chunks at
-// e4m3 220 in place of 172.
+// on 8 (13 for each): 768 us in chunks, 695 whole; unequal units can lose (16 prompts of 200 to
+// 2,000 queries at up to 9,000 tokens, 425 in chunks, 449 whole).  With 2 as the limit 1,500 queries of
+// heads of 256 on 6,001 tokens (2.5 for each) would take 255 us in place of 217, chunks at
+// e4m3 222 in place of 172.
 constexpr int kQueryWhole = 4;
 struct QuerySpace {
   int64_t next, open, parts, bytes;
