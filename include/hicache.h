@@ -792,7 +792,7 @@ int hicache_query_workspace(const hicache_pool_desc *desc, int32_t batch, int64_
  * hicache_decode_attention over the prefix's tokens and then the sequence's, but a
  * group's prefix is read once for all of its sequences.  Sequences of no group (in front
  * of group_starts[0], behind group_starts[groups]) have their own tokens alone, and
- * groups may be 0 (the three arrays NULL).  group_starts must ascend, as q_starts of
+ * groups may be 0 (the three arrays NULL, max_prefix_pages 0).  group_starts must ascend, as q_starts of
  * hicache_query_attention.
  * It is the faster call where reading the prefix for each sequence would take over
  * some 270 MB: with cache rows of 2 KB each of K and V from 32 sequences on 2,048

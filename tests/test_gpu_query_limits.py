@@ -129,3 +129,17 @@ def test_prefix_bad_starts_and_lengths(starts, sure, bad):
     rows = [present((cache.rows[0][owner[b]][:prefix[owner[b]]] if owner[b] >= 0 else []) + cache.rows[1][b]) for b in sure]
     want = ref.attend(q[sure], k, v, rows, d ** -0.5, joins=5)
     ref.check_decode(out[2:-2][sure], want, q.dtype, torch.bfloat16, lse=lse[2:-2][sure])
+
+
+def test_prefix_without_a_table():
+    """No groups, and a prefix table without columns."""
+    own = [0, 33, 200]
+    cache = Cache([[], own], 2, 128, 16, seed=17)
+    q = queries(3, 8, 128, "bf16")
+    ws = workspace(hc.prefix_workspace(cache.desc, 3, 0, 8, 128, 0, cache.tables[1].shape[1]))
+    out, lse = torch.full_like(q, 7.0), torch.full((3, 8), 5.0, device="cuda")
+    none = torch.zeros((0, 0), dtype=torch.int32, device="cuda")
+    hc.prefix_attention(cache.kv, cache.desc, 0, q, i32([0]), none, i32([]), cache.tables[1],
+                        i32(own), out, ws, lse=lse)
+    want = ref.attend(q, *cache.plain(), [present(r) for r in cache.rows[1]], 128 ** -0.5, joins=5)
+    ref.check_decode(out, want, q.dtype, torch.bfloat16, lse=lse)

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import tiered_kv_cache_gb300 as hc
-from test_query_refusals import desc, merge, run_host
+from test_query_refusals import PREFIX, call, desc, merge, run_host
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -65,3 +65,17 @@ def test_merge_refuses_heads_that_overlap(heads, stride):
     # apart, the call goes on to what is checked next
     assert merge(**{**change, "out_h": 8, "lse": 4 << 20 | 2}) == "ALIGNMENT"
     assert merge(**{**change, "out_t": 8, "out_h": 16, "lse": 4 << 20 | 2}) == "ALIGNMENT"
+
+
+def test_prefix_without_a_table():
+    """Without groups there is no prefix table: its width may be 0."""
+    out, d = ctypes.c_int64(), desc()
+    ask = lambda groups, wide: hc.library().hicache_prefix_workspace(ctypes.byref(d), 3, groups, 4, 128, wide, 20, ctypes.byref(out))  # noqa: E731
+    assert ask(0, 1) == 0
+    one = out.value
+    assert ask(0, 0) == 0 and out.value == one
+    assert ask(1, 0) == -1 and ask(0, -1) == -1
+    none = {**PREFIX, "groups": 0, "starts": 0, "shared": 0, "prefix": 0, "wide": 0, "pb": 0}
+    # the sizes pass: what is checked behind them refuses
+    assert call("hicache_prefix_attention", hc._PREFIX_DESC, {**none, "lse": PREFIX["lse"] + 2}, d) == "ALIGNMENT"
+    assert call("hicache_prefix_attention", hc._PREFIX_DESC, {**none, "groups": 1}, d) == "INVALID_ARG"

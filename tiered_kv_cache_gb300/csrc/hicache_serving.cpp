@@ -236,6 +236,8 @@ int prefix_space(const hicache::QueryParams &q, PrefixSpace *s) {
 // Checks the sizes of a call over prefixes.
 int prefix_sizes(const Shape &s, int64_t batch, int64_t groups, int64_t q_heads, int64_t head_dim, int64_t max_prefix_pages,
                  int64_t max_pages, hicache::QueryParams *q) {
+  // (without groups there is no table, and its width is whatever the caller has)
+  if (groups == 0 && max_prefix_pages == 0) max_prefix_pages = 1;
   int rc = query_sizes(s, groups, batch, q_heads, head_dim, max_prefix_pages, q);
   if (rc) return rc;
   hicache::DecodeParams d{};
