@@ -19,7 +19,7 @@ def test_parts_of_own_tokens(tmp_path):
     table; the workspace holds as many."""
     assert run_host(tmp_path, """
   const long long most = INT_MAX - 1024ll;            // max_pages * page_size
-  for (long long n : {0ll, 1ll, 4095ll, 4096ll, 4097ll, 8192ll, 1000000007ll, most - 4096, most - 3072, most - 3071, most - 1, most}) {
+  for (long long n : {0ll, 1ll, 4095ll, 4096ll, 4097ll, 8192ll, 1000000007ll, most - 4096, most + 1024 - kOwnTokens, most + 1025 - kOwnTokens, most - 1, most}) {
     const long long want = (n + kOwnTokens - 1) / kOwnTokens;
     if (own_parts(int32_t(n)) != want) return 1;
     long long next = 0;
